@@ -367,10 +367,209 @@ LL_API int loglinear_bwd(const void* q, const void* k, const void* v, const floa
  * not valid).  Bit 1: a wait for another tile's published state ran out of time (the
  * output of that tile is not valid).  Bit 2: loglinear_bwd was given a fwd_workspace
  * that a tensor-core loglinear_fwd with the same B, T, H, Hqk and dv did not write (its
- * layout tag does not match; the gradients are not valid).  The launch itself still
- * reported success.
+ * layout tag does not match; the gradients are not valid).  Bit 3: a wait of loglinear_glr_fwd
+ * or _bwd for the tile before ran out of time (the results are not valid).  Bit 4:
+ * loglinear_glr_step was given a slot out of range, or one that an earlier row has (that
+ * row was left out).  The launch itself still reported success.
  */
 LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
+
+/*
+ * Gated linear recurrence, per channel:
+ *     h_t = a_t h_{t-1} + b_t x_t,   a_t = exp(log_a_t),
+ *     b_t = 1 (LL_GLR_NONE), 1 - a_t (LL_GLR_ONE_MINUS) or sqrt(1 - a_t^2) (LL_GLR_SQRT).
+ * The vector-state recurrence of gated layers that stand between attention layers; the
+ * sources have no counterpart.  One pass: every input is read once, every output written once.
+ *   x          [B, T, D] in_dtype; log_a [B, T, D] gate_dtype (<= 0 expected; -inf is a = 0).
+ *              gate_dtype is LL_F32 or in_dtype (else LL_ERR_UNSUPPORTED).  Both may be
+ *              strided: element strides of the batch and position dimensions (h is not
+ *              read), channels contiguous; NULL = dense.
+ *   cu_seqlens NULL: B sequences of T tokens.  Else device int32 [N + 1], 0 = cu[0] <= cu[1]
+ *              <= ... <= T, with B = 1: sequence n holds tokens cu[n] .. cu[n+1] - 1, and
+ *              nothing passes from one to the next, infinities and NaN included.  Rows
+ *              behind cu[N] are neither read nor written.  The library does not read the bounds
+ *              on the host; bounds out of order give wrong sequences, but no access outside
+ *              the arrays.
+ *   N          number of sequences (ignored without cu_seqlens: B)
+ *   h0         [N, D] fp32 state before the first token; NULL = zero
+ *   out        [B, T, D] out_dtype: h_t
+ *   state_out  NULL, or [N, D] fp32: the state after the last token (h0 for an empty sequence)
+ * State, gates and sums are fp32; out is rounded once.
+ * workspace: loglinear_glr_workspace_size() bytes (may be 0; then it may be NULL), 256-byte
+ *   aligned, scratch; two calls that run concurrently need two.
+ * Errors: LL_ERR_INVALID (null pointer, negative size or stride, unknown scale, cu_seqlens with
+ * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T > 2^30, or more than 2^31 - 1 tiles),
+ * LL_ERR_WORKSPACE, LL_ERR_ALIGN (a pointer not aligned to its element, the workspace),
+ * LL_ERR_CUDA.  B, T or D = 0 is a no-op, but that state_out still receives h0.
+ */
+typedef enum { LL_GLR_NONE = 0, LL_GLR_ONE_MINUS = 1, LL_GLR_SQRT = 2 } ll_glr_scale;
+
+LL_API int loglinear_glr_workspace_size(int64_t B, int64_t T, int64_t D, size_t* bytes);
+LL_API int loglinear_glr_fwd(const void* x, const ll_strides* x_strides, const void* log_a,
+                             const ll_strides* log_a_strides, const float* h0,
+                             const int32_t* cu_seqlens, int64_t N, void* out, float* state_out,
+                             int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype,
+                             int out_dtype, int scale, void* workspace, size_t workspace_bytes,
+                             ll_stream_t stream);
+
+/*
+ * Gradients of loglinear_glr_fwd, given dout = dL/d out and (or NULL) dstate = dL/d state_out:
+ *     g_t = dout_t + a_{t+1} g_{t+1}  (+ dstate at the sequence's last token)
+ *     dx_t = b_t g_t,   dlog_a_t = a_t h_{t-1} g_t + b'(log_a_t) x_t g_t,   dh0 = a g at the first
+ * h is the forward's out (its rounding enters dlog_a).  Where b = sqrt(1 - a^2) is 0, its
+ * derivative, which is infinite, is taken as 0.
+ *   h, dout, dx   [B, T, D] grad_dtype, dense;  dlog_a [B, T, D] gate_dtype, dense
+ *   x             may be NULL with LL_GLR_NONE, whose gradients do not read it
+ *   dstate, dh0   [N, D] fp32 or NULL (dh0 of an empty sequence is its dstate, or zero)
+ * x, log_a, h0, cu_seqlens, N, sizes, workspace and errors as loglinear_glr_fwd.
+ */
+LL_API int loglinear_glr_bwd(const void* x, const ll_strides* x_strides, const void* log_a,
+                             const ll_strides* log_a_strides, const float* h0,
+                             const int32_t* cu_seqlens, int64_t N, const void* h,
+                             const void* dout, const float* dstate, void* dx, void* dlog_a,
+                             float* dh0, int64_t B, int64_t T, int64_t D, int in_dtype,
+                             int gate_dtype, int grad_dtype, int scale, void* workspace,
+                             size_t workspace_bytes, ll_stream_t stream);
+
+/*
+ * One token of the recurrence for each of B rows: state[slot] <- a state[slot] + b x, out = the new
+ * state.
+ *   state  [S, D] fp32, updated in place;  x [B, D] in_dtype;  log_a [B, D] gate_dtype
+ *   slots  NULL (row b has slot b; then S >= B, else LL_ERR_SHAPE), or device int32 [B]: the
+ *          row's slot; -1 leaves the row out (its out is not written).  A slot out of range, or
+ *          one that an earlier row has, leaves the row out too and raises bit 4 of
+ *          loglinear_device_error.
+ *   out    [B, D] out_dtype
+ * Errors: LL_ERR_INVALID, LL_ERR_SHAPE, LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (B > 65535),
+ * LL_ERR_ALIGN, LL_ERR_CUDA.
+ */
+LL_API int loglinear_glr_step(float* state, int64_t S, const int32_t* slots, const void* x,
+                              const void* log_a, void* out, int64_t B, int64_t D, int in_dtype,
+                              int gate_dtype, int out_dtype, int scale, ll_stream_t stream);
+
+/*
+ * The paged decode cache: decoding for sequences that are each at a position of their own.
+ *
+ * loglinear_decode_step keeps a dense state [B, H, L, dk, dv] whose rows are all at one
+ * position, and reads and rewrites every level that holds data.  The cache keeps, for a slot
+ * that holds n positions, the raw tokens of its current block (n mod 64 of them; the levels
+ * inside a block are summed from them), and for every set bit i of j = n / 64 one page
+ * [H, dk, dv] fp32: the state of the aligned run of 2^i blocks that the Fenwick partition has
+ * there (token level 7 + i), as it was at its last token.  Its decay since then is one
+ * number per head.  Pages are written once, at a block's last token, and may be shared.
+ *
+ * Every array is the caller's.  `free` below: a page with reference count 0; the lowest free
+ * pages are taken first, in the order of the rows.  A new cache has page_table all -1 and
+ * refcount all 0; the other arrays need no initial value.
+ */
+#define LL_CACHE_BLOCK 64
+
+typedef struct {
+  int64_t slots, n_pages;  /* >= 1; n_pages <= 2^30 */
+  int64_t H, Hqk, dk, dv;  /* Hqk divides H; 1 <= dk <= 128; dv a multiple of 4, 4 <= dv <= 128 */
+  int64_t levels;          /* M: pages a slot can hold, 1 <= M <= 24; a slot holds fewer than
+                              64 * 2^M positions */
+  int dtype;               /* LL_F32 or LL_BF16: the type of k and v */
+  float* pages;            /* [n_pages, H, dk, dv], 16-byte aligned */
+  int32_t* page_table;     /* [slots, M]: the page of each level, or -1 */
+  int32_t* refcount;       /* [n_pages]: slots that hold the page */
+  void* win_k;             /* [slots, Hqk, 64, dk] dtype: the block's keys; 16-byte aligned */
+  void* win_v;             /* [slots, H, 64, dv] dtype: its values; 16-byte aligned */
+  float* win_log_a;        /* [slots, H, 64]: its log decays */
+  float* page_log;         /* [slots, 2, M, H]: for blocks of even and of odd number, each page's
+                              log decay from its last token to the block's start */
+  int32_t* page_from;      /* [slots, 2]: token of the block from which pages decay on */
+  int32_t* scratch;        /* loglinear_cache_scratch_size() bytes */
+  uint32_t* error;         /* [1] bits below, raised by kernels; the caller reads and clears it */
+} ll_cache;
+
+/* Raised on the device by rows that are then left out (their slot and output as they were). */
+#define LL_CACHE_ERR_SLOT 1u      /* slot out of range (other than -1), or given to an earlier row */
+#define LL_CACHE_ERR_POSITION 2u  /* position outside the cache */
+#define LL_CACHE_ERR_PAGES 4u     /* no free page was left (the slot is left without it) */
+#define LL_CACHE_ERR_MISSING 8u   /* a page that the position needs is not there */
+
+LL_API int loglinear_cache_scratch_size(int64_t slots, int64_t n_pages, size_t* bytes);
+
+/*
+ * Conventions of the calls on a cache: `slots` (and src, dst) device int32 [n], -1 leaves the row
+ * out; `pos` device int32 [n], the positions each row's slot holds, read from device memory so
+ * that a captured graph can be replayed.  Calls on one cache have to be ordered (one stream, or
+ * events); its arrays are read and written by all of them.  n = 0 is a no-op.
+ * Errors: LL_ERR_INVALID (null pointer or descriptor, negative size), LL_ERR_SHAPE (Hqk, too few
+ * levels L), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (sizes outside the descriptor's limits, too many
+ * rows for a launch), LL_ERR_ALIGN, LL_ERR_CUDA.
+ */
+
+/*
+ * The page reservation that goes before a step at the same positions: each slot gives up the
+ * pages that are no longer live at pos and, where pos is a block's last position, takes the
+ * page that the block is folded into.  May be left out when no row is at a block's first or
+ * last position; may be repeated.
+ */
+LL_API int loglinear_cache_reserve(const ll_cache* cache, const int32_t* slots,
+                                   const int32_t* pos, int64_t n, ll_stream_t stream);
+
+/*
+ * One decode step for n rows, each at its own position t = pos[row] (the definition of
+ * loglinear_decode_step):
+ *     out = sum_{s <= t} lambda[level(t, s)] exp(sum_{u=s+1..t} log_a_u) (q_t . k_s) v_s,
+ * with the sum over whole blocks taken from the pages.  The token joins the slot's block; at a
+ * block's last position the pages below level ctz(j + 1) and the block are folded into the page
+ * of that level.  Repeating a step at the same position repeats its result.
+ *   q, k   [n, Hqk, dk] cache dtype;  v [n, H, dv] cache dtype
+ *   log_a  [n, H] fp32 or NULL (no decay);  lambda [n, H, L] fp32, L >= M + 7
+ *   out    [n, H, dv] out_dtype
+ * pos below 64 * 2^M - 1.
+ */
+LL_API int loglinear_cache_step(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                                const void* q, const void* k, const void* v, const float* log_a,
+                                const float* lambda, void* out, int64_t n, int64_t L,
+                                int out_dtype, ll_stream_t stream);
+
+/*
+ * Puts n prompts of T positions into their slots, which give up what they held: the dense
+ * states after position T - 1 as loglinear_prefill writes them, and the last T mod 64 tokens.
+ * Where T is a multiple of 64 the levels that a step at T would merge are added into one page.
+ *   state     [n, H, L, dk, dv] fp32, 16-byte aligned; L >= bit_length(T - 1) + 1
+ *   k, v      the prompt's last Tk tokens, [n, Tk, Hqk, dk] and [n, Tk, H, dv] cache dtype,
+ *             Tk >= T mod 64;  log_a [n, Tk, H] fp32 or NULL.  Element strides of the batch,
+ *             position and head dimensions (features contiguous); NULL = dense.
+ */
+LL_API int loglinear_cache_load(const ll_cache* cache, const int32_t* slots, int64_t n,
+                                int64_t T, const float* state, int64_t L, const void* k,
+                                const ll_strides* k_strides, const void* v,
+                                const ll_strides* v_strides, const float* log_a,
+                                const ll_strides* log_a_strides, int64_t Tk, ll_stream_t stream);
+
+/*
+ * Dense states of n slots that hold pos[row] positions, from which loglinear_decode_step goes on
+ * at t = pos[row] (or loglinear_cache_load on another cache).  Levels that are empty are zero.
+ * Where pos is a multiple of 64, the levels that step pos merges are given as their sum, in
+ * the highest of them, lssb(pos).  A slot may be given twice.
+ *   state_out [n, H, L, dk, dv] fp32, 16-byte aligned; L >= M + 7
+ */
+LL_API int loglinear_cache_store(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                                 float* state_out, int64_t n, int64_t L, ll_stream_t stream);
+
+/*
+ * Slot dst[row] becomes a copy of slot src[row], which holds pos[row] positions; what it held is
+ * given up.  Pages are shared, the block's tokens copied.  A source may be given many times; a
+ * target is given once and is no row's source.
+ */
+LL_API int loglinear_cache_fork(const ll_cache* cache, const int32_t* src, const int32_t* dst,
+                                const int32_t* pos, int64_t n, ll_stream_t stream);
+
+/* The slots give up their pages. */
+LL_API int loglinear_cache_free(const ll_cache* cache, const int32_t* slots, int64_t n,
+                                ll_stream_t stream);
+
+/*
+ * Moves pages so that those in use are the lowest: the i-th lowest free page below their number
+ * takes the i-th lowest page in use above it.  *n_live (device int32) receives their number;
+ * the pages from there on are free.
+ */
+LL_API int loglinear_cache_compact(const ll_cache* cache, int32_t* n_live, ll_stream_t stream);
 
 /*
  * loglinear_fwd for callers that cannot allocate device memory.  The paper has no

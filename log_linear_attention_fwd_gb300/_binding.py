@@ -28,9 +28,19 @@ class LLStrides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("t", ctypes.c_int64), ("h", ctypes.c_int64)]
 
 
+class LLCache(ctypes.Structure):
+    """ll_cache: sizes and arrays of a paged decode cache."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("slots", "n_pages", "H", "Hqk", "dk", "dv",
+                                              "levels")] + \
+        [("dtype", ctypes.c_int)] + \
+        [(n, ctypes.c_void_p) for n in ("pages", "page_table", "refcount", "win_k", "win_v",
+                                        "win_log_a", "page_log", "page_from", "scratch", "error")]
+
+
 # Every symbol include/loglinear.h declares, with its ctypes signature.
 _i64, _int, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 _sp = ctypes.POINTER(LLStrides)
+_cp = ctypes.POINTER(LLCache)
 SIGNATURES = {
     "loglinear_version": (_int, []),
     "loglinear_status_string": (ctypes.c_char_p, [_int]),
@@ -72,6 +82,23 @@ SIGNATURES = {
     "loglinear_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                              _i64, _i64, _i64, _i64, _i64, _int, _int, _int, _vp, _sz, _vp, _sz,
                              _vp]),
+    "loglinear_glr_workspace_size": (_int, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
+    "loglinear_glr_fwd": (_int, [_vp, _sp, _vp, _sp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
+                                 _int, _int, _int, _int, _vp, _sz, _vp]),
+    "loglinear_glr_bwd": (_int, [_vp, _sp, _vp, _sp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _i64, _i64, _i64, _int, _int, _int, _int, _vp, _sz, _vp]),
+    "loglinear_glr_step": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int,
+                                  _int, _vp]),
+    "loglinear_cache_scratch_size": (_int, [_i64, _i64, ctypes.POINTER(_sz)]),
+    "loglinear_cache_reserve": (_int, [_cp, _vp, _vp, _i64, _vp]),
+    "loglinear_cache_step": (_int, [_cp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int,
+                                    _vp]),
+    "loglinear_cache_load": (_int, [_cp, _vp, _i64, _i64, _vp, _i64, _vp, _sp, _vp, _sp, _vp, _sp,
+                                    _i64, _vp]),
+    "loglinear_cache_store": (_int, [_cp, _vp, _vp, _vp, _i64, _i64, _vp]),
+    "loglinear_cache_fork": (_int, [_cp, _vp, _vp, _vp, _i64, _vp]),
+    "loglinear_cache_free": (_int, [_cp, _vp, _i64, _vp]),
+    "loglinear_cache_compact": (_int, [_cp, _vp, _vp]),
 }
 
 
@@ -466,3 +493,315 @@ def debug_level_map(T, chunk, path="auto", stream=None):
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_debug_level_map")
     return out
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+
+GLR_SCALES = {"none": 0, "one_minus": 1, "sqrt": 2}
+
+
+def _here(name, t, dtype=None, shape=None):
+    """_check_dev for one tensor of a call whose kernels run on the current device."""
+    if t is None:
+        return
+    _check_dev(name, t, dtype, shape)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _token_strides(name, t, shape, dtype=None, features=True):
+    """An input with strided batch, position (and head) dimensions, its features (if it has
+    any) contiguous: its strides, or None when dense."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return None
+    if features and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    s = t.stride()[:-1] if features else t.stride()
+    return ctypes.byref(LLStrides(s[0], s[1], s[2] if len(s) > 2 else 0))
+
+
+def _empty(stream, *shape, **kw):
+    """torch.empty owned by the stream the kernels run on, so that memory freed after the call
+    is only reused behind them."""
+    if stream is None:
+        return torch.empty(*shape, **kw)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, **kw)
+
+
+def glr_workspace_size(B, T, D) -> int:
+    out = ctypes.c_size_t(0)
+    st = _lib.loglinear_glr_workspace_size(B, T, D, ctypes.byref(out))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_glr_workspace_size")
+    return int(out.value)
+
+
+def _glr_workspace(workspace, B, T, D, device, stream):
+    if workspace is None:
+        n = glr_workspace_size(B, T, D)
+        workspace = _empty(stream, n, device=device, dtype=torch.uint8) if n else None
+    _here("workspace", workspace, torch.uint8)
+    return workspace, 0 if workspace is None else workspace.numel()
+
+
+def _glr_sequences(cu_seqlens, B):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have shape [N + 1]")
+    _here("cu_seqlens", cu_seqlens, torch.int32)
+    return cu_seqlens.numel() - 1
+
+
+def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None, out_dtype=None,
+                      state=None, workspace=None, stream=None):
+    """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + b_t x_t per channel; x, log_a
+    [B,T,D] (may be views with contiguous channels), log_a fp32 or x's dtype; scale: b = 1
+    ("none"), 1 - a ("one_minus") or sqrt(1 - a^2) ("sqrt").  cu_seqlens int32 [N+1] packs N
+    sequences into B = 1.  h0, state: [N,D] fp32 first states and, when given, where the last
+    ones go.  Returns out [B,T,D]."""
+    B, T, D = x.shape
+    xs = _token_strides("x", x, (B, T, D))
+    ls = _token_strides("log_a", log_a, (B, T, D))
+    N = _glr_sequences(cu_seqlens, B)
+    _here("h0", h0, torch.float32, (N, D))
+    _here("state", state, torch.float32, (N, D))
+    if out is None:
+        out = _empty(stream, B, T, D, device=x.device, dtype=out_dtype or x.dtype)
+    _here("out", out, shape=(B, T, D))
+    workspace, ws_bytes = _glr_workspace(workspace, B, T, D, x.device, stream)
+    st = _lib.loglinear_glr_fwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
+                                _ptr(out), _ptr(state), B, T, D, _dtype_code(x),
+                                _dtype_code(log_a), _dtype_code(out), GLR_SCALES[scale],
+                                _ptr(workspace), ws_bytes, _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_glr_fwd")
+    return out
+
+
+def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none", dstate=None,
+                      workspace=None, stream=None):
+    """Gradients of loglinear_glr_fwd: out is its result, dout (same dtype) the gradient of it,
+    dstate [N,D] fp32 that of the last states.  Returns (dx, dlog_a, dh0); dx in dout's dtype,
+    dlog_a in log_a's, dh0 fp32 (None without h0).  x may be None with scale "none"."""
+    B, T, D = log_a.shape
+    xs = _token_strides("x", x, (B, T, D))
+    ls = _token_strides("log_a", log_a, (B, T, D))
+    N = _glr_sequences(cu_seqlens, B)
+    _here("out", out, shape=(B, T, D))
+    _here("dout", dout, out.dtype, (B, T, D))
+    _here("h0", h0, torch.float32, (N, D))
+    _here("dstate", dstate, torch.float32, (N, D))
+    dx = _empty(stream, B, T, D, device=out.device, dtype=dout.dtype)
+    dla = _empty(stream, B, T, D, device=out.device, dtype=log_a.dtype)
+    dh0 = None if h0 is None else _empty(stream, N, D, device=out.device, dtype=torch.float32)
+    workspace, ws_bytes = _glr_workspace(workspace, B, T, D, out.device, stream)
+    gate = _dtype_code(log_a)
+    st = _lib.loglinear_glr_bwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
+                                _ptr(out), _ptr(dout), _ptr(dstate), _ptr(dx), _ptr(dla),
+                                _ptr(dh0), B, T, D, gate if x is None else _dtype_code(x), gate,
+                                _dtype_code(out), GLR_SCALES[scale], _ptr(workspace), ws_bytes,
+                                _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_glr_bwd")
+    return dx, dla, dh0
+
+
+def loglinear_glr_step(state, x, log_a, slots=None, scale="none", out=None, out_dtype=None,
+                       stream=None):
+    """One token of the recurrence per row: state [S,D] fp32 is updated in place at slots (int32
+    [B], -1 leaves the row out; None: row b is slot b).  x, log_a [B,D].  Returns out [B,D]."""
+    B, D = x.shape
+    _here("x", x)
+    _here("log_a", log_a, shape=(B, D))
+    if state.dim() != 2 or state.shape[1] != D:
+        raise ValueError(f"state has shape {tuple(state.shape)}, expected (S, {D})")
+    _here("state", state, torch.float32)
+    _here("slots", slots, torch.int32, (B,))
+    if out is None:
+        out = _empty(stream, B, D, device=x.device, dtype=out_dtype or x.dtype)
+    _here("out", out, shape=(B, D))
+    st = _lib.loglinear_glr_step(_ptr(state), state.shape[0], _ptr(slots), _ptr(x), _ptr(log_a),
+                                 _ptr(out), B, D, _dtype_code(x), _dtype_code(log_a),
+                                 _dtype_code(out), GLR_SCALES[scale], _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_glr_step")
+    return out
+
+
+# ---------------------------------------------------------------- paged decode cache
+
+CACHE_BLOCK = 64  # positions of a block (LL_CACHE_BLOCK)
+CACHE_ERR_SLOT, CACHE_ERR_POSITION, CACHE_ERR_PAGES, CACHE_ERR_MISSING = 1, 2, 4, 8
+
+
+class LogLinearCache:
+    """A paged decode cache over tensors of the caller's (see ll_cache in include/loglinear.h):
+    pages [n_pages,H,dk,dv] fp32, page_table [slots,M] int32 (-1: none), refcount [n_pages]
+    int32, win_k [slots,Hqk,64,dk] and win_v [slots,H,64,dv] (fp32 or bf16), win_log_a
+    [slots,H,64], page_log [slots,2,M,H] fp32 and page_from [slots,2] int32.  `empty` makes
+    them.  Calls on one cache have to be ordered: one stream, or events between streams."""
+
+    def __init__(self, pages, page_table, refcount, win_k, win_v, win_log_a, page_log, page_from):
+        P, H, dk, dv = pages.shape
+        S, M = page_table.shape
+        Hqk = win_k.shape[1]
+        _here("pages", pages, torch.float32)
+        _here("page_table", page_table, torch.int32)
+        _here("refcount", refcount, torch.int32, (P,))
+        _here("win_k", win_k, None, (S, Hqk, CACHE_BLOCK, dk))
+        _here("win_v", win_v, win_k.dtype, (S, H, CACHE_BLOCK, dv))
+        _here("win_log_a", win_log_a, torch.float32, (S, H, CACHE_BLOCK))
+        _here("page_log", page_log, torch.float32, (S, 2, M, H))
+        _here("page_from", page_from, torch.int32, (S, 2))
+        self.pages, self.page_table, self.refcount = pages, page_table, refcount
+        self.win_k, self.win_v, self.win_log_a = win_k, win_v, win_log_a
+        self.page_log, self.page_from = page_log, page_from
+        self.slots, self.levels, self.heads, self.qk_heads = S, M, H, Hqk
+        self.dk, self.dv, self.dtype, self.device = dk, dv, win_k.dtype, pages.device
+        size = ctypes.c_size_t(0)
+        st = _lib.loglinear_cache_scratch_size(S, P, ctypes.byref(size))
+        if st != LL_OK:
+            raise LoglinearError(st, "loglinear_cache_scratch_size")
+        self.scratch = torch.empty(size.value, device=pages.device, dtype=torch.uint8)
+        self.error_word = torch.zeros(1, device=pages.device, dtype=torch.int32)
+        self._struct = LLCache(S, P, H, Hqk, dk, dv, M, _dtype_code(win_k),
+                               *(t.data_ptr() for t in (pages, page_table, refcount, win_k, win_v,
+                                                        win_log_a, page_log, page_from,
+                                                        self.scratch, self.error_word)))
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, slots, n_pages, H, dk, dv, levels, Hqk=None, dtype=torch.bfloat16,
+              device="cuda"):
+        """A cache that holds nothing: `slots` sequences of fewer than 64 * 2^levels positions
+        over a pool of n_pages pages."""
+        Hqk = H if Hqk is None else Hqk
+
+        def new(*shape, dt=torch.float32):
+            return torch.zeros(*shape, device=device, dtype=dt)
+
+        i32 = torch.int32
+        return cls(pages=torch.empty(n_pages, H, dk, dv, device=device),
+                   page_table=torch.full((slots, levels), -1, device=device, dtype=i32),
+                   refcount=new(n_pages, dt=i32), win_k=new(slots, Hqk, CACHE_BLOCK, dk, dt=dtype),
+                   win_v=new(slots, H, CACHE_BLOCK, dv, dt=dtype),
+                   win_log_a=new(slots, H, CACHE_BLOCK), page_log=new(slots, 2, levels, H),
+                   page_from=new(slots, 2, dt=i32))
+
+    def error(self) -> int:
+        """Reads and clears the cache's error word (CACHE_ERR_* bits; synchronises)."""
+        bits = int(self.error_word.item())
+        if bits:
+            self.error_word.zero_()
+        return bits
+
+    def _rows(self, **named):
+        n = None
+        for name, t in named.items():
+            n = t.numel() if n is None else n
+            _here(name, t, torch.int32, (n,))
+        return n
+
+
+def loglinear_cache_reserve(cache, slots, pos, stream=None):
+    """The page reservation that goes before a loglinear_cache_step at the same slots and
+    positions (int32 [n] each): pages no longer live are given up, and slots at a block's last
+    position take the page it is folded into."""
+    n = cache._rows(slots=slots, pos=pos)
+    st = _lib.loglinear_cache_reserve(cache._ref, _ptr(slots), _ptr(pos), n, _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_reserve")
+
+
+def loglinear_cache_step(cache, slots, pos, q, k, v, log_a, lam, out=None, out_dtype=None,
+                         stream=None):
+    """One decode step for n rows, row i being slot slots[i] at position pos[i].  q, k [n,Hqk,dk],
+    v [n,H,dv] in the cache's dtype; log_a [n,H] fp32 or None; lam [n,H,L] fp32, L >= levels + 7.
+    Rows with slot -1 are left out (their out is not written).  Returns out [n,H,dv]."""
+    n = cache._rows(slots=slots, pos=pos)
+    L = lam.shape[-1]
+    _here("q", q, cache.dtype, (n, cache.qk_heads, cache.dk))
+    _here("k", k, cache.dtype, (n, cache.qk_heads, cache.dk))
+    _here("v", v, cache.dtype, (n, cache.heads, cache.dv))
+    _here("log_a", log_a, torch.float32, (n, cache.heads))
+    _here("lam", lam, torch.float32, (n, cache.heads, L))
+    if out is None:
+        out = _empty(stream, n, cache.heads, cache.dv, device=q.device, dtype=out_dtype or q.dtype)
+    _here("out", out, shape=(n, cache.heads, cache.dv))
+    st = _lib.loglinear_cache_step(cache._ref, _ptr(slots), _ptr(pos), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(log_a), _ptr(lam), _ptr(out), n, L, _dtype_code(out),
+                                   _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_step")
+    return out
+
+
+def loglinear_cache_load(cache, slots, T, state, k, v, log_a, stream=None):
+    """Puts n prompts of T positions into slots (int32 [n]), which give up what they held.  state
+    [n,H,L,dk,dv] fp32 as loglinear_prefill returns it; k [n,Tk,Hqk,dk], v [n,Tk,H,dv], log_a
+    [n,Tk,H] or None: the prompt's last Tk >= T mod 64 tokens (views such as k[:, -64:] do)."""
+    n = cache._rows(slots=slots)
+    L, Tk = state.shape[2], k.shape[1]
+    _here("state", state, torch.float32, (n, cache.heads, L, cache.dk, cache.dv))
+    sk = _token_strides("k", k, (n, Tk, cache.qk_heads, cache.dk), cache.dtype)
+    sv = _token_strides("v", v, (n, Tk, cache.heads, cache.dv), cache.dtype)
+    sa = _token_strides("log_a", log_a, (n, Tk, cache.heads), torch.float32, features=False)
+    st = _lib.loglinear_cache_load(cache._ref, _ptr(slots), n, T, _ptr(state), L, _ptr(k), sk,
+                                   _ptr(v), sv, _ptr(log_a), sa, Tk, _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_load")
+
+
+def loglinear_cache_store(cache, slots, pos, state=None, stream=None):
+    """Dense states [n,H,L,dk,dv] fp32 (L >= levels + 7) of slots that hold pos positions, from
+    which loglinear_decode_step goes on at t = pos.  Returns state."""
+    n = cache._rows(slots=slots, pos=pos)
+    if state is None:
+        state = _empty(stream, n, cache.heads, cache.levels + 7, cache.dk, cache.dv,
+                       device=cache.device)
+    L = state.shape[2]
+    _here("state", state, torch.float32, (n, cache.heads, L, cache.dk, cache.dv))
+    st = _lib.loglinear_cache_store(cache._ref, _ptr(slots), _ptr(pos), _ptr(state), n, L,
+                                    _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_store")
+    return state
+
+
+def loglinear_cache_fork(cache, src, dst, pos, stream=None):
+    """Slot dst[i] becomes a copy of slot src[i], which holds pos[i] positions (int32 [n] each):
+    pages are shared, the block's tokens copied."""
+    n = cache._rows(src=src, dst=dst, pos=pos)
+    st = _lib.loglinear_cache_fork(cache._ref, _ptr(src), _ptr(dst), _ptr(pos), n, _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_fork")
+
+
+def loglinear_cache_free(cache, slots, stream=None):
+    """The slots (int32 [n]) give up their pages."""
+    n = cache._rows(slots=slots)
+    st = _lib.loglinear_cache_free(cache._ref, _ptr(slots), n, _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_free")
+
+
+def loglinear_cache_compact(cache, live=None, stream=None):
+    """Moves pages so that those in use are the lowest.  Returns their number, int32 [1] on the
+    device."""
+    if live is None:
+        live = _empty(stream, 1, device=cache.device, dtype=torch.int32)
+    _here("live", live, torch.int32, (1,))
+    st = _lib.loglinear_cache_compact(cache._ref, _ptr(live), _stream(stream))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_compact")
+    return live

@@ -233,6 +233,51 @@ cudaError_t launch_gdn_fwd(const void* q, const void* k, const void* v, const fl
                            int T, int H, int Hqk, int dk, int dv, int L, int levels, int in_dtype,
                            int out_dtype, cudaStream_t s);
 
+// Gated linear recurrence (glr.cu).  x and log_a with batch and position strides; the other
+// arrays dense.
+struct GlrArgs {
+  const void* x;        // may be null in a backward without an input scale
+  const void* log_a;
+  int64_t sx[2], sl[2];
+  const float* h0;      // may be null
+  const int* cu;        // may be null: B sequences of T tokens
+  int N;
+  int B, T, D;
+  void* out;            // forward
+  float* state;         // may be null
+  const void* h;        // backward
+  const void* dout;
+  const float* dstate;  // may be null
+  void* dx;
+  void* dlog_a;
+  float* dh0;           // may be null
+};
+size_t glr_workspace_bytes(int64_t B, int64_t T, int64_t D);
+int64_t glr_tiles(int64_t B, int64_t T, int64_t D);  // CTAs of a launch, at most
+cudaError_t launch_glr(const GlrArgs& p, int in_dtype, int gate_dtype, int out_dtype, int scale,
+                       bool backward, void* ws, cudaStream_t s);
+cudaError_t launch_glr_step(float* state, const int* slots, int S, const void* x, const void* la,
+                            void* out, int B, int D, int in_dtype, int gate_dtype, int out_dtype,
+                            int scale, cudaStream_t s);
+cudaError_t glr_take_error(cudaStream_t s, unsigned* flags);
+
+// Paged decode cache (cache.cu).
+size_t cache_scratch_bytes(int64_t slots, int64_t n_pages);
+cudaError_t launch_cache_reserve(const ll_cache& c, const int* slots, const int* pos, int64_t n,
+                                 cudaStream_t s);  // pos null: free
+cudaError_t launch_cache_step(const ll_cache& c, const int* slots, const int* pos, const void* q,
+                              const void* k, const void* v, const float* log_a, const float* lam,
+                              void* out, int n, int L, int out_dtype, cudaStream_t s);
+cudaError_t launch_cache_load(const ll_cache& c, const int* slots, int64_t n, int T,
+                              const float* state, int L, const void* k, const int64_t* sk,
+                              const void* v, const int64_t* sv, const float* log_a,
+                              const int64_t* sa, int Tk, cudaStream_t s);
+cudaError_t launch_cache_store(const ll_cache& c, const int* slots, const int* pos, float* state,
+                               int64_t n, int L, cudaStream_t s);
+cudaError_t launch_cache_fork(const ll_cache& c, const int* src, const int* dst, const int* pos,
+                              int64_t n, cudaStream_t s);
+cudaError_t launch_cache_compact(const ll_cache& c, int* n_live, cudaStream_t s);
+
 cudaError_t launch_level_map(int T, int tile, int lc, int8_t* levels, cudaStream_t s);
 
 // Records a CUDA error for loglinear_last_cuda_error() and returns LL_ERR_CUDA.

@@ -625,10 +625,11 @@ int loglinear_bwd(const void* q, const void* k, const void* v, const float* log_
 
 int loglinear_device_error(ll_stream_t stream, unsigned* flags) {
   if (!flags) return LL_ERR_INVALID;
-  unsigned f1 = 0, f2 = 0;
+  unsigned f1 = 0, f2 = 0, f3 = 0;
   cudaError_t e = tc_take_error(reinterpret_cast<cudaStream_t>(stream), &f1);
   if (e == cudaSuccess) e = tcb_take_error(reinterpret_cast<cudaStream_t>(stream), &f2);
-  *flags = f1 | f2;
+  if (e == cudaSuccess) e = glr_take_error(reinterpret_cast<cudaStream_t>(stream), &f3);
+  *flags = f1 | f2 | f3 << 3;
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
 
@@ -642,6 +643,289 @@ int loglinear_debug_level_map(int64_t T, int chunk, int path, int8_t* levels,
   if (st != LL_OK) return st;
   const cudaError_t e = launch_level_map((int)T, tile, log2_exact(tile), levels,
                                          reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- gated linear recurrence
+
+namespace {
+
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t size_of(int dtype) { return dtype == LL_F32 ? 4 : 2; }
+
+int check_glr(int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype, int out_dtype,
+              int scale) {
+  if (B < 0 || T < 0 || D < 0) return LL_ERR_INVALID;
+  if (!dtype_ok(in_dtype) || !dtype_ok(gate_dtype) || !dtype_ok(out_dtype)) return LL_ERR_DTYPE;
+  if (scale != LL_GLR_NONE && scale != LL_GLR_ONE_MINUS && scale != LL_GLR_SQRT)
+    return LL_ERR_INVALID;
+  if (gate_dtype != LL_F32 && gate_dtype != in_dtype) return LL_ERR_UNSUPPORTED;
+  return LL_OK;
+}
+
+int check_glr_tiles(int64_t B, int64_t T, int64_t D) {
+  if (T > (1 << 30) || B > INT32_MAX || D > INT32_MAX - 64) return LL_ERR_UNSUPPORTED;
+  if (B > 0 && D > 0 && (B > INT32_MAX / ((D + 31) / 32) || glr_tiles(B, T, D) > INT32_MAX))
+    return LL_ERR_UNSUPPORTED;
+  return LL_OK;
+}
+
+// Checks and arguments that the forward and the backward share.  LL_OK with *empty: there are
+// no sequences or no channels.
+int glr_common(GlrArgs* a, const void* x, const ll_strides* xs, const void* log_a,
+               const ll_strides* ls, const float* h0, const int32_t* cu, int64_t N, int64_t B,
+               int64_t T, int64_t D, int in_dtype, int gate_dtype, bool x_needed,
+               void* workspace, size_t workspace_bytes, bool* empty) {
+  int st = check_glr_tiles(B, T, D);
+  if (st != LL_OK) return st;
+  if (cu && B != 1) return LL_ERR_INVALID;
+  if (cu && (N < 0 || N > INT32_MAX - 1)) return LL_ERR_INVALID;
+  const int64_t n = cu ? N : B;
+  *empty = n == 0 || D == 0;
+  if (*empty) return LL_OK;
+  if (T > 0 && ((x_needed && !x) || !log_a)) return LL_ERR_INVALID;
+  const size_t need = glr_workspace_bytes(B, T, D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return LL_ERR_WORKSPACE;
+  if (need > 0 && !aligned_to(workspace, 256)) return LL_ERR_ALIGN;
+  if (!aligned_to(x, size_of(in_dtype)) || !aligned_to(log_a, size_of(gate_dtype)) ||
+      !aligned_to(h0, 4) || !aligned_to(cu, 4))
+    return LL_ERR_ALIGN;
+  memset(a, 0, sizeof(*a));
+  a->x = x; a->log_a = log_a; a->h0 = h0; a->cu = cu; a->N = (int)n;
+  a->B = (int)B; a->T = (int)T; a->D = (int)D;
+  const ll_strides* given[2] = {xs, ls};
+  int64_t* to[2] = {a->sx, a->sl};
+  for (int i = 0; i < 2; ++i) {
+    to[i][0] = given[i] && B > 1 ? given[i]->b : T * D;
+    to[i][1] = given[i] && T > 1 ? given[i]->t : D;
+    if (to[i][0] < 0 || to[i][1] < 0) return LL_ERR_INVALID;
+  }
+  return LL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int loglinear_glr_workspace_size(int64_t B, int64_t T, int64_t D, size_t* bytes) {
+  if (!bytes || B < 0 || T < 0 || D < 0) return LL_ERR_INVALID;
+  const int st = check_glr_tiles(B, T, D);
+  if (st != LL_OK) return st;
+  *bytes = glr_workspace_bytes(B, T, D);
+  return LL_OK;
+}
+
+int loglinear_glr_fwd(const void* x, const ll_strides* x_strides, const void* log_a,
+                      const ll_strides* log_a_strides, const float* h0,
+                      const int32_t* cu_seqlens, int64_t N, void* out, float* state_out,
+                      int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype,
+                      int out_dtype, int scale, void* workspace, size_t workspace_bytes,
+                      ll_stream_t stream) {
+  int st = check_glr(B, T, D, in_dtype, gate_dtype, out_dtype, scale);
+  if (st != LL_OK) return st;
+  GlrArgs a;
+  bool empty;
+  st = glr_common(&a, x, x_strides, log_a, log_a_strides, h0, cu_seqlens, N, B, T, D, in_dtype,
+                  gate_dtype, true, workspace, workspace_bytes, &empty);
+  if (st != LL_OK || empty || (T == 0 && !state_out)) return st;
+  if (T > 0 && !out) return LL_ERR_INVALID;
+  if (!aligned_to(out, size_of(out_dtype)) || !aligned_to(state_out, 4)) return LL_ERR_ALIGN;
+  a.out = out;
+  a.state = state_out;
+  const cudaError_t e = launch_glr(a, in_dtype, gate_dtype, out_dtype, scale, false, workspace,
+                                   reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_glr_bwd(const void* x, const ll_strides* x_strides, const void* log_a,
+                      const ll_strides* log_a_strides, const float* h0,
+                      const int32_t* cu_seqlens, int64_t N, const void* h, const void* dout,
+                      const float* dstate, void* dx, void* dlog_a, float* dh0, int64_t B,
+                      int64_t T, int64_t D, int in_dtype, int gate_dtype, int grad_dtype,
+                      int scale, void* workspace, size_t workspace_bytes, ll_stream_t stream) {
+  int st = check_glr(B, T, D, in_dtype, gate_dtype, grad_dtype, scale);
+  if (st != LL_OK) return st;
+  GlrArgs a;
+  bool empty;
+  st = glr_common(&a, x, x_strides, log_a, log_a_strides, h0, cu_seqlens, N, B, T, D, in_dtype,
+                  gate_dtype, scale != LL_GLR_NONE, workspace, workspace_bytes, &empty);
+  if (st != LL_OK || empty || (T == 0 && !dh0)) return st;
+  if (T > 0 && (!h || !dout || !dx || !dlog_a)) return LL_ERR_INVALID;
+  const size_t g = size_of(grad_dtype);
+  if (!aligned_to(h, g) || !aligned_to(dout, g) || !aligned_to(dx, g) ||
+      !aligned_to(dlog_a, size_of(gate_dtype)) || !aligned_to(dstate, 4) || !aligned_to(dh0, 4))
+    return LL_ERR_ALIGN;
+  a.h = h; a.dout = dout; a.dstate = dstate; a.dx = dx; a.dlog_a = dlog_a; a.dh0 = dh0;
+  const cudaError_t e = launch_glr(a, in_dtype, gate_dtype, grad_dtype, scale, true, workspace,
+                                   reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_glr_step(float* state, int64_t S, const int32_t* slots, const void* x,
+                       const void* log_a, void* out, int64_t B, int64_t D, int in_dtype,
+                       int gate_dtype, int out_dtype, int scale, ll_stream_t stream) {
+  const int st = check_glr(B, 1, D, in_dtype, gate_dtype, out_dtype, scale);
+  if (st != LL_OK) return st;
+  if (S < 0) return LL_ERR_INVALID;
+  if (!slots && S < B) return LL_ERR_SHAPE;
+  if (B > 65535 || S > INT32_MAX || D > INT32_MAX - 1024) return LL_ERR_UNSUPPORTED;
+  if (B == 0 || D == 0) return LL_OK;
+  if (!state || !x || !log_a || !out) return LL_ERR_INVALID;
+  if (!aligned_to(state, 4) || !aligned_to(slots, 4) || !aligned_to(x, size_of(in_dtype)) ||
+      !aligned_to(log_a, size_of(gate_dtype)) || !aligned_to(out, size_of(out_dtype)))
+    return LL_ERR_ALIGN;
+  const cudaError_t e =
+      launch_glr_step(state, slots, (int)S, x, log_a, out, (int)B, (int)D, in_dtype, gate_dtype,
+                      out_dtype, scale, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- paged decode cache
+
+namespace {
+
+int check_cache(const ll_cache* c, int64_t n) {
+  if (!c || n < 0) return LL_ERR_INVALID;
+  if (c->slots < 1 || c->n_pages < 1 || c->H < 1 || c->dk < 1 || c->dv < 1 || c->levels < 1)
+    return LL_ERR_INVALID;
+  const int sh = check_qk_heads(c->H, c->Hqk);
+  if (sh != LL_OK) return sh;
+  if (!dtype_ok(c->dtype)) return LL_ERR_DTYPE;
+  if (c->dk > kMaxHeadDim || c->dv > kMaxHeadDim || c->dv % 4 != 0 || c->levels > 24 ||
+      c->n_pages > (1 << 30) || c->slots > INT32_MAX / 64 || c->H > INT32_MAX / 64)
+    return LL_ERR_UNSUPPORTED;
+  // rows x heads x column splits (at most 8) are a launch's CTAs
+  if (n > INT32_MAX / (8 * c->H)) return LL_ERR_UNSUPPORTED;
+  if (!c->pages || !c->page_table || !c->refcount || !c->win_k || !c->win_v || !c->win_log_a ||
+      !c->page_log || !c->page_from || !c->scratch || !c->error)
+    return LL_ERR_INVALID;
+  if (!aligned16(c->pages) || !aligned16(c->win_k) || !aligned16(c->win_v) ||
+      !aligned_to(c->page_table, 4) || !aligned_to(c->refcount, 4) ||
+      !aligned_to(c->win_log_a, 4) || !aligned_to(c->page_log, 4) ||
+      !aligned_to(c->page_from, 4) || !aligned_to(c->scratch, 4) || !aligned_to(c->error, 4))
+    return LL_ERR_ALIGN;
+  return LL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int loglinear_cache_scratch_size(int64_t slots, int64_t n_pages, size_t* bytes) {
+  if (!bytes || slots < 1 || n_pages < 1) return LL_ERR_INVALID;
+  if (n_pages > (1 << 30) || slots > INT32_MAX / 64) return LL_ERR_UNSUPPORTED;
+  *bytes = cache_scratch_bytes(slots, n_pages);
+  return LL_OK;
+}
+
+int loglinear_cache_reserve(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                            int64_t n, ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK || n == 0) return st;
+  if (!slots || !pos) return LL_ERR_INVALID;
+  if (!aligned_to(slots, 4) || !aligned_to(pos, 4)) return LL_ERR_ALIGN;
+  const cudaError_t e =
+      launch_cache_reserve(*cache, slots, pos, n, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_step(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                         const void* q, const void* k, const void* v, const float* log_a,
+                         const float* lambda, void* out, int64_t n, int64_t L, int out_dtype,
+                         ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK) return st;
+  if (!dtype_ok(out_dtype)) return LL_ERR_DTYPE;
+  if (L < cache->levels + 7) return LL_ERR_SHAPE;
+  if (L > 64) return LL_ERR_UNSUPPORTED;
+  if (n == 0) return LL_OK;
+  if (!slots || !pos || !q || !k || !v || !lambda || !out) return LL_ERR_INVALID;
+  const size_t e_in = size_of(cache->dtype);
+  if (!aligned_to(slots, 4) || !aligned_to(pos, 4) || !aligned_to(q, e_in) ||
+      !aligned_to(k, e_in) || !aligned_to(v, e_in) || !aligned_to(log_a, 4) ||
+      !aligned_to(lambda, 4) || !aligned_to(out, size_of(out_dtype)))
+    return LL_ERR_ALIGN;
+  const cudaError_t e = launch_cache_step(*cache, slots, pos, q, k, v, log_a, lambda, out, (int)n,
+                                          (int)L, out_dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_load(const ll_cache* cache, const int32_t* slots, int64_t n, int64_t T,
+                         const float* state, int64_t L, const void* k,
+                         const ll_strides* k_strides, const void* v, const ll_strides* v_strides,
+                         const float* log_a, const ll_strides* log_a_strides, int64_t Tk,
+                         ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK) return st;
+  if (T < 0 || L < 1 || Tk < 0) return LL_ERR_INVALID;
+  if (T > ((int64_t)LL_CACHE_BLOCK << cache->levels) - 1 || L > 64 || Tk > INT32_MAX)
+    return LL_ERR_UNSUPPORTED;
+  if (T > 0 && L < bit_length(T - 1) + 1) return LL_ERR_SHAPE;
+  if (Tk < T % LL_CACHE_BLOCK) return LL_ERR_SHAPE;
+  if (n == 0) return LL_OK;
+  if (!slots || (T > 0 && !state) || (T % LL_CACHE_BLOCK > 0 && (!k || !v))) return LL_ERR_INVALID;
+  const size_t e_in = size_of(cache->dtype);
+  if (!aligned_to(slots, 4) || !aligned16(state) || !aligned_to(k, e_in) || !aligned_to(v, e_in) ||
+      !aligned_to(log_a, 4))
+    return LL_ERR_ALIGN;
+  int64_t sk[3], sv[3], sa[3];
+  resolve_strides(k_strides, n, Tk, cache->Hqk, cache->dk, sk);
+  resolve_strides(v_strides, n, Tk, cache->H, cache->dv, sv);
+  resolve_strides(log_a_strides, n, Tk, cache->H, 1, sa);
+  for (int i = 0; i < 3; ++i)
+    if (sk[i] < 0 || sv[i] < 0 || sa[i] < 0) return LL_ERR_INVALID;
+  const cudaError_t e = launch_cache_load(*cache, slots, n, (int)T, state, (int)L, k, sk, v, sv,
+                                          log_a, sa, (int)Tk, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_store(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                          float* state_out, int64_t n, int64_t L, ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK) return st;
+  if (L < cache->levels + 7) return LL_ERR_SHAPE;
+  if (L > 64) return LL_ERR_UNSUPPORTED;
+  if (n == 0) return LL_OK;
+  if (!slots || !pos || !state_out) return LL_ERR_INVALID;
+  if (!aligned_to(slots, 4) || !aligned_to(pos, 4) || !aligned16(state_out)) return LL_ERR_ALIGN;
+  const cudaError_t e = launch_cache_store(*cache, slots, pos, state_out, n, (int)L,
+                                           reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_fork(const ll_cache* cache, const int32_t* src, const int32_t* dst,
+                         const int32_t* pos, int64_t n, ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK || n == 0) return st;
+  if (!src || !dst || !pos) return LL_ERR_INVALID;
+  if (!aligned_to(src, 4) || !aligned_to(dst, 4) || !aligned_to(pos, 4)) return LL_ERR_ALIGN;
+  const cudaError_t e =
+      launch_cache_fork(*cache, src, dst, pos, n, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_free(const ll_cache* cache, const int32_t* slots, int64_t n,
+                         ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK || n == 0) return st;
+  if (!slots) return LL_ERR_INVALID;
+  if (!aligned_to(slots, 4)) return LL_ERR_ALIGN;
+  const cudaError_t e =
+      launch_cache_reserve(*cache, slots, nullptr, n, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_compact(const ll_cache* cache, int32_t* n_live, ll_stream_t stream) {
+  const int st = check_cache(cache, 0);
+  if (st != LL_OK) return st;
+  if (!n_live) return LL_ERR_INVALID;
+  if (!aligned_to(n_live, 4)) return LL_ERR_ALIGN;
+  const cudaError_t e =
+      launch_cache_compact(*cache, n_live, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
 
