@@ -367,10 +367,9 @@ LL_API int loglinear_bwd(const void* q, const void* k, const void* v, const floa
  * not valid).  Bit 1: a wait for another tile's published state ran out of time (the
  * output of that tile is not valid).  Bit 2: loglinear_bwd was given a fwd_workspace
  * that a tensor-core loglinear_fwd with the same B, T, H, Hqk and dv did not write (its
- * layout tag does not match; the gradients are not valid).  Bit 3: a wait of loglinear_glr_fwd
- * or _bwd for the tile before ran out of time (the results are not valid).  Bit 4:
- * loglinear_glr_step was given a slot out of range, or one that an earlier row has (that
- * row was left out).  The launch itself still reported success.
+ * layout tag does not match; the gradients are not valid).  Bit 4: loglinear_glr_step was given
+ * a slot out of range, or one that an earlier row has (that row was left out).  The launch
+ * itself still reported success.
  */
 LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
 
@@ -395,22 +394,17 @@ LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
  *   out        [B, T, D] out_dtype: h_t
  *   state_out  NULL, or [N, D] fp32: the state after the last token (h0 for an empty sequence)
  * State, gates and sums are fp32; out is rounded once.
- * workspace: loglinear_glr_workspace_size() bytes (may be 0; then it may be NULL), 256-byte
- *   aligned, scratch; two calls that run concurrently need two.
  * Errors: LL_ERR_INVALID (null pointer, negative size or stride, unknown scale, cu_seqlens with
- * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T > 2^30, or more than 2^31 - 1 tiles),
- * LL_ERR_WORKSPACE, LL_ERR_ALIGN (a pointer not aligned to its element, the workspace),
- * LL_ERR_CUDA.  B, T or D = 0 is a no-op, but that state_out still receives h0.
+ * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T > 2^30, B or D or B * ceil(D / 64) above
+ * 2^27), LL_ERR_ALIGN (a pointer not aligned to its element), LL_ERR_CUDA.  B, T or D = 0 is a no-op, but that state_out still receives h0.
  */
 typedef enum { LL_GLR_NONE = 0, LL_GLR_ONE_MINUS = 1, LL_GLR_SQRT = 2 } ll_glr_scale;
 
-LL_API int loglinear_glr_workspace_size(int64_t B, int64_t T, int64_t D, size_t* bytes);
 LL_API int loglinear_glr_fwd(const void* x, const ll_strides* x_strides, const void* log_a,
                              const ll_strides* log_a_strides, const float* h0,
                              const int32_t* cu_seqlens, int64_t N, void* out, float* state_out,
                              int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype,
-                             int out_dtype, int scale, void* workspace, size_t workspace_bytes,
-                             ll_stream_t stream);
+                             int out_dtype, int scale, ll_stream_t stream);
 
 /*
  * Gradients of loglinear_glr_fwd, given dout = dL/d out and (or NULL) dstate = dL/d state_out:
@@ -421,15 +415,14 @@ LL_API int loglinear_glr_fwd(const void* x, const ll_strides* x_strides, const v
  *   h, dout, dx   [B, T, D] grad_dtype, dense;  dlog_a [B, T, D] gate_dtype, dense
  *   x             may be NULL with LL_GLR_NONE, whose gradients do not read it
  *   dstate, dh0   [N, D] fp32 or NULL (dh0 of an empty sequence is its dstate, or zero)
- * x, log_a, h0, cu_seqlens, N, sizes, workspace and errors as loglinear_glr_fwd.
+ * x, log_a, h0, cu_seqlens, N, sizes and errors as loglinear_glr_fwd.
  */
 LL_API int loglinear_glr_bwd(const void* x, const ll_strides* x_strides, const void* log_a,
                              const ll_strides* log_a_strides, const float* h0,
                              const int32_t* cu_seqlens, int64_t N, const void* h,
                              const void* dout, const float* dstate, void* dx, void* dlog_a,
                              float* dh0, int64_t B, int64_t T, int64_t D, int in_dtype,
-                             int gate_dtype, int grad_dtype, int scale, void* workspace,
-                             size_t workspace_bytes, ll_stream_t stream);
+                             int gate_dtype, int grad_dtype, int scale, ll_stream_t stream);
 
 /*
  * One token of the recurrence for each of B rows: state[slot] <- a state[slot] + b x, out = the new

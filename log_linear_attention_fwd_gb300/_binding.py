@@ -82,11 +82,10 @@ SIGNATURES = {
     "loglinear_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                              _i64, _i64, _i64, _i64, _i64, _int, _int, _int, _vp, _sz, _vp, _sz,
                              _vp]),
-    "loglinear_glr_workspace_size": (_int, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
     "loglinear_glr_fwd": (_int, [_vp, _sp, _vp, _sp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
-                                 _int, _int, _int, _int, _vp, _sz, _vp]),
+                                 _int, _int, _int, _int, _vp]),
     "loglinear_glr_bwd": (_int, [_vp, _sp, _vp, _sp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
-                                 _i64, _i64, _i64, _int, _int, _int, _int, _vp, _sz, _vp]),
+                                 _i64, _i64, _i64, _int, _int, _int, _int, _vp]),
     "loglinear_glr_step": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int,
                                   _int, _vp]),
     "loglinear_cache_scratch_size": (_int, [_i64, _i64, ctypes.POINTER(_sz)]),
@@ -537,22 +536,6 @@ def _empty(stream, *shape, **kw):
         return torch.empty(*shape, **kw)
 
 
-def glr_workspace_size(B, T, D) -> int:
-    out = ctypes.c_size_t(0)
-    st = _lib.loglinear_glr_workspace_size(B, T, D, ctypes.byref(out))
-    if st != LL_OK:
-        raise LoglinearError(st, "loglinear_glr_workspace_size")
-    return int(out.value)
-
-
-def _glr_workspace(workspace, B, T, D, device, stream):
-    if workspace is None:
-        n = glr_workspace_size(B, T, D)
-        workspace = _empty(stream, n, device=device, dtype=torch.uint8) if n else None
-    _here("workspace", workspace, torch.uint8)
-    return workspace, 0 if workspace is None else workspace.numel()
-
-
 def _glr_sequences(cu_seqlens, B):
     if cu_seqlens is None:
         return B
@@ -563,7 +546,7 @@ def _glr_sequences(cu_seqlens, B):
 
 
 def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None, out_dtype=None,
-                      state=None, workspace=None, stream=None):
+                      state=None, stream=None):
     """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + b_t x_t per channel; x, log_a
     [B,T,D] (may be views with contiguous channels), log_a fp32 or x's dtype; scale: b = 1
     ("none"), 1 - a ("one_minus") or sqrt(1 - a^2) ("sqrt").  cu_seqlens int32 [N+1] packs N
@@ -578,18 +561,17 @@ def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None
     if out is None:
         out = _empty(stream, B, T, D, device=x.device, dtype=out_dtype or x.dtype)
     _here("out", out, shape=(B, T, D))
-    workspace, ws_bytes = _glr_workspace(workspace, B, T, D, x.device, stream)
     st = _lib.loglinear_glr_fwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
                                 _ptr(out), _ptr(state), B, T, D, _dtype_code(x),
                                 _dtype_code(log_a), _dtype_code(out), GLR_SCALES[scale],
-                                _ptr(workspace), ws_bytes, _stream(stream))
+                                _stream(stream))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_fwd")
     return out
 
 
 def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none", dstate=None,
-                      workspace=None, stream=None):
+                      stream=None):
     """Gradients of loglinear_glr_fwd: out is its result, dout (same dtype) the gradient of it,
     dstate [N,D] fp32 that of the last states.  Returns (dx, dlog_a, dh0); dx in dout's dtype,
     dlog_a in log_a's, dh0 fp32 (None without h0).  x may be None with scale "none"."""
@@ -604,13 +586,11 @@ def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none
     dx = _empty(stream, B, T, D, device=out.device, dtype=dout.dtype)
     dla = _empty(stream, B, T, D, device=out.device, dtype=log_a.dtype)
     dh0 = None if h0 is None else _empty(stream, N, D, device=out.device, dtype=torch.float32)
-    workspace, ws_bytes = _glr_workspace(workspace, B, T, D, out.device, stream)
     gate = _dtype_code(log_a)
     st = _lib.loglinear_glr_bwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
                                 _ptr(out), _ptr(dout), _ptr(dstate), _ptr(dx), _ptr(dla),
                                 _ptr(dh0), B, T, D, gate if x is None else _dtype_code(x), gate,
-                                _dtype_code(out), GLR_SCALES[scale], _ptr(workspace), ws_bytes,
-                                _stream(stream))
+                                _dtype_code(out), GLR_SCALES[scale], _stream(stream))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_bwd")
     return dx, dla, dh0

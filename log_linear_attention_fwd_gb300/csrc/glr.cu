@@ -2,18 +2,19 @@
 // b_t = 1, 1 - a_t or sqrt(1 - a_t^2); its gradients; and its single-token step.
 //
 // Forward and backward are one scan each.  The maps c -> A c + H of consecutive tokens compose
-// to a map of the same form, so a segment of tokens is known by two floats per channel.  A CTA
-// takes a tile of 8 * S tokens by 32 * V channels: lane = V adjacent channels, warp = S
-// consecutive tokens, whose inputs stay in registers.  Each warp folds its S tokens, the CTA
-// folds its 8 warps, publishes the tile's (A, H), folds its predecessors' maps back to the
-// first whose carry is final (a decoupled look-back, kLook predecessors at a time), publishes
-// its own carry and then runs its tokens once more from the carry, in registers.  Every input
-// is read once and every output written once; the published maps add 24 / (8 S) bytes to the
-// 8 to 16 bytes an element moves.  The backward is the same scan with time reversed.
+// to a map of the same form, so a segment of tokens is known by two floats per channel.  A
+// cluster of Z CTAs owns 64 channels of one batch entry and marches through time, Z tiles of
+// 8 S tokens per step: lane = 2 channels, warp = S consecutive tokens, which it folds into one
+// map; the CTA folds its 8 warps' maps and hands the result to every CTA of the cluster through
+// distributed shared memory; after one cluster barrier each CTA knows the carry into its
+// tile and, from all Z maps, the carry into the next step.  Then the warps run their tokens
+// from their carry, in registers.  Every input is read once and every output written once,
+// nothing goes through global memory in between, no CTA waits on a flag, and the folds have a
+// fixed order, so results do not depend on timing.  The next tile's inputs are copied to
+// shared memory (cp.async) while this one is worked on.
 //
-// Tiles are taken by ticket, oldest time first, so a CTA only ever waits for tiles that are
-// already running.  The wait is bounded (kWaitLimitNs): a CTA that gives up raises the device
-// error word and publishes zeros, so that the tiles after it do not wait in turn.
+// Z is chosen so that batch entries x channel blocks x Z CTAs fill the GPU (cluster_of).
+// The backward is the same scan with time reversed.
 //
 // A sequence start is a reset: its map ignores the carry.  It is marked by A = -0.0 (a real A
 // is never negative), not by A = 0, because 0 * inf would let an overflow of one sequence
@@ -25,73 +26,130 @@
 
 namespace ll {
 
-// bit 0: a look-back wait ran out of time; bit 1: a step was given a slot that is out of range
-// or given twice
+// bit 0: a step was given a slot that is out of range or given twice
 __device__ unsigned int g_glr_error = 0;
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCh = 64;        // channels of a CTA: two per lane
+constexpr int kMaxCluster = 8;
 
-// ---------------------------------------------------------------- element access
+// ---------------------------------------------------------------- gates
 
-// V adjacent elements; V = 2 needs alignment to 2 elements.
-template <typename T, int V>
-struct Pack;
-template <>
-struct Pack<float, 1> {
-  float r;
-  __device__ __forceinline__ void load(const float* p) { r = *p; }
-  __device__ __forceinline__ float get(int) const { return r; }
-  static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
-};
-template <>
-struct Pack<float, 2> {
-  float2 r;
-  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float2*>(p); }
-  __device__ __forceinline__ float get(int i) const { return i ? r.y : r.x; }
-  static __device__ __forceinline__ void store(float* p, const float* v) {
-    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-  }
-};
-template <>
-struct Pack<__nv_bfloat16, 1> {
-  __nv_bfloat16 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *p; }
-  __device__ __forceinline__ float get(int) const { return __bfloat162float(r); }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *p = __float2bfloat16_rn(v[0]);
-  }
-};
-template <>
-struct Pack<__nv_bfloat16, 2> {
-  __nv_bfloat162 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = *reinterpret_cast<const __nv_bfloat162*>(p);
-  }
-  __device__ __forceinline__ float get(int i) const {
-    return i ? __high2float(r) : __low2float(r);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
-  }
-};
+// a = exp(la) and m = 1 - a.  Gates live near a = 1, where 1 - a computed from a would lose the
+// digits that la still has: for |la| <= 1/2 the Taylor sum of exp(la) - 1 (8 terms, its
+// remainder is below 2^-27) gives m, and a from it to half a unit; beyond, exp itself is far
+// enough from 1.  The terms cost 8 multiply-adds; expf and expm1f together three times that.
+__device__ __forceinline__ void gate_of(float la, float* a, float* m) {
+  float p = 1.f / 40320.f;
+  p = fmaf(p, la, 1.f / 5040.f);
+  p = fmaf(p, la, 1.f / 720.f);
+  p = fmaf(p, la, 1.f / 120.f);
+  p = fmaf(p, la, 1.f / 24.f);
+  p = fmaf(p, la, 1.f / 6.f);
+  p = fmaf(p, la, 0.5f);
+  p = fmaf(p, la, 1.f);
+  p *= la;
+  const float e = __expf(la);
+  const bool near = fabsf(la) <= 0.5f;
+  *a = near ? 1.f + p : e;
+  *m = near ? -p : 1.f - e;
+}
 
-// b(log a), and with kGrad its derivative.  The differences from 1 go through expm1: near
-// a = 1, where such gates live, 1 - a would lose the digits that a itself still has.
-// At a = 1 (log a >= 0) the square root's b is 0 and its infinite derivative is taken as 0.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error below 2^-22
+  return y;
+}
+
+// b from a and m: 1 - a^2 = m (2 - m).  0 where a >= 1.
 template <int kScale>
-__device__ __forceinline__ float scale_of(float la) {
-  if (kScale == LL_GLR_ONE_MINUS) return -expm1f(la);
-  if (kScale == LL_GLR_SQRT) return sqrtf(fmaxf(-expm1f(2.f * la), 0.f));
+__device__ __forceinline__ float scale_of(float m) {
+  if (kScale == LL_GLR_ONE_MINUS) return m;
+  if (kScale == LL_GLR_SQRT) {
+    const float v = m * (2.f - m);
+    return sqrt_approx(v < 0.f ? 0.f : v);  // a NaN stays one
+  }
   return 1.f;
 }
+// db / d log a.  The square root's is infinite at a = 1 and taken as 0 there.
 template <int kScale>
 __device__ __forceinline__ float scale_grad(float a, float b) {
   if (kScale == LL_GLR_ONE_MINUS) return -a;
-  if (kScale == LL_GLR_SQRT) return b > 0.f ? -a * a / b : 0.f;
+  if (kScale == LL_GLR_SQRT) return b > 0.f ? -__fdividef(a * a, b) : 0.f;
   return 0.f;
+}
+
+// ---------------------------------------------------------------- element access
+
+__device__ __forceinline__ float2 pair_of(const float* p) {
+  return *reinterpret_cast<const float2*>(p);
+}
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ void put_pair(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void put_pair(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
+// How a pair of channels goes to global memory: both at once, one by one, or only the first.
+enum { kPairs = 0, kSingles = 1, kFirst = 2 };
+template <typename T>
+__device__ __forceinline__ void store_pair(T* p, float2 v, int how) {
+  if (how == kPairs) {
+    put_pair(p, v);
+  } else {
+    p[0] = from_f32<T>(v.x);
+    if (how == kSingles) p[1] = from_f32<T>(v.y);
+  }
+}
+__device__ __forceinline__ float2 load_state(const float* p, int how) {
+  return make_float2(p[0], how == kFirst ? 0.f : p[1]);
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Rows [lo, hi) of a tile [kRows][64] of which `cols` channels exist, src addressing row 0.
+// bytes: the widest copy that pointers, strides and the number of channels allow (16, 4 or one
+// element).  What is not copied keeps its old contents, which no live lane uses.
+template <typename T, int kRows>
+__device__ __forceinline__ void fill(T* dst, const T* src, int64_t stride, int lo, int hi,
+                                     int cols, int bytes) {
+  if (bytes == 16) {
+    constexpr int per = 16 / sizeof(T), chunks = kCh / per;
+#pragma unroll
+    for (int i = threadIdx.x; i < kRows * chunks; i += kThreads) {
+      const int r = i / chunks, c = (i % chunks) * per;
+      if (r >= lo && r < hi && c < cols) cp_async16(dst + r * kCh + c, src + r * stride + c);
+    }
+  } else if (bytes == 4) {
+    constexpr int per = 4 / sizeof(T), chunks = kCh / per;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kRows * chunks; i += kThreads) {
+      const int r = i / chunks, c = (i % chunks) * per;
+      if (r >= lo && r < hi && c < cols)
+        tc::cp_async4(dst + r * kCh + c, src + r * stride + c, 4);
+    }
+  } else {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kRows * kCh; i += kThreads) {
+      const int r = i / kCh, c = i % kCh;
+      if (r >= lo && r < hi && c < cols) dst[r * kCh + c] = src[r * stride + c];
+    }
+  }
 }
 
 // ---------------------------------------------------------------- maps c -> A c + H
@@ -99,10 +157,10 @@ __device__ __forceinline__ float scale_grad(float a, float b) {
 __device__ __forceinline__ float apply(float A, float H, float c) {
   return signbit(A) ? H : fmaf(A, c, H);
 }
-// (A, H) after (A0, H0), into (A0, H0).
-__device__ __forceinline__ void then(float& A0, float& H0, float A, float H) {
-  H0 = apply(A, H, H0);
-  A0 = signbit(A) || signbit(A0) ? -0.f : A * A0;
+// (A, H) after m, into m.
+__device__ __forceinline__ void then(float2& m, float2 n) {
+  m.y = apply(n.x, n.y, m.y);
+  m.x = signbit(n.x) || signbit(m.x) ? -0.f : n.x * m.x;
 }
 
 // ---------------------------------------------------------------- sequences
@@ -140,12 +198,13 @@ __device__ __forceinline__ Span span_of(const int* cu, int N, int T, int b, int 
     if (e <= s) continue;
     if (s >= lo) r.first |= 1u << (s - lo);
     if (e <= hi && e > lo) r.last |= 1u << (e - 1 - lo);
-    for (int t = max(s, lo); t < min(e, hi); ++t) r.on |= 1u << (t - lo);
+    const int f = max(s, lo) - lo, g = min(e, hi) - lo;
+    if (g > f) r.on |= ((1u << (g - f)) - 1u) << f;
   }
   return r;
 }
 
-// The sequence after n that is not empty (callers stop at the last one themselves).
+// The sequence after (before) n that is not empty; callers stop at the last (first) themselves.
 __device__ __forceinline__ int next_sequence(const int* cu, int N, int n) {
   if (!cu) return n;
   do ++n;
@@ -159,257 +218,195 @@ __device__ __forceinline__ int previous_sequence(const int* cu, int n) {
   return max(n, 0);
 }
 
-// ---------------------------------------------------------------- look-back
+// ---------------------------------------------------------------- the cluster's scan
 
-constexpr int kAgg = 1, kFinal = 2;  // flag values: the tile's map, and also its carry
-
-__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void store_release(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-
-// Waits until a tile has published something; 0 if it does not within the limit.
-__device__ __forceinline__ uint32_t wait_flag(const uint32_t* p) {
-  uint32_t v = load_acquire(p);
-  if (v) return v;
-  const uint64_t t0 = tc::global_timer_ns();
-  while (!(v = load_acquire(p)))
-    if (tc::global_timer_ns() - t0 > tc::kWaitLimitNs) return 0;
-  return v;
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Writes v to the same shared-memory address of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote(float2* p, uint32_t rank, float2 v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
 }
 
-struct Link {
-  float* A;          // [tiles][CH] the tiles' maps and
-  float* H;
-  float* C;          // final carries, of this batch entry and channel block
-  uint32_t* flags;   // [tiles]
-};
-
-template <int CH>
 struct LinkSmem {
-  float A[kWarps][CH], H[kWarps][CH];  // the warps' maps
-  float lA[kThreads / CH][CH], lH[kThreads / CH][CH];
-  float carry[CH];
-  uint32_t flag[kThreads / CH];
-  uint32_t ticket;
+  float2 warp[kWarps][kCh];            // the warps' maps
+  float2 tile[2][kMaxCluster][kCh];    // the cluster's tiles' maps, of even and odd steps
+  float carry[kCh];                    // into this CTA's tile
 };
 
-// The carry into tile i: publishes the tile's map, folds the predecessors' and publishes the
-// tile's own carry.  Leaves the carry in sm.carry.  All threads call it, after the warps' maps
-// are in sm.A and sm.H (no barrier in between needed).
-template <int CH>
-__device__ __forceinline__ void link_tile(LinkSmem<CH>& sm, const Link& k, int i, int tiles) {
-  constexpr int kLook = kThreads / CH;
-  const int tid = threadIdx.x, ch = tid % CH, grp = tid / CH;
-  float A = 1.f, H = 0.f;
+// After the warps' maps of step k are in sm.warp: the carry into this CTA's tile goes to
+// sm.carry, and `c` (threads below 64, their channel's carry into the step) moves on to the
+// next step.  All threads of the cluster call it; ends with a block barrier.
+__device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, float& c) {
+  const int tid = threadIdx.x;
   __syncthreads();
-  if (tid < CH) {
-    A = sm.A[0][ch];
-    H = sm.H[0][ch];
+  if (tid < kCh) {
+    float2 m = sm.warp[0][tid];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) then(A, H, sm.A[w][ch], sm.H[w][ch]);
-    if (i == 0) sm.carry[ch] = 0.f;
-    if (tiles > 1) {
-      if (i == 0) {
-        __stcg(k.C + ch, apply(A, H, 0.f));
-      } else {
-        __stcg(k.A + (int64_t)i * CH + ch, A);
-        __stcg(k.H + (int64_t)i * CH + ch, H);
+    for (int w = 1; w < kWarps; ++w) then(m, sm.warp[w][tid]);
+    if (Z == 1) {
+      sm.carry[tid] = c;
+      c = apply(m.x, m.y, c);
+    } else {
+      for (int z = 0; z < Z; ++z) store_remote(&sm.tile[k & 1][rank][tid], z, m);
+    }
+  }
+  if (Z > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (tid < kCh) {
+      for (int z = 0; z < Z; ++z) {
+        if (z == rank) sm.carry[tid] = c;
+        const float2 m = sm.tile[k & 1][z][tid];
+        c = apply(m.x, m.y, c);
       }
     }
   }
   __syncthreads();
-  if (tiles == 1) return;
-  if (tid == 0) store_release(k.flags + i, i == 0 ? kFinal : kAgg);
-  if (i == 0) return;
-  // the predecessors i-1, i-2, ... in groups of kLook, nearest first
-  float bA = 1.f, bH = 0.f;  // (threads below CH) the map of what has been folded so far
-  for (int top = i - 1;; top -= kLook) {
-    const int j = top - grp;
-    if (ch == 0) {
-      uint32_t f = kFinal;
-      if (j >= 0 && !(f = wait_flag(k.flags + j))) {
-        atomicOr(&g_glr_error, 1u);
-        f = 3u;
-      }
-      sm.flag[grp] = f;
-    }
-    __syncthreads();
-    const uint32_t f = sm.flag[grp];
-    float a = -0.f, h = 0.f;
-    if (j >= 0 && f != 3u) {
-      if (f == kFinal) {
-        h = __ldcg(k.C + (int64_t)j * CH + ch);
-      } else {
-        a = __ldcg(k.A + (int64_t)j * CH + ch);
-        h = __ldcg(k.H + (int64_t)j * CH + ch);
-      }
-    }
-    sm.lA[grp][ch] = a;
-    sm.lH[grp][ch] = h;
-    bool done = false;
-#pragma unroll
-    for (int g = 0; g < kLook; ++g) done |= sm.flag[g] != kAgg;
-    __syncthreads();
-    if (tid < CH) {
-#pragma unroll
-      for (int g = 0; g < kLook; ++g) {  // the map so far comes after the farther one
-        float fA = sm.lA[g][ch], fH = sm.lH[g][ch];
-        then(fA, fH, bA, bH);
-        bA = fA;
-        bH = fH;
-      }
-    }
-    if (done) break;
-  }
-  if (tid < CH) {
-    const float c = bH;  // a final carry resets, so nothing before it is left in bA
-    sm.carry[ch] = c;
-    __stcg(k.C + (int64_t)i * CH + ch, apply(A, H, c));
-  }
-  __syncthreads();
-  if (tid == 0) store_release(k.flags + i, kFinal);
 }
 
 // The carry into warp w's tokens, from the tile's and the warps before it.
-template <int CH>
-__device__ __forceinline__ float warp_carry(const LinkSmem<CH>& sm, int w, int ch) {
-  float c = sm.carry[ch];
-  for (int u = 0; u < w; ++u) c = apply(sm.A[u][ch], sm.H[u][ch], c);
+__device__ __forceinline__ float2 warp_carry(const LinkSmem& sm, int w, int cl) {
+  float2 c = *reinterpret_cast<const float2*>(&sm.carry[cl]);
+  for (int u = 0; u < w; ++u) {
+    const float4 m = *reinterpret_cast<const float4*>(&sm.warp[u][cl]);
+    c.x = apply(m.x, m.y, c.x);
+    c.y = apply(m.z, m.w, c.y);
+  }
   return c;
 }
 
 struct Geometry {
-  int tiles, blocks;  // tiles of time, blocks of channels
-  float* agg;         // [3][B][blocks][tiles][CH]
-  uint32_t* flags;    // [B][blocks][tiles], then the ticket
+  int Z;          // CTAs of a cluster
+  int blocks;     // channel blocks
+  int pairs;      // the outputs and states can be written two channels at a time
+  int x, la, h, dout;  // bytes of a copy (fill)
 };
 
-// This CTA's tile (time, channel block, batch entry), by ticket.
-template <int CH>
-__device__ __forceinline__ void take_tile(LinkSmem<CH>& sm, const Geometry& g, int B, int* i,
-                                          int* blk, int* b) {
-  const int per = g.blocks * B;
-  uint32_t ticket = blockIdx.x;
-  if (g.tiles > 1) {
-    if (threadIdx.x == 0) sm.ticket = atomicAdd(g.flags + (int64_t)g.tiles * per, 1u);
-    __syncthreads();
-    ticket = sm.ticket;
-  }
-  *i = ticket / per;
-  const int rest = ticket - *i * per;
-  *b = rest / g.blocks;
-  *blk = rest - *b * g.blocks;
-}
-
-template <int CH>
-__device__ __forceinline__ Link link_of(const Geometry& g, int B, int blk, int b) {
-  const int64_t line = (int64_t)b * g.blocks + blk, all = (int64_t)B * g.blocks * g.tiles * CH;
-  Link k;
-  k.A = g.agg + line * g.tiles * CH;
-  k.H = k.A + all;
-  k.C = k.H + all;
-  k.flags = g.flags + line * g.tiles;
-  return k;
-}
-
 // Sequences without tokens: their state is the one they came with (dst = src, or zero).
-template <int V>
 __device__ __forceinline__ void empty_sequences(const int* cu, int N, int T, int b, int D, int ch,
-                                                const float* src, float* dst) {
-  if (!dst || ch >= D) return;
+                                                int how, const float* src, float* dst) {
+  if (!dst) return;
   const int w = threadIdx.x >> 5;
   const int n0 = cu ? w : (w == 0 && T == 0 ? b : N), step = cu ? kWarps : N;
   for (int n = n0; n < N; n += step) {
     if (cu && __ldg(cu + n + 1) > __ldg(cu + n)) continue;
-    for (int v = 0; v < V; ++v)
-      dst[(int64_t)n * D + ch + v] = src ? src[(int64_t)n * D + ch + v] : 0.f;
+    const int64_t at = (int64_t)n * D + ch;
+    store_pair(dst + at, src ? load_state(src + at, how) : make_float2(0.f, 0.f), how);
   }
 }
 
 // ---------------------------------------------------------------- forward
 
-template <typename InT, typename GateT, typename OutT, int V, int S, int kScale>
+template <typename InT, typename GateT, int S>
+struct FwdStage {
+  GateT la[kWarps * S][kCh];
+  InT x[kWarps * S][kCh];
+};
+
+constexpr int kFwdStages = 2;
+
+template <typename InT, typename GateT, typename OutT, int S, int kScale>
 __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometry geo) {
-  constexpr int CH = 32 * V;
-  __shared__ LinkSmem<CH> sm;
-  int i, blk, b;
-  take_tile(sm, geo, p.B, &i, &blk, &b);
+  constexpr int kRows = kWarps * S;
+  using Stage = FwdStage<InT, GateT, S>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Stage* stages = reinterpret_cast<Stage*>(dyn);
+  __shared__ __align__(16) LinkSmem sm;
+  const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
+  if (Z > 1) cluster_arrive();
+  const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int cl = lane * V, ch = blk * CH + cl;
-  const int lo = (i * kWarps + w) * S;
+  const int cl = 2 * lane, ch = blk * kCh + cl;
   const bool live = ch < p.D;
-  const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + ch;
-  const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + ch;
-  Pack<InT, V> xr[S];
-  Pack<GateT, V> lr[S];
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (live && lo + s < p.T) {
-      lr[s].load(la + (int64_t)(lo + s) * p.sl[1]);
-      xr[s].load(x + (int64_t)(lo + s) * p.sx[1]);
+  const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
+  const int cols = min(kCh, p.D - blk * kCh);
+  const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + blk * kCh;
+  const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + blk * kCh;
+  OutT* out = static_cast<OutT*>(p.out) + (int64_t)b * p.T * p.D + ch;
+  const int steps = (p.T + Z * kRows - 1) / (Z * kRows);
+  auto issue = [&](int k) {
+    if (k < steps) {
+      Stage& st = stages[k % kFwdStages];
+      const int t0 = (k * Z + rank) * kRows, rows = min(kRows, p.T - t0);
+      fill<GateT, kRows>(&st.la[0][0], la + (int64_t)t0 * p.sl[1], p.sl[1], 0, rows, cols, geo.la);
+      fill<InT, kRows>(&st.x[0][0], x + (int64_t)t0 * p.sx[1], p.sx[1], 0, rows, cols, geo.x);
     }
-  const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
-  if (i == 0) empty_sequences<V>(p.cu, p.N, p.T, b, p.D, ch, p.h0, p.state);
-  float a[S][V], u[S][V], A[V], H[V];
+    cp_async_commit();
+  };
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = 1.f;
-    H[v] = 0.f;
-  }
-  int n = span.n0;
+  for (int k = 0; k < kFwdStages - 1; ++k) issue(k);
+  if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
+  if (Z > 1) cluster_wait();
+  float c = 0.f;
+  for (int k = 0; k < steps; ++k) {
+    cp_async_wait<kFwdStages - 2>();
+    __syncthreads();
+    issue(k + kFwdStages - 1);
+    const Stage& st = stages[k % kFwdStages];
+    const int lo = (k * Z + rank) * kRows + w * S;
+    const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
+    float2 a[S], u[S], A = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+    int n = span.n0;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const bool on = live && (span.on >> s & 1);
-    const bool first = span.first >> s & 1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float l = on ? lr[s].get(v) : 0.f;
-      a[s][v] = expf(l);
-      u[s][v] = on ? scale_of<kScale>(l) * xr[s].get(v) : 0.f;
+    for (int s = 0; s < S; ++s) {
+      const float2 l = pair_of(&st.la[w * S + s][cl]), xv = pair_of(&st.x[w * S + s][cl]);
+      float mx, my;
+      gate_of(l.x, &a[s].x, &mx);
+      gate_of(l.y, &a[s].y, &my);
+      u[s] = make_float2(scale_of<kScale>(mx) * xv.x, scale_of<kScale>(my) * xv.y);
     }
-    if (first) {
-      if (on && p.h0) {
+    if (span.on != (1u << S) - 1u || span.first || (span.last && p.cu)) {
+      // some tokens are not there, or a sequence begins (rare)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          u[s][v] = fmaf(a[s][v], p.h0[(int64_t)n * p.D + ch + v], u[s][v]);
+      for (int s = 0; s < S; ++s) {
+        if (!(span.on >> s & 1)) {
+          a[s] = make_float2(1.f, 1.f);
+          u[s] = make_float2(0.f, 0.f);
+        }
+        if (span.first >> s & 1) {
+          if (p.h0 && live) {
+            const float2 h0 = load_state(p.h0 + (int64_t)n * p.D + ch, how);
+            u[s] = make_float2(fmaf(a[s].x, h0.x, u[s].x), fmaf(a[s].y, h0.y, u[s].y));
+          }
+          a[s] = make_float2(-0.f, -0.f);
+        }
+        if (span.last >> s & 1) n = next_sequence(p.cu, p.N, n);
+        H = make_float2(apply(a[s].x, u[s].x, H.x), apply(a[s].y, u[s].y, H.y));
+        A = span.first >> s & 1 ? a[s] : make_float2(A.x * a[s].x, A.y * a[s].y);
       }
+    } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) a[s][v] = -0.f;
+      for (int s = 0; s < S; ++s) {
+        H = make_float2(fmaf(a[s].x, H.x, u[s].x), fmaf(a[s].y, H.y, u[s].y));
+        A = make_float2(A.x * a[s].x, A.y * a[s].y);
+      }
     }
-    if (span.last >> s & 1) n = next_sequence(p.cu, p.N, n);
+    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A.x, H.x, A.y, H.y);
+    link_step(sm, k, Z, rank, c);
+    float2 h = warp_carry(sm, w, cl);
+    OutT* o = out + (int64_t)lo * p.D;
+    n = span.n0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      H[v] = apply(a[s][v], u[s][v], H[v]);
-      A[v] *= a[s][v];
-      if (first) A[v] = -0.f;
+    for (int s = 0; s < S; ++s) {
+      h = make_float2(apply(a[s].x, u[s].x, h.x), apply(a[s].y, u[s].y, h.y));
+      if (live && (span.on >> s & 1)) store_pair(o + (int64_t)s * p.D, h, how);
+      if (span.last >> s & 1) {
+        if (live && p.state) store_pair(p.state + (int64_t)n * p.D + ch, h, how);
+        n = next_sequence(p.cu, p.N, n);
+      }
     }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sm.A[w][cl + v] = A[v];
-    sm.H[w][cl + v] = H[v];
-  }
-  link_tile<CH>(sm, link_of<CH>(geo, p.B, blk, b), i, geo.tiles);
-  if (!live) return;
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = warp_carry<CH>(sm, w, cl + v);
-  OutT* out = static_cast<OutT*>(p.out) + ((int64_t)b * p.T + lo) * p.D + ch;
-  n = span.n0;
-#pragma unroll
-  for (int s = 0; s < S; ++s) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = apply(a[s][v], u[s][v], h[v]);
-    if (span.on >> s & 1) Pack<OutT, V>::store(out + (int64_t)s * p.D, h);
-    if (span.last >> s & 1) {
-      if (p.state) Pack<float, V>::store(p.state + (int64_t)n * p.D + ch, h);
-      n = next_sequence(p.cu, p.N, n);
-    }
+    __syncwarp();
   }
 }
 
@@ -418,109 +415,136 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
 // With g_t the gradient of h_t: g_t = dout_t + a_{t+1} g_{t+1} (plus the final state's gradient
 // at the end of a sequence), dx_t = b_t g_t, dlog_a_t = a_t h_{t-1} g_t + b'(log a_t) x_t g_t and
 // the first state's gradient is a_t g_t at the sequence's first token.  The carry from t to t-1
-// is c_t = a_t g_t = a_t c_{t+1} + a_t dout_t, scanned with tile 0 the last in time.
+// is c_t = a_t g_t = a_t c_{t+1} + a_t dout_t, scanned from the end: rank 0's warp 0 holds the
+// last S tokens of a step.
 
-template <typename InT, typename GateT, typename GradT, int V, int S, int kScale>
+template <typename InT, typename GateT, typename GradT, int S, bool kX>
+struct BwdStage {
+  GateT la[kWarps * S][kCh];
+  GradT dout[kWarps * S][kCh];
+  GradT h[kWarps * S][kCh];  // of the token before
+  InT x[kX ? kWarps * S : 1][kCh];
+};
+
+constexpr int kBwdStages = 2;
+
+template <typename InT, typename GateT, typename GradT, int S, int kScale>
 __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometry geo) {
-  constexpr int CH = 32 * V;
+  constexpr int kRows = kWarps * S;
   constexpr bool kX = kScale != LL_GLR_NONE;
-  __shared__ LinkSmem<CH> sm;
-  int i, blk, b;
-  take_tile(sm, geo, p.B, &i, &blk, &b);
+  using Stage = BwdStage<InT, GateT, GradT, S, kX>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Stage* stages = reinterpret_cast<Stage*>(dyn);
+  __shared__ __align__(16) LinkSmem sm;
+  const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
+  if (Z > 1) cluster_arrive();
+  const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int cl = lane * V, ch = blk * CH + cl;
-  // warp w holds the w-th segment from the tile's end
-  const int lo = ((geo.tiles - 1 - i) * kWarps + (kWarps - 1 - w)) * S;
+  const int cl = 2 * lane, ch = blk * kCh + cl;
   const bool live = ch < p.D;
-  const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + ch;
-  const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + ch;
-  const int64_t at = ((int64_t)b * p.T + lo) * p.D + ch;
-  const GradT* dout = static_cast<const GradT*>(p.dout) + at;
-  const GradT* hs = static_cast<const GradT*>(p.h) + at;
-  Pack<InT, V> xr[S];
-  Pack<GateT, V> lr[S];
-  Pack<GradT, V> gr[S], hr[S];  // hr[s]: h of the token before lo + s
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (live && lo + s < p.T) {
-      lr[s].load(la + (int64_t)(lo + s) * p.sl[1]);
-      gr[s].load(dout + (int64_t)s * p.D);
+  const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
+  const int cols = min(kCh, p.D - blk * kCh);
+  const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + blk * kCh;
+  const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + blk * kCh;
+  const int64_t base = (int64_t)b * p.T * p.D + blk * kCh;
+  const GradT* dout = static_cast<const GradT*>(p.dout) + base;
+  const GradT* hs = static_cast<const GradT*>(p.h) + base;
+  GradT* dx = static_cast<GradT*>(p.dx) + base + cl;
+  GateT* dla = static_cast<GateT*>(p.dlog_a) + base + cl;
+  const int steps = (p.T + Z * kRows - 1) / (Z * kRows);
+  // the tile of step k: steps, then ranks, count from the end of the tiles that cover [0, T)
+  auto tile_start = [&](int k) { return ((steps - 1 - k) * Z + (Z - 1 - rank)) * kRows; };
+  auto issue = [&](int k) {
+    if (k < steps) {
+      Stage& st = stages[k % kBwdStages];
+      const int t0 = tile_start(k), rows = min(kRows, p.T - t0);
+      const int64_t at = (int64_t)t0 * p.D;
+      fill<GateT, kRows>(&st.la[0][0], la + (int64_t)t0 * p.sl[1], p.sl[1], 0, rows, cols, geo.la);
+      fill<GradT, kRows>(&st.dout[0][0], dout + at, p.D, 0, rows, cols, geo.dout);
+      fill<GradT, kRows>(&st.h[0][0], hs + at - p.D, p.D, t0 == 0, rows, cols, geo.h);
+      if (kX)
+        fill<InT, kRows>(&st.x[0][0], x + (int64_t)t0 * p.sx[1], p.sx[1], 0, rows, cols, geo.x);
     }
+    cp_async_commit();
+  };
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (live && lo + s < p.T) {
-      if (lo + s > 0) hr[s].load(hs + (int64_t)(s - 1) * p.D);
-      if (kX) xr[s].load(x + (int64_t)(lo + s) * p.sx[1]);
+  for (int k = 0; k < kBwdStages - 1; ++k) issue(k);
+  if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
+  if (Z > 1) cluster_wait();
+  float carry = 0.f;
+  for (int k = 0; k < steps; ++k) {
+    cp_async_wait<kBwdStages - 2>();
+    __syncthreads();
+    issue(k + kBwdStages - 1);
+    const Stage& st = stages[k % kBwdStages];
+    const int row0 = (kWarps - 1 - w) * S, lo = tile_start(k) + row0;
+    const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
+    int n_last = span.n0;  // the sequence of the last token that is on
+    if (p.cu) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
     }
-  const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
-  if (i == 0) empty_sequences<V>(p.cu, p.N, p.T, b, p.D, ch, p.dstate, p.dh0);
-  // the sequence of the last token that is on
-  int n_last = span.n0;
+    float2 a[S], bs[S], d[S], A = make_float2(1.f, 1.f), E = make_float2(0.f, 0.f);
+    int n = n_last;
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
-  float A[V], E[V], a[S][V], d[S][V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = 1.f;
-    E[v] = 0.f;
-  }
-  int n = n_last;
-#pragma unroll
-  for (int s = S - 1; s >= 0; --s) {
-    const bool on = live && (span.on >> s & 1);
-    const bool last = span.last >> s & 1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      a[s][v] = on ? expf(lr[s].get(v)) : 1.f;
-      d[s][v] = on ? gr[s].get(v) : 0.f;
+    for (int s = S - 1; s >= 0; --s) {
+      const bool on = span.on >> s & 1, last = span.last >> s & 1;
+      const float2 l = pair_of(&st.la[row0 + s][cl]);
+      float mx, my;
+      gate_of(l.x, &a[s].x, &mx);
+      gate_of(l.y, &a[s].y, &my);
+      bs[s] = make_float2(scale_of<kScale>(mx), scale_of<kScale>(my));
+      d[s] = pair_of(&st.dout[row0 + s][cl]);
+      if (!on) {
+        a[s] = make_float2(1.f, 1.f);
+        d[s] = make_float2(0.f, 0.f);
+      }
+      if (last) {
+        if (p.dstate && live) {
+          const float2 ds = load_state(p.dstate + (int64_t)n * p.D + ch, how);
+          d[s] = make_float2(d[s].x + ds.x, d[s].y + ds.y);
+        }
+        E = make_float2(0.f, 0.f);  // nothing comes from the sequence behind
+        A = make_float2(-0.f, -0.f);
+      } else {
+        A = make_float2(A.x * a[s].x, A.y * a[s].y);
+      }
+      E = make_float2(a[s].x * (d[s].x + E.x), a[s].y * (d[s].y + E.y));
+      if (span.first >> s & 1) n = previous_sequence(p.cu, n);
     }
-    if (last && on && p.dstate) {
+    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A.x, E.x, A.y, E.y);
+    link_step(sm, k, Z, rank, carry);
+    float2 c = warp_carry(sm, w, cl);
+    n = n_last;
 #pragma unroll
-      for (int v = 0; v < V; ++v) d[s][v] += p.dstate[(int64_t)n * p.D + ch + v];
+    for (int s = S - 1; s >= 0; --s) {
+      if (!live || !(span.on >> s & 1)) continue;
+      const bool last = span.last >> s & 1, first = span.first >> s & 1;
+      if (last) c = make_float2(0.f, 0.f);
+      const float2 g = make_float2(d[s].x + c.x, d[s].y + c.y);
+      float2 before = make_float2(0.f, 0.f);
+      if (!first) {
+        if (lo + s > 0) before = pair_of(&st.h[row0 + s][cl]);
+      } else if (p.h0) {
+        before = load_state(p.h0 + (int64_t)n * p.D + ch, how);
+      }
+      c = make_float2(a[s].x * g.x, a[s].y * g.y);
+      float2 ol = make_float2(c.x * before.x, c.y * before.y);
+      if (kX) {
+        const float2 xv = pair_of(&st.x[row0 + s][cl]);
+        ol.x = fmaf(scale_grad<kScale>(a[s].x, bs[s].x) * xv.x, g.x, ol.x);
+        ol.y = fmaf(scale_grad<kScale>(a[s].y, bs[s].y) * xv.y, g.y, ol.y);
+      }
+      const int64_t at = (int64_t)(lo + s) * p.D;
+      store_pair(dx + at, make_float2(bs[s].x * g.x, bs[s].y * g.y), how);
+      store_pair(dla + at, ol, how);
+      if (first) {
+        if (p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, c, how);
+        n = previous_sequence(p.cu, n);
+      }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      E[v] = a[s][v] * (last ? d[s][v] : d[s][v] + E[v]);
-      A[v] = last ? -0.f : A[v] * a[s][v];
-    }
-    if (span.first >> s & 1) n = previous_sequence(p.cu, n);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sm.A[w][cl + v] = A[v];
-    sm.H[w][cl + v] = E[v];
-  }
-  link_tile<CH>(sm, link_of<CH>(geo, p.B, blk, b), i, geo.tiles);
-  if (!live) return;
-  float c[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) c[v] = warp_carry<CH>(sm, w, cl + v);
-  GradT* dx = static_cast<GradT*>(p.dx) + at;
-  GateT* dla = static_cast<GateT*>(p.dlog_a) + at;
-  n = n_last;
-#pragma unroll
-  for (int s = S - 1; s >= 0; --s) {
-    if (!(span.on >> s & 1)) continue;
-    const bool last = span.last >> s & 1, first = span.first >> s & 1;
-    float ox[V], ol[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float g = last ? d[s][v] : d[s][v] + c[v];
-      const float before =
-          first ? (p.h0 ? p.h0[(int64_t)n * p.D + ch + v] : 0.f) : (lo + s > 0 ? hr[s].get(v) : 0.f);
-      const float bs = scale_of<kScale>(lr[s].get(v));
-      c[v] = a[s][v] * g;
-      ox[v] = bs * g;
-      ol[v] = c[v] * before;
-      if (kX) ol[v] = fmaf(scale_grad<kScale>(a[s][v], bs) * xr[s].get(v), g, ol[v]);
-    }
-    Pack<GradT, V>::store(dx + (int64_t)s * p.D, ox);
-    Pack<GateT, V>::store(dla + (int64_t)s * p.D, ol);
-    if (first) {
-      if (p.dh0) Pack<float, V>::store(p.dh0 + (int64_t)n * p.D + ch, c);
-      n = previous_sequence(p.cu, n);
-    }
+    __syncwarp();
   }
 }
 
@@ -529,20 +553,29 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
 // One token per row: state[slot] <- a state[slot] + b x, out = the new state.  A slot given
 // twice belongs to its first row; the rows after it, and rows whose slot is out of range, are
 // left out and raise the error word.
-template <typename InT, typename GateT, typename OutT, int V, int kScale>
+template <typename InT, typename GateT, typename OutT, int kScale>
 __global__ void __launch_bounds__(kThreads) glr_step_kernel(
     float* __restrict__ state, const int* __restrict__ slots, int S, const InT* __restrict__ x,
-    const GateT* __restrict__ la, OutT* __restrict__ out, int D) {
+    const GateT* __restrict__ la, OutT* __restrict__ out, int D, int pairs) {
   const int row = blockIdx.y;
-  const int ch = (blockIdx.x * kThreads + threadIdx.x) * V;
-  int64_t slot = row;
+  const int ch = (blockIdx.x * kThreads + threadIdx.x) * 2;
   const bool on = ch < D;
-  Pack<InT, V> xr;
-  Pack<GateT, V> lr;
+  const int how = ch + 1 >= D ? kFirst : pairs ? kPairs : kSingles;
+  int64_t slot = row;
+  float2 xv = make_float2(0.f, 0.f), l = xv;
   const int64_t at = (int64_t)row * D + ch;
   if (on) {
-    xr.load(x + at);
-    lr.load(la + at);
+    if (how == kPairs) {
+      xv = pair_of(x + at);
+      l = pair_of(la + at);
+    } else {
+      xv.x = to_f32(x[at]);
+      l.x = to_f32(la[at]);
+      if (how == kSingles) {
+        xv.y = to_f32(x[at + 1]);
+        l.y = to_f32(la[at + 1]);
+      }
+    }
   }
   if (slots) {
     const int sl = slots[row];
@@ -551,98 +584,108 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(
     twice = __syncthreads_or(twice);
     if (sl == -1) return;
     if (sl < 0 || sl >= S || twice) {
-      if (threadIdx.x == 0) atomicOr(&g_glr_error, 2u);
+      if (threadIdx.x == 0) atomicOr(&g_glr_error, 1u);
       return;
     }
     slot = sl;
   }
   if (!on) return;
   float* st = state + slot * D + ch;
-  Pack<float, V> h0;
-  h0.load(st);
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float l = lr.get(v);
-    h[v] = fmaf(expf(l), h0.get(v), scale_of<kScale>(l) * xr.get(v));
-  }
-  Pack<float, V>::store(st, h);
-  Pack<OutT, V>::store(out + at, h);
+  const float2 h0 = load_state(st, how);
+  float ax, ay, mx, my;
+  gate_of(l.x, &ax, &mx);
+  gate_of(l.y, &ay, &my);
+  const float2 h = make_float2(fmaf(ax, h0.x, scale_of<kScale>(mx) * xv.x),
+                               fmaf(ay, h0.y, scale_of<kScale>(my) * xv.y));
+  store_pair(st, h, how);
+  store_pair(out + at, h, how);
 }
 
 // ---------------------------------------------------------------- launch
 
-constexpr int kSteps = 8;  // tokens a warp holds
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-int tiles_of(int64_t T) {
-  const int64_t t = (T + kWarps * kSteps - 1) / (kWarps * kSteps);
-  return (int)(t < 1 ? 1 : t);
-}
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// Channels two at a time wherever pointers and strides allow it.
-bool pairs_ok(const GlrArgs& p, int in_size, int gate_size, int out_size) {
-  auto ok = [](const void* q, size_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
-  return p.D % 2 == 0 && p.sx[0] % 2 == 0 && p.sx[1] % 2 == 0 && p.sl[0] % 2 == 0 &&
-         p.sl[1] % 2 == 0 && ok(p.x, 2 * in_size) && ok(p.log_a, 2 * gate_size) &&
-         ok(p.dlog_a, 2 * gate_size) && ok(p.out, 2 * out_size) && ok(p.h, 2 * out_size) &&
-         ok(p.dout, 2 * out_size) && ok(p.dx, 2 * out_size) && ok(p.h0, 8) && ok(p.state, 8) &&
-         ok(p.dstate, 8) && ok(p.dh0, 8);
-}
-
-template <typename InT, typename GateT, typename OutT, int V, int kScale>
-cudaError_t launch(const GlrArgs& p, bool backward, void* ws, cudaStream_t s) {
-  constexpr int CH = 32 * V;
-  Geometry g;
-  g.tiles = tiles_of(p.T);
-  g.blocks = (p.D + CH - 1) / CH;
-  const size_t lines = (size_t)p.B * g.blocks * g.tiles;
-  g.agg = static_cast<float*>(ws);
-  g.flags = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + align256(lines * CH * 12));
-  if (g.tiles > 1) {
-    const cudaError_t e = cudaMemsetAsync(g.flags, 0, (lines + 1) * sizeof(uint32_t), s);
-    if (e != cudaSuccess) return e;
+// Bytes of a copy that pointer, batch stride, row stride and width allow.
+int copy_bytes(const void* p, int64_t sb, int64_t st, int64_t D, int size) {
+  for (int bytes = 16; bytes >= 4; bytes /= 4) {
+    const int per = bytes / size;
+    if (per >= 1 && aligned(p, bytes) && sb % per == 0 && st % per == 0 && D % per == 0)
+      return bytes;
   }
-  if (backward)
-    glr_bwd_kernel<InT, GateT, OutT, V, kSteps, kScale><<<(unsigned)lines, kThreads, 0, s>>>(p, g);
-  else
-    glr_fwd_kernel<InT, GateT, OutT, V, kSteps, kScale><<<(unsigned)lines, kThreads, 0, s>>>(p, g);
-  return cudaGetLastError();
+  return size;
+}
+
+// CTAs that share a channel block: doubled while that keeps the launch within two CTAs per SM and
+// a step within the sequence.
+int cluster_of(int64_t items, int64_t T, int rows) {
+  int Z = 1;
+  while (Z < kMaxCluster && items * Z * 2 <= 2 * 152 && (int64_t)Z * rows < T) Z *= 2;
+  return Z;
+}
+
+template <typename K>
+cudaError_t launch_cluster(K kernel, const GlrArgs& p, const Geometry& g, size_t smem,
+                           cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.B * g.blocks * g.Z));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = g.Z;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = g.Z > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, g);
 }
 
 template <typename InT, typename GateT, typename OutT, int kScale>
-cudaError_t launch_v(const GlrArgs& p, bool backward, void* ws, cudaStream_t s) {
-  return pairs_ok(p, sizeof(InT), sizeof(GateT), sizeof(OutT))
-             ? launch<InT, GateT, OutT, 2, kScale>(p, backward, ws, s)
-             : launch<InT, GateT, OutT, 1, kScale>(p, backward, ws, s);
+cudaError_t launch(const GlrArgs& p, bool backward, cudaStream_t s) {
+  Geometry g;
+  g.blocks = (p.D + kCh - 1) / kCh;
+  const int64_t dense = (int64_t)p.T * p.D, items = (int64_t)p.B * g.blocks;
+  const size_t o = 2 * sizeof(OutT);
+  g.pairs = p.D % 2 == 0 && aligned(p.out, o) && aligned(p.state, 8) && aligned(p.dx, o) &&
+            aligned(p.dlog_a, 2 * sizeof(GateT)) && aligned(p.dh0, 8);
+  g.x = copy_bytes(p.x, p.sx[0], p.sx[1], p.D, sizeof(InT));
+  g.la = copy_bytes(p.log_a, p.sl[0], p.sl[1], p.D, sizeof(GateT));
+  g.h = copy_bytes(p.h, dense, p.D, p.D, sizeof(OutT));
+  g.dout = copy_bytes(p.dout, dense, p.D, p.D, sizeof(OutT));
+  // a warp's tokens: as many as leave room for two CTAs of two stages per SM
+  if (backward) {
+    constexpr int S = sizeof(GateT) + 2 * sizeof(OutT) + sizeof(InT) <= 10 ? 8 : 4;
+    g.Z = cluster_of(items, p.T, kWarps * S);
+    using Stage = BwdStage<InT, GateT, OutT, S, kScale != LL_GLR_NONE>;
+    return launch_cluster(glr_bwd_kernel<InT, GateT, OutT, S, kScale>, p, g,
+                          kBwdStages * sizeof(Stage), s);
+  }
+  constexpr int S = sizeof(GateT) + sizeof(InT) <= 6 ? 16 : 8;
+  g.Z = cluster_of(items, p.T, kWarps * S);
+  return launch_cluster(glr_fwd_kernel<InT, GateT, OutT, S, kScale>, p, g,
+                        kFwdStages * sizeof(FwdStage<InT, GateT, S>), s);
 }
 
 template <typename InT, typename GateT, typename OutT>
-cudaError_t launch_scale(const GlrArgs& p, int scale, bool backward, void* ws, cudaStream_t s) {
-  if (scale == LL_GLR_NONE) return launch_v<InT, GateT, OutT, LL_GLR_NONE>(p, backward, ws, s);
-  if (scale == LL_GLR_ONE_MINUS)
-    return launch_v<InT, GateT, OutT, LL_GLR_ONE_MINUS>(p, backward, ws, s);
-  return launch_v<InT, GateT, OutT, LL_GLR_SQRT>(p, backward, ws, s);
+cudaError_t launch_scale(const GlrArgs& p, int scale, bool backward, cudaStream_t s) {
+  if (scale == LL_GLR_NONE) return launch<InT, GateT, OutT, LL_GLR_NONE>(p, backward, s);
+  if (scale == LL_GLR_ONE_MINUS) return launch<InT, GateT, OutT, LL_GLR_ONE_MINUS>(p, backward, s);
+  return launch<InT, GateT, OutT, LL_GLR_SQRT>(p, backward, s);
 }
 
 template <typename InT, typename GateT, typename OutT, int kScale>
 cudaError_t launch_step(float* state, const int* slots, int S, const void* x, const void* la,
                         void* out, int B, int D, cudaStream_t s) {
-  auto ok = [](const void* q, size_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
-  const bool two = D % 2 == 0 && ok(state, 8) && ok(x, 2 * sizeof(InT)) &&
-                   ok(la, 2 * sizeof(GateT)) && ok(out, 2 * sizeof(OutT));
-  const int per = kThreads * (two ? 2 : 1);
-  const dim3 grid((D + per - 1) / per, B);
-  const InT* xi = static_cast<const InT*>(x);
-  const GateT* lg = static_cast<const GateT*>(la);
-  OutT* o = static_cast<OutT*>(out);
-  if (two)
-    glr_step_kernel<InT, GateT, OutT, 2, kScale>
-        <<<grid, kThreads, 0, s>>>(state, slots, S, xi, lg, o, D);
-  else
-    glr_step_kernel<InT, GateT, OutT, 1, kScale>
-        <<<grid, kThreads, 0, s>>>(state, slots, S, xi, lg, o, D);
+  const int pairs = D % 2 == 0 && aligned(state, 8) && aligned(x, 2 * sizeof(InT)) &&
+                    aligned(la, 2 * sizeof(GateT)) && aligned(out, 2 * sizeof(OutT));
+  const dim3 grid((D + 2 * kThreads - 1) / (2 * kThreads), B);
+  glr_step_kernel<InT, GateT, OutT, kScale><<<grid, kThreads, 0, s>>>(
+      state, slots, S, static_cast<const InT*>(x), static_cast<const GateT*>(la),
+      static_cast<OutT*>(out), D, pairs);
   return cudaGetLastError();
 }
 
@@ -658,27 +701,18 @@ cudaError_t step_scale(float* state, const int* slots, int S, const void* x, con
 
 }  // namespace
 
-// Sized for the widest form (one channel per lane), whichever the call takes.
-int64_t glr_tiles(int64_t B, int64_t T, int64_t D) { return B * ((D + 31) / 32) * tiles_of(T); }
-
-size_t glr_workspace_bytes(int64_t B, int64_t T, int64_t D) {
-  if (tiles_of(T) <= 1) return 0;
-  const size_t lines = (size_t)glr_tiles(B, T, D);
-  return align256(lines * 64 * 12) + align256((lines + 1) * sizeof(uint32_t));
-}
-
 cudaError_t launch_glr(const GlrArgs& p, int in_dtype, int gate_dtype, int out_dtype, int scale,
-                       bool backward, void* ws, cudaStream_t s) {
+                       bool backward, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
   const bool o32 = out_dtype == LL_F32;
   if (in_dtype == LL_F32)
-    return o32 ? launch_scale<float, float, float>(p, scale, backward, ws, s)
-               : launch_scale<float, float, bf16>(p, scale, backward, ws, s);
+    return o32 ? launch_scale<float, float, float>(p, scale, backward, s)
+               : launch_scale<float, float, bf16>(p, scale, backward, s);
   if (gate_dtype == LL_F32)
-    return o32 ? launch_scale<bf16, float, float>(p, scale, backward, ws, s)
-               : launch_scale<bf16, float, bf16>(p, scale, backward, ws, s);
-  return o32 ? launch_scale<bf16, bf16, float>(p, scale, backward, ws, s)
-             : launch_scale<bf16, bf16, bf16>(p, scale, backward, ws, s);
+    return o32 ? launch_scale<bf16, float, float>(p, scale, backward, s)
+               : launch_scale<bf16, float, bf16>(p, scale, backward, s);
+  return o32 ? launch_scale<bf16, bf16, float>(p, scale, backward, s)
+             : launch_scale<bf16, bf16, bf16>(p, scale, backward, s);
 }
 
 cudaError_t launch_glr_step(float* state, const int* slots, int S, const void* x, const void* la,

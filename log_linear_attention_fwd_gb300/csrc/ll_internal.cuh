@@ -252,10 +252,8 @@ struct GlrArgs {
   void* dlog_a;
   float* dh0;           // may be null
 };
-size_t glr_workspace_bytes(int64_t B, int64_t T, int64_t D);
-int64_t glr_tiles(int64_t B, int64_t T, int64_t D);  // CTAs of a launch, at most
 cudaError_t launch_glr(const GlrArgs& p, int in_dtype, int gate_dtype, int out_dtype, int scale,
-                       bool backward, void* ws, cudaStream_t s);
+                       bool backward, cudaStream_t s);
 cudaError_t launch_glr_step(float* state, const int* slots, int S, const void* x, const void* la,
                             void* out, int B, int D, int in_dtype, int gate_dtype, int out_dtype,
                             int scale, cudaStream_t s);

@@ -629,7 +629,7 @@ int loglinear_device_error(ll_stream_t stream, unsigned* flags) {
   cudaError_t e = tc_take_error(reinterpret_cast<cudaStream_t>(stream), &f1);
   if (e == cudaSuccess) e = tcb_take_error(reinterpret_cast<cudaStream_t>(stream), &f2);
   if (e == cudaSuccess) e = glr_take_error(reinterpret_cast<cudaStream_t>(stream), &f3);
-  *flags = f1 | f2 | f3 << 3;
+  *flags = f1 | f2 | f3 << 4;
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
 
@@ -665,30 +665,20 @@ int check_glr(int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype, int
   return LL_OK;
 }
 
-int check_glr_tiles(int64_t B, int64_t T, int64_t D) {
-  if (T > (1 << 30) || B > INT32_MAX || D > INT32_MAX - 64) return LL_ERR_UNSUPPORTED;
-  if (B > 0 && D > 0 && (B > INT32_MAX / ((D + 31) / 32) || glr_tiles(B, T, D) > INT32_MAX))
-    return LL_ERR_UNSUPPORTED;
-  return LL_OK;
-}
-
 // Checks and arguments that the forward and the backward share.  LL_OK with *empty: there are
 // no sequences or no channels.
 int glr_common(GlrArgs* a, const void* x, const ll_strides* xs, const void* log_a,
                const ll_strides* ls, const float* h0, const int32_t* cu, int64_t N, int64_t B,
-               int64_t T, int64_t D, int in_dtype, int gate_dtype, bool x_needed,
-               void* workspace, size_t workspace_bytes, bool* empty) {
-  int st = check_glr_tiles(B, T, D);
-  if (st != LL_OK) return st;
+               int64_t T, int64_t D, int in_dtype, int gate_dtype, bool x_needed, bool* empty) {
+  // a launch has B x ceil(D / 64) clusters of at most 8 CTAs
+  if (T > (1 << 30) || B > INT32_MAX / 16 || D > INT32_MAX / 16) return LL_ERR_UNSUPPORTED;
+  if (B * ((D + 63) / 64) > INT32_MAX / 16) return LL_ERR_UNSUPPORTED;
   if (cu && B != 1) return LL_ERR_INVALID;
   if (cu && (N < 0 || N > INT32_MAX - 1)) return LL_ERR_INVALID;
   const int64_t n = cu ? N : B;
   *empty = n == 0 || D == 0;
   if (*empty) return LL_OK;
   if (T > 0 && ((x_needed && !x) || !log_a)) return LL_ERR_INVALID;
-  const size_t need = glr_workspace_bytes(B, T, D);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return LL_ERR_WORKSPACE;
-  if (need > 0 && !aligned_to(workspace, 256)) return LL_ERR_ALIGN;
   if (!aligned_to(x, size_of(in_dtype)) || !aligned_to(log_a, size_of(gate_dtype)) ||
       !aligned_to(h0, 4) || !aligned_to(cu, 4))
     return LL_ERR_ALIGN;
@@ -709,32 +699,23 @@ int glr_common(GlrArgs* a, const void* x, const ll_strides* xs, const void* log_
 
 extern "C" {
 
-int loglinear_glr_workspace_size(int64_t B, int64_t T, int64_t D, size_t* bytes) {
-  if (!bytes || B < 0 || T < 0 || D < 0) return LL_ERR_INVALID;
-  const int st = check_glr_tiles(B, T, D);
-  if (st != LL_OK) return st;
-  *bytes = glr_workspace_bytes(B, T, D);
-  return LL_OK;
-}
-
 int loglinear_glr_fwd(const void* x, const ll_strides* x_strides, const void* log_a,
                       const ll_strides* log_a_strides, const float* h0,
                       const int32_t* cu_seqlens, int64_t N, void* out, float* state_out,
                       int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype,
-                      int out_dtype, int scale, void* workspace, size_t workspace_bytes,
-                      ll_stream_t stream) {
+                      int out_dtype, int scale, ll_stream_t stream) {
   int st = check_glr(B, T, D, in_dtype, gate_dtype, out_dtype, scale);
   if (st != LL_OK) return st;
   GlrArgs a;
   bool empty;
   st = glr_common(&a, x, x_strides, log_a, log_a_strides, h0, cu_seqlens, N, B, T, D, in_dtype,
-                  gate_dtype, true, workspace, workspace_bytes, &empty);
+                  gate_dtype, true, &empty);
   if (st != LL_OK || empty || (T == 0 && !state_out)) return st;
   if (T > 0 && !out) return LL_ERR_INVALID;
   if (!aligned_to(out, size_of(out_dtype)) || !aligned_to(state_out, 4)) return LL_ERR_ALIGN;
   a.out = out;
   a.state = state_out;
-  const cudaError_t e = launch_glr(a, in_dtype, gate_dtype, out_dtype, scale, false, workspace,
+  const cudaError_t e = launch_glr(a, in_dtype, gate_dtype, out_dtype, scale, false,
                                    reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
@@ -744,13 +725,13 @@ int loglinear_glr_bwd(const void* x, const ll_strides* x_strides, const void* lo
                       const int32_t* cu_seqlens, int64_t N, const void* h, const void* dout,
                       const float* dstate, void* dx, void* dlog_a, float* dh0, int64_t B,
                       int64_t T, int64_t D, int in_dtype, int gate_dtype, int grad_dtype,
-                      int scale, void* workspace, size_t workspace_bytes, ll_stream_t stream) {
+                      int scale, ll_stream_t stream) {
   int st = check_glr(B, T, D, in_dtype, gate_dtype, grad_dtype, scale);
   if (st != LL_OK) return st;
   GlrArgs a;
   bool empty;
   st = glr_common(&a, x, x_strides, log_a, log_a_strides, h0, cu_seqlens, N, B, T, D, in_dtype,
-                  gate_dtype, scale != LL_GLR_NONE, workspace, workspace_bytes, &empty);
+                  gate_dtype, scale != LL_GLR_NONE, &empty);
   if (st != LL_OK || empty || (T == 0 && !dh0)) return st;
   if (T > 0 && (!h || !dout || !dx || !dlog_a)) return LL_ERR_INVALID;
   const size_t g = size_of(grad_dtype);
@@ -758,7 +739,7 @@ int loglinear_glr_bwd(const void* x, const ll_strides* x_strides, const void* lo
       !aligned_to(dlog_a, size_of(gate_dtype)) || !aligned_to(dstate, 4) || !aligned_to(dh0, 4))
     return LL_ERR_ALIGN;
   a.h = h; a.dout = dout; a.dstate = dstate; a.dx = dx; a.dlog_a = dlog_a; a.dh0 = dh0;
-  const cudaError_t e = launch_glr(a, in_dtype, gate_dtype, grad_dtype, scale, true, workspace,
+  const cudaError_t e = launch_glr(a, in_dtype, gate_dtype, grad_dtype, scale, true,
                                    reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }

@@ -23,3 +23,8 @@ from .gdn_oracle import (  # noqa: F401
     gdn_recurrence,
     gdn_states_from_buckets,
 )
+from .glr_oracle import (  # noqa: F401
+    glr_backward,
+    glr_forward,
+    glr_scale,
+)
