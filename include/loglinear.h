@@ -367,9 +367,10 @@ LL_API int loglinear_bwd(const void* q, const void* k, const void* v, const floa
  * not valid).  Bit 1: a wait for another tile's published state ran out of time (the
  * output of that tile is not valid).  Bit 2: loglinear_bwd was given a fwd_workspace
  * that a tensor-core loglinear_fwd with the same B, T, H, Hqk and dv did not write (its
- * layout tag does not match; the gradients are not valid).  Bit 4: loglinear_glr_step was given
- * a slot out of range, or one that an earlier row has (that row was left out).  The launch
- * itself still reported success.
+ * layout tag does not match; the gradients are not valid).  Bit 3: a wait inside loglinear_glr_fwd or
+ * _bwd ran out of time (the results are not valid).  Bit 4: loglinear_glr_step was given a
+ * slot out of range, or one that an earlier row has (that row was left out).  The launch itself
+ * still reported success.
  */
 LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
 

@@ -4,7 +4,7 @@
 // Forward and backward are one scan each.  The maps c -> A c + H of consecutive tokens compose
 // to a map of the same form, so a segment of tokens is known by two floats per channel.  A
 // cluster of Z CTAs owns 64 channels of one batch entry and marches through time, Z tiles of
-// 8 S tokens per step: lane = 2 channels, warp = S consecutive tokens, which it folds into one
+// 16 S tokens per step: lane = 2 channels, warp = S consecutive tokens, which it folds into one
 // map; the CTA folds its 8 warps' maps and hands the result to every CTA of the cluster through
 // distributed shared memory; after one cluster barrier each CTA knows the carry into its
 // tile and, from all Z maps, the carry into the next step.  Then the warps run their tokens
@@ -26,60 +26,106 @@
 
 namespace ll {
 
-// bit 0: a step was given a slot that is out of range or given twice
+// bit 0: a step was given a slot that is out of range or given twice; bit 1: a wait for the
+// cluster's maps ran out of time
 __device__ unsigned int g_glr_error = 0;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCh = 64;        // channels of a CTA: two per lane
 constexpr int kMaxCluster = 8;
 
+// ---------------------------------------------------------------- pairs of fp32
+
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack(x, x); }
+__device__ __forceinline__ f32x2 to_pair(float2 v) { return pack(v.x, v.y); }
+
 // ---------------------------------------------------------------- gates
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error below 2^-22
+  return y;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error below 2^-22
+  return y;
+}
+
 // a = exp(la) and m = 1 - a.  Gates live near a = 1, where 1 - a computed from a would lose the
-// digits that la still has: for |la| <= 1/2 the Taylor sum of exp(la) - 1 (8 terms, its
-// remainder is below 2^-27) gives m, and a from it to half a unit; beyond, exp itself is far
-// enough from 1.  The terms cost 8 multiply-adds; expf and expm1f together three times that.
+// digits that la still has: for |la| <= 1/4 the Taylor sum of exp(la) - 1 (6 terms, its
+// remainder is below 2^-24) gives m, and a from it to half a unit; beyond, exp itself is far
+// enough from 1 (m off by 2^-20 at most).  Scalar, for its constants are then part of the
+// instructions; packed ones would hold registers.
 __device__ __forceinline__ void gate_of(float la, float* a, float* m) {
-  float p = 1.f / 40320.f;
-  p = fmaf(p, la, 1.f / 5040.f);
-  p = fmaf(p, la, 1.f / 720.f);
-  p = fmaf(p, la, 1.f / 120.f);
+  float p = fmaf(1.f / 720.f, la, 1.f / 120.f);
   p = fmaf(p, la, 1.f / 24.f);
   p = fmaf(p, la, 1.f / 6.f);
   p = fmaf(p, la, 0.5f);
   p = fmaf(p, la, 1.f);
-  p *= la;
-  const float e = __expf(la);
-  const bool near = fabsf(la) <= 0.5f;
-  *a = near ? 1.f + p : e;
-  *m = near ? -p : 1.f - e;
+  const float e = exp2_approx(la * 1.44269504f);
+  const bool near = fabsf(la) <= 0.25f;
+  *a = near ? fmaf(p, la, 1.f) : e;
+  *m = near ? p * -la : 1.f - e;
+}
+__device__ __forceinline__ void gate_of(float2 la, f32x2* a, float2* m) {
+  float x, y;
+  gate_of(la.x, &x, &m->x);
+  gate_of(la.y, &y, &m->y);
+  *a = pack(x, y);
 }
 
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error below 2^-22
-  return y;
+// b from m: 1 - a^2 = m (2 - m).  0 where a >= 1; a NaN stays one.
+__device__ __forceinline__ float sqrt_scale(float m) {
+  float v;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(v) : "f"(m * (2.f - m)));
+  return sqrt_approx(v);
 }
-
-// b from a and m: 1 - a^2 = m (2 - m).  0 where a >= 1.
 template <int kScale>
-__device__ __forceinline__ float scale_of(float m) {
-  if (kScale == LL_GLR_ONE_MINUS) return m;
-  if (kScale == LL_GLR_SQRT) {
-    const float v = m * (2.f - m);
-    return sqrt_approx(v < 0.f ? 0.f : v);  // a NaN stays one
-  }
-  return 1.f;
+__device__ __forceinline__ f32x2 scale_of(float2 m) {
+  if (kScale == LL_GLR_ONE_MINUS) return pack(m.x, m.y);
+  if (kScale == LL_GLR_SQRT) return pack(sqrt_scale(m.x), sqrt_scale(m.y));
+  return both(1.f);
 }
 // db / d log a.  The square root's is infinite at a = 1 and taken as 0 there.
 template <int kScale>
-__device__ __forceinline__ float scale_grad(float a, float b) {
-  if (kScale == LL_GLR_ONE_MINUS) return -a;
-  if (kScale == LL_GLR_SQRT) return b > 0.f ? -__fdividef(a * a, b) : 0.f;
-  return 0.f;
+__device__ __forceinline__ f32x2 scale_grad(f32x2 a, f32x2 b) {
+  if (kScale == LL_GLR_ONE_MINUS) return mul2(a, both(-1.f));
+  if (kScale == LL_GLR_SQRT) {
+    const float2 q = unpack(mul2(a, mul2(a, both(-1.f)))), d = unpack(b);
+    return pack(d.x > 0.f ? __fdividef(q.x, d.x) : 0.f, d.y > 0.f ? __fdividef(q.y, d.y) : 0.f);
+  }
+  return both(0.f);
 }
 
 // ---------------------------------------------------------------- element access
@@ -129,22 +175,32 @@ template <typename T, int kRows>
 __device__ __forceinline__ void fill(T* dst, const T* src, int64_t stride, int lo, int hi,
                                      int cols, int bytes) {
   if (bytes == 16) {
-    constexpr int per = 16 / sizeof(T), chunks = kCh / per;
+    constexpr int per = 16 / sizeof(T), chunks = kCh / per, pass = kThreads / chunks;
+    const int r0 = threadIdx.x / chunks, c = (threadIdx.x % chunks) * per;
+    const T* p = src + r0 * stride + c;
+    T* d = dst + r0 * kCh + c;
+    if (lo == 0 && hi >= kRows && cols == kCh && kRows % pass == 0) {
 #pragma unroll
-    for (int i = threadIdx.x; i < kRows * chunks; i += kThreads) {
-      const int r = i / chunks, c = (i % chunks) * per;
-      if (r >= lo && r < hi && c < cols) cp_async16(dst + r * kCh + c, src + r * stride + c);
+      for (int r = 0; r < kRows; r += pass) {
+        cp_async16(d + r * kCh, p);
+        p += pass * stride;
+      }
+    } else {
+#pragma unroll 1
+      for (int r = r0; r < kRows; r += pass) {
+        if (r >= lo && r < hi && c < cols) cp_async16(dst + r * kCh + c, src + r * stride + c);
+      }
     }
   } else if (bytes == 4) {
     constexpr int per = 4 / sizeof(T), chunks = kCh / per;
-#pragma unroll 8
+#pragma unroll 4
     for (int i = threadIdx.x; i < kRows * chunks; i += kThreads) {
       const int r = i / chunks, c = (i % chunks) * per;
       if (r >= lo && r < hi && c < cols)
         tc::cp_async4(dst + r * kCh + c, src + r * stride + c, 4);
     }
   } else {
-#pragma unroll 8
+#pragma unroll 4
     for (int i = threadIdx.x; i < kRows * kCh; i += kThreads) {
       const int r = i / kCh, c = i % kCh;
       if (r >= lo && r < hi && c < cols) dst[r * kCh + c] = src[r * stride + c];
@@ -225,50 +281,71 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
+__device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Writes v to the same shared-memory address of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float2* p, uint32_t rank, float2 v) {
-  uint32_t at;
+// Writes v to p in the shared memory of CTA `rank` of the cluster and counts its 8 bytes on that
+// CTA's bar.
+__device__ __forceinline__ void send(float2* p, uint64_t* bar, uint32_t rank, float2 v) {
+  uint32_t at, b;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(tc::smem_u32(bar)), "r"(rank));
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+      "f"(v.x), "f"(v.y), "r"(b)
+      : "memory");
 }
 
 struct LinkSmem {
-  float2 warp[kWarps][kCh];            // the warps' maps
+  float2 warp[kWarps][kCh];            // the warps' maps; then those of all warps before
   float2 tile[2][kMaxCluster][kCh];    // the cluster's tiles' maps, of even and odd steps
   float carry[kCh];                    // into this CTA's tile
+  uint64_t bar[2];                     // the tiles' maps of even and odd steps are there
 };
 
+// Before the first step; ends with a barrier over the cluster.
+__device__ __forceinline__ void link_init(LinkSmem& sm, int Z) {
+  if (Z == 1) return;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&sm.bar[0], 1);
+    tc::mbar_init(&sm.bar[1], 1);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  cluster_sync();
+}
+
 // After the warps' maps of step k are in sm.warp: the carry into this CTA's tile goes to
-// sm.carry, and `c` (threads below 64, their channel's carry into the step) moves on to the
-// next step.  All threads of the cluster call it; ends with a block barrier.
+// sm.carry, sm.warp to the maps of the warps before, and `c` (threads below 64, their channel's
+// carry into the step) moves on to the next step.  Starts and ends with a block barrier.
+//
+// A CTA sends its map of step k + 1 after it has read the maps of step k, and has those of step
+// k + 1 before it sends that of step k + 2: two buffers are enough.  It leaves the last step
+// only with every map that is sent to it in place.
 __device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, float& c) {
   const int tid = threadIdx.x;
   __syncthreads();
   if (tid < kCh) {
+    if (Z > 1 && tid == 0) tc::mbar_arrive_expect_tx(&sm.bar[k & 1], Z * kCh * sizeof(float2));
     float2 m = sm.warp[0][tid];
+    sm.warp[0][tid] = make_float2(1.f, 0.f);
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) then(m, sm.warp[w][tid]);
+    for (int w = 1; w < kWarps; ++w) {
+      const float2 n = sm.warp[w][tid];
+      sm.warp[w][tid] = m;
+      then(m, n);
+    }
     if (Z == 1) {
       sm.carry[tid] = c;
       c = apply(m.x, m.y, c);
     } else {
-      for (int z = 0; z < Z; ++z) store_remote(&sm.tile[k & 1][rank][tid], z, m);
-    }
-  }
-  if (Z > 1) {
-    cluster_arrive();
-    cluster_wait();
-    if (tid < kCh) {
+      for (int z = 0; z < Z; ++z) send(&sm.tile[k & 1][rank][tid], &sm.bar[k & 1], z, m);
+      if (!tc::mbar_wait(&sm.bar[k & 1], (k >> 1) & 1)) atomicOr(&g_glr_error, 2u);
       for (int z = 0; z < Z; ++z) {
         if (z == rank) sm.carry[tid] = c;
-        const float2 m = sm.tile[k & 1][z][tid];
-        c = apply(m.x, m.y, c);
+        const float2 n = sm.tile[k & 1][z][tid];
+        c = apply(n.x, n.y, c);
       }
     }
   }
@@ -276,14 +353,10 @@ __device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, 
 }
 
 // The carry into warp w's tokens, from the tile's and the warps before it.
-__device__ __forceinline__ float2 warp_carry(const LinkSmem& sm, int w, int cl) {
-  float2 c = *reinterpret_cast<const float2*>(&sm.carry[cl]);
-  for (int u = 0; u < w; ++u) {
-    const float4 m = *reinterpret_cast<const float4*>(&sm.warp[u][cl]);
-    c.x = apply(m.x, m.y, c.x);
-    c.y = apply(m.z, m.w, c.y);
-  }
-  return c;
+__device__ __forceinline__ f32x2 warp_carry(const LinkSmem& sm, int w, int cl) {
+  const float2 c = *reinterpret_cast<const float2*>(&sm.carry[cl]);
+  const float4 m = *reinterpret_cast<const float4*>(&sm.warp[w][cl]);
+  return pack(apply(m.x, m.y, c.x), apply(m.z, m.w, c.y));
 }
 
 struct Geometry {
@@ -324,13 +397,13 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
-  if (Z > 1) cluster_arrive();
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int cl = 2 * lane, ch = blk * kCh + cl;
   const bool live = ch < p.D;
   const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
   const int cols = min(kCh, p.D - blk * kCh);
+  const bool whole = geo.pairs && cols == kCh;
   const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + blk * kCh;
   const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + blk * kCh;
   OutT* out = static_cast<OutT*>(p.out) + (int64_t)b * p.T * p.D + ch;
@@ -347,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
 #pragma unroll
   for (int k = 0; k < kFwdStages - 1; ++k) issue(k);
   if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
-  if (Z > 1) cluster_wait();
+  link_init(sm, Z);
   float c = 0.f;
   for (int k = 0; k < steps; ++k) {
     cp_async_wait<kFwdStages - 2>();
@@ -356,54 +429,64 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
     const Stage& st = stages[k % kFwdStages];
     const int lo = (k * Z + rank) * kRows + w * S;
     const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
-    float2 a[S], u[S], A = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
-    int n = span.n0;
+    f32x2 a[S], u[S], A = both(1.f), H = both(0.f);
+    // plain: every token and channel is there, and no sequence begins or ends
+    const bool plain = whole && span.on == (1u << S) - 1u && !(span.first | span.last);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const float2 l = pair_of(&st.la[w * S + s][cl]), xv = pair_of(&st.x[w * S + s][cl]);
-      float mx, my;
-      gate_of(l.x, &a[s].x, &mx);
-      gate_of(l.y, &a[s].y, &my);
-      u[s] = make_float2(scale_of<kScale>(mx) * xv.x, scale_of<kScale>(my) * xv.y);
+      float2 m;
+      gate_of(pair_of(&st.la[w * S + s][cl]), &a[s], &m);
+      u[s] = mul2(scale_of<kScale>(m), to_pair(pair_of(&st.x[w * S + s][cl])));
     }
-    if (span.on != (1u << S) - 1u || span.first || (span.last && p.cu)) {
-      // some tokens are not there, or a sequence begins (rare)
+    if (plain) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        H = fma2(a[s], H, u[s]);
+        A = mul2(A, a[s]);
+      }
+    } else {
+      int n = span.n0;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         if (!(span.on >> s & 1)) {
-          a[s] = make_float2(1.f, 1.f);
-          u[s] = make_float2(0.f, 0.f);
+          a[s] = both(1.f);
+          u[s] = both(0.f);
         }
         if (span.first >> s & 1) {
-          if (p.h0 && live) {
-            const float2 h0 = load_state(p.h0 + (int64_t)n * p.D + ch, how);
-            u[s] = make_float2(fmaf(a[s].x, h0.x, u[s].x), fmaf(a[s].y, h0.y, u[s].y));
-          }
-          a[s] = make_float2(-0.f, -0.f);
+          if (p.h0 && live) u[s] = fma2(a[s], to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how)), u[s]);
+          a[s] = A = both(-0.f);
+          H = both(0.f);
+        } else {
+          A = mul2(A, a[s]);
         }
         if (span.last >> s & 1) n = next_sequence(p.cu, p.N, n);
-        H = make_float2(apply(a[s].x, u[s].x, H.x), apply(a[s].y, u[s].y, H.y));
-        A = span.first >> s & 1 ? a[s] : make_float2(A.x * a[s].x, A.y * a[s].y);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        H = make_float2(fmaf(a[s].x, H.x, u[s].x), fmaf(a[s].y, H.y, u[s].y));
-        A = make_float2(A.x * a[s].x, A.y * a[s].y);
+        H = fma2(a[s], H, u[s]);
       }
     }
-    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A.x, H.x, A.y, H.y);
+    const float2 A1 = unpack(A), H1 = unpack(H);
+    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A1.x, H1.x, A1.y, H1.y);
     link_step(sm, k, Z, rank, c);
-    float2 h = warp_carry(sm, w, cl);
+    f32x2 h = warp_carry(sm, w, cl);
     OutT* o = out + (int64_t)lo * p.D;
-    n = span.n0;
+    if (plain) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      h = make_float2(apply(a[s].x, u[s].x, h.x), apply(a[s].y, u[s].y, h.y));
-      if (live && (span.on >> s & 1)) store_pair(o + (int64_t)s * p.D, h, how);
-      if (span.last >> s & 1) {
-        if (live && p.state) store_pair(p.state + (int64_t)n * p.D + ch, h, how);
-        n = next_sequence(p.cu, p.N, n);
+      for (int s = 0; s < S; ++s) {
+        h = fma2(a[s], h, u[s]);
+        put_pair(o, unpack(h));
+        o += p.D;
+      }
+    } else {
+      int n = span.n0;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if (span.first >> s & 1) h = both(0.f);  // a is -0 there: h = u
+        h = fma2(a[s], h, u[s]);
+        if (live && (span.on >> s & 1)) store_pair(o, unpack(h), how);
+        o += p.D;
+        if (span.last >> s & 1) {
+          if (live && p.state) store_pair(p.state + (int64_t)n * p.D + ch, unpack(h), how);
+          n = next_sequence(p.cu, p.N, n);
+        }
       }
     }
     __syncwarp();
@@ -437,13 +520,13 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
-  if (Z > 1) cluster_arrive();
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int cl = 2 * lane, ch = blk * kCh + cl;
   const bool live = ch < p.D;
   const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
   const int cols = min(kCh, p.D - blk * kCh);
+  const bool whole = geo.pairs && cols == kCh;
   const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + blk * kCh;
   const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + blk * kCh;
   const int64_t base = (int64_t)b * p.T * p.D + blk * kCh;
@@ -470,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
 #pragma unroll
   for (int k = 0; k < kBwdStages - 1; ++k) issue(k);
   if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
-  if (Z > 1) cluster_wait();
+  link_init(sm, Z);
   float carry = 0.f;
   for (int k = 0; k < steps; ++k) {
     cp_async_wait<kBwdStages - 2>();
@@ -485,63 +568,81 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
       for (int s = 0; s < S; ++s)
         if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
     }
-    float2 a[S], bs[S], d[S], A = make_float2(1.f, 1.f), E = make_float2(0.f, 0.f);
-    int n = n_last;
+    f32x2 a[S], bs[S], d[S], A = both(1.f), E = both(0.f);
+    const bool plain = whole && span.on == (1u << S) - 1u && !(span.first | span.last);
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
-      const bool on = span.on >> s & 1, last = span.last >> s & 1;
-      const float2 l = pair_of(&st.la[row0 + s][cl]);
-      float mx, my;
-      gate_of(l.x, &a[s].x, &mx);
-      gate_of(l.y, &a[s].y, &my);
-      bs[s] = make_float2(scale_of<kScale>(mx), scale_of<kScale>(my));
-      d[s] = pair_of(&st.dout[row0 + s][cl]);
-      if (!on) {
-        a[s] = make_float2(1.f, 1.f);
-        d[s] = make_float2(0.f, 0.f);
-      }
-      if (last) {
-        if (p.dstate && live) {
-          const float2 ds = load_state(p.dstate + (int64_t)n * p.D + ch, how);
-          d[s] = make_float2(d[s].x + ds.x, d[s].y + ds.y);
-        }
-        E = make_float2(0.f, 0.f);  // nothing comes from the sequence behind
-        A = make_float2(-0.f, -0.f);
-      } else {
-        A = make_float2(A.x * a[s].x, A.y * a[s].y);
-      }
-      E = make_float2(a[s].x * (d[s].x + E.x), a[s].y * (d[s].y + E.y));
-      if (span.first >> s & 1) n = previous_sequence(p.cu, n);
+      float2 m;
+      gate_of(pair_of(&st.la[row0 + s][cl]), &a[s], &m);
+      bs[s] = scale_of<kScale>(m);
+      d[s] = to_pair(pair_of(&st.dout[row0 + s][cl]));
     }
-    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A.x, E.x, A.y, E.y);
-    link_step(sm, k, Z, rank, carry);
-    float2 c = warp_carry(sm, w, cl);
-    n = n_last;
+    if (plain) {
 #pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      if (!live || !(span.on >> s & 1)) continue;
-      const bool last = span.last >> s & 1, first = span.first >> s & 1;
-      if (last) c = make_float2(0.f, 0.f);
-      const float2 g = make_float2(d[s].x + c.x, d[s].y + c.y);
-      float2 before = make_float2(0.f, 0.f);
-      if (!first) {
-        if (lo + s > 0) before = pair_of(&st.h[row0 + s][cl]);
-      } else if (p.h0) {
-        before = load_state(p.h0 + (int64_t)n * p.D + ch, how);
+      for (int s = S - 1; s >= 0; --s) {
+        A = mul2(A, a[s]);
+        E = mul2(a[s], add2(d[s], E));
       }
-      c = make_float2(a[s].x * g.x, a[s].y * g.y);
-      float2 ol = make_float2(c.x * before.x, c.y * before.y);
-      if (kX) {
-        const float2 xv = pair_of(&st.x[row0 + s][cl]);
-        ol.x = fmaf(scale_grad<kScale>(a[s].x, bs[s].x) * xv.x, g.x, ol.x);
-        ol.y = fmaf(scale_grad<kScale>(a[s].y, bs[s].y) * xv.y, g.y, ol.y);
+    } else {
+      int n = n_last;
+#pragma unroll
+      for (int s = S - 1; s >= 0; --s) {
+        if (!(span.on >> s & 1)) {
+          a[s] = both(1.f);
+          d[s] = both(0.f);
+        }
+        A = mul2(A, a[s]);
+        if (span.last >> s & 1) {
+          if (p.dstate && live) d[s] = add2(d[s], to_pair(load_state(p.dstate + (int64_t)n * p.D + ch, how)));
+          E = both(0.f);  // nothing comes from the sequence behind
+          A = both(-0.f);
+        }
+        E = mul2(a[s], add2(d[s], E));
+        if (span.first >> s & 1) n = previous_sequence(p.cu, n);
       }
-      const int64_t at = (int64_t)(lo + s) * p.D;
-      store_pair(dx + at, make_float2(bs[s].x * g.x, bs[s].y * g.y), how);
-      store_pair(dla + at, ol, how);
-      if (first) {
-        if (p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, c, how);
-        n = previous_sequence(p.cu, n);
+    }
+    const float2 A1 = unpack(A), E1 = unpack(E);
+    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A1.x, E1.x, A1.y, E1.y);
+    link_step(sm, k, Z, rank, carry);
+    f32x2 c = warp_carry(sm, w, cl);
+    GradT* ox = dx + (int64_t)(lo + S - 1) * p.D;
+    GateT* ol = dla + (int64_t)(lo + S - 1) * p.D;
+    if (plain) {
+#pragma unroll
+      for (int s = S - 1; s >= 0; --s) {
+        const f32x2 g = add2(d[s], c);
+        c = mul2(a[s], g);
+        f32x2 l = mul2(c, to_pair(pair_of(&st.h[row0 + s][cl])));
+        if (kX)
+          l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(pair_of(&st.x[row0 + s][cl]))), g, l);
+        put_pair(ox, unpack(mul2(bs[s], g)));
+        put_pair(ol, unpack(l));
+        ox -= p.D;
+        ol -= p.D;
+      }
+    } else {
+      int n = n_last;
+#pragma unroll
+      for (int s = S - 1; s >= 0; --s, ox -= p.D, ol -= p.D) {
+        if (!live || !(span.on >> s & 1)) continue;
+        if (span.last >> s & 1) c = both(0.f);
+        const f32x2 g = add2(d[s], c);
+        f32x2 before = both(0.f);
+        if (!(span.first >> s & 1)) {
+          if (lo + s > 0) before = to_pair(pair_of(&st.h[row0 + s][cl]));
+        } else if (p.h0) {
+          before = to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how));
+        }
+        c = mul2(a[s], g);
+        f32x2 l = mul2(c, before);
+        if (kX)
+          l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(pair_of(&st.x[row0 + s][cl]))), g, l);
+        store_pair(ox, unpack(mul2(bs[s], g)), how);
+        store_pair(ol, unpack(l), how);
+        if (span.first >> s & 1) {
+          if (p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, unpack(c), how);
+          n = previous_sequence(p.cu, n);
+        }
       }
     }
     __syncwarp();
@@ -553,12 +654,14 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
 // One token per row: state[slot] <- a state[slot] + b x, out = the new state.  A slot given
 // twice belongs to its first row; the rows after it, and rows whose slot is out of range, are
 // left out and raise the error word.
+constexpr int kStepThreads = 256;
+
 template <typename InT, typename GateT, typename OutT, int kScale>
-__global__ void __launch_bounds__(kThreads) glr_step_kernel(
+__global__ void __launch_bounds__(kStepThreads) glr_step_kernel(
     float* __restrict__ state, const int* __restrict__ slots, int S, const InT* __restrict__ x,
     const GateT* __restrict__ la, OutT* __restrict__ out, int D, int pairs) {
   const int row = blockIdx.y;
-  const int ch = (blockIdx.x * kThreads + threadIdx.x) * 2;
+  const int ch = (blockIdx.x * kStepThreads + threadIdx.x) * 2;
   const bool on = ch < D;
   const int how = ch + 1 >= D ? kFirst : pairs ? kPairs : kSingles;
   int64_t slot = row;
@@ -580,7 +683,7 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(
   if (slots) {
     const int sl = slots[row];
     bool twice = false;
-    for (int r = threadIdx.x; r < row; r += kThreads) twice |= slots[r] == sl;
+    for (int r = threadIdx.x; r < row; r += kStepThreads) twice |= slots[r] == sl;
     twice = __syncthreads_or(twice);
     if (sl == -1) return;
     if (sl < 0 || sl >= S || twice) {
@@ -591,12 +694,10 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(
   }
   if (!on) return;
   float* st = state + slot * D + ch;
-  const float2 h0 = load_state(st, how);
-  float ax, ay, mx, my;
-  gate_of(l.x, &ax, &mx);
-  gate_of(l.y, &ay, &my);
-  const float2 h = make_float2(fmaf(ax, h0.x, scale_of<kScale>(mx) * xv.x),
-                               fmaf(ay, h0.y, scale_of<kScale>(my) * xv.y));
+  f32x2 a;
+  float2 m;
+  gate_of(l, &a, &m);
+  const float2 h = unpack(fma2(a, to_pair(load_state(st, how)), mul2(scale_of<kScale>(m), to_pair(xv))));
   store_pair(st, h, how);
   store_pair(out + at, h, how);
 }
@@ -658,13 +759,13 @@ cudaError_t launch(const GlrArgs& p, bool backward, cudaStream_t s) {
   g.dout = copy_bytes(p.dout, dense, p.D, p.D, sizeof(OutT));
   // a warp's tokens: as many as leave room for two CTAs of two stages per SM
   if (backward) {
-    constexpr int S = sizeof(GateT) + 2 * sizeof(OutT) + sizeof(InT) <= 10 ? 8 : 4;
+    constexpr int S = sizeof(GateT) + 2 * sizeof(OutT) + sizeof(InT) <= 10 ? 4 : 2;
     g.Z = cluster_of(items, p.T, kWarps * S);
     using Stage = BwdStage<InT, GateT, OutT, S, kScale != LL_GLR_NONE>;
     return launch_cluster(glr_bwd_kernel<InT, GateT, OutT, S, kScale>, p, g,
                           kBwdStages * sizeof(Stage), s);
   }
-  constexpr int S = sizeof(GateT) + sizeof(InT) <= 6 ? 16 : 8;
+  constexpr int S = sizeof(GateT) + sizeof(InT) <= 6 ? 8 : 4;
   g.Z = cluster_of(items, p.T, kWarps * S);
   return launch_cluster(glr_fwd_kernel<InT, GateT, OutT, S, kScale>, p, g,
                         kFwdStages * sizeof(FwdStage<InT, GateT, S>), s);
@@ -682,8 +783,8 @@ cudaError_t launch_step(float* state, const int* slots, int S, const void* x, co
                         void* out, int B, int D, cudaStream_t s) {
   const int pairs = D % 2 == 0 && aligned(state, 8) && aligned(x, 2 * sizeof(InT)) &&
                     aligned(la, 2 * sizeof(GateT)) && aligned(out, 2 * sizeof(OutT));
-  const dim3 grid((D + 2 * kThreads - 1) / (2 * kThreads), B);
-  glr_step_kernel<InT, GateT, OutT, kScale><<<grid, kThreads, 0, s>>>(
+  const dim3 grid((D + 2 * kStepThreads - 1) / (2 * kStepThreads), B);
+  glr_step_kernel<InT, GateT, OutT, kScale><<<grid, kStepThreads, 0, s>>>(
       state, slots, S, static_cast<const InT*>(x), static_cast<const GateT*>(la),
       static_cast<OutT*>(out), D, pairs);
   return cudaGetLastError();

@@ -629,7 +629,7 @@ int loglinear_device_error(ll_stream_t stream, unsigned* flags) {
   cudaError_t e = tc_take_error(reinterpret_cast<cudaStream_t>(stream), &f1);
   if (e == cudaSuccess) e = tcb_take_error(reinterpret_cast<cudaStream_t>(stream), &f2);
   if (e == cudaSuccess) e = glr_take_error(reinterpret_cast<cudaStream_t>(stream), &f3);
-  *flags = f1 | f2 | f3 << 4;
+  *flags = f1 | f2 | (f3 & 1u) << 4 | (f3 & 2u) << 2;
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
 
