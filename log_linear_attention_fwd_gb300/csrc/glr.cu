@@ -2,16 +2,18 @@
 // b_t = 1, 1 - a_t or sqrt(1 - a_t^2); its gradients; and its single-token step.
 //
 // Forward and backward are one scan each.  The maps c -> A c + H of consecutive tokens compose
-// to a map of the same form, so a segment of tokens is known by two floats per channel.  A
-// cluster of Z CTAs owns 64 channels of one batch entry and marches through time, Z tiles of
-// 16 S tokens per step: lane = 2 channels, warp = S consecutive tokens, which it folds into one
-// map; the CTA folds its 8 warps' maps and hands the result to every CTA of the cluster through
-// distributed shared memory; after one cluster barrier each CTA knows the carry into its
-// tile and, from all Z maps, the carry into the next step.  Then the warps run their tokens
+// to a map of the same form, so a run of tokens is known by two floats per channel.  A cluster
+// of Z CTAs owns 32 channels of one batch entry and marches through time, Z tiles of 16 S tokens
+// per step: lane = 2 channels, half a warp = S consecutive tokens (a segment), which it folds
+// into one map; the CTA folds its 16 segments' maps and sends the result to every CTA of the
+// cluster (st.async into their shared memory, which counts the bytes on an mbarrier there: a
+// cluster barrier would also wait for the step's global stores).  From the Z maps each CTA has
+// the carry into its tile and the carry into the next step, and the segments run their tokens
 // from their carry, in registers.  Every input is read once and every output written once,
-// nothing goes through global memory in between, no CTA waits on a flag, and the folds have a
-// fixed order, so results do not depend on timing.  The next tile's inputs are copied to
-// shared memory (cp.async) while this one is worked on.
+// nothing goes through global memory in between, and the folds have a fixed order, so results
+// do not depend on timing.  The next tile's inputs are copied to shared memory (cp.async)
+// while this one is worked on, and four small CTAs share an SM, so that one folds and waits
+// while the others compute.
 //
 // Z is chosen so that batch entries x channel blocks x Z CTAs fill the GPU (cluster_of).
 // The backward is the same scan with time reversed.
@@ -32,9 +34,10 @@ __device__ unsigned int g_glr_error = 0;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCh = 64;        // channels of a CTA: two per lane
+constexpr int kThreads = 256;
+constexpr int kCh = 32;                      // channels of a CTA: two per lane
+constexpr int kSegs = kThreads / (kCh / 2);  // segments of a tile
+constexpr int kPerSm = 4;                    // CTAs per SM, shared memory permitting
 constexpr int kMaxCluster = 8;
 
 // ---------------------------------------------------------------- pairs of fp32
@@ -168,42 +171,56 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Rows [lo, hi) of a tile [kRows][64] of which `cols` channels exist, src addressing row 0.
-// bytes: the widest copy that pointers, strides and the number of channels allow (16, 4 or one
-// element).  What is not copied keeps its old contents, which no live lane uses.
-template <typename T, int kRows>
-__device__ __forceinline__ void fill(T* dst, const T* src, int64_t stride, int lo, int hi,
+// A tile in shared memory: 16 S tokens of 32 channels.  The two segments of a warp are read at
+// once; bf16 rows are half a bank line, so odd segments have each pair of rows swapped.
+template <typename T, int S>
+struct Tile {
+  T v[kSegs * S * kCh];
+  static __device__ __forceinline__ int place(int row) {
+    return sizeof(T) == 2 ? row ^ (row / S & 1) : row;
+  }
+  __device__ __forceinline__ T* at(int row, int ch) { return v + place(row) * kCh + ch; }
+  __device__ __forceinline__ float2 pair(int seg, int s, int ch) const {
+    const int odd = sizeof(T) == 2 ? seg & 1 : 0;
+    return pair_of(v + seg * S * kCh + (s ^ odd) * kCh + ch);
+  }
+};
+
+// Rows [lo, hi) of a tile of which `cols` channels exist, src addressing row 0.  bytes: the
+// widest copy that pointers, strides and the number of channels allow (16, 4 or one element).
+// What is not copied keeps its old contents, which no live lane uses.
+template <typename T, int S>
+__device__ __forceinline__ void fill(Tile<T, S>& dst, const T* src, int64_t stride, int lo, int hi,
                                      int cols, int bytes) {
+  constexpr int rows = kSegs * S;
   if (bytes == 16) {
     constexpr int per = 16 / sizeof(T), chunks = kCh / per, pass = kThreads / chunks;
     const int r0 = threadIdx.x / chunks, c = (threadIdx.x % chunks) * per;
-    const T* p = src + r0 * stride + c;
-    T* d = dst + r0 * kCh + c;
-    if (lo == 0 && hi >= kRows && cols == kCh && kRows % pass == 0) {
+    if (lo == 0 && hi >= rows && cols == kCh && rows % pass == 0) {
+      const T* p = src + r0 * stride + c;
 #pragma unroll
-      for (int r = 0; r < kRows; r += pass) {
-        cp_async16(d + r * kCh, p);
+      for (int r = 0; r < rows; r += pass) {
+        cp_async16(dst.at(r0 + r, c), p);
         p += pass * stride;
       }
     } else {
 #pragma unroll 1
-      for (int r = r0; r < kRows; r += pass) {
-        if (r >= lo && r < hi && c < cols) cp_async16(dst + r * kCh + c, src + r * stride + c);
+      for (int r = r0; r < rows; r += pass) {
+        if (r >= lo && r < hi && c < cols) cp_async16(dst.at(r, c), src + r * stride + c);
       }
     }
   } else if (bytes == 4) {
     constexpr int per = 4 / sizeof(T), chunks = kCh / per;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < kRows * chunks; i += kThreads) {
+    for (int i = threadIdx.x; i < rows * chunks; i += kThreads) {
       const int r = i / chunks, c = (i % chunks) * per;
-      if (r >= lo && r < hi && c < cols)
-        tc::cp_async4(dst + r * kCh + c, src + r * stride + c, 4);
+      if (r >= lo && r < hi && c < cols) tc::cp_async4(dst.at(r, c), src + r * stride + c, 4);
     }
   } else {
 #pragma unroll 4
-    for (int i = threadIdx.x; i < kRows * kCh; i += kThreads) {
+    for (int i = threadIdx.x; i < rows * kCh; i += kThreads) {
       const int r = i / kCh, c = i % kCh;
-      if (r >= lo && r < hi && c < cols) dst[r * kCh + c] = src[r * stride + c];
+      if (r >= lo && r < hi && c < cols) *dst.at(r, c) = src[r * stride + c];
     }
   }
 }
@@ -298,10 +315,10 @@ __device__ __forceinline__ void send(float2* p, uint64_t* bar, uint32_t rank, fl
 }
 
 struct LinkSmem {
-  float2 warp[kWarps][kCh];            // the warps' maps; then those of all warps before
-  float2 tile[2][kMaxCluster][kCh];    // the cluster's tiles' maps, of even and odd steps
-  float carry[kCh];                    // into this CTA's tile
-  uint64_t bar[2];                     // the tiles' maps of even and odd steps are there
+  // the segments' maps; then entry g: that of segments 0 .. g, and the last: the carry into the tile
+  float2 seg[kSegs][kCh];
+  float2 tile[2][kMaxCluster - 1][kCh];  // the other tiles' maps, of even and odd steps
+  uint64_t bar[2];                       // they are there
 };
 
 // Before the first step; ends with a barrier over the cluster.
@@ -316,9 +333,8 @@ __device__ __forceinline__ void link_init(LinkSmem& sm, int Z) {
   cluster_sync();
 }
 
-// After the warps' maps of step k are in sm.warp: the carry into this CTA's tile goes to
-// sm.carry, sm.warp to the maps of the warps before, and `c` (threads below 64, their channel's
-// carry into the step) moves on to the next step.  Starts and ends with a block barrier.
+// After the segments' maps of step k are in sm.seg: folds them, and moves `c` (warp 0, a channel
+// per lane: the carry into the step) on to the next step.  Starts and ends with a block barrier.
 //
 // A CTA sends its map of step k + 1 after it has read the maps of step k, and has those of step
 // k + 1 before it sends that of step k + 2: two buffers are enough.  It leaves the last step
@@ -327,24 +343,24 @@ __device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, 
   const int tid = threadIdx.x;
   __syncthreads();
   if (tid < kCh) {
-    if (Z > 1 && tid == 0) tc::mbar_arrive_expect_tx(&sm.bar[k & 1], Z * kCh * sizeof(float2));
-    float2 m = sm.warp[0][tid];
-    sm.warp[0][tid] = make_float2(1.f, 0.f);
+    if (Z > 1 && tid == 0)
+      tc::mbar_arrive_expect_tx(&sm.bar[k & 1], (Z - 1) * kCh * sizeof(float2));
+    float2 m = sm.seg[0][tid];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      const float2 n = sm.warp[w][tid];
-      sm.warp[w][tid] = m;
-      then(m, n);
+    for (int g = 1; g < kSegs; ++g) {
+      then(m, sm.seg[g][tid]);
+      if (g < kSegs - 1) sm.seg[g][tid] = m;
     }
     if (Z == 1) {
-      sm.carry[tid] = c;
+      sm.seg[kSegs - 1][tid].x = c;
       c = apply(m.x, m.y, c);
     } else {
-      for (int z = 0; z < Z; ++z) send(&sm.tile[k & 1][rank][tid], &sm.bar[k & 1], z, m);
+      for (int z = 0; z < Z; ++z)
+        if (z != rank) send(&sm.tile[k & 1][rank - (rank > z)][tid], &sm.bar[k & 1], z, m);
       if (!tc::mbar_wait(&sm.bar[k & 1], (k >> 1) & 1)) atomicOr(&g_glr_error, 2u);
       for (int z = 0; z < Z; ++z) {
-        if (z == rank) sm.carry[tid] = c;
-        const float2 n = sm.tile[k & 1][z][tid];
+        if (z == rank) sm.seg[kSegs - 1][tid].x = c;
+        const float2 n = z == rank ? m : sm.tile[k & 1][z - (z > rank)][tid];
         c = apply(n.x, n.y, c);
       }
     }
@@ -352,11 +368,12 @@ __device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, 
   __syncthreads();
 }
 
-// The carry into warp w's tokens, from the tile's and the warps before it.
-__device__ __forceinline__ f32x2 warp_carry(const LinkSmem& sm, int w, int cl) {
-  const float2 c = *reinterpret_cast<const float2*>(&sm.carry[cl]);
-  const float4 m = *reinterpret_cast<const float4*>(&sm.warp[w][cl]);
-  return pack(apply(m.x, m.y, c.x), apply(m.z, m.w, c.y));
+// The carry into a segment, from the tile's and the segments before it.
+__device__ __forceinline__ f32x2 segment_carry(const LinkSmem& sm, int g, int cl) {
+  const float4 c = *reinterpret_cast<const float4*>(&sm.seg[kSegs - 1][cl]);
+  if (g == 0) return pack(c.x, c.z);
+  const float4 m = *reinterpret_cast<const float4*>(&sm.seg[g - 1][cl]);
+  return pack(apply(m.x, m.y, c.x), apply(m.z, m.w, c.z));
 }
 
 struct Geometry {
@@ -370,8 +387,8 @@ struct Geometry {
 __device__ __forceinline__ void empty_sequences(const int* cu, int N, int T, int b, int D, int ch,
                                                 int how, const float* src, float* dst) {
   if (!dst) return;
-  const int w = threadIdx.x >> 5;
-  const int n0 = cu ? w : (w == 0 && T == 0 ? b : N), step = cu ? kWarps : N;
+  const int g = threadIdx.x / (kCh / 2);
+  const int n0 = cu ? g : (g == 0 && T == 0 ? b : N), step = cu ? kSegs : N;
   for (int n = n0; n < N; n += step) {
     if (cu && __ldg(cu + n + 1) > __ldg(cu + n)) continue;
     const int64_t at = (int64_t)n * D + ch;
@@ -383,23 +400,23 @@ __device__ __forceinline__ void empty_sequences(const int* cu, int N, int T, int
 
 template <typename InT, typename GateT, int S>
 struct FwdStage {
-  GateT la[kWarps * S][kCh];
-  InT x[kWarps * S][kCh];
+  Tile<GateT, S> la;
+  Tile<InT, S> x;
 };
 
 constexpr int kFwdStages = 2;
 
 template <typename InT, typename GateT, typename OutT, int S, int kScale>
-__global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometry geo) {
-  constexpr int kRows = kWarps * S;
+__global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Geometry geo) {
+  constexpr int kRows = kSegs * S;
   using Stage = FwdStage<InT, GateT, S>;
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int cl = 2 * lane, ch = blk * kCh + cl;
+  const int seg = threadIdx.x / (kCh / 2);
+  const int cl = 2 * (threadIdx.x % (kCh / 2)), ch = blk * kCh + cl;
   const bool live = ch < p.D;
   const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
   const int cols = min(kCh, p.D - blk * kCh);
@@ -412,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
     if (k < steps) {
       Stage& st = stages[k % kFwdStages];
       const int t0 = (k * Z + rank) * kRows, rows = min(kRows, p.T - t0);
-      fill<GateT, kRows>(&st.la[0][0], la + (int64_t)t0 * p.sl[1], p.sl[1], 0, rows, cols, geo.la);
-      fill<InT, kRows>(&st.x[0][0], x + (int64_t)t0 * p.sx[1], p.sx[1], 0, rows, cols, geo.x);
+      fill(st.la, la + (int64_t)t0 * p.sl[1], p.sl[1], 0, rows, cols, geo.la);
+      fill(st.x, x + (int64_t)t0 * p.sx[1], p.sx[1], 0, rows, cols, geo.x);
     }
     cp_async_commit();
   };
@@ -427,16 +444,16 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
     __syncthreads();
     issue(k + kFwdStages - 1);
     const Stage& st = stages[k % kFwdStages];
-    const int lo = (k * Z + rank) * kRows + w * S;
+    const int lo = (k * Z + rank) * kRows + seg * S;
     const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
     f32x2 a[S], u[S], A = both(1.f), H = both(0.f);
     // plain: every token and channel is there, and no sequence begins or ends
-    const bool plain = whole && span.on == (1u << S) - 1u && !(span.first | span.last);
+    const bool plain = __all_sync(0xffffffffu, whole && span.on == (1u << S) - 1u && !(span.first | span.last));
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       float2 m;
-      gate_of(pair_of(&st.la[w * S + s][cl]), &a[s], &m);
-      u[s] = mul2(scale_of<kScale>(m), to_pair(pair_of(&st.x[w * S + s][cl])));
+      gate_of(st.la.pair(seg, s, cl), &a[s], &m);
+      u[s] = mul2(scale_of<kScale>(m), to_pair(st.x.pair(seg, s, cl)));
     }
     if (plain) {
 #pragma unroll
@@ -464,9 +481,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
       }
     }
     const float2 A1 = unpack(A), H1 = unpack(H);
-    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A1.x, H1.x, A1.y, H1.y);
+    *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, H1.x, A1.y, H1.y);
     link_step(sm, k, Z, rank, c);
-    f32x2 h = warp_carry(sm, w, cl);
+    f32x2 h = segment_carry(sm, seg, cl);
     OutT* o = out + (int64_t)lo * p.D;
     if (plain) {
 #pragma unroll
@@ -498,22 +515,28 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(GlrArgs p, Geometr
 // With g_t the gradient of h_t: g_t = dout_t + a_{t+1} g_{t+1} (plus the final state's gradient
 // at the end of a sequence), dx_t = b_t g_t, dlog_a_t = a_t h_{t-1} g_t + b'(log a_t) x_t g_t and
 // the first state's gradient is a_t g_t at the sequence's first token.  The carry from t to t-1
-// is c_t = a_t g_t = a_t c_{t+1} + a_t dout_t, scanned from the end: rank 0's warp 0 holds the
-// last S tokens of a step.
+// is c_t = a_t g_t = a_t c_{t+1} + a_t dout_t, scanned from the end: rank 0's segment 0 holds
+// the last S tokens of a step.
 
 template <typename InT, typename GateT, typename GradT, int S, bool kX>
 struct BwdStage {
-  GateT la[kWarps * S][kCh];
-  GradT dout[kWarps * S][kCh];
-  GradT h[kWarps * S][kCh];  // of the token before
-  InT x[kX ? kWarps * S : 1][kCh];
+  Tile<GateT, S> la;
+  Tile<GradT, S> dout;
+  Tile<GradT, S> h;  // of the token before
+  Tile<InT, S> x;
+};
+template <typename InT, typename GateT, typename GradT, int S>
+struct BwdStage<InT, GateT, GradT, S, false> {
+  Tile<GateT, S> la;
+  Tile<GradT, S> dout;
+  Tile<GradT, S> h;
 };
 
 constexpr int kBwdStages = 2;
 
 template <typename InT, typename GateT, typename GradT, int S, int kScale>
-__global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometry geo) {
-  constexpr int kRows = kWarps * S;
+__global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Geometry geo) {
+  constexpr int kRows = kSegs * S;
   constexpr bool kX = kScale != LL_GLR_NONE;
   using Stage = BwdStage<InT, GateT, GradT, S, kX>;
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -521,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int cl = 2 * lane, ch = blk * kCh + cl;
+  const int seg = threadIdx.x / (kCh / 2);
+  const int cl = 2 * (threadIdx.x % (kCh / 2)), ch = blk * kCh + cl;
   const bool live = ch < p.D;
   const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
   const int cols = min(kCh, p.D - blk * kCh);
@@ -542,11 +565,10 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
       Stage& st = stages[k % kBwdStages];
       const int t0 = tile_start(k), rows = min(kRows, p.T - t0);
       const int64_t at = (int64_t)t0 * p.D;
-      fill<GateT, kRows>(&st.la[0][0], la + (int64_t)t0 * p.sl[1], p.sl[1], 0, rows, cols, geo.la);
-      fill<GradT, kRows>(&st.dout[0][0], dout + at, p.D, 0, rows, cols, geo.dout);
-      fill<GradT, kRows>(&st.h[0][0], hs + at - p.D, p.D, t0 == 0, rows, cols, geo.h);
-      if (kX)
-        fill<InT, kRows>(&st.x[0][0], x + (int64_t)t0 * p.sx[1], p.sx[1], 0, rows, cols, geo.x);
+      fill(st.la, la + (int64_t)t0 * p.sl[1], p.sl[1], 0, rows, cols, geo.la);
+      fill(st.dout, dout + at, p.D, 0, rows, cols, geo.dout);
+      fill(st.h, hs + at - p.D, p.D, t0 == 0, rows, cols, geo.h);
+      if constexpr (kX) fill(st.x, x + (int64_t)t0 * p.sx[1], p.sx[1], 0, rows, cols, geo.x);
     }
     cp_async_commit();
   };
@@ -560,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
     __syncthreads();
     issue(k + kBwdStages - 1);
     const Stage& st = stages[k % kBwdStages];
-    const int row0 = (kWarps - 1 - w) * S, lo = tile_start(k) + row0;
+    const int back = kSegs - 1 - seg, lo = tile_start(k) + back * S;
     const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
     int n_last = span.n0;  // the sequence of the last token that is on
     if (p.cu) {
@@ -569,13 +591,13 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
         if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
     }
     f32x2 a[S], bs[S], d[S], A = both(1.f), E = both(0.f);
-    const bool plain = whole && span.on == (1u << S) - 1u && !(span.first | span.last);
+    const bool plain = __all_sync(0xffffffffu, whole && span.on == (1u << S) - 1u && !(span.first | span.last));
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
       float2 m;
-      gate_of(pair_of(&st.la[row0 + s][cl]), &a[s], &m);
+      gate_of(st.la.pair(back, s, cl), &a[s], &m);
       bs[s] = scale_of<kScale>(m);
-      d[s] = to_pair(pair_of(&st.dout[row0 + s][cl]));
+      d[s] = to_pair(st.dout.pair(back, s, cl));
     }
     if (plain) {
 #pragma unroll
@@ -602,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
       }
     }
     const float2 A1 = unpack(A), E1 = unpack(E);
-    *reinterpret_cast<float4*>(&sm.warp[w][cl]) = make_float4(A1.x, E1.x, A1.y, E1.y);
+    *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, E1.x, A1.y, E1.y);
     link_step(sm, k, Z, rank, carry);
-    f32x2 c = warp_carry(sm, w, cl);
+    f32x2 c = segment_carry(sm, seg, cl);
     GradT* ox = dx + (int64_t)(lo + S - 1) * p.D;
     GateT* ol = dla + (int64_t)(lo + S - 1) * p.D;
     if (plain) {
@@ -612,9 +634,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
       for (int s = S - 1; s >= 0; --s) {
         const f32x2 g = add2(d[s], c);
         c = mul2(a[s], g);
-        f32x2 l = mul2(c, to_pair(pair_of(&st.h[row0 + s][cl])));
-        if (kX)
-          l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(pair_of(&st.x[row0 + s][cl]))), g, l);
+        f32x2 l = mul2(c, to_pair(st.h.pair(back, s, cl)));
+        if constexpr (kX)
+          l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(st.x.pair(back, s, cl))), g, l);
         put_pair(ox, unpack(mul2(bs[s], g)));
         put_pair(ol, unpack(l));
         ox -= p.D;
@@ -629,14 +651,14 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(GlrArgs p, Geometr
         const f32x2 g = add2(d[s], c);
         f32x2 before = both(0.f);
         if (!(span.first >> s & 1)) {
-          if (lo + s > 0) before = to_pair(pair_of(&st.h[row0 + s][cl]));
+          if (lo + s > 0) before = to_pair(st.h.pair(back, s, cl));
         } else if (p.h0) {
           before = to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how));
         }
         c = mul2(a[s], g);
         f32x2 l = mul2(c, before);
-        if (kX)
-          l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(pair_of(&st.x[row0 + s][cl]))), g, l);
+        if constexpr (kX)
+          l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(st.x.pair(back, s, cl))), g, l);
         store_pair(ox, unpack(mul2(bs[s], g)), how);
         store_pair(ol, unpack(l), how);
         if (span.first >> s & 1) {
@@ -716,11 +738,13 @@ int copy_bytes(const void* p, int64_t sb, int64_t st, int64_t D, int size) {
   return size;
 }
 
-// CTAs that share a channel block: doubled while that keeps the launch within two CTAs per SM and
-// a step within the sequence.
-int cluster_of(int64_t items, int64_t T, int rows) {
+// CTAs that share a channel block: doubled while the launch stays within what the SMs hold at
+// once and a step within the sequence.
+int cluster_of(int64_t items, int64_t T, int rows, size_t smem) {
+  const int64_t fit = (int64_t)(233472 / (smem + sizeof(LinkSmem) + 1024));
+  const int64_t slots = 152 * (fit < kPerSm ? fit : kPerSm);
   int Z = 1;
-  while (Z < kMaxCluster && items * Z * 2 <= 2 * 152 && (int64_t)Z * rows < T) Z *= 2;
+  while (Z < kMaxCluster && items * Z * 2 <= slots && (int64_t)Z * rows < T) Z *= 2;
   return Z;
 }
 
@@ -757,18 +781,16 @@ cudaError_t launch(const GlrArgs& p, bool backward, cudaStream_t s) {
   g.la = copy_bytes(p.log_a, p.sl[0], p.sl[1], p.D, sizeof(GateT));
   g.h = copy_bytes(p.h, dense, p.D, p.D, sizeof(OutT));
   g.dout = copy_bytes(p.dout, dense, p.D, p.D, sizeof(OutT));
-  // a warp's tokens: as many as leave room for two CTAs of two stages per SM
   if (backward) {
-    constexpr int S = sizeof(GateT) + 2 * sizeof(OutT) + sizeof(InT) <= 10 ? 4 : 2;
-    g.Z = cluster_of(items, p.T, kWarps * S);
-    using Stage = BwdStage<InT, GateT, OutT, S, kScale != LL_GLR_NONE>;
-    return launch_cluster(glr_bwd_kernel<InT, GateT, OutT, S, kScale>, p, g,
-                          kBwdStages * sizeof(Stage), s);
+    constexpr int S = 4;  // the backward keeps three values per token in registers
+    constexpr size_t smem = kBwdStages * sizeof(BwdStage<InT, GateT, OutT, S, kScale != LL_GLR_NONE>);
+    g.Z = cluster_of(items, p.T, kSegs * S, smem);
+    return launch_cluster(glr_bwd_kernel<InT, GateT, OutT, S, kScale>, p, g, smem, s);
   }
-  constexpr int S = sizeof(GateT) + sizeof(InT) <= 6 ? 8 : 4;
-  g.Z = cluster_of(items, p.T, kWarps * S);
-  return launch_cluster(glr_fwd_kernel<InT, GateT, OutT, S, kScale>, p, g,
-                        kFwdStages * sizeof(FwdStage<InT, GateT, S>), s);
+  constexpr int S = 8;
+  constexpr size_t smem = kFwdStages * sizeof(FwdStage<InT, GateT, S>);
+  g.Z = cluster_of(items, p.T, kSegs * S, smem);
+  return launch_cluster(glr_fwd_kernel<InT, GateT, OutT, S, kScale>, p, g, smem, s);
 }
 
 template <typename InT, typename GateT, typename OutT>
