@@ -86,38 +86,39 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 }
 
 // a = exp(la) and m = 1 - a.  Gates live near a = 1, where 1 - a computed from a would lose the
-// digits that la still has: for |la| <= 1/4 the Taylor sum of exp(la) - 1 (6 terms, its
+// digits that la still has: for |la| <= 1/4 the Taylor sum of 1 - exp(la) (6 terms, its
 // remainder is below 2^-24) gives m, and a from it to half a unit; beyond, exp itself is far
-// enough from 1 (m off by 2^-20 at most).  Scalar, for its constants are then part of the
-// instructions; packed ones would hold registers.
-__device__ __forceinline__ void gate_of(float la, float* a, float* m) {
-  float p = fmaf(1.f / 720.f, la, 1.f / 120.f);
-  p = fmaf(p, la, 1.f / 24.f);
-  p = fmaf(p, la, 1.f / 6.f);
-  p = fmaf(p, la, 0.5f);
-  p = fmaf(p, la, 1.f);
-  const float e = exp2_approx(la * 1.44269504f);
-  const bool near = fabsf(la) <= 0.25f;
-  *a = near ? fmaf(p, la, 1.f) : e;
-  *m = near ? p * -la : 1.f - e;
-}
-__device__ __forceinline__ void gate_of(float2 la, f32x2* a, float2* m) {
-  float x, y;
-  gate_of(la.x, &x, &m->x);
-  gate_of(la.y, &y, &m->y);
-  *a = pack(x, y);
+// enough from 1 (m off by 2^-20 at most).
+__device__ __forceinline__ void gate_of(float2 la, f32x2* a, f32x2* m) {
+  const f32x2 l = to_pair(la);
+  f32x2 p = fma2(both(-1.f / 720.f), l, both(-1.f / 120.f));
+  p = fma2(p, l, both(-1.f / 24.f));
+  p = fma2(p, l, both(-1.f / 6.f));
+  p = fma2(p, l, both(-0.5f));
+  p = fma2(p, l, both(-1.f));
+  const f32x2 m0 = mul2(p, l);
+  const float2 s = unpack(mul2(l, both(1.44269504f)));
+  const f32x2 e = pack(exp2_approx(s.x), exp2_approx(s.y));
+  const float2 near_m = unpack(m0), near_a = unpack(fma2(m0, both(-1.f), both(1.f)));
+  const float2 far_a = unpack(e), far_m = unpack(fma2(e, both(-1.f), both(1.f)));
+  const bool nx = fabsf(la.x) <= 0.25f, ny = fabsf(la.y) <= 0.25f;
+  *a = pack(nx ? near_a.x : far_a.x, ny ? near_a.y : far_a.y);
+  *m = pack(nx ? near_m.x : far_m.x, ny ? near_m.y : far_m.y);
 }
 
 // b from m: 1 - a^2 = m (2 - m).  0 where a >= 1; a NaN stays one.
-__device__ __forceinline__ float sqrt_scale(float m) {
+__device__ __forceinline__ float sqrt_clamped(float x) {
   float v;
-  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(v) : "f"(m * (2.f - m)));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(v) : "f"(x));
   return sqrt_approx(v);
 }
 template <int kScale>
-__device__ __forceinline__ f32x2 scale_of(float2 m) {
-  if (kScale == LL_GLR_ONE_MINUS) return pack(m.x, m.y);
-  if (kScale == LL_GLR_SQRT) return pack(sqrt_scale(m.x), sqrt_scale(m.y));
+__device__ __forceinline__ f32x2 scale_of(f32x2 m) {
+  if (kScale == LL_GLR_ONE_MINUS) return m;
+  if (kScale == LL_GLR_SQRT) {
+    const float2 v = unpack(mul2(m, fma2(m, both(-1.f), both(2.f))));
+    return pack(sqrt_clamped(v.x), sqrt_clamped(v.y));
+  }
   return both(1.f);
 }
 // db / d log a.  The square root's is infinite at a = 1 and taken as 0 there.
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     const bool plain = __all_sync(0xffffffffu, whole && span.on == (1u << S) - 1u && !(span.first | span.last));
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      float2 m;
+      f32x2 m;
       gate_of(st.la.pair(seg, s, cl), &a[s], &m);
       u[s] = mul2(scale_of<kScale>(m), to_pair(st.x.pair(seg, s, cl)));
     }
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     const bool plain = __all_sync(0xffffffffu, whole && span.on == (1u << S) - 1u && !(span.first | span.last));
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
-      float2 m;
+      f32x2 m;
       gate_of(st.la.pair(back, s, cl), &a[s], &m);
       bs[s] = scale_of<kScale>(m);
       d[s] = to_pair(st.dout.pair(back, s, cl));
@@ -716,8 +717,7 @@ __global__ void __launch_bounds__(kStepThreads) glr_step_kernel(
   }
   if (!on) return;
   float* st = state + slot * D + ch;
-  f32x2 a;
-  float2 m;
+  f32x2 a, m;
   gate_of(l, &a, &m);
   const float2 h = unpack(fma2(a, to_pair(load_state(st, how)), mul2(scale_of<kScale>(m), to_pair(xv))));
   store_pair(st, h, how);
