@@ -482,6 +482,8 @@ typedef struct {
 #define LL_CACHE_ERR_POSITION 2u  /* position outside the cache */
 #define LL_CACHE_ERR_PAGES 4u     /* no free page was left (the slot is left without it) */
 #define LL_CACHE_ERR_MISSING 8u   /* a page that the position needs is not there */
+#define LL_CACHE_ERR_WAIT 16u     /* a wait inside loglinear_cache_step ran out of time; the rows'
+                                     results are not valid */
 
 LL_API int loglinear_cache_scratch_size(int64_t slots, int64_t n_pages, size_t* bytes);
 

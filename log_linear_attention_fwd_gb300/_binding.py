@@ -621,7 +621,7 @@ def loglinear_glr_step(state, x, log_a, slots=None, scale="none", out=None, out_
 # ---------------------------------------------------------------- paged decode cache
 
 CACHE_BLOCK = 64  # positions of a block (LL_CACHE_BLOCK)
-CACHE_ERR_SLOT, CACHE_ERR_POSITION, CACHE_ERR_PAGES, CACHE_ERR_MISSING = 1, 2, 4, 8
+CACHE_ERR_SLOT, CACHE_ERR_POSITION, CACHE_ERR_PAGES, CACHE_ERR_MISSING, CACHE_ERR_WAIT = 1, 2, 4, 8, 16
 
 
 class LogLinearCache:

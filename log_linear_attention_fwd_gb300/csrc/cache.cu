@@ -17,7 +17,10 @@
 //
 // A page is free when its reference count is 0, and the lowest free ones are taken first, in
 // the order of the rows that ask: the result of every call is determined by its inputs.
+#include <algorithm>
+
 #include "ll_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace ll {
 namespace {
@@ -318,8 +321,18 @@ __device__ __forceinline__ void block_decays(const float* la, int r, int from, f
 
 // ---------------------------------------------------------------- step
 
-constexpr int kStepThreads = 256;
-constexpr int kStepWarps = kStepThreads / 32;
+// One CTA per (row, head, dv / split columns); the columns of a state do not mix, so CTAs that
+// share a head share nothing but the scores, which each computes.  A producer warp brings the
+// block's tokens and then the pages, in stages of up to 16 KB, to shared memory by bulk
+// copies; eight warps consume them.  Bound by HBM: a page of 128 x 128 is 64 KB for 32 KFLOP, and
+// what counts is that copies are always in flight (two CTAs of four stages per SM).  A stage is
+// kRowsPer rows per thread of one page; the pages of a row chunk come one after the other, so
+// that a fold can sum them and the tokens' products for its rows in registers.
+constexpr int kConsumers = 256;
+constexpr int kStepThreads = kConsumers + 32;
+constexpr int kStepWarps = kConsumers / 32;
+constexpr int kRowsPer = 4;
+constexpr int kStageFloats = kConsumers * 4 * kRowsPer;
 constexpr int kMaxLevels = 24;
 
 template <typename T>
@@ -339,6 +352,14 @@ __device__ __forceinline__ float4 fma4(float s, float4 x, float4 y) {
   return make_float4(fmaf(s, x.x, y.x), fmaf(s, x.y, y.y), fmaf(s, x.z, y.z), fmaf(s, x.w, y.w));
 }
 
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
 struct StepArgs {
   const int* slots;
   const int* pos;
@@ -348,31 +369,34 @@ struct StepArgs {
   const float* log_a;  // may be null
   const float* lam;
   void* out;
-  int n, L, split;
+  int n, L, split, stages;
 };
 
-// One CTA per (row, head, dv / split columns).  The columns of a state do not mix, so CTAs that
-// share a head share nothing but the scores, which each computes.
+// Shared memory behind the stages: the block's keys and values.
+template <typename T>
+__host__ __device__ constexpr size_t window_bytes(int dk, int cols) {
+  return sizeof(T) * kW * (size_t)(dk + cols);
+}
+
 template <typename T, typename OutT>
-__global__ void __launch_bounds__(kStepThreads) cache_step_kernel(ll_cache c, StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c, StepArgs a) {
+  extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ __align__(16) float vs[128];
+  __shared__ float4 red[kConsumers];
   __shared__ float qs[128], ks[128], lam[kMaxLevels + kLogW + 1], tok[kW], p[kW];
-  __shared__ float4 red[kStepThreads];
   __shared__ float page_e[kMaxLevels], since_s, self_s;
-  __shared__ int page_at[kMaxLevels], page_lv[kMaxLevels], dest_s, bad_s;
+  __shared__ int page_at[kMaxLevels], page_lv[kMaxLevels], dest_s;
+  __shared__ uint64_t full[8], empty[8], window;
   const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
   const int M = (int)c.levels, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int sp = blockIdx.x % a.split;
   const int64_t bh = blockIdx.x / a.split, row = bh / H;
   const int h = (int)(bh - row * H), hq = h / G;
   const int s = a.slots[row], t = a.pos[row];
+  if (s == -1) return;
   // rows with a slot that is out of range, given to an earlier row, or at a position outside the
   // cache are left as they are
-  bool twice = false;
-  for (int64_t r = tid; r < row; r += kStepThreads) twice |= a.slots[r] == s;
-  twice = __syncthreads_or(twice);
-  if (s == -1) return;
-  unsigned bad = s < 0 || s >= c.slots || twice ? LL_CACHE_ERR_SLOT : 0;
+  unsigned bad = s < 0 || s >= c.slots ? LL_CACHE_ERR_SLOT : 0;
   if (!bad && !position_ok(c, t)) bad = LL_CACHE_ERR_POSITION;
   if (bad) {
     if (tid == 0 && sp == 0 && h == 0) raise(c, bad);
@@ -381,121 +405,185 @@ __global__ void __launch_bounds__(kStepThreads) cache_step_kernel(ll_cache c, St
   const int j = t >> kLogW, r = t & (kW - 1), par = j & 1;
   const bool fold = r == kW - 1;
   const int to = fold ? __ffs(j + 1) - 1 : -1;  // the level the block is folded to
-  if (tid == 0) bad_s = 0;
+  const int live = __popc(j);
   const int cols = dv / a.split, col0 = sp * cols;
-  const T* q = static_cast<const T*>(a.q) + (row * c.Hqk + hq) * dk;
+  const int groups = cols >> 2, lanes = kConsumers / groups;  // column groups, threads down the rows
+  const int per = min(kRowsPer, (dk + lanes - 1) / lanes);    // rows of a thread in a stage
+  const int span = per * lanes, chunks = (dk + span - 1) / span;
+  float* ring = reinterpret_cast<float*>(dyn);
+  T* wks = reinterpret_cast<T*>(dyn + (size_t)a.stages * kStageFloats * 4);
+  T* wvs = wks + kW * dk;
   const T* k = static_cast<const T*>(a.k) + (row * c.Hqk + hq) * dk;
   const T* v = static_cast<const T*>(a.v) + bh * dv + col0;
-  const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + hq) * kW * dk;
-  const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv + col0;
-  const float* wa = c.win_log_a + ((int64_t)s * H + h) * kW;
-  for (int i = tid; i < dk; i += kStepThreads) {
-    qs[i] = to_f32(q[i]);
-    ks[i] = to_f32(k[i]);
-  }
-  for (int i = tid; i < cols; i += kStepThreads) vs[i] = to_f32(v[i]);
-  for (int i = tid; i < M + kLogW + 1; i += kStepThreads) lam[i] = a.lam[bh * a.L + i];
   const float la = a.log_a ? a.log_a[bh] : 0.f;
-  __syncthreads();
-  if (w == 0) {
-    block_decays(wa, r, c.page_from[s * 2 + par], tok, &since_s);
-    __syncwarp();
-    // the live pages, lowest level first
-    const bool live = lane < M && (j >> lane) & 1;
-    int e = -1;
-    if (lane < M && (live || lane == to)) {
-      e = c.page_table[(int64_t)s * M + lane];
-      if (e < 0 || e >= c.n_pages) bad_s = 1;
+  bool ok = true;
+  if (w == kStepWarps) {  // the producer
+    if (lane == 0) {
+      for (int i = 0; i < a.stages; ++i) {
+        tc::mbar_init(&full[i], 1);
+        tc::mbar_init(&empty[i], kStepWarps);
+      }
+      tc::mbar_init(&window, 1);
+      tc::fence_mbar_init();
     }
-    const float log = live ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] + since_s + la : 0.f;
-    if (live) {
+    __syncwarp();
+    // the block's tokens: keys in one piece, rounded up to 16 bytes (still inside the window)
+    const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + hq) * kW * dk;
+    const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv + col0;
+    if (r > 0) {
+      const uint32_t nk = (r * dk * sizeof(T) + 15) & ~15u;
+      const uint32_t nv = a.split == 1 ? (r * dv * sizeof(T) + 15) & ~15u : r * cols * sizeof(T);
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&window, nk + nv);
+        bulk_load(wks, wk, nk, &window);
+        if (a.split == 1) bulk_load(wvs, wv, nv, &window);
+      }
+      __syncwarp();
+      if (a.split > 1)
+        for (int i = lane; i < r; i += 32)
+          bulk_load(wvs + i * cols, wv + (int64_t)i * dv, cols * sizeof(T), &window);
+    }
+    // the live pages, lowest level first
+    const bool here = lane < M && (j >> lane) & 1;
+    int e = 0;
+    if (here || lane == to) {
+      e = c.page_table[(int64_t)s * M + lane];
+      if (e < 0 || e >= c.n_pages) ok = false;
+    }
+    if (here) {
       const int at = __popc(j & ((1 << lane) - 1));
       page_at[at] = e;
       page_lv[at] = lane;
-      page_e[at] = expf(log);
-      if (fold && sp == 0 && lane > to)
-        c.page_log[(((int64_t)s * 2 + (par ^ 1)) * M + lane) * H + h] = log;
     }
-    if (fold && lane == to) dest_s = e;
+    if (lane == to) dest_s = e;
+  } else {
+    if (w == 0) {
+      block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], tok, &since_s);
+      const bool here = lane < M && (j >> lane) & 1;
+      const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
+      __syncwarp();
+      if (here) page_e[__popc(j & ((1 << lane) - 1))] = log + since_s + la;
+      for (int i = lane; i < kW; i += 32) tok[i] = expf(tok[i] + la);
+    }
+    const T* q = static_cast<const T*>(a.q) + (row * c.Hqk + hq) * dk;
+    for (int i = tid; i < dk; i += kConsumers) {
+      qs[i] = to_f32(q[i]);
+      ks[i] = to_f32(k[i]);
+    }
+    for (int i = tid; i < cols; i += kConsumers) vs[i] = to_f32(v[i]);
+    for (int i = tid; i < M + kLogW + 1; i += kConsumers) lam[i] = a.lam[bh * a.L + i];
+    for (int64_t i = tid; i < row; i += kConsumers)
+      if (a.slots[i] == s) bad = LL_CACHE_ERR_SLOT;
   }
-  __syncthreads();
-  if (bad_s) {  // a page the position needs is not there
-    if (tid == 0 && sp == 0 && h == 0) raise(c, LL_CACHE_ERR_MISSING);
+  const bool twice = __syncthreads_or(bad != 0);
+  const bool missing = !__syncthreads_and(ok);
+  if (twice || missing) {
+    if (tid == 0 && sp == 0 && h == 0) raise(c, twice ? LL_CACHE_ERR_SLOT : LL_CACHE_ERR_MISSING);
+    if (w == kStepWarps && r > 0) tc::mbar_wait(&window, 0);  // its copies end before the CTA does
+    return;
+  }
+  if (w == kStepWarps) {
+    int st = 0, phase = 0;
+    for (int ck = 0; ck < chunks; ++ck) {
+      const int d0 = ck * span, n = min(span, dk - d0);
+      for (int m = 0; m < live; ++m) {
+        ok = tc::mbar_wait(&empty[st], phase ^ 1) && ok;
+        const float* P = c.pages + (((int64_t)page_at[m] * H + h) * dk + d0) * dv + col0;
+        float* dst = ring + st * kStageFloats;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], n * cols * 4);
+        __syncwarp();
+        if (a.split == 1) {
+          if (lane == 0) bulk_load(dst, P, n * dv * 4, &full[st]);
+        } else {
+          for (int d = lane; d < n; d += 32)
+            bulk_load(dst + d * cols, P + (int64_t)d * dv, cols * 4, &full[st]);
+        }
+        if (++st == a.stages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+    }
     return;
   }
   // scores of the block's tokens: a warp takes every eighth
+  if (r > 0) ok = tc::mbar_wait(&window, 0);
   for (int i = w; i <= r; i += kStepWarps) {
-    const T* kr = i < r ? wk + i * dk : k;
     float x = 0.f;
-    for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], to_f32(kr[d]), x);
+    if (i < r) {
+      for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], to_f32(wks[i * dk + d]), x);
+    } else {
+      for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], ks[d], x);
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     if (lane == 0) {
       if (i == r) self_s = lam[0] * x;
-      else p[i] = lam[fenwick_level(r, i)] * expf(tok[i] + la) * x;
+      else p[i] = lam[fenwick_level(r, i)] * tok[i] * x;
     }
   }
-  __syncthreads();
-  const int groups = cols >> 2, rows = kStepThreads / groups;
   const int cg = tid % groups, row0 = tid / groups;
-  const bool on = row0 < rows;
+  const bool on = row0 < lanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+  const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * cg);
   if (on) {
-    if (row0 == 0) acc = fma4(self_s, *reinterpret_cast<const float4*>(vs + 4 * cg), acc);
-    for (int i = row0; i < r; i += rows) acc = fma4(p[i], load4(wv + i * dv + 4 * cg), acc);
-    const int live = __popc(j);
-    const int64_t size = (int64_t)dk * dv;
-    if (!fold) {
-      for (int m = 0; m < live; ++m) {
-        const float* P = c.pages + ((int64_t)page_at[m] * H + h) * size + col0 + 4 * cg;
-        const float wt = page_e[m] * lam[kLogW + 1 + page_lv[m]];
-#pragma unroll 8
-        for (int d = row0; d < dk; d += rows)
-          acc = fma4(wt * qs[d], __ldcs(reinterpret_cast<const float4*>(P + d * dv)), acc);
+    if (row0 == 0) acc = fma4(self_s, v4, acc);
+    for (int i = row0; i < r; i += lanes) acc = fma4(p[i], load4(wvs + i * cols + 4 * cg), acc);
+  }
+  int st = 0, phase = 0;
+  for (int ck = 0; ck < chunks; ++ck) {
+    const int d0 = ck * span + per * row0;
+    const int n = on ? min(per, dk - d0) : 0;  // this thread's rows (below 1: none)
+    float qr[kRowsPer];
+    float4 sum[kRowsPer];
+#pragma unroll
+    for (int x = 0; x < kRowsPer; ++x) {
+      qr[x] = x < n ? qs[d0 + x] : 0.f;
+      sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int m = 0; m < live; ++m) {
+      ok = tc::mbar_wait(&full[st], phase) && ok;
+      const float* P = ring + st * kStageFloats + per * row0 * cols + 4 * cg;
+      const float e = expf(page_e[m]);
+      float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kRowsPer; ++x)
+        if (x < n) {
+          const float4 y = *reinterpret_cast<const float4*>(P + x * cols);
+          part = fma4(qr[x], y, part);
+          if (page_lv[m] < to) sum[x] = fma4(e, y, sum[x]);
+        }
+      acc = fma4(e * lam[kLogW + 1 + page_lv[m]], part, acc);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[st]);
+      if (++st == a.stages) {
+        st = 0;
+        phase ^= 1;
       }
-    } else {
-      for (int d0 = row0; d0 < dk; d0 += 4 * rows) {
-        float4 sum[4];
+    }
+    if (fold && n > 0) {
+      for (int i = 0; i < r; ++i) {
+        const float4 y = load4(wvs + i * cols + 4 * cg);
+        const float e = tok[i];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int m = 0; m < live; ++m) {
-          const float* P = c.pages + ((int64_t)page_at[m] * H + h) * size + col0 + 4 * cg;
-          const float wt = page_e[m] * lam[kLogW + 1 + page_lv[m]];
-          const float e = page_lv[m] < to ? page_e[m] : 0.f;
+        for (int x = 0; x < kRowsPer; ++x)
+          if (x < n) sum[x] = fma4(e * to_f32(wks[i * dk + d0 + x]), y, sum[x]);
+      }
+      if (ok) {
+        float* D = c.pages + (((int64_t)dest_s * H + h) * dk + d0) * dv + col0 + 4 * cg;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int d = d0 + x * rows;
-            if (d >= dk) continue;
-            const float4 y = __ldcs(reinterpret_cast<const float4*>(P + d * dv));
-            acc = fma4(wt * qs[d], y, acc);
-            if (page_lv[m] < to) sum[x] = fma4(e, y, sum[x]);
-          }
-        }
-        for (int i = 0; i < r; ++i) {
-          const float4 y = load4(wv + i * dv + 4 * cg);
-          const float e = expf(tok[i] + la);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int d = d0 + x * rows;
-            if (d < dk) sum[x] = fma4(e * to_f32(wk[i * dk + d]), y, sum[x]);
-          }
-        }
-        float* D = c.pages + ((int64_t)dest_s * H + h) * size + col0 + 4 * cg;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int d = d0 + x * rows;
-          if (d < dk)
-            *reinterpret_cast<float4*>(D + d * dv) =
-                fma4(ks[d], *reinterpret_cast<const float4*>(vs + 4 * cg), sum[x]);
-        }
+        for (int x = 0; x < kRowsPer; ++x)
+          if (x < n) *reinterpret_cast<float4*>(D + (int64_t)x * dv) = fma4(ks[d0 + x], v4, sum[x]);
       }
     }
   }
   red[tid] = acc;
-  __syncthreads();
+  if (!ok) raise(c, LL_CACHE_ERR_WAIT);
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
   if (tid < groups) {
     float4 x = red[tid];
-    for (int i = 1; i < rows; ++i) {
+    for (int i = 1; i < lanes; ++i) {
       const float4 y = red[tid + i * groups];
       x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
     }
@@ -506,15 +594,17 @@ __global__ void __launch_bounds__(kStepThreads) cache_step_kernel(ll_cache c, St
     o[3] = from_f32<OutT>(x.w);
   }
   // this token joins the block
-  for (int i = tid; i < cols; i += kStepThreads)
+  for (int i = tid; i < cols; i += kConsumers)
     static_cast<T*>(c.win_v)[(((int64_t)s * H + h) * kW + r) * dv + col0 + i] = v[i];
   if (sp == 0) {
     if (h % G == 0)
-      for (int i = tid; i < dk; i += kStepThreads)
+      for (int i = tid; i < dk; i += kConsumers)
         static_cast<T*>(c.win_k)[(((int64_t)s * c.Hqk + hq) * kW + r) * dk + i] = k[i];
-    if (tid == 0) {
-      c.win_log_a[((int64_t)s * H + h) * kW + r] = la;
-      if (fold) {
+    if (tid == 0) c.win_log_a[((int64_t)s * H + h) * kW + r] = la;
+    if (fold) {  // what the next block's steps read
+      if (tid < live && page_lv[tid] > to)
+        c.page_log[(((int64_t)s * 2 + (par ^ 1)) * M + page_lv[tid]) * H + h] = page_e[tid];
+      if (tid == 0) {
         c.page_log[(((int64_t)s * 2 + (par ^ 1)) * M + to) * H + h] = 0.f;
         if (h == 0) c.page_from[s * 2 + (par ^ 1)] = 0;
       }
@@ -734,11 +824,11 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
   }
 }
 
-// CTAs per (row, head): as many column splits (of 16 columns or more) as it takes for two CTAs
-// per SM.
+// CTAs per (row, head): as many column splits (of 16 columns or more, in whole 16-byte pieces of
+// a bf16 row) as it takes for two CTAs per SM.
 int step_split(int64_t rows_heads, int dv) {
   int split = 1;
-  while (rows_heads * split < 2 * 152 && dv % (8 * split) == 0 && dv / (2 * split) >= 16) split *= 2;
+  while (rows_heads * split < 2 * 152 && dv % (16 * split) == 0 && dv / (2 * split) >= 16) split *= 2;
   return split;
 }
 
@@ -754,23 +844,36 @@ cudaError_t launch_cache_reserve(const ll_cache& c, const int* slots, const int*
   return cudaGetLastError();
 }
 
+namespace {
+
+template <typename T, typename OutT>
+cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
+  const size_t window = window_bytes<T>((int)c.dk, (int)c.dv / a.split);
+  // as many stages as leave room for two CTAs per SM (and at least two)
+  a.stages = (int)std::max<size_t>(2, std::min<size_t>(8, (108 * 1024 - window) / (kStageFloats * 4)));
+  const size_t smem = window + (size_t)a.stages * kStageFloats * 4;
+  const cudaError_t e = cudaFuncSetAttribute(cache_step_kernel<T, OutT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)((int64_t)a.n * c.H * a.split);
+  cache_step_kernel<T, OutT><<<grid, kStepThreads, smem, s>>>(c, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_cache_step(const ll_cache& c, const int* slots, const int* pos, const void* q,
                               const void* k, const void* v, const float* log_a, const float* lam,
                               void* out, int n, int L, int out_dtype, cudaStream_t s) {
   StepArgs a;
   a.slots = slots; a.pos = pos; a.q = q; a.k = k; a.v = v; a.log_a = log_a; a.lam = lam;
-  a.out = out; a.n = n; a.L = L;
+  a.out = out; a.n = n; a.L = L; a.stages = 0;
   a.split = step_split((int64_t)n * c.H, (int)c.dv);
-  const unsigned grid = (unsigned)((int64_t)n * c.H * a.split);
   const bool o32 = out_dtype == LL_F32;
-  if (c.dtype == LL_F32) {
-    if (o32) cache_step_kernel<float, float><<<grid, kStepThreads, 0, s>>>(c, a);
-    else cache_step_kernel<float, __nv_bfloat16><<<grid, kStepThreads, 0, s>>>(c, a);
-  } else {
-    if (o32) cache_step_kernel<__nv_bfloat16, float><<<grid, kStepThreads, 0, s>>>(c, a);
-    else cache_step_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kStepThreads, 0, s>>>(c, a);
-  }
-  return cudaGetLastError();
+  if (c.dtype == LL_F32)
+    return o32 ? launch_step<float, float>(c, a, s) : launch_step<float, __nv_bfloat16>(c, a, s);
+  return o32 ? launch_step<__nv_bfloat16, float>(c, a, s)
+             : launch_step<__nv_bfloat16, __nv_bfloat16>(c, a, s);
 }
 
 cudaError_t launch_cache_load(const ll_cache& c, const int* slots, int64_t n, int T,
