@@ -321,19 +321,22 @@ __device__ __forceinline__ void block_decays(const float* la, int r, int from, f
 
 // ---------------------------------------------------------------- step
 
-// One CTA per (row, head, dv / split columns); the columns of a state do not mix, so CTAs that
-// share a head share nothing but the scores, which each computes.  A producer warp brings the
-// block's tokens and then the pages, in stages of up to 16 KB, to shared memory by bulk
-// copies; eight warps consume them.  Bound by HBM: a page of 128 x 128 is 64 KB for 32 KFLOP, and
-// what counts is that copies are always in flight (two CTAs of four stages per SM).  A stage is
-// kRowsPer rows per thread of one page; the pages of a row chunk come one after the other, so
-// that a fold can sum them and the tokens' products for its rows in registers.
+// A cluster of `split` CTAs per (row, head): each takes a share of the states' rows and of the block's
+// tokens, and the first adds up their parts of the output (distributed shared memory).  Shares
+// of rows are contiguous in a page; shares of columns were measured at twice the time for a
+// single sequence, since each of their rows is a copy of its own.  A producer warp brings the
+// tokens and then the pages, in stages of up to 16 KB, to shared memory by bulk copies; eight
+// warps consume them.  Bound by HBM: a page of 128 x 128 is 64 KB for 32 KFLOP, and what counts
+// is that copies are always in flight (two CTAs of four stages per SM).  A stage is kRowsPer
+// rows per thread of one page; the pages of a row chunk come one after the other, so that a fold
+// can sum them and the tokens' products for its rows in registers.
 constexpr int kConsumers = 256;
 constexpr int kStepThreads = kConsumers + 32;
 constexpr int kStepWarps = kConsumers / 32;
 constexpr int kRowsPer = 4;
 constexpr int kStageFloats = kConsumers * 4 * kRowsPer;
 constexpr int kMaxLevels = 24;
+constexpr int kMaxSplit = 8;  // CTAs of a cluster
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
@@ -360,6 +363,25 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+__device__ __forceinline__ float4 add4(float4 x, float4 y) {
+  return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Writes v to p in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote4(float* p, uint32_t rank, float4 v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
 struct StepArgs {
   const int* slots;
   const int* pos;
@@ -372,16 +394,10 @@ struct StepArgs {
   int n, L, split, stages;
 };
 
-// Shared memory behind the stages: the block's keys and values.
-template <typename T>
-__host__ __device__ constexpr size_t window_bytes(int dk, int cols) {
-  return sizeof(T) * kW * (size_t)(dk + cols);
-}
-
 template <typename T, typename OutT>
 __global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c, StepArgs a) {
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ __align__(16) float vs[128];
+  __shared__ __align__(16) float vs[128], parts[kMaxSplit][128];
   __shared__ float4 red[kConsumers];
   __shared__ float qs[128], ks[128], lam[kMaxLevels + kLogW + 1], tok[kW], p[kW];
   __shared__ float page_e[kMaxLevels], since_s, self_s;
@@ -389,8 +405,8 @@ __global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c,
   __shared__ uint64_t full[8], empty[8], window;
   const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
   const int M = (int)c.levels, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int sp = blockIdx.x % a.split;
-  const int64_t bh = blockIdx.x / a.split, row = bh / H;
+  const int Z = a.split, sp = blockIdx.x % Z;  // the CTA's rank in its cluster
+  const int64_t bh = blockIdx.x / Z, row = bh / H;
   const int h = (int)(bh - row * H), hq = h / G;
   const int s = a.slots[row], t = a.pos[row];
   if (s == -1) return;
@@ -406,15 +422,19 @@ __global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c,
   const bool fold = r == kW - 1;
   const int to = fold ? __ffs(j + 1) - 1 : -1;  // the level the block is folded to
   const int live = __popc(j);
-  const int cols = dv / a.split, col0 = sp * cols;
-  const int groups = cols >> 2, lanes = kConsumers / groups;  // column groups, threads down the rows
-  const int per = min(kRowsPer, (dk + lanes - 1) / lanes);    // rows of a thread in a stage
-  const int span = per * lanes, chunks = (dk + span - 1) / span;
+  // this CTA's state rows [k0, k1) and tokens [t0, t1); a fold needs all tokens' products, so it
+  // brings them all
+  const int share = (dk + Z - 1) / Z, k0 = min(dk, sp * share), k1 = min(dk, k0 + share);
+  const int tokens = ((r + Z - 1) / Z + 7) & ~7, t0 = min(r, sp * tokens), t1 = min(r, t0 + tokens);
+  const int b0 = fold ? 0 : t0, b1 = fold ? r : t1;  // tokens to bring
+  const int groups = dv >> 2, lanes = kConsumers / groups;       // column groups, threads down the rows
+  const int per = min(kRowsPer, (share + lanes - 1) / lanes);    // rows of a thread in a stage
+  const int span = per * lanes, chunks = (k1 - k0 + span - 1) / span;
   float* ring = reinterpret_cast<float*>(dyn);
   T* wks = reinterpret_cast<T*>(dyn + (size_t)a.stages * kStageFloats * 4);
   T* wvs = wks + kW * dk;
   const T* k = static_cast<const T*>(a.k) + (row * c.Hqk + hq) * dk;
-  const T* v = static_cast<const T*>(a.v) + bh * dv + col0;
+  const T* v = static_cast<const T*>(a.v) + bh * dv;
   const float la = a.log_a ? a.log_a[bh] : 0.f;
   bool ok = true;
   if (w == kStepWarps) {  // the producer
@@ -425,24 +445,19 @@ __global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c,
       }
       tc::mbar_init(&window, 1);
       tc::fence_mbar_init();
+      if (b1 > b0) {
+        // whole rows from a multiple of 8 rows on: 16-byte aligned; the length is rounded up to
+        // 16 bytes, still inside the window
+        const int64_t ok0 = (((int64_t)s * c.Hqk + hq) * kW + b0) * dk;
+        const int64_t ov0 = (((int64_t)s * H + h) * kW + b0) * dv;
+        const uint32_t nk = ((b1 - b0) * dk * sizeof(T) + 15) & ~15u;
+        const uint32_t nv = ((b1 - b0) * dv * sizeof(T) + 15) & ~15u;
+        tc::mbar_arrive_expect_tx(&window, nk + nv);
+        bulk_load(wks + b0 * dk, static_cast<const T*>(c.win_k) + ok0, nk, &window);
+        bulk_load(wvs + b0 * dv, static_cast<const T*>(c.win_v) + ov0, nv, &window);
+      }
     }
     __syncwarp();
-    // the block's tokens: keys in one piece, rounded up to 16 bytes (still inside the window)
-    const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + hq) * kW * dk;
-    const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv + col0;
-    if (r > 0) {
-      const uint32_t nk = (r * dk * sizeof(T) + 15) & ~15u;
-      const uint32_t nv = a.split == 1 ? (r * dv * sizeof(T) + 15) & ~15u : r * cols * sizeof(T);
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&window, nk + nv);
-        bulk_load(wks, wk, nk, &window);
-        if (a.split == 1) bulk_load(wvs, wv, nv, &window);
-      }
-      __syncwarp();
-      if (a.split > 1)
-        for (int i = lane; i < r; i += 32)
-          bulk_load(wvs + i * cols, wv + (int64_t)i * dv, cols * sizeof(T), &window);
-    }
     // the live pages, lowest level first
     const bool here = lane < M && (j >> lane) & 1;
     int e = 0;
@@ -470,135 +485,140 @@ __global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c,
       qs[i] = to_f32(q[i]);
       ks[i] = to_f32(k[i]);
     }
-    for (int i = tid; i < cols; i += kConsumers) vs[i] = to_f32(v[i]);
+    for (int i = tid; i < dv; i += kConsumers) vs[i] = to_f32(v[i]);
     for (int i = tid; i < M + kLogW + 1; i += kConsumers) lam[i] = a.lam[bh * a.L + i];
     for (int64_t i = tid; i < row; i += kConsumers)
       if (a.slots[i] == s) bad = LL_CACHE_ERR_SLOT;
   }
   const bool twice = __syncthreads_or(bad != 0);
   const bool missing = !__syncthreads_and(ok);
-  if (twice || missing) {
+  if (twice || missing) {  // the same for the whole cluster
     if (tid == 0 && sp == 0 && h == 0) raise(c, twice ? LL_CACHE_ERR_SLOT : LL_CACHE_ERR_MISSING);
-    if (w == kStepWarps && r > 0) tc::mbar_wait(&window, 0);  // its copies end before the CTA does
+    if (w == kStepWarps && b1 > b0) tc::mbar_wait(&window, 0);  // its copies end before the CTA does
     return;
   }
+  if (Z > 1) cluster_arrive();  // this CTA is there
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (w == kStepWarps) {
     int st = 0, phase = 0;
-    for (int ck = 0; ck < chunks; ++ck) {
-      const int d0 = ck * span, n = min(span, dk - d0);
+    for (int ck = 0; ck < chunks && lane == 0; ++ck) {
+      const int d0 = k0 + ck * span, bytes = min(span, k1 - d0) * dv * 4;
       for (int m = 0; m < live; ++m) {
         ok = tc::mbar_wait(&empty[st], phase ^ 1) && ok;
-        const float* P = c.pages + (((int64_t)page_at[m] * H + h) * dk + d0) * dv + col0;
-        float* dst = ring + st * kStageFloats;
-        if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], n * cols * 4);
-        __syncwarp();
-        if (a.split == 1) {
-          if (lane == 0) bulk_load(dst, P, n * dv * 4, &full[st]);
-        } else {
-          for (int d = lane; d < n; d += 32)
-            bulk_load(dst + d * cols, P + (int64_t)d * dv, cols * 4, &full[st]);
-        }
+        tc::mbar_arrive_expect_tx(&full[st], bytes);
+        bulk_load(ring + st * kStageFloats, c.pages + (((int64_t)page_at[m] * H + h) * dk + d0) * dv,
+                  bytes, &full[st]);
         if (++st == a.stages) {
           st = 0;
           phase ^= 1;
         }
       }
     }
-    return;
-  }
-  // scores of the block's tokens: a warp takes every eighth
-  if (r > 0) ok = tc::mbar_wait(&window, 0);
-  for (int i = w; i <= r; i += kStepWarps) {
-    float x = 0.f;
-    if (i < r) {
+  } else {
+    // scores of the CTA's tokens: a warp takes every eighth; the first CTA has the new one too
+    if (b1 > b0) ok = tc::mbar_wait(&window, 0);
+    for (int i = t0 + w; i < t1; i += kStepWarps) {
+      float x = 0.f;
       for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], to_f32(wks[i * dk + d]), x);
-    } else {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      if (lane == 0) p[i] = lam[fenwick_level(r, i)] * tok[i] * x;
+    }
+    if (sp == 0 && w == 0) {
+      float x = 0.f;
       for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], ks[d], x);
-    }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    if (lane == 0) {
-      if (i == r) self_s = lam[0] * x;
-      else p[i] = lam[fenwick_level(r, i)] * tok[i] * x;
+      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      if (lane == 0) self_s = lam[0] * x;
     }
-  }
-  const int cg = tid % groups, row0 = tid / groups;
-  const bool on = row0 < lanes;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-  const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * cg);
-  if (on) {
-    if (row0 == 0) acc = fma4(self_s, v4, acc);
-    for (int i = row0; i < r; i += lanes) acc = fma4(p[i], load4(wvs + i * cols + 4 * cg), acc);
-  }
-  int st = 0, phase = 0;
-  for (int ck = 0; ck < chunks; ++ck) {
-    const int d0 = ck * span + per * row0;
-    const int n = on ? min(per, dk - d0) : 0;  // this thread's rows (below 1: none)
-    float qr[kRowsPer];
-    float4 sum[kRowsPer];
-#pragma unroll
-    for (int x = 0; x < kRowsPer; ++x) {
-      qr[x] = x < n ? qs[d0 + x] : 0.f;
-      sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int cg = tid % groups, row0 = tid / groups;
+    const bool on = row0 < lanes;
+    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+    const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * cg);
+    if (on) {
+      if (row0 == 0 && sp == 0) acc = fma4(self_s, v4, acc);
+      for (int i = t0 + row0; i < t1; i += lanes) acc = fma4(p[i], load4(wvs + i * dv + 4 * cg), acc);
     }
-    for (int m = 0; m < live; ++m) {
-      ok = tc::mbar_wait(&full[st], phase) && ok;
-      const float* P = ring + st * kStageFloats + per * row0 * cols + 4 * cg;
-      const float e = expf(page_e[m]);
-      float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
+    int st = 0, phase = 0;
+    for (int ck = 0; ck < chunks; ++ck) {
+      const int d0 = k0 + ck * span + per * row0;
+      const int n = on ? min(per, k1 - d0) : 0;  // this thread's rows (below 1: none)
+      float qr[kRowsPer];
+      float4 sum[kRowsPer];
 #pragma unroll
-      for (int x = 0; x < kRowsPer; ++x)
-        if (x < n) {
-          const float4 y = *reinterpret_cast<const float4*>(P + x * cols);
-          part = fma4(qr[x], y, part);
-          if (page_lv[m] < to) sum[x] = fma4(e, y, sum[x]);
+      for (int x = 0; x < kRowsPer; ++x) {
+        qr[x] = x < n ? qs[d0 + x] : 0.f;
+        sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      for (int m = 0; m < live; ++m) {
+        ok = tc::mbar_wait(&full[st], phase) && ok;
+        const float* P = ring + st * kStageFloats + per * row0 * dv + 4 * cg;
+        const float e = expf(page_e[m]);
+        float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kRowsPer; ++x)
+          if (x < n) {
+            const float4 y = *reinterpret_cast<const float4*>(P + x * dv);
+            part = fma4(qr[x], y, part);
+            if (page_lv[m] < to) sum[x] = fma4(e, y, sum[x]);
+          }
+        acc = fma4(e * lam[kLogW + 1 + page_lv[m]], part, acc);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&empty[st]);
+        if (++st == a.stages) {
+          st = 0;
+          phase ^= 1;
         }
-      acc = fma4(e * lam[kLogW + 1 + page_lv[m]], part, acc);
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty[st]);
-      if (++st == a.stages) {
-        st = 0;
-        phase ^= 1;
+      }
+      if (fold && n > 0) {
+        for (int i = 0; i < r; ++i) {
+          const float4 y = load4(wvs + i * dv + 4 * cg);
+          const float e = tok[i];
+#pragma unroll
+          for (int x = 0; x < kRowsPer; ++x)
+            if (x < n) sum[x] = fma4(e * to_f32(wks[i * dk + d0 + x]), y, sum[x]);
+        }
+        if (ok) {
+          float* D = c.pages + (((int64_t)dest_s * H + h) * dk + d0) * dv + 4 * cg;
+#pragma unroll
+          for (int x = 0; x < kRowsPer; ++x)
+            if (x < n) *reinterpret_cast<float4*>(D + x * dv) = fma4(ks[d0 + x], v4, sum[x]);
+        }
       }
     }
-    if (fold && n > 0) {
-      for (int i = 0; i < r; ++i) {
-        const float4 y = load4(wvs + i * cols + 4 * cg);
-        const float e = tok[i];
-#pragma unroll
-        for (int x = 0; x < kRowsPer; ++x)
-          if (x < n) sum[x] = fma4(e * to_f32(wks[i * dk + d0 + x]), y, sum[x]);
-      }
-      if (ok) {
-        float* D = c.pages + (((int64_t)dest_s * H + h) * dk + d0) * dv + col0 + 4 * cg;
-#pragma unroll
-        for (int x = 0; x < kRowsPer; ++x)
-          if (x < n) *reinterpret_cast<float4*>(D + (int64_t)x * dv) = fma4(ks[d0 + x], v4, sum[x]);
-      }
+    red[tid] = acc;
+    if (!ok) raise(c, LL_CACHE_ERR_WAIT);
+    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+    if (tid < groups) {
+      acc = red[tid];
+      for (int i = 1; i < lanes; ++i) acc = add4(acc, red[tid + i * groups]);
     }
   }
-  red[tid] = acc;
-  if (!ok) raise(c, LL_CACHE_ERR_WAIT);
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-  if (tid < groups) {
-    float4 x = red[tid];
-    for (int i = 1; i < lanes; ++i) {
-      const float4 y = red[tid + i * groups];
-      x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  if (Z > 1) {
+    __syncwarp();
+    cluster_wait();  // all CTAs are there
+    if (tid < groups) store_remote4(&parts[sp][4 * tid], 0, acc);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (sp == 0 && tid < groups) {
+      acc = *reinterpret_cast<const float4*>(&parts[0][4 * tid]);
+      for (int z = 1; z < Z; ++z) acc = add4(acc, *reinterpret_cast<const float4*>(&parts[z][4 * tid]));
     }
-    OutT* o = static_cast<OutT*>(a.out) + bh * dv + col0 + 4 * tid;
-    o[0] = from_f32<OutT>(x.x);
-    o[1] = from_f32<OutT>(x.y);
-    o[2] = from_f32<OutT>(x.z);
-    o[3] = from_f32<OutT>(x.w);
+  }
+  if (sp == 0 && tid < groups) {
+    OutT* o = static_cast<OutT*>(a.out) + bh * dv + 4 * tid;
+    o[0] = from_f32<OutT>(acc.x);
+    o[1] = from_f32<OutT>(acc.y);
+    o[2] = from_f32<OutT>(acc.z);
+    o[3] = from_f32<OutT>(acc.w);
   }
   // this token joins the block
-  for (int i = tid; i < cols; i += kConsumers)
-    static_cast<T*>(c.win_v)[(((int64_t)s * H + h) * kW + r) * dv + col0 + i] = v[i];
-  if (sp == 0) {
+  if (sp == Z - 1) {
+    for (int i = tid; i < dv; i += kStepThreads)
+      static_cast<T*>(c.win_v)[(((int64_t)s * H + h) * kW + r) * dv + i] = v[i];
     if (h % G == 0)
-      for (int i = tid; i < dk; i += kConsumers)
+      for (int i = tid; i < dk; i += kStepThreads)
         static_cast<T*>(c.win_k)[(((int64_t)s * c.Hqk + hq) * kW + r) * dk + i] = k[i];
     if (tid == 0) c.win_log_a[((int64_t)s * H + h) * kW + r] = la;
     if (fold) {  // what the next block's steps read
@@ -824,11 +844,11 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
   }
 }
 
-// CTAs per (row, head): as many column splits (of 16 columns or more, in whole 16-byte pieces of
-// a bf16 row) as it takes for two CTAs per SM.
-int step_split(int64_t rows_heads, int dv) {
+// CTAs per (row, head): doubled while that leaves the launch within two CTAs per SM, and each at
+// least 16 rows of the states.
+int step_split(int64_t rows_heads, int dk) {
   int split = 1;
-  while (rows_heads * split < 2 * 152 && dv % (16 * split) == 0 && dv / (2 * split) >= 16) split *= 2;
+  while (split < kMaxSplit && rows_heads * split * 2 <= 2 * 152 && dk >= 32 * split) split *= 2;
   return split;
 }
 
@@ -848,16 +868,26 @@ namespace {
 
 template <typename T, typename OutT>
 cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
-  const size_t window = window_bytes<T>((int)c.dk, (int)c.dv / a.split);
-  // as many stages as leave room for two CTAs per SM (and at least two)
-  a.stages = (int)std::max<size_t>(2, std::min<size_t>(8, (108 * 1024 - window) / (kStageFloats * 4)));
+  const size_t window = sizeof(T) * kW * (size_t)(c.dk + c.dv);
+  // as many stages as leave room for two CTAs per SM (and at least two); 12 KB are static
+  a.stages = (int)std::max<size_t>(2, std::min<size_t>(8, (100 * 1024 - window) / (kStageFloats * 4)));
   const size_t smem = window + (size_t)a.stages * kStageFloats * 4;
   const cudaError_t e = cudaFuncSetAttribute(cache_step_kernel<T, OutT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)((int64_t)a.n * c.H * a.split);
-  cache_step_kernel<T, OutT><<<grid, kStepThreads, smem, s>>>(c, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.n * c.H * a.split));
+  cfg.blockDim = dim3(kStepThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, cache_step_kernel<T, OutT>, c, a);
 }
 
 }  // namespace
@@ -868,7 +898,7 @@ cudaError_t launch_cache_step(const ll_cache& c, const int* slots, const int* po
   StepArgs a;
   a.slots = slots; a.pos = pos; a.q = q; a.k = k; a.v = v; a.log_a = log_a; a.lam = lam;
   a.out = out; a.n = n; a.L = L; a.stages = 0;
-  a.split = step_split((int64_t)n * c.H, (int)c.dv);
+  a.split = step_split((int64_t)n * c.H, (int)c.dk);
   const bool o32 = out_dtype == LL_F32;
   if (c.dtype == LL_F32)
     return o32 ? launch_step<float, float>(c, a, s) : launch_step<float, __nv_bfloat16>(c, a, s);
