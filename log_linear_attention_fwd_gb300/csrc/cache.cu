@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_load_kernel(
 // after[i] = sum of la[u], i < u < r (0 at and past r - 1), and *since = sum of la[u], from <= u
 // < r, for r <= 64 values.  One warp; sums run from the end, in one order.
 __device__ __forceinline__ void block_decays(const float* la, int r, int from, float* after,
-                                             float* since) {
+                                             float* since) {  // *since in every lane
   const int lane = threadIdx.x & 31;
   const float x0 = lane < r ? la[lane] : 0.f, x1 = lane + 32 < r ? la[lane + 32] : 0.f;
   float y0 = x0, y1 = x1;  // inclusive sums from the end of each half
@@ -316,27 +316,39 @@ __device__ __forceinline__ void block_decays(const float* la, int r, int from, f
   after[lane] = n0;
   after[lane + 32] = n1;
   const float f0 = __shfl_sync(0xffffffffu, y0, from & 31), f1 = __shfl_sync(0xffffffffu, y1, from & 31);
-  if (lane == 0) *since = from >= r ? 0.f : from < 32 ? f0 : f1;
+  *since = from >= r ? 0.f : from < 32 ? f0 : f1;
 }
 
 // ---------------------------------------------------------------- step
 
-// A cluster of `split` CTAs per (row, head): each takes a share of the states' rows and of the block's
-// tokens, and the first adds up their parts of the output (distributed shared memory).  Shares
-// of rows are contiguous in a page; shares of columns were measured at twice the time for a
-// single sequence, since each of their rows is a copy of its own.  A producer warp brings the
-// tokens and then the pages, in stages of up to 16 KB, to shared memory by bulk copies; eight
-// warps consume them.  Bound by HBM: a page of 128 x 128 is 64 KB for 32 KFLOP, and what counts
-// is that copies are always in flight (two CTAs of four stages per SM).  A stage is kRowsPer
-// rows per thread of one page; the pages of a row chunk come one after the other, so that a fold
-// can sum them and the tokens' products for its rows in registers.
+// An item is one (row, head).  A producer warp brings its block's tokens and then its pages, in
+// stages of up to 16 KB, to shared memory by bulk copies, and eight warps consume them.  Bound by
+// HBM: a page of 128 x 128 is 64 KB for 32 KFLOP.  The two forms of the kernel:
+//
+// queue: two persistent CTAs per SM (one alone is bound by its warps' latency: 195 us where two take
+// ... at 128 rows of position 16300).  A scheduler thread takes the grid's pending items (cluster
+// launch control) and kLoaders warps bring the next items' small inputs, so that copies are in
+// flight across items, and an item's loads, scores and reduction hide behind another's pages.
+//
+// split: for batches of fewer items than SMs.  A cluster of `split` CTAs per item, each with a
+// share of the states' rows and of the block's tokens, whose first adds up their parts of the
+// output (distributed shared memory); all warps load the item's inputs.  Shares of rows are
+// contiguous in a page; shares of columns took twice the time for a single sequence, each of
+// their rows being a copy of its own.
+//
+// A stage is kRowsPer rows per thread of one page; the pages of a row chunk come one after the
+// other, so that a fold can sum them and the tokens' products for its rows in registers.
 constexpr int kConsumers = 256;
-constexpr int kStepThreads = kConsumers + 32;
 constexpr int kStepWarps = kConsumers / 32;
+constexpr int kProducer = kStepWarps, kScheduler = kStepWarps + 1, kFirstLoader = kStepWarps + 2;
+constexpr int kLoaders = 2;  // and items on their way
+constexpr int kQueueThreads = kConsumers + 64 + 32 * kLoaders;
+constexpr int kSplitThreads = kConsumers + 96;  // one loader
 constexpr int kRowsPer = 4;
 constexpr int kStageFloats = kConsumers * 4 * kRowsPer;
 constexpr int kMaxLevels = 24;
 constexpr int kMaxSplit = 8;  // CTAs of a cluster
+constexpr int kMaxStages = 8;
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
@@ -382,6 +394,15 @@ __device__ __forceinline__ void store_remote4(float* p, uint32_t rank, float4 v)
                : "memory");
 }
 
+template <typename OutT>
+__device__ __forceinline__ void store_out(void* out, int64_t at, float4 v) {
+  OutT* o = static_cast<OutT*>(out) + at;
+  o[0] = from_f32<OutT>(v.x);
+  o[1] = from_f32<OutT>(v.y);
+  o[2] = from_f32<OutT>(v.z);
+  o[3] = from_f32<OutT>(v.w);
+}
+
 struct StepArgs {
   const int* slots;
   const int* pos;
@@ -394,241 +415,534 @@ struct StepArgs {
   int n, L, split, stages;
 };
 
-template <typename T, typename OutT>
-__global__ void __launch_bounds__(kStepThreads, 2) cache_step_kernel(ll_cache c, StepArgs a) {
-  extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ __align__(16) float vs[128], parts[kMaxSplit][128];
-  __shared__ float4 red[kConsumers];
-  __shared__ float qs[128], ks[128], lam[kMaxLevels + kLogW + 1], tok[kW], p[kW];
-  __shared__ float page_e[kMaxLevels], since_s, self_s;
-  __shared__ int page_at[kMaxLevels], page_lv[kMaxLevels], dest_s;
-  __shared__ uint64_t full[8], empty[8], window;
-  const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
-  const int M = (int)c.levels, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int Z = a.split, sp = blockIdx.x % Z;  // the CTA's rank in its cluster
-  const int64_t bh = blockIdx.x / Z, row = bh / H;
-  const int h = (int)(bh - row * H), hq = h / G;
-  const int s = a.slots[row], t = a.pos[row];
-  if (s == -1) return;
-  // rows with a slot that is out of range, given to an earlier row, or at a position outside the
-  // cache are left as they are
-  unsigned bad = s < 0 || s >= c.slots ? LL_CACHE_ERR_SLOT : 0;
-  if (!bad && !position_ok(c, t)) bad = LL_CACHE_ERR_POSITION;
-  if (bad) {
-    if (tid == 0 && sp == 0 && h == 0) raise(c, bad);
-    return;
+// What the warps of a CTA hand each other.
+struct __align__(16) Item {  // its vectors are read four at a time
+  float q[128], k[128], v[128];
+  float lam[kMaxLevels + kLogW + 1];
+  float tok[kW];                // decay from each token of the block to the new one
+  // the live pages, lowest level first: log decay, decay, decay times lambda
+  float page_log[kMaxLevels], page_e[kMaxLevels], page_w[kMaxLevels];
+  int page_at[kMaxLevels], page_lv[kMaxLevels];
+  int kind, row, h, slot, pos, dest;  // kind: kRun, kSkip or kStop
+  float log_a;
+};
+enum { kRun, kSkip, kStop };
+
+struct StepSmem {
+  Item item[kLoaders];
+  __align__(16) float parts[kMaxSplit][128];
+  float4 red[kConsumers];
+  float p[kW], self;
+  int index[kLoaders];          // the items the loaders are to bring
+  __align__(16) uint4 next;     // cluster launch control's answer
+  uint64_t index_full[kLoaders], index_empty[kLoaders], item_full[kLoaders], item_empty[kLoaders];
+  uint64_t window_full, window_empty, answered;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+};
+
+// Asks for a pending CTA of the grid in this one's stead; the answer goes to *to.
+__device__ __forceinline__ void ask_next(uint4* to, uint64_t* bar) {
+  tc::mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          tc::smem_u32(to)),
+      "r"(tc::smem_u32(bar))
+      : "memory");
+}
+// The CTA's index, or -1 where none was pending.
+__device__ __forceinline__ int read_next(const uint4* from) {
+  uint32_t got, x = 0;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(tc::smem_u32(from))
+      : "memory");
+  tc::fence_proxy_async_smem();  // the next answer is written behind this read
+  return got ? (int)x : -1;
+}
+
+// The item's vectors, by thread i0 of `step`.  True where an earlier row has its slot.
+template <typename T>
+__device__ __forceinline__ bool load_vectors(const ll_cache& c, const StepArgs& a, int row, int h, int s,
+                                             int i0, int step, Item& it) {
+  const int Hqk = (int)c.Hqk, G = (int)c.H / Hqk, dk = (int)c.dk, dv = (int)c.dv, M = (int)c.levels;
+  const int64_t bh = (int64_t)row * (int)c.H + h;
+  const T* q = static_cast<const T*>(a.q) + ((int64_t)row * Hqk + h / G) * dk;
+  const T* k = static_cast<const T*>(a.k) + ((int64_t)row * Hqk + h / G) * dk;
+  const T* v = static_cast<const T*>(a.v) + bh * dv;
+#pragma unroll 4
+  for (int i = i0; i < dk; i += step) {
+    it.q[i] = to_f32(q[i]);
+    it.k[i] = to_f32(k[i]);
   }
+#pragma unroll 4
+  for (int i = i0; i < dv; i += step) it.v[i] = to_f32(v[i]);
+  for (int i = i0; i < M + kLogW + 1; i += step) it.lam[i] = a.lam[bh * a.L + i];
+  bool twice = false;
+#pragma unroll 4
+  for (int i = i0; i < row; i += step) twice |= a.slots[i] == s;
+  return twice;
+}
+
+// Why a row cannot be served, before its pages are looked at.
+__device__ __forceinline__ unsigned row_bad(const ll_cache& c, int s, int t) {
+  if (s < 0 || s >= c.slots) return LL_CACHE_ERR_SLOT;
+  return position_ok(c, t) ? 0 : LL_CACHE_ERR_POSITION;
+}
+
+// The item's decays and pages, by one warp; s and t are fine.  False where a page is missing.
+__device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a, int row, int h, int s,
+                                           int t, Item& it) {
+  const int lane = threadIdx.x & 31, H = (int)c.H, M = (int)c.levels;
+  const int64_t bh = (int64_t)row * H + h;
   const int j = t >> kLogW, r = t & (kW - 1), par = j & 1;
-  const bool fold = r == kW - 1;
-  const int to = fold ? __ffs(j + 1) - 1 : -1;  // the level the block is folded to
-  const int live = __popc(j);
-  // this CTA's state rows [k0, k1) and tokens [t0, t1); a fold needs all tokens' products, so it
-  // brings them all
-  const int share = (dk + Z - 1) / Z, k0 = min(dk, sp * share), k1 = min(dk, k0 + share);
-  const int tokens = ((r + Z - 1) / Z + 7) & ~7, t0 = min(r, sp * tokens), t1 = min(r, t0 + tokens);
-  const int b0 = fold ? 0 : t0, b1 = fold ? r : t1;  // tokens to bring
-  const int groups = dv >> 2, lanes = kConsumers / groups;       // column groups, threads down the rows
-  const int per = min(kRowsPer, (share + lanes - 1) / lanes);    // rows of a thread in a stage
-  const int span = per * lanes, chunks = (k1 - k0 + span - 1) / span;
+  const int to = r == kW - 1 ? __ffs(j + 1) - 1 : -1;
+  const bool here = lane < M && (j >> lane) & 1;
+  const int e = here || lane == to ? c.page_table[(int64_t)s * M + lane] : 0;
+  const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
+  const float la = a.log_a ? a.log_a[bh] : 0.f;
+  const float lam = here ? a.lam[bh * a.L + kLogW + 1 + lane] : 0.f;
+  float since;
+  block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], it.tok, &since);
+  it.tok[lane] = expf(it.tok[lane] + la);
+  it.tok[lane + 32] = expf(it.tok[lane + 32] + la);
+  if (here) {
+    const int at = __popc(j & ((1 << lane) - 1));
+    it.page_at[at] = e;
+    it.page_lv[at] = lane;
+    it.page_log[at] = log + since + la;
+    it.page_e[at] = expf(log + since + la);
+    it.page_w[at] = it.page_e[at] * lam;
+  }
+  if (lane == to) it.dest = e;
+  if (lane == 0) {
+    it.log_a = la;
+    it.row = row;
+    it.h = h;
+    it.slot = s;
+    it.pos = t;
+  }
+  return __all_sync(0xffffffffu, e >= 0 && e < c.n_pages);
+}
+
+// An item's geometry in a CTA: its state rows [k0, k1) and tokens [t0, t1).  A fold needs all
+// tokens' products, so it brings them all ([b0, b1)).
+struct Part {
+  int j, r, to, live;
+  bool fold;
+  int k0, k1, t0, t1, b0, b1;
+};
+__device__ __forceinline__ Part part_of(int pos, int dk, int Z, int sp) {
+  Part p;
+  p.j = pos >> kLogW;
+  p.r = pos & (kW - 1);
+  p.fold = p.r == kW - 1;
+  p.to = p.fold ? __ffs(p.j + 1) - 1 : -1;  // the level the block is folded to
+  p.live = __popc(p.j);
+  const int share = (dk + Z - 1) / Z;
+  p.k0 = min(dk, sp * share);
+  p.k1 = min(dk, p.k0 + share);
+  const int tokens = ((p.r + Z - 1) / Z + 7) & ~7;  // whole 16-byte pieces, whatever the row
+  p.t0 = min(p.r, sp * tokens);
+  p.t1 = min(p.r, p.t0 + tokens);
+  p.b0 = p.fold ? 0 : p.t0;
+  p.b1 = p.fold ? p.r : p.t1;
+  return p;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kConsumers) : "memory");
+}
+// Whether x is true in any consumer.
+__device__ __forceinline__ bool consumer_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(kConsumers)
+      : "memory");
+  return r != 0;
+}
+
+template <typename T, typename OutT, bool kQueue>
+__global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
+    cache_step_kernel(ll_cache c, StepArgs a) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ StepSmem sm;
+  const int H = (int)c.H, Hqk = (int)c.Hqk, G = H / Hqk, dk = (int)c.dk, dv = (int)c.dv, M = (int)c.levels;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int Z = kQueue ? 1 : a.split, sp = kQueue ? 0 : blockIdx.x % Z;  // the CTA's rank in its cluster
+  const int groups = dv >> 2, lanes = kConsumers / groups;  // column groups, threads down the rows
+  const int per = min(kRowsPer, ((dk + Z - 1) / Z + lanes - 1) / lanes);  // rows of a thread in a stage
+  const int span = per * lanes;
   float* ring = reinterpret_cast<float*>(dyn);
   T* wks = reinterpret_cast<T*>(dyn + (size_t)a.stages * kStageFloats * 4);
   T* wvs = wks + kW * dk;
-  const T* k = static_cast<const T*>(a.k) + (row * c.Hqk + hq) * dk;
-  const T* v = static_cast<const T*>(a.v) + bh * dv;
-  const float la = a.log_a ? a.log_a[bh] : 0.f;
-  bool ok = true;
-  if (w == kStepWarps) {  // the producer
-    if (lane == 0) {
-      for (int i = 0; i < a.stages; ++i) {
-        tc::mbar_init(&full[i], 1);
-        tc::mbar_init(&empty[i], kStepWarps);
-      }
-      tc::mbar_init(&window, 1);
-      tc::fence_mbar_init();
-      if (b1 > b0) {
-        // whole rows from a multiple of 8 rows on: 16-byte aligned; the length is rounded up to
-        // 16 bytes, still inside the window
-        const int64_t ok0 = (((int64_t)s * c.Hqk + hq) * kW + b0) * dk;
-        const int64_t ov0 = (((int64_t)s * H + h) * kW + b0) * dv;
-        const uint32_t nk = ((b1 - b0) * dk * sizeof(T) + 15) & ~15u;
-        const uint32_t nv = ((b1 - b0) * dv * sizeof(T) + 15) & ~15u;
-        tc::mbar_arrive_expect_tx(&window, nk + nv);
-        bulk_load(wks + b0 * dk, static_cast<const T*>(c.win_k) + ok0, nk, &window);
-        bulk_load(wvs + b0 * dv, static_cast<const T*>(c.win_v) + ov0, nv, &window);
-      }
+  if (tid == 0) {
+    for (int i = 0; i < kLoaders; ++i) {
+      tc::mbar_init(&sm.index_full[i], 1);
+      tc::mbar_init(&sm.index_empty[i], 1);
+      tc::mbar_init(&sm.item_full[i], 1);
+      tc::mbar_init(&sm.item_empty[i], kStepWarps + 1);  // the consumers and the producer
     }
-    __syncwarp();
-    // the live pages, lowest level first
-    const bool here = lane < M && (j >> lane) & 1;
-    int e = 0;
-    if (here || lane == to) {
-      e = c.page_table[(int64_t)s * M + lane];
-      if (e < 0 || e >= c.n_pages) ok = false;
+    tc::mbar_init(&sm.window_full, 1);
+    tc::mbar_init(&sm.window_empty, kStepWarps);
+    tc::mbar_init(&sm.answered, 1);
+    for (int i = 0; i < a.stages; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], kStepWarps);
     }
-    if (here) {
-      const int at = __popc(j & ((1 << lane) - 1));
-      page_at[at] = e;
-      page_lv[at] = lane;
+    tc::fence_mbar_init();
+  }
+  // the block's tokens [b0, b1): whole rows from a multiple of 8 rows on, so 16-byte aligned; the
+  // length is rounded up to 16 bytes, still inside the window.  Without tokens the barrier takes
+  // an empty phase.
+  auto bring_window = [&](int64_t s, int h, const Part& g) {
+    const uint32_t nk = ((g.b1 - g.b0) * dk * sizeof(T) + 15) & ~15u;
+    const uint32_t nv = ((g.b1 - g.b0) * dv * sizeof(T) + 15) & ~15u;
+    tc::mbar_arrive_expect_tx(&sm.window_full, nk + nv);
+    if (g.b1 > g.b0) {
+      bulk_load(wks + g.b0 * dk, static_cast<const T*>(c.win_k) + ((s * Hqk + h / G) * kW + g.b0) * dk, nk,
+                &sm.window_full);
+      bulk_load(wvs + g.b0 * dv, static_cast<const T*>(c.win_v) + ((s * H + h) * kW + g.b0) * dv, nv,
+                &sm.window_full);
     }
-    if (lane == to) dest_s = e;
+  };
+  bool ok = true, brought = false;
+  if (kQueue) {
+    __syncthreads();
   } else {
-    if (w == 0) {
-      block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], tok, &since_s);
-      const bool here = lane < M && (j >> lane) & 1;
-      const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
-      __syncwarp();
-      if (here) page_e[__popc(j & ((1 << lane) - 1))] = log + since_s + la;
-      for (int i = lane; i < kW; i += 32) tok[i] = expf(tok[i] + la);
+    if (Z > 1) cluster_arrive();  // this CTA is there
+    const int index = blockIdx.x / Z, row = index / H, h = index - row * H, s = a.slots[row], t = a.pos[row];
+    const unsigned bad = s == -1 ? 0 : row_bad(c, s, t);
+    const bool run = s != -1 && !bad;
+    __syncthreads();  // the barriers are there
+    bool twice = false, there = true;
+    if (run) {
+      if (w == kProducer) {
+        if (lane == 0) bring_window(s, h, part_of(t, dk, Z, sp));
+        brought = true;
+      } else if (w == kScheduler + 1) {
+        there = load_links(c, a, row, h, s, t, sm.item[0]);
+      } else if (w < kStepWarps) {
+        twice = load_vectors<T>(c, a, row, h, s, tid, kConsumers, sm.item[0]);
+      }
     }
-    const T* q = static_cast<const T*>(a.q) + (row * c.Hqk + hq) * dk;
-    for (int i = tid; i < dk; i += kConsumers) {
-      qs[i] = to_f32(q[i]);
-      ks[i] = to_f32(k[i]);
+    twice = __syncthreads_or(twice);
+    there = __syncthreads_and(there);
+    if (tid == 0) {
+      const unsigned why = bad ? bad : twice ? LL_CACHE_ERR_SLOT : there ? 0 : LL_CACHE_ERR_MISSING;
+      if (why && sp == 0 && h == 0) raise(c, why);
+      sm.item[0].kind = run && !why ? kRun : kSkip;
     }
-    for (int i = tid; i < dv; i += kConsumers) vs[i] = to_f32(v[i]);
-    for (int i = tid; i < M + kLogW + 1; i += kConsumers) lam[i] = a.lam[bh * a.L + i];
-    for (int64_t i = tid; i < row; i += kConsumers)
-      if (a.slots[i] == s) bad = LL_CACHE_ERR_SLOT;
+    __syncthreads();
   }
-  const bool twice = __syncthreads_or(bad != 0);
-  const bool missing = !__syncthreads_and(ok);
-  if (twice || missing) {  // the same for the whole cluster
-    if (tid == 0 && sp == 0 && h == 0) raise(c, twice ? LL_CACHE_ERR_SLOT : LL_CACHE_ERR_MISSING);
-    if (w == kStepWarps && b1 > b0) tc::mbar_wait(&window, 0);  // its copies end before the CTA does
-    return;
-  }
-  if (Z > 1) cluster_arrive();  // this CTA is there
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (w == kStepWarps) {
-    int st = 0, phase = 0;
-    for (int ck = 0; ck < chunks && lane == 0; ++ck) {
-      const int d0 = k0 + ck * span, bytes = min(span, k1 - d0) * dv * 4;
-      for (int m = 0; m < live; ++m) {
-        ok = tc::mbar_wait(&empty[st], phase ^ 1) && ok;
-        tc::mbar_arrive_expect_tx(&full[st], bytes);
-        bulk_load(ring + st * kStageFloats, c.pages + (((int64_t)page_at[m] * H + h) * dk + d0) * dv,
-                  bytes, &full[st]);
-        if (++st == a.stages) {
-          st = 0;
-          phase ^= 1;
+  if (kQueue && w >= kFirstLoader) {
+    const int L = w - kFirstLoader;
+    Item& it = sm.item[L];
+    for (int turn = 0;; turn ^= 1) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&sm.index_full[L], turn));
+      if (!ok) break;
+      const int index = sm.index[L];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.index_empty[L]);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&sm.item_empty[L], turn ^ 1));
+      if (!ok) break;
+      int kind = kStop;
+      if (index >= 0) {
+        const int row = index / H, h = index - row * H, s = a.slots[row], t = a.pos[row];
+        kind = kSkip;
+        if (s != -1) {
+          unsigned why = row_bad(c, s, t);
+          if (!why) {
+            const bool twice = load_vectors<T>(c, a, row, h, s, lane, 32, it);
+            if (!load_links(c, a, row, h, s, t, it)) why = LL_CACHE_ERR_MISSING;
+            if (__any_sync(0xffffffffu, twice)) why = LL_CACHE_ERR_SLOT;
+          }
+          if (!why) kind = kRun;
+          else if (lane == 0 && h == 0) raise(c, why);
         }
       }
+      if (lane == 0) it.kind = kind;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.item_full[L]);
+      if (index < 0) break;
     }
-  } else {
-    // scores of the CTA's tokens: a warp takes every eighth; the first CTA has the new one too
-    if (b1 > b0) ok = tc::mbar_wait(&window, 0);
-    for (int i = t0 + w; i < t1; i += kStepWarps) {
-      float x = 0.f;
-      for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], to_f32(wks[i * dk + d]), x);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      if (lane == 0) p[i] = lam[fenwick_level(r, i)] * tok[i] * x;
+    if (!ok && lane == 0) raise(c, LL_CACHE_ERR_WAIT);
+  } else if (kQueue && w == kScheduler) {
+    if (lane == 0) {
+      int next = blockIdx.x, after = -1;  // after: loaders that have been told to stop
+      for (int n = 0, L = 0, turn = 0; ok && after < kLoaders - 1; ++n) {
+        if (next >= 0) ask_next(&sm.next, &sm.answered);
+        ok = tc::mbar_wait_short(&sm.index_empty[L], turn ^ 1);
+        sm.index[L] = next;
+        tc::mbar_arrive(&sm.index_full[L]);
+        if (next < 0) {
+          ++after;
+        } else {
+          const bool got = tc::mbar_wait_short(&sm.answered, n & 1);
+          ok = ok && got;
+          next = got ? read_next(&sm.next) : -1;
+        }
+        if (++L == kLoaders) {
+          L = 0;
+          turn ^= 1;
+        }
+      }
+      if (!ok) raise(c, LL_CACHE_ERR_WAIT);
     }
-    if (sp == 0 && w == 0) {
-      float x = 0.f;
-      for (int d = lane; d < dk; d += 32) x = fmaf(qs[d], ks[d], x);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      if (lane == 0) self_s = lam[0] * x;
+    __syncwarp();
+  } else if (w == kProducer) {
+    int st = 0, phase = 0, ib = 0, turn = 0, used = brought ? 1 : 0;
+    while (lane == 0) {
+      if (kQueue && !(ok = tc::mbar_wait_short(&sm.item_full[ib], turn))) break;
+      const Item& it = sm.item[ib];
+      if (it.kind == kStop || (!kQueue && it.kind == kSkip)) break;
+      if (it.kind == kRun) {
+        const Part g = part_of(it.pos, dk, Z, sp);
+        const int h = it.h;
+        if (kQueue) {
+          if (!(ok = tc::mbar_wait_short(&sm.window_empty, (used & 1) ^ 1))) break;
+          bring_window(it.slot, h, g);
+          ++used;
+        }
+        for (int d0 = g.k0; d0 < g.k1 && ok; d0 += span) {
+          const int bytes = min(span, g.k1 - d0) * dv * 4;
+          for (int m = 0; m < g.live; ++m) {
+            if (!(ok = tc::mbar_wait_short(&sm.empty[st], phase ^ 1))) break;
+            tc::mbar_arrive_expect_tx(&sm.full[st], bytes);
+            bulk_load(ring + st * kStageFloats,
+                      c.pages + (((int64_t)it.page_at[m] * H + h) * dk + d0) * dv, bytes, &sm.full[st]);
+            if (++st == a.stages) {
+              st = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        if (!ok) break;
+      }
+      if (!kQueue) break;
+      tc::mbar_arrive(&sm.item_empty[ib]);
+      if (++ib == kLoaders) {
+        ib = 0;
+        turn ^= 1;
+      }
     }
+    if (lane == 0 && !ok) raise(c, LL_CACHE_ERR_WAIT);
+    if (lane == 0 && (!ok || !kQueue)) {  // the copies on their way end before the CTA does
+      for (int i = 0; i < a.stages; ++i)  // each stage's last use (none: the barrier is fresh)
+        tc::mbar_wait_short(&sm.full[i], i < st ? phase : phase ^ 1);
+      tc::mbar_wait_short(&sm.window_full, (used & 1) ^ 1);
+    }
+    __syncwarp();
+  } else if (w < kStepWarps) {
     const int cg = tid % groups, row0 = tid / groups;
     const bool on = row0 < lanes;
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-    const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * cg);
-    if (on) {
-      if (row0 == 0 && sp == 0) acc = fma4(self_s, v4, acc);
-      for (int i = t0 + row0; i < t1; i += lanes) acc = fma4(p[i], load4(wvs + i * dv + 4 * cg), acc);
-    }
     int st = 0, phase = 0;
-    for (int ck = 0; ck < chunks; ++ck) {
-      const int d0 = k0 + ck * span + per * row0;
-      const int n = on ? min(per, k1 - d0) : 0;  // this thread's rows (below 1: none)
-      float qr[kRowsPer];
-      float4 sum[kRowsPer];
-#pragma unroll
-      for (int x = 0; x < kRowsPer; ++x) {
-        qr[x] = x < n ? qs[d0 + x] : 0.f;
-        sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    int ib = 0, turn = 0, used = 0;  // item buffer, its phase; items with a window so far
+    for (;;) {
+      if (kQueue) {
+        // one wait that ran out of time ends the CTA's work, in all warps alike
+        ok = tc::mbar_wait_short(&sm.item_full[ib], turn) && ok;
+        if (consumer_any(!ok)) {
+          ok = false;
+          break;
+        }
       }
-      for (int m = 0; m < live; ++m) {
-        ok = tc::mbar_wait(&full[st], phase) && ok;
-        const float* P = ring + st * kStageFloats + per * row0 * dv + 4 * cg;
-        const float e = expf(page_e[m]);
-        float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kRowsPer; ++x)
-          if (x < n) {
-            const float4 y = *reinterpret_cast<const float4*>(P + x * dv);
-            part = fma4(qr[x], y, part);
-            if (page_lv[m] < to) sum[x] = fma4(e, y, sum[x]);
-          }
-        acc = fma4(e * lam[kLogW + 1 + page_lv[m]], part, acc);
+      const Item& it = sm.item[ib];
+      if (it.kind == kStop) break;
+      if (it.kind == kSkip) {
+        if (!kQueue) break;
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&empty[st]);
-        if (++st == a.stages) {
-          st = 0;
-          phase ^= 1;
+        if (lane == 0) tc::mbar_arrive(&sm.item_empty[ib]);
+        if (++ib == kLoaders) {
+          ib = 0;
+          turn ^= 1;
         }
+        continue;
       }
-      if (fold && n > 0) {
-        for (int i = 0; i < r; ++i) {
-          const float4 y = load4(wvs + i * dv + 4 * cg);
-          const float e = tok[i];
+      const Part g = part_of(it.pos, dk, Z, sp);
+      ok = tc::mbar_wait_short(&sm.window_full, used & 1) && ok;
+      ++used;
+      // scores of the CTA's tokens, a warp every eighth; the cluster's first has the new one too
+      float qv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) qv[u] = lane + 32 * u < dk ? it.q[lane + 32 * u] : 0.f;
+#pragma unroll 4
+      for (int i = g.t0 + w; i < g.t1; i += kStepWarps) {
+        float x = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (lane + 32 * u < dk) x = fmaf(qv[u], to_f32(wks[i * dk + lane + 32 * u]), x);
+        x = warp_sum(x);
+        if (lane == 0) sm.p[i] = it.lam[fenwick_level(g.r, i)] * it.tok[i] * x;
+      }
+      if (w == 0 && (kQueue || sp == 0)) {
+        float x = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (lane + 32 * u < dk) x = fmaf(qv[u], it.k[lane + 32 * u], x);
+        x = warp_sum(x);
+        if (lane == 0) sm.self = it.lam[0] * x;
+      }
+      consumer_sync();
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 v4 = *reinterpret_cast<const float4*>(it.v + 4 * cg);
+      if (on) {
+        if (row0 == 0 && (kQueue || sp == 0)) acc = fma4(sm.self, v4, acc);
+#pragma unroll 4
+        for (int i = g.t0 + row0; i < g.t1; i += lanes) acc = fma4(sm.p[i], load4(wvs + i * dv + 4 * cg), acc);
+      }
+      if (kQueue && !g.fold) {  // the next item's tokens may come
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.window_empty);
+      }
+      const int h = it.h;
+      const int64_t bh = (int64_t)it.row * H + h;
+      for (int c0 = g.k0; c0 < g.k1; c0 += span) {
+        const int d0 = c0 + per * row0;
+        const int rows = on ? min(per, g.k1 - d0) : 0;  // this thread's rows (below 1: none)
+        float qr[kRowsPer];
+#pragma unroll
+        for (int x = 0; x < kRowsPer; ++x) qr[x] = x < rows ? it.q[d0 + x] : 0.f;
+        const float* mine = ring + per * row0 * dv + 4 * cg;
+        if (!g.fold) {
+          for (int m = 0; m < g.live; ++m) {
+            ok = tc::mbar_wait_short(&sm.full[st], phase) && ok;
+            const float* P = mine + st * kStageFloats;
+            float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < kRowsPer; ++x)
+              if (x < rows) part = fma4(qr[x], *reinterpret_cast<const float4*>(P + x * dv), part);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
+            acc = fma4(it.page_w[m], part, acc);
+            if (++st == a.stages) {
+              st = 0;
+              phase ^= 1;
+            }
+          }
+          continue;
+        }
+        float4 sum[kRowsPer];
+#pragma unroll
+        for (int x = 0; x < kRowsPer; ++x) sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int m = 0; m < g.live; ++m) {
+          ok = tc::mbar_wait_short(&sm.full[st], phase) && ok;
+          const float* P = mine + st * kStageFloats;
+          const float e = it.page_lv[m] < g.to ? it.page_e[m] : 0.f;
+          float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int x = 0; x < kRowsPer; ++x)
-            if (x < n) sum[x] = fma4(e * to_f32(wks[i * dk + d0 + x]), y, sum[x]);
+            if (x < rows) {
+              const float4 y = *reinterpret_cast<const float4*>(P + x * dv);
+              part = fma4(qr[x], y, part);
+              if (it.page_lv[m] < g.to) sum[x] = fma4(e, y, sum[x]);
+            }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
+          acc = fma4(it.page_w[m], part, acc);
+          if (++st == a.stages) {
+            st = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) {
-          float* D = c.pages + (((int64_t)dest_s * H + h) * dk + d0) * dv + 4 * cg;
+        if (rows > 0) {
+          const bool quads = rows == 4 && dk % 4 == 0 && d0 % 4 == 0;  // four keys in one load
+#pragma unroll 2
+          for (int i = 0; i < g.r; ++i) {
+            const float4 y = load4(wvs + i * dv + 4 * cg);
+            const float e = it.tok[i];
+            const T* kr = wks + i * dk + d0;
+            float4 k4;
+            if (quads) {
+              k4 = load4(kr);
+            } else {
+              k4.x = to_f32(kr[0]);
+              k4.y = rows > 1 ? to_f32(kr[1]) : 0.f;
+              k4.z = rows > 2 ? to_f32(kr[2]) : 0.f;
+              k4.w = rows > 3 ? to_f32(kr[3]) : 0.f;
+            }
+            sum[0] = fma4(e * k4.x, y, sum[0]);
+            sum[1] = fma4(e * k4.y, y, sum[1]);
+            sum[2] = fma4(e * k4.z, y, sum[2]);
+            sum[3] = fma4(e * k4.w, y, sum[3]);
+          }
+          if (ok) {
+            float* D = c.pages + (((int64_t)it.dest * H + h) * dk + d0) * dv + 4 * cg;
 #pragma unroll
-          for (int x = 0; x < kRowsPer; ++x)
-            if (x < n) *reinterpret_cast<float4*>(D + x * dv) = fma4(ks[d0 + x], v4, sum[x]);
+            for (int x = 0; x < kRowsPer; ++x)
+              if (x < rows) *reinterpret_cast<float4*>(D + x * dv) = fma4(it.k[d0 + x], v4, sum[x]);
+          }
         }
       }
-    }
-    red[tid] = acc;
-    if (!ok) raise(c, LL_CACHE_ERR_WAIT);
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-    if (tid < groups) {
-      acc = red[tid];
-      for (int i = 1; i < lanes; ++i) acc = add4(acc, red[tid + i * groups]);
-    }
-  }
-  if (Z > 1) {
-    __syncwarp();
-    cluster_wait();  // all CTAs are there
-    if (tid < groups) store_remote4(&parts[sp][4 * tid], 0, acc);
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    if (sp == 0 && tid < groups) {
-      acc = *reinterpret_cast<const float4*>(&parts[0][4 * tid]);
-      for (int z = 1; z < Z; ++z) acc = add4(acc, *reinterpret_cast<const float4*>(&parts[z][4 * tid]));
-    }
-  }
-  if (sp == 0 && tid < groups) {
-    OutT* o = static_cast<OutT*>(a.out) + bh * dv + 4 * tid;
-    o[0] = from_f32<OutT>(acc.x);
-    o[1] = from_f32<OutT>(acc.y);
-    o[2] = from_f32<OutT>(acc.z);
-    o[3] = from_f32<OutT>(acc.w);
-  }
-  // this token joins the block
-  if (sp == Z - 1) {
-    for (int i = tid; i < dv; i += kStepThreads)
-      static_cast<T*>(c.win_v)[(((int64_t)s * H + h) * kW + r) * dv + i] = v[i];
-    if (h % G == 0)
-      for (int i = tid; i < dk; i += kStepThreads)
-        static_cast<T*>(c.win_k)[(((int64_t)s * c.Hqk + hq) * kW + r) * dk + i] = k[i];
-    if (tid == 0) c.win_log_a[((int64_t)s * H + h) * kW + r] = la;
-    if (fold) {  // what the next block's steps read
-      if (tid < live && page_lv[tid] > to)
-        c.page_log[(((int64_t)s * 2 + (par ^ 1)) * M + page_lv[tid]) * H + h] = page_e[tid];
-      if (tid == 0) {
-        c.page_log[(((int64_t)s * 2 + (par ^ 1)) * M + to) * H + h] = 0.f;
-        if (h == 0) c.page_from[s * 2 + (par ^ 1)] = 0;
+      if (kQueue && g.fold) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.window_empty);
+      }
+      sm.red[tid] = acc;
+      consumer_sync();
+      if (tid < groups) {
+        acc = sm.red[tid];
+#pragma unroll 4
+        for (int i = 1; i < lanes; ++i) acc = add4(acc, sm.red[tid + i * groups]);
+        if (kQueue) store_out<OutT>(a.out, bh * dv + 4 * tid, acc);
+      }
+      // this token joins the block
+      if (kQueue || sp == Z - 1) {
+        const int64_t s = it.slot;  // q, k and v are exact in fp32: back to T they are what they were
+        if (tid < dv) static_cast<T*>(c.win_v)[((s * H + h) * kW + g.r) * dv + tid] = from_f32<T>(it.v[tid]);
+        if (h % G == 0 && tid < dk)
+          static_cast<T*>(c.win_k)[((s * Hqk + h / G) * kW + g.r) * dk + tid] = from_f32<T>(it.k[tid]);
+        if (tid == 0) c.win_log_a[(s * H + h) * kW + g.r] = it.log_a;
+        if (g.fold) {  // what the next block's steps read
+          const int par = (g.j & 1) ^ 1;
+          if (tid < g.live && it.page_lv[tid] > g.to)
+            c.page_log[((s * 2 + par) * M + it.page_lv[tid]) * H + h] = it.page_log[tid];
+          if (tid == 0) {
+            c.page_log[((s * 2 + par) * M + g.to) * H + h] = 0.f;
+            if (h == 0) c.page_from[s * 2 + par] = 0;
+          }
+        }
+      }
+      if (!kQueue) break;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.item_empty[ib]);
+      if (++ib == kLoaders) {
+        ib = 0;
+        turn ^= 1;
       }
     }
+    if (!ok && lane == 0) raise(c, LL_CACHE_ERR_WAIT);
+  }
+  if (!kQueue) {
+    const bool run = sm.item[0].kind == kRun;
+    if (Z > 1) {
+      __syncwarp();
+      cluster_wait();  // all CTAs are there
+      if (run && tid < groups) store_remote4(&sm.parts[sp][4 * tid], 0, acc);
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      if (run && sp == 0 && tid < groups) {
+        acc = *reinterpret_cast<const float4*>(&sm.parts[0][4 * tid]);
+        for (int z = 1; z < Z; ++z)
+          acc = add4(acc, *reinterpret_cast<const float4*>(&sm.parts[z][4 * tid]));
+      }
+    }
+    if (run && sp == 0 && tid < groups) store_out<OutT>(a.out, ((int64_t)sm.item[0].row * H + sm.item[0].h) * dv + 4 * tid, acc);
   }
 }
 
@@ -844,11 +1158,11 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
   }
 }
 
-// CTAs per (row, head): doubled while that leaves the launch within two CTAs per SM, and each at
-// least 16 rows of the states.
+// CTAs per (row, head): doubled while that leaves the launch within the SMs, and each at least 16
+// rows of the states.
 int step_split(int64_t rows_heads, int dk) {
   int split = 1;
-  while (split < kMaxSplit && rows_heads * split * 2 <= 2 * 152 && dk >= 32 * split) split *= 2;
+  while (split < kMaxSplit && rows_heads * split * 2 <= 152 && dk >= 32 * split) split *= 2;
   return split;
 }
 
@@ -866,18 +1180,19 @@ cudaError_t launch_cache_reserve(const ll_cache& c, const int* slots, const int*
 
 namespace {
 
-template <typename T, typename OutT>
+template <typename T, typename OutT, bool kQueue>
 cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
   const size_t window = sizeof(T) * kW * (size_t)(c.dk + c.dv);
-  // as many stages as leave room for two CTAs per SM (and at least two); 12 KB are static
-  a.stages = (int)std::max<size_t>(2, std::min<size_t>(8, (100 * 1024 - window) / (kStageFloats * 4)));
+  // as many stages as leave room for two CTAs per SM (228 KB, 1 KB per CTA its own), at least two
+  a.stages = (int)std::max<size_t>(2, std::min<size_t>(kMaxStages, (115000 - sizeof(StepSmem) - window) / (kStageFloats * 4)));
   const size_t smem = window + (size_t)a.stages * kStageFloats * 4;
-  const cudaError_t e = cudaFuncSetAttribute(cache_step_kernel<T, OutT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const auto kernel = cache_step_kernel<T, OutT, kQueue>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.n * c.H * a.split));
-  cfg.blockDim = dim3(kStepThreads);
+  cfg.blockDim = dim3(kQueue ? kQueueThreads : kSplitThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -887,7 +1202,15 @@ cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, cache_step_kernel<T, OutT>, c, a);
+  return cudaLaunchKernelEx(&cfg, kernel, c, a);
+}
+
+// The queue where there is an item for every SM, the split form below that.
+template <typename T, typename OutT>
+cudaError_t launch_form(const ll_cache& c, StepArgs a, cudaStream_t s) {
+  const int64_t items = (int64_t)a.n * c.H;
+  a.split = items > 152 ? 1 : step_split(items, (int)c.dk);
+  return items > 152 ? launch_step<T, OutT, true>(c, a, s) : launch_step<T, OutT, false>(c, a, s);
 }
 
 }  // namespace
@@ -898,12 +1221,12 @@ cudaError_t launch_cache_step(const ll_cache& c, const int* slots, const int* po
   StepArgs a;
   a.slots = slots; a.pos = pos; a.q = q; a.k = k; a.v = v; a.log_a = log_a; a.lam = lam;
   a.out = out; a.n = n; a.L = L; a.stages = 0;
-  a.split = step_split((int64_t)n * c.H, (int)c.dk);
+  a.split = 1;
   const bool o32 = out_dtype == LL_F32;
   if (c.dtype == LL_F32)
-    return o32 ? launch_step<float, float>(c, a, s) : launch_step<float, __nv_bfloat16>(c, a, s);
-  return o32 ? launch_step<__nv_bfloat16, float>(c, a, s)
-             : launch_step<__nv_bfloat16, __nv_bfloat16>(c, a, s);
+    return o32 ? launch_form<float, float>(c, a, s) : launch_form<float, __nv_bfloat16>(c, a, s);
+  return o32 ? launch_form<__nv_bfloat16, float>(c, a, s)
+             : launch_form<__nv_bfloat16, __nv_bfloat16>(c, a, s);
 }
 
 cudaError_t launch_cache_load(const ll_cache& c, const int* slots, int64_t n, int T,

@@ -358,7 +358,7 @@ __device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, 
     } else {
       for (int z = 0; z < Z; ++z)
         if (z != rank) send(&sm.tile[k & 1][rank - (rank > z)][tid], &sm.bar[k & 1], z, m);
-      if (!tc::mbar_wait(&sm.bar[k & 1], (k >> 1) & 1)) atomicOr(&g_glr_error, 2u);
+      if (!tc::mbar_wait_short(&sm.bar[k & 1], (k >> 1) & 1)) atomicOr(&g_glr_error, 2u);
       for (int z = 0; z < Z; ++z) {
         if (z == rank) sm.seg[kSegs - 1][tid].x = c;
         const float2 n = z == rank ? m : sm.tile[k & 1][z - (z > rank)][tid];

@@ -220,6 +220,59 @@ def test_sequences_at_positions_of_their_own(LL):
     assert cache.error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,H,Hqk,dk,dv", [(70, 3, 3, 16, 8), (40, 4, 2, 33, 20), (26, 6, 1, 128, 128),
+                                           (160, 1, 1, 64, 36), (400, 2, 1, 8, 4)])
+def test_batches_of_more_items_than_sms(LL, n, H, Hqk, dk, dv, dtype):
+    """Rows at positions all over, block ends among them, with rows that are padding or cannot be
+    served in between; three steps, each against the dense step in fp64, and the states after."""
+    M = 8
+    L = M + 7
+    rng = np.random.default_rng(n)
+    cache = poison(LL.LogLinearCache.empty(n, 5 * n, H, dk, dv, M, Hqk=Hqk, dtype=DT[dtype]))
+    kinds = [0, 1, 62, 63, 64, 126, 127, 4095, 4094, 8190, 12345, 61] + rng.integers(0, 16000, 6).tolist()
+    T = [kinds[i % len(kinds)] for i in range(n)]
+    slots = rng.permutation(n)
+    ref = np.zeros((n, H, L, dk, dv))
+    for t0 in sorted(set(T)):
+        rows = [i for i in range(n) if T[i] == t0]
+        S, tok = dense_inputs(t0, len(rows), H, dk, dv, L, seed=t0, dtype=dtype, Hqk=Hqk)
+        prompt = tok(64)
+        if t0 % 64:
+            S = block_states(S, prompt, t0)
+        c = {k: v.cuda() for k, v in prompt.items()}
+        LL.loglinear_cache_load(cache, i32(slots[rows]), t0, S.cuda(), c["k"], c["v"], c["log_a"])
+        ref[rows] = S.double().numpy()
+    assert cache.error() == 0
+    _, tok = dense_inputs(1, n, H, dk, dv, L, seed=3, dtype=dtype, Hqk=Hqk)
+    x = tok(3)
+    s = i32(slots)
+    idle = [3, n - 1]
+    s_idle = s.clone()
+    s_idle[idle[0]], s_idle[idle[1]] = -1, n + 5
+    for i in range(3):
+        p = i32([t + i for t in T])
+        a = {k: v[:, i].contiguous().cuda() for k, v in x.items()}
+        args = (a["q"], a["k"], a["v"], a["log_a"], a["lam"])
+        LL.loglinear_cache_reserve(cache, s, p)
+        out = torch.full((n, H, dv), 7.0).cuda()
+        LL.loglinear_cache_step(cache, s_idle, p, *args, out=out)
+        assert torch.all(out[idle] == 7) and cache.error() == LL.CACHE_ERR_SLOT
+        LL.loglinear_cache_step(cache, s, p, *args, out=out)
+        assert cache.error() == 0
+        y = {k: to64(v[:, i]) for k, v in x.items()}
+        y["q"], y["k"] = (np.repeat(y[k], H // Hqk, axis=1) for k in ("q", "k"))
+        for b in range(n):
+            new, want = oracle.decode_step(ref[b:b + 1], *(y[k][b:b + 1] for k in ("q", "k", "v", "log_a", "lam")), T[b] + i)
+            ref[b] = new[0]
+            check(out[b].cpu(), want[0])
+    got = LL.loglinear_cache_store(cache, s, i32([t + 3 for t in T])).cpu()
+    for b in range(n):
+        if (T[b] + 3) % 64:
+            check(got[b], ref[b])
+    invariants(cache, {int(slots[b]): T[b] + 3 for b in range(n)})
+
+
 def filled(LL, seed=0, n=3, T=(100, 200, 320), spare=12, dtype="f32", M=4):
     """A cache with n sequences decoded from nothing, and their inputs."""
     H, dk, dv = 2, 16, 8
