@@ -416,10 +416,12 @@ struct StepArgs {
 };
 
 // What the warps of a CTA hand each other.
-struct __align__(16) Item {  // its vectors are read four at a time
-  float q[128], k[128], v[128];
+struct __align__(16) Item {
+  __align__(16) float q[128];   // v and tok are read as vectors
+  __align__(16) float k[128];
+  __align__(16) float v[128];
+  __align__(16) float tok[kW];  // decay from each token of the block to the new one
   float lam[kMaxLevels + kLogW + 1];
-  float tok[kW];                // decay from each token of the block to the new one
   // the live pages, lowest level first: log decay, decay, decay times lambda
   float page_log[kMaxLevels], page_e[kMaxLevels], page_w[kMaxLevels];
   int page_at[kMaxLevels], page_lv[kMaxLevels];
@@ -510,7 +512,7 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
   float since;
   block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], it.tok, &since);
   it.tok[lane] = expf(it.tok[lane] + la);
-  it.tok[lane + 32] = expf(it.tok[lane + 32] + la);
+  it.tok[lane + 32] = lane + 32 == r ? 1.f : expf(it.tok[lane + 32] + la);  // a fold's own token: 1
   if (here) {
     const int at = __popc(j & ((1 << lane) - 1));
     it.page_at[at] = e;
@@ -530,14 +532,18 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
   return __all_sync(0xffffffffu, e >= 0 && e < c.n_pages);
 }
 
+constexpr int kPad = 8;  // elements
+
 // An item's geometry in a CTA: its state rows [k0, k1) and tokens [t0, t1).  A fold needs all
 // tokens' products, so it brings them all ([b0, b1)).
 struct Part {
   int j, r, to, live;
-  bool fold;
+  bool fold, mma;  // mma: the fold's token products come from the tensor cores
   int k0, k1, t0, t1, b0, b1;
+  int kp, vp;      // elements from token to token in the window: set off by 16 bytes for mma
 };
-__device__ __forceinline__ Part part_of(int pos, int dk, int Z, int sp) {
+template <typename T>
+__device__ __forceinline__ Part part_of(int pos, int dk, int dv, int Z, int sp) {
   Part p;
   p.j = pos >> kLogW;
   p.r = pos & (kW - 1);
@@ -552,6 +558,11 @@ __device__ __forceinline__ Part part_of(int pos, int dk, int Z, int sp) {
   p.t1 = min(p.r, p.t0 + tokens);
   p.b0 = p.fold ? 0 : p.t0;
   p.b1 = p.fold ? p.r : p.t1;
+  // tensor cores: bf16 tokens whose rows are whole 16-byte pieces
+  p.mma = sizeof(T) == 2 && p.fold && dk % 8 == 0 && dv % 8 == 0 && p.k0 % 8 == 0 &&
+          (p.k1 - p.k0) % 16 == 0;
+  p.kp = p.mma ? dk + kPad : dk;
+  p.vp = p.mma ? dv + kPad : dv;
   return p;
 }
 
@@ -575,6 +586,68 @@ __device__ __forceinline__ bool consumer_any(bool x) {
   return r != 0;
 }
 
+// The products of a fold's 64 tokens for state rows [k0, k1) (a multiple of 16), by the consumer
+// warps, to D [dk][dv]: sum over s of k_s (e_s v_s)^T on the tensor cores, bf16 keys as they are
+// and e v split into three bf16 parts, which together are its fp32 value; products and sums
+// are fp32.  (Multiply-adds took 10 us more per fold, the tail of a ragged batch.)
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], const __nv_bfloat16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(tc::smem_u32(p))
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t take_bf16(float2& x) {  // x's leading bf16 parts; x keeps the rest
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+  const float2 f = __bfloat1622float2(h);
+  x.x -= f.x;
+  x.y -= f.y;
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void fold_tokens(const __nv_bfloat16* wks, const __nv_bfloat16* wvs,
+                                            const float* tok, int kp, int vp, int dv, int k0, int k1,
+                                            float* D) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int g = lane >> 2, i = 2 * (lane & 3);
+  // ldmatrix rows: lanes 0-7, 8-15, 16-23, 24-31 address the four 8 x 8 matrices
+  const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
+  for (int nt = w; nt < dv / 8; nt += kStepWarps) {
+    uint32_t b[kW / 16][3][2];
+#pragma unroll
+    for (int ks = 0; ks < kW / 16; ks += 2) {
+      uint32_t r[4];  // tokens 16 ks .. + 31 of 8 columns
+      ldmatrix_trans(r, wvs + (16 * ks + lane) * vp + 8 * nt);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int s = 16 * ks + 8 * u + i;
+        float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[u]));
+        const float2 e = *reinterpret_cast<const float2*>(tok + s);
+        x = make_float2(x.x * e.x, x.y * e.y);
+#pragma unroll
+        for (int v = 0; v < 3; ++v) b[ks + (u >> 1)][v][u & 1] = take_bf16(x);
+      }
+    }
+    for (int d = k0; d < k1; d += 16) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < kW / 16; ++ks) {
+        uint32_t a[4];
+        ldmatrix_trans(a, wks + (16 * ks + mrow) * kp + d + mcol);
+#pragma unroll
+        for (int v = 2; v >= 0; --v) mma_bf16(c, a, b[ks][v][0], b[ks][v][1]);
+      }
+      *reinterpret_cast<float2*>(D + (d + g) * dv + 8 * nt + i) = make_float2(c[0], c[1]);
+      *reinterpret_cast<float2*>(D + (d + g + 8) * dv + 8 * nt + i) = make_float2(c[2], c[3]);
+    }
+  }
+}
+
 template <typename T, typename OutT, bool kQueue>
 __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
     cache_step_kernel(ll_cache c, StepArgs a) {
@@ -588,7 +661,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
   const int span = per * lanes;
   float* ring = reinterpret_cast<float*>(dyn);
   T* wks = reinterpret_cast<T*>(dyn + (size_t)a.stages * kStageFloats * 4);
-  T* wvs = wks + kW * dk;
+  T* wvs = wks + kW * (dk + kPad);
   if (tid == 0) {
     for (int i = 0; i < kLoaders; ++i) {
       tc::mbar_init(&sm.index_full[i], 1);
@@ -611,12 +684,17 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
   auto bring_window = [&](int64_t s, int h, const Part& g) {
     const uint32_t nk = ((g.b1 - g.b0) * dk * sizeof(T) + 15) & ~15u;
     const uint32_t nv = ((g.b1 - g.b0) * dv * sizeof(T) + 15) & ~15u;
-    tc::mbar_arrive_expect_tx(&sm.window_full, nk + nv);
-    if (g.b1 > g.b0) {
-      bulk_load(wks + g.b0 * dk, static_cast<const T*>(c.win_k) + ((s * Hqk + h / G) * kW + g.b0) * dk, nk,
-                &sm.window_full);
-      bulk_load(wvs + g.b0 * dv, static_cast<const T*>(c.win_v) + ((s * H + h) * kW + g.b0) * dv, nv,
-                &sm.window_full);
+    const T* wk = static_cast<const T*>(c.win_k) + (s * Hqk + h / G) * kW * dk;
+    const T* wv = static_cast<const T*>(c.win_v) + (s * H + h) * kW * dv;
+    tc::mbar_arrive_expect_tx(&sm.window_full, nk + nv);  // (mma: rows of whole 16 bytes, no rounding)
+    if (g.mma) {
+      for (int i = g.b0; i < g.b1; ++i) {
+        bulk_load(wks + i * g.kp, wk + i * dk, dk * sizeof(T), &sm.window_full);
+        bulk_load(wvs + i * g.vp, wv + i * dv, dv * sizeof(T), &sm.window_full);
+      }
+    } else if (g.b1 > g.b0) {
+      bulk_load(wks + g.b0 * dk, wk + g.b0 * dk, nk, &sm.window_full);
+      bulk_load(wvs + g.b0 * dv, wv + g.b0 * dv, nv, &sm.window_full);
     }
   };
   bool ok = true, brought = false;
@@ -631,7 +709,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
     bool twice = false, there = true;
     if (run) {
       if (w == kProducer) {
-        if (lane == 0) bring_window(s, h, part_of(t, dk, Z, sp));
+        if (lane == 0) bring_window(s, h, part_of<T>(t, dk, dv, Z, sp));
         brought = true;
       } else if (w == kScheduler + 1) {
         there = load_links(c, a, row, h, s, t, sm.item[0]);
@@ -711,7 +789,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
       const Item& it = sm.item[ib];
       if (it.kind == kStop || (!kQueue && it.kind == kSkip)) break;
       if (it.kind == kRun) {
-        const Part g = part_of(it.pos, dk, Z, sp);
+        const Part g = part_of<T>(it.pos, dk, dv, Z, sp);
         const int h = it.h;
         if (kQueue) {
           if (!(ok = tc::mbar_wait_short(&sm.window_empty, (used & 1) ^ 1))) break;
@@ -773,9 +851,13 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
         }
         continue;
       }
-      const Part g = part_of(it.pos, dk, Z, sp);
+      const Part g = part_of<T>(it.pos, dk, dv, Z, sp);
       ok = tc::mbar_wait_short(&sm.window_full, used & 1) && ok;
       ++used;
+      if (g.mma) {  // the new token joins the others
+        if (tid < dk) wks[(kW - 1) * g.kp + tid] = from_f32<T>(it.k[tid]);
+        if (tid < dv) wvs[(kW - 1) * g.vp + tid] = from_f32<T>(it.v[tid]);
+      }
       // scores of the CTA's tokens, a warp every eighth; the cluster's first has the new one too
       float qv[4];
 #pragma unroll
@@ -785,7 +867,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
         float x = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (lane + 32 * u < dk) x = fmaf(qv[u], to_f32(wks[i * dk + lane + 32 * u]), x);
+          if (lane + 32 * u < dk) x = fmaf(qv[u], to_f32(wks[i * g.kp + lane + 32 * u]), x);
         x = warp_sum(x);
         if (lane == 0) sm.p[i] = it.lam[fenwick_level(g.r, i)] * it.tok[i] * x;
       }
@@ -803,14 +885,22 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
       if (on) {
         if (row0 == 0 && (kQueue || sp == 0)) acc = fma4(sm.self, v4, acc);
 #pragma unroll 4
-        for (int i = g.t0 + row0; i < g.t1; i += lanes) acc = fma4(sm.p[i], load4(wvs + i * dv + 4 * cg), acc);
-      }
-      if (kQueue && !g.fold) {  // the next item's tokens may come
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.window_empty);
+        for (int i = g.t0 + row0; i < g.t1; i += lanes) acc = fma4(sm.p[i], load4(wvs + i * g.vp + 4 * cg), acc);
       }
       const int h = it.h;
       const int64_t bh = (int64_t)it.row * H + h;
+      float* folded = c.pages + ((int64_t)it.dest * H + h) * dk * dv;  // (g.fold)
+      if constexpr (sizeof(T) == 2) {
+        if (g.mma) {
+          fold_tokens(wks, wvs, it.tok, g.kp, g.vp, dv, g.k0, g.k1, folded);
+          tc::fence_proxy_async_smem();  // the next bulk copy is written behind the new token
+          consumer_sync();
+        }
+      }
+      if (kQueue && (!g.fold || g.mma)) {  // the next item's tokens may come
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.window_empty);
+      }
       for (int c0 = g.k0; c0 < g.k1; c0 += span) {
         const int d0 = c0 + per * row0;
         const int rows = on ? min(per, g.k1 - d0) : 0;  // this thread's rows (below 1: none)
@@ -837,8 +927,10 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
           continue;
         }
         float4 sum[kRowsPer];
+        float4* D = reinterpret_cast<float4*>(folded + d0 * dv + 4 * cg);
 #pragma unroll
-        for (int x = 0; x < kRowsPer; ++x) sum[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < kRowsPer; ++x)
+          sum[x] = g.mma && x < rows ? __ldcg(D + x * groups) : make_float4(0.f, 0.f, 0.f, 0.f);
         for (int m = 0; m < g.live; ++m) {
           ok = tc::mbar_wait_short(&sm.full[st], phase) && ok;
           const float* P = mine + st * kStageFloats;
@@ -861,8 +953,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
         }
         if (rows > 0) {
           const bool quads = rows == 4 && dk % 4 == 0 && d0 % 4 == 0;  // four keys in one load
-#pragma unroll 2
-          for (int i = 0; i < g.r; ++i) {
+          for (int i = 0; i < g.r && !g.mma; ++i) {
             const float4 y = load4(wvs + i * dv + 4 * cg);
             const float e = it.tok[i];
             const T* kr = wks + i * dk + d0;
@@ -880,15 +971,12 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
             sum[2] = fma4(e * k4.z, y, sum[2]);
             sum[3] = fma4(e * k4.w, y, sum[3]);
           }
-          if (ok) {
-            float* D = c.pages + (((int64_t)it.dest * H + h) * dk + d0) * dv + 4 * cg;
 #pragma unroll
-            for (int x = 0; x < kRowsPer; ++x)
-              if (x < rows) *reinterpret_cast<float4*>(D + x * dv) = fma4(it.k[d0 + x], v4, sum[x]);
-          }
+          for (int x = 0; x < kRowsPer; ++x)
+            if (x < rows && ok) D[x * groups] = g.mma ? sum[x] : fma4(it.k[d0 + x], v4, sum[x]);
         }
       }
-      if (kQueue && g.fold) {
+      if (kQueue && g.fold && !g.mma) {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.window_empty);
       }
@@ -1182,7 +1270,7 @@ namespace {
 
 template <typename T, typename OutT, bool kQueue>
 cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
-  const size_t window = sizeof(T) * kW * (size_t)(c.dk + c.dv);
+  const size_t window = sizeof(T) * kW * (size_t)(c.dk + c.dv + 2 * kPad);
   // as many stages as leave room for two CTAs per SM (228 KB, 1 KB per CTA its own), at least two
   a.stages = (int)std::max<size_t>(2, std::min<size_t>(kMaxStages, (115000 - sizeof(StepSmem) - window) / (kStageFloats * 4)));
   const size_t smem = window + (size_t)a.stages * kStageFloats * 4;
