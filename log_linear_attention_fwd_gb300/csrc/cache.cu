@@ -292,10 +292,9 @@ __global__ void __launch_bounds__(kCopyThreads) cache_load_kernel(
 
 // after[i] = sum of la[u], i < u < r (0 at and past r - 1), and *since = sum of la[u], from <= u
 // < r, for r <= 64 values.  One warp; sums run from the end, in one order.
-__device__ __forceinline__ void block_decays(const float* la, int r, int from, float* after,
-                                             float* since) {  // *since in every lane
-  const int lane = threadIdx.x & 31;
-  const float x0 = lane < r ? la[lane] : 0.f, x1 = lane + 32 < r ? la[lane + 32] : 0.f;
+__device__ __forceinline__ void block_decays(float x0, float x1, int r, int from, float* after,
+                                             float* since) {
+  const int lane = threadIdx.x & 31;  // x0, x1: la[lane] and la[lane + 32], 0 from r on
   float y0 = x0, y1 = x1;  // inclusive sums from the end of each half
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -317,6 +316,12 @@ __device__ __forceinline__ void block_decays(const float* la, int r, int from, f
   after[lane + 32] = n1;
   const float f0 = __shfl_sync(0xffffffffu, y0, from & 31), f1 = __shfl_sync(0xffffffffu, y1, from & 31);
   *since = from >= r ? 0.f : from < 32 ? f0 : f1;
+}
+
+__device__ __forceinline__ void block_decays(const float* la, int r, int from, float* after,
+                                             float* since) {  // *since in every lane
+  const int lane = threadIdx.x & 31;
+  block_decays(lane < r ? la[lane] : 0.f, lane + 32 < r ? la[lane + 32] : 0.f, r, from, after, since);
 }
 
 // ---------------------------------------------------------------- step
@@ -468,28 +473,48 @@ __device__ __forceinline__ int read_next(const uint4* from) {
   return got ? (int)x : -1;
 }
 
-// The item's vectors, by thread i0 of `step`.  True where an earlier row has its slot.
-template <typename T>
-__device__ __forceinline__ bool load_vectors(const ll_cache& c, const StepArgs& a, int row, int h, int s,
-                                             int i0, int step, Item& it) {
-  const int Hqk = (int)c.Hqk, G = (int)c.H / Hqk, dk = (int)c.dk, dv = (int)c.dv, M = (int)c.levels;
-  const int64_t bh = (int64_t)row * (int)c.H + h;
-  const T* q = static_cast<const T*>(a.q) + ((int64_t)row * Hqk + h / G) * dk;
-  const T* k = static_cast<const T*>(a.k) + ((int64_t)row * Hqk + h / G) * dk;
-  const T* v = static_cast<const T*>(a.v) + bh * dv;
+// The item's vectors, by thread i0 of kStep: all loads first (fetch), for a loader warp's time is
+// the latency of its loads, one after the other or all at once; then to shared memory (put).
+template <typename T, int kStep>
+struct Vectors {
+  static constexpr int N = kStep < 128 ? 128 / kStep : 1;
+  T q[N], k[N], v[N];
+  float lam;
+  bool twice;  // an earlier row has its slot
+  __device__ __forceinline__ void fetch(const ll_cache& c, const StepArgs& a, int row, int h, int s, int i0) {
+    const int Hqk = (int)c.Hqk, G = (int)c.H / Hqk, dk = (int)c.dk, dv = (int)c.dv;
+    const int64_t bh = (int64_t)row * (int)c.H + h;
+    const T* gq = static_cast<const T*>(a.q) + ((int64_t)row * Hqk + h / G) * dk;
+    const T* gk = static_cast<const T*>(a.k) + ((int64_t)row * Hqk + h / G) * dk;
+    const T* gv = static_cast<const T*>(a.v) + bh * dv;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + u * kStep;
+      if (i < dk) {
+        q[u] = gq[i];
+        k[u] = gk[i];
+      }
+      if (i < dv) v[u] = gv[i];
+    }
+    if (i0 < (int)c.levels + kLogW + 1) lam = a.lam[bh * a.L + i0];
+    twice = false;
 #pragma unroll 4
-  for (int i = i0; i < dk; i += step) {
-    it.q[i] = to_f32(q[i]);
-    it.k[i] = to_f32(k[i]);
+    for (int i = i0; i < row; i += kStep) twice |= a.slots[i] == s;
   }
-#pragma unroll 4
-  for (int i = i0; i < dv; i += step) it.v[i] = to_f32(v[i]);
-  for (int i = i0; i < M + kLogW + 1; i += step) it.lam[i] = a.lam[bh * a.L + i];
-  bool twice = false;
-#pragma unroll 4
-  for (int i = i0; i < row; i += step) twice |= a.slots[i] == s;
-  return twice;
-}
+  __device__ __forceinline__ void put(const ll_cache& c, int i0, Item& it) const {
+    const int dk = (int)c.dk, dv = (int)c.dv;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + u * kStep;
+      if (i < dk) {
+        it.q[i] = to_f32(q[u]);
+        it.k[i] = to_f32(k[u]);
+      }
+      if (i < dv) it.v[i] = to_f32(v[u]);
+    }
+    if (i0 < (int)c.levels + kLogW + 1) it.lam[i0] = lam;
+  }
+};
 
 // Why a row cannot be served, before its pages are looked at.
 __device__ __forceinline__ unsigned row_bad(const ll_cache& c, int s, int t) {
@@ -509,8 +534,10 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
   const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
   const float la = a.log_a ? a.log_a[bh] : 0.f;
   const float lam = here ? a.lam[bh * a.L + kLogW + 1 + lane] : 0.f;
+  const float* wa = c.win_log_a + ((int64_t)s * H + h) * kW;
+  const float x0 = lane < r ? wa[lane] : 0.f, x1 = lane + 32 < r ? wa[lane + 32] : 0.f;
   float since;
-  block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], it.tok, &since);
+  block_decays(x0, x1, r, c.page_from[s * 2 + par], it.tok, &since);
   it.tok[lane] = expf(it.tok[lane] + la);
   it.tok[lane + 32] = lane + 32 == r ? 1.f : expf(it.tok[lane + 32] + la);  // a fold's own token: 1
   if (here) {
@@ -714,7 +741,10 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
       } else if (w == kScheduler + 1) {
         there = load_links(c, a, row, h, s, t, sm.item[0]);
       } else if (w < kStepWarps) {
-        twice = load_vectors<T>(c, a, row, h, s, tid, kConsumers, sm.item[0]);
+        Vectors<T, kConsumers> x;
+        x.fetch(c, a, row, h, s, tid);
+        x.put(c, tid, sm.item[0]);
+        twice = x.twice;
       }
     }
     twice = __syncthreads_or(twice);
@@ -745,9 +775,11 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
         if (s != -1) {
           unsigned why = row_bad(c, s, t);
           if (!why) {
-            const bool twice = load_vectors<T>(c, a, row, h, s, lane, 32, it);
+            Vectors<T, 32> x;
+            x.fetch(c, a, row, h, s, lane);
             if (!load_links(c, a, row, h, s, t, it)) why = LL_CACHE_ERR_MISSING;
-            if (__any_sync(0xffffffffu, twice)) why = LL_CACHE_ERR_SLOT;
+            x.put(c, lane, it);
+            if (__any_sync(0xffffffffu, x.twice)) why = LL_CACHE_ERR_SLOT;
           }
           if (!why) kind = kRun;
           else if (lane == 0 && h == 0) raise(c, why);
