@@ -508,6 +508,24 @@ def _here(name, t, dtype=None, shape=None):
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
+def _at(name, t, dtype, shape, dev):
+    """The address of a contiguous tensor on device `dev`, the current one (None: no tensor).
+    A step's calls take about as long on the host as on the GPU: one test where all is well."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _here(name, t, dtype, shape)
+    raise ValueError(f"{name} is not as expected")
+
+
+def _raw_stream(stream, dev):
+    """The stream's handle (None: the current one)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)  # current_stream() takes 3 us
+    return stream.cuda_stream
+
+
 def _token_strides(name, t, shape, dtype=None, features=True):
     """An input with strided batch, position (and head) dimensions, its features (if it has
     any) contiguous: its strides, or None when dense."""
@@ -561,10 +579,10 @@ def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None
     if out is None:
         out = _empty(stream, B, T, D, device=x.device, dtype=out_dtype or x.dtype)
     _here("out", out, shape=(B, T, D))
-    st = _lib.loglinear_glr_fwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
-                                _ptr(out), _ptr(state), B, T, D, _dtype_code(x),
-                                _dtype_code(log_a), _dtype_code(out), GLR_SCALES[scale],
-                                _stream(stream))
+    st = _lib.loglinear_glr_fwd(x.data_ptr(), xs, log_a.data_ptr(), ls, _ptr(h0),
+                                _ptr(cu_seqlens), N, out.data_ptr(), _ptr(state), B, T, D,
+                                _dtype_code(x), _dtype_code(log_a), _dtype_code(out),
+                                GLR_SCALES[scale], _raw_stream(stream, out.get_device()))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_fwd")
     return out
@@ -590,7 +608,8 @@ def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none
     st = _lib.loglinear_glr_bwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
                                 _ptr(out), _ptr(dout), _ptr(dstate), _ptr(dx), _ptr(dla),
                                 _ptr(dh0), B, T, D, gate if x is None else _dtype_code(x), gate,
-                                _dtype_code(out), GLR_SCALES[scale], _stream(stream))
+                                _dtype_code(out), GLR_SCALES[scale],
+                                _raw_stream(stream, out.get_device()))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_bwd")
     return dx, dla, dh0
@@ -601,18 +620,19 @@ def loglinear_glr_step(state, x, log_a, slots=None, scale="none", out=None, out_
     """One token of the recurrence per row: state [S,D] fp32 is updated in place at slots (int32
     [B], -1 leaves the row out; None: row b is slot b).  x, log_a [B,D].  Returns out [B,D]."""
     B, D = x.shape
-    _here("x", x)
-    _here("log_a", log_a, shape=(B, D))
+    dev = x.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"x must be a CUDA tensor on the current device, got {x.device}")
     if state.dim() != 2 or state.shape[1] != D:
         raise ValueError(f"state has shape {tuple(state.shape)}, expected (S, {D})")
-    _here("state", state, torch.float32)
-    _here("slots", slots, torch.int32, (B,))
     if out is None:
         out = _empty(stream, B, D, device=x.device, dtype=out_dtype or x.dtype)
-    _here("out", out, shape=(B, D))
-    st = _lib.loglinear_glr_step(_ptr(state), state.shape[0], _ptr(slots), _ptr(x), _ptr(log_a),
-                                 _ptr(out), B, D, _dtype_code(x), _dtype_code(log_a),
-                                 _dtype_code(out), GLR_SCALES[scale], _stream(stream))
+    st = _lib.loglinear_glr_step(
+        _at("state", state, torch.float32, state.shape, dev), state.shape[0],
+        _at("slots", slots, torch.int32, (B,), dev), _at("x", x, x.dtype, (B, D), dev),
+        _at("log_a", log_a, log_a.dtype, (B, D), dev), _at("out", out, out.dtype, (B, D), dev), B, D,
+        _dtype_code(x), _dtype_code(log_a), _dtype_code(out), GLR_SCALES[scale],
+        _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_step")
     return out
@@ -685,20 +705,22 @@ class LogLinearCache:
             self.error_word.zero_()
         return bits
 
-    def _rows(self, **named):
-        n = None
-        for name, t in named.items():
-            n = t.numel() if n is None else n
-            _here(name, t, torch.int32, (n,))
-        return n
+    def _dev(self):
+        """The cache's device, which has to be the current one."""
+        dev = self.device.index
+        if torch.cuda.current_device() != dev:
+            raise ValueError(f"the cache is on {self.device}, not on the current device")
+        return dev
 
 
 def loglinear_cache_reserve(cache, slots, pos, stream=None):
     """The page reservation that goes before a loglinear_cache_step at the same slots and
     positions (int32 [n] each): pages no longer live are given up, and slots at a block's last
     position take the page it is folded into."""
-    n = cache._rows(slots=slots, pos=pos)
-    st = _lib.loglinear_cache_reserve(cache._ref, _ptr(slots), _ptr(pos), n, _stream(stream))
+    dev, n = cache._dev(), slots.numel()
+    st = _lib.loglinear_cache_reserve(cache._ref, _at("slots", slots, torch.int32, (n,), dev),
+                                      _at("pos", pos, torch.int32, (n,), dev), n,
+                                      _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_reserve")
 
@@ -708,19 +730,16 @@ def loglinear_cache_step(cache, slots, pos, q, k, v, log_a, lam, out=None, out_d
     """One decode step for n rows, row i being slot slots[i] at position pos[i].  q, k [n,Hqk,dk],
     v [n,H,dv] in the cache's dtype; log_a [n,H] fp32 or None; lam [n,H,L] fp32, L >= levels + 7.
     Rows with slot -1 are left out (their out is not written).  Returns out [n,H,dv]."""
-    n = cache._rows(slots=slots, pos=pos)
-    L = lam.shape[-1]
-    _here("q", q, cache.dtype, (n, cache.qk_heads, cache.dk))
-    _here("k", k, cache.dtype, (n, cache.qk_heads, cache.dk))
-    _here("v", v, cache.dtype, (n, cache.heads, cache.dv))
-    _here("log_a", log_a, torch.float32, (n, cache.heads))
-    _here("lam", lam, torch.float32, (n, cache.heads, L))
+    dev, n, L = cache._dev(), slots.numel(), lam.shape[-1]
+    dt, H, qk = cache.dtype, cache.heads, (n, cache.qk_heads, cache.dk)
     if out is None:
-        out = _empty(stream, n, cache.heads, cache.dv, device=q.device, dtype=out_dtype or q.dtype)
-    _here("out", out, shape=(n, cache.heads, cache.dv))
-    st = _lib.loglinear_cache_step(cache._ref, _ptr(slots), _ptr(pos), _ptr(q), _ptr(k), _ptr(v),
-                                   _ptr(log_a), _ptr(lam), _ptr(out), n, L, _dtype_code(out),
-                                   _stream(stream))
+        out = _empty(stream, n, H, cache.dv, device=q.device, dtype=out_dtype or q.dtype)
+    st = _lib.loglinear_cache_step(
+        cache._ref, _at("slots", slots, torch.int32, (n,), dev), _at("pos", pos, torch.int32, (n,), dev),
+        _at("q", q, dt, qk, dev), _at("k", k, dt, qk, dev), _at("v", v, dt, (n, H, cache.dv), dev),
+        _at("log_a", log_a, torch.float32, (n, H), dev), _at("lam", lam, torch.float32, (n, H, L), dev),
+        _at("out", out, out.dtype, (n, H, cache.dv), dev), n, L, _dtype_code(out),
+        _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_step")
     return out
@@ -730,14 +749,15 @@ def loglinear_cache_load(cache, slots, T, state, k, v, log_a, stream=None):
     """Puts n prompts of T positions into slots (int32 [n]), which give up what they held.  state
     [n,H,L,dk,dv] fp32 as loglinear_prefill returns it; k [n,Tk,Hqk,dk], v [n,Tk,H,dv], log_a
     [n,Tk,H] or None: the prompt's last Tk >= T mod 64 tokens (views such as k[:, -64:] do)."""
-    n = cache._rows(slots=slots)
+    dev, n = cache._dev(), slots.numel()
     L, Tk = state.shape[2], k.shape[1]
-    _here("state", state, torch.float32, (n, cache.heads, L, cache.dk, cache.dv))
     sk = _token_strides("k", k, (n, Tk, cache.qk_heads, cache.dk), cache.dtype)
     sv = _token_strides("v", v, (n, Tk, cache.heads, cache.dv), cache.dtype)
     sa = _token_strides("log_a", log_a, (n, Tk, cache.heads), torch.float32, features=False)
-    st = _lib.loglinear_cache_load(cache._ref, _ptr(slots), n, T, _ptr(state), L, _ptr(k), sk,
-                                   _ptr(v), sv, _ptr(log_a), sa, Tk, _stream(stream))
+    st = _lib.loglinear_cache_load(
+        cache._ref, _at("slots", slots, torch.int32, (n,), dev), n, T,
+        _at("state", state, torch.float32, (n, cache.heads, L, cache.dk, cache.dv), dev), L,
+        k.data_ptr(), sk, v.data_ptr(), sv, _ptr(log_a), sa, Tk, _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_load")
 
@@ -745,14 +765,15 @@ def loglinear_cache_load(cache, slots, T, state, k, v, log_a, stream=None):
 def loglinear_cache_store(cache, slots, pos, state=None, stream=None):
     """Dense states [n,H,L,dk,dv] fp32 (L >= levels + 7) of slots that hold pos positions, from
     which loglinear_decode_step goes on at t = pos.  Returns state."""
-    n = cache._rows(slots=slots, pos=pos)
+    dev, n = cache._dev(), slots.numel()
     if state is None:
         state = _empty(stream, n, cache.heads, cache.levels + 7, cache.dk, cache.dv,
                        device=cache.device)
     L = state.shape[2]
-    _here("state", state, torch.float32, (n, cache.heads, L, cache.dk, cache.dv))
-    st = _lib.loglinear_cache_store(cache._ref, _ptr(slots), _ptr(pos), _ptr(state), n, L,
-                                    _stream(stream))
+    st = _lib.loglinear_cache_store(
+        cache._ref, _at("slots", slots, torch.int32, (n,), dev), _at("pos", pos, torch.int32, (n,), dev),
+        _at("state", state, torch.float32, (n, cache.heads, L, cache.dk, cache.dv), dev), n, L,
+        _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_store")
     return state
@@ -761,16 +782,19 @@ def loglinear_cache_store(cache, slots, pos, state=None, stream=None):
 def loglinear_cache_fork(cache, src, dst, pos, stream=None):
     """Slot dst[i] becomes a copy of slot src[i], which holds pos[i] positions (int32 [n] each):
     pages are shared, the block's tokens copied."""
-    n = cache._rows(src=src, dst=dst, pos=pos)
-    st = _lib.loglinear_cache_fork(cache._ref, _ptr(src), _ptr(dst), _ptr(pos), n, _stream(stream))
+    dev, n = cache._dev(), src.numel()
+    st = _lib.loglinear_cache_fork(
+        cache._ref, _at("src", src, torch.int32, (n,), dev), _at("dst", dst, torch.int32, (n,), dev),
+        _at("pos", pos, torch.int32, (n,), dev), n, _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_fork")
 
 
 def loglinear_cache_free(cache, slots, stream=None):
     """The slots (int32 [n]) give up their pages."""
-    n = cache._rows(slots=slots)
-    st = _lib.loglinear_cache_free(cache._ref, _ptr(slots), n, _stream(stream))
+    dev, n = cache._dev(), slots.numel()
+    st = _lib.loglinear_cache_free(cache._ref, _at("slots", slots, torch.int32, (n,), dev), n,
+                                   _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_free")
 
@@ -778,10 +802,11 @@ def loglinear_cache_free(cache, slots, stream=None):
 def loglinear_cache_compact(cache, live=None, stream=None):
     """Moves pages so that those in use are the lowest.  Returns their number, int32 [1] on the
     device."""
+    dev = cache._dev()
     if live is None:
         live = _empty(stream, 1, device=cache.device, dtype=torch.int32)
-    _here("live", live, torch.int32, (1,))
-    st = _lib.loglinear_cache_compact(cache._ref, _ptr(live), _stream(stream))
+    st = _lib.loglinear_cache_compact(cache._ref, _at("live", live, torch.int32, (1,), dev),
+                                      _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_compact")
     return live
