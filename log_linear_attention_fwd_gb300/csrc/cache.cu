@@ -231,6 +231,45 @@ __global__ void __launch_bounds__(kPlanThreads) cache_load_plan_kernel(ll_cache 
 }
 
 constexpr int kCopyThreads = 256;
+constexpr int kFlight = 8;  // 16-byte loads a thread has on their way: 32 KB per CTA
+
+// dst[i] = f(src[i]) for n float4, by the CTA; src is read once, with kFlight loads in flight.
+template <typename F>
+__device__ __forceinline__ void copy4(float4* dst, const float4* src, int64_t n, F f) {
+  for (int64_t i0 = 0; i0 < n; i0 += kFlight * kCopyThreads) {
+    float4 x[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int64_t i = i0 + u * kCopyThreads + threadIdx.x;
+      if (i < n) x[u] = __ldcs(src + i);
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int64_t i = i0 + u * kCopyThreads + threadIdx.x;
+      if (i < n) __stcs(dst + i, f(x[u]));
+    }
+  }
+}
+
+// rows x width elements to dst (dense, 16-byte aligned) from src (row stride `stride`), by the CTA.
+template <typename T>
+__device__ __forceinline__ void copy_rows(T* dst, const T* src, int64_t stride, int rows, int width) {
+  constexpr int per = 16 / sizeof(T);
+  if (width % per == 0 && stride % per == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+    const int chunks = width / per, n = rows * chunks;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kCopyThreads) {
+      const int r = i / chunks, c = i - r * chunks;
+      reinterpret_cast<uint4*>(dst)[i] = *reinterpret_cast<const uint4*>(src + r * stride + c * per);
+    }
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < rows * width; i += kCopyThreads) {
+      const int r = i / width;
+      dst[i] = src[r * stride + (i - r * width)];
+    }
+  }
+}
 
 struct TokenStrides {
   int64_t k[3], v[3], a[3];  // batch, position, head
@@ -262,27 +301,29 @@ __global__ void __launch_bounds__(kCopyThreads) cache_load_kernel(
     const float4* src = reinterpret_cast<const float4*>(state + (row * H + h) * (int64_t)L * size);
     float4* dst = reinterpret_cast<float4*>(c.pages + ((int64_t)e * H + h) * size);
     const int64_t n4 = size / 4;
-    for (int64_t i = threadIdx.x; i < n4; i += kCopyThreads) {
-      float4 x = __ldcs(src + lo * n4 + i);
-      for (int l = lo + 1; l <= hi; ++l) {
-        const float4 y = __ldcs(src + l * n4 + i);
-        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    if (!sum) {
+      copy4(dst, src + lo * n4, n4, [](float4 x) { return x; });
+    } else {
+      for (int64_t i = threadIdx.x; i < n4; i += kCopyThreads) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int l = lo; l <= hi; ++l) {
+          const float4 y = __ldcs(src + l * n4 + i);
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        __stcs(dst + i, x);
       }
-      dst[i] = x;
     }
     if (threadIdx.x == 0) c.page_log[(((int64_t)s * 2 + par) * M + m) * H + h] = 0.f;
     return;
   }
   if (h == 0 && threadIdx.x == 0) c.page_from[s * 2 + par] = r;
   const int t0 = Tk - r;  // the block's tokens are the last r given
-  T_* wv = static_cast<T_*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
-  for (int i = threadIdx.x; i < r * dv; i += kCopyThreads)
-    wv[i] = v[row * st.v[0] + (t0 + i / dv) * st.v[1] + h * st.v[2] + i % dv];
-  if (h % G == 0) {
-    T_* wk = static_cast<T_*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk;
-    for (int i = threadIdx.x; i < r * dk; i += kCopyThreads)
-      wk[i] = k[row * st.k[0] + (t0 + i / dk) * st.k[1] + (h / G) * st.k[2] + i % dk];
-  }
+  copy_rows(static_cast<T_*>(c.win_v) + ((int64_t)s * H + h) * kW * dv,
+            v + row * st.v[0] + t0 * st.v[1] + h * st.v[2], st.v[1], r, dv);
+  if (h % G == 0)
+    copy_rows(static_cast<T_*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk,
+              k + row * st.k[0] + t0 * st.k[1] + (h / G) * st.k[2], st.k[1], r, dk);
   for (int i = threadIdx.x; i < r; i += kCopyThreads)
     c.win_log_a[((int64_t)s * H + h) * kW + i] =
         log_a ? log_a[row * st.a[0] + (t0 + i) * st.a[1] + h * st.a[2]] : 0.f;
@@ -1073,7 +1114,8 @@ template <typename T>
 __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
     ll_cache c, const int* __restrict__ slots, const int* __restrict__ pos,
     float* __restrict__ state, int L) {
-  __shared__ float tok[kW], since_s, es[kW];
+  __shared__ float tok[kW], since_s;
+  __shared__ __align__(16) float ks[kW / 2][128], vs[kW / 2][128];  // a level's tokens, keys decayed
   const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
   const int M = (int)c.levels, tid = threadIdx.x, level = blockIdx.y;
   const int64_t row = blockIdx.x / H;
@@ -1086,32 +1128,16 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
     return;
   }
   const int j = n >> kLogW, r = n & (kW - 1), par = j & 1;
-  if (tid < 32)
-    block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], tok, &since_s);
-  __syncthreads();
   const int64_t size = (int64_t)dk * dv, n4 = size / 4;
   float4* dst = reinterpret_cast<float4*>(state + ((row * H + h) * (int64_t)L + level) * size);
   // a page i is level 7 + i; after a whole block the lowest one holds the sum of the levels that
   // the next step merges, and stands in the highest of them
   const int low = r == 0 && j ? __ffs(j) - 1 : -1;
   const int m = low >= 0 && level == kLogW + low ? low : level - kLogW - 1;
-  if (m >= 0 && m < M && (j >> m & 1) && !(m == low && level != kLogW + low)) {
-    const int e = c.page_table[(int64_t)s * M + m];
-    if (e < 0 || e >= c.n_pages) {
-      if (tid == 0) raise(c, LL_CACHE_ERR_MISSING);
-      return;
-    }
-    const float f = expf(c.page_log[(((int64_t)s * 2 + par) * M + m) * H + h] + since_s);
-    const float4* src = reinterpret_cast<const float4*>(c.pages + ((int64_t)e * H + h) * size);
-    for (int64_t i = tid; i < n4; i += kCopyThreads) {
-      const float4 x = __ldcs(src + i);
-      __stcs(dst + i, make_float4(f * x.x, f * x.y, f * x.z, f * x.w));
-    }
-    return;
-  }
-  // tokens lo .. hi - 1 of the block, as seen from its last one
+  const bool page = m >= 0 && m < M && (j >> m & 1) && !(m == low && level != kLogW + low);
+  // else tokens lo .. hi - 1 of the block, as seen from its last one
   int lo = 0, hi = 0;
-  if (r > 0 && level <= kLogW) {
+  if (!page && r > 0 && level <= kLogW) {
     const int last = r - 1;
     if (level == 0) {
       lo = last;
@@ -1121,16 +1147,57 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
       hi = lo + (1 << (level - 1));
     }
   }
-  for (int i = lo + tid; i < hi; i += kCopyThreads) es[i] = expf(tok[i]);
+  if (!page && lo == hi) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t i = tid; i < n4; i += kCopyThreads) __stcs(dst + i, zero);
+    return;
+  }
+  const int e = page ? c.page_table[(int64_t)s * M + m] : 0;
+  const float log = page ? c.page_log[(((int64_t)s * 2 + par) * M + m) * H + h] : 0.f;
+  if (tid < 32)
+    block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], tok, &since_s);
   __syncthreads();
-  const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk;
-  const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
-  for (int64_t i = tid; i < n4; i += kCopyThreads) {
-    const int d = (int)(4 * i / dv), col = (int)(4 * i - (int64_t)d * dv);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int u = lo; u < hi; ++u)
-      x = fma4(es[u] * to_f32(wk[u * dk + d]), load4(wv + u * dv + col), x);
-    __stcs(dst + i, x);
+  if (page) {
+    if (e < 0 || e >= c.n_pages) {
+      if (tid == 0) raise(c, LL_CACHE_ERR_MISSING);
+      return;
+    }
+    const float f = expf(log + since_s);
+    const float4* src = reinterpret_cast<const float4*>(c.pages + ((int64_t)e * H + h) * size);
+    copy4(dst, src, n4, [f](float4 x) { return make_float4(f * x.x, f * x.y, f * x.z, f * x.w); });
+    return;
+  }
+  const T* wk = static_cast<const T*>(c.win_k) + (((int64_t)s * c.Hqk + h / G) * kW + lo) * dk;
+  const T* wv = static_cast<const T*>(c.win_v) + (((int64_t)s * H + h) * kW + lo) * dv;
+  const int n_tok = hi - lo;
+#pragma unroll 4
+  for (int i = tid; i < n_tok * dk; i += kCopyThreads) {
+    const int u = i / dk;
+    ks[u][i - u * dk] = expf(tok[lo + u]) * to_f32(wk[i]);
+  }
+#pragma unroll 4
+  for (int i = tid; i < n_tok * dv; i += kCopyThreads) {
+    const int u = i / dv;
+    vs[u][i - u * dv] = to_f32(wv[i]);
+  }
+  __syncthreads();
+  // four rows of four columns per thread and pass
+  const int groups = dv / 4, lanes = kCopyThreads / groups, col = 4 * (tid % groups);
+  for (int d = 4 * (tid / groups); tid / groups < lanes && d < dk; d += 4 * lanes) {
+    float4 x[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) x[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < n_tok; ++u) {
+      const float4 v4 = *reinterpret_cast<const float4*>(&vs[u][col]);
+      const float4 k4 = *reinterpret_cast<const float4*>(&ks[u][d]);  // (past dk: not stored)
+      x[0] = fma4(k4.x, v4, x[0]);
+      x[1] = fma4(k4.y, v4, x[1]);
+      x[2] = fma4(k4.z, v4, x[2]);
+      x[3] = fma4(k4.w, v4, x[3]);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (d + y < dk) __stcs(dst + ((int64_t)(d + y) * dv + col) / 4, x[y]);
   }
 }
 
@@ -1194,14 +1261,11 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(ll_cache c,
   const int* owner = scratch_of(c).owner;
   if (!owns(c, owner, d, row) || fork_bad(c, owner, s, t)) return;
   const int j = t >> kLogW, r = t & (kW - 1), par = j & 1;
-  const T* fv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
-  T* tv = static_cast<T*>(c.win_v) + ((int64_t)d * H + h) * kW * dv;
-  for (int i = tid; i < r * dv; i += kCopyThreads) tv[i] = fv[i];
-  if (h % G == 0) {
-    const T* fk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk;
-    T* tk = static_cast<T*>(c.win_k) + ((int64_t)d * c.Hqk + h / G) * kW * dk;
-    for (int i = tid; i < r * dk; i += kCopyThreads) tk[i] = fk[i];
-  }
+  copy_rows(static_cast<T*>(c.win_v) + ((int64_t)d * H + h) * kW * dv,
+            static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv, r * dv, 1, r * dv);
+  if (h % G == 0)
+    copy_rows(static_cast<T*>(c.win_k) + ((int64_t)d * c.Hqk + h / G) * kW * dk,
+              static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk, r * dk, 1, r * dk);
   for (int i = tid; i < r; i += kCopyThreads)
     c.win_log_a[((int64_t)d * H + h) * kW + i] = c.win_log_a[((int64_t)s * H + h) * kW + i];
   for (int m = tid; m < M; m += kCopyThreads)
@@ -1254,7 +1318,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(ll_cac
   }
 }
 
-constexpr int kMoveChunk = 16 * kCopyThreads;  // floats a CTA moves at a time
+constexpr int kMoveChunk = 4 * kFlight * kCopyThreads;  // floats a CTA moves at a time
 
 __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
   const Scratch sc = scratch_of(c);
@@ -1264,17 +1328,8 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
     const int64_t i = it / chunks, o = (it - i * chunks) * kMoveChunk;
     const float* f = c.pages + sc.from[i] * size;
     float* t = c.pages + sc.to[i] * size;
-    float4 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t at = o + 4 * (u * kCopyThreads + threadIdx.x);
-      if (at < size) x[u] = __ldcs(reinterpret_cast<const float4*>(f + at));
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t at = o + 4 * (u * kCopyThreads + threadIdx.x);
-      if (at < size) __stcs(reinterpret_cast<float4*>(t + at), x[u]);
-    }
+    copy4(reinterpret_cast<float4*>(t + o), reinterpret_cast<const float4*>(f + o),
+          min((int64_t)kMoveChunk, size - o) / 4, [](float4 x) { return x; });
   }
 }
 
