@@ -393,7 +393,8 @@ LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
  *   N          number of sequences (ignored without cu_seqlens: B)
  *   h0         [N, D] fp32 state before the first token; NULL = zero
  *   out        [B, T, D] out_dtype: h_t
- *   state_out  NULL, or [N, D] fp32: the state after the last token (h0 for an empty sequence)
+ *   state_out  NULL, or [N, D] fp32: the state after the last token (h0 for an empty sequence);
+ *              may be h0 itself
  * State, gates and sums are fp32; out is rounded once.
  * Errors: LL_ERR_INVALID (null pointer, negative size or stride, unknown scale, cu_seqlens with
  * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T > 2^30, B or D or B * ceil(D / 32) above
@@ -415,7 +416,8 @@ LL_API int loglinear_glr_fwd(const void* x, const ll_strides* x_strides, const v
  * derivative, which is infinite, is taken as 0.
  *   h, dout, dx   [B, T, D] grad_dtype, dense;  dlog_a [B, T, D] gate_dtype, dense
  *   x             may be NULL with LL_GLR_NONE, whose gradients do not read it
- *   dstate, dh0   [N, D] fp32 or NULL (dh0 of an empty sequence is its dstate, or zero)
+ *   dstate, dh0   [N, D] fp32 or NULL (dh0 of an empty sequence is its dstate, or zero); may be
+ *                 the same array
  * x, log_a, h0, cu_seqlens, N, sizes and errors as loglinear_glr_fwd.
  */
 LL_API int loglinear_glr_bwd(const void* x, const ll_strides* x_strides, const void* log_a,
@@ -481,7 +483,8 @@ typedef struct {
 #define LL_CACHE_ERR_SLOT 1u      /* slot out of range (other than -1), or given to an earlier row */
 #define LL_CACHE_ERR_POSITION 2u  /* position outside the cache */
 #define LL_CACHE_ERR_PAGES 4u     /* no free page was left (the slot is left without it) */
-#define LL_CACHE_ERR_MISSING 8u   /* a page that the position needs is not there */
+#define LL_CACHE_ERR_MISSING 8u   /* a page that the position needs is not there, or the page that
+                                     a step would fold into is shared (not reserved) */
 #define LL_CACHE_ERR_WAIT 16u     /* a wait inside loglinear_cache_step ran out of time; the rows'
                                      results are not valid */
 
@@ -500,8 +503,8 @@ LL_API int loglinear_cache_scratch_size(int64_t slots, int64_t n_pages, size_t* 
 /*
  * The page reservation that goes before a step at the same positions: each slot gives up the
  * pages that are no longer live at pos and, where pos is a block's last position, takes the
- * page that the block is folded into.  May be left out when no row is at a block's first or
- * last position; may be repeated.
+ * page that the block is folded into.  Needed at a block's last position; at other positions it
+ * only gives pages back to the pool (at a block's first one).  May be repeated.
  */
 LL_API int loglinear_cache_reserve(const ll_cache* cache, const int32_t* slots,
                                    const int32_t* pos, int64_t n, ll_stream_t stream);

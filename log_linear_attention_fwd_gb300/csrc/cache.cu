@@ -142,12 +142,23 @@ __device__ void take_pages(const ll_cache& c, const int* want, int count) {
 // ---------------------------------------------------------------- reserve, free
 
 // reserve (pos given): each slot keeps the pages that are live at its position and, at a
-// block's last position, has the page its fold goes to.  free (pos null): no page is kept.
+// block's last position, has the page its fold goes to.  That page is the slot's alone: one that is
+// left over from earlier positions and shared is given up like the others.  free (pos null): no
+// page is kept.
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c, const int* slots,
                                                                      const int* pos, int64_t n) {
   const Scratch sc = scratch_of(c);
   const int M = (int)c.levels;
   claim_slots(c, slots, n, sc.owner);
+  if (pos) {  // mark shared pages where folds go to, before any count changes: -2 - page
+    for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
+      const int s = slots[r], t = pos[r];
+      if (!owns(c, sc.owner, s, r) || !position_ok(c, t) || (t & (kW - 1)) != kW - 1) continue;
+      int* e = c.page_table + (int64_t)s * M + __ffs((t >> kLogW) + 1) - 1;
+      if (*e >= 0 && *e < c.n_pages && __ldcg(c.refcount + *e) != 1) *e = -2 - *e;
+    }
+    __syncthreads();
+  }
   for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
     const int64_t r = k / M;
     const int m = (int)(k - r * M), s = slots[r];
@@ -163,8 +174,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
       keep = (j >> m) & 1 || ((t & (kW - 1)) == kW - 1 && m == __ffs(j + 1) - 1);
     }
     int* e = c.page_table + (int64_t)s * M + m;
-    if (!keep && *e >= 0) {
-      drop_page(c, *e);
+    if (*e < -1 || (!keep && *e >= 0)) {
+      drop_page(c, *e < -1 ? -2 - *e : *e);
       *e = -1;
     }
   }
@@ -572,6 +583,8 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
   const int to = r == kW - 1 ? __ffs(j + 1) - 1 : -1;
   const bool here = lane < M && (j >> lane) & 1;
   const int e = here || lane == to ? c.page_table[(int64_t)s * M + lane] : 0;
+  // a fold writes only to a page of the slot's own
+  const bool shared = lane == to && e >= 0 && e < c.n_pages && c.refcount[e] != 1;
   const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
   const float la = a.log_a ? a.log_a[bh] : 0.f;
   const float lam = here ? a.lam[bh * a.L + kLogW + 1 + lane] : 0.f;
@@ -597,7 +610,7 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
     it.slot = s;
     it.pos = t;
   }
-  return __all_sync(0xffffffffu, e >= 0 && e < c.n_pages);
+  return __all_sync(0xffffffffu, e >= 0 && e < c.n_pages && !shared);
 }
 
 constexpr int kPad = 8;  // elements

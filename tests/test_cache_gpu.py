@@ -273,10 +273,10 @@ def test_batches_of_more_items_than_sms(LL, n, H, Hqk, dk, dv, dtype):
     invariants(cache, {int(slots[b]): T[b] + 3 for b in range(n)})
 
 
-def filled(LL, seed=0, n=3, T=(100, 200, 320), spare=12, dtype="f32", M=4):
+def filled(LL, seed=0, n=3, T=(100, 200, 320), spare=12, dtype="f32", M=4, more=80):
     """A cache with n sequences decoded from nothing, and their inputs."""
     H, dk, dv = 2, 16, 8
-    cfg = W.FwdConfig("c", n, H, max(T) + 80, dk, dv, 16, M + 7, dtype, True, "softplus", seed=seed)
+    cfg = W.FwdConfig("c", n, H, max(T) + more, dk, dv, 16, M + 7, dtype, True, "softplus", seed=seed)
     x = W.make_fwd_inputs(cfg)
     cache = poison(LL.LogLinearCache.empty(8, 3 * n + spare, H, dk, dv, M, dtype=DT[dtype]))
     for i in range(n):
@@ -337,6 +337,32 @@ def test_fork(LL):
     invariants(cache, {7: T[2] + 70, 6: T[1] + 70, 0: T[0]})
     LL.loglinear_cache_free(cache, i32([0, 1, 6, 7]))
     assert int(cache.refcount.sum()) == 0 and torch.all(cache.page_table == -1)
+    assert cache.error() == 0
+
+
+def test_a_fold_never_writes_a_shared_page(LL):
+    """Pages left over from earlier positions (no reservation at the blocks' first positions) may
+    still be a fork's live ones: the reservation at the block's end replaces them, and a step
+    without it is refused."""
+    cache, x, _ = filled(LL, n=1, T=(64 + 10,), more=160)  # page of level 0 is live in slot 0
+    LL.loglinear_cache_fork(cache, i32([0, 0]), i32([3, 4]), i32([74, 74]))
+    want = oracle.forward_direct(x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+    pos = 74
+    one = {k: v[:1] for k, v in x.items()}
+    while pos < 191:                                       # slots 0 and 4 go on; slot 3 stays at 74
+        got, (pos, _) = decode(LL, cache, {k: torch.cat([v, v]) for k, v in one.items()}, [0, 4], [pos, pos], 1,
+                               reserve=pos in (127,))
+        check(got[:, 0].cpu(), want[[0, 0], pos - 1])
+    assert cache.error() == 0 and (cache.page_table[[0, 3, 4], 0] == cache.page_table[0, 0]).all()
+    snap = snapshot(cache)
+    d = token(one, [0], [191])                             # position 191 folds into level 0
+    LL.loglinear_cache_step(cache, i32([0]), i32([191]), d["q"], d["k"], d["v"], d["log_a"], d["lam"])
+    assert cache.error() == LL.CACHE_ERR_MISSING and same(snap, snapshot(cache))
+    got, _ = decode(LL, cache, {k: torch.cat([v, v]) for k, v in one.items()}, [0, 4], [191, 191], 40)
+    check(got.cpu(), want[[0, 0], 191:231])
+    invariants(cache, {0: 231, 4: 231, 3: 74})
+    got, _ = decode(LL, cache, one, [3], [74], 40)         # and the fork that stayed is whole
+    check(got.cpu(), want[:1, 74:114])
     assert cache.error() == 0
 
 

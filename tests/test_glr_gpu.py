@@ -293,6 +293,17 @@ def test_step_bad_slots(LL):
     assert LL.device_error() == 0
 
 
+@pytest.mark.parametrize("T", [1, 700, 9000])
+def test_states_in_place(LL, T):
+    """The last states may go where the first ones are, and likewise their gradients."""
+    x, la = dev(*make(2, T, 70, seed=T))
+    h0 = torch.randn(2, 70, generator=torch.Generator().manual_seed(1)).cuda()
+    state, both = torch.empty_like(h0), h0.clone()
+    a = LL.loglinear_glr_fwd(x, la, h0=h0, state=state, scale="sqrt")
+    b = LL.loglinear_glr_fwd(x, la, h0=both, state=both, scale="sqrt")
+    assert torch.equal(a, b) and torch.equal(state, both)
+
+
 def test_side_stream_and_graph(LL):
     x, la = dev(*make(2, 700, 96, "bf16", "f32", seed=12))
     want = LL.loglinear_glr_fwd(x, la, scale="sqrt")
