@@ -50,6 +50,32 @@ __host__ __device__ Scratch scratch_of(const ll_cache& c) {
   return s;
 }
 
+// The page operators are a small kernel that settles the tables and a large one that follows it;
+// the second is launched while the first runs (programmatic dependent launch), and waits for
+// its end before it touches memory: that hides the launch, 1 to 2 us.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_following(bool early, void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                             int cluster, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = early;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 __device__ __forceinline__ void raise(const ll_cache& c, unsigned bits) {
   atomicOr(c.error, bits);
 }
@@ -147,30 +173,62 @@ __device__ void take_pages(const ll_cache& c, const int* want, int count) {
 // page is kept.
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c, const int* slots,
                                                                      const int* pos, int64_t n) {
+  __shared__ int slot_s[kPlanThreads], pos_s[kPlanThreads];
   const Scratch sc = scratch_of(c);
-  const int M = (int)c.levels;
-  claim_slots(c, slots, n, sc.owner);
-  if (pos) {  // mark shared pages where folds go to, before any count changes: -2 - page
-    for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-      const int s = slots[r], t = pos[r];
-      if (!owns(c, sc.owner, s, r) || !position_ok(c, t) || (t & (kW - 1)) != kW - 1) continue;
+  const int M = (int)c.levels, tid = threadIdx.x;
+  let_next_start();
+  // the rows in shared memory, -1 for those that are left out; one at a time per thread where
+  // they fit, else their owners go through global memory
+  const bool few = n <= kPlanThreads;
+  if (few) {
+    const int s = tid < n ? slots[tid] : -1, t = tid < n && pos ? pos[tid] : 0;
+    slot_s[tid] = s;
+    __syncthreads();
+    bool bad = s < -1 || s >= c.slots;
+    if (s >= 0)
+      for (int i = 0; i < tid; ++i) bad |= slot_s[i] == s;
+    if (bad) raise(c, LL_CACHE_ERR_SLOT);
+    bool in = s >= 0 && !bad;
+    if (in && pos && !position_ok(c, t)) {
+      raise(c, LL_CACHE_ERR_POSITION);
+      in = false;
+    }
+    __syncthreads();
+    slot_s[tid] = in ? s : -1;
+    pos_s[tid] = t;
+  } else {
+    claim_slots(c, slots, n, sc.owner);
+    for (int64_t r = tid; pos && r < n; r += kPlanThreads)
+      if (owns(c, sc.owner, slots[r], r) && !position_ok(c, pos[r])) raise(c, LL_CACHE_ERR_POSITION);
+  }
+  auto slot_of = [&](int64_t r) {
+    if (few) return slot_s[r];
+    const int s = slots[r];
+    return owns(c, sc.owner, s, r) && (!pos || position_ok(c, pos[r])) ? s : -1;
+  };
+  auto pos_of = [&](int64_t r) { return few ? pos_s[r] : pos[r]; };
+  __syncthreads();
+  bool folds = false;
+  if (pos) {
+    for (int64_t r = tid; r < n; r += kPlanThreads) folds |= slot_of(r) >= 0 && (pos_of(r) & (kW - 1)) == kW - 1;
+    folds = __syncthreads_or(folds);
+  }
+  if (folds) {  // mark shared pages where folds go to, before any count changes: -2 - page
+    for (int64_t r = tid; r < n; r += kPlanThreads) {
+      const int s = slot_of(r), t = pos_of(r);
+      if (s < 0 || (t & (kW - 1)) != kW - 1) continue;
       int* e = c.page_table + (int64_t)s * M + __ffs((t >> kLogW) + 1) - 1;
       if (*e >= 0 && *e < c.n_pages && __ldcg(c.refcount + *e) != 1) *e = -2 - *e;
     }
     __syncthreads();
   }
-  for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
+  for (int64_t k = tid; k < n * M; k += kPlanThreads) {
     const int64_t r = k / M;
-    const int m = (int)(k - r * M), s = slots[r];
-    if (!owns(c, sc.owner, s, r)) continue;
+    const int m = (int)(k - r * M), s = slot_of(r);
+    if (s < 0) continue;
     bool keep = false;
     if (pos) {
-      const int t = pos[r];
-      if (!position_ok(c, t)) {
-        if (m == 0) raise(c, LL_CACHE_ERR_POSITION);
-        continue;
-      }
-      const int j = t >> kLogW;
+      const int t = pos_of(r), j = t >> kLogW;
       keep = (j >> m) & 1 || ((t & (kW - 1)) == kW - 1 && m == __ffs(j + 1) - 1);
     }
     int* e = c.page_table + (int64_t)s * M + m;
@@ -179,15 +237,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
       *e = -1;
     }
   }
-  if (!pos) return;
+  if (!folds) return;
   __syncthreads();
   int count = 0;
   for (int64_t base = 0; base < n; base += kPlanThreads) {
-    const int64_t r = base + threadIdx.x;
+    const int64_t r = base + tid;
     int at = -1;
-    if (r < n && owns(c, sc.owner, slots[r], r) && position_ok(c, pos[r]) &&
-        (pos[r] & (kW - 1)) == kW - 1) {
-      const int64_t e = (int64_t)slots[r] * M + __ffs((pos[r] >> kLogW) + 1) - 1;
+    if (r < n && slot_of(r) >= 0 && (pos_of(r) & (kW - 1)) == kW - 1) {
+      const int64_t e = (int64_t)slot_of(r) * M + __ffs((pos_of(r) >> kLogW) + 1) - 1;
       if (c.page_table[e] < 0) at = (int)e;
     }
     int total;
@@ -197,7 +254,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
   }
   if (count == 0) return;
   __syncthreads();
-  if (count > c.n_pages && threadIdx.x == 0) raise(c, LL_CACHE_ERR_PAGES);
+  if (count > c.n_pages && tid == 0) raise(c, LL_CACHE_ERR_PAGES);
   take_pages(c, sc.from, (int)min((int64_t)count, c.n_pages));
 }
 
@@ -209,6 +266,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_load_plan_kernel(ll_cache 
                                                                        int64_t n, int64_t T) {
   const Scratch sc = scratch_of(c);
   const int M = (int)c.levels, j = (int)(T >> kLogW), per = __popc(j);
+  let_next_start();
   claim_slots(c, slots, n, sc.owner);
   for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
     const int64_t r = k / M;
@@ -296,6 +354,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_load_kernel(
     TokenStrides st) {
   const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
   const int64_t row = blockIdx.x / H;
+  wait_for_previous();
   const int h = (int)(blockIdx.x - row * H), s = slots[row];
   if (!owns(c, scratch_of(c).owner, s, row)) return;
   const int j = T >> kLogW, r = T & (kW - 1), par = j & 1;
@@ -759,6 +818,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
     }
     tc::fence_mbar_init();
   }
+  wait_for_previous();
   // the block's tokens [b0, b1): whole rows from a multiple of 8 rows on, so 16-byte aligned; the
   // length is rounded up to 16 bytes, still inside the window.  Without tokens the barrier takes
   // an empty phase.
@@ -1228,6 +1288,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ll_cache 
                                                                        const int* pos, int64_t n) {
   const Scratch sc = scratch_of(c);
   const int M = (int)c.levels;
+  let_next_start();
   for (int64_t r = threadIdx.x; r < n; r += kPlanThreads)
     if (src[r] >= 0 && src[r] < c.slots) sc.owner[src[r]] = kNone;
   __syncthreads();
@@ -1270,6 +1331,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(ll_cache c,
   const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
   const int M = (int)c.levels, tid = threadIdx.x;
   const int64_t row = blockIdx.x / H;
+  wait_for_previous();
   const int h = (int)(blockIdx.x - row * H), s = src[row], d = dst[row], t = pos[row];
   const int* owner = scratch_of(c).owner;
   if (!owns(c, owner, d, row) || fork_bad(c, owner, s, t)) return;
@@ -1294,6 +1356,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(ll_cache c,
 // above it; tables and counts follow here, the pages in cache_move_kernel.
 __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(ll_cache c, int* n_live) {
   const Scratch sc = scratch_of(c);
+  let_next_start();
   int live = 0;
   for (int64_t base = 0; base < c.n_pages; base += kPlanThreads) {
     const int64_t p = base + threadIdx.x;
@@ -1335,6 +1398,7 @@ constexpr int kMoveChunk = 4 * kFlight * kCopyThreads;  // floats a CTA moves at
 
 __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
   const Scratch sc = scratch_of(c);
+  wait_for_previous();
   const int64_t size = c.H * c.dk * c.dv, chunks = (size + kMoveChunk - 1) / kMoveChunk;
   const int64_t items = *sc.count * chunks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -1378,19 +1442,10 @@ cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.n * c.H * a.split));
-  cfg.blockDim = dim3(kQueue ? kQueueThreads : kSplitThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = a.split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = a.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, c, a);
+  // early only in the split form (8.3 -> 7.5 us with the reservation): in the queue's, CTAs that
+  // find the reservation's still on their SM cost more than the launch (101 -> 104 us)
+  return launch_following(!kQueue, kernel, dim3((unsigned)((int64_t)a.n * c.H * a.split)),
+                          kQueue ? kQueueThreads : kSplitThreads, smem, a.split, s, c, a);
 }
 
 // The queue where there is an item for every SM, the split form below that.
@@ -1434,14 +1489,11 @@ cudaError_t launch_cache_load(const ll_cache& c, const int* slots, int64_t n, in
   for (int x = T >> kLogW; x; x &= x - 1) ++per;
   const dim3 grid((unsigned)(n * c.H), per + 1);
   if (c.dtype == LL_F32)
-    cache_load_kernel<float><<<grid, kCopyThreads, 0, s>>>(
-        c, slots, T, state, L, static_cast<const float*>(k), static_cast<const float*>(v), log_a,
-        Tk, st);
-  else
-    cache_load_kernel<__nv_bfloat16><<<grid, kCopyThreads, 0, s>>>(
-        c, slots, T, state, L, static_cast<const __nv_bfloat16*>(k),
-        static_cast<const __nv_bfloat16*>(v), log_a, Tk, st);
-  return cudaGetLastError();
+    return launch_following(true, cache_load_kernel<float>, grid, kCopyThreads, 0, 1, s, c, slots, T, state, L,
+                            static_cast<const float*>(k), static_cast<const float*>(v), log_a, Tk, st);
+  return launch_following(true, cache_load_kernel<__nv_bfloat16>, grid, kCopyThreads, 0, 1, s, c, slots, T, state,
+                          L, static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+                          log_a, Tk, st);
 }
 
 cudaError_t launch_cache_store(const ll_cache& c, const int* slots, const int* pos, float* state,
@@ -1458,17 +1510,17 @@ cudaError_t launch_cache_fork(const ll_cache& c, const int* src, const int* dst,
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(n * c.H);
-  if (c.dtype == LL_F32) cache_fork_kernel<float><<<grid, kCopyThreads, 0, s>>>(c, src, dst, pos);
-  else cache_fork_kernel<__nv_bfloat16><<<grid, kCopyThreads, 0, s>>>(c, src, dst, pos);
-  return cudaGetLastError();
+  return c.dtype == LL_F32
+             ? launch_following(true, cache_fork_kernel<float>, dim3(grid), kCopyThreads, 0, 1, s, c, src, dst, pos)
+             : launch_following(true, cache_fork_kernel<__nv_bfloat16>, dim3(grid), kCopyThreads, 0, 1, s, c, src,
+                                dst, pos);
 }
 
 cudaError_t launch_cache_compact(const ll_cache& c, int* n_live, cudaStream_t s) {
   cache_compact_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, n_live);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache_move_kernel<<<152 * 4, kCopyThreads, 0, s>>>(c);
-  return cudaGetLastError();
+  return launch_following(true, cache_move_kernel, dim3(152 * 4), kCopyThreads, 0, 1, s, c);
 }
 
 }  // namespace ll
