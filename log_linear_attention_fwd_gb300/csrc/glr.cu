@@ -319,7 +319,8 @@ struct LinkSmem {
   // the segments' maps; then entry g: that of segments 0 .. g, and the last: the carry into the tile
   float2 seg[kSegs][kCh];
   float2 tile[2][kMaxCluster - 1][kCh];  // the other tiles' maps, of even and odd steps
-  uint64_t bar[2];                       // they are there
+  Span span[kSegs];                      // the segments' sequences
+  uint64_t bar[2];                       // the maps are there
 };
 
 // Before the first step; ends with a barrier over the cluster.
@@ -335,14 +336,18 @@ __device__ __forceinline__ void link_init(LinkSmem& sm, int Z) {
 }
 
 // After the segments' maps of step k are in sm.seg: folds them, and moves `c` (warp 0, a channel
-// per lane: the carry into the step) on to the next step.  Starts and ends with a block barrier.
+// per lane: the carry into the step) on to the next step.  Meanwhile warp 1 looks up the sequences
+// of the next step's segments, spans(g): dependent loads of up to 2 us for packed sequences.
+// Starts and ends with a block barrier.
 //
 // A CTA sends its map of step k + 1 after it has read the maps of step k, and has those of step
 // k + 1 before it sends that of step k + 2: two buffers are enough.  It leaves the last step
 // only with every map that is sent to it in place.
-__device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, float& c) {
+template <typename F>
+__device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, float& c, F spans) {
   const int tid = threadIdx.x;
   __syncthreads();
+  if (tid >= 32 && tid < 32 + kSegs) sm.span[tid - 32] = spans(tid - 32);
   if (tid < kCh) {
     if (Z > 1 && tid == 0)
       tc::mbar_arrive_expect_tx(&sm.bar[k & 1], (Z - 1) * kCh * sizeof(float2));
@@ -421,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
   const bool live = ch < p.D;
   const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
   const int cols = min(kCh, p.D - blk * kCh);
-  const bool whole = geo.pairs && cols == kCh;
   const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + blk * kCh;
   const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + blk * kCh;
   OutT* out = static_cast<OutT*>(p.out) + (int64_t)b * p.T * p.D + ch;
@@ -439,6 +443,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
   for (int k = 0; k < kFwdStages - 1; ++k) issue(k);
   if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
   link_init(sm, Z);
+  auto spans = [&](int k, int g) { return span_of<S>(p.cu, p.N, p.T, b, (k * Z + rank) * kRows + g * S); };
+  if (threadIdx.x < kSegs) sm.span[threadIdx.x] = spans(0, threadIdx.x);
   float c = 0.f;
   for (int k = 0; k < steps; ++k) {
     cp_async_wait<kFwdStages - 2>();
@@ -446,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     issue(k + kFwdStages - 1);
     const Stage& st = stages[k % kFwdStages];
     const int lo = (k * Z + rank) * kRows + seg * S;
-    const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
+    const Span span = sm.span[seg];
     f32x2 a[S], u[S], A = both(1.f), H = both(0.f);
-    // plain: every token and channel is there, and no sequence begins or ends
-    const bool plain = __all_sync(0xffffffffu, whole && span.on == (1u << S) - 1u && !(span.first | span.last));
+    // plain: every token is there, no sequence begins or ends, and pairs go out as pairs
+    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u && !(span.first | span.last));
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       f32x2 m;
@@ -466,43 +472,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
       int n = span.n0;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        if (!(span.on >> s & 1)) {
-          a[s] = both(1.f);
-          u[s] = both(0.f);
+        const bool on = span.on >> s & 1, first = span.first >> s & 1;
+        u[s] = on ? u[s] : both(0.f);
+        a[s] = on ? a[s] : both(1.f);
+        if (p.h0) {
+          if (first && live) u[s] = fma2(a[s], to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how)), u[s]);
+          if (span.last >> s & 1) n = next_sequence(p.cu, p.N, n);
         }
-        if (span.first >> s & 1) {
-          if (p.h0 && live) u[s] = fma2(a[s], to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how)), u[s]);
-          a[s] = A = both(-0.f);
-          H = both(0.f);
-        } else {
-          A = mul2(A, a[s]);
-        }
-        if (span.last >> s & 1) n = next_sequence(p.cu, p.N, n);
-        H = fma2(a[s], H, u[s]);
+        a[s] = first ? both(-0.f) : a[s];
+        A = first ? both(-0.f) : mul2(A, a[s]);
+        H = fma2(a[s], first ? both(0.f) : H, u[s]);
       }
     }
     const float2 A1 = unpack(A), H1 = unpack(H);
     *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, H1.x, A1.y, H1.y);
-    link_step(sm, k, Z, rank, c);
+    link_step(sm, k, Z, rank, c, [&](int g) { return spans(k + 1, g); });
     f32x2 h = segment_carry(sm, seg, cl);
     OutT* o = out + (int64_t)lo * p.D;
     if (plain) {
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         h = fma2(a[s], h, u[s]);
-        put_pair(o, unpack(h));
+        if (live) put_pair(o, unpack(h));
         o += p.D;
       }
     } else {
       int n = span.n0;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        if (span.first >> s & 1) h = both(0.f);  // a is -0 there: h = u
-        h = fma2(a[s], h, u[s]);
+        h = fma2(a[s], span.first >> s & 1 ? both(0.f) : h, u[s]);  // (a is -0 there: h = u)
         if (live && (span.on >> s & 1)) store_pair(o, unpack(h), how);
         o += p.D;
-        if (span.last >> s & 1) {
-          if (live && p.state) store_pair(p.state + (int64_t)n * p.D + ch, unpack(h), how);
+        if (p.state && (span.last >> s & 1)) {
+          if (live) store_pair(p.state + (int64_t)n * p.D + ch, unpack(h), how);
           n = next_sequence(p.cu, p.N, n);
         }
       }
@@ -550,7 +552,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
   const bool live = ch < p.D;
   const int how = ch + 1 >= p.D ? kFirst : geo.pairs ? kPairs : kSingles;
   const int cols = min(kCh, p.D - blk * kCh);
-  const bool whole = geo.pairs && cols == kCh;
   const InT* x = static_cast<const InT*>(p.x) + b * p.sx[0] + blk * kCh;
   const GateT* la = static_cast<const GateT*>(p.log_a) + b * p.sl[0] + blk * kCh;
   const int64_t base = (int64_t)b * p.T * p.D + blk * kCh;
@@ -577,6 +578,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
   for (int k = 0; k < kBwdStages - 1; ++k) issue(k);
   if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
   link_init(sm, Z);
+  auto spans = [&](int k, int g) {
+    return span_of<S>(p.cu, p.N, p.T, b, k < steps ? tile_start(k) + (kSegs - 1 - g) * S : p.T);
+  };
+  if (threadIdx.x < kSegs) sm.span[threadIdx.x] = spans(0, threadIdx.x);
   float carry = 0.f;
   for (int k = 0; k < steps; ++k) {
     cp_async_wait<kBwdStages - 2>();
@@ -584,15 +589,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     issue(k + kBwdStages - 1);
     const Stage& st = stages[k % kBwdStages];
     const int back = kSegs - 1 - seg, lo = tile_start(k) + back * S;
-    const Span span = span_of<S>(p.cu, p.N, p.T, b, lo);
+    const Span span = sm.span[seg];
     int n_last = span.n0;  // the sequence of the last token that is on
-    if (p.cu) {
+    if (p.cu && (p.dstate || p.h0 || p.dh0)) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
         if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
     }
     f32x2 a[S], bs[S], d[S], A = both(1.f), E = both(0.f);
-    const bool plain = __all_sync(0xffffffffu, whole && span.on == (1u << S) - 1u && !(span.first | span.last));
+    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u && !(span.first | span.last));
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
       f32x2 m;
@@ -610,23 +615,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
       int n = n_last;
 #pragma unroll
       for (int s = S - 1; s >= 0; --s) {
-        if (!(span.on >> s & 1)) {
-          a[s] = both(1.f);
-          d[s] = both(0.f);
+        const bool on = span.on >> s & 1, last = span.last >> s & 1;
+        a[s] = on ? a[s] : both(1.f);
+        d[s] = on ? d[s] : both(0.f);
+        if (p.dstate) {
+          if (last && live) d[s] = add2(d[s], to_pair(load_state(p.dstate + (int64_t)n * p.D + ch, how)));
+          if (span.first >> s & 1) n = previous_sequence(p.cu, n);
         }
-        A = mul2(A, a[s]);
-        if (span.last >> s & 1) {
-          if (p.dstate && live) d[s] = add2(d[s], to_pair(load_state(p.dstate + (int64_t)n * p.D + ch, how)));
-          E = both(0.f);  // nothing comes from the sequence behind
-          A = both(-0.f);
-        }
-        E = mul2(a[s], add2(d[s], E));
-        if (span.first >> s & 1) n = previous_sequence(p.cu, n);
+        A = last ? both(-0.f) : mul2(A, a[s]);  // nothing comes from the sequence behind
+        E = mul2(a[s], last ? d[s] : add2(d[s], E));
       }
     }
     const float2 A1 = unpack(A), E1 = unpack(E);
     *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, E1.x, A1.y, E1.y);
-    link_step(sm, k, Z, rank, carry);
+    link_step(sm, k, Z, rank, carry, [&](int g) { return spans(k + 1, g); });
     f32x2 c = segment_carry(sm, seg, cl);
     GradT* ox = dx + (int64_t)(lo + S - 1) * p.D;
     GateT* ol = dla + (int64_t)(lo + S - 1) * p.D;
@@ -638,8 +640,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
         f32x2 l = mul2(c, to_pair(st.h.pair(back, s, cl)));
         if constexpr (kX)
           l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(st.x.pair(back, s, cl))), g, l);
-        put_pair(ox, unpack(mul2(bs[s], g)));
-        put_pair(ol, unpack(l));
+        if (live) {
+          put_pair(ox, unpack(mul2(bs[s], g)));
+          put_pair(ol, unpack(l));
+        }
         ox -= p.D;
         ol -= p.D;
       }
@@ -647,23 +651,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
       int n = n_last;
 #pragma unroll
       for (int s = S - 1; s >= 0; --s, ox -= p.D, ol -= p.D) {
-        if (!live || !(span.on >> s & 1)) continue;
-        if (span.last >> s & 1) c = both(0.f);
-        const f32x2 g = add2(d[s], c);
-        f32x2 before = both(0.f);
-        if (!(span.first >> s & 1)) {
-          if (lo + s > 0) before = to_pair(st.h.pair(back, s, cl));
-        } else if (p.h0) {
-          before = to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how));
-        }
-        c = mul2(a[s], g);
+        const bool on = span.on >> s & 1, first = span.first >> s & 1;
+        const f32x2 g = span.last >> s & 1 ? d[s] : add2(d[s], c);
+        f32x2 before = first || lo + s == 0 ? both(0.f) : to_pair(st.h.pair(back, s, cl));
+        if (p.h0 && first && live) before = to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how));
+        c = on ? mul2(a[s], g) : c;
         f32x2 l = mul2(c, before);
         if constexpr (kX)
           l = fma2(mul2(scale_grad<kScale>(a[s], bs[s]), to_pair(st.x.pair(back, s, cl))), g, l);
-        store_pair(ox, unpack(mul2(bs[s], g)), how);
-        store_pair(ol, unpack(l), how);
-        if (span.first >> s & 1) {
-          if (p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, unpack(c), how);
+        if (live && on) {
+          store_pair(ox, unpack(mul2(bs[s], g)), how);
+          store_pair(ol, unpack(l), how);
+        }
+        if (first && (p.h0 || p.dh0)) {
+          if (live && p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, unpack(c), how);
           n = previous_sequence(p.cu, n);
         }
       }
