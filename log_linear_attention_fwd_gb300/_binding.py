@@ -519,6 +519,14 @@ def _at(name, t, dtype, shape, dev):
     raise ValueError(f"{name} is not as expected")
 
 
+def _current_device_of(name, t):
+    """The current device, which has to be t's."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
+    return dev
+
+
 def _raw_stream(stream, dev):
     """The stream's handle (None: the current one)."""
     if stream is None:
@@ -559,8 +567,16 @@ def _glr_sequences(cu_seqlens, B):
         return B
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must have shape [N + 1]")
-    _here("cu_seqlens", cu_seqlens, torch.int32)
     return cu_seqlens.numel() - 1
+
+
+def _glr_input(name, t, shape, dev):
+    """Address and strides (None: dense) of an input."""
+    if t is None:
+        return None, None
+    if t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), None
+    return t.data_ptr(), _token_strides(name, t, shape)
 
 
 def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None, out_dtype=None,
@@ -570,19 +586,19 @@ def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None
     ("none"), 1 - a ("one_minus") or sqrt(1 - a^2) ("sqrt").  cu_seqlens int32 [N+1] packs N
     sequences into B = 1.  h0, state: [N,D] fp32 first states and, when given, where the last
     ones go.  Returns out [B,T,D]."""
-    B, T, D = x.shape
-    xs = _token_strides("x", x, (B, T, D))
-    ls = _token_strides("log_a", log_a, (B, T, D))
+    shape = B, T, D = x.shape
+    dev = _current_device_of("x", x)
+    xp, xs = _glr_input("x", x, shape, dev)
+    lp, ls = _glr_input("log_a", log_a, shape, dev)
     N = _glr_sequences(cu_seqlens, B)
-    _here("h0", h0, torch.float32, (N, D))
-    _here("state", state, torch.float32, (N, D))
     if out is None:
         out = _empty(stream, B, T, D, device=x.device, dtype=out_dtype or x.dtype)
-    _here("out", out, shape=(B, T, D))
-    st = _lib.loglinear_glr_fwd(x.data_ptr(), xs, log_a.data_ptr(), ls, _ptr(h0),
-                                _ptr(cu_seqlens), N, out.data_ptr(), _ptr(state), B, T, D,
-                                _dtype_code(x), _dtype_code(log_a), _dtype_code(out),
-                                GLR_SCALES[scale], _raw_stream(stream, out.get_device()))
+    st = _lib.loglinear_glr_fwd(
+        xp, xs, lp, ls, _at("h0", h0, torch.float32, (N, D), dev),
+        _at("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev), N,
+        _at("out", out, out.dtype, shape, dev), _at("state", state, torch.float32, (N, D), dev), B,
+        T, D, _dtype_code(x), _dtype_code(log_a), _dtype_code(out), GLR_SCALES[scale],
+        _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_fwd")
     return out
@@ -593,23 +609,24 @@ def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none
     """Gradients of loglinear_glr_fwd: out is its result, dout (same dtype) the gradient of it,
     dstate [N,D] fp32 that of the last states.  Returns (dx, dlog_a, dh0); dx in dout's dtype,
     dlog_a in log_a's, dh0 fp32 (None without h0).  x may be None with scale "none"."""
-    B, T, D = log_a.shape
-    xs = _token_strides("x", x, (B, T, D))
-    ls = _token_strides("log_a", log_a, (B, T, D))
+    shape = B, T, D = log_a.shape
+    dev = _current_device_of("log_a", log_a)
+    xp, xs = _glr_input("x", x, shape, dev)
+    lp, ls = _glr_input("log_a", log_a, shape, dev)
     N = _glr_sequences(cu_seqlens, B)
-    _here("out", out, shape=(B, T, D))
-    _here("dout", dout, out.dtype, (B, T, D))
-    _here("h0", h0, torch.float32, (N, D))
-    _here("dstate", dstate, torch.float32, (N, D))
+    op = _at("out", out, out.dtype, shape, dev)
+    gp = _at("dout", dout, out.dtype, shape, dev)
+    hp = _at("h0", h0, torch.float32, (N, D), dev)
+    sp = _at("dstate", dstate, torch.float32, (N, D), dev)
+    cp = _at("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
     dx = _empty(stream, B, T, D, device=out.device, dtype=dout.dtype)
     dla = _empty(stream, B, T, D, device=out.device, dtype=log_a.dtype)
     dh0 = None if h0 is None else _empty(stream, N, D, device=out.device, dtype=torch.float32)
     gate = _dtype_code(log_a)
-    st = _lib.loglinear_glr_bwd(_ptr(x), xs, _ptr(log_a), ls, _ptr(h0), _ptr(cu_seqlens), N,
-                                _ptr(out), _ptr(dout), _ptr(dstate), _ptr(dx), _ptr(dla),
-                                _ptr(dh0), B, T, D, gate if x is None else _dtype_code(x), gate,
-                                _dtype_code(out), GLR_SCALES[scale],
-                                _raw_stream(stream, out.get_device()))
+    st = _lib.loglinear_glr_bwd(xp, xs, lp, ls, hp, cp, N, op, gp, sp, dx.data_ptr(),
+                                dla.data_ptr(), None if dh0 is None else dh0.data_ptr(), B, T, D,
+                                gate if x is None else _dtype_code(x), gate, _dtype_code(out),
+                                GLR_SCALES[scale], _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_bwd")
     return dx, dla, dh0
@@ -620,9 +637,7 @@ def loglinear_glr_step(state, x, log_a, slots=None, scale="none", out=None, out_
     """One token of the recurrence per row: state [S,D] fp32 is updated in place at slots (int32
     [B], -1 leaves the row out; None: row b is slot b).  x, log_a [B,D].  Returns out [B,D]."""
     B, D = x.shape
-    dev = x.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"x must be a CUDA tensor on the current device, got {x.device}")
+    dev = _current_device_of("x", x)
     if state.dim() != 2 or state.shape[1] != D:
         raise ValueError(f"state has shape {tuple(state.shape)}, expected (S, {D})")
     if out is None:
