@@ -15,12 +15,13 @@
 // while this one is worked on, and four small CTAs share an SM, so that one folds and waits
 // while the others compute.
 //
-// Z is chosen so that batch entries x channel blocks x Z CTAs fill the GPU (cluster_of).
+// Z is chosen so that batch entries x channel blocks x Z CTAs fill the GPU (launch_cluster).
 // The backward is the same scan with time reversed.
 //
 // A sequence start is a reset: its map ignores the carry.  It is marked by A = -0.0 (a real A
 // is never negative), not by A = 0, because 0 * inf would let an overflow of one sequence
 // reach the next.
+#include <atomic>
 #include <cmath>
 
 #include "ll_internal.cuh"
@@ -38,7 +39,7 @@ constexpr int kThreads = 256;
 constexpr int kCh = 32;                      // channels of a CTA: two per lane
 constexpr int kSegs = kThreads / (kCh / 2);  // segments of a tile
 constexpr int kPerSm = 4;                    // CTAs per SM, shared memory permitting
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 // ---------------------------------------------------------------- pairs of fp32
 
@@ -318,10 +319,12 @@ __device__ __forceinline__ void send(float2* p, uint64_t* bar, uint32_t rank, fl
 struct LinkSmem {
   // the segments' maps; then entry g: that of segments 0 .. g, and the last: the carry into the tile
   float2 seg[kSegs][kCh];
-  float2 tile[2][kMaxCluster - 1][kCh];  // the other tiles' maps, of even and odd steps
-  Span span[kSegs];                      // the segments' sequences
-  uint64_t bar[2];                       // the maps are there
+  Span span[kSegs];  // the segments' sequences
+  uint64_t bar[2];   // the other tiles' maps are there
 };
+// The other tiles' maps, of even and odd steps, behind the stages: one per other CTA.
+typedef float2 TileMaps[2][kCh];
+constexpr size_t maps_bytes(int Z) { return (Z - 1) * sizeof(TileMaps); }
 
 // Before the first step; ends with a barrier over the cluster.
 __device__ __forceinline__ void link_init(LinkSmem& sm, int Z) {
@@ -344,7 +347,8 @@ __device__ __forceinline__ void link_init(LinkSmem& sm, int Z) {
 // k + 1 before it sends that of step k + 2: two buffers are enough.  It leaves the last step
 // only with every map that is sent to it in place.
 template <typename F>
-__device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, float& c, F spans) {
+__device__ __forceinline__ void link_step(LinkSmem& sm, TileMaps* maps, int k, int Z, int rank,
+                                          float& c, F spans) {
   const int tid = threadIdx.x;
   __syncthreads();
   if (tid >= 32 && tid < 32 + kSegs) sm.span[tid - 32] = spans(tid - 32);
@@ -362,11 +366,11 @@ __device__ __forceinline__ void link_step(LinkSmem& sm, int k, int Z, int rank, 
       c = apply(m.x, m.y, c);
     } else {
       for (int z = 0; z < Z; ++z)
-        if (z != rank) send(&sm.tile[k & 1][rank - (rank > z)][tid], &sm.bar[k & 1], z, m);
+        if (z != rank) send(&maps[rank - (rank > z)][k & 1][tid], &sm.bar[k & 1], z, m);
       if (!tc::mbar_wait_short(&sm.bar[k & 1], (k >> 1) & 1)) atomicOr(&g_glr_error, 2u);
       for (int z = 0; z < Z; ++z) {
         if (z == rank) sm.seg[kSegs - 1][tid].x = c;
-        const float2 n = z == rank ? m : sm.tile[k & 1][z - (z > rank)][tid];
+        const float2 n = z == rank ? m : maps[z - (z > rank)][k & 1][tid];
         c = apply(n.x, n.y, c);
       }
     }
@@ -418,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
   using Stage = FwdStage<InT, GateT, S>;
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
+  TileMaps* maps = reinterpret_cast<TileMaps*>(stages + kFwdStages);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
@@ -455,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     const Span span = sm.span[seg];
     f32x2 a[S], u[S], A = both(1.f), H = both(0.f);
     // plain: every token is there, no sequence begins or ends, and pairs go out as pairs
-    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u && !(span.first | span.last));
+    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u &&
+                                                   !(span.first | span.last));
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       f32x2 m;
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     }
     const float2 A1 = unpack(A), H1 = unpack(H);
     *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, H1.x, A1.y, H1.y);
-    link_step(sm, k, Z, rank, c, [&](int g) { return spans(k + 1, g); });
+    link_step(sm, maps, k, Z, rank, c, [&](int g) { return spans(k + 1, g); });
     f32x2 h = segment_carry(sm, seg, cl);
     OutT* o = out + (int64_t)lo * p.D;
     if (plain) {
@@ -544,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
   using Stage = BwdStage<InT, GateT, GradT, S, kX>;
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
+  TileMaps* maps = reinterpret_cast<TileMaps*>(stages + kBwdStages);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
@@ -597,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
         if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
     }
     f32x2 a[S], bs[S], d[S], A = both(1.f), E = both(0.f);
-    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u && !(span.first | span.last));
+    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u &&
+                                                   !(span.first | span.last));
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
       f32x2 m;
@@ -628,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     }
     const float2 A1 = unpack(A), E1 = unpack(E);
     *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, E1.x, A1.y, E1.y);
-    link_step(sm, k, Z, rank, carry, [&](int g) { return spans(k + 1, g); });
+    link_step(sm, maps, k, Z, rank, carry, [&](int g) { return spans(k + 1, g); });
     f32x2 c = segment_carry(sm, seg, cl);
     GradT* ox = dx + (int64_t)(lo + S - 1) * p.D;
     GateT* ol = dla + (int64_t)(lo + S - 1) * p.D;
@@ -739,42 +747,65 @@ int copy_bytes(const void* p, int64_t sb, int64_t st, int64_t D, int size) {
   return size;
 }
 
-// CTAs that share a channel block: doubled while the launch stays within what the SMs hold at
-// once and a step within the sequence.
-int cluster_of(int64_t items, int64_t T, int rows, size_t smem) {
-  const int64_t fit = (int64_t)(233472 / (smem + sizeof(LinkSmem) + 1024));
-  const int64_t slots = 152 * (fit < kPerSm ? fit : kPerSm);
-  int Z = 1;
-  while (Z < kMaxCluster && items * Z * 2 <= slots && (int64_t)Z * rows < T) Z *= 2;
-  return Z;
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  Launch(int64_t items, int Z, size_t stages, cudaStream_t s) {
+    cfg.gridDim = dim3((unsigned)(items * Z));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = stages + maps_bytes(Z);
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = Z;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = Z > 1 ? 1 : 0;
+  }
+};
+
+// How many clusters of Z = 2^i CTAs the GPU holds at once; asked for once per kernel and Z.
+template <auto kKernel>
+cudaError_t clusters_held(int i, size_t stages, int* n) {
+  static std::atomic<int> known[5];
+  *n = known[i].load(std::memory_order_relaxed);
+  if (*n) return cudaSuccess;
+  const Launch l(1, 1 << i, stages, nullptr);
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kKernel, &l.cfg);
+  if (e == cudaSuccess) known[i].store(*n, std::memory_order_relaxed);
+  return e;
 }
 
-template <typename K>
-cudaError_t launch_cluster(K kernel, const GlrArgs& p, const Geometry& g, size_t smem,
+// Z, the CTAs that share a channel block, is doubled while the clusters all run at once and a
+// step stays within the sequence.  Clusters of 16 instead of 8 at the most: 65536 tokens of 512
+// channels 167 -> 123 us forward and 320 -> 232 us backward, 4096 tokens of 256 channels
+// 11.6 -> 9.4 us and 17.3 -> 13.6 us.  Where one cluster has to wait for the others: 2500 tokens
+// of 514 channels, fp32, forward 21 us with Z = 16 (17 clusters, of which 16 run) and 15 with 8.
+template <auto kKernel>
+cudaError_t launch_cluster(const GlrArgs& p, Geometry& g, int rows, size_t stages,
                            cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(stages + maps_bytes(kMaxCluster)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const int64_t items = (int64_t)p.B * g.blocks;
+  g.Z = 1;
+  for (int i = 1; e == cudaSuccess && g.Z < kMaxCluster && (int64_t)g.Z * rows < p.T; ++i) {
+    int held = 0;
+    e = clusters_held<kKernel>(i, stages, &held);
+    if (items > held) break;
+    g.Z *= 2;
+  }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.B * g.blocks * g.Z));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = g.Z;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = g.Z > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p, g);
+  const Launch l(items, g.Z, stages, s);
+  return cudaLaunchKernelEx(&l.cfg, kKernel, p, (const Geometry&)g);
 }
 
 template <typename InT, typename GateT, typename OutT, int kScale>
 cudaError_t launch(const GlrArgs& p, bool backward, cudaStream_t s) {
   Geometry g;
   g.blocks = (p.D + kCh - 1) / kCh;
-  const int64_t dense = (int64_t)p.T * p.D, items = (int64_t)p.B * g.blocks;
+  const int64_t dense = (int64_t)p.T * p.D;
   const size_t o = 2 * sizeof(OutT);
   g.pairs = p.D % 2 == 0 && aligned(p.out, o) && aligned(p.state, 8) && aligned(p.dx, o) &&
             aligned(p.dlog_a, 2 * sizeof(GateT)) && aligned(p.dh0, 8);
@@ -784,14 +815,12 @@ cudaError_t launch(const GlrArgs& p, bool backward, cudaStream_t s) {
   g.dout = copy_bytes(p.dout, dense, p.D, p.D, sizeof(OutT));
   if (backward) {
     constexpr int S = 4;  // the backward keeps three values per token in registers
-    constexpr size_t smem = kBwdStages * sizeof(BwdStage<InT, GateT, OutT, S, kScale != LL_GLR_NONE>);
-    g.Z = cluster_of(items, p.T, kSegs * S, smem);
-    return launch_cluster(glr_bwd_kernel<InT, GateT, OutT, S, kScale>, p, g, smem, s);
+    constexpr size_t stages = kBwdStages * sizeof(BwdStage<InT, GateT, OutT, S, kScale != LL_GLR_NONE>);
+    return launch_cluster<glr_bwd_kernel<InT, GateT, OutT, S, kScale>>(p, g, kSegs * S, stages, s);
   }
   constexpr int S = 8;
-  constexpr size_t smem = kFwdStages * sizeof(FwdStage<InT, GateT, S>);
-  g.Z = cluster_of(items, p.T, kSegs * S, smem);
-  return launch_cluster(glr_fwd_kernel<InT, GateT, OutT, S, kScale>, p, g, smem, s);
+  constexpr size_t stages = kFwdStages * sizeof(FwdStage<InT, GateT, S>);
+  return launch_cluster<glr_fwd_kernel<InT, GateT, OutT, S, kScale>>(p, g, kSegs * S, stages, s);
 }
 
 template <typename InT, typename GateT, typename OutT>
