@@ -764,23 +764,23 @@ struct Launch {
   }
 };
 
-// How many clusters of Z = 2^i CTAs the GPU holds at once; asked for once per kernel and Z.
+// How many clusters of Z CTAs the GPU holds at once; asked for once per kernel and Z.
 template <auto kKernel>
-cudaError_t clusters_held(int i, size_t stages, int* n) {
-  static std::atomic<int> known[5];
-  *n = known[i].load(std::memory_order_relaxed);
+cudaError_t clusters_held(int Z, size_t stages, int* n) {
+  static std::atomic<int> known[kMaxCluster + 1];
+  *n = known[Z].load(std::memory_order_relaxed);
   if (*n) return cudaSuccess;
-  const Launch l(1, 1 << i, stages, nullptr);
+  const Launch l(1, Z, stages, nullptr);
   const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kKernel, &l.cfg);
-  if (e == cudaSuccess) known[i].store(*n, std::memory_order_relaxed);
+  if (e == cudaSuccess) known[Z].store(*n, std::memory_order_relaxed);
   return e;
 }
 
-// Z, the CTAs that share a channel block, is doubled while the clusters all run at once and a
-// step stays within the sequence.  Clusters of 16 instead of 8 at the most: 65536 tokens of 512
-// channels 167 -> 123 us forward and 320 -> 232 us backward, 4096 tokens of 256 channels
-// 11.6 -> 9.4 us and 17.3 -> 13.6 us.  Where one cluster has to wait for the others: 2500 tokens
-// of 514 channels, fp32, forward 21 us with Z = 16 (17 clusters, of which 16 run) and 15 with 8.
+// Z, the CTAs that share a channel block: as many as leave all clusters running at once (at most
+// kMaxCluster), then as few as take no more steps.  Forward and backward: 65536 tokens of 512
+// channels, bf16: 124 and 230 us with Z = 16, 167 and 316 with 8; 9001 of 1000, fp32: 30 and 45
+// with 12, 31 and 49 with 8.  Where a cluster waits for the others: 2500 of 514, fp32, forward 21 us
+// with 16 (17 clusters, of which 14 run), 11 with 10 and 15 with 8.
 template <auto kKernel>
 cudaError_t launch_cluster(const GlrArgs& p, Geometry& g, int rows, size_t stages,
                            cudaStream_t s) {
@@ -789,14 +789,16 @@ cudaError_t launch_cluster(const GlrArgs& p, Geometry& g, int rows, size_t stage
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   const int64_t items = (int64_t)p.B * g.blocks;
-  g.Z = 1;
-  for (int i = 1; e == cudaSuccess && g.Z < kMaxCluster && (int64_t)g.Z * rows < p.T; ++i) {
+  const int tiles = (int)(((int64_t)p.T + rows - 1) / rows);
+  g.Z = tiles < 1 ? 1 : tiles < kMaxCluster ? tiles : kMaxCluster;
+  for (; e == cudaSuccess && g.Z > 1; --g.Z) {
     int held = 0;
-    e = clusters_held<kKernel>(i, stages, &held);
-    if (items > held) break;
-    g.Z *= 2;
+    e = clusters_held<kKernel>(g.Z, stages, &held);
+    if (items <= held) break;
   }
   if (e != cudaSuccess) return e;
+  const int steps = (tiles + g.Z - 1) / g.Z;
+  if (steps > 0) g.Z = (tiles + steps - 1) / steps;
   const Launch l(items, g.Z, stages, s);
   return cudaLaunchKernelEx(&l.cfg, kKernel, p, (const Geometry&)g);
 }
