@@ -15,6 +15,13 @@
 // while this one is worked on, and four small CTAs share an SM, so that one folds and waits
 // while the others compute.
 //
+// What bounds them is issue and the exchange, not HBM: 76 instructions per token and pair of
+// channels, half of them the gate (measured with parts switched off, B8 T2048 D2048 bf16: all 73
+// us, without gates 62, without the exchange 67, neither 57, and 39.6 is HBM's time).  Forward,
+// b = sqrt(1 - a^2), bf16 with fp32 gates, D 2048: T 16384 73 us, 3.7 TB/s; B8 T2048 64; B16 T1024
+// 58, 4.6 TB/s.  Backward: B4 T4096 124 us, 4.3 TB/s.  Packed, 9001 tokens of 1000 channels in
+// fp32: forward 33 us, backward 49.
+//
 // Z is chosen so that batch entries x channel blocks x Z CTAs fill the GPU (launch_cluster).
 // The backward is the same scan with time reversed.
 //
@@ -764,15 +771,16 @@ struct Launch {
   }
 };
 
-// How many clusters of Z CTAs the GPU holds at once; asked for once per kernel and Z.
+// How many clusters of Z CTAs a device holds at once; asked for once per kernel, Z and device (of
+// the first kDevices: the answer takes the runtime longer than the launch).
+constexpr int kDevices = 16;
 template <auto kKernel>
-cudaError_t clusters_held(int Z, size_t stages, int* n) {
-  static std::atomic<int> known[kMaxCluster + 1];
-  *n = known[Z].load(std::memory_order_relaxed);
-  if (*n) return cudaSuccess;
+cudaError_t clusters_held(int dev, int Z, size_t stages, int* n) {
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];
+  if (dev < kDevices && (*n = known[dev][Z].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
   const Launch l(1, Z, stages, nullptr);
   const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kKernel, &l.cfg);
-  if (e == cudaSuccess) known[Z].store(*n, std::memory_order_relaxed);
+  if (e == cudaSuccess && dev < kDevices) known[dev][Z].store(*n, std::memory_order_relaxed);
   return e;
 }
 
@@ -791,9 +799,11 @@ cudaError_t launch_cluster(const GlrArgs& p, Geometry& g, int rows, size_t stage
   const int64_t items = (int64_t)p.B * g.blocks;
   const int tiles = (int)(((int64_t)p.T + rows - 1) / rows);
   g.Z = tiles < 1 ? 1 : tiles < kMaxCluster ? tiles : kMaxCluster;
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   for (; e == cudaSuccess && g.Z > 1; --g.Z) {
     int held = 0;
-    e = clusters_held<kKernel>(g.Z, stages, &held);
+    e = clusters_held<kKernel>(dev, g.Z, stages, &held);
     if (items <= held) break;
   }
   if (e != cudaSuccess) return e;
