@@ -28,6 +28,7 @@
 // A sequence start is a reset: its map ignores the carry.  It is marked by A = -0.0 (a real A
 // is never negative), not by A = 0, because 0 * inf would let an overflow of one sequence
 // reach the next.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -270,12 +271,12 @@ __device__ __forceinline__ Span span_of(const int* cu, int N, int T, int b, int 
   int l = 0, h = N;  // the first n with cu[n+1] > lo
   while (l < h) {
     const int m = (l + h) >> 1;
-    if (__ldg(cu + m + 1) > lo) h = m;
+    if (cu[m + 1] > lo) h = m;
     else l = m + 1;
   }
   r.n0 = min(l, N - 1);
   for (int n = l; n < N; ++n) {
-    const int s = __ldg(cu + n), e = __ldg(cu + n + 1);
+    const int s = cu[n], e = cu[n + 1];
     if (s >= hi) break;
     if (e <= s) continue;
     if (s >= lo) r.first |= 1u << (s - lo);
@@ -290,13 +291,13 @@ __device__ __forceinline__ Span span_of(const int* cu, int N, int T, int b, int 
 __device__ __forceinline__ int next_sequence(const int* cu, int N, int n) {
   if (!cu) return n;
   do ++n;
-  while (n < N - 1 && __ldg(cu + n + 1) <= __ldg(cu + n));
+  while (n < N - 1 && cu[n + 1] <= cu[n]);
   return min(n, N - 1);
 }
 __device__ __forceinline__ int previous_sequence(const int* cu, int n) {
   if (!cu) return n;
   do --n;
-  while (n > 0 && __ldg(cu + n + 1) <= __ldg(cu + n));
+  while (n > 0 && cu[n + 1] <= cu[n]);
   return max(n, 0);
 }
 
@@ -332,17 +333,25 @@ struct LinkSmem {
 // The other tiles' maps, of even and odd steps, behind the stages: one per other CTA.
 typedef float2 TileMaps[2][kCh];
 constexpr size_t maps_bytes(int Z) { return (Z - 1) * sizeof(TileMaps); }
+// Bounds of up to this many sequences are read from shared memory, behind the maps.
+constexpr int kBounds = 256;
 
-// Before the first step; ends with a barrier over the cluster.
+// The sequences' bounds: a copy at `to`, or where they are.  To be used behind a block barrier.
+__device__ __forceinline__ const int* bounds_of(const GlrArgs& p, void* to) {
+  if (!p.cu || p.N >= kBounds) return p.cu;
+  for (int n = threadIdx.x; n <= p.N; n += kThreads) static_cast<int*>(to)[n] = __ldg(p.cu + n);
+  return static_cast<int*>(to);
+}
+
+// Before the first step; a barrier over the cluster.
 __device__ __forceinline__ void link_init(LinkSmem& sm, int Z) {
-  if (Z == 1) return;
-  if (threadIdx.x == 0) {
+  if (Z > 1 && threadIdx.x == 0) {
     tc::mbar_init(&sm.bar[0], 1);
     tc::mbar_init(&sm.bar[1], 1);
     tc::fence_mbar_init();
   }
   __syncthreads();
-  cluster_sync();
+  if (Z > 1) cluster_sync();
 }
 
 // After the segments' maps of step k are in sm.seg: folds them, and moves `c` (warp 0, a channel
@@ -407,7 +416,7 @@ __device__ __forceinline__ void empty_sequences(const int* cu, int N, int T, int
   const int g = threadIdx.x / (kCh / 2);
   const int n0 = cu ? g : (g == 0 && T == 0 ? b : N), step = cu ? kSegs : N;
   for (int n = n0; n < N; n += step) {
-    if (cu && __ldg(cu + n + 1) > __ldg(cu + n)) continue;
+    if (cu && cu[n + 1] > cu[n]) continue;
     const int64_t at = (int64_t)n * D + ch;
     store_pair(dst + at, src ? load_state(src + at, how) : make_float2(0.f, 0.f), how);
   }
@@ -430,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   TileMaps* maps = reinterpret_cast<TileMaps*>(stages + kFwdStages);
+  const int* cu = bounds_of(p, maps + geo.Z - 1);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
@@ -453,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
   };
 #pragma unroll
   for (int k = 0; k < kFwdStages - 1; ++k) issue(k);
-  if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
   link_init(sm, Z);
-  auto spans = [&](int k, int g) { return span_of<S>(p.cu, p.N, p.T, b, (k * Z + rank) * kRows + g * S); };
+  if (rank == 0 && live) empty_sequences(cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
+  auto spans = [&](int k, int g) { return span_of<S>(cu, p.N, p.T, b, (k * Z + rank) * kRows + g * S); };
   if (threadIdx.x < kSegs) sm.span[threadIdx.x] = spans(0, threadIdx.x);
   float c = 0.f;
   for (int k = 0; k < steps; ++k) {
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
         a[s] = on ? a[s] : both(1.f);
         if (p.h0) {
           if (first && live) u[s] = fma2(a[s], to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how)), u[s]);
-          if (span.last >> s & 1) n = next_sequence(p.cu, p.N, n);
+          if (span.last >> s & 1) n = next_sequence(cu, p.N, n);
         }
         a[s] = first ? both(-0.f) : a[s];
         A = first ? both(-0.f) : mul2(A, a[s]);
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
         o += p.D;
         if (p.state && (span.last >> s & 1)) {
           if (live) store_pair(p.state + (int64_t)n * p.D + ch, unpack(h), how);
-          n = next_sequence(p.cu, p.N, n);
+          n = next_sequence(cu, p.N, n);
         }
       }
     }
@@ -558,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   TileMaps* maps = reinterpret_cast<TileMaps*>(stages + kBwdStages);
+  const int* cu = bounds_of(p, maps + geo.Z - 1);
   __shared__ __align__(16) LinkSmem sm;
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
@@ -590,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
   };
 #pragma unroll
   for (int k = 0; k < kBwdStages - 1; ++k) issue(k);
-  if (rank == 0 && live) empty_sequences(p.cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
   link_init(sm, Z);
+  if (rank == 0 && live) empty_sequences(cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
   auto spans = [&](int k, int g) {
-    return span_of<S>(p.cu, p.N, p.T, b, k < steps ? tile_start(k) + (kSegs - 1 - g) * S : p.T);
+    return span_of<S>(cu, p.N, p.T, b, k < steps ? tile_start(k) + (kSegs - 1 - g) * S : p.T);
   };
   if (threadIdx.x < kSegs) sm.span[threadIdx.x] = spans(0, threadIdx.x);
   float carry = 0.f;
@@ -605,10 +616,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     const int back = kSegs - 1 - seg, lo = tile_start(k) + back * S;
     const Span span = sm.span[seg];
     int n_last = span.n0;  // the sequence of the last token that is on
-    if (p.cu && (p.dstate || p.h0 || p.dh0)) {
+    if (cu && (p.dstate || p.h0 || p.dh0)) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
-        if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(p.cu, p.N, n_last);
+        if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(cu, p.N, n_last);
     }
     f32x2 a[S], bs[S], d[S], A = both(1.f), E = both(0.f);
     const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u &&
@@ -635,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
         d[s] = on ? d[s] : both(0.f);
         if (p.dstate) {
           if (last && live) d[s] = add2(d[s], to_pair(load_state(p.dstate + (int64_t)n * p.D + ch, how)));
-          if (span.first >> s & 1) n = previous_sequence(p.cu, n);
+          if (span.first >> s & 1) n = previous_sequence(cu, n);
         }
         A = last ? both(-0.f) : mul2(A, a[s]);  // nothing comes from the sequence behind
         E = mul2(a[s], last ? d[s] : add2(d[s], E));
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
         }
         if (first && (p.h0 || p.dh0)) {
           if (live && p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, unpack(c), how);
-          n = previous_sequence(p.cu, n);
+          n = previous_sequence(cu, n);
         }
       }
     }
@@ -757,10 +768,10 @@ int copy_bytes(const void* p, int64_t sb, int64_t st, int64_t D, int size) {
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
-  Launch(int64_t items, int Z, size_t stages, cudaStream_t s) {
+  Launch(int64_t items, int Z, size_t stages, bool bounds, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(items * Z));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = stages + maps_bytes(Z);
+    cfg.dynamicSmemBytes = stages + maps_bytes(Z) + (bounds ? kBounds * sizeof(int) : 0);
     cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = Z;
@@ -771,16 +782,17 @@ struct Launch {
   }
 };
 
-// How many clusters of Z CTAs a device holds at once; asked for once per kernel, Z and device (of
-// the first kDevices: the answer takes the runtime longer than the launch).
+// How many clusters of Z CTAs a device holds at once; asked for once per kernel, Z, bounds and
+// device (of the first kDevices: the answer takes the runtime longer than the launch).
 constexpr int kDevices = 16;
 template <auto kKernel>
-cudaError_t clusters_held(int dev, int Z, size_t stages, int* n) {
-  static std::atomic<int> known[kDevices][kMaxCluster + 1];
-  if (dev < kDevices && (*n = known[dev][Z].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  const Launch l(1, Z, stages, nullptr);
+cudaError_t clusters_held(int dev, int Z, size_t stages, bool bounds, int* n) {
+  static std::atomic<int> table[kDevices + 1][kMaxCluster + 1][2];
+  std::atomic<int>& known = table[std::min(dev, kDevices)][Z][bounds];
+  if (dev < kDevices && (*n = known.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  const Launch l(1, Z, stages, bounds, nullptr);
   const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kKernel, &l.cfg);
-  if (e == cudaSuccess && dev < kDevices) known[dev][Z].store(*n, std::memory_order_relaxed);
+  if (e == cudaSuccess) known.store(*n, std::memory_order_relaxed);
   return e;
 }
 
@@ -793,23 +805,24 @@ template <auto kKernel>
 cudaError_t launch_cluster(const GlrArgs& p, Geometry& g, int rows, size_t stages,
                            cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(stages + maps_bytes(kMaxCluster)));
+                                       (int)(stages + maps_bytes(kMaxCluster) + kBounds * sizeof(int)));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   const int64_t items = (int64_t)p.B * g.blocks;
   const int tiles = (int)(((int64_t)p.T + rows - 1) / rows);
   g.Z = tiles < 1 ? 1 : tiles < kMaxCluster ? tiles : kMaxCluster;
+  const bool bounds = p.cu && p.N < kBounds;
   int dev = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   for (; e == cudaSuccess && g.Z > 1; --g.Z) {
     int held = 0;
-    e = clusters_held<kKernel>(dev, g.Z, stages, &held);
+    e = clusters_held<kKernel>(dev, g.Z, stages, bounds, &held);
     if (items <= held) break;
   }
   if (e != cudaSuccess) return e;
   const int steps = (tiles + g.Z - 1) / g.Z;
   if (steps > 0) g.Z = (tiles + steps - 1) / steps;
-  const Launch l(items, g.Z, stages, s);
+  const Launch l(items, g.Z, stages, bounds, s);
   return cudaLaunchKernelEx(&l.cfg, kKernel, p, (const Geometry&)g);
 }
 
