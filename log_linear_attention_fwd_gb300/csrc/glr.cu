@@ -255,6 +255,15 @@ struct Span {
   int n0;
 };
 
+// The tokens that need more than the recurrence, in either half of the warp: that are not there,
+// or begin or end a sequence; all where outputs do not go out as pairs.
+template <int S>
+__device__ __forceinline__ uint32_t odd_tokens(const Span& v, int pairs) {
+  constexpr uint32_t all = (1u << S) - 1u;
+  const uint32_t odd = __reduce_or_sync(0xffffffffu, (~v.on & all) | v.first | v.last);
+  return pairs ? odd : all;
+}
+
 // cu == null: sequence b holds [0, T).  cu: sequence n holds [cu[n], cu[n+1]); malformed bounds
 // give wrong spans, but never a token outside [0, T) or a sequence outside [0, N).
 template <int S>
@@ -329,6 +338,7 @@ struct LinkSmem {
   float2 seg[kSegs][kCh];
   Span span[kSegs];  // the segments' sequences
   uint64_t bar[2];   // the other tiles' maps are there
+  const int* cu;     // the sequences' bounds: here they cost no registers between their uses
 };
 // The other tiles' maps, of even and odd steps, behind the stages: one per other CTA.
 typedef float2 TileMaps[2][kCh];
@@ -336,11 +346,13 @@ constexpr size_t maps_bytes(int Z) { return (Z - 1) * sizeof(TileMaps); }
 // Bounds of up to this many sequences are read from shared memory, behind the maps.
 constexpr int kBounds = 256;
 
-// The sequences' bounds: a copy at `to`, or where they are.  To be used behind a block barrier.
-__device__ __forceinline__ const int* bounds_of(const GlrArgs& p, void* to) {
-  if (!p.cu || p.N >= kBounds) return p.cu;
+// Sets sm.cu to the sequences' bounds: a copy at `to`, or where they are.  To be used behind a
+// block barrier.
+__device__ __forceinline__ void place_bounds(LinkSmem& sm, const GlrArgs& p, void* to) {
+  const bool copy = p.cu && p.N < kBounds;
+  if (threadIdx.x == 0) sm.cu = copy ? static_cast<int*>(to) : p.cu;
+  if (!copy) return;
   for (int n = threadIdx.x; n <= p.N; n += kThreads) static_cast<int*>(to)[n] = __ldg(p.cu + n);
-  return static_cast<int*>(to);
 }
 
 // Before the first step; a barrier over the cluster.
@@ -439,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   TileMaps* maps = reinterpret_cast<TileMaps*>(stages + kFwdStages);
-  const int* cu = bounds_of(p, maps + geo.Z - 1);
   __shared__ __align__(16) LinkSmem sm;
+  place_bounds(sm, p, maps + geo.Z - 1);
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
   const int seg = threadIdx.x / (kCh / 2);
@@ -464,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
 #pragma unroll
   for (int k = 0; k < kFwdStages - 1; ++k) issue(k);
   link_init(sm, Z);
-  if (rank == 0 && live) empty_sequences(cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
-  auto spans = [&](int k, int g) { return span_of<S>(cu, p.N, p.T, b, (k * Z + rank) * kRows + g * S); };
+  if (rank == 0 && live) empty_sequences(sm.cu, p.N, p.T, b, p.D, ch, how, p.h0, p.state);
+  auto spans = [&](int k, int g) { return span_of<S>(sm.cu, p.N, p.T, b, (k * Z + rank) * kRows + g * S); };
   if (threadIdx.x < kSegs) sm.span[threadIdx.x] = spans(0, threadIdx.x);
   float c = 0.f;
   for (int k = 0; k < steps; ++k) {
@@ -476,16 +488,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     const int lo = (k * Z + rank) * kRows + seg * S;
     const Span span = sm.span[seg];
     f32x2 a[S], u[S], A = both(1.f), H = both(0.f);
-    // plain: every token is there, no sequence begins or ends, and pairs go out as pairs
-    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u &&
-                                                   !(span.first | span.last));
+    const uint32_t odd = odd_tokens<S>(span, geo.pairs);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       f32x2 m;
       gate_of(st.la.pair(seg, s, cl), &a[s], &m);
       u[s] = mul2(scale_of<kScale>(m), to_pair(st.x.pair(seg, s, cl)));
     }
-    if (plain) {
+    if (!odd) {
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         H = fma2(a[s], H, u[s]);
@@ -495,12 +505,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
       int n = span.n0;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
+        if (!(odd >> s & 1)) {
+          H = fma2(a[s], H, u[s]);
+          A = mul2(A, a[s]);
+          continue;
+        }
         const bool on = span.on >> s & 1, first = span.first >> s & 1;
         u[s] = on ? u[s] : both(0.f);
         a[s] = on ? a[s] : both(1.f);
         if (p.h0) {
           if (first && live) u[s] = fma2(a[s], to_pair(load_state(p.h0 + (int64_t)n * p.D + ch, how)), u[s]);
-          if (span.last >> s & 1) n = next_sequence(cu, p.N, n);
+          if (span.last >> s & 1) n = next_sequence(sm.cu, p.N, n);
         }
         a[s] = first ? both(-0.f) : a[s];
         A = first ? both(-0.f) : mul2(A, a[s]);
@@ -512,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     link_step(sm, maps, k, Z, rank, c, [&](int g) { return spans(k + 1, g); });
     f32x2 h = segment_carry(sm, seg, cl);
     OutT* o = out + (int64_t)lo * p.D;
-    if (plain) {
+    if (!odd) {
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         h = fma2(a[s], h, u[s]);
@@ -523,12 +538,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
       int n = span.n0;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
+        if (!(odd >> s & 1)) {
+          h = fma2(a[s], h, u[s]);
+          if (live) put_pair(o, unpack(h));
+          o += p.D;
+          continue;
+        }
         h = fma2(a[s], span.first >> s & 1 ? both(0.f) : h, u[s]);  // (a is -0 there: h = u)
         if (live && (span.on >> s & 1)) store_pair(o, unpack(h), how);
         o += p.D;
         if (p.state && (span.last >> s & 1)) {
           if (live) store_pair(p.state + (int64_t)n * p.D + ch, unpack(h), how);
-          n = next_sequence(cu, p.N, n);
+          n = next_sequence(sm.cu, p.N, n);
         }
       }
     }
@@ -568,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
   extern __shared__ __align__(16) uint8_t dyn[];
   Stage* stages = reinterpret_cast<Stage*>(dyn);
   TileMaps* maps = reinterpret_cast<TileMaps*>(stages + kBwdStages);
-  const int* cu = bounds_of(p, maps + geo.Z - 1);
   __shared__ __align__(16) LinkSmem sm;
+  place_bounds(sm, p, maps + geo.Z - 1);
   const int Z = geo.Z, rank = Z > 1 ? (int)cluster_rank() : 0;
   const int item = blockIdx.x / Z, b = item / geo.blocks, blk = item - b * geo.blocks;
   const int seg = threadIdx.x / (kCh / 2);
@@ -602,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
 #pragma unroll
   for (int k = 0; k < kBwdStages - 1; ++k) issue(k);
   link_init(sm, Z);
-  if (rank == 0 && live) empty_sequences(cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
+  if (rank == 0 && live) empty_sequences(sm.cu, p.N, p.T, b, p.D, ch, how, p.dstate, p.dh0);
   auto spans = [&](int k, int g) {
-    return span_of<S>(cu, p.N, p.T, b, k < steps ? tile_start(k) + (kSegs - 1 - g) * S : p.T);
+    return span_of<S>(sm.cu, p.N, p.T, b, k < steps ? tile_start(k) + (kSegs - 1 - g) * S : p.T);
   };
   if (threadIdx.x < kSegs) sm.span[threadIdx.x] = spans(0, threadIdx.x);
   float carry = 0.f;
@@ -616,14 +637,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     const int back = kSegs - 1 - seg, lo = tile_start(k) + back * S;
     const Span span = sm.span[seg];
     int n_last = span.n0;  // the sequence of the last token that is on
-    if (cu && (p.dstate || p.h0 || p.dh0)) {
+    if (p.cu && (p.dstate || p.h0 || p.dh0)) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
-        if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(cu, p.N, n_last);
+        if ((span.last >> s & 1) && (span.on >> s) > 1u) n_last = next_sequence(sm.cu, p.N, n_last);
     }
     f32x2 a[S], bs[S], d[S], A = both(1.f), E = both(0.f);
-    const bool plain = __all_sync(0xffffffffu, geo.pairs && span.on == (1u << S) - 1u &&
-                                                   !(span.first | span.last));
+    const uint32_t odd = odd_tokens<S>(span, geo.pairs);
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
       f32x2 m;
@@ -631,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
       bs[s] = scale_of<kScale>(m);
       d[s] = to_pair(st.dout.pair(back, s, cl));
     }
-    if (plain) {
+    if (!odd) {
 #pragma unroll
       for (int s = S - 1; s >= 0; --s) {
         A = mul2(A, a[s]);
@@ -646,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
         d[s] = on ? d[s] : both(0.f);
         if (p.dstate) {
           if (last && live) d[s] = add2(d[s], to_pair(load_state(p.dstate + (int64_t)n * p.D + ch, how)));
-          if (span.first >> s & 1) n = previous_sequence(cu, n);
+          if (span.first >> s & 1) n = previous_sequence(sm.cu, n);
         }
         A = last ? both(-0.f) : mul2(A, a[s]);  // nothing comes from the sequence behind
         E = mul2(a[s], last ? d[s] : add2(d[s], E));
@@ -658,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     f32x2 c = segment_carry(sm, seg, cl);
     GradT* ox = dx + (int64_t)(lo + S - 1) * p.D;
     GateT* ol = dla + (int64_t)(lo + S - 1) * p.D;
-    if (plain) {
+    if (!odd) {
 #pragma unroll
       for (int s = S - 1; s >= 0; --s) {
         const f32x2 g = add2(d[s], c);
@@ -691,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
         }
         if (first && (p.h0 || p.dh0)) {
           if (live && p.dh0) store_pair(p.dh0 + (int64_t)n * p.D + ch, unpack(c), how);
-          n = previous_sequence(cu, n);
+          n = previous_sequence(sm.cu, n);
         }
       }
     }
