@@ -15,12 +15,13 @@
 // while this one is worked on, and four small CTAs share an SM, so that one folds and waits
 // while the others compute.
 //
-// What bounds them is issue and the exchange, not HBM: 76 instructions per token and pair of
+// What bounds them is issue and the exchange, not HBM: 75 instructions per token and pair of
 // channels, half of them the gate (measured with parts switched off, B8 T2048 D2048 bf16: all 73
-// us, without gates 62, without the exchange 67, neither 57, and 39.6 is HBM's time).  Forward,
-// b = sqrt(1 - a^2), bf16 with fp32 gates, D 2048: T 16384 73 us, 3.7 TB/s; B8 T2048 64; B16 T1024
-// 58, 4.6 TB/s.  Backward: B4 T4096 124 us, 4.3 TB/s.  Packed, 9001 tokens of 1000 channels in
-// fp32: forward 33 us, backward 49.
+// us, without gates 62, without the exchange 67, neither 57; HBM's time is 39.6), and 512 CTAs that
+// put four on some SMs and none on others.  Forward, b = sqrt(1 - a^2), bf16 with fp32 gates,
+// D 2048: T 16384 68 us, 3.9 TB/s; B4 T4096 63, 4.3 TB/s.  Backward: B4 T4096 119 us, 4.5 TB/s.
+// Packed in 37 sequences with first states, 9001 tokens of 1000 channels, fp32: forward 33 us,
+// backward 57.  Kept out of registers, the address of the sequences' bounds alone was worth 6%.
 //
 // Z is chosen so that batch entries x channel blocks x Z CTAs fill the GPU (launch_cluster).
 // The backward is the same scan with time reversed.
@@ -343,13 +344,18 @@ struct LinkSmem {
 // The other tiles' maps, of even and odd steps, behind the stages: one per other CTA.
 typedef float2 TileMaps[2][kCh];
 constexpr size_t maps_bytes(int Z) { return (Z - 1) * sizeof(TileMaps); }
-// Bounds of up to this many sequences are read from shared memory, behind the maps.
-constexpr int kBounds = 256;
+// Bounds of fewer than kManyBounds sequences are read from shared memory, behind the maps: room for
+// kManyBounds, or for kFewBounds where these do (1 KB less can be a CTA more per SM: 2500 tokens of
+// 514 channels, fp32, backward 22.4 -> 21.4 us).
+constexpr int kFewBounds = 16, kManyBounds = 256;
+__host__ __device__ __forceinline__ int bounds_room(const GlrArgs& p) {
+  return !p.cu || p.N >= kManyBounds ? 0 : p.N < kFewBounds ? kFewBounds : kManyBounds;
+}
 
 // Sets sm.cu to the sequences' bounds: a copy at `to`, or where they are.  To be used behind a
 // block barrier.
 __device__ __forceinline__ void place_bounds(LinkSmem& sm, const GlrArgs& p, void* to) {
-  const bool copy = p.cu && p.N < kBounds;
+  const bool copy = bounds_room(p) != 0;
   if (threadIdx.x == 0) sm.cu = copy ? static_cast<int*>(to) : p.cu;
   if (!copy) return;
   for (int n = threadIdx.x; n <= p.N; n += kThreads) static_cast<int*>(to)[n] = __ldg(p.cu + n);
@@ -723,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
 
 // One token per row: state[slot] <- a state[slot] + b x, out = the new state.  A slot given
 // twice belongs to its first row; the rows after it, and rows whose slot is out of range, are
-// left out and raise the error word.
+// left out and raise the error word.  2.1 us for 128 rows of 2048 channels in a graph, the launch
+// itself; 12 for 1024 rows of 4096 (67 MB, 5.7 TB/s).
 constexpr int kStepThreads = 256;
 
 template <typename InT, typename GateT, typename OutT, int kScale>
@@ -788,10 +795,10 @@ int copy_bytes(const void* p, int64_t sb, int64_t st, int64_t D, int size) {
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
-  Launch(int64_t items, int Z, size_t stages, bool bounds, cudaStream_t s) {
+  Launch(int64_t items, int Z, size_t stages, int bounds, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(items * Z));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = stages + maps_bytes(Z) + (bounds ? kBounds * sizeof(int) : 0);
+    cfg.dynamicSmemBytes = stages + maps_bytes(Z) + bounds * sizeof(int);
     cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = Z;
@@ -806,9 +813,9 @@ struct Launch {
 // device (of the first kDevices: the answer takes the runtime longer than the launch).
 constexpr int kDevices = 16;
 template <auto kKernel>
-cudaError_t clusters_held(int dev, int Z, size_t stages, bool bounds, int* n) {
-  static std::atomic<int> table[kDevices + 1][kMaxCluster + 1][2];
-  std::atomic<int>& known = table[std::min(dev, kDevices)][Z][bounds];
+cudaError_t clusters_held(int dev, int Z, size_t stages, int bounds, int* n) {
+  static std::atomic<int> table[kDevices + 1][kMaxCluster + 1][3];
+  std::atomic<int>& known = table[std::min(dev, kDevices)][Z][(bounds > 0) + (bounds > kFewBounds)];
   if (dev < kDevices && (*n = known.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
   const Launch l(1, Z, stages, bounds, nullptr);
   const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kKernel, &l.cfg);
@@ -818,20 +825,20 @@ cudaError_t clusters_held(int dev, int Z, size_t stages, bool bounds, int* n) {
 
 // Z, the CTAs that share a channel block: as many as leave all clusters running at once (at most
 // kMaxCluster), then as few as take no more steps.  Forward and backward: 65536 tokens of 512
-// channels, bf16: 124 and 230 us with Z = 16, 167 and 316 with 8; 9001 of 1000, fp32: 30 and 45
+// channels, bf16, 124 and 230 us with Z = 16, 167 and 316 with 8; 9001 of 1000, fp32, 30 and 45
 // with 12, 31 and 49 with 8.  Where a cluster waits for the others: 2500 of 514, fp32, forward 21 us
 // with 16 (17 clusters, of which 14 run), 11 with 10 and 15 with 8.
 template <auto kKernel>
 cudaError_t launch_cluster(const GlrArgs& p, Geometry& g, int rows, size_t stages,
                            cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(stages + maps_bytes(kMaxCluster) + kBounds * sizeof(int)));
+                                       (int)(stages + maps_bytes(kMaxCluster) + kManyBounds * sizeof(int)));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   const int64_t items = (int64_t)p.B * g.blocks;
   const int tiles = (int)(((int64_t)p.T + rows - 1) / rows);
   g.Z = tiles < 1 ? 1 : tiles < kMaxCluster ? tiles : kMaxCluster;
-  const bool bounds = p.cu && p.N < kBounds;
+  const int bounds = bounds_room(p);
   int dev = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   for (; e == cudaSuccess && g.Z > 1; --g.Z) {
