@@ -412,6 +412,17 @@ __device__ __forceinline__ void link_step(LinkSmem& sm, TileMaps* maps, int k, i
   __syncthreads();
 }
 
+// After the last step.  Where a wait ran out of time (only then are maps to this CTA still on their
+// way), the CTA stays until all of the cluster have sent theirs and, with a limit again, until they
+// are here.  (relaxed: the outputs need no order here, and a release would wait for them)
+__device__ __forceinline__ void link_done(LinkSmem& sm, int steps, int Z) {
+  if (Z == 1) return;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int k = max(steps - 2, 0); k < steps && threadIdx.x == 0; ++k)
+    tc::mbar_wait_short(&sm.bar[k & 1], (k >> 1) & 1);
+}
+
 // The carry into a segment, from the tile's and the segments before it.
 __device__ __forceinline__ f32x2 segment_carry(const LinkSmem& sm, int g, int cl) {
   const float4 c = *reinterpret_cast<const float4*>(&sm.seg[kSegs - 1][cl]);
@@ -561,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     }
     __syncwarp();
   }
+  link_done(sm, steps, Z);
 }
 
 // ---------------------------------------------------------------- backward
@@ -723,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     }
     __syncwarp();
   }
+  link_done(sm, steps, Z);
 }
 
 // ---------------------------------------------------------------- step

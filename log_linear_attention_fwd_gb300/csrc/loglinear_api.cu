@@ -670,7 +670,7 @@ int check_glr(int64_t B, int64_t T, int64_t D, int in_dtype, int gate_dtype, int
 int glr_common(GlrArgs* a, const void* x, const ll_strides* xs, const void* log_a,
                const ll_strides* ls, const float* h0, const int32_t* cu, int64_t N, int64_t B,
                int64_t T, int64_t D, int in_dtype, int gate_dtype, bool x_needed, bool* empty) {
-  // a launch has B x ceil(D / 32) clusters of at most 8 CTAs
+  // a launch has B x ceil(D / 32) clusters of at most 16 CTAs
   if (T > (1 << 30) || B > INT32_MAX / 16 || D > INT32_MAX / 16) return LL_ERR_UNSUPPORTED;
   if (B * ((D + 31) / 32) > INT32_MAX / 16) return LL_ERR_UNSUPPORTED;
   if (cu && B != 1) return LL_ERR_INVALID;
