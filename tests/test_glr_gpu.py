@@ -5,6 +5,10 @@ times that, independently per step; with 1 - a >= 0.01 (k up to about 100) that 
 sqrt(100) * 2^-22 = 2.4e-6 of the state, and 1e-5 (TOL_F32) bounds it.  bf16 results add half a
 step of the type, 2^-8 of each value.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -182,6 +186,59 @@ def test_long_sums_are_exact(LL):
         assert torch.equal(out.cpu(), x.cumsum(1))
         dx, _, _ = LL.loglinear_glr_bwd(None, la.cuda(), out, x.cuda())
         assert torch.equal(dx.cpu(), x.flip(1).cumsum(1).flip(1))
+
+
+def test_clusters_of_odd_sizes_are_exact(LL):
+    """As above, where a channel block's CTAs are not a power of two, and packed."""
+    for T, D in ((1300, 40), (2500, 514), (9001, 1000)):
+        g = torch.Generator().manual_seed(T)
+        x = torch.randint(-2, 3, (1, T, D), generator=g).float()
+        la = torch.zeros(1, T, D)
+        h0 = torch.randint(-9, 10, (3, D), generator=g).float()
+        cu = [0, T // 3, T // 2 + 1, T]
+        c = torch.tensor(cu, dtype=torch.int32).cuda()
+        state = torch.empty(3, D).cuda()
+        out = LL.loglinear_glr_fwd(x.cuda(), la.cuda(), h0=h0.cuda(), cu_seqlens=c, state=state)
+        dx, _, dh0 = LL.loglinear_glr_bwd(None, la.cuda(), out, x.cuda(), h0=h0.cuda(), cu_seqlens=c,
+                                          dstate=h0.cuda())
+        for n, (lo, hi) in enumerate(zip(cu, cu[1:])):
+            want = x[0, lo:hi].cumsum(0) + h0[n]
+            assert torch.equal(out[0, lo:hi].cpu(), want) and torch.equal(state[n].cpu(), want[-1])
+            back = x[0, lo:hi].flip(0).cumsum(0).flip(0) + h0[n]
+            assert torch.equal(dx[0, lo:hi].cpu(), back) and torch.equal(dh0[n].cpu(), back[0])
+
+
+@pytest.mark.parametrize("n", [15, 16, 255, 256, 257])
+def test_numbers_of_sequences(LL, n):
+    """Around the counts at which the bounds are read from another place."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 6, (n,), generator=g)
+    cu = np.concatenate([[0], np.cumsum(lens.numpy())]).tolist()
+    T, D = cu[-1] + 3, 12
+    x, la = make(1, T, D, seed=n)
+    fwd_bwd(LL, x, la, "sqrt", h0=torch.randn(n, D, generator=g), cu=cu,
+            dout=torch.randn(1, T, D, generator=g), ds=torch.randn(n, D, generator=g))
+
+
+def test_first_call_inside_a_capture(LL):
+    """What a call asks of the runtime the first time is allowed while a stream is captured."""
+    code = """
+import torch, log_linear_attention_fwd_gb300 as LL
+x, la = torch.randn(1, 3000, 70).cuda(), -torch.rand(1, 3000, 70).cuda()
+cu, out = torch.tensor([0, 5, 1000, 3000], dtype=torch.int32).cuda(), torch.empty_like(x)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    LL.loglinear_glr_fwd(x, la, out=out, scale="sqrt", cu_seqlens=cu)
+    grads = LL.loglinear_glr_bwd(x, la, out, x, scale="sqrt", cu_seqlens=cu)
+g.replay()
+o = LL.loglinear_glr_fwd(x, la, scale="sqrt", cu_seqlens=cu)
+want = LL.loglinear_glr_bwd(x, la, o, x, scale="sqrt", cu_seqlens=cu)
+assert torch.equal(o, out) and all(torch.equal(a, b) for a, b in zip(grads[:2], want[:2]))
+assert LL.device_error() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
 
 
 def test_results_do_not_depend_on_timing(LL):
