@@ -417,6 +417,45 @@ def test_pages_are_taken_lowest_first(LL):
     assert cache.error() == 0
 
 
+def test_more_rows_than_a_plan_has_threads(LL):
+    """1500 rows at once (their owners go through memory) against two calls of fewer rows."""
+    n, H, d, M = 1500, 2, 8, 3
+    g = torch.Generator().manual_seed(5)
+    perm = torch.randperm(1600, generator=g)[:n].to(torch.int32)
+    perm[torch.randperm(n, generator=g)[:40]] = -1
+    pos = torch.full((n,), 63, dtype=torch.int32)
+    pos[torch.randperm(n, generator=g)[:300]] = 62
+    perm, pos = perm.cuda(), pos.cuda()
+    S = torch.randn(n, H, M + 7, d, d, generator=g).cuda()
+    k, v = torch.randn(n, 63, H, d, generator=g).cuda(), torch.randn(n, 63, H, d, generator=g).cuda()
+    la, lam = -torch.rand(n, 63, H, generator=g).cuda(), torch.rand(n, H, M + 7, generator=g).cuda()
+    parts = {1: [slice(0, n)], 2: [slice(0, 700), slice(700, n)]}
+    got = {}
+    for calls in parts:
+        cache = poison(LL.LogLinearCache.empty(1600, 1400, H, d, d, M, dtype=torch.float32))
+        out = torch.full((n, H, d), 7.0).cuda()
+        for at in parts[calls]:
+            cut = lambda t: t[at].contiguous()  # noqa: E731
+            LL.loglinear_cache_load(cache, cut(perm), 62, cut(S), k[at, :62], v[at, :62], la[at, :62])
+        for last in (62, 63):  # (rows at 62 are repeated)
+            for at in parts[calls]:
+                cut = lambda t: t[at].contiguous()  # noqa: E731
+                p = torch.minimum(pos, torch.full_like(pos, last))
+                LL.loglinear_cache_reserve(cache, cut(perm), cut(p))
+                LL.loglinear_cache_step(cache, cut(perm), cut(p), cut(k[:, 0]), cut(k[:, 1]), cut(v[:, 0]),
+                                        cut(la[:, 62]), cut(lam), out=out[at])
+        assert cache.error() == 0
+        got[calls] = (out, cache.page_table, cache.refcount)
+        invariants(cache, {int(s): 64 for s, p in zip(perm, pos) if s >= 0 and p == 63})
+    for a, b in zip(got[1], got[2]):
+        assert torch.equal(a, b)
+    assert torch.all(got[1][0][perm < 0] == 7)
+    twice = perm.clone()
+    twice[1400] = perm[perm >= 0][3]
+    LL.loglinear_cache_reserve(cache, twice, pos)
+    assert cache.error() == LL.CACHE_ERR_SLOT
+
+
 def test_pool_runs_out(LL):
     """A row that gets no page is left out, the others go on; nothing is written astray."""
     H, dk, dv, M = 2, 16, 8, 3
