@@ -397,7 +397,7 @@ LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
  *              may be h0 itself
  * State, gates and sums are fp32; out is rounded once.
  * Errors: LL_ERR_INVALID (null pointer, negative size or stride, unknown scale, cu_seqlens with
- * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T > 2^30, B or D or B * ceil(D / 32) above
+ * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T or N > 2^30, B or D or B * ceil(D / 32) above
  * 2^27), LL_ERR_ALIGN (a pointer not aligned to its element), LL_ERR_CUDA.  B, T or D = 0 is a no-op, but that state_out still receives h0.
  */
 typedef enum { LL_GLR_NONE = 0, LL_GLR_ONE_MINUS = 1, LL_GLR_SQRT = 2 } ll_glr_scale;

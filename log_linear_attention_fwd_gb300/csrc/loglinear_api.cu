@@ -674,7 +674,8 @@ int glr_common(GlrArgs* a, const void* x, const ll_strides* xs, const void* log_
   if (T > (1 << 30) || B > INT32_MAX / 16 || D > INT32_MAX / 16) return LL_ERR_UNSUPPORTED;
   if (B * ((D + 31) / 32) > INT32_MAX / 16) return LL_ERR_UNSUPPORTED;
   if (cu && B != 1) return LL_ERR_INVALID;
-  if (cu && (N < 0 || N > INT32_MAX - 1)) return LL_ERR_INVALID;
+  if (cu && N < 0) return LL_ERR_INVALID;
+  if (cu && N > (1 << 30)) return LL_ERR_UNSUPPORTED;  // the search over the bounds adds two indices
   const int64_t n = cu ? N : B;
   *empty = n == 0 || D == 0;
   if (*empty) return LL_OK;

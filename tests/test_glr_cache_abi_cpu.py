@@ -42,6 +42,20 @@ def test_glr_fwd(L):
         assert call(x=None, la=None, out=None, **kw) == L.LL_OK
 
 
+@pytest.mark.parametrize("name", ["loglinear_glr_fwd", "loglinear_glr_bwd"])
+def test_glr_most_sequences(L, name):
+    """The search over the bounds halves the sum of two indices in 32 bits: at most 2^30 sequences.
+    D = 0, so that a count that is accepted launches nothing."""
+    rest = (P, None) if name == "loglinear_glr_fwd" else (P, P, None, P, P, None)
+
+    def call(N, D):
+        return getattr(L.lib(), name)(P, None, P, None, None, P, N, *rest, 1, 10, D, 0, 0, 0, 0, None)
+
+    for N in (2 ** 30 + 1, 2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31, 2 ** 40):
+        assert call(N, 0) == call(N, 8) == L.LL_ERR_UNSUPPORTED, N
+    assert call(2 ** 30, 0) == L.LL_OK and call(-1, 0) == L.LL_ERR_INVALID
+
+
 def test_glr_bwd(L):
     f = L.lib().loglinear_glr_bwd
     ok = dict(x=P, xs=None, la=P, ls=None, h0=None, cu=None, N=0, h=P, dout=P, dstate=None, dx=P, dla=P,
