@@ -1287,7 +1287,8 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
 // ---------------------------------------------------------------- fork
 
 // A row is left out where its target is not its own, its source is not a slot or is some row's
-// target, or its position is outside the cache.  owner: the targets' rows, kNone for sources.
+// target, its position is outside the cache, or a page that it needs of its source is not there.
+// owner: the targets' rows, ~row of those that are left out, kNone for sources.
 __device__ __forceinline__ unsigned fork_bad(const ll_cache& c, const int* owner, int s, int t) {
   if (s < 0 || s >= c.slots || __ldcg(owner + s) != kNone) return LL_CACHE_ERR_SLOT;
   return t < 0 || t > ((int64_t)kW << c.levels) - 1 ? LL_CACHE_ERR_POSITION : 0;
@@ -1303,32 +1304,34 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ll_cache 
     if (src[r] >= 0 && src[r] < c.slots) sc.owner[src[r]] = kNone;
   __syncthreads();
   claim_slots(c, dst, n, sc.owner);
-  // first every target gives up its pages, then it takes a share of its source's
-  for (int take = 0; take < 2; ++take) {
-    for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
-      const int64_t r = k / M;
-      const int m = (int)(k - r * M), s = src[r], d = dst[r], t = pos[r];
-      if (!owns(c, sc.owner, d, r)) continue;
-      const unsigned bad = fork_bad(c, sc.owner, s, t);
-      if (bad) {
-        if (m == 0 && !take) raise(c, bad);
-        continue;
-      }
-      int* e = c.page_table + (int64_t)d * M + m;
-      if (!take) {
-        if (*e >= 0) drop_page(c, *e);
-        *e = -1;
-      } else if ((t >> kLogW) >> m & 1) {
-        const int page = c.page_table[(int64_t)s * M + m];
-        if (page < 0 || page >= c.n_pages) {
-          raise(c, LL_CACHE_ERR_MISSING);
-        } else {
-          atomicAdd(c.refcount + page, 1);
-          *e = page;
-        }
-      }
+  __syncthreads();
+  // nothing changes before it is settled which rows are served
+  for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
+    const int64_t r = k / M;
+    const int m = (int)(k - r * M), s = src[r], d = dst[r], t = pos[r];
+    if (d < 0 || d >= c.slots) continue;
+    const int o = __ldcg(sc.owner + d);
+    if (o != r && o != ~(int)r) continue;
+    unsigned bad = fork_bad(c, sc.owner, s, t);
+    if (bad) {
+      if (m == 0) raise(c, bad);
+    } else if ((t >> kLogW) >> m & 1) {
+      const int page = c.page_table[(int64_t)s * M + m];
+      if (page < 0 || page >= c.n_pages) raise(c, bad = LL_CACHE_ERR_MISSING);
     }
-    __syncthreads();
+    if (bad) sc.owner[d] = ~(int)r;
+  }
+  __syncthreads();
+  // every target gives up its pages and takes a share of its source's (which is no target)
+  for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
+    const int64_t r = k / M;
+    const int m = (int)(k - r * M), s = src[r], d = dst[r], t = pos[r];
+    if (!owns(c, sc.owner, d, r)) continue;
+    int* e = c.page_table + (int64_t)d * M + m;
+    const int page = (t >> kLogW) >> m & 1 ? c.page_table[(int64_t)s * M + m] : -1;
+    drop_page(c, *e);
+    if (page >= 0) atomicAdd(c.refcount + page, 1);
+    *e = page;
   }
 }
 
@@ -1346,7 +1349,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(ll_cache c,
   wait_for_previous();
   const int h = (int)(blockIdx.x - row * H), s = src[row], d = dst[row], t = pos[row];
   const int* owner = scratch_of(c).owner;
-  if (!owns(c, owner, d, row) || fork_bad(c, owner, s, t)) return;
+  if (!owns(c, owner, d, row)) return;
   const int j = t >> kLogW, r = t & (kW - 1), par = j & 1;
   copy_rows(static_cast<T*>(c.win_v) + ((int64_t)d * H + h) * kW * dv,
             static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv, r * dv, 1, r * dv);

@@ -593,3 +593,30 @@ def test_large_pool_offsets(LL):
     k, v, la = (to64(x[n][0, :64, 5]) for n in ("k", "v", "log_a"))
     w = np.exp(to64(x["log_a"][0, :70, 5]).sum() - np.cumsum(la))
     check(dense[0, 5, 7].cpu(), np.einsum("s,sd,se->de", w, k, v))
+
+
+@pytest.mark.parametrize("gone", [-1, 10 ** 6, -7])
+def test_a_fork_without_its_sources_pages_is_left_out(LL, gone):
+    """A source whose page is not there: its row's target stays as it was, pages, tokens and
+    counts; so does what would be forked from that target.  The other rows are served."""
+    cache, x, T = filled(LL)                                   # slot 1 holds pages 0 and 1, slot 2 pages 0 and 2
+    cache.refcount[cache.page_table[1, 1]] -= 1
+    cache.page_table[1, 1] = gone
+    LL.loglinear_cache_fork(cache, i32([2]), i32([4]), i32([T[2]]))
+    assert cache.error() == 0
+    snap = snapshot(cache)
+    LL.loglinear_cache_fork(cache, i32([1, 4]), i32([4, 6]), i32([T[1], T[2]]))
+    assert cache.error() == LL.CACHE_ERR_MISSING | LL.CACHE_ERR_SLOT and same(snap, snapshot(cache))
+    LL.loglinear_cache_fork(cache, i32([1, 0]), i32([4, 5]), i32([T[1], T[0]]))
+    assert cache.error() == LL.CACHE_ERR_MISSING
+    now = snapshot(cache)
+    keep = [0, 1, 2, 3, 4, 6, 7]
+    assert same([t[keep] for t in (snap[1], *snap[3:])], [t[keep] for t in (now[1], *now[3:])])
+    snap[2][cache.page_table[0, 0]] += 1
+    assert same(snap[:1] + snap[2:3], now[:1] + now[2:3])
+    want = oracle.forward_direct(x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+    both = {k: v[[2, 0]] for k, v in x.items()}
+    got, _ = decode(LL, cache, both, [4, 5], [T[2], T[0]], 40)
+    check(got[0].cpu(), want[2, T[2]:T[2] + 40])
+    check(got[1].cpu(), want[0, T[0]:T[0] + 40])
+    assert cache.error() == 0
