@@ -1206,11 +1206,19 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
   if (s == -1) return;
   unsigned bad = s < 0 || s >= c.slots ? LL_CACHE_ERR_SLOT : 0;
   if (!bad && (n < 0 || n > ((int64_t)kW << M) - 1)) bad = LL_CACHE_ERR_POSITION;
-  if (bad) {
-    if (tid == 0 && h == 0 && level == 0) raise(c, bad);
+  const int j = n >> kLogW, r = n & (kW - 1), par = j & 1;
+  // a level without its page leaves out the whole row: every warp of it looks at all of them, a
+  // level per lane (a block barrier instead: 56.2 us)
+  const int lane = tid & 31;
+  int held = 0;
+  if (!bad && lane < M && (j >> lane & 1)) {
+    held = c.page_table[(int64_t)s * M + lane];
+    if (held < 0 || held >= c.n_pages) bad = LL_CACHE_ERR_MISSING;
+  }
+  if (__any_sync(0xffffffffu, bad)) {
+    if (bad && tid < 32 && h == 0 && level == 0) raise(c, bad);
     return;
   }
-  const int j = n >> kLogW, r = n & (kW - 1), par = j & 1;
   const int64_t size = (int64_t)dk * dv, n4 = size / 4;
   float4* dst = reinterpret_cast<float4*>(state + ((row * H + h) * (int64_t)L + level) * size);
   // a page i is level 7 + i; after a whole block the lowest one holds the sum of the levels that
@@ -1235,16 +1243,12 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
     for (int64_t i = tid; i < n4; i += kCopyThreads) __stcs(dst + i, zero);
     return;
   }
-  const int e = page ? c.page_table[(int64_t)s * M + m] : 0;
+  const int e = __shfl_sync(0xffffffffu, held, m & 31);  // (page: m < M)
   const float log = page ? c.page_log[(((int64_t)s * 2 + par) * M + m) * H + h] : 0.f;
   if (tid < 32)
     block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], tok, &since_s);
   __syncthreads();
   if (page) {
-    if (e < 0 || e >= c.n_pages) {
-      if (tid == 0) raise(c, LL_CACHE_ERR_MISSING);
-      return;
-    }
     const float f = expf(log + since_s);
     const float4* src = reinterpret_cast<const float4*>(c.pages + ((int64_t)e * H + h) * size);
     copy4(dst, src, n4, [f](float4 x) { return make_float4(f * x.x, f * x.y, f * x.z, f * x.w); });

@@ -620,3 +620,20 @@ def test_a_fork_without_its_sources_pages_is_left_out(LL, gone):
     check(got[0].cpu(), want[2, T[2]:T[2] + 40])
     check(got[1].cpu(), want[0, T[0]:T[0] + 40])
     assert cache.error() == 0
+
+
+def test_a_store_without_its_pages_is_left_out(LL):
+    """A row whose page is not there, or whose position is outside the cache, keeps its output
+    whole; the others are served."""
+    cache, x, T = filled(LL)
+    M = cache.levels
+    want = LL.loglinear_cache_store(cache, i32([0]), i32([T[0]]))
+    for gone in (-1, 10 ** 6, -7):
+        cache.page_table[2, 2] = gone
+        st = torch.full((4, 2, M + 7, 16, 8), 3.0).cuda()
+        LL.loglinear_cache_store(cache, i32([2, 0, 2, -1]), i32([T[2], T[0], T[2] - 1, 0]), st)
+        assert cache.error() == LL.CACHE_ERR_MISSING
+        assert torch.all(st[[0, 2, 3]] == 3) and torch.equal(st[1], want[0])   # (319 is in block 4: page 2 too)
+    st = torch.full((2, 2, M + 7, 16, 8), 3.0).cuda()
+    LL.loglinear_cache_store(cache, i32([0, 0]), i32([-1, T[0]]), st)
+    assert cache.error() == LL.CACHE_ERR_POSITION and torch.all(st[0] == 3) and torch.equal(st[1], want[0])
