@@ -481,7 +481,8 @@ typedef struct {
 
 /* Raised on the device by rows that are then left out (their slot and output as they were). */
 #define LL_CACHE_ERR_SLOT 1u      /* slot out of range (other than -1), or given to an earlier row */
-#define LL_CACHE_ERR_POSITION 2u  /* position outside the cache */
+#define LL_CACHE_ERR_POSITION 2u  /* position outside the cache, or before the end of the prompt that
+                                     was loaded, in a block with pages */
 #define LL_CACHE_ERR_PAGES 4u     /* no free page was left (the slot is left without it) */
 #define LL_CACHE_ERR_MISSING 8u   /* a page that the position needs is not there, or the page that
                                      a step would fold into is shared (not reserved) */

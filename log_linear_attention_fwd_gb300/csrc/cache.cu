@@ -139,6 +139,13 @@ __device__ __forceinline__ bool position_ok(const ll_cache& c, int64_t t) {
   return t >= 0 && t < ((int64_t)kW << c.levels) - 1;
 }
 
+// Whether a slot's pages, if it has any at n positions, have already decayed past there: a prompt
+// was loaded up to a later position of the block.
+__device__ __forceinline__ bool before_pages(const ll_cache& c, int s, int n) {
+  const int j = n >> kLogW;
+  return j && c.page_from[s * 2 + (j & 1)] > (n & (kW - 1));
+}
+
 // Gives the lowest free pages to the table entries want[0..count), in that order.
 __device__ void take_pages(const ll_cache& c, const int* want, int count) {
   int given = 0;
@@ -549,6 +556,7 @@ struct __align__(16) Item {
   float page_log[kMaxLevels], page_e[kMaxLevels], page_w[kMaxLevels];
   int page_at[kMaxLevels], page_lv[kMaxLevels];
   int kind, row, h, slot, pos, dest;  // kind: kRun, kSkip or kStop
+  unsigned why;                       // (split) what load_links found
   float log_a;
 };
 enum { kRun, kSkip, kStop };
@@ -640,8 +648,8 @@ __device__ __forceinline__ unsigned row_bad(const ll_cache& c, int s, int t) {
   return position_ok(c, t) ? 0 : LL_CACHE_ERR_POSITION;
 }
 
-// The item's decays and pages, by one warp; s and t are fine.  False where a page is missing.
-__device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a, int row, int h, int s,
+// The item's decays and pages, by one warp; s and t are fine.  Returns why the row cannot be served.
+__device__ __forceinline__ unsigned load_links(const ll_cache& c, const StepArgs& a, int row, int h, int s,
                                            int t, Item& it) {
   const int lane = threadIdx.x & 31, H = (int)c.H, M = (int)c.levels;
   const int64_t bh = (int64_t)row * H + h;
@@ -656,8 +664,9 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
   const float lam = here ? a.lam[bh * a.L + kLogW + 1 + lane] : 0.f;
   const float* wa = c.win_log_a + ((int64_t)s * H + h) * kW;
   const float x0 = lane < r ? wa[lane] : 0.f, x1 = lane + 32 < r ? wa[lane + 32] : 0.f;
+  const int from = c.page_from[s * 2 + par];
   float since;
-  block_decays(x0, x1, r, c.page_from[s * 2 + par], it.tok, &since);
+  block_decays(x0, x1, r, from, it.tok, &since);
   it.tok[lane] = expf(it.tok[lane] + la);
   it.tok[lane + 32] = lane + 32 == r ? 1.f : expf(it.tok[lane + 32] + la);  // a fold's own token: 1
   if (here) {
@@ -676,7 +685,8 @@ __device__ __forceinline__ bool load_links(const ll_cache& c, const StepArgs& a,
     it.slot = s;
     it.pos = t;
   }
-  return __all_sync(0xffffffffu, e >= 0 && e < c.n_pages && !shared);
+  if (__any_sync(0xffffffffu, e < 0 || e >= c.n_pages || shared)) return LL_CACHE_ERR_MISSING;
+  return j && from > r ? LL_CACHE_ERR_POSITION : 0;  // (as before_pages)
 }
 
 constexpr int kPad = 8;  // elements
@@ -854,13 +864,14 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
     const unsigned bad = s == -1 ? 0 : row_bad(c, s, t);
     const bool run = s != -1 && !bad;
     __syncthreads();  // the barriers are there
-    bool twice = false, there = true;
+    bool twice = false;
     if (run) {
       if (w == kProducer) {
         if (lane == 0) bring_window(s, h, part_of<T>(t, dk, dv, Z, sp));
         brought = true;
       } else if (w == kScheduler + 1) {
-        there = load_links(c, a, row, h, s, t, sm.item[0]);
+        const unsigned why = load_links(c, a, row, h, s, t, sm.item[0]);
+        if (lane == 0) sm.item[0].why = why;
       } else if (w < kStepWarps) {
         Vectors<T, kConsumers> x;
         x.fetch(c, a, row, h, s, tid);
@@ -869,9 +880,8 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
       }
     }
     twice = __syncthreads_or(twice);
-    there = __syncthreads_and(there);
     if (tid == 0) {
-      const unsigned why = bad ? bad : twice ? LL_CACHE_ERR_SLOT : there ? 0 : LL_CACHE_ERR_MISSING;
+      const unsigned why = bad ? bad : twice ? LL_CACHE_ERR_SLOT : run ? sm.item[0].why : 0;
       if (why && sp == 0 && h == 0) raise(c, why);
       sm.item[0].kind = run && !why ? kRun : kSkip;
     }
@@ -898,7 +908,7 @@ __global__ void __launch_bounds__(kQueue ? kQueueThreads : kSplitThreads, 2)
           if (!why) {
             Vectors<T, 32> x;
             x.fetch(c, a, row, h, s, lane);
-            if (!load_links(c, a, row, h, s, t, it)) why = LL_CACHE_ERR_MISSING;
+            why = load_links(c, a, row, h, s, t, it);
             x.put(c, lane, it);
             if (__any_sync(0xffffffffu, x.twice)) why = LL_CACHE_ERR_SLOT;
           }
@@ -1213,7 +1223,9 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
   int held = 0;
   if (!bad && lane < M && (j >> lane & 1)) {
     held = c.page_table[(int64_t)s * M + lane];
+    const bool before = before_pages(c, s, n);
     if (held < 0 || held >= c.n_pages) bad = LL_CACHE_ERR_MISSING;
+    else if (before) bad = LL_CACHE_ERR_POSITION;
   }
   if (__any_sync(0xffffffffu, bad)) {
     if (bad && tid < 32 && h == 0 && level == 0) raise(c, bad);
@@ -1291,7 +1303,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_store_kernel(
 // ---------------------------------------------------------------- fork
 
 // A row is left out where its target is not its own, its source is not a slot or is some row's
-// target, its position is outside the cache, or a page that it needs of its source is not there.
+// target, its position is outside the cache or one that its pages are past, or a page that it needs of its source is not there.
 // owner: the targets' rows, ~row of those that are left out, kNone for sources.
 __device__ __forceinline__ unsigned fork_bad(const ll_cache& c, const int* owner, int s, int t) {
   if (s < 0 || s >= c.slots || __ldcg(owner + s) != kNone) return LL_CACHE_ERR_SLOT;
@@ -1321,7 +1333,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ll_cache 
       if (m == 0) raise(c, bad);
     } else if ((t >> kLogW) >> m & 1) {
       const int page = c.page_table[(int64_t)s * M + m];
+      const bool before = before_pages(c, s, t);
       if (page < 0 || page >= c.n_pages) raise(c, bad = LL_CACHE_ERR_MISSING);
+      else if (before) raise(c, bad = LL_CACHE_ERR_POSITION);
     }
     if (bad) sc.owner[d] = ~(int)r;
   }

@@ -637,3 +637,42 @@ def test_a_store_without_its_pages_is_left_out(LL):
     st = torch.full((2, 2, M + 7, 16, 8), 3.0).cuda()
     LL.loglinear_cache_store(cache, i32([0, 0]), i32([-1, T[0]]), st)
     assert cache.error() == LL.CACHE_ERR_POSITION and torch.all(st[0] == 3) and torch.equal(st[1], want[0])
+
+
+@pytest.mark.parametrize("rows", [2, 90])
+def test_going_back_before_the_load(LL, rows):
+    """A loaded prompt's pages have decayed to its end: a position before it, in a block with
+    pages, is refused by the step, the store and the fork, and changes nothing."""
+    H, dk, dv, M, T = 2, 16, 8, 3, 100
+    L = M + 7
+    S, tok = dense_inputs(T, rows, H, dk, dv, L, seed=T)
+    prompt = tok(64)
+    S = block_states(S, prompt, T)
+    x = tok(3)
+    cache = poison(LL.LogLinearCache.empty(rows + 2, 2 * rows, H, dk, dv, M, dtype=torch.float32))
+    slots = torch.arange(rows, dtype=torch.int32).cuda()
+    c = lambda t: t.cuda()  # noqa: E731
+    LL.loglinear_cache_load(cache, slots, T, c(S), c(prompt["k"]), c(prompt["v"]), c(prompt["log_a"]))
+    arg = lambda i: [x[k][:, i].contiguous().cuda() for k in ("q", "k", "v", "log_a", "lam")]  # noqa: E731
+    one = LL.loglinear_cache_step(cache, slots, torch.full_like(slots, T), *arg(0))
+    LL.loglinear_cache_step(cache, slots, torch.full_like(slots, T + 1), *arg(1))
+    assert cache.error() == 0
+    snap = snapshot(cache)
+    pos = torch.full_like(slots, T)
+    pos[1] = T - 1
+    out = torch.full_like(one, 7.0)
+    LL.loglinear_cache_step(cache, slots, pos, *arg(0), out=out)
+    assert cache.error() == LL.CACHE_ERR_POSITION and torch.all(out[1] == 7)
+    assert torch.equal(out[0], one[0]) and torch.equal(out[2:], one[2:]) and same(snap, snapshot(cache))
+    st = torch.full((rows, H, L, dk, dv), 3.0).cuda()
+    LL.loglinear_cache_store(cache, slots, pos, st)
+    assert cache.error() == LL.CACHE_ERR_POSITION and torch.all(st[1] == 3)
+    check(st[0].cpu(), S[0].numpy())
+    LL.loglinear_cache_fork(cache, slots[:2].contiguous(), i32([rows, rows + 1]), pos[:2].contiguous())
+    assert cache.error() == LL.CACHE_ERR_POSITION
+    assert cache.page_table[rows, 0] == cache.page_table[0, 0] and torch.all(cache.page_table[rows + 1] == -1)
+    # in block 0 there are no pages, so any position of it may come again
+    LL.loglinear_cache_load(cache, slots[:1].contiguous(), 36, c(S[:1]), c(prompt["k"][:1]), c(prompt["v"][:1]),
+                            c(prompt["log_a"][:1]))
+    LL.loglinear_cache_step(cache, slots[:1].contiguous(), i32([20]), *(t[:1].contiguous() for t in arg(2)))
+    assert cache.error() == 0
