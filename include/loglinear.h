@@ -516,7 +516,11 @@ LL_API int loglinear_cache_reserve(const ll_cache* cache, const int32_t* slots,
  *     out = sum_{s <= t} lambda[level(t, s)] exp(sum_{u=s+1..t} log_a_u) (q_t . k_s) v_s,
  * with the sum over whole blocks taken from the pages.  The token joins the slot's block; at a
  * block's last position the pages below level ctz(j + 1) and the block are folded into the page
- * of that level.  Repeating a step at the same position repeats its result.
+ * of that level.  Repeating a step at the same position repeats its result, and a slot may go back
+ * to earlier positions of the block (rejected drafts), its end included; but only until a call has
+ * been made for it at a position of the next block, whose tokens replace the block's and whose
+ * reservation gives up its pages, and not to before the end of a loaded prompt where the block
+ * has pages.  Drafts that cross a block's end belong on a fork.
  *   q, k   [n, Hqk, dk] cache dtype;  v [n, H, dv] cache dtype
  *   log_a  [n, H] fp32 or NULL (no decay);  lambda [n, H, L] fp32, L >= M + 7
  *   out    [n, H, dv] out_dtype

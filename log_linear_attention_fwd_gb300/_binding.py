@@ -744,7 +744,9 @@ def loglinear_cache_step(cache, slots, pos, q, k, v, log_a, lam, out=None, out_d
                          stream=None):
     """One decode step for n rows, row i being slot slots[i] at position pos[i].  q, k [n,Hqk,dk],
     v [n,H,dv] in the cache's dtype; log_a [n,H] fp32 or None; lam [n,H,L] fp32, L >= levels + 7.
-    Rows with slot -1 are left out (their out is not written).  Returns out [n,H,dv]."""
+    Rows with slot -1 are left out (their out is not written).  A slot may go back to earlier
+    positions of its block until it has been called for in the next one (drafts that cross a block's
+    end: on a fork).  Returns out [n,H,dv]."""
     dev, n, L = cache._dev(), slots.numel(), lam.shape[-1]
     dt, H, qk = cache.dtype, cache.heads, (n, cache.qk_heads, cache.dk)
     if out is None:

@@ -676,3 +676,34 @@ def test_going_back_before_the_load(LL, rows):
                             c(prompt["log_a"][:1]))
     LL.loglinear_cache_step(cache, slots[:1].contiguous(), i32([20]), *(t[:1].contiguous() for t in arg(2)))
     assert cache.error() == 0
+
+
+@pytest.mark.parametrize("at", [70, 127])
+def test_going_back_inside_a_block(LL, at):
+    """Positions of the current block may come again with other tokens, its end among them."""
+    cache, x, _ = filled(LL, n=1, T=(128,), more=60)           # block 1 has been folded
+    back = {k: v.clone() for k, v in x.items()}
+    g = torch.Generator().manual_seed(1)
+    for k in ("q", "k", "v"):
+        back[k][:, at:] = torch.randn(back[k][:, at:].shape, generator=g)
+    want = oracle.forward_direct(*(back[k] for k in ("q", "k", "v", "log_a", "lam")))
+    got, _ = decode(LL, cache, back, [0], [at], 188 - at)
+    check(got.cpu(), want[:, at:188])
+    invariants(cache, {0: 188})
+    assert cache.error() == 0
+
+
+def test_a_draft_across_a_blocks_end_on_a_fork(LL):
+    """Drafted tokens that cross a block's end are decoded on a fork; rejected, the slot goes on
+    from where it was."""
+    cache, x, _ = filled(LL, n=1, T=(126,), more=60)
+    draft = {k: v.clone() for k, v in x.items()}
+    draft["v"][:, 126:] = draft["v"][:, :draft["v"].shape[1] - 126]
+    LL.loglinear_cache_fork(cache, i32([0]), i32([5]), i32([126]))
+    got, _ = decode(LL, cache, draft, [5], [126], 6)
+    check(got.cpu(), oracle.forward_direct(*(draft[k] for k in ("q", "k", "v", "log_a", "lam")))[:, 126:132])
+    LL.loglinear_cache_free(cache, i32([5]))
+    got, _ = decode(LL, cache, x, [0], [126], 60)
+    check(got.cpu(), oracle.forward_direct(*(x[k] for k in ("q", "k", "v", "log_a", "lam")))[:, 126:186])
+    invariants(cache, {0: 186})
+    assert cache.error() == 0
