@@ -108,21 +108,24 @@ __device__ int block_scan(int v, int* total) {
 }
 
 // Gives each named slot to the lowest row that names it.  Rows that name a slot out of range
-// other than -1, or one that an earlier row has, raise the error word.
-__device__ void claim_slots(const ll_cache& c, const int* slots, int64_t n, int* owner) {
+// other than -1, or one that an earlier row has, raise the error word.  src: rows with -1 there
+// name none.
+__device__ void claim_slots(const ll_cache& c, const int* slots, int64_t n, int* owner,
+                            const int* src = nullptr) {
+  auto slot_of = [&](int64_t r) { return src && src[r] == -1 ? -1 : slots[r]; };
   for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-    const int s = slots[r];
+    const int s = slot_of(r);
     if (s >= 0 && s < c.slots) owner[s] = kNone;
   }
   __syncthreads();
   for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-    const int s = slots[r];
+    const int s = slot_of(r);
     if (s >= 0 && s < c.slots) atomicMin(owner + s, (int)r);
     else if (s != -1) raise(c, LL_CACHE_ERR_SLOT);
   }
   __syncthreads();
   for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-    const int s = slots[r];
+    const int s = slot_of(r);
     if (s >= 0 && s < c.slots && __ldcg(owner + s) != r) raise(c, LL_CACHE_ERR_SLOT);
   }
 }
@@ -1319,13 +1322,13 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ll_cache 
   for (int64_t r = threadIdx.x; r < n; r += kPlanThreads)
     if (src[r] >= 0 && src[r] < c.slots) sc.owner[src[r]] = kNone;
   __syncthreads();
-  claim_slots(c, dst, n, sc.owner);
+  claim_slots(c, dst, n, sc.owner, src);
   __syncthreads();
   // nothing changes before it is settled which rows are served
   for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
     const int64_t r = k / M;
     const int m = (int)(k - r * M), s = src[r], d = dst[r], t = pos[r];
-    if (d < 0 || d >= c.slots) continue;
+    if (s == -1 || d < 0 || d >= c.slots) continue;
     const int o = __ldcg(sc.owner + d);
     if (o != r && o != ~(int)r) continue;
     unsigned bad = fork_bad(c, sc.owner, s, t);
@@ -1344,7 +1347,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ll_cache 
   for (int64_t k = threadIdx.x; k < n * M; k += kPlanThreads) {
     const int64_t r = k / M;
     const int m = (int)(k - r * M), s = src[r], d = dst[r], t = pos[r];
-    if (!owns(c, sc.owner, d, r)) continue;
+    if (s == -1 || !owns(c, sc.owner, d, r)) continue;  // (-1: nobody's owner was settled here)
     int* e = c.page_table + (int64_t)d * M + m;
     const int page = (t >> kLogW) >> m & 1 ? c.page_table[(int64_t)s * M + m] : -1;
     drop_page(c, *e);
@@ -1367,7 +1370,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(ll_cache c,
   wait_for_previous();
   const int h = (int)(blockIdx.x - row * H), s = src[row], d = dst[row], t = pos[row];
   const int* owner = scratch_of(c).owner;
-  if (!owns(c, owner, d, row)) return;
+  if (s == -1 || !owns(c, owner, d, row)) return;
   const int j = t >> kLogW, r = t & (kW - 1), par = j & 1;
   copy_rows(static_cast<T*>(c.win_v) + ((int64_t)d * H + h) * kW * dv,
             static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv, r * dv, 1, r * dv);

@@ -707,3 +707,23 @@ def test_a_draft_across_a_blocks_end_on_a_fork(LL):
     check(got.cpu(), oracle.forward_direct(*(x[k] for k in ("q", "k", "v", "log_a", "lam")))[:, 126:186])
     invariants(cache, {0: 186})
     assert cache.error() == 0
+
+
+def test_fork_rows_without_a_source_are_padding(LL):
+    """-1 as a source leaves the row out, as it does as a target: no error, and the target is
+    free for another row."""
+    cache, x, T = filled(LL)
+    snap = snapshot(cache)
+    LL.loglinear_cache_fork(cache, i32([-1, 1, 0, -1]), i32([5, 5, -1, -1]), i32([0, T[1], T[0], -9]))
+    assert cache.error() == 0 and torch.equal(cache.page_table[5], cache.page_table[1])
+    assert torch.equal(cache.page_table[:5], snap[1][:5])
+    invariants(cache, {5: T[1], 1: T[1]})
+    want = oracle.forward_direct(x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+    got, _ = decode(LL, cache, {k: v[1:2] for k, v in x.items()}, [5], [T[1]], 10)
+    check(got[0].cpu(), want[1, T[1]:T[1] + 10])
+    # a slot that the row had as its target in the call before, which is not its own now
+    now = snapshot(cache)
+    LL.loglinear_cache_fork(cache, i32([0, -1]), i32([6, 5]), i32([T[0], T[1]]))
+    assert cache.error() == 0 and torch.equal(cache.page_table[:6], now[1][:6])
+    assert same([t[5] for t in now[3:]], [t[5] for t in snapshot(cache)[3:]])
+    invariants(cache, {6: T[0], 5: T[1] + 10})
