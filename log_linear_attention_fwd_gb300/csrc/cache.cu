@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
       const int s = slot_of(r), t = pos_of(r);
       if (s < 0 || (t & (kW - 1)) != kW - 1) continue;
       int* e = c.page_table + (int64_t)s * M + __ffs((t >> kLogW) + 1) - 1;
-      if (*e >= 0 && *e < c.n_pages && __ldcg(c.refcount + *e) != 1) *e = -2 - *e;
+      if (*e < 0 || *e >= c.n_pages) *e = -1;  // (a table that was overwritten: no page, and no mark)
+      else if (__ldcg(c.refcount + *e) != 1) *e = -2 - *e;
     }
     __syncthreads();
   }
@@ -237,14 +238,15 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
     const int64_t r = k / M;
     const int m = (int)(k - r * M), s = slot_of(r);
     if (s < 0) continue;
-    bool keep = false;
+    bool keep = false, to = false;
     if (pos) {
       const int t = pos_of(r), j = t >> kLogW;
-      keep = (j >> m) & 1 || ((t & (kW - 1)) == kW - 1 && m == __ffs(j + 1) - 1);
+      to = (t & (kW - 1)) == kW - 1 && m == __ffs(j + 1) - 1;
+      keep = to || (j >> m) & 1;
     }
     int* e = c.page_table + (int64_t)s * M + m;
     if (*e < -1 || (!keep && *e >= 0)) {
-      drop_page(c, *e < -1 ? -2 - *e : *e);
+      drop_page(c, to ? -2 - *e : *e);  // (below -1 elsewhere: no page)
       *e = -1;
     }
   }

@@ -727,3 +727,23 @@ def test_fork_rows_without_a_source_are_padding(LL):
     assert cache.error() == 0 and torch.equal(cache.page_table[:6], now[1][:6])
     assert same([t[5] for t in now[3:]], [t[5] for t in snapshot(cache)[3:]])
     invariants(cache, {6: T[0], 5: T[1] + 10})
+
+
+def test_a_table_entry_that_is_no_page_counts_for_none(LL):
+    """Entries below -1 and past the pool in a table that was overwritten: whoever holds the other
+    pages keeps them."""
+    cache, x, T = filled(LL)
+    for call in (lambda: LL.loglinear_cache_free(cache, i32([2])),
+                 lambda: LL.loglinear_cache_reserve(cache, i32([2]), i32([383]))):
+        cache.page_table[2] = i32([-2, 10 ** 6, -3, -4])       # (383: block 5 is live and folds into page 1)
+        count = cache.refcount.clone()
+        call()
+        taken = cache.page_table[2][cache.page_table[2] >= 0].tolist()
+        taken = [e for e in taken if e < len(count)]
+        assert all(count[e] == 0 for e in taken) and len(taken) <= 1
+        count[taken] = 1
+        assert torch.equal(cache.refcount, count) and cache.error() == 0
+    want = oracle.forward_direct(x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+    got, _ = decode(LL, cache, {k: v[:2] for k, v in x.items()}, [0, 1], T[:2], 70)
+    check(got[0].cpu(), want[0, T[0]:T[0] + 70])
+    check(got[1].cpu(), want[1, T[1]:T[1] + 70])
