@@ -751,7 +751,10 @@ __device__ __forceinline__ bool consumer_any(bool x) {
 // The products of a fold's 64 tokens for state rows [k0, k1) (a multiple of 16), by the consumer
 // warps, to D [dk][dv]: sum over s of k_s (e_s v_s)^T on the tensor cores, bf16 keys as they are
 // and e v split into three bf16 parts, which together are its fp32 value; products and sums
-// are fp32.  (Multiply-adds took 10 us more per fold, the tail of a ragged batch.)
+// are fp32.  (Multiply-adds took 10 us more per fold, the tail of a ragged batch.)  Infinities come
+// out as in the sum itself, where the parts' products are all of one sign: the parts are cut off
+// towards zero, and what is left of a value that is not 0 is never 0 or NaN (infinity less
+// itself) but at least the least bf16, whose product with a key is below any normal number.
 __device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], const __nv_bfloat16* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -765,12 +768,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t take_bf16(float2& x) {  // x's leading bf16 parts; x keeps the rest
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-  const float2 f = __bfloat1622float2(h);
-  x.x -= f.x;
-  x.y -= f.y;
-  return *reinterpret_cast<const uint32_t*>(&h);
+// x's leading bf16 parts (x >= 0); x keeps the rest, at least `least`.
+__device__ __forceinline__ uint32_t take_bf16(float2& x, float2 least) {
+  uint32_t h;
+  asm("cvt.rz.bf16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(x.x), "f"(x.y));
+  const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h));
+  x = make_float2(fmaxf(x.x - f.x, least.x), fmaxf(x.y - f.y, least.y));
+  return h;
 }
 __device__ __forceinline__ void fold_tokens(const __nv_bfloat16* wks, const __nv_bfloat16* wvs,
                                             const float* tok, int kp, int vp, int dv, int k0, int k1,
@@ -790,9 +794,11 @@ __device__ __forceinline__ void fold_tokens(const __nv_bfloat16* wks, const __nv
         const int s = 16 * ks + 8 * u + i;
         float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[u]));
         const float2 e = *reinterpret_cast<const float2*>(tok + s);
-        x = make_float2(x.x * e.x, x.y * e.y);
+        x = make_float2(fabsf(x.x * e.x), fabsf(x.y * e.y));
+        const float2 least = make_float2(fminf(x.x, 0x1p-133f), fminf(x.y, 0x1p-133f));
+        const uint32_t sign = r[u] & 0x80008000u;
 #pragma unroll
-        for (int v = 0; v < 3; ++v) b[ks + (u >> 1)][v][u & 1] = take_bf16(x);
+        for (int v = 0; v < 3; ++v) b[ks + (u >> 1)][v][u & 1] = take_bf16(x, least) | sign;
       }
     }
     for (int d = k0; d < k1; d += 16) {

@@ -747,3 +747,47 @@ def test_a_table_entry_that_is_no_page_counts_for_none(LL):
     got, _ = decode(LL, cache, {k: v[:2] for k, v in x.items()}, [0, 1], T[:2], 70)
     check(got[0].cpu(), want[0, T[0]:T[0] + 70])
     check(got[1].cpu(), want[1, T[1]:T[1] + 70])
+
+
+@pytest.mark.parametrize("rows", [1, 160])
+@pytest.mark.parametrize("what", ["v", "k", "new v", "new k", "nan"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_fold_of_infinities(LL, dtype, what, rows):
+    """An infinite key or value: the page has its infinities where sum_s e k_s v_s has them, NaN
+    where that has, and the other elements whole."""
+    H, dk, dv, M = 1, 32, 16, 2
+    g = torch.Generator().manual_seed(7)
+    sign = lambda *s: (0.5 + torch.rand(*s, generator=g)) * (torch.randint(0, 2, s, generator=g) * 2 - 1)  # noqa: E731
+    k, v = (sign(1, 64, H, d).to(DT[dtype]) for d in (dk, dv))   # no zeros but one column of values
+    v[..., 12] = 0.0
+    la = -0.1 * torch.rand(1, 64, H, generator=g)
+    at = 63 if "new" in what else 21
+    if "v" in what:
+        v[0, at, 0, 3], v[0, at, 0, 9] = float("inf"), -float("inf")
+    elif "k" in what:
+        k[0, at, 0, 5], k[0, at, 0, 30] = float("inf"), -float("inf")
+    else:
+        k[0, at, 0, 5] = float("nan")
+    w = np.exp(to64(la[0, :, 0]).sum() - np.cumsum(to64(la[0, :, 0])))
+    with np.errstate(invalid="ignore"):
+        want = sum(w[s] * np.outer(to64(k[0, s, 0]), to64(v[0, s, 0])) for s in range(64))
+    cache = poison(LL.LogLinearCache.empty(rows, rows, H, dk, dv, M, dtype=DT[dtype]))
+    slots = torch.arange(rows, dtype=torch.int32).cuda()
+    rep = lambda t: t.expand(rows, *t.shape[1:]).contiguous().cuda()  # noqa: E731
+    for t in (slice(0, 63), slice(63, 64)):
+        if t.start == 0:
+            S = torch.zeros(rows, H, M + 7, dk, dv).cuda()
+            LL.loglinear_cache_load(cache, slots, 63, S, rep(k[:, t]), rep(v[:, t]), rep(la[:, t]))
+        else:
+            p = torch.full_like(slots, 63)
+            LL.loglinear_cache_reserve(cache, slots, p)
+            lam = torch.ones(rows, H, M + 7).cuda()
+            LL.loglinear_cache_step(cache, slots, p, rep(k[:, 63]), rep(k[:, 63]), rep(v[:, 63]), rep(la[:, 63]), lam)
+    assert cache.error() == 0
+    pages = cache.pages[cache.page_table[:, 0].long()][:, 0].cpu()
+    for page in pages[:: max(1, rows // 4)]:
+        got = to64(page)
+        fin = np.isfinite(want)
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~fin], want[~fin], equal_nan=True)
+        assert np.all(got[want == 0] == 0) and np.sum(want == 0) >= dk - 2
+        check(torch.from_numpy(got[fin]).float(), want[fin])
