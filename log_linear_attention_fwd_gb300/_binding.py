@@ -713,11 +713,14 @@ class LogLinearCache:
                    win_log_a=new(slots, H, CACHE_BLOCK), page_log=new(slots, 2, levels, H),
                    page_from=new(slots, 2, dt=i32))
 
-    def error(self) -> int:
-        """Reads and clears the cache's error word (CACHE_ERR_* bits; synchronises)."""
-        bits = int(self.error_word.item())
-        if bits:
-            self.error_word.zero_()
+    def error(self, stream=None) -> int:
+        """Reads and clears the cache's error word (CACHE_ERR_* bits) behind the calls made so far on
+        `stream` (None: the current one), which it synchronises.  Calls that went to another
+        stream are only seen once that one is ordered before it."""
+        with torch.cuda.stream(stream):  # (None: no change)
+            bits = int(self.error_word.item())
+            if bits:
+                self.error_word.zero_()
         return bits
 
     def _dev(self):

@@ -791,3 +791,17 @@ def test_a_fold_of_infinities(LL, dtype, what, rows):
         assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~fin], want[~fin], equal_nan=True)
         assert np.all(got[want == 0] == 0) and np.sum(want == 0) >= dk - 2
         check(torch.from_numpy(got[fin]).float(), want[fin])
+
+
+def test_the_error_word_of_calls_on_another_stream(LL):
+    """Read and cleared on the stream that the calls went to, behind them."""
+    cache, x, T = filled(LL)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s = i32([99])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                          # about 10 ms
+    LL.loglinear_cache_free(cache, s, stream=side)
+    assert cache.error(stream=side) == LL.CACHE_ERR_SLOT
+    assert cache.error() == 0 and cache.error(stream=side) == 0
