@@ -395,7 +395,10 @@ LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
  *   out        [B, T, D] out_dtype: h_t
  *   state_out  NULL, or [N, D] fp32: the state after the last token (h0 for an empty sequence);
  *              may be h0 itself
- * State, gates and sums are fp32; out is rounded once.
+ * State, gates and sums are fp32; out is rounded once.  Gates below 2^-126 are 0.  An infinite state
+ * stays infinite through gates that are not 0, however many, and is NaN behind one that is, as
+ * token by token; but runs of tokens are summed before the state that comes into them is added, so
+ * what only passes fp32's range in between may do so in one order and not in the other.
  * Errors: LL_ERR_INVALID (null pointer, negative size or stride, unknown scale, cu_seqlens with
  * B other than 1), LL_ERR_DTYPE, LL_ERR_UNSUPPORTED (T or N > 2^30, B or D or B * ceil(D / 32) above
  * 2^27), LL_ERR_ALIGN (a pointer not aligned to its element), LL_ERR_CUDA.  B, T or D = 0 is a no-op, but that state_out still receives h0.

@@ -241,10 +241,34 @@ __device__ __forceinline__ void fill(Tile<T, S>& dst, const T* src, int64_t stri
 __device__ __forceinline__ float apply(float A, float H, float c) {
   return signbit(A) ? H : fmaf(A, c, H);
 }
+// A product of gates that are not 0 is not 0 here, but at least kLeast: an infinite carry stays
+// infinite through gates however small, and becomes NaN through a gate of 0, as token by token.
+// To a finite carry's part that makes a difference of at most 2^-149 of it.
+constexpr float kLeast = 0x1p-149f;
 // (A, H) after m, into m.
 __device__ __forceinline__ void then(float2& m, float2 n) {
   m.y = apply(n.x, n.y, m.y);
-  m.x = signbit(n.x) || signbit(m.x) ? -0.f : n.x * m.x;
+  float t, p;  // t: the smaller factor, -0 where either is; p: a NaN stays one
+  asm("min.f32 %0, %1, %2;" : "=f"(t) : "f"(n.x), "f"(m.x));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(p) : "f"(n.x * m.x), "f"(fminf(t, kLeast)));
+  m.x = __uint_as_float(__float_as_uint(p) | (__float_as_uint(t) & 0x80000000u));
+}
+// Sets the products of the S gates of a segment, to[0].x and to[1].x, to kLeast where they came out as
+// 0 and no gate is.  (Rare, and behind the store of the products: the backward's registers.)
+template <int S>
+__device__ __forceinline__ void keep_products(float2* to, f32x2 A, const f32x2 (&a)[S]) {
+  const float2 p = unpack(A);
+  const bool x = __float_as_uint(p.x) == 0, y = __float_as_uint(p.y) == 0;  // (-0 marks a reset)
+  if (!x && !y) return;
+  bool zx = false, zy = false;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const float2 g = unpack(a[s]);
+    zx |= g.x == 0.f;
+    zy |= g.y == 0.f;
+  }
+  if (x && !zx) to[0].x = kLeast;
+  if (y && !zy) to[1].x = kLeast;
 }
 
 // ---------------------------------------------------------------- sequences
@@ -541,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_fwd_kernel(GlrArgs p, Ge
     }
     const float2 A1 = unpack(A), H1 = unpack(H);
     *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, H1.x, A1.y, H1.y);
+    keep_products<S>(&sm.seg[seg][cl], A, a);
     link_step(sm, maps, k, Z, rank, c, [&](int g) { return spans(k + 1, g); });
     f32x2 h = segment_carry(sm, seg, cl);
     OutT* o = out + (int64_t)lo * p.D;
@@ -692,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) glr_bwd_kernel(GlrArgs p, Ge
     }
     const float2 A1 = unpack(A), E1 = unpack(E);
     *reinterpret_cast<float4*>(&sm.seg[seg][cl]) = make_float4(A1.x, E1.x, A1.y, E1.y);
+    keep_products<S>(&sm.seg[seg][cl], A, a);
     link_step(sm, maps, k, Z, rank, carry, [&](int g) { return spans(k + 1, g); });
     f32x2 c = segment_carry(sm, seg, cl);
     GradT* ox = dx + (int64_t)(lo + S - 1) * p.D;

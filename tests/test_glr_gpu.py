@@ -396,3 +396,31 @@ def test_headline_size(LL):
     w = oracle.glr_backward(cut(x), cut(la), cut(out), cut(dout), "sqrt")
     check(cut(dx).cpu(), w[0])
     check(cut(dla).cpu(), w[1])
+
+
+@pytest.mark.parametrize("la0", [-1.5, -60.0])
+@pytest.mark.parametrize("T,D,packed", [(70, 3, False), (3000, 40, False), (700, 6, True)])
+def test_infinite_states_stay_infinite(LL, la0, T, D, packed):
+    """An infinity times gates that are not 0 is one, however many: also where the gates' product
+    is below the type's range.  Through a gate of 0 it becomes NaN."""
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(1, T, D, generator=g)
+    la = la0 * (0.75 + 0.25 * torch.rand(1, T, D, generator=g))
+    dout = torch.randn(1, T, D, generator=g)
+    x[0, 10, 0], x[0, 3, 1], dout[0, T - 5, 0], dout[0, T - 2, 1] = float("inf"), -float("inf"), float("inf"), -float("inf")
+    la[0, T // 2, 1] = -float("inf")
+    cu = [0, T // 3, T // 3, T - 1] if packed else None
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32).cuda()
+    xd, ld, dd = dev(x, la, dout)
+    out = LL.loglinear_glr_fwd(xd, ld, cu_seqlens=c, scale="one_minus")
+    dx, dla, _ = LL.loglinear_glr_bwd(xd, ld, out, dd, cu_seqlens=c, scale="one_minus")
+    n = T if cu is None else cu[-1]
+    with np.errstate(invalid="ignore"):
+        want, _ = oracle.glr_forward(x, la, "one_minus", cu=cu)
+        grads = oracle.glr_backward(x, la, out, dout, "one_minus", cu=cu)
+    for got, w, name in ((out, want, "out"), (dx, grads[0], "dx"), (dla, grads[1], "dlog_a")):
+        got, w = to64(got)[:, :n], w[:, :n]
+        fin = np.isfinite(w)
+        assert np.array_equal(got[~fin], w[~fin], equal_nan=True), name
+        check(torch.from_numpy(got[fin]).float(), w[fin], name)
+    assert np.isinf(want[0, T // 3 - 1, 0]) and np.isinf(to64(dx)[0, 2 * T // 3, 0])
