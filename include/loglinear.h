@@ -387,7 +387,8 @@ LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
  *   cu_seqlens NULL: B sequences of T tokens.  Else device int32 [N + 1], 0 = cu[0] <= cu[1]
  *              <= ... <= T, with B = 1: sequence n holds tokens cu[n] .. cu[n+1] - 1, and
  *              nothing passes from one to the next, infinities and NaN included.  Rows
- *              behind cu[N] are neither read nor written.  The library does not read the bounds
+ *              behind cu[N] may hold anything, and their outputs (and gradients) are left as
+ *              they were.  The library does not read the bounds
  *              on the host; bounds out of order give wrong sequences, but no access outside
  *              the arrays.
  *   N          number of sequences (ignored without cu_seqlens: B)

@@ -584,8 +584,8 @@ def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None
     """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + b_t x_t per channel; x, log_a
     [B,T,D] (may be views with contiguous channels), log_a fp32 or x's dtype; scale: b = 1
     ("none"), 1 - a ("one_minus") or sqrt(1 - a^2) ("sqrt").  cu_seqlens int32 [N+1] packs N
-    sequences into B = 1.  h0, state: [N,D] fp32 first states and, when given, where the last
-    ones go.  Returns out [B,T,D]."""
+    sequences into B = 1; rows of out that none of them has are not written.  h0, state: [N,D] fp32
+    first states and, when given, where the last ones go.  Returns out [B,T,D]."""
     shape = B, T, D = x.shape
     dev = _current_device_of("x", x)
     xp, xs = _glr_input("x", x, shape, dev)
@@ -605,10 +605,12 @@ def loglinear_glr_fwd(x, log_a, h0=None, cu_seqlens=None, scale="none", out=None
 
 
 def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none", dstate=None,
-                      stream=None):
+                      stream=None, dx=None, dlog_a=None, dh0=None):
     """Gradients of loglinear_glr_fwd: out is its result, dout (same dtype) the gradient of it,
     dstate [N,D] fp32 that of the last states.  Returns (dx, dlog_a, dh0); dx in dout's dtype,
-    dlog_a in log_a's, dh0 fp32 (None without h0).  x may be None with scale "none"."""
+    dlog_a in log_a's, dh0 fp32 (None without h0; dh0 may be dstate itself).  x may be None with
+    scale "none".  Rows of dx and dlog_a that no sequence of cu_seqlens has are not written: give
+    both, zeroed once, where a padded batch's gradients go on as a whole."""
     shape = B, T, D = log_a.shape
     dev = _current_device_of("log_a", log_a)
     xp, xs = _glr_input("x", x, shape, dev)
@@ -619,17 +621,22 @@ def loglinear_glr_bwd(x, log_a, out, dout, h0=None, cu_seqlens=None, scale="none
     hp = _at("h0", h0, torch.float32, (N, D), dev)
     sp = _at("dstate", dstate, torch.float32, (N, D), dev)
     cp = _at("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
-    dx = _empty(stream, B, T, D, device=out.device, dtype=dout.dtype)
-    dla = _empty(stream, B, T, D, device=out.device, dtype=log_a.dtype)
-    dh0 = None if h0 is None else _empty(stream, N, D, device=out.device, dtype=torch.float32)
+    if dx is None:
+        dx = _empty(stream, B, T, D, device=out.device, dtype=dout.dtype)
+    if dlog_a is None:
+        dlog_a = _empty(stream, B, T, D, device=out.device, dtype=log_a.dtype)
+    if dh0 is None and h0 is not None:
+        dh0 = _empty(stream, N, D, device=out.device, dtype=torch.float32)
     gate = _dtype_code(log_a)
-    st = _lib.loglinear_glr_bwd(xp, xs, lp, ls, hp, cp, N, op, gp, sp, dx.data_ptr(),
-                                dla.data_ptr(), None if dh0 is None else dh0.data_ptr(), B, T, D,
+    st = _lib.loglinear_glr_bwd(xp, xs, lp, ls, hp, cp, N, op, gp, sp,
+                                _at("dx", dx, dout.dtype, shape, dev),
+                                _at("dlog_a", dlog_a, log_a.dtype, shape, dev),
+                                _at("dh0", dh0, torch.float32, (N, D), dev), B, T, D,
                                 gate if x is None else _dtype_code(x), gate, _dtype_code(out),
                                 GLR_SCALES[scale], _raw_stream(stream, dev))
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_glr_bwd")
-    return dx, dla, dh0
+    return dx, dlog_a, dh0
 
 
 def loglinear_glr_step(state, x, log_a, slots=None, scale="none", out=None, out_dtype=None,

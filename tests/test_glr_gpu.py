@@ -424,3 +424,24 @@ def test_infinite_states_stay_infinite(LL, la0, T, D, packed):
         assert np.array_equal(got[~fin], w[~fin], equal_nan=True), name
         check(torch.from_numpy(got[fin]).float(), w[fin], name)
     assert np.isinf(want[0, T // 3 - 1, 0]) and np.isinf(to64(dx)[0, 2 * T // 3, 0])
+
+
+def test_gradients_behind_the_last_sequence_stay(LL):
+    """Results that are given: rows that no sequence has are left as they are."""
+    T, D, cu = 200, 12, [0, 30, 77]
+    x, la = make(1, T, D, seed=2)
+    g = torch.Generator().manual_seed(1)
+    h0, ds = torch.randn(2, D, generator=g), torch.randn(2, D, generator=g)
+    dout = torch.randn(1, T, D, generator=g)
+    for t in (x, la, dout):
+        t[:, 77:] = float("nan")
+    xd, ld, hd, sd, dd = dev(x, la, h0, ds, dout)
+    c = torch.tensor(cu, dtype=torch.int32).cuda()
+    out = LL.loglinear_glr_fwd(xd, ld, h0=hd, cu_seqlens=c, scale="sqrt")
+    dx, dla = torch.zeros(1, T, D).cuda(), torch.zeros(1, T, D).cuda()
+    got = LL.loglinear_glr_bwd(xd, ld, out, dd, h0=hd, cu_seqlens=c, scale="sqrt", dstate=sd, dx=dx, dlog_a=dla, dh0=sd)
+    assert got[0] is dx and got[1] is dla and got[2] is sd
+    assert torch.all(dx[:, 77:] == 0) and torch.all(dla[:, 77:] == 0)
+    want = oracle.glr_backward(x[:, :77], la[:, :77], out[:, :77], dout[:, :77], "sqrt", h0=h0, dstate=ds, cu=cu)
+    for a, b in zip((dx[:, :77], dla[:, :77], sd), want):
+        check(a.cpu(), b)
