@@ -445,3 +445,43 @@ def test_gradients_behind_the_last_sequence_stay(LL):
     want = oracle.glr_backward(x[:, :77], la[:, :77], out[:, :77], dout[:, :77], "sqrt", h0=h0, dstate=ds, cu=cu)
     for a, b in zip((dx[:, :77], dla[:, :77], sd), want):
         check(a.cpu(), b)
+
+
+@pytest.mark.parametrize("cu", [None, [0, 0, 5, 300, 300, 1700, 1990, 1990]])
+def test_state_gradients_in_place(LL, cu):
+    """dstate and dh0 may be one array, empty sequences included; and packed states in place."""
+    import ctypes
+    from log_linear_attention_fwd_gb300 import _binding
+    B, T, D = (2, 2000, 70) if cu is None else (1, 2000, 70)
+    n = B if cu is None else len(cu) - 1
+    x, la = dev(*make(B, T, D, seed=3))
+    g = torch.Generator().manual_seed(1)
+    h0, ds, dout = (torch.randn(*s, generator=g).cuda() for s in ((n, D), (n, D), (B, T, D)))
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32).cuda()
+    state, both = torch.empty_like(h0), h0.clone()
+    out = LL.loglinear_glr_fwd(x, la, h0=h0, state=state, scale="sqrt", cu_seqlens=c)
+    again = LL.loglinear_glr_fwd(x, la, h0=both, state=both, scale="sqrt", cu_seqlens=c)
+    end = T if cu is None else cu[-1]
+    assert torch.equal(out[:, :end], again[:, :end]) and torch.equal(state, both)
+    want = LL.loglinear_glr_bwd(x, la, out, dout, h0=h0, dstate=ds, scale="sqrt", cu_seqlens=c)
+    both, dx, dla = ds.clone(), torch.empty_like(x), torch.empty_like(la)
+    p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = _binding.lib().loglinear_glr_bwd(p(x), None, p(la), None, p(h0), p(c), n, p(out), p(dout), p(both), p(dx),
+                                          p(dla), p(both), B, T, D, 0, 0, 0, 2,
+                                          ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0
+    assert all(torch.equal(a[:, :end], b[:, :end]) for a, b in zip((dx, dla), want)) and torch.equal(both, want[2])
+
+
+@pytest.mark.parametrize("scale", ["none", "one_minus", "sqrt"])
+@pytest.mark.parametrize("dtype,gate", [("f32", "f32"), ("bf16", "bf16")])
+def test_step_scales(LL, scale, dtype, gate):
+    B, T, D = 2, 5, 33
+    x, la = make(B, T, D, dtype, gate, seed=4)
+    h0 = torch.randn(B, D, generator=torch.Generator().manual_seed(1))
+    want, last = oracle.glr_forward(x, la, scale, h0=h0)
+    state = h0.cuda()
+    for t in range(T):
+        check(LL.loglinear_glr_step(state, x[:, t].contiguous().cuda(), la[:, t].contiguous().cuda(), scale=scale).cpu(),
+              want[:, t])
+    check(state.cpu(), last)
