@@ -468,8 +468,10 @@ __device__ __forceinline__ void block_decays(const float* la, int r, int from, f
 // share of the states' rows and of the block's tokens, whose first adds up their parts of the
 // output (distributed shared memory); all warps load the item's inputs.  Shares of rows are
 // contiguous in a page; shares of columns took twice the time for a single sequence, each of
-// their rows being a copy of its own.  One sequence of 16 heads at position 12345: 5.8 us, the
+// their rows being a copy of its own.  One sequence of 16 heads at position 12345: 5.4 us, the
 // latency of a launch and of reads that wait for one another (position, table, pages, sums).
+//
+// bf16 tokens spill 7 words (split) and 5 words (queue) at the 80 registers that two CTAs leave.
 //
 // A stage is kRowsPer rows per thread of one page; the pages of a row chunk come one after the
 // other, so that a fold can sum them and the tokens' products for its rows in registers.
@@ -1365,8 +1367,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ll_cache 
 }
 
 // One CTA per (row, head): the tokens of the source's block, and its pages' decays; the pages
-// themselves are shared.  16 slots to 4 copies each: 14 us for 41 MB with the plan, half of it the
-// two launches' latencies.
+// themselves are shared.  16 slots to 4 copies each: 13 us for 41 MB with the plan, which is a chain
+// of reads that wait for one another (slots, owners, tables, counts: more than half of it).
 template <typename T>
 __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(ll_cache c,
                                                                   const int* __restrict__ src,
@@ -1489,7 +1491,8 @@ namespace {
 template <typename T, typename OutT, bool kQueue>
 cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
   const size_t window = sizeof(T) * kW * (size_t)(c.dk + c.dv + 2 * kPad);
-  // as many stages as leave room for two CTAs per SM (228 KB, 1 KB per CTA its own), at least two
+  // as many stages as leave room for two CTAs per SM (228 KB, 1 KB per CTA its own), at least two:
+  // with fp32 tokens of dk = dv = 128 (window 68 KB) that is 256 bytes too many per CTA, and one runs
   a.stages = (int)std::max<size_t>(2, std::min<size_t>(kMaxStages, (115000 - sizeof(StepSmem) - window) / (kStageFloats * 4)));
   const size_t smem = window + (size_t)a.stages * kStageFloats * 4;
   const auto kernel = cache_step_kernel<T, OutT, kQueue>;

@@ -16,10 +16,11 @@
 // while the others compute.
 //
 // What bounds them is issue and the exchange, not HBM: 75 instructions per token and pair of
-// channels, half of them the gate (measured with parts switched off, B8 T2048 D2048 bf16: all 73
-// us, without gates 62, without the exchange 67, neither 57; HBM's time is 39.6), and 512 CTAs that
-// put four on some SMs and none on others.  Forward, b = sqrt(1 - a^2), bf16 with fp32 gates,
-// D 2048: T 16384 68 us, 3.9 TB/s; B4 T4096 63, 4.3 TB/s.  Backward: B4 T4096 119 us, 4.5 TB/s.
+// channels in the forward, 160 in the backward, and 512 CTAs that put four on some SMs and none on
+// others.  With parts switched off, D 2048 bf16 with fp32 gates, b = sqrt(1 - a^2): the forward of T
+// 16384 takes 68 us, 54 without the gates, 57.5 without the exchange between CTAs, 44.5 without
+// both (HBM's time is 39.6); the backward of B4 T4096 120, 105, 110.5 and 94 (79.1).  That is 3.9 and
+// 4.5 TB/s; the forward of B8 T2048, whose channel blocks have a CTA each, takes 57 us, 4.7 TB/s.
 // Packed in 37 sequences with first states, 9001 tokens of 1000 channels, fp32: forward 33 us,
 // backward 57.  Kept out of registers, the address of the sequences' bounds alone was worth 6%.
 //

@@ -780,7 +780,7 @@ int check_cache(const ll_cache* c, int64_t n) {
   if (c->dk > kMaxHeadDim || c->dv > kMaxHeadDim || c->dv % 4 != 0 || c->levels > 24 ||
       c->n_pages > (1 << 30) || c->slots > INT32_MAX / 64 || c->H > INT32_MAX / 64)
     return LL_ERR_UNSUPPORTED;
-  // rows x heads x column splits (at most 8) are a launch's CTAs
+  // rows x heads x shares of the state's rows (at most 8) are a launch's CTAs
   if (n > INT32_MAX / (8 * c->H)) return LL_ERR_UNSUPPORTED;
   if (!c->pages || !c->page_table || !c->refcount || !c->win_k || !c->win_v || !c->win_log_a ||
       !c->page_log || !c->page_from || !c->scratch || !c->error)
