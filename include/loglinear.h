@@ -369,8 +369,9 @@ LL_API int loglinear_bwd(const void* q, const void* k, const void* v, const floa
  * that a tensor-core loglinear_fwd with the same B, T, H, Hqk and dv did not write (its
  * layout tag does not match; the gradients are not valid).  Bit 3: a wait inside loglinear_glr_fwd or
  * _bwd ran out of time (the results are not valid).  Bit 4: loglinear_glr_step was given a
- * slot out of range, or one that an earlier row has (that row was left out).  The launch itself
- * still reported success.
+ * slot out of range, or one that an earlier row has (that row was left out).  Bit 5:
+ * loglinear_tree_verify was given a row that is no tree, or a token outside the vocabulary (that
+ * row accepted nothing).  The launch itself still reported success.
  */
 LL_API int loglinear_device_error(ll_stream_t stream, unsigned* flags);
 
@@ -490,8 +491,10 @@ typedef struct {
 #define LL_CACHE_ERR_PAGES 4u     /* no free page was left (the slot is left without it) */
 #define LL_CACHE_ERR_MISSING 8u   /* a page that the position needs is not there, or the page that
                                      a step would fold into is shared (not reserved) */
-#define LL_CACHE_ERR_WAIT 16u     /* a wait inside loglinear_cache_step ran out of time; the rows'
+#define LL_CACHE_ERR_WAIT 16u     /* a wait inside loglinear_cache_step or _tree ran out of time; the rows'
                                      results are not valid */
+#define LL_CACHE_ERR_TREE 32u     /* a node's parent does not come before it or is left out, or a path
+                                     names a node that is not there */
 
 LL_API int loglinear_cache_scratch_size(int64_t slots, int64_t n_pages, size_t* bytes);
 
@@ -578,6 +581,91 @@ LL_API int loglinear_cache_free(const ll_cache* cache, const int32_t* slots, int
  * the pages from there on are free.
  */
 LL_API int loglinear_cache_compact(const ll_cache* cache, int32_t* n_live, ll_stream_t stream);
+
+/*
+ * Speculative decoding over the cache.  A round takes, per sequence, a tree of N drafted tokens
+ * whose node 0 is the pending token (sampled last, not yet in the cache): loglinear_cache_tree
+ * runs the layers' attention for all nodes, loglinear_tree_verify settles which drafts stand and draws
+ * the next pending token, and loglinear_cache_accept puts the accepted path into the cache.
+ *
+ * parents: device int32 [n, N], 1 <= N <= LL_TREE_MAX.  A node's parent comes before it; -1: it
+ * has none (depth 0: it follows the context); -2: the node is left out (padding), and so has no
+ * children.  A parent that is not before its node, below -2, or left out is an error of the row.
+ */
+#define LL_TREE_MAX 64
+
+/*
+ * The decode step's attention for the nodes of a tree behind each slot's pos[row] positions, of
+ * which nothing is written: node i at depth d stands at t = pos[row] + d, and
+ *     out_i = sum_s lambda_i[level(t, s)] exp(sum of log_a behind s up to t) (q_i . k_s) v_s
+ * over the context, the nodes above it and itself.  A tree may run over the end of a block, with no
+ * fork or reservation; a slot may be given by many rows.  A node's output depends on its own
+ * path alone, infinities and NaN in other nodes included.
+ *   parents [n, N];  q, k [n, N, Hqk, dk], v [n, N, H, dv] cache dtype, strided as in
+ *           loglinear_cache_load (batch, node, head; NULL = dense)
+ *   log_a   [n, N, H] fp32 or NULL (no decay);  lambda [n, N, H, L] fp32, L >= M + 7
+ *   out     [n, N, H, dv] out_dtype; rows with slot -1 and nodes that are left out are not written
+ * Every node's t below 64 * 2^M - 1 (else POSITION).  A row that cannot be served is left out and
+ * raises the cache's error word.  Errors as the cache's calls; LL_ERR_UNSUPPORTED: N > LL_TREE_MAX;
+ * LL_ERR_INVALID: N < 1, a negative stride.
+ */
+LL_API int loglinear_cache_tree(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                                const int32_t* parents, const void* q, const ll_strides* q_strides,
+                                const void* k, const ll_strides* k_strides, const void* v,
+                                const ll_strides* v_strides, const float* log_a,
+                                const float* lambda, void* out, int64_t n, int64_t N, int64_t L,
+                                int out_dtype, ll_stream_t stream);
+
+/*
+ * The nodes path[row][0], path[row][1], ... (up to the first -1) join the slot at pos[row],
+ * pos[row] + 1, ..., as steps there would have left them: tokens, and at a block's end the fold.
+ * The reservation is included: the slot gives up pages that are no longer live at pos and, where
+ * the path ends the block, takes the page of the fold, lowest free pages first, in the order of the
+ * rows.  May be repeated at the same position (other drafts), unless the path went into the next
+ * block, whose tokens replace the block's.
+ *   path    device int32 [n, D], 1 <= D <= LL_TREE_MAX: nodes, in [0, N); whether they are a
+ *           path of the tree is not checked.  Empty (-1 first): only the reservation
+ *   k, v, log_a  the tree's, as in loglinear_cache_tree
+ *   new_pos device int32 [n], not pos itself: pos[row] + the path's length; rows that are left out
+ *           keep theirs
+ * A slot given to an earlier row, a path that is too long for the cache, names no node, or folds
+ * without its pages: the row is left out (its pages reserved) and the error word raised.
+ */
+LL_API int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                                  const int32_t* path, const void* k, const ll_strides* k_strides,
+                                  const void* v, const ll_strides* v_strides, const float* log_a,
+                                  int32_t* new_pos, int64_t n, int64_t N, int64_t D,
+                                  ll_stream_t stream);
+
+/*
+ * Verification of drafts by speculative sampling: the accepted tokens and the next one are
+ * distributed as the target's.  The walk starts at node 0 and tries the current node's children in the
+ * order of their index, with R the target's row P of that node and Z = 1 at first.  Node i, token x:
+ *     draft NULL (drafts that were given, such as the likeliest tokens): accepted where u_i Z < R(x);
+ *         else R(x) is taken off Z and set to 0.
+ *     draft (each child drawn from its parent's row Q of it, independently): accepted where
+ *         u_i Z Q(x) < R(x); else R <- max(R - Z Q, 0) and Z <- the sum of R.
+ * Where none is accepted, the next token is the lowest index at which the running sum of R is above
+ * u_0 times its whole (of P, where R is all 0; -1, where P is too).
+ *   parents, tokens  int32 [n, N];  tokens of nodes with a parent in [0, V)
+ *   probs, draft     [n, N, V] dtype (LL_F32 or LL_BF16): the distribution of the token after each node
+ *                    by the target and (or NULL) by the model that drafted; values outside [0, 1] count
+ *                    as the nearer bound, NaN as 0.  Rows of nodes that the walk does not reach are not
+ *                    read, but for their children's tokens' values
+ *   u                [n, N] fp32 in [0, 1) (others count as the nearest, NaN as 0); u_0 draws the token
+ *   path             [n, N] int32: node 0, the accepted nodes, then -1;  count [n] int32: their number
+ *   token            [n] int32: the next pending token
+ * A row whose node 0 is left out (-2) gets an empty path and token -1.  One that is no tree, whose
+ * node 0 is no root or that has a token outside the vocabulary does too, and raises bit 5 of
+ * loglinear_device_error.  Sums are exact to 2^-52 per value, in any order: the results do not
+ * depend on the launch.
+ * Errors: LL_ERR_INVALID (null pointer, negative size, N or V < 1), LL_ERR_DTYPE,
+ * LL_ERR_UNSUPPORTED (N > LL_TREE_MAX, V > 2^30, n > 2^24), LL_ERR_ALIGN, LL_ERR_CUDA.  n = 0 is a no-op.
+ */
+LL_API int loglinear_tree_verify(const int32_t* parents, const int32_t* tokens, const void* probs,
+                                 const void* draft, const float* u, int32_t* path, int32_t* count,
+                                 int32_t* token, int64_t n, int64_t N, int64_t V, int dtype,
+                                 ll_stream_t stream);
 
 /*
  * loglinear_fwd for callers that cannot allocate device memory.  The paper has no

@@ -98,6 +98,12 @@ SIGNATURES = {
     "loglinear_cache_fork": (_int, [_cp, _vp, _vp, _vp, _i64, _vp]),
     "loglinear_cache_free": (_int, [_cp, _vp, _i64, _vp]),
     "loglinear_cache_compact": (_int, [_cp, _vp, _vp]),
+    "loglinear_cache_tree": (_int, [_cp, _vp, _vp, _vp, _vp, _sp, _vp, _sp, _vp, _sp, _vp, _vp, _vp,
+                                    _i64, _i64, _i64, _int, _vp]),
+    "loglinear_cache_accept": (_int, [_cp, _vp, _vp, _vp, _vp, _sp, _vp, _sp, _vp, _vp, _i64, _i64,
+                                      _i64, _vp]),
+    "loglinear_tree_verify": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int,
+                                     _vp]),
 }
 
 
@@ -664,6 +670,8 @@ def loglinear_glr_step(state, x, log_a, slots=None, scale="none", out=None, out_
 
 CACHE_BLOCK = 64  # positions of a block (LL_CACHE_BLOCK)
 CACHE_ERR_SLOT, CACHE_ERR_POSITION, CACHE_ERR_PAGES, CACHE_ERR_MISSING, CACHE_ERR_WAIT = 1, 2, 4, 8, 16
+CACHE_ERR_TREE = 32
+TREE_MAX = 64  # nodes of a tree (LL_TREE_MAX)
 
 
 class LogLinearCache:
@@ -837,3 +845,90 @@ def loglinear_cache_compact(cache, live=None, stream=None):
     if st != LL_OK:
         raise LoglinearError(st, "loglinear_cache_compact")
     return live
+
+
+# ---------------------------------------------------------------- speculative decoding
+
+def _drafts(name, t, shape, dtype, dev):
+    """Address and strides (None: dense) of a tree's q, k or v, views with contiguous features."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), None
+    return t.data_ptr(), _token_strides(name, t, shape, dtype)
+
+
+def loglinear_cache_tree(cache, slots, pos, parents, q, k, v, log_a, lam, out=None, out_dtype=None,
+                         stream=None):
+    """The decode step's attention for trees of N <= 64 drafted tokens: row i's nodes follow the
+    pos[i] positions of slot slots[i] (int32 [n]; -1 leaves the row out) and their own parents.
+    parents [n,N] int32: an earlier node, -1 (the context) or -2 (the node is left out; its out is not
+    written).  q, k [n,N,Hqk,dk], v [n,N,H,dv] in the cache's dtype (may be views with
+    contiguous features); log_a [n,N,H] fp32 or None; lam [n,N,H,L] fp32, L >= levels + 7.  The cache
+    is not changed.  Returns out [n,N,H,dv]."""
+    dev, n, L = cache._dev(), slots.numel(), lam.shape[-1]
+    N = q.shape[1]
+    dt, H, qk, vs = cache.dtype, cache.heads, (n, N, cache.qk_heads, cache.dk), (n, N, cache.heads, cache.dv)
+    qp, sq = _drafts("q", q, qk, dt, dev)
+    kp, sk = _drafts("k", k, qk, dt, dev)
+    vp, sv = _drafts("v", v, vs, dt, dev)
+    if out is None:
+        out = _empty(stream, *vs, device=q.device, dtype=out_dtype or q.dtype)
+    st = _lib.loglinear_cache_tree(
+        cache._ref, _at("slots", slots, torch.int32, (n,), dev), _at("pos", pos, torch.int32, (n,), dev),
+        _at("parents", parents, torch.int32, (n, N), dev), qp, sq, kp, sk, vp, sv,
+        _at("log_a", log_a, torch.float32, (n, N, H), dev),
+        _at("lam", lam, torch.float32, (n, N, H, L), dev), _at("out", out, out.dtype, vs, dev), n, N, L,
+        _dtype_code(out), _raw_stream(stream, dev))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_tree")
+    return out
+
+
+def loglinear_tree_verify(parents, tokens, probs, u, draft=None, path=None, count=None, token=None,
+                          stream=None):
+    """Which drafts of a tree stand, by speculative sampling from given random numbers.  parents,
+    tokens [n,N] int32 (node 0: the pending token; a row whose node 0 is -2 is padding); probs
+    [n,N,V] fp32 or bf16: the target's distribution after each node; u [n,N] fp32 in [0,1), u[:,0] for
+    the next token; draft [n,N,V] in probs' dtype: the distribution that each node's children were drawn
+    from, or None for drafts that were given.  Returns (path [n,N] int32: node 0, the accepted
+    nodes, -1 behind them; count [n] int32; token [n] int32: the next pending token)."""
+    dev = _current_device_of("probs", probs)
+    if probs.dim() != 3:
+        raise ValueError(f"probs has shape {tuple(probs.shape)}, expected (n, N, V)")
+    n, N, V = probs.shape
+    i32 = torch.int32
+    if path is None:
+        path = _empty(stream, n, N, device=probs.device, dtype=i32)
+    if count is None:
+        count = _empty(stream, n, device=probs.device, dtype=i32)
+    if token is None:
+        token = _empty(stream, n, device=probs.device, dtype=i32)
+    st = _lib.loglinear_tree_verify(
+        _at("parents", parents, i32, (n, N), dev), _at("tokens", tokens, i32, (n, N), dev),
+        _at("probs", probs, probs.dtype, (n, N, V), dev), _at("draft", draft, probs.dtype, (n, N, V), dev),
+        _at("u", u, torch.float32, (n, N), dev), _at("path", path, i32, (n, N), dev),
+        _at("count", count, i32, (n,), dev), _at("token", token, i32, (n,), dev), n, N, V,
+        _dtype_code(probs), _raw_stream(stream, dev))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_tree_verify")
+    return path, count, token
+
+
+def loglinear_cache_accept(cache, slots, pos, path, k, v, log_a, new_pos=None, stream=None):
+    """The nodes of path ([n,D] int32, up to the first -1) join their slots from pos on, as
+    loglinear_cache_step would have put them there, reservation and fold included; k, v, log_a are
+    those of loglinear_cache_tree.  Returns new_pos [n] int32, pos + the path's length (rows that are
+    left out keep what it held: give one that is initialised where that matters)."""
+    dev, n = cache._dev(), slots.numel()
+    N, D = k.shape[1], path.shape[-1]
+    kp, sk = _drafts("k", k, (n, N, cache.qk_heads, cache.dk), cache.dtype, dev)
+    vp, sv = _drafts("v", v, (n, N, cache.heads, cache.dv), cache.dtype, dev)
+    if new_pos is None:
+        new_pos = _empty(stream, n, device=cache.device, dtype=torch.int32)
+    st = _lib.loglinear_cache_accept(
+        cache._ref, _at("slots", slots, torch.int32, (n,), dev), _at("pos", pos, torch.int32, (n,), dev),
+        _at("path", path, torch.int32, (n, D), dev), kp, sk, vp, sv,
+        _at("log_a", log_a, torch.float32, (n, N, cache.heads), dev),
+        _at("new_pos", new_pos, torch.int32, (n,), dev), n, N, D, _raw_stream(stream, dev))
+    if st != LL_OK:
+        raise LoglinearError(st, "loglinear_cache_accept")
+    return new_pos

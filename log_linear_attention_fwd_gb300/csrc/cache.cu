@@ -19,161 +19,10 @@
 // the order of the rows that ask: the result of every call is determined by its inputs.
 #include <algorithm>
 
-#include "ll_internal.cuh"
-#include "tc_ptx.cuh"
+#include "cache_common.cuh"
 
 namespace ll {
 namespace {
-
-constexpr int kW = LL_CACHE_BLOCK;   // positions of a block
-constexpr int kLogW = 6;             // log2(kW)
-static_assert(kW == 1 << kLogW, "block length");
-
-constexpr int kPlanThreads = 1024;
-constexpr int kNone = 0x7fffffff;
-
-// Scratch of the page operators: who owns each slot in this call, two lists and a map of pages.
-struct Scratch {
-  int* owner;  // [slots] lowest row of this call that names the slot
-  int* from;   // [n_pages]
-  int* to;     // [n_pages]
-  int* map;    // [n_pages]
-  int* count;  // [1]
-};
-__host__ __device__ Scratch scratch_of(const ll_cache& c) {
-  Scratch s;
-  s.owner = c.scratch;
-  s.from = s.owner + c.slots;
-  s.to = s.from + c.n_pages;
-  s.map = s.to + c.n_pages;
-  s.count = s.map + c.n_pages;
-  return s;
-}
-
-// The page operators are a small kernel that settles the tables and a large one that follows it;
-// the second is launched while the first runs (programmatic dependent launch), and waits for
-// its end before it touches memory: that hides the launch, 1 to 2 us.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... Params, typename... Args>
-cudaError_t launch_following(bool early, void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
-                             int cluster, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = early;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-__device__ __forceinline__ void raise(const ll_cache& c, unsigned bits) {
-  atomicOr(c.error, bits);
-}
-
-// Sum of v over the threads before this one; *total over all.  kPlanThreads threads.
-__device__ int block_scan(int v, int* total) {
-  __shared__ int part[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();  // part may still be read from the call before
-  if (lane == 31) part[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    int p = part[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, p, d);
-      if (lane >= d) p += y;
-    }
-    part[lane] = p;
-  }
-  __syncthreads();
-  *total = part[kPlanThreads / 32 - 1];
-  return x - v + (w ? part[w - 1] : 0);
-}
-
-// Gives each named slot to the lowest row that names it.  Rows that name a slot out of range
-// other than -1, or one that an earlier row has, raise the error word.  src: rows with -1 there
-// name none.
-__device__ void claim_slots(const ll_cache& c, const int* slots, int64_t n, int* owner,
-                            const int* src = nullptr) {
-  auto slot_of = [&](int64_t r) { return src && src[r] == -1 ? -1 : slots[r]; };
-  for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-    const int s = slot_of(r);
-    if (s >= 0 && s < c.slots) owner[s] = kNone;
-  }
-  __syncthreads();
-  for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-    const int s = slot_of(r);
-    if (s >= 0 && s < c.slots) atomicMin(owner + s, (int)r);
-    else if (s != -1) raise(c, LL_CACHE_ERR_SLOT);
-  }
-  __syncthreads();
-  for (int64_t r = threadIdx.x; r < n; r += kPlanThreads) {
-    const int s = slot_of(r);
-    if (s >= 0 && s < c.slots && __ldcg(owner + s) != r) raise(c, LL_CACHE_ERR_SLOT);
-  }
-}
-__device__ __forceinline__ bool owns(const ll_cache& c, const int* owner, int s, int64_t r) {
-  return s >= 0 && s < c.slots && __ldcg(owner + s) == r;
-}
-
-__device__ __forceinline__ void drop_page(const ll_cache& c, int e) {
-  if (e >= 0 && e < c.n_pages) atomicSub(c.refcount + e, 1);
-}
-
-// The last position a step can take: its block's fold still has a level to go to.
-__device__ __forceinline__ bool position_ok(const ll_cache& c, int64_t t) {
-  return t >= 0 && t < ((int64_t)kW << c.levels) - 1;
-}
-
-// Whether a slot's pages, if it has any at n positions, have already decayed past there: a prompt
-// was loaded up to a later position of the block.
-__device__ __forceinline__ bool before_pages(const ll_cache& c, int s, int n) {
-  const int j = n >> kLogW;
-  return j && c.page_from[s * 2 + (j & 1)] > (n & (kW - 1));
-}
-
-// Gives the lowest free pages to the table entries want[0..count), in that order.
-__device__ void take_pages(const ll_cache& c, const int* want, int count) {
-  int given = 0;
-  for (int64_t base = 0; base < c.n_pages && given < count; base += kPlanThreads * 4) {
-    const int64_t p0 = base + threadIdx.x * 4;
-    int free_of[4], mine = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      free_of[i] = p0 + i < c.n_pages && __ldcg(c.refcount + p0 + i) == 0;
-      mine += free_of[i];
-    }
-    int total, rank = given + block_scan(mine, &total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (free_of[i]) {
-        if (rank < count) {
-          c.page_table[__ldcg(want + rank)] = (int)(p0 + i);
-          c.refcount[p0 + i] = 1;
-        }
-        ++rank;
-      }
-    given += total;
-  }
-  if (given < count && threadIdx.x == 0) raise(c, LL_CACHE_ERR_PAGES);
-}
 
 // ---------------------------------------------------------------- reserve, free
 
@@ -186,7 +35,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
                                                                      const int* pos, int64_t n) {
   __shared__ int slot_s[kPlanThreads], pos_s[kPlanThreads];
   const Scratch sc = scratch_of(c);
-  const int M = (int)c.levels, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   let_next_start();
   // the rows in shared memory, -1 for those that are left out; one at a time per thread where
   // they fit, else their owners go through global memory
@@ -217,58 +66,10 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c,
     const int s = slots[r];
     return owns(c, sc.owner, s, r) && (!pos || position_ok(c, pos[r])) ? s : -1;
   };
-  auto pos_of = [&](int64_t r) { return few ? pos_s[r] : pos[r]; };
+  auto pos_of = [&](int64_t r) { return !pos ? 0 : few ? pos_s[r] : pos[r]; };
   __syncthreads();
-  bool folds = false;
-  if (pos) {
-    for (int64_t r = tid; r < n; r += kPlanThreads) folds |= slot_of(r) >= 0 && (pos_of(r) & (kW - 1)) == kW - 1;
-    folds = __syncthreads_or(folds);
-  }
-  if (folds) {  // mark shared pages where folds go to, before any count changes: -2 - page
-    for (int64_t r = tid; r < n; r += kPlanThreads) {
-      const int s = slot_of(r), t = pos_of(r);
-      if (s < 0 || (t & (kW - 1)) != kW - 1) continue;
-      int* e = c.page_table + (int64_t)s * M + __ffs((t >> kLogW) + 1) - 1;
-      if (*e < 0 || *e >= c.n_pages) *e = -1;  // (a table that was overwritten: no page, and no mark)
-      else if (__ldcg(c.refcount + *e) != 1) *e = -2 - *e;
-    }
-    __syncthreads();
-  }
-  for (int64_t k = tid; k < n * M; k += kPlanThreads) {
-    const int64_t r = k / M;
-    const int m = (int)(k - r * M), s = slot_of(r);
-    if (s < 0) continue;
-    bool keep = false, to = false;
-    if (pos) {
-      const int t = pos_of(r), j = t >> kLogW;
-      to = (t & (kW - 1)) == kW - 1 && m == __ffs(j + 1) - 1;
-      keep = to || (j >> m) & 1;
-    }
-    int* e = c.page_table + (int64_t)s * M + m;
-    if (*e < -1 || (!keep && *e >= 0)) {
-      drop_page(c, to ? -2 - *e : *e);  // (below -1 elsewhere: no page)
-      *e = -1;
-    }
-  }
-  if (!folds) return;
-  __syncthreads();
-  int count = 0;
-  for (int64_t base = 0; base < n; base += kPlanThreads) {
-    const int64_t r = base + tid;
-    int at = -1;
-    if (r < n && slot_of(r) >= 0 && (pos_of(r) & (kW - 1)) == kW - 1) {
-      const int64_t e = (int64_t)slot_of(r) * M + __ffs((pos_of(r) >> kLogW) + 1) - 1;
-      if (c.page_table[e] < 0) at = (int)e;
-    }
-    int total;
-    const int rank = count + block_scan(at >= 0, &total);
-    if (at >= 0 && rank < c.n_pages) sc.from[rank] = at;
-    count += total;
-  }
-  if (count == 0) return;
-  __syncthreads();
-  if (count > c.n_pages && tid == 0) raise(c, LL_CACHE_ERR_PAGES);
-  take_pages(c, sc.from, (int)min((int64_t)count, c.n_pages));
+  settle_pages(c, n, slot_of, [&](int64_t r) { return pos_of(r) >> kLogW; },
+               [&](int64_t r) { return (pos_of(r) & (kW - 1)) == kW - 1; });
 }
 
 // ---------------------------------------------------------------- load
@@ -414,42 +215,6 @@ __global__ void __launch_bounds__(kCopyThreads) cache_load_kernel(
         log_a ? log_a[row * st.a[0] + (t0 + i) * st.a[1] + h * st.a[2]] : 0.f;
 }
 
-// ---------------------------------------------------------------- decays inside a block
-
-// after[i] = sum of la[u], i < u < r (0 at and past r - 1), and *since = sum of la[u], from <= u
-// < r, for r <= 64 values.  One warp; sums run from the end, in one order.
-__device__ __forceinline__ void block_decays(float x0, float x1, int r, int from, float* after,
-                                             float* since) {
-  const int lane = threadIdx.x & 31;  // x0, x1: la[lane] and la[lane + 32], 0 from r on
-  float y0 = x0, y1 = x1;  // inclusive sums from the end of each half
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const float z0 = __shfl_down_sync(0xffffffffu, y0, d);
-    const float z1 = __shfl_down_sync(0xffffffffu, y1, d);
-    if (lane + d < 32) {
-      y0 += z0;
-      y1 += z1;
-    }
-  }
-  const float upper = __shfl_sync(0xffffffffu, y1, 0);
-  y0 += upper;
-  float n0 = __shfl_down_sync(0xffffffffu, y0, 1), n1 = __shfl_down_sync(0xffffffffu, y1, 1);
-  if (lane == 31) {
-    n0 = upper;
-    n1 = 0.f;
-  }
-  after[lane] = n0;
-  after[lane + 32] = n1;
-  const float f0 = __shfl_sync(0xffffffffu, y0, from & 31), f1 = __shfl_sync(0xffffffffu, y1, from & 31);
-  *since = from >= r ? 0.f : from < 32 ? f0 : f1;
-}
-
-__device__ __forceinline__ void block_decays(const float* la, int r, int from, float* after,
-                                             float* since) {  // *since in every lane
-  const int lane = threadIdx.x & 31;
-  block_decays(lane < r ? la[lane] : 0.f, lane + 32 < r ? la[lane + 32] : 0.f, r, from, after, since);
-}
-
 // ---------------------------------------------------------------- step
 
 // An item is one (row, head).  A producer warp brings its block's tokens and then its pages, in
@@ -483,62 +248,8 @@ constexpr int kQueueThreads = kConsumers + 64 + 32 * kLoaders;
 constexpr int kSplitThreads = kConsumers + 96;  // one loader
 constexpr int kRowsPer = 4;
 constexpr int kStageFloats = kConsumers * 4 * kRowsPer;
-constexpr int kMaxLevels = 24;
 constexpr int kMaxSplit = 8;  // CTAs of a cluster
 constexpr int kMaxStages = 8;
-
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ float4 fma4(float s, float4 x, float4 y) {
-  return make_float4(fmaf(s, x.x, y.x), fmaf(s, x.y, y.y), fmaf(s, x.z, y.z), fmaf(s, x.w, y.w));
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          tc::smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ float4 add4(float4 x, float4 y) {
-  return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-}
-
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Writes v to p in the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote4(float* p, uint32_t rank, float4 v) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
-}
-
-template <typename OutT>
-__device__ __forceinline__ void store_out(void* out, int64_t at, float4 v) {
-  OutT* o = static_cast<OutT*>(out) + at;
-  o[0] = from_f32<OutT>(v.x);
-  o[1] = from_f32<OutT>(v.y);
-  o[2] = from_f32<OutT>(v.z);
-  o[3] = from_f32<OutT>(v.w);
-}
 
 struct StepArgs {
   const int* slots;
@@ -649,12 +360,6 @@ struct Vectors {
   }
 };
 
-// Why a row cannot be served, before its pages are looked at.
-__device__ __forceinline__ unsigned row_bad(const ll_cache& c, int s, int t) {
-  if (s < 0 || s >= c.slots) return LL_CACHE_ERR_SLOT;
-  return position_ok(c, t) ? 0 : LL_CACHE_ERR_POSITION;
-}
-
 // The item's decays and pages, by one warp; s and t are fine.  Returns why the row cannot be served.
 __device__ __forceinline__ unsigned load_links(const ll_cache& c, const StepArgs& a, int row, int h, int s,
                                            int t, Item& it) {
@@ -730,11 +435,6 @@ __device__ __forceinline__ Part part_of(int pos, int dk, int dv, int Z, int sp) 
   return p;
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  return x;
-}
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(kConsumers) : "memory");
 }
@@ -757,27 +457,6 @@ __device__ __forceinline__ bool consumer_any(bool x) {
 // out as in the sum itself, where the parts' products are all of one sign: the parts are cut off
 // towards zero, and what is left of a value that is not 0 is never 0 or NaN (infinity less
 // itself) but at least the least bf16, whose product with a key is below any normal number.
-__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], const __nv_bfloat16* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(tc::smem_u32(p))
-               : "memory");
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// x's leading bf16 parts (x >= 0); x keeps the rest, at least `least`.
-__device__ __forceinline__ uint32_t take_bf16(float2& x, float2 least) {
-  uint32_t h;
-  asm("cvt.rz.bf16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(x.x), "f"(x.y));
-  const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h));
-  x = make_float2(fmaxf(x.x - f.x, least.x), fmaxf(x.y - f.y, least.y));
-  return h;
-}
 __device__ __forceinline__ void fold_tokens(const __nv_bfloat16* wks, const __nv_bfloat16* wvs,
                                             const float* tok, int kp, int vp, int dv, int k0, int k1,
                                             float* D) {
@@ -1456,14 +1135,6 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(ll_cache c) {
     copy4(reinterpret_cast<float4*>(t + o), reinterpret_cast<const float4*>(f + o),
           min((int64_t)kMoveChunk, size - o) / 4, [](float4 x) { return x; });
   }
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    return 152;
-  return n;
 }
 
 // CTAs per (row, head): doubled while that leaves the launch within the SMs, and each at least 16

@@ -276,6 +276,20 @@ cudaError_t launch_cache_fork(const ll_cache& c, const int* src, const int* dst,
                               int64_t n, cudaStream_t s);
 cudaError_t launch_cache_compact(const ll_cache& c, int* n_live, cudaStream_t s);
 
+cudaError_t launch_cache_tree(const ll_cache& c, const int* slots, const int* pos, const int* parents,
+                              const void* q, const int64_t* sq, const void* k, const int64_t* sk,
+                              const void* v, const int64_t* sv, const float* log_a, const float* lam,
+                              void* out, int n, int N, int L, int out_dtype, cudaStream_t s);
+cudaError_t launch_cache_accept(const ll_cache& c, const int* slots, const int* pos, const int* path,
+                                const void* k, const int64_t* sk, const void* v, const int64_t* sv,
+                                const float* log_a, int* new_pos, int n, int N, int D, cudaStream_t s);
+
+// Verification of drafts (tree_verify.cu).
+cudaError_t launch_tree_verify(const int* parents, const int* tokens, const void* probs, const void* draft,
+                               const float* u, int* path, int* count, int* token, int n, int N, int64_t V,
+                               int dtype, cudaStream_t s);
+cudaError_t verify_take_error(cudaStream_t s, unsigned* flags);
+
 cudaError_t launch_level_map(int T, int tile, int lc, int8_t* levels, cudaStream_t s);
 
 // Records a CUDA error for loglinear_last_cuda_error() and returns LL_ERR_CUDA.

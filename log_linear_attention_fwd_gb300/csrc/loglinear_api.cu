@@ -625,11 +625,12 @@ int loglinear_bwd(const void* q, const void* k, const void* v, const float* log_
 
 int loglinear_device_error(ll_stream_t stream, unsigned* flags) {
   if (!flags) return LL_ERR_INVALID;
-  unsigned f1 = 0, f2 = 0, f3 = 0;
+  unsigned f1 = 0, f2 = 0, f3 = 0, f4 = 0;
   cudaError_t e = tc_take_error(reinterpret_cast<cudaStream_t>(stream), &f1);
   if (e == cudaSuccess) e = tcb_take_error(reinterpret_cast<cudaStream_t>(stream), &f2);
   if (e == cudaSuccess) e = glr_take_error(reinterpret_cast<cudaStream_t>(stream), &f3);
-  *flags = f1 | f2 | (f3 & 1u) << 4 | (f3 & 2u) << 2;
+  if (e == cudaSuccess) e = verify_take_error(reinterpret_cast<cudaStream_t>(stream), &f4);
+  *flags = f1 | f2 | (f3 & 1u) << 4 | (f3 & 2u) << 2 | f4;
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
 
@@ -908,6 +909,79 @@ int loglinear_cache_compact(const ll_cache* cache, int32_t* n_live, ll_stream_t 
   if (!aligned_to(n_live, 4)) return LL_ERR_ALIGN;
   const cudaError_t e =
       launch_cache_compact(*cache, n_live, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_tree(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                         const int32_t* parents, const void* q, const ll_strides* q_strides,
+                         const void* k, const ll_strides* k_strides, const void* v,
+                         const ll_strides* v_strides, const float* log_a, const float* lambda,
+                         void* out, int64_t n, int64_t N, int64_t L, int out_dtype,
+                         ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK) return st;
+  if (!dtype_ok(out_dtype)) return LL_ERR_DTYPE;
+  if (N < 1) return LL_ERR_INVALID;
+  if (L < cache->levels + 7) return LL_ERR_SHAPE;
+  if (N > LL_TREE_MAX || L > 64) return LL_ERR_UNSUPPORTED;
+  if (n == 0) return LL_OK;
+  if (!slots || !pos || !parents || !q || !k || !v || !lambda || !out) return LL_ERR_INVALID;
+  const size_t e_in = size_of(cache->dtype);
+  if (!aligned_to(slots, 4) || !aligned_to(pos, 4) || !aligned_to(parents, 4) ||
+      !aligned_to(q, e_in) || !aligned_to(k, e_in) || !aligned_to(v, e_in) || !aligned_to(log_a, 4) ||
+      !aligned_to(lambda, 4) || !aligned_to(out, size_of(out_dtype)))
+    return LL_ERR_ALIGN;
+  int64_t sq[3], sk[3], sv[3];
+  resolve_strides(q_strides, n, N, cache->Hqk, cache->dk, sq);
+  resolve_strides(k_strides, n, N, cache->Hqk, cache->dk, sk);
+  resolve_strides(v_strides, n, N, cache->H, cache->dv, sv);
+  for (int i = 0; i < 3; ++i)
+    if (sq[i] < 0 || sk[i] < 0 || sv[i] < 0) return LL_ERR_INVALID;
+  const cudaError_t e = launch_cache_tree(*cache, slots, pos, parents, q, sq, k, sk, v, sv, log_a, lambda, out,
+                                          (int)n, (int)N, (int)L, out_dtype,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
+                           const int32_t* path, const void* k, const ll_strides* k_strides,
+                           const void* v, const ll_strides* v_strides, const float* log_a,
+                           int32_t* new_pos, int64_t n, int64_t N, int64_t D, ll_stream_t stream) {
+  const int st = check_cache(cache, n);
+  if (st != LL_OK) return st;
+  if (N < 1 || D < 1) return LL_ERR_INVALID;
+  if (N > LL_TREE_MAX || D > LL_TREE_MAX) return LL_ERR_UNSUPPORTED;
+  if (n == 0) return LL_OK;
+  if (!slots || !pos || !path || !k || !v || !new_pos || new_pos == pos) return LL_ERR_INVALID;
+  const size_t e_in = size_of(cache->dtype);
+  if (!aligned_to(slots, 4) || !aligned_to(pos, 4) || !aligned_to(path, 4) || !aligned_to(k, e_in) ||
+      !aligned_to(v, e_in) || !aligned_to(log_a, 4) || !aligned_to(new_pos, 4))
+    return LL_ERR_ALIGN;
+  int64_t sk[3], sv[3];
+  resolve_strides(k_strides, n, N, cache->Hqk, cache->dk, sk);
+  resolve_strides(v_strides, n, N, cache->H, cache->dv, sv);
+  for (int i = 0; i < 3; ++i)
+    if (sk[i] < 0 || sv[i] < 0) return LL_ERR_INVALID;
+  const cudaError_t e = launch_cache_accept(*cache, slots, pos, path, k, sk, v, sv, log_a, new_pos, (int)n,
+                                            (int)N, (int)D, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : cuda_fail(e);
+}
+
+int loglinear_tree_verify(const int32_t* parents, const int32_t* tokens, const void* probs,
+                          const void* draft, const float* u, int32_t* path, int32_t* count,
+                          int32_t* token, int64_t n, int64_t N, int64_t V, int dtype,
+                          ll_stream_t stream) {
+  if (n < 0 || N < 1 || V < 1) return LL_ERR_INVALID;
+  if (!dtype_ok(dtype)) return LL_ERR_DTYPE;
+  if (N > LL_TREE_MAX || V > (1 << 30) || n > (1 << 24)) return LL_ERR_UNSUPPORTED;
+  if (n == 0) return LL_OK;
+  if (!parents || !tokens || !probs || !u || !path || !count || !token) return LL_ERR_INVALID;
+  if (!aligned_to(parents, 4) || !aligned_to(tokens, 4) || !aligned_to(probs, size_of(dtype)) ||
+      !aligned_to(draft, size_of(dtype)) || !aligned_to(u, 4) || !aligned_to(path, 4) ||
+      !aligned_to(count, 4) || !aligned_to(token, 4))
+    return LL_ERR_ALIGN;
+  const cudaError_t e = launch_tree_verify(parents, tokens, probs, draft, u, path, count, token, (int)n, (int)N,
+                                           V, dtype, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LL_OK : cuda_fail(e);
 }
 

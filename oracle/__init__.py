@@ -28,3 +28,8 @@ from .glr_oracle import (  # noqa: F401
     glr_forward,
     glr_scale,
 )
+from .tree_oracle import (  # noqa: F401
+    tree_attention,
+    tree_paths,
+    tree_verify,
+)
