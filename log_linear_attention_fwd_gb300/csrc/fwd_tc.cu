@@ -804,6 +804,21 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int width) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The decode cache's pages, [n_pages, H, dk, dv] fp32: boxes of `rows` rows x 32 columns of one
+// (page, head), 128-byte swizzle; rows and columns past the page read as 0.
+bool make_pages_map(CUtensorMap* m, const float* base, int64_t n_pages, int64_t H, int64_t dk, int64_t dv,
+                    int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)dv, (cuuint64_t)dk, (cuuint64_t)H, (cuuint64_t)n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)dv * 4, (cuuint64_t)(dk * dv) * 4, (cuuint64_t)(H * dk * dv) * 4};
+  cuuint32_t box[4] = {32, (cuuint32_t)rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<float*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_forward_supported(int64_t dk, int64_t dv, int in_dtype, int /*chunk*/) {
   return in_dtype == LL_BF16 && dk == kD && (dv == 64 || dv == 128);
 }

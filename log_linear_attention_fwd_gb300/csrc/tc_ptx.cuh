@@ -362,5 +362,8 @@ bool make_tokens_map_strided(CUtensorMap* m, const void* base, int B, int T, int
                              const int64_t* strides);
 // [rows][width] bf16 matrices, boxes of 128 rows x 64 columns, 128-byte swizzle.
 bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int width);
+// [n_pages, H, dk, dv] fp32 pages, boxes of `rows` rows x 32 columns, 128-byte swizzle.
+bool make_pages_map(CUtensorMap* m, const float* base, int64_t n_pages, int64_t H, int64_t dk, int64_t dv,
+                    int rows);
 
 }  // namespace ll
