@@ -29,7 +29,7 @@ struct TreeArgs {
   const float* lam;
   void* out;
   int n, N, L, out_f32;
-  int split, groups, stages, box_log;
+  int split, groups, own, stages, box_log;  // own: stages that are only the ring's
 };
 
 // A CTA serves one (row, head) for up to 8 NT nodes: eight consumer warps, and a producer warp that
@@ -54,10 +54,11 @@ struct Parts {
   static constexpr int page = sizeof(T) == 2 ? 2 : 3;    // of a page and of a token's weight
 };
 
-// Shared memory behind the ring, in bytes.
+// Shared memory behind the ring's own stages, in bytes.  The tokens' weights and values are done with
+// before the pages: whole stages of their place then join the ring.
 struct TreeLayout {
-  int kq, vp, tp;                // elements from row to row: q and k, v, weights
-  int q, k, v, lam, pw, end;     // where each begins; the weights' parts and the last sums take k's place
+  int kq, vp, tp;             // elements from row to row: q, v, weights
+  int p, v, q, lam, pw, end;  // where each begins
 };
 template <typename T, int NT>
 __host__ __device__ __forceinline__ TreeLayout tree_layout(int dk, int dv, int N) {
@@ -66,13 +67,10 @@ __host__ __device__ __forceinline__ TreeLayout tree_layout(int dk, int dv, int N
   l.kq = dk16 + 8;  // an odd number of 16-byte pieces: ldmatrix without conflicts
   l.vp = dv16 + (sizeof(T) == 2 ? 8 : 4);
   l.tp = tokens + 8;
-  l.q = 0;
-  l.k = l.q + Parts<T>::in * 8 * NT * l.kq * 2;
-  int k = tokens * l.kq * (int)sizeof(T);
-  const int p = Parts<T>::page * 8 * NT * l.tp * 2, red = kTreeWarps * NT * 512;
-  k = k > p ? k : p;
-  l.v = l.k + (k > red ? k : red);
-  l.lam = l.v + tokens * l.vp * (int)sizeof(T);
+  l.p = 0;
+  l.v = l.p + Parts<T>::page * 8 * NT * l.tp * 2;
+  l.q = l.v + tokens * l.vp * (int)sizeof(T);
+  l.lam = l.q + Parts<T>::in * 8 * NT * l.kq * 2;
   l.pw = l.lam + 8 * NT * kLamPitch * 4;
   l.end = l.pw + kMaxLevels * 8 * NT * 4;
   return l;
@@ -88,8 +86,10 @@ struct TreeSmem {
   int up[kNodes], depth[kNodes];
   unsigned long long above[kNodes];  // nodes on the path, itself included
   float since;
-  unsigned bad;
+  unsigned bad[kTreeWarps + 1];      // what each warp found
+  unsigned bad_tree[2];
   int odd;                           // a node's v has infinities or NaN
+  int odd_q;                         // a query has
 };
 
 __device__ __forceinline__ void consumer_sync() {
@@ -131,6 +131,19 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&part)[N]) {
   part[N - 1] = h | sign;
 }
 
+// The same for a page's values, in half the instructions: an infinity becomes the largest value and
+// an infinity.  What is left may be 0, which only matters to an infinite query.
+template <int N>
+__device__ __forceinline__ void split2_page(float x, float y, uint32_t (&part)[N]) {
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i) {
+    asm("cvt.rz.satfinite.bf16x2.f32 %0, %2, %1;" : "=r"(part[i]) : "f"(x), "f"(y));
+    x -= __uint_as_float(part[i] << 16);
+    y -= __uint_as_float(part[i] & 0xffff0000u);
+  }
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(part[N - 1]) : "f"(x), "f"(y));
+}
+
 // Fragments of mma.m16n8k16.  B from rows [n][k] in shared memory, NT tiles of 8 rows, at k0.
 template <int NT>
 __device__ __forceinline__ void load_b(uint32_t (&b)[NT][2], const __nv_bfloat16* rows, int pitch, int k0) {
@@ -149,20 +162,42 @@ __device__ __forceinline__ void load_b(uint32_t (&b)[NT][2], const __nv_bfloat16
     }
   }
 }
-// A from rows [m][k]: 16 tokens' keys.
-__device__ __forceinline__ void load_a_rows(uint32_t (&a)[1][4], const __nv_bfloat16* rows, int pitch, int k0) {
-  const int lane = threadIdx.x & 31;
-  ldmatrix4(a[0], rows + ((lane & 7) + ((lane >> 3) & 1) * 8) * pitch + k0 + (lane >> 4) * 8);
+// 8 values of a row from column k on, 0 past `width`, as words of bf16 parts.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&word)[N][4], const __nv_bfloat16* row, int k, int width, bool vec) {
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  if (vec) {
+    if (k < width) x = *reinterpret_cast<const uint4*>(row + k);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) e[u] = k + u < width ? __bfloat16_as_ushort(row[k + u]) : 0u;
+    x = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
+  word[0][0] = x.x;
+  word[0][1] = x.y;
+  word[0][2] = x.z;
+  word[0][3] = x.w;
 }
-__device__ __forceinline__ void load_a_rows(uint32_t (&a)[3][4], const float* rows, int pitch, int k0) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, i = 2 * (lane & 3);
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&word)[N][4], const float* row, int k, int width, bool vec) {
+  float e[8];
+  if (vec) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (k < width) x = *reinterpret_cast<const float4*>(row + k);
+    if (k + 4 < width) y = *reinterpret_cast<const float4*>(row + k + 4);
+    e[0] = x.x; e[1] = x.y; e[2] = x.z; e[3] = x.w;
+    e[4] = y.x; e[5] = y.y; e[6] = y.z; e[7] = y.w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) e[u] = k + u < width ? row[k + u] : 0.f;
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const float2 x = *reinterpret_cast<const float2*>(rows + (g + (u & 1) * 8) * pitch + k0 + i + (u >> 1) * 8);
-    uint32_t part[3];
-    split2(x.x, x.y, part);
+    uint32_t part[N];
+    split2(e[2 * u], e[2 * u + 1], part);
 #pragma unroll
-    for (int j = 0; j < 3; ++j) a[j][u] = part[j];
+    for (int j = 0; j < N; ++j) word[j][u] = part[j];
   }
 }
 // A from rows [k][m]: 16 tokens' values, columns m0 .. m0 + 15.
@@ -182,48 +217,60 @@ __device__ __forceinline__ void load_a_cols(uint32_t (&a)[3][4], const float* ro
   }
 }
 
-// `rows` rows of `width` elements to shared memory, by the consumers: asynchronously where all are
-// whole 16-byte pieces; columns up to the next multiple of 16 become 0 with zero_pad.
-template <typename T>
-__device__ __forceinline__ void bring_rows(T* dst, int pitch, const T* src, int64_t stride, int rows, int width,
-                                           bool zero_pad) {
+// The consumers' way over `rows` rows of `width` elements: f(row, first column, elements) by each
+// thread in turn, 16 bytes at a time with `vec` and one element without; no divisions.
+template <typename T, typename F>
+__device__ __forceinline__ void over_rows(int rows, int width, bool vec, F f) {
   constexpr int per = 16 / sizeof(T);
-  if (width % per == 0 && (stride * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-    const int chunks = width / per;
-    for (int x = threadIdx.x; x < rows * chunks; x += kConsumerThreads) {
-      const int r = x / chunks, c = (x - r * chunks) * per;
-      cp_async16(dst + r * pitch + c, src + r * stride + c);
-    }
+  const int pieces = vec ? width / per : width;
+  const int log = 32 - __clz(pieces - 1);  // (1 piece: 0)
+  const int c = threadIdx.x & ((1 << log) - 1);
+  if (c >= pieces) return;
+  if (vec) {
+#pragma unroll 4
+    for (int r = threadIdx.x >> log; r < rows; r += kConsumerThreads >> log) f(r, c * per, per);
   } else {
 #pragma unroll 4
-    for (int x = threadIdx.x; x < rows * width; x += kConsumerThreads) {
-      const int r = x / width;
-      dst[r * pitch + x - r * width] = src[r * stride + (x - r * width)];
-    }
+    for (int r = threadIdx.x >> log; r < rows; r += kConsumerThreads >> log) f(r, c, 1);
   }
-  const int pad = zero_pad ? (16 - (width & 15)) & 15 : 0;
-  for (int x = threadIdx.x; x < rows * pad; x += kConsumerThreads)
-    dst[x / pad * pitch + width + x % pad] = from_f32<T>(0.f);
 }
-// The queries, as bf16 parts [parts][rows][pitch].
+template <typename T>
+__device__ __forceinline__ bool whole_pieces(const T* p, int64_t stride, int width) {
+  return ((width | stride) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+// Rows to shared memory, asynchronously where they are whole 16-byte pieces.
+template <typename T>
+__device__ __forceinline__ void bring_rows(T* dst, int pitch, const T* src, int64_t stride, int rows, int width) {
+  over_rows<T>(rows, width, whole_pieces(src, stride, width), [&](int r, int c, int n) {
+    if (n > 1) cp_async16(dst + r * pitch + c, src + r * stride + c);
+    else dst[r * pitch + c] = src[r * stride + c];
+  });
+}
+// The queries, as bf16 parts [parts][rows][pitch], columns up to the next multiple of 16 as 0.
 __device__ __forceinline__ void bring_queries(__nv_bfloat16* dst, int pitch, int /*all*/, const __nv_bfloat16* src,
                                               int64_t stride, int rows, int width) {
-  bring_rows(dst, pitch, src, stride, rows, width, true);
+  bring_rows(dst, pitch, src, stride, rows, width);
+  const int pad = -width & 15;
+  if ((int)threadIdx.x < rows)
+    for (int x = 0; x < pad; ++x) dst[threadIdx.x * pitch + width + x] = __float2bfloat16_rn(0.f);
 }
 __device__ __forceinline__ void bring_queries(__nv_bfloat16* dst, int pitch, int all, const float* src,
                                               int64_t stride, int rows, int width) {
   const int pairs = ((width + 15) & ~15) / 2;
-#pragma unroll 4
-  for (int x = threadIdx.x; x < rows * pairs; x += kConsumerThreads) {
-    const int r = x / pairs, c = 2 * (x - r * pairs);
+  over_rows<float>(rows, pairs, false, [&](int r, int p, int) {
+    const int c = 2 * p;
     uint32_t part[3];
     split2(c < width ? src[r * stride + c] : 0.f, c + 1 < width ? src[r * stride + c + 1] : 0.f, part);
 #pragma unroll
     for (int j = 0; j < 3; ++j) *reinterpret_cast<uint32_t*>(dst + (j * all + r) * pitch + c) = part[j];
-  }
+  });
 }
 
+// Infinity or NaN, in x or in either half of two bf16.
 __device__ __forceinline__ bool is_odd(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+__device__ __forceinline__ bool is_odd2(uint32_t x) {
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
 
 __device__ __forceinline__ float4 load_remote4(const float* p, uint32_t rank) {
   uint32_t at;
@@ -257,16 +304,15 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   }
   const int N = min(a.N, node0 + NQ), queries = N - node0;  // nodes that matter here
   const int j = pos >> kLogW, r = pos & (kW - 1), par = j & 1, to = __ffs(j + 1) - 1, live = __popc(j);
-  uint8_t* body = dyn + (size_t)a.stages * kStageBytes;
+  uint8_t* body = dyn + (size_t)a.own * kStageBytes;
   const TreeLayout lay = tree_layout<T, NT>(dk, dv, a.N);
-  __nv_bfloat16* qs = reinterpret_cast<__nv_bfloat16*>(body + lay.q);
-  T* ks = reinterpret_cast<T*>(body + lay.k);
-  __nv_bfloat16* ps = reinterpret_cast<__nv_bfloat16*>(body + lay.k);
-  float* red = reinterpret_cast<float*>(body + lay.k);
+  __nv_bfloat16* ps = reinterpret_cast<__nv_bfloat16*>(body + lay.p);
   T* vs = reinterpret_cast<T*>(body + lay.v);
+  __nv_bfloat16* qs = reinterpret_cast<__nv_bfloat16*>(body + lay.q);
   float* lam_s = reinterpret_cast<float*>(body + lay.lam);
   float* page_w = reinterpret_cast<float*>(body + lay.pw);
-  float* wt = reinterpret_cast<float*>(dyn + (size_t)(a.stages - 1) * kStageBytes);  // the last stage, until the pages need it
+  float* wt = reinterpret_cast<float*>(dyn + (size_t)(a.own - 1) * kStageBytes);  // the last own stage, until the pages need it
+  float* red = reinterpret_cast<float*>(dyn);                                       // the ring, behind the pages
 
   // geometry of the pages: col_boxes boxes of 32 columns, the rows in stages of `span`
   const int col_boxes = (dv + 31) / 32, box_log = a.box_log, box_rows = 1 << box_log, box_bytes = box_rows * 128;
@@ -274,22 +320,12 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   const int steps = (dk + 15) / 16, share = (steps + Z - 1) / Z * 16;
   const int k0 = min(dk, sp * share), k1 = min(dk, k0 + share);  // this CTA's rows
 
-  if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      tc::mbar_init(&sm.full[i], 1);
-      tc::mbar_init(&sm.empty[i], kTreeWarps);
-    }
-    tc::fence_mbar_init();
-    sm.bad = before_pages(c, s, pos) ? LL_CACHE_ERR_POSITION : 0;
-    sm.odd = 0;
-  }
-  __syncthreads();
-
+  auto stage_at = [&](int i) { return dyn + (size_t)i * kStageBytes; };  // (those behind the ring's own: the tokens' place)
   // the producer's place in the pages: page, row; stage and how often it was used
   int m = 0, d0 = k0, st = 0, use = 0;
   auto bring_stage = [&]() {
     const int rows = min(span, k1 - d0), boxes = (rows + box_rows - 1) >> box_log;
-    uint8_t* to_ = dyn + (size_t)st * kStageBytes;
+    uint8_t* to_ = stage_at(st);
     tc::mbar_arrive_expect_tx(&sm.full[st], boxes * col_boxes * box_bytes);
     for (int b = 0; b < boxes; ++b)
       for (int x = 0; x < col_boxes; ++x)
@@ -304,11 +340,32 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
       ++use;
     }
   };
+  const T* gk = static_cast<const T*>(a.k) + row * a.sk[0] + (h / G) * a.sk[2];
+  const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
+  const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk;
+  const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
+  const int lanes_g = lane >> 2, lanes_i = 2 * (lane & 3);
+  const int tiles = kW / 16 + (N + 15) / 16;  // of 16 tokens: the block's, then the nodes; one per warp
+  const bool mine = w < tiles && w % Z == sp && (w >= kW / 16 || 16 * w < r);
+  const bool v_vec = whole_pieces(gv, a.sv[1], dv);
+  const T* key[2];  // the thread's rows of its warp's tile: tokens g and g + 8, null where there is none
+  bool key_vec = false;
+  uint32_t key_word[sizeof(T) == 2 ? 4 : 1][2][kIn][4];  // (bf16) all of them, on their way from the start
   bool ok = true;
   if (w == kTreeWarps) {
+    if (lane == 0) {
+      for (int i = 0; i < a.stages; ++i) {
+        tc::mbar_init(&sm.full[i], 1);
+        tc::mbar_init(&sm.empty[i], kTreeWarps);
+      }
+      tc::fence_mbar_init();
+      sm.odd = 0;
+      sm.odd_q = 0;
+    }
     const bool here = lane < M && (j >> lane) & 1;
     const int e = here ? c.page_table[(int64_t)s * M + lane] : 0;
     const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
+    const bool before = before_pages(c, s, pos);
     if (here) {
       const int at = __popc(j & ((1 << lane) - 1));
       sm.page_at[at] = e;
@@ -316,57 +373,98 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
       sm.page_log[at] = log;
     }
     const bool missing = __any_sync(0xffffffffu, e < 0 || e >= c.n_pages);
-    if (missing && lane == 0) atomicOr(&sm.bad, LL_CACHE_ERR_MISSING);
-    if (!missing && lane == 0 && k0 < k1)
-      while (m < live && use == 0 && st < a.stages - 1) bring_stage();
+    if (lane == 0) {
+      sm.bad[w] = (missing ? LL_CACHE_ERR_MISSING : 0) | (before ? LL_CACHE_ERR_POSITION : 0);
+      if (!missing && k0 < k1)
+        while (m < live && use == 0 && st < a.own - 1) bring_stage();
+    }
     __syncwarp();
   } else {
-    const T* gq = static_cast<const T*>(a.q) + row * a.sq[0] + (h / G) * a.sq[2] + node0 * a.sq[1];
-    const T* gk = static_cast<const T*>(a.k) + row * a.sk[0] + (h / G) * a.sk[2];
-    const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
-    const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk;
-    const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
-    bring_queries(qs, lay.kq, NQ, gq, a.sq[1], queries, dk);
-    bring_rows(ks, lay.kq, wk, dk, r, dk, true);
-    bring_rows(ks + kW * lay.kq, lay.kq, gk, a.sk[1], N, dk, true);
+    int up = -2;
+    float la = 0.f;
+    if (tid < a.N) {
+      up = a.parents[(int64_t)row * a.N + tid];
+      if (a.log_a) la = a.log_a[((int64_t)row * a.N + tid) * H + h];
+    }
+    bring_queries(qs, lay.kq, NQ, static_cast<const T*>(a.q) + row * a.sq[0] + (h / G) * a.sq[2] + node0 * a.sq[1],
+                  a.sq[1], queries, dk);
+    for (int q = w; q < queries; q += kTreeWarps)
+      if (lane < M + kLogW + 1)
+        tc::cp_async4(lam_s + q * kLamPitch + lane, a.lam + (((int64_t)row * a.N + node0 + q) * H + h) * a.L + lane, 4);
     cp_async_commit();
-    bring_rows(vs, lay.vp, wv, dv, r, dv, false);
-    bring_rows(vs + kW * lay.vp, lay.vp, gv, a.sv[1], N, dv, false);
+    bring_rows(vs, lay.vp, wv, dv, r, dv);
+    bring_rows(vs + kW * lay.vp, lay.vp, gv, a.sv[1], N, dv);
     cp_async_commit();
-    for (int x = tid; x < (((r + 15) & ~15) - r) * dv; x += kConsumerThreads)  // no tokens: no values
-      vs[(r + x / dv) * lay.vp + x % dv] = from_f32<T>(0.f);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = 16 * w + lanes_g + 8 * u;
+      key[u] = !mine ? nullptr : x < kW ? (x < r ? wk + x * dk : nullptr) : x - kW < N ? gk + (x - kW) * a.sk[1] : nullptr;
+    }
+    key_vec = w < kW / 16 ? whole_pieces(wk, dk, dk) : whole_pieces(gk, a.sk[1], dk);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) load_words(key_word[d][u], key[u], 32 * d + 4 * lanes_i, key[u] ? dk : 0, key_vec);
+    }
+    // no tokens, no values: up to a whole tile behind the block's and the nodes
+    over_rows<T>(-r & 15, dv, false, [&](int y, int x, int) { vs[(r + y) * lay.vp + x] = from_f32<T>(0.f); });
+    over_rows<T>(-N & 15, dv, false, [&](int y, int x, int) { vs[(kW + N + y) * lay.vp + x] = from_f32<T>(0.f); });
+    unsigned bad = 0;
     if (tid < kNodes) {
-      const int up = tid < a.N ? a.parents[(int64_t)row * a.N + tid] : -2;
       const bool fine = up < tid && up >= -2;
-      if (!fine) atomicOr(&sm.bad, LL_CACHE_ERR_TREE);
+      if (!fine) bad = LL_CACHE_ERR_TREE;
       sm.up[tid] = fine ? up : -2;
-      sm.la[tid] = fine && up != -2 && a.log_a ? a.log_a[((int64_t)row * a.N + tid) * H + h] : 0.f;
+      sm.la[tid] = up != -2 ? la : 0.f;
     } else if (w == 2) {
       float since;
       block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], sm.after, &since);
       if (lane == 0) sm.since = since;
     }
-    for (int x = tid; x < queries * kLamPitch; x += kConsumerThreads)
-      if (x % kLamPitch < M + kLogW + 1)
-        lam_s[x] = a.lam[(((int64_t)row * a.N + node0 + x / kLamPitch) * H + h) * a.L + x % kLamPitch];
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (lane == 0) sm.bad[w] = bad;
+    cp_async_wait<1>();
   }
   __syncthreads();
-  if (tid < kNodes) {
+  if (tid < kNodes) {  // the nodes' paths; weights and log decays along those of the queries
     unsigned long long above = 0;
+    unsigned bad = 0;
     int depth = -1;
     const bool in = sm.up[tid] != -2;
     for (int x = tid; in && x >= 0; x = sm.up[x]) {
       above |= 1ull << x;
       ++depth;
-      if (sm.up[x] == -2) atomicOr(&sm.bad, LL_CACHE_ERR_TREE);  // a child of a node that is left out
+      if (sm.up[x] == -2) bad = LL_CACHE_ERR_TREE;  // a child of a node that is left out
     }
-    if (in && !position_ok(c, (int64_t)pos + depth)) atomicOr(&sm.bad, LL_CACHE_ERR_POSITION);
+    const int q = tid - node0, t = pos + depth;
+    if (in && !position_ok(c, t)) bad |= LL_CACHE_ERR_POSITION;
     sm.above[tid] = above;
     sm.depth[tid] = depth;
+    if (in && !bad && q >= 0 && q < queries) {
+      float acc = 0.f;  // log a behind x up to the node
+      for (int x = tid, tx = t; x >= 0; x = sm.up[x], --tx) {
+        wt[q * kNodes + x] = lam_s[q * kLamPitch + fenwick_level(t, tx)] * expf(acc);
+        acc += sm.la[x];
+      }
+      sm.first[tid] = acc;
+    }
+    tc::fence_proxy_async_smem();  // the stage's pages are written behind the weights
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (lane == 0) sm.bad_tree[w] = bad;
+  } else if (w < kTreeWarps) {  // queries that are infinite or NaN
+    bool odd = false;
+    for (int q = w - 2; q < queries; q += kTreeWarps - 2)
+      for (int x = 2 * lane; x < dk; x += 64)
+#pragma unroll
+        for (int y = 0; y < kIn; ++y) odd |= is_odd2(*reinterpret_cast<const uint32_t*>(qs + (y * NQ + q) * lay.kq + x));
+    if (odd) sm.odd_q = 1;
   }
   __syncthreads();
-  if (sm.bad) {
-    if (tid == 0 && speaks) raise(c, sm.bad);
+  unsigned bad = sm.bad_tree[0] | sm.bad_tree[1];
+#pragma unroll
+  for (int i = 0; i <= kTreeWarps; ++i) bad |= sm.bad[i];
+  if (bad) {
+    if (tid == 0 && speaks) raise(c, bad);
     if (w == kTreeWarps) {
       for (int i = 0; lane == 0 && i < st; ++i) tc::mbar_wait_short(&sm.full[i], 0);  // the copies on their way
     } else {
@@ -378,8 +476,8 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   if (w == kTreeWarps) {
     if (lane == 0 && k0 < k1) {
       while (m < live) {
-        // the last stage has one more release: of the tree's weights
-        const int released = use + (st == a.stages - 1);
+        // the last own stage and those behind it have one more release, of what they hold first
+        const int released = use + (st >= a.own - 1);
         if (released && !(ok = tc::mbar_wait_short(&sm.empty[st], (released - 1) & 1))) break;
         bring_stage();
       }
@@ -393,104 +491,80 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
     }
     __syncwarp();
   } else {
-    // log decays of the paths, and the weight of every node above another: sums along the path
-    if (tid < queries && sm.up[node0 + tid] != -2) {
-      const int i = node0 + tid, t = pos + sm.depth[i];
-      float acc = 0.f;  // log a behind x up to the node
-      for (int x = i; x >= 0; x = sm.up[x]) {
-        wt[tid * kNodes + x] = lam_s[tid * kLamPitch + fenwick_level(t, pos + sm.depth[x])] * expf(acc);
-        acc += sm.la[x];
-      }
-      sm.first[i] = acc;
-      tc::fence_proxy_async_smem();  // the stage's pages are written behind the weights
-    }
-    cp_async_wait<1>();
-    consumer_sync();
-    // scores of 16 tokens per warp, K q^T, weighted
-    const int lanes_g = lane >> 2, lanes_i = 2 * (lane & 3);
-    const int tiles = kW / 16 + (N + 15) / 16;  // of tokens: the block's, then the nodes
-    const bool mine = w < tiles && w % Z == sp && (w >= kW / 16 || 16 * w < r);
-    float sc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) sc[t][u] = 0.f;
+    // scores of 16 tokens per warp, K q^T, weighted.  Each thread has 8 neighbouring values of a row, so the
+    // sum goes over them in another order than the fragments': the same for keys and queries.
     if (mine) {
-      for (int d = 0; d < dk; d += 16) {
-        uint32_t ka[kIn][4];
-        load_a_rows(ka, ks + 16 * w * lay.kq, lay.kq, d);
-#pragma unroll
-        for (int y = kIn - 1; y >= 0; --y) {
-          uint32_t qb[NT][2];
-          load_b<NT>(qb, qs + y * NQ * lay.kq, lay.kq, d);
-#pragma unroll
-          for (int x = kIn - 1 - y; x >= 0; --x)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma_bf16(sc[t], ka[x], qb[t][0], qb[t][1]);
-        }
-      }
+      float sc[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int q = 8 * t + lanes_i + (u & 1), x = 16 * w + lanes_g + (u >> 1) * 8, i = node0 + q;
-          float f = 0.f;
-          bool on = false;
-          if (q < queries && sm.up[i] != -2) {
-            if (x < kW) {
-              on = x < r;
-              if (on)
-                f = lam_s[q * kLamPitch + fenwick_level(pos + sm.depth[i], (j << kLogW) + x)] *
-                    expf(sm.after[x] + sm.first[i]);
-            } else if (x - kW < N) {
-              on = sm.above[i] >> (x - kW) & 1;
-              if (on) f = wt[q * kNodes + x - kW];
+        for (int u = 0; u < 4; ++u) sc[t][u] = 0.f;
+      const int dk16 = (dk + 15) & ~15;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int at = 32 * d + 4 * lanes_i;
+        if (32 * d >= dk) break;
+        uint32_t kw[2][kIn][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) kw[u][0][x] = key_word[d][u][0][x];
+          } else {
+            load_words(kw[u], key[u], at, key[u] ? dk : 0, key_vec);
+          }
+        }
+#pragma unroll
+        for (int y = kIn - 1; y >= 0; --y)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (at < dk16) q = *reinterpret_cast<const uint4*>(qs + (y * NQ + 8 * t + lanes_g) * lay.kq + at);
+#pragma unroll
+            for (int x = kIn - 1 - y; x >= 0; --x) {
+              const uint32_t lo[4] = {kw[0][x][0], kw[1][x][0], kw[0][x][1], kw[1][x][1]};
+              const uint32_t hi[4] = {kw[0][x][2], kw[1][x][2], kw[0][x][3], kw[1][x][3]};
+              mma_bf16(sc[t], lo, q.x, q.y);
+              mma_bf16(sc[t], hi, q.z, q.w);
             }
           }
-          sc[t][u] = on ? f * sc[t][u] : 0.f;
+      }
+      const bool nodes = w >= kW / 16;
+      const int x0 = 16 * w + lanes_g - (nodes ? kW : 0);  // the thread's tokens: x0 and x0 + 8
+      const float after0 = nodes ? 0.f : sm.after[x0], after1 = nodes ? 0.f : sm.after[x0 + 8];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int q = 8 * t + lanes_i;
+        float2 f[2];  // [token][node]
+        if (nodes) {
+          const unsigned long long a0 = sm.above[node0 + q] >> x0, a1 = sm.above[node0 + q + 1] >> x0;
+          f[0].x = a0 & 1 ? wt[q * kNodes + x0] * sc[t][0] : 0.f;
+          f[0].y = a1 & 1 ? wt[(q + 1) * kNodes + x0] * sc[t][1] : 0.f;
+          f[1].x = a0 >> 8 & 1 ? wt[q * kNodes + x0 + 8] * sc[t][2] : 0.f;
+          f[1].y = a1 >> 8 & 1 ? wt[(q + 1) * kNodes + x0 + 8] * sc[t][3] : 0.f;
+        } else {
+          const int2 depth = *reinterpret_cast<const int2*>(&sm.depth[node0 + q]);
+          const float2 first = *reinterpret_cast<const float2*>(&sm.first[node0 + q]);
+          const float* lam0 = lam_s + q * kLamPitch;
+          const int t0 = pos + depth.x, t1 = pos + depth.y, s0 = (j << kLogW) + x0, s1 = s0 + 8;
+          f[0].x = depth.x >= 0 && s0 < pos ? lam0[fenwick_level(t0, s0)] * expf(after0 + first.x) * sc[t][0] : 0.f;
+          f[1].x = depth.x >= 0 && s1 < pos ? lam0[fenwick_level(t0, s1)] * expf(after1 + first.x) * sc[t][2] : 0.f;
+          lam0 += kLamPitch;
+          f[0].y = depth.y >= 0 && s0 < pos ? lam0[fenwick_level(t1, s0)] * expf(after0 + first.y) * sc[t][1] : 0.f;
+          f[1].y = depth.y >= 0 && s1 < pos ? lam0[fenwick_level(t1, s1)] * expf(after1 + first.y) * sc[t][3] : 0.f;
         }
-    }
-    cp_async_wait<0>();
-    consumer_sync();  // the keys and the tree's weights are done with, the values are there
-    if (lane == 0) tc::mbar_arrive(&sm.empty[a.stages - 1]);
-    if (mine) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < 4; u += 2) {
+        for (int u = 0; u < 2; ++u) {
           uint32_t part[kPage];
-          split2(sc[t][u], sc[t][u + 1], part);
-          __nv_bfloat16* at = ps + (8 * t + lanes_i) * lay.tp + 16 * w + lanes_g + (u >> 1) * 8;
+          split2(f[u].x, f[u].y, part);
+          __nv_bfloat16* at = ps + q * lay.tp + 16 * w + lanes_g + 8 * u;
 #pragma unroll
           for (int x = 0; x < kPage; ++x) {
             at[x * NQ * lay.tp] = __ushort_as_bfloat16((unsigned short)(part[x] & 0xffffu));
             at[x * NQ * lay.tp + lay.tp] = __ushort_as_bfloat16((unsigned short)(part[x] >> 16));
           }
         }
-    }
-    // values of nodes: none where a node is left out; infinities and NaN go by themselves, to the
-    // nodes below them alone
-    {
-      const int rows = (N + 15) & ~15;
-      bool odd = false;
-      for (int x = tid; x < rows * (dv / 4); x += kConsumerThreads) {
-        const int y = x / (dv / 4);
-        T* p = vs + (kW + y) * lay.vp + 4 * (x - y * (dv / 4));
-        if (y >= N || sm.up[y] == -2) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) p[u] = from_f32<T>(0.f);
-        } else {
-          const float4 v = load4(p);
-          if (is_odd(v.x) || is_odd(v.y) || is_odd(v.z) || is_odd(v.w)) {
-            odd = true;
-            if (is_odd(v.x)) p[0] = from_f32<T>(0.f);
-            if (is_odd(v.y)) p[1] = from_f32<T>(0.f);
-            if (is_odd(v.z)) p[2] = from_f32<T>(0.f);
-            if (is_odd(v.w)) p[3] = from_f32<T>(0.f);
-          }
-        }
       }
-      if (odd) sm.odd = 1;
     }
     for (int x = tid; x < live * NQ; x += kConsumerThreads) {
       const int y = x / NQ, q = x - y * NQ, i = node0 + q;
@@ -501,7 +575,30 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
       }
       page_w[x] = f;
     }
-    consumer_sync();
+    // values of nodes, each thread the ones it brought: none where a node is left out; infinities and
+    // NaN go by themselves, to the nodes below them alone
+    cp_async_wait<0>();
+    over_rows<T>(N, dv, v_vec, [&](int y, int x, int n) {
+      T* p = vs + (kW + y) * lay.vp + x;
+      const bool out = sm.up[y] == -2;
+      if (n > 1) {
+        uint4 v = *reinterpret_cast<const uint4*>(p);
+        bool odd;
+        if constexpr (sizeof(T) == 2) odd = is_odd2(v.x) || is_odd2(v.y) || is_odd2(v.z) || is_odd2(v.w);
+        else odd = is_odd(__uint_as_float(v.x)) || is_odd(__uint_as_float(v.y)) || is_odd(__uint_as_float(v.z)) || is_odd(__uint_as_float(v.w));
+        if (odd || out) {
+          if (!out) sm.odd = 1;
+#pragma unroll
+          for (int u = 0; u < 16 / (int)sizeof(T); ++u)
+            if (out || is_odd(to_f32(p[u]))) p[u] = from_f32<T>(0.f);
+        }
+      } else if (out || is_odd(to_f32(*p))) {
+        if (!out) sm.odd = 1;
+        *p = from_f32<T>(0.f);
+      }
+    });
+    consumer_sync();  // the tokens' weights and values are there, the tree's weights are done with
+    if (lane == 0) tc::mbar_arrive(&sm.empty[a.own - 1]);
 
     // a warp's 16 columns; where there are few, warps share them by tokens and by rows of the pages
     const int cols = (dv + 15) / 16, wide = cols > 4 ? 8 : cols > 2 ? 4 : cols;
@@ -546,7 +643,6 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
     }
     const int col = 16 * ct + 2 * lanes_g;
     if (sm.odd && on && kp == 0 && col < dv) {
-      const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
       for (int y = 0; y < N; ++y) {
         if ((kW + y) / 16 % Z != sp) continue;
         const float v0 = to_f32(gv[y * a.sv[1] + col]), v1 = to_f32(gv[y * a.sv[1] + col + 1]);
@@ -565,7 +661,16 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
       }
     }
 
+    if (a.stages > a.own) {  // the tokens' weights and values are done with
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int i = a.own; i < a.stages; ++i) tc::mbar_arrive(&sm.empty[i]);
+    }
+
     // the pages
+    const bool plain = sm.odd_q == 0;
+    const int mine_rows = wide > 1 ? 32 : 16;  // neighbouring rows of a stage that a warp takes
     int st_ = 0, phase = 0;
     const int chunk = 4 * (ct & 1) + (lanes_g >> 1);
     const uint32_t off0 = tc::sw128_offset(lanes_i, chunk) + (lanes_g & 1) * 8;
@@ -579,32 +684,44 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
       for (int d = k0; d < k1; d += span) {
         if (ok) ok = tc::mbar_wait_short(&sm.full[st_], phase);
         if (on) {
-          const uint8_t* stage = dyn + (size_t)st_ * kStageBytes + (ct >> 1) * box_bytes;
-          for (int y = 16 * kp; y < min(span, k1 - d); y += 16 * kparts) {
-            const uint8_t* at = stage + (y >> box_log) * col_boxes * box_bytes + (y & (box_rows - 1)) * 128;
-            const float2 x0 = *reinterpret_cast<const float2*>(at + off0), x1 = *reinterpret_cast<const float2*>(at + off1);
-            const float2 x2 = *reinterpret_cast<const float2*>(at + off0 + 1024), x3 = *reinterpret_cast<const float2*>(at + off1 + 1024);
-            uint32_t pa[kPage][4], p0[kPage], p1[kPage], p2[kPage], p3[kPage];
-            split2(x0.x, x1.x, p0);
-            split2(x0.y, x1.y, p1);
-            split2(x2.x, x3.x, p2);
-            split2(x2.y, x3.y, p3);
+          const uint8_t* stage = stage_at(st_) + (ct >> 1) * box_bytes;
+          const int rows = min(span, k1 - d);
+          for (int y0 = mine_rows * kp; y0 < rows; y0 += mine_rows * kparts) {
+            float2 v[2][4];
 #pragma unroll
-            for (int u = 0; u < kPage; ++u) {
-              pa[u][0] = p0[u];
-              pa[u][1] = p1[u];
-              pa[u][2] = p2[u];
-              pa[u][3] = p3[u];
+            for (int z = 0; z < 2; ++z) {
+              const int y = y0 + 16 * z;
+              if (z && (mine_rows == 16 || y >= rows)) continue;
+              const uint8_t* at = stage + (y >> box_log) * col_boxes * box_bytes + (y & (box_rows - 1)) * 128;
+              v[z][0] = *reinterpret_cast<const float2*>(at + off0);
+              v[z][1] = *reinterpret_cast<const float2*>(at + off1);
+              v[z][2] = *reinterpret_cast<const float2*>(at + off0 + 1024);
+              v[z][3] = *reinterpret_cast<const float2*>(at + off1 + 1024);
             }
 #pragma unroll
-            for (int v = kIn - 1; v >= 0; --v) {
-              uint32_t qb[NT][2];
-              load_b<NT>(qb, qs + v * NQ * lay.kq, lay.kq, d + y);
+            for (int z = 0; z < 2; ++z) {
+              const int y = y0 + 16 * z;
+              if (z && (mine_rows == 16 || y >= rows)) continue;
+              uint32_t pa[kPage][4];
 #pragma unroll
-              for (int u = kPage - 1; u >= 0; --u)
-                if (u + v < kPage)
+              for (int u = 0; u < 4; ++u) {
+                const float2 lo = v[z][u & 2], hi = v[z][(u & 2) + 1];
+                uint32_t cut[kPage];
+                if (plain) split2_page(u & 1 ? lo.y : lo.x, u & 1 ? hi.y : hi.x, cut);
+                else split2(u & 1 ? lo.y : lo.x, u & 1 ? hi.y : hi.x, cut);
 #pragma unroll
-                  for (int t = 0; t < NT; ++t) mma_bf16(part[t], pa[u], qb[t][0], qb[t][1]);
+                for (int x_ = 0; x_ < kPage; ++x_) pa[x_][u] = cut[x_];
+              }
+#pragma unroll
+              for (int v_ = kIn - 1; v_ >= 0; --v_) {
+                uint32_t qb[NT][2];
+                load_b<NT>(qb, qs + v_ * NQ * lay.kq, lay.kq, d + y);
+#pragma unroll
+                for (int u = kPage - 1; u >= 0; --u)
+                  if (u + v_ < kPage)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_bf16(part[t], pa[u], qb[t][0], qb[t][1]);
+              }
             }
           }
         }
@@ -659,7 +776,7 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
 #pragma unroll
         for (int t = 0; t < NT; ++t) put(t, ct, acc[t]);
     } else {
-      consumer_sync();  // the tokens' weights are done with
+      consumer_sync();  // the ring is done with
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         *reinterpret_cast<float4*>(red + ((t * kTreeWarps + w) * 32 + lane) * 4) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
@@ -708,7 +825,7 @@ int tree_split(int64_t items, int dk, int sms) {
   return split;
 }
 
-constexpr size_t kSmTwo = 115000, kSmOne = 232448;  // shared memory of a CTA where two are on an SM, and of one alone
+constexpr size_t kSmTwo = 115712, kSmOne = 232448;  // shared memory of a CTA where two are on an SM, and of one alone
 
 template <typename T, int NT>
 cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
@@ -718,11 +835,15 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   a.split = tree_split(items, dk, sm_count());
   const int share = ((dk + 15) / 16 + a.split - 1) / a.split * 16;
   a.box_log = share % 32 ? 4 : 5;
-  const size_t body = (size_t)tree_layout<T, NT>(dk, dv, a.N).end + sizeof(TreeSmem) + 1024;
+  const TreeLayout lay = tree_layout<T, NT>(dk, dv, a.N);
+  const size_t fixed = sizeof(TreeSmem) + 1024;
+  // two CTAs on an SM where that leaves the ring two stages from the start, or one and three later
+  const int later = lay.q / kStageBytes;
   size_t room = kSmTwo;
-  if (body + 2 * kStageBytes > room) room = kSmOne;
-  a.stages = (int)std::min<size_t>(kMaxTreeStages, (room - body) / kStageBytes);
-  const size_t smem = (size_t)a.stages * kStageBytes + tree_layout<T, NT>(dk, dv, a.N).end;
+  if (fixed + lay.end + (later >= 3 ? 1 : 2) * kStageBytes > room) room = kSmOne;
+  a.own = (int)std::min<size_t>(kMaxTreeStages, (room - fixed - lay.end) / kStageBytes);
+  a.stages = std::min(kMaxTreeStages, a.own + later);
+  const size_t smem = (size_t)a.own * kStageBytes + lay.end;
   CUtensorMap pages;
   if (!make_pages_map(&pages, c.pages, c.n_pages, c.H, c.dk, c.dv, 1 << a.box_log)) return cudaErrorInvalidValue;
   const auto kernel = cache_tree_kernel<T, NT>;
