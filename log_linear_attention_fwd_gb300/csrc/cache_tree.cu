@@ -9,6 +9,7 @@
 // ctz(j + 1) and block j itself as one Fenwick bucket, level 7 + ctz(j + 1).  So a tree that
 // runs over a block's end needs no fold, and nothing is written but the outputs.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache_common.cuh"
 
@@ -29,7 +30,7 @@ struct TreeArgs {
   const float* lam;
   void* out;
   int n, N, L, out_f32;
-  int split, groups, own, stages, box_log;  // own: stages that are only the ring's
+  int split, groups, own, stages, box_rows;  // own: stages that are only the ring's
 };
 
 // A CTA serves one (row, head) for up to 8 NT nodes: eight consumer warps, and a producer warp that
@@ -76,6 +77,10 @@ __host__ __device__ __forceinline__ TreeLayout tree_layout(int dk, int dv, int N
   return l;
 }
 
+// CTAs that registers leave on an SM.
+template <typename T, int NT>
+constexpr int tree_ctas() { return sizeof(T) == 2 ? (NT <= 4 ? 3 : 1) : 1; }
+
 struct TreeSmem {
   uint64_t full[kMaxTreeStages], empty[kMaxTreeStages];
   float after[kW];                   // log decay from each token of the block to the context's last
@@ -103,17 +108,17 @@ template <int kLeft>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const __nv_bfloat16* p) {
+__device__ __forceinline__ void ldmatrix4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(tc::smem_u32(p))
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(at)
                : "memory");
 }
-__device__ __forceinline__ void ldmatrix2(uint32_t& r0, uint32_t& r1, const __nv_bfloat16* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
-               : "=r"(r0), "=r"(r1)
-               : "r"(tc::smem_u32(p))
-               : "memory");
+__device__ __forceinline__ void ldmatrix2(uint32_t& r0, uint32_t& r1, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void load2(float2& v, uint32_t at) {
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
 }
 
 // x and y as bf16 parts, packed.  Cut off towards zero but for the last, and what is left of a value
@@ -149,17 +154,11 @@ template <int NT>
 __device__ __forceinline__ void load_b(uint32_t (&b)[NT][2], const __nv_bfloat16* rows, int pitch, int k0) {
   const int lane = threadIdx.x & 31;
   if constexpr (NT == 1) {
-    ldmatrix2(b[0][0], b[0][1], rows + (lane & 7) * pitch + k0 + ((lane >> 3) & 1) * 8);
+    ldmatrix2(b[0][0], b[0][1], tc::smem_u32(rows + (lane & 7) * pitch + k0 + ((lane >> 3) & 1) * 8));
   } else {
+    const uint32_t at = tc::smem_u32(rows + ((lane & 7) + ((lane >> 4) << 3)) * pitch + k0 + ((lane >> 3) & 1) * 8);
 #pragma unroll
-    for (int t = 0; t < NT; t += 2) {
-      uint32_t r[4];
-      ldmatrix4(r, rows + (8 * t + (lane & 7) + ((lane >> 4) << 3)) * pitch + k0 + ((lane >> 3) & 1) * 8);
-      b[t][0] = r[0];
-      b[t][1] = r[1];
-      b[t + 1][0] = r[2];
-      b[t + 1][1] = r[3];
-    }
+    for (int t = 0; t < NT; t += 2) ldmatrix4(b[t][0], b[t][1], b[t + 1][0], b[t + 1][1], at + 16 * t * pitch);
   }
 }
 // 8 values of a row from column k on, 0 past `width`, as words of bf16 parts.
@@ -285,7 +284,7 @@ __device__ __forceinline__ float4 load_remote4(const float* p, uint32_t rank) {
 
 // grid: (row, head, group of nodes, share of the cluster), the last fastest.
 template <typename T, int NT>
-__global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 1)
+__global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
     cache_tree_kernel(const __grid_constant__ CUtensorMap pages, ll_cache c, TreeArgs a) {
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ TreeSmem sm;
@@ -314,9 +313,8 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   float* wt = reinterpret_cast<float*>(dyn + (size_t)(a.own - 1) * kStageBytes);  // the last own stage, until the pages need it
   float* red = reinterpret_cast<float*>(dyn);                                       // the ring, behind the pages
 
-  // geometry of the pages: col_boxes boxes of 32 columns, the rows in stages of `span`
-  const int col_boxes = (dv + 31) / 32, box_log = a.box_log, box_rows = 1 << box_log, box_bytes = box_rows * 128;
-  const int span = col_boxes == 1 ? 128 : col_boxes == 2 ? 64 : 32;
+  // geometry of the pages: col_boxes boxes of 32 columns, the rows in stages of box_rows
+  const int col_boxes = (dv + 31) / 32, box_rows = a.box_rows, box_bytes = box_rows * 128;
   const int steps = (dk + 15) / 16, share = (steps + Z - 1) / Z * 16;
   const int k0 = min(dk, sp * share), k1 = min(dk, k0 + share);  // this CTA's rows
 
@@ -324,14 +322,11 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   // the producer's place in the pages: page, row; stage and how often it was used
   int m = 0, d0 = k0, st = 0, use = 0;
   auto bring_stage = [&]() {
-    const int rows = min(span, k1 - d0), boxes = (rows + box_rows - 1) >> box_log;
-    uint8_t* to_ = stage_at(st);
-    tc::mbar_arrive_expect_tx(&sm.full[st], boxes * col_boxes * box_bytes);
-    for (int b = 0; b < boxes; ++b)
-      for (int x = 0; x < col_boxes; ++x)
-        tc::tma_load_4d(&pages, &sm.full[st], to_ + (b * col_boxes + x) * box_bytes, 32 * x, d0 + b * box_rows, h,
-                        sm.page_at[m]);
-    if ((d0 += span) >= k1) {
+    uint8_t* at = stage_at(st);
+    tc::mbar_arrive_expect_tx(&sm.full[st], col_boxes * box_bytes);
+    for (int x = 0; x < col_boxes; ++x)
+      tc::tma_load_4d(&pages, &sm.full[st], at + x * box_bytes, 32 * x, d0, h, sm.page_at[m]);
+    if ((d0 += box_rows) >= k1) {
       d0 = k0;
       ++m;
     }
@@ -350,6 +345,8 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   const bool v_vec = whole_pieces(gv, a.sv[1], dv);
   const T* key[2];  // the thread's rows of its warp's tile: tokens g and g + 8, null where there is none
   bool key_vec = false;
+  // the last two consumer warps have a node per thread: their tiles are there for most nodes only
+  const int node = w < kTreeWarps ? tid - (kConsumerThreads - kNodes) : -1;
   uint32_t key_word[sizeof(T) == 2 ? 4 : 1][2][kIn][4];  // (bf16) all of them, on their way from the start
   bool ok = true;
   if (w == kTreeWarps) {
@@ -382,9 +379,9 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
   } else {
     int up = -2;
     float la = 0.f;
-    if (tid < a.N) {
-      up = a.parents[(int64_t)row * a.N + tid];
-      if (a.log_a) la = a.log_a[((int64_t)row * a.N + tid) * H + h];
+    if (node >= 0 && node < a.N) {
+      up = a.parents[(int64_t)row * a.N + node];
+      if (a.log_a) la = a.log_a[((int64_t)row * a.N + node) * H + h];
     }
     bring_queries(qs, lay.kq, NQ, static_cast<const T*>(a.q) + row * a.sq[0] + (h / G) * a.sq[2] + node0 * a.sq[1],
                   a.sq[1], queries, dk);
@@ -411,12 +408,12 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
     over_rows<T>(-r & 15, dv, false, [&](int y, int x, int) { vs[(r + y) * lay.vp + x] = from_f32<T>(0.f); });
     over_rows<T>(-N & 15, dv, false, [&](int y, int x, int) { vs[(kW + N + y) * lay.vp + x] = from_f32<T>(0.f); });
     unsigned bad = 0;
-    if (tid < kNodes) {
-      const bool fine = up < tid && up >= -2;
+    if (node >= 0) {
+      const bool fine = up < node && up >= -2;
       if (!fine) bad = LL_CACHE_ERR_TREE;
-      sm.up[tid] = fine ? up : -2;
-      sm.la[tid] = up != -2 ? la : 0.f;
-    } else if (w == 2) {
+      sm.up[node] = fine ? up : -2;
+      sm.la[node] = up != -2 ? la : 0.f;
+    } else if (w == 0) {
       float since;
       block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], sm.after, &since);
       if (lane == 0) sm.since = since;
@@ -426,38 +423,77 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
     cp_async_wait<1>();
   }
   __syncthreads();
-  if (tid < kNodes) {  // the nodes' paths; weights and log decays along those of the queries
+  if (node >= 0) {  // the nodes' paths; weights and log decays along those of the queries
     unsigned long long above = 0;
     unsigned bad = 0;
     int depth = -1;
-    const bool in = sm.up[tid] != -2;
-    for (int x = tid; in && x >= 0; x = sm.up[x]) {
+    const bool in = sm.up[node] != -2;
+    for (int x = node; in && x >= 0; x = sm.up[x]) {
       above |= 1ull << x;
       ++depth;
       if (sm.up[x] == -2) bad = LL_CACHE_ERR_TREE;  // a child of a node that is left out
     }
-    const int q = tid - node0, t = pos + depth;
+    const int q = node - node0, t = pos + depth;
     if (in && !position_ok(c, t)) bad |= LL_CACHE_ERR_POSITION;
-    sm.above[tid] = above;
-    sm.depth[tid] = depth;
+    sm.above[node] = above;
+    sm.depth[node] = depth;
     if (in && !bad && q >= 0 && q < queries) {
       float acc = 0.f;  // log a behind x up to the node
-      for (int x = tid, tx = t; x >= 0; x = sm.up[x], --tx) {
+      for (int x = node, tx = t; x >= 0; x = sm.up[x], --tx) {
         wt[q * kNodes + x] = lam_s[q * kLamPitch + fenwick_level(t, tx)] * expf(acc);
         acc += sm.la[x];
       }
-      sm.first[tid] = acc;
+      sm.first[node] = acc;
     }
     tc::fence_proxy_async_smem();  // the stage's pages are written behind the weights
     bad = __reduce_or_sync(0xffffffffu, bad);
-    if (lane == 0) sm.bad_tree[w] = bad;
+    if (lane == 0) sm.bad_tree[w - (kTreeWarps - 2)] = bad;
   } else if (w < kTreeWarps) {  // queries that are infinite or NaN
     bool odd = false;
-    for (int q = w - 2; q < queries; q += kTreeWarps - 2)
+    for (int q = w; q < queries; q += kTreeWarps - 2)
       for (int x = 2 * lane; x < dk; x += 64)
 #pragma unroll
         for (int y = 0; y < kIn; ++y) odd |= is_odd2(*reinterpret_cast<const uint32_t*>(qs + (y * NQ + q) * lay.kq + x));
     if (odd) sm.odd_q = 1;
+  }
+  float sc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sc[t][u] = 0.f;
+  // scores of 16 tokens per warp, K q^T, not yet weighted.  Each thread has 8 neighbouring values of a row, so the
+  // sum goes over them in another order than the fragments': the same for keys and queries.
+  if (mine) {
+    const int dk16 = (dk + 15) & ~15;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int at = 32 * d + 4 * lanes_i;
+      if (32 * d >= dk) break;
+      uint32_t kw[2][kIn][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) kw[u][0][x] = key_word[d][u][0][x];
+        } else {
+          load_words(kw[u], key[u], at, key[u] ? dk : 0, key_vec);
+        }
+      }
+#pragma unroll
+      for (int y = kIn - 1; y >= 0; --y)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint4 q = make_uint4(0u, 0u, 0u, 0u);
+          if (at < dk16) q = *reinterpret_cast<const uint4*>(qs + (y * NQ + 8 * t + lanes_g) * lay.kq + at);
+#pragma unroll
+          for (int x = kIn - 1 - y; x >= 0; --x) {
+            const uint32_t lo[4] = {kw[0][x][0], kw[1][x][0], kw[0][x][1], kw[1][x][1]};
+            const uint32_t hi[4] = {kw[0][x][2], kw[1][x][2], kw[0][x][3], kw[1][x][3]};
+            mma_bf16(sc[t], lo, q.x, q.y);
+            mma_bf16(sc[t], hi, q.z, q.w);
+          }
+        }
+    }
   }
   __syncthreads();
   unsigned bad = sm.bad_tree[0] | sm.bad_tree[1];
@@ -491,44 +527,8 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
     }
     __syncwarp();
   } else {
-    // scores of 16 tokens per warp, K q^T, weighted.  Each thread has 8 neighbouring values of a row, so the
-    // sum goes over them in another order than the fragments': the same for keys and queries.
+    // the weighted scores
     if (mine) {
-      float sc[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sc[t][u] = 0.f;
-      const int dk16 = (dk + 15) & ~15;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int at = 32 * d + 4 * lanes_i;
-        if (32 * d >= dk) break;
-        uint32_t kw[2][kIn][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) kw[u][0][x] = key_word[d][u][0][x];
-          } else {
-            load_words(kw[u], key[u], at, key[u] ? dk : 0, key_vec);
-          }
-        }
-#pragma unroll
-        for (int y = kIn - 1; y >= 0; --y)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (at < dk16) q = *reinterpret_cast<const uint4*>(qs + (y * NQ + 8 * t + lanes_g) * lay.kq + at);
-#pragma unroll
-            for (int x = kIn - 1 - y; x >= 0; --x) {
-              const uint32_t lo[4] = {kw[0][x][0], kw[1][x][0], kw[0][x][1], kw[1][x][1]};
-              const uint32_t hi[4] = {kw[0][x][2], kw[1][x][2], kw[0][x][3], kw[1][x][3]};
-              mma_bf16(sc[t], lo, q.x, q.y);
-              mma_bf16(sc[t], hi, q.z, q.w);
-            }
-          }
-      }
       const bool nodes = w >= kW / 16;
       const int x0 = 16 * w + lanes_g - (nodes ? kW : 0);  // the thread's tokens: x0 and x0 + 8
       const float after0 = nodes ? 0.f : sm.after[x0], after1 = nodes ? 0.f : sm.after[x0 + 8];
@@ -668,78 +668,82 @@ __global__ void __launch_bounds__(kTreeThreads, sizeof(T) == 2 && NT <= 4 ? 2 : 
         for (int i = a.own; i < a.stages; ++i) tc::mbar_arrive(&sm.empty[i]);
     }
 
-    // the pages
-    const bool plain = sm.odd_q == 0;
-    const int mine_rows = wide > 1 ? 32 : 16;  // neighbouring rows of a stage that a warp takes
-    int st_ = 0, phase = 0;
+    // the pages.  A warp takes two neighbouring steps of 16 rows of each stage (one where eight warps share
+    // a column tile); addresses are kept as shared-memory offsets, in steps of a stage.
     const int chunk = 4 * (ct & 1) + (lanes_g >> 1);
-    const uint32_t off0 = tc::sw128_offset(lanes_i, chunk) + (lanes_g & 1) * 8;
-    const uint32_t off1 = tc::sw128_offset(lanes_i + 1, chunk) + (lanes_g & 1) * 8;
-    for (int x = 0; x < live && k0 < k1; ++x) {
-      float part[NT][4];
+    const uint32_t rows_at = tc::smem_u32(dyn) + (ct >> 1) * box_bytes + (lanes_g & 1) * 8 + 2048 * (wide > 1 ? 2 * kp : kp);
+    const uint32_t off0 = tc::sw128_offset(lanes_i, chunk), off1 = tc::sw128_offset(lanes_i + 1, chunk);
+    const int first_row = 16 * (wide > 1 ? 2 * kp : kp);
+    const uint32_t q_at = tc::smem_u32(qs) + ((lane & 7) + (NT > 1 ? (lane >> 4) << 3 : 0)) * lay.kq * 2 +
+                          ((lane >> 3) & 1) * 16 + 2 * first_row;
+    const uint32_t q_tiles = 16 * lay.kq * 2, q_parts = NQ * lay.kq * 2;
+    auto over_pages = [&](auto robust) {
+      int stage = 0, phase = 0;
+      for (int x = 0; x < live; ++x) {
+        float part[NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) part[t][u] = 0.f;
-      for (int d = k0; d < k1; d += span) {
-        if (ok) ok = tc::mbar_wait_short(&sm.full[st_], phase);
-        if (on) {
-          const uint8_t* stage = stage_at(st_) + (ct >> 1) * box_bytes;
-          const int rows = min(span, k1 - d);
-          for (int y0 = mine_rows * kp; y0 < rows; y0 += mine_rows * kparts) {
-            float2 v[2][4];
+          for (int u = 0; u < 4; ++u) part[t][u] = 0.f;
+        for (int d = k0; d < k1; d += box_rows) {
+          if (ok) ok = tc::mbar_wait_short(&sm.full[stage], phase);
+          const uint32_t at = rows_at + stage * kStageBytes, qa = q_at + 2 * d;
+          const int rows = min(box_rows, k1 - d) - first_row;  // from this warp's first on
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int y = y0 + 16 * z;
-              if (z && (mine_rows == 16 || y >= rows)) continue;
-              const uint8_t* at = stage + (y >> box_log) * col_boxes * box_bytes + (y & (box_rows - 1)) * 128;
-              v[z][0] = *reinterpret_cast<const float2*>(at + off0);
-              v[z][1] = *reinterpret_cast<const float2*>(at + off1);
-              v[z][2] = *reinterpret_cast<const float2*>(at + off0 + 1024);
-              v[z][3] = *reinterpret_cast<const float2*>(at + off1 + 1024);
+          for (int z = 0; z < 2; ++z) {
+            if (!on || 16 * z >= rows || (z && wide == 1)) continue;
+            float2 v[4];
+            load2(v[0], at + off0 + 2048 * z);
+            load2(v[1], at + off1 + 2048 * z);
+            load2(v[2], at + off0 + 2048 * z + 1024);
+            load2(v[3], at + off1 + 2048 * z + 1024);
+            uint32_t pa[kPage][4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t cut[kPage];
+              const float lo = u & 1 ? v[u & 2].y : v[u & 2].x, hi = u & 1 ? v[(u & 2) + 1].y : v[(u & 2) + 1].x;
+              if constexpr (decltype(robust)::value) split2(lo, hi, cut);
+              else split2_page(lo, hi, cut);
+#pragma unroll
+              for (int y = 0; y < kPage; ++y) pa[y][u] = cut[y];
             }
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int y = y0 + 16 * z;
-              if (z && (mine_rows == 16 || y >= rows)) continue;
-              uint32_t pa[kPage][4];
+            for (int y = kIn - 1; y >= 0; --y) {
+              uint32_t qb[NT][2];
+              const uint32_t q = qa + y * q_parts + 32 * z;
+              if constexpr (NT == 1) {
+                ldmatrix2(qb[0][0], qb[0][1], q);
+              } else {
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float2 lo = v[z][u & 2], hi = v[z][(u & 2) + 1];
-                uint32_t cut[kPage];
-                if (plain) split2_page(u & 1 ? lo.y : lo.x, u & 1 ? hi.y : hi.x, cut);
-                else split2(u & 1 ? lo.y : lo.x, u & 1 ? hi.y : hi.x, cut);
-#pragma unroll
-                for (int x_ = 0; x_ < kPage; ++x_) pa[x_][u] = cut[x_];
+                for (int t = 0; t < NT; t += 2) ldmatrix4(qb[t][0], qb[t][1], qb[t + 1][0], qb[t + 1][1], q + (t / 2) * q_tiles);
               }
 #pragma unroll
-              for (int v_ = kIn - 1; v_ >= 0; --v_) {
-                uint32_t qb[NT][2];
-                load_b<NT>(qb, qs + v_ * NQ * lay.kq, lay.kq, d + y);
+              for (int u = kPage - 1; u >= 0; --u)
+                if (u + y < kPage)
 #pragma unroll
-                for (int u = kPage - 1; u >= 0; --u)
-                  if (u + v_ < kPage)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma_bf16(part[t], pa[u], qb[t][0], qb[t][1]);
-              }
+                  for (int t = 0; t < NT; ++t) mma_bf16(part[t], pa[u], qb[t][0], qb[t][1]);
             }
           }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.empty[stage]);
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.empty[st_]);
-        if (++st_ == a.stages) {
-          st_ = 0;
-          phase ^= 1;
-        }
-      }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float2 f = *reinterpret_cast<const float2*>(page_w + x * NQ + 8 * t + lanes_i);
-        acc[t][0] = fmaf(f.x, part[t][0], acc[t][0]);
-        acc[t][1] = fmaf(f.y, part[t][1], acc[t][1]);
-        acc[t][2] = fmaf(f.x, part[t][2], acc[t][2]);
-        acc[t][3] = fmaf(f.y, part[t][3], acc[t][3]);
+        for (int t = 0; t < NT; ++t) {
+          const float2 f = *reinterpret_cast<const float2*>(page_w + x * NQ + 8 * t + lanes_i);
+          acc[t][0] = fmaf(f.x, part[t][0], acc[t][0]);
+          acc[t][1] = fmaf(f.y, part[t][1], acc[t][1]);
+          acc[t][2] = fmaf(f.x, part[t][2], acc[t][2]);
+          acc[t][3] = fmaf(f.y, part[t][3], acc[t][3]);
+        }
       }
+    };
+    if (k0 < k1) {
+      if (sm.odd_q) over_pages(std::true_type());
+      else over_pages(std::false_type());
     }
     if (!ok && lane == 0) raise(c, LL_CACHE_ERR_WAIT);
 
@@ -825,7 +829,7 @@ int tree_split(int64_t items, int dk, int sms) {
   return split;
 }
 
-constexpr size_t kSmTwo = 115712, kSmOne = 232448;  // shared memory of a CTA where two are on an SM, and of one alone
+constexpr size_t kSm = 233472;  // shared memory of an SM
 
 template <typename T, int NT>
 cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
@@ -834,18 +838,19 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   const int64_t items = (int64_t)a.n * c.H * a.groups;
   a.split = tree_split(items, dk, sm_count());
   const int share = ((dk + 15) / 16 + a.split - 1) / a.split * 16;
-  a.box_log = share % 32 ? 4 : 5;
+  const int col_boxes = (dv + 31) / 32;
+  a.box_rows = std::min(col_boxes == 1 ? 128 : col_boxes == 2 ? 64 : 32, share);  // a stage, or a CTA's share
   const TreeLayout lay = tree_layout<T, NT>(dk, dv, a.N);
-  const size_t fixed = sizeof(TreeSmem) + 1024;
-  // two CTAs on an SM where that leaves the ring two stages from the start, or one and three later
+  const size_t fixed = sizeof(TreeSmem) + 2048;  // (1024 of each CTA are the system's)
+  // as many CTAs on an SM as leave the ring three stages, one of them from the start
   const int later = lay.q / kStageBytes;
-  size_t room = kSmTwo;
-  if (fixed + lay.end + (later >= 3 ? 1 : 2) * kStageBytes > room) room = kSmOne;
-  a.own = (int)std::min<size_t>(kMaxTreeStages, (room - fixed - lay.end) / kStageBytes);
+  int ctas = tree_ctas<T, NT>();
+  while (ctas > 1 && fixed + lay.end + std::max(1, 3 - later) * kStageBytes > kSm / ctas) --ctas;
+  a.own = (int)std::min<size_t>(kMaxTreeStages, (kSm / ctas - fixed - lay.end) / kStageBytes);
   a.stages = std::min(kMaxTreeStages, a.own + later);
   const size_t smem = (size_t)a.own * kStageBytes + lay.end;
   CUtensorMap pages;
-  if (!make_pages_map(&pages, c.pages, c.n_pages, c.H, c.dk, c.dv, 1 << a.box_log)) return cudaErrorInvalidValue;
+  if (!make_pages_map(&pages, c.pages, c.n_pages, c.H, c.dk, c.dv, a.box_rows)) return cudaErrorInvalidValue;
   const auto kernel = cache_tree_kernel<T, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
