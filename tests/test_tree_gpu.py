@@ -2,10 +2,13 @@
 its drafts and the appending of the accepted path, against fp64.
 
 Tolerances as for the cache's step (tests/test_cache_gpu.py): fp32 outputs are sums of up to
-a few hundred products of fp32 values whose decays are off by a few 2^-24, rel-L2 below 1e-5; bf16
-tokens are exact inputs, but the pages and the tokens' weights enter the products as two bf16 parts
-with bf16 caches, cut off at 2^-16 of each value: with fp32 outputs another 2^-15 of the scale, and bf16 outputs
-add half a step, 2^-8 of each value.  Tokens, paths and tables are equal.
+a few hundred products of fp32 values whose decays are off by a few 2^-24, rel-L2 below 1e-5.  With bf16
+caches the tokens are exact inputs, but a token's weight enters its product as two bf16 parts, off by
+2^-17 of it: with fp32 outputs another 2^-15 of the scale.  bf16 outputs add their half step, 2^-8 of each
+value, and the half step of tf32 at which the pages are read, 2^-11 of each product: the signs
+are random, so the outputs' rms is the root of the products' sum of squares, and the sum of their
+magnitudes is at most sqrt(n) of that, n < 1024 products (4 pages of 128 rows and the tokens): 32 rms.
+Tokens, paths and tables are equal.
 """
 import numpy as np
 import pytest
@@ -17,7 +20,7 @@ from tests.helpers import TOL_F32, rel_l2, to64
 from tests.test_cache_gpu import DT, i32, invariants, poison, same, snapshot
 
 pytestmark = pytest.mark.gpu
-TWO_PARTS = 2.0 ** -15
+TWO_PARTS, ONE_PART = 2.0 ** -15, 2.0 ** -11
 
 
 @pytest.fixture(scope="module")
@@ -27,14 +30,13 @@ def LL():
 
 
 def check(got, want, parts=False):
-    tol = TOL_F32 + (TWO_PARTS if parts else 0.0)
     got, want = got[~np.isnan(want)], want[~np.isnan(want)]
     if got.dtype == torch.float32:
+        tol = TOL_F32 + (TWO_PARTS if parts else 0.0)
         assert rel_l2(got, want) <= tol, rel_l2(got, want)
     else:
         rms = float(np.sqrt(np.mean(np.square(want))))
-        # two parts: each product off by 2^-15 of itself, and |sum of products| <= 16 rms of the outputs here
-        off = np.abs(to64(got) - want) - (2.0 ** -8 * np.abs(want) + (16 * tol) * rms)
+        off = np.abs(to64(got) - want) - (2.0 ** -8 * np.abs(want) + 32 * (TOL_F32 + (ONE_PART if parts else 0.0)) * rms)
         assert off.max() <= 0, off.max()
 
 
