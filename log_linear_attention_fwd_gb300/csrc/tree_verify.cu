@@ -8,13 +8,20 @@
 //     u Z_k q(x) < R_k(x)         (drafts drawn from q: then R_{k+1} = max(R_k - Z_k q, 0), Z_{k+1} = sum of it)
 // and else the next one is tried; where none is left the next token is drawn from R_k.  So the
 // tokens are distributed as the target's own.  R_k is max(P - S_k q, 0) with S_k = Z_0 + .. + Z_{k-1}, as
-// what has once reached 0 stays there: one multiply-add per value, whatever was rejected before.
+// what has once reached 0 stays there: one product per value, whatever was rejected before.
 //
-// Sums over a vocabulary are 64-bit fixed point with 52 fractional bits: exact for values of
-// 2^-28 and above, cut at 2^-52 below, and the same in every order, so the token drawn depends on
-// no launch shape (fp32 sums move the boundaries of 1e5 tokens by more than the tokens' own
-// width; fp64 adds run at 1/64 of the rate).
-#include "ll_internal.cuh"
+// Sums over a vocabulary are 64-bit fixed point with 43 fractional bits: the same in every order, so
+// the token drawn depends on no launch shape.  fp32 sums would move the boundaries between 1e5 tokens by
+// more than the tokens' own width; fp64 runs at 1/64 of fp32's rate here.
+//
+// A cluster serves a row, each warp of it a run of the vocabulary.  All CTAs walk alike, from the
+// children's values in shared memory; a pass over the vocabulary (one per rejection of a drawn draft, one at the
+// end of the walk otherwise) reads the row or two rows once and leaves a sum per warp, and the run that
+// holds the drawn token is read again.  Bound by HBM for batches: 128 rows of 131072 fp32 values and their drafts',
+// 134 MB; a single row is a chain of five latencies (tree, children's values, pass, cluster, run).
+#include <algorithm>
+
+#include "cache_common.cuh"
 
 namespace ll {
 namespace {
@@ -22,24 +29,30 @@ namespace {
 __device__ unsigned g_verify_error;
 
 constexpr int kNodes = LL_TREE_MAX;
-constexpr int kFraction = 52;
+constexpr int kFraction = 43;
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifySplit = 8;  // CTAs of a cluster
 typedef unsigned long long Mass;
+constexpr Mass kOne = 1ull << kFraction;
 
-// x as fixed point; below 0 and NaN: 0, above 1: 1.
-__device__ __forceinline__ Mass to_mass(float x) {
-  const unsigned b = __float_as_uint(__saturatef(x));
-  const Mass m = (Mass)(b & 0x7fffffu | 0x800000u) << (kFraction - 23);  // of an x in [1, 2)
-  return m >> min(127u - (b >> 23), 63u);
+// x in [0, 1] (below and NaN: 0, above: 1) as fixed point, to the nearest, plus kBias.  A sum with 8
+// has x's first 20 fractional bits as its last ones, and what is left plus 2^-20 the next 23.
+constexpr Mass kBias = ((Mass)0x41000000u << 23) + 0x35800000u;
+__device__ __forceinline__ Mass biased_mass(float x) {
+  x = __saturatef(x);
+  const float hi = __fadd_rz(x, 8.f);
+  const float lo = __fadd_rn(__fsub_rn(x, __fsub_rn(hi, 8.f)), 0x1p-20f);
+  return (Mass)__float_as_uint(hi) * (1u << 23) + __float_as_uint(lo);
 }
-// floor(s x) for x in [0, 1], s < 2^62.
+__device__ __forceinline__ Mass to_mass(float x) { return biased_mass(x) - kBias; }
+// floor(s x), x as above, for s < 2^62.
 __device__ __forceinline__ Mass mass_times(Mass s, float x) {
-  const unsigned b = __float_as_uint(__saturatef(x)), m = b & 0x7fffffu | 0x800000u;
+  const unsigned b = __float_as_uint(__saturatef(x)), m = (b & 0x7fffffu) | 0x800000u;
   const Mass lo = (s & 0xffffffffu) * m, hi = (s >> 32) * m + (lo >> 32);  // s m = hi 2^32 + low word of lo
-  // s m 2^-23 2^-(127 - exponent)
-  const unsigned shift = 127u - (b >> 23);
-  const Mass x23 = hi << 9 | (lo & 0xffffffffu) >> 23;
-  return x23 >> min(shift, 63u);
+  const Mass y = hi << 9 | (lo & 0xffffffffu) >> 23;                        // s times the significand
+  return y >> min(127u - (b >> 23), 63u);
 }
+__device__ __forceinline__ Mass less(Mass p, Mass q) { return p > q ? p - q : 0; }
 
 struct VerifyArgs {
   const int* parents;
@@ -50,146 +63,284 @@ struct VerifyArgs {
   int* path;
   int* count;
   int* token;
-  int n, N;
+  int N, split;
   int64_t V;
 };
 
-constexpr int kVerifyThreads = 512;
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t x = (&w.x)[sizeof(T) == 2 ? i >> 1 : i];
+    return __uint_as_float(sizeof(T) == 4 ? x : i & 1 ? x & 0xffff0000u : x << 16);
+  }
+};
 
-__device__ Mass block_sum(Mass x, Mass* part) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
-  __syncthreads();
-  Mass t = 0;
-  for (int i = 0; i < kVerifyThreads / 32; ++i) t += part[i];
-  return t;
+// What is drawn from: P alone (kPlain), max(P - Q, 0) (kFirst) or max(P - S Q, 0) (kMore).
+enum Kind { kPlain, kFirst, kMore };
+template <int kKind>
+__device__ __forceinline__ Mass rest_of(float p, float q, Mass S) {
+  if (kKind == kPlain) return to_mass(p);
+  if (kKind == kFirst) return less(biased_mass(p), biased_mass(q));
+  return less(to_mass(p), mass_times(S, q));
 }
 
-// One CTA per row.
+// The calling warp's sum over [lo, hi) of a row.  vec: the two rows lie alike to 16 bytes, `off` elements behind one.
+template <typename T, int kKind>
+__device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int64_t hi, bool vec, int off, Mass S) {
+  constexpr int n = Vec<T>::n, kFlight = 4;
+  const int lane = threadIdx.x & 31;
+  int64_t a = hi, b = hi;  // whole vectors: [a, b)
+  if (vec) {
+    a = min(hi, ((lo + off + n - 1) & ~(int64_t)(n - 1)) - off);
+    b = max(a, ((hi + off) & ~(int64_t)(n - 1)) - off);
+  }
+  Mass sum = 0;
+  auto one = [&](int64_t x) { sum += rest_of<kKind>(to_f32(P[x]), kKind == kPlain ? 0.f : to_f32(Q[x]), S); };
+#pragma unroll 1
+  for (int64_t x = lo + lane; x < a; x += 32) one(x);
+#pragma unroll 1
+  for (int64_t x = b + lane; x < hi; x += 32) one(x);
+#pragma unroll 1
+  for (int64_t x0 = a + lane * n; x0 < b; x0 += 32 * n * kFlight) {
+    Vec<T> p[kFlight], q[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int64_t x = x0 + u * 32 * n;
+      p[u].w = q[u].w = make_uint4(0u, 0u, 0u, 0u);
+      if (x < b) {
+        p[u].w = __ldg(reinterpret_cast<const uint4*>(P + x));
+        if (kKind != kPlain) q[u].w = __ldg(reinterpret_cast<const uint4*>(Q + x));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+#pragma unroll
+      for (int i = 0; i < n; ++i) sum += rest_of<kKind>(p[u].at(i), kKind == kPlain ? 0.f : q[u].at(i), S);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
+}
+
+struct VerifySmem {
+  int up[kNodes], tok[kNodes];
+  float px[kNodes], qx[kNodes], us[kNodes];
+  Mass warp_sum[kVerifyWarps], scan[kVerifyWarps];
+  Mass cta_sum[2][kVerifySplit];  // of the cluster's CTAs, by turns
+};
+
+__device__ __forceinline__ void store_remote(Mass* p, uint32_t rank, Mass v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+
+// grid: row, CTA of its cluster (fastest).
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) tree_verify_kernel(VerifyArgs a) {
-  __shared__ int up[kNodes], tok[kNodes];
-  __shared__ float px[kNodes], qx[kNodes], us[kNodes];
-  __shared__ Mass part[kVerifyThreads / 32];
-  __shared__ unsigned bad_s;
-  __shared__ int hit;
-  const int tid = threadIdx.x, N = a.N, row = blockIdx.x;
-  const int64_t V = a.V;
-  if (tid == 0) {
-    bad_s = 0;
-    hit = kNodes;
+__global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyArgs a) {
+  __shared__ VerifySmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, N = a.N;
+  const int C = a.split, rank = blockIdx.x % C;
+  const int64_t V = a.V, row = blockIdx.x / C;
+  const T* P0 = static_cast<const T*>(a.probs) + row * N * V;
+  const T* Q0 = a.draft ? static_cast<const T*>(a.draft) + row * N * V : nullptr;
+  if (C > 1) cluster_arrive();  // this CTA is there
+  bool bad = false;
+  if (tid < kNodes) {
+    int up = -2, x = 0;
+    if (tid < N) {
+      up = a.parents[row * N + tid];
+      x = a.tokens[row * N + tid];
+      sm.us[tid] = fminf(fmaxf(a.u[row * N + tid], 0.f), 0x1.fffffep-1f);
+    }
+    const bool child = up >= 0 && up < tid;
+    bad = child ? x < 0 || x >= V : up != -1 && up != -2;
+    if (bad) up = -2;
+    sm.up[tid] = up;
+    sm.tok[tid] = x;
+    if (up >= 0) {
+      sm.px[tid] = to_f32(P0[up * V + x]);
+      if (Q0) sm.qx[tid] = to_f32(Q0[up * V + x]);
+    }
   }
   __syncthreads();
-  const T* P0 = static_cast<const T*>(a.probs) + (int64_t)row * N * V;
-  const T* Q0 = a.draft ? static_cast<const T*>(a.draft) + (int64_t)row * N * V : nullptr;
-  if (tid < N) {
-    const int p = a.parents[(int64_t)row * N + tid], x = a.tokens[(int64_t)row * N + tid];
-    const bool child = p >= 0 && p < tid;
-    const bool fine = child ? x >= 0 && x < V : p == -1 || p == -2;
-    if (!fine) bad_s = 1;
-    up[tid] = child && fine ? p : p == -1 ? -1 : -2;
-    tok[tid] = x;
-    px[tid] = child && fine ? to_f32(P0[p * V + x]) : 0.f;
-    qx[tid] = child && fine && Q0 ? to_f32(Q0[p * V + x]) : 0.f;
-    us[tid] = fminf(fmaxf(a.u[(int64_t)row * N + tid], 0.f), 0x1.fffffep-1f);
-  }
-  __syncthreads();
-  if (tid < N && up[tid] >= 0 && up[up[tid]] == -2) bad_s = 1;
-  __syncthreads();
-  int* path = a.path + (int64_t)row * N;
-  for (int i = tid; i < N; i += kVerifyThreads) path[i] = -1;
-  if (bad_s || up[0] != -1) {
-    if (tid == 0) {
-      if (bad_s) atomicOr(&g_verify_error, 1u << 5);
+  if (tid < kNodes && sm.up[tid] >= 0) bad |= sm.up[sm.up[tid]] == -2;
+  bad = __syncthreads_or(bad);
+  int* path = a.path + row * N;
+  if (rank == 0 && tid == 0) a.token[row] = -1;  // (the clusters' barriers order it before the token itself)
+  if (bad || sm.up[0] != -1) {
+    if (rank == 0 && tid < N) path[tid] = -1;
+    if (rank == 0 && tid == 0) {
+      if (bad) atomicOr(&g_verify_error, 1u << 5);
       a.count[row] = 0;
-      a.token[row] = -1;
     }
     return;
   }
-  __syncthreads();
-  int cur = 0, count = 1;
-  if (tid == 0) path[0] = 0;
-  const Mass one = 1ull << kFraction;
-  Mass S = 0, Z = one;
-  unsigned long long gone = 0;  // rejected children (drafts that were given)
-  for (int i = 1; i < N; ++i) {
-    if (up[i] != cur) continue;
-    bool ok;
-    const double z = (double)Z * 0x1p-52 * (double)us[i];
-    if (!Q0) {
-      bool left = true;
-      for (int x = cur + 1; x < i; ++x) left &= !(gone >> x & 1) || tok[x] != tok[i];
-      const Mass R = left ? to_mass(px[i]) : 0;
-      ok = z < (double)R * 0x1p-52;
-      if (!ok) {
-        Z -= R < Z ? R : Z;
-        gone |= 1ull << i;
-      }
-    } else {
-      const Mass p = to_mass(px[i]), q = mass_times(S, qx[i]);
-      ok = z * (double)__saturatef(qx[i]) < (double)(p > q ? p - q : 0) * 0x1p-52;
-      if (!ok) {
-        S += Z;
-        Mass sum = 0;
-        for (int64_t x = tid; x < V; x += kVerifyThreads) {
-          const Mass p1 = to_mass(to_f32(P0[cur * V + x])), q1 = mass_times(S, to_f32(Q0[cur * V + x]));
-          sum += p1 > q1 ? p1 - q1 : 0;
-        }
-        Z = block_sum(sum, part);
-      }
-    }
-    if (ok) {
-      cur = i;
-      S = 0;
-      Z = one;
-      gone = 0;
-      if (tid == 0) path[count] = i;
-      ++count;
-    }
-  }
-  // the next token: the first index whose running sum passes u_0 of the whole
-  auto mass_of = [&](int64_t x, bool full) -> Mass {
-    const Mass p = to_mass(to_f32(P0[cur * V + x]));
-    if (full) return p;
-    if (Q0) {
-      const Mass q = S ? mass_times(S, to_f32(Q0[cur * V + x])) : 0;
-      return p > q ? p - q : 0;
-    }
-    for (unsigned long long g = gone; g; g &= g - 1)
-      if (tok[__ffsll(g) - 1] == x) return 0;
-    return p;
+
+  // this warp's run of the vocabulary
+  int cur = 0;
+  const int64_t runs = (int64_t)C * kVerifyWarps, len = ((V + runs - 1) / runs + 7) & ~(int64_t)7;
+  auto run_at = [&](int64_t k, int off) { return k <= 0 ? 0 : k >= runs ? V : min(V, k * len - off); };
+  int passes = 0;
+  Mass total = 0, before = 0;  // of the last pass: of all, and of the CTAs before this one
+  unsigned long long gone = 0;  // rejected children (drafts that were given), one per token
+  bool waited = C == 1;
+  auto place = [&](const T* P, const T* Q, int* off) {  // how the rows lie
+    constexpr int n = Vec<T>::n;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(P), q = Q ? reinterpret_cast<uintptr_t>(Q) : p;
+    *off = (int)(p / sizeof(T)) & (n - 1);
+    return ((p ^ q) & 15u) == 0;
   };
-  const int64_t share = (V + kVerifyThreads - 1) / kVerifyThreads, lo = min(V, tid * share), hi = min(V, lo + share);
-  for (int full = 0; full < 2; ++full) {
-    Mass sum = 0;
-    for (int64_t x = lo; x < hi; ++x) sum += mass_of(x, full);
-    const Mass total = block_sum(sum, part);
-    if (total == 0) continue;  // nothing is left: from the target's row itself
-    Mass before = sum;  // over the threads before this one
+  auto pass = [&](Mass S, bool plain) {
+    const T* P = P0 + cur * V;
+    const T* Q = plain || !Q0 || S == 0 ? nullptr : Q0 + cur * V;
+    int off;
+    const bool vec = place(P, Q, &off);
+    const int64_t k = (int64_t)rank * kVerifyWarps + w, lo = run_at(k, off), hi = run_at(k + 1, off);
+    Mass sum = !Q          ? sum_run<T, kPlain>(P, Q, lo, hi, vec, off, S)
+               : S == kOne ? sum_run<T, kFirst>(P, Q, lo, hi, vec, off, S)
+                           : sum_run<T, kMore>(P, Q, lo, hi, vec, off, S);
+    if (!plain)
+      for (unsigned long long g = gone; g; g &= g - 1) {
+        const int i = __ffsll(g) - 1;
+        if (sm.tok[i] >= lo && sm.tok[i] < hi) sum -= to_mass(sm.px[i]);
+      }
+    if (lane == 0) sm.warp_sum[w] = sum;
+    __syncthreads();
+    Mass mine = 0;
+    for (int i = 0; i < kVerifyWarps; ++i) mine += sm.warp_sum[i];
+    total = mine;
+    before = 0;
+    if (C > 1) {
+      if (!waited) cluster_wait();  // all CTAs are there
+      waited = true;
+      Mass* slot = sm.cta_sum[passes & 1];
+      if (tid < C) store_remote(slot + rank, tid, mine);
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      total = 0;
+      for (int i = 0; i < C; ++i) {
+        if (i < rank) before += slot[i];
+        total += slot[i];
+      }
+    }
+    ++passes;
+  };
+
+  int count = 1, passed = -1;  // passed: the node of the last pass, with the present S
+  if (rank == 0 && tid == 0) path[0] = 0;
+  Mass S = 0, Z = kOne;
+  const int up0 = sm.up[lane], up1 = sm.up[lane + 32];
+  for (;;) {
+    unsigned long long kids = __ballot_sync(0xffffffffu, up0 == cur) |
+                              (unsigned long long)__ballot_sync(0xffffffffu, up1 == cur) << 32;
+    bool moved = false;
+    for (; kids && !moved; kids &= kids - 1) {
+      const int i = __ffsll(kids) - 1;
+      const float p = sm.px[i], u = sm.us[i];
+      bool ok;
+      if (!Q0) {
+        bool left = true;
+        for (unsigned long long g = gone; g; g &= g - 1) left &= sm.tok[__ffsll(g) - 1] != sm.tok[i];
+        const Mass R = left ? to_mass(p) : 0;
+        ok = mass_times(Z, u) < R;
+        if (!ok && left) {
+          Z = less(Z, R);
+          gone |= 1ull << i;
+        }
+      } else {
+        const float q = __saturatef(sm.qx[i]);
+        if (S == 0) {  // exactly: the product's rounding error decides where it is p
+          const float t = u * q, e = fmaf(u, q, -t), sp = __saturatef(p);
+          ok = t < sp || (t == sp && e < 0.f);
+        } else {
+          const Mass R = S == kOne ? less(biased_mass(p), biased_mass(q)) : less(to_mass(p), mass_times(S, q));
+          ok = mass_times(mass_times(Z, q), u) < R;
+        }
+        if (!ok) {
+          S += Z;
+          pass(S, false);
+          Z = total;
+          passed = cur;
+        }
+      }
+      if (ok) {
+        cur = i;
+        S = 0;
+        Z = kOne;
+        gone = 0;
+        passed = -1;
+        if (rank == 0 && tid == 0) path[count] = i;
+        ++count;
+        moved = true;
+      }
+    }
+    if (!moved) break;
+  }
+  if (rank == 0) {
+    if (tid >= count && tid < N) path[tid] = -1;
+    if (tid == 0) a.count[row] = count;
+  }
+
+  // the next token: the first index whose running sum passes u_0 of the whole
+  bool plain = false;
+  if (passed != cur) pass(S, false);
+  if (total == 0) {  // nothing is left: from the target's row itself
+    plain = true;
+    pass(0, true);
+  }
+  if (total == 0) return;
+  Mass target = min(mass_times(total, sm.us[0]), total - 1);
+  Mass mine = 0;
+  for (int i = 0; i < kVerifyWarps; ++i) mine += sm.warp_sum[i];
+  if (target < before || target - before >= mine) return;  // another CTA's
+  target -= before;
+  int run = 0;
+  while (target >= sm.warp_sum[run]) target -= sm.warp_sum[run++];  // (ends: target is below their sum)
+  const T* P = P0 + cur * V;
+  const T* Q = plain || !Q0 || S == 0 ? nullptr : Q0 + cur * V;
+  int off;
+  place(P, Q, &off);
+  const int64_t k = (int64_t)rank * kVerifyWarps + run, lo = run_at(k, off), hi = run_at(k + 1, off);
+  const int64_t each = (hi - lo + kVerifyThreads - 1) / kVerifyThreads;
+  const int64_t from = min(hi, lo + tid * each), to = min(hi, from + each);
+  auto mass_at = [&](int64_t x) -> Mass {
+    const float p = to_f32(P[x]);
+    if (Q) return S == kOne ? rest_of<kFirst>(p, to_f32(Q[x]), S) : rest_of<kMore>(p, to_f32(Q[x]), S);
+    if (!plain)
+      for (unsigned long long g = gone; g; g &= g - 1)
+        if (sm.tok[__ffsll(g) - 1] == x) return 0;
+    return to_mass(p);
+  };
+  Mass sum = 0;
+#pragma unroll 4
+  for (int64_t x = from; x < to; ++x) sum += mass_at(x);
+  Mass upto = sum;  // over the threads up to this one
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const Mass y = __shfl_up_sync(0xffffffffu, before, d);
-      if ((tid & 31) >= d) before += y;
-    }
-    before -= sum;
-    for (int i = 0; i < tid >> 5; ++i) before += part[i];
-    const Mass target = mass_times(total, us[0]);
-    if (before <= target && target < before + sum) {
-      int64_t x = lo;
-      for (Mass cum = before; x < hi; ++x)
-        if ((cum += mass_of(x, full)) > target) break;
-      a.token[row] = (int)x;
-      hit = 1;
-    }
-    break;
+  for (int d = 1; d < 32; d <<= 1) {
+    const Mass y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
   }
+  if (lane == 31) sm.scan[w] = upto;
   __syncthreads();
-  if (tid == 0) {
-    a.count[row] = count;
-    if (hit != 1) a.token[row] = -1;
+  for (int i = 0; i < w; ++i) upto += sm.scan[i];
+  if (upto - sum <= target && target < upto) {
+    Mass cum = upto - sum;
+    int64_t x = from;
+    while (x < to - 1 && (cum += mass_at(x)) <= target) ++x;
+    a.token[row] = (int)x;
   }
+}
+
+template <typename T>
+cudaError_t launch(VerifyArgs a, int n, cudaStream_t s) {
+  // CTAs per row: doubled while all of them run at once (four to an SM) and each has 2048 values
+  a.split = 1;
+  while (a.split < kVerifySplit && (int64_t)n * a.split * 2 <= 4 * sm_count() && a.V >= (int64_t)4096 * a.split) a.split *= 2;
+  return launch_following(false, tree_verify_kernel<T>, dim3((unsigned)n * a.split), kVerifyThreads, 0, a.split, s, a);
 }
 
 }  // namespace
@@ -199,10 +350,8 @@ cudaError_t launch_tree_verify(const int* parents, const int* tokens, const void
                                int dtype, cudaStream_t s) {
   VerifyArgs a;
   a.parents = parents; a.tokens = tokens; a.probs = probs; a.draft = draft; a.u = u; a.path = path;
-  a.count = count; a.token = token; a.n = n; a.N = N; a.V = V;
-  if (dtype == LL_F32) tree_verify_kernel<float><<<n, kVerifyThreads, 0, s>>>(a);
-  else tree_verify_kernel<__nv_bfloat16><<<n, kVerifyThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  a.count = count; a.token = token; a.N = N; a.V = V; a.split = 1;
+  return dtype == LL_F32 ? launch<float>(a, n, s) : launch<__nv_bfloat16>(a, n, s);
 }
 
 cudaError_t verify_take_error(cudaStream_t s, unsigned* flags) {
