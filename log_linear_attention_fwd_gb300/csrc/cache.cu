@@ -466,22 +466,7 @@ __device__ __forceinline__ void fold_tokens(const __nv_bfloat16* wks, const __nv
   const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
   for (int nt = w; nt < dv / 8; nt += kStepWarps) {
     uint32_t b[kW / 16][3][2];
-#pragma unroll
-    for (int ks = 0; ks < kW / 16; ks += 2) {
-      uint32_t r[4];  // tokens 16 ks .. + 31 of 8 columns
-      ldmatrix_trans(r, wvs + (16 * ks + lane) * vp + 8 * nt);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int s = 16 * ks + 8 * u + i;
-        float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[u]));
-        const float2 e = *reinterpret_cast<const float2*>(tok + s);
-        x = make_float2(fabsf(x.x * e.x), fabsf(x.y * e.y));
-        const float2 least = make_float2(fminf(x.x, 0x1p-133f), fminf(x.y, 0x1p-133f));
-        const uint32_t sign = r[u] & 0x80008000u;
-#pragma unroll
-        for (int v = 0; v < 3; ++v) b[ks + (u >> 1)][v][u & 1] = take_bf16(x, least) | sign;
-      }
-    }
+    load_decayed(b, wvs + 8 * nt, tok, vp);
     for (int d = k0; d < k1; d += 16) {
       float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1148,7 +1133,7 @@ int step_split(int64_t rows_heads, int dk, int sms) {
 }  // namespace
 
 size_t cache_scratch_bytes(int64_t slots, int64_t n_pages) {
-  return sizeof(int) * (size_t)(slots + 3 * n_pages + 1);
+  return sizeof(int) * (size_t)(2 * slots + 3 * n_pages + 1);
 }
 
 cudaError_t launch_cache_reserve(const ll_cache& c, const int* slots, const int* pos, int64_t n,

@@ -62,7 +62,10 @@ __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, A
     const int count = tid < a.n ? count_s[tid] : 0;
     const unsigned why = named ? accept_bad(c, s, pos, count) : 0;
     if (why) raise(c, why);
-    if (named) sc.owner[s] = why ? ~tid : tid;
+    if (named) {
+      sc.owner[s] = why ? ~tid : tid;
+      sc.done[s] = 0;
+    }
     __syncthreads();
     slot_s[tid] = named && !why ? s : -1;
     block_s[tid] = pos >> kLogW;
@@ -80,6 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, A
     const unsigned why = accept_bad(c, s, a.pos[r], path_length(a, r));
     if (why) raise(c, why);
     if (why) sc.owner[s] = ~(int)r;
+    sc.done[s] = 0;
   }
   __syncthreads();
   settle_pages(c, a.n, [&](int64_t r) { return owns(c, sc.owner, a.slots[r], r) ? a.slots[r] : -1; },
@@ -87,110 +91,228 @@ __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, A
                [&](int64_t r) { return (a.pos[r] & (kW - 1)) + path_length(a, r) >= kW; });
 }
 
-constexpr int kAcceptThreads = 256;
+constexpr int kAcceptThreads = 256, kAcceptWarps = kAcceptThreads / 32;
+constexpr int kPad = 8;  // elements that set a token's row off by 16 bytes
 
-// A row's fold, as far as its CTAs have to agree on it.
-struct Fold {
-  int dest;      // the page, -1 without a fold
-  unsigned why;  // the row cannot be served
-};
-__device__ __forceinline__ Fold fold_of(const ll_cache& c, int s, int pos, int count) {
-  Fold f = {-1, 0};
-  const int j = pos >> kLogW, M = (int)c.levels, to = __ffs(j + 1) - 1;
-  if ((pos & (kW - 1)) + count < kW) return f;
-  for (int m = 0; m < M; ++m) {
-    if (m != to && !(j >> m & 1)) continue;
-    const int e = c.page_table[(int64_t)s * M + m];
-    if (e < 0 || e >= c.n_pages || (m == to && c.refcount[e] != 1)) f.why = LL_CACHE_ERR_MISSING;
-    else if (m == to) f.dest = e;
-  }
-  return f;
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
 
-// One CTA per (row, head): the block that ends with the path, folded.
-template <typename T>
-__global__ void __launch_bounds__(kAcceptThreads) accept_fold_kernel(ll_cache c, AcceptArgs a) {
-  __shared__ float tok[kW], since_s;
-  const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv, M = (int)c.levels;
-  const int tid = threadIdx.x, row = blockIdx.x / H, h = blockIdx.x - row * H, s = a.slots[row], pos = a.pos[row];
+// Rows of `width` elements from src_of(row) to dst_of(row), by the CTA; whole 16-byte pieces (vec) or elements.
+template <typename T, typename Src, typename Dst>
+__device__ __forceinline__ void copy_tokens(int rows, int width, bool vec, Src src_of, Dst dst_of) {
+  constexpr int per = 16 / sizeof(T), kLanes = 128 / per;  // pieces of 128 columns
+  if (vec) {
+    const int x = (threadIdx.x & (kLanes - 1)) * per;
+    if (x < width)
+      for (int r = threadIdx.x / kLanes; r < rows; r += kAcceptThreads / kLanes)
+        *reinterpret_cast<uint4*>(dst_of(r) + x) = *reinterpret_cast<const uint4*>(src_of(r) + x);
+  } else {
+    const int x = threadIdx.x & 127;
+    if (x < width)
+      for (int r = threadIdx.x >> 7; r < rows; r += kAcceptThreads >> 7) dst_of(r)[x] = src_of(r)[x];
+  }
+}
+
+// One CTA per (row, head): the path's tokens to their places and, where they end the block, its fold: the sum
+// of the pages below the level that it goes to, decayed, and of the 64 tokens' products.  kMma: bf16 tokens of whole
+// 16-byte pieces, whose products run on the tensor cores, exact keys against decayed values in three bf16
+// parts, as in the step; else fp32 multiply-adds.  The pages go from HBM to the fragments and the new
+// page from there.  Tokens of the next block replace those that the fold reads: a head's own
+// values behind its own reads, the keys that heads share by the row's last CTA to have read them.
+template <typename T, bool kMma>
+__global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll_cache c, AcceptArgs a) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ __align__(8) float tok[kW];
+  __shared__ float page_e[kMaxLevels];
+  __shared__ int page_at[kMaxLevels], path[LL_TREE_MAX];
+  __shared__ int count_s, last_s;
+  __shared__ unsigned why_s;
+  const int H = (int)c.H, Hqk = (int)c.Hqk, G = H / Hqk, dk = (int)c.dk, dv = (int)c.dv, M = (int)c.levels;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int row = blockIdx.x / H, h = blockIdx.x - row * H, hq = h / G;
   wait_for_previous();
-  if (!owns(c, scratch_of(c).owner, s, row)) return;
-  const int count = path_length(a, row), j = pos >> kLogW, r = pos & (kW - 1), par = j & 1, to = __ffs(j + 1) - 1;
-  const Fold f = fold_of(c, s, pos, count);
-  if (f.why && tid == 0 && h == 0) raise(c, f.why);
-  if (f.why || f.dest < 0) return;
-  const int* path = a.path + (int64_t)row * a.D;
-  if (tid < 32) {
-    auto la = [&](int i) {
-      if (i < r) return c.win_log_a[((int64_t)s * H + h) * kW + i];
-      return a.log_a ? a.log_a[((int64_t)row * a.N + path[i - r]) * H + h] : 0.f;
-    };
-    float since;
-    block_decays(la(tid), la(tid + 32), kW, c.page_from[s * 2 + par], tok, &since);
-    tok[tid] = expf(tok[tid]);
-    tok[tid + 32] = expf(tok[tid + 32]);
-    since_s = since;
+  const int s = a.slots[row], pos = a.pos[row];
+  const Scratch sc = scratch_of(c);
+  if (!owns(c, sc.owner, s, row)) return;
+  const int j = pos >> kLogW, r = pos & (kW - 1), par = j & 1, to = __ffs(j + 1) - 1;
+  if (w == 0) {
+    const int x = lane < a.D ? a.path[(int64_t)row * a.D + lane] : -1, y = lane + 32 < a.D ? a.path[(int64_t)row * a.D + lane + 32] : -1;
+    path[lane] = x;
+    path[lane + 32] = y;
+    const unsigned x_end = __ballot_sync(0xffffffffu, x < 0), y_end = __ballot_sync(0xffffffffu, y < 0);
+    if (lane == 0) count_s = x_end ? __ffs(x_end) - 1 : y_end ? 31 + __ffs(y_end) : 64;
+  } else if (w == 1) {  // the fold's pages, in case
+    const bool here = lane < M && (lane == to || (j >> lane & 1));
+    const int e = here ? c.page_table[(int64_t)s * M + lane] : 0;
+    const bool gone = here && (e < 0 || e >= c.n_pages || (lane == to && c.refcount[e] != 1));
+    if (lane < M) page_at[lane] = e;
+    const bool why = __any_sync(0xffffffffu, gone);
+    if (lane == 0) why_s = why ? LL_CACHE_ERR_MISSING : 0;
   }
   __syncthreads();
-  const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * c.Hqk + h / G) * kW * dk;
-  const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
-  const T* gk = static_cast<const T*>(a.k) + row * a.sk[0] + (h / G) * a.sk[2];
-  const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
-  float* D = c.pages + ((int64_t)f.dest * H + h) * dk * dv;
-  for (int x = tid; x < dk * dv; x += kAcceptThreads) {
-    const int d = x / dv, e = x - d * dv;
-    float sum = 0.f;
-    for (int m = 0; m < to; ++m) {
-      const float w = expf(c.page_log[(((int64_t)s * 2 + par) * M + m) * H + h] + since_s);
-      sum = fmaf(w, c.pages[((int64_t)c.page_table[(int64_t)s * M + m] * H + h) * dk * dv + x], sum);
-    }
-    for (int i = 0; i < kW; ++i) {
-      const float key = to_f32(i < r ? wk[i * dk + d] : gk[path[i - r] * a.sk[1] + d]);
-      sum = fmaf(tok[i] * key, to_f32(i < r ? wv[i * dv + e] : gv[path[i - r] * a.sv[1] + e]), sum);
-    }
-    D[x] = sum;
+  const int count = count_s;
+  const bool fold = r + count >= kW;
+  if (fold && why_s) {
+    if (tid == 0 && h == 0) raise(c, why_s);
+    return;
   }
-  // what the next block's calls read
-  for (int m = tid; m < M; m += kAcceptThreads)
-    if (m == to) c.page_log[(((int64_t)s * 2 + 1 - par) * M + m) * H + h] = 0.f;
-    else if (m > to && (j >> m & 1))
-      c.page_log[(((int64_t)s * 2 + 1 - par) * M + m) * H + h] = c.page_log[(((int64_t)s * 2 + par) * M + m) * H + h] + since_s;
-  if (h == 0 && tid == 0) c.page_from[s * 2 + 1 - par] = 0;
+  const T* gk = static_cast<const T*>(a.k) + row * a.sk[0] + hq * a.sk[2];
+  const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
+  const float* ga = a.log_a ? a.log_a + (int64_t)row * a.N * H + h : nullptr;
+  T* wk = static_cast<T*>(c.win_k) + ((int64_t)s * Hqk + hq) * kW * dk;
+  T* wv = static_cast<T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
+  float* wa = c.win_log_a + ((int64_t)s * H + h) * kW;
+  const bool k_vec = ((dk | a.sk[0] | a.sk[1] | a.sk[2]) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.k) & 15u) == 0;
+  const bool v_vec = ((dv | a.sv[0] | a.sv[1] | a.sv[2]) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.v) & 15u) == 0;
+  const int ends = min(count, kW - r);  // tokens in this block
+  if (fold) {
+    // the 64 tokens, of the block and of the path
+    auto key = [&](int i) { return i < r ? wk + i * dk : gk + path[i - r] * a.sk[1]; };
+    auto value = [&](int i) { return i < r ? wv + i * dv : gv + path[i - r] * a.sv[1]; };
+    const int kp = kMma ? dk + kPad : (dk + 3) & ~3, vp = kMma ? dv + kPad : dv;
+    __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(dyn);
+    __nv_bfloat16* vs = ks + kW * kp;
+    float* kf = reinterpret_cast<float*>(dyn);
+    float* vf = kf + kW * kp;
+    if constexpr (kMma) {
+      const int x = (tid & 15) * 8;
+      for (int i = tid >> 4; i < kW; i += kAcceptThreads / 16) {
+        if (x < dk) cp_async16(ks + i * kp + x, key(i) + x);
+        if (x < dv) cp_async16(vs + i * vp + x, value(i) + x);
+      }
+    } else {
+      const int x = tid & 127;
+#pragma unroll 4
+      for (int i = tid >> 7; i < kW; i += kAcceptThreads >> 7) {
+        if (x < kp) kf[i * kp + x] = x < dk ? to_f32(key(i)[x]) : 0.f;
+        if (x < dv) vf[i * vp + x] = to_f32(value(i)[x]);
+      }
+    }
+    if (w == 0) {
+      auto la = [&](int i) { return i < r ? wa[i] : ga ? ga[(int64_t)path[i - r] * H] : 0.f; };
+      float since;
+      block_decays(la(lane), la(lane + 32), kW, c.page_from[s * 2 + par], tok, &since);
+      tok[lane] = expf(tok[lane]);
+      tok[lane + 32] = expf(tok[lane + 32]);
+      const bool here = lane < M && (j >> lane & 1);
+      float* log = c.page_log + ((int64_t)s * 2 * M + lane) * H + h;
+      const float old = here ? log[(int64_t)par * M * H] + since : 0.f;
+      if (here && lane < to) page_e[lane] = expf(old);
+      // what the next block's calls read
+      if (lane < M && (lane == to || (here && lane > to))) log[(int64_t)(1 - par) * M * H] = lane == to ? 0.f : old;
+      if (h == 0 && lane == 0) c.page_from[s * 2 + 1 - par] = 0;
+    }
+    if constexpr (kMma) tc::cp_async_wait_all();
+    __syncthreads();
+    const int64_t size = (int64_t)dk * dv;
+    float* D = c.pages + ((int64_t)page_at[to] * H + h) * size;
+    auto page = [&](int m) { return c.pages + ((int64_t)page_at[m] * H + h) * size; };
+    if constexpr (kMma) {
+      const int g = lane >> 2, i = 2 * (lane & 3);
+      const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
+      for (int nt = w; nt < dv / 8; nt += kAcceptWarps) {
+        uint32_t b[kW / 16][3][2];
+        load_decayed(b, vs + 8 * nt, tok, vp);
+        // two row tiles at a time: their pages' values are on the way while the products run
+        for (int d = 0; d < dk; d += 32) {
+          const int64_t at = (int64_t)(d + g) * dv + 8 * nt + i;
+          float2 x[4];  // rows g, g + 8, g + 16, g + 24
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] = make_float2(0.f, 0.f);
+          for (int m = 0; m < to; ++m) {
+            const float e = page_e[m];
+            const float* P = page(m) + at;
+            float2 y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = d + 8 * u < dk ? __ldcs(reinterpret_cast<const float2*>(P + 8 * u * dv)) : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = make_float2(fmaf(e, y[u].x, x[u].x), fmaf(e, y[u].y, x[u].y));
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (d + 16 * z >= dk) continue;
+            float f[4] = {x[2 * z].x, x[2 * z].y, x[2 * z + 1].x, x[2 * z + 1].y};
+#pragma unroll
+            for (int q = 0; q < kW / 16; ++q) {
+              uint32_t ka[4];
+              ldmatrix_trans(ka, ks + (16 * q + mrow) * kp + d + 16 * z + mcol);
+#pragma unroll
+              for (int v = 2; v >= 0; --v) mma_bf16(f, ka, b[q][v][0], b[q][v][1]);
+            }
+            *reinterpret_cast<float2*>(D + at + 16 * z * dv) = make_float2(f[0], f[1]);
+            *reinterpret_cast<float2*>(D + at + (16 * z + 8) * dv) = make_float2(f[2], f[3]);
+          }
+        }
+      }
+    } else {  // four rows of four columns per thread and pass
+      const int groups = dv / 4, lanes = kAcceptThreads / groups, col = 4 * (tid % groups);
+      for (int d = 4 * (tid / groups); tid / groups < lanes && d < dk; d += 4 * lanes) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int m = 0; m < to; ++m)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (d + u < dk) x[u] = fma4(page_e[m], *reinterpret_cast<const float4*>(page(m) + (int64_t)(d + u) * dv + col), x[u]);
+        for (int i = 0; i < kW; ++i) {
+          const float4 v4 = *reinterpret_cast<const float4*>(vf + i * vp + col);
+          const float4 k4 = *reinterpret_cast<const float4*>(kf + i * kp + d);
+          const float e = tok[i];
+          x[0] = fma4(e * k4.x, v4, x[0]);
+          x[1] = fma4(e * k4.y, v4, x[1]);
+          x[2] = fma4(e * k4.z, v4, x[2]);
+          x[3] = fma4(e * k4.w, v4, x[3]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (d + u < dk) *reinterpret_cast<float4*>(D + (int64_t)(d + u) * dv + col) = x[u];
+      }
+    }
+  }
+  // the tokens to their places: first those of this block, which no fold reads there
+  if (h % G == 0)
+    copy_tokens<T>(ends, dk, k_vec, [&](int d) { return gk + path[d] * a.sk[1]; }, [&](int d) { return wk + (r + d) * dk; });
+  copy_tokens<T>(count, dv, v_vec, [&](int d) { return gv + path[d] * a.sv[1]; },
+                 [&](int d) { return wv + ((r + d) & (kW - 1)) * dv; });
+  for (int d = tid; d < count; d += kAcceptThreads) wa[(r + d) & (kW - 1)] = ga ? ga[(int64_t)path[d] * H] : 0.f;
+  if (h == 0 && tid == 0) a.new_pos[row] = pos + count;
+  if (count == ends) return;
+  // then the keys of the next block, by the row's last CTA to have read this one's
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    last_s = atomicAdd(sc.done + s, 1) == H - 1;
+  }
+  __syncthreads();
+  if (!last_s) return;
+  T* all_k = static_cast<T*>(c.win_k) + (int64_t)s * Hqk * kW * dk;
+  const T* all_g = static_cast<const T*>(a.k) + row * a.sk[0];
+  for (int q = 0; q < Hqk; ++q)
+    copy_tokens<T>(count - ends, dk, k_vec, [&](int d) { return all_g + q * a.sk[2] + path[ends + d] * a.sk[1]; },
+                   [&](int d) { return all_k + ((int64_t)q * kW + d) * dk; });
 }
 
-// One CTA per (row, head): the path's tokens to their places.
-template <typename T>
-__global__ void __launch_bounds__(kAcceptThreads) accept_tokens_kernel(ll_cache c, AcceptArgs a) {
-  const int H = (int)c.H, G = (int)(c.H / c.Hqk), dk = (int)c.dk, dv = (int)c.dv;
-  const int tid = threadIdx.x, row = blockIdx.x / H, h = blockIdx.x - row * H, s = a.slots[row], pos = a.pos[row];
-  if (!owns(c, scratch_of(c).owner, s, row)) return;
-  const int count = path_length(a, row);
-  if (fold_of(c, s, pos, count).why) return;
-  const T* gk = static_cast<const T*>(a.k) + row * a.sk[0] + (h / G) * a.sk[2];
-  const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
-  for (int d = 0; d < count; ++d) {
-    const int x = a.path[(int64_t)row * a.D + d], i = (pos + d) & (kW - 1);
-    if (h % G == 0)
-      for (int e = tid; e < dk; e += kAcceptThreads)
-        static_cast<T*>(c.win_k)[(((int64_t)s * c.Hqk + h / G) * kW + i) * dk + e] = gk[x * a.sk[1] + e];
-    for (int e = tid; e < dv; e += kAcceptThreads)
-      static_cast<T*>(c.win_v)[(((int64_t)s * H + h) * kW + i) * dv + e] = gv[x * a.sv[1] + e];
-    if (tid == 0)
-      c.win_log_a[((int64_t)s * H + h) * kW + i] = a.log_a ? a.log_a[((int64_t)row * a.N + x) * H + h] : 0.f;
-  }
-  if (h == 0 && tid == 0) a.new_pos[row] = pos + count;
+template <typename T, bool kMma>
+cudaError_t launch_main(const ll_cache& c, const AcceptArgs& a, cudaStream_t s) {
+  const size_t row = kMma ? sizeof(T) * (size_t)(c.dk + c.dv + 2 * kPad) : sizeof(float) * (size_t)(((c.dk + 3) & ~3) + c.dv);
+  const auto kernel = accept_kernel<T, kMma>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kW * row));
+  if (e != cudaSuccess) return e;
+  return launch_following(true, kernel, dim3((unsigned)(a.n * c.H)), kAcceptThreads, kW * row, 1, s, c, a);
 }
 
 template <typename T>
 cudaError_t launch(const ll_cache& c, const AcceptArgs& a, cudaStream_t s) {
   accept_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)(a.n * c.H);
-  e = launch_following(true, accept_fold_kernel<T>, dim3(grid), kAcceptThreads, 0, 1, s, c, a);
-  if (e != cudaSuccess) return e;
-  accept_tokens_kernel<T><<<grid, kAcceptThreads, 0, s>>>(c, a);
-  return cudaGetLastError();
+  if constexpr (sizeof(T) == 2) {
+    const int64_t all = c.dk | c.dv | a.sk[0] | a.sk[1] | a.sk[2] | a.sv[0] | a.sv[1] | a.sv[2];
+    const bool whole = all % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15u) == 0;
+    if (whole && c.dk % 16 == 0) return launch_main<T, true>(c, a, s);
+  }
+  return launch_main<T, false>(c, a, s);
 }
 
 }  // namespace

@@ -19,6 +19,7 @@ constexpr int kNone = 0x7fffffff;
 // Scratch of the page operators: who owns each slot in this call, two lists and a map of pages.
 struct Scratch {
   int* owner;  // [slots] lowest row of this call that names the slot
+  int* done;   // [slots] CTAs that have read the slot's block
   int* from;   // [n_pages]
   int* to;     // [n_pages]
   int* map;    // [n_pages]
@@ -27,7 +28,8 @@ struct Scratch {
 __host__ __device__ __forceinline__ Scratch scratch_of(const ll_cache& c) {
   Scratch s;
   s.owner = c.scratch;
-  s.from = s.owner + c.slots;
+  s.done = s.owner + c.slots;
+  s.from = s.done + c.slots;
   s.to = s.from + c.n_pages;
   s.map = s.to + c.n_pages;
   s.count = s.map + c.n_pages;
@@ -340,6 +342,29 @@ __device__ __forceinline__ uint32_t take_bf16(float2& x, float2 least) {
   x = make_float2(fmaxf(x.x - f.x, least.x), fmaxf(x.y - f.y, least.y));
   return h;
 }
+// The B fragments of a fold: 8 columns of the block's 64 values, decayed, as three bf16 parts which together are
+// the fp32 product; infinities as take_bf16 keeps them.  wvs: [token][vp], tok: the tokens' decays.
+__device__ __forceinline__ void load_decayed(uint32_t (&b)[kW / 16][3][2], const __nv_bfloat16* wvs, const float* tok,
+                                             int vp) {
+  const int lane = threadIdx.x & 31, i = 2 * (lane & 3);
+#pragma unroll
+  for (int ks = 0; ks < kW / 16; ks += 2) {
+    uint32_t r[4];  // tokens 16 ks .. + 31 of 8 columns
+    ldmatrix_trans(r, wvs + (16 * ks + lane) * vp);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = 16 * ks + 8 * u + i;
+      float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[u]));
+      const float2 e = *reinterpret_cast<const float2*>(tok + s);
+      x = make_float2(fabsf(x.x * e.x), fabsf(x.y * e.y));
+      const float2 least = make_float2(fminf(x.x, 0x1p-133f), fminf(x.y, 0x1p-133f));
+      const uint32_t sign = r[u] & 0x80008000u;
+#pragma unroll
+      for (int v = 0; v < 3; ++v) b[ks + (u >> 1)][v][u & 1] = take_bf16(x, least) | sign;
+    }
+  }
+}
+
 inline int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
