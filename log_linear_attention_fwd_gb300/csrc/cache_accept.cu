@@ -92,21 +92,30 @@ __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, A
 }
 
 constexpr int kAcceptThreads = 256, kAcceptWarps = kAcceptThreads / 32;
+constexpr int kTogether = 2;  // pages whose loads are on their way together, 8 of a thread
 constexpr int kPad = 8;  // elements that set a token's row off by 16 bytes
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Rows of `width` elements from src_of(row) to dst_of(row), by the CTA; whole 16-byte pieces (vec) or elements.
+// Rows of `width` elements from src_of(row) to dst_of(row), by the CTA; whole 16-byte pieces (vec), four of a thread
+// on their way, or elements.
 template <typename T, typename Src, typename Dst>
 __device__ __forceinline__ void copy_tokens(int rows, int width, bool vec, Src src_of, Dst dst_of) {
-  constexpr int per = 16 / sizeof(T), kLanes = 128 / per;  // pieces of 128 columns
+  constexpr int per = 16 / sizeof(T), kLanes = 128 / per, kStep = kAcceptThreads / kLanes;  // pieces of 128 columns
   if (vec) {
     const int x = (threadIdx.x & (kLanes - 1)) * per;
     if (x < width)
-      for (int r = threadIdx.x / kLanes; r < rows; r += kAcceptThreads / kLanes)
-        *reinterpret_cast<uint4*>(dst_of(r) + x) = *reinterpret_cast<const uint4*>(src_of(r) + x);
+      for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += 4 * kStep) {
+        uint4 y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (r0 + u * kStep < rows) y[u] = *reinterpret_cast<const uint4*>(src_of(r0 + u * kStep) + x);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (r0 + u * kStep < rows) *reinterpret_cast<uint4*>(dst_of(r0 + u * kStep) + x) = y[u];
+      }
   } else {
     const int x = threadIdx.x & 127;
     if (x < width)
@@ -114,11 +123,39 @@ __device__ __forceinline__ void copy_tokens(int rows, int width, bool vec, Src s
   }
 }
 
+constexpr int kTokenHeads = 4;  // heads of a CTA that only copies tokens
+
+// Tokens d0 .. d1 - 1 of the row's path, the first of which follows r tokens of the block (they stay inside one),
+// to their places: the values of heads [h0, h1), the keys [q0, q1).
+template <typename T>
+__device__ __forceinline__ void put_values(const ll_cache& c, const AcceptArgs& a, int row, int s, int r, const int* path,
+                                           int d0, int d1, int h0, int h1) {
+  const int H = (int)c.H, dv = (int)c.dv, n = d1 - d0, at = (r + d0) & (kW - 1);
+  const T* gv = static_cast<const T*>(a.v) + row * a.sv[0];
+  T* wv = static_cast<T*>(c.win_v) + ((int64_t)s * H * kW + at) * dv;
+  const bool vec = ((dv | a.sv[0] | a.sv[1] | a.sv[2]) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.v) & 15u) == 0;
+  copy_tokens<T>(n * (h1 - h0), dv, vec, [&](int i) { return gv + (h0 + i / n) * a.sv[2] + path[d0 + i % n] * a.sv[1]; },
+                 [&](int i) { return wv + (int64_t)((h0 + i / n) * kW + i % n) * dv; });
+  for (int i = threadIdx.x; i < n * (h1 - h0); i += kAcceptThreads) {
+    const int h = h0 + i / n, d = i % n;
+    c.win_log_a[((int64_t)s * H + h) * kW + at + d] = a.log_a ? a.log_a[((int64_t)row * a.N + path[d0 + d]) * H + h] : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put_keys(const ll_cache& c, const AcceptArgs& a, int row, int s, int r, const int* path, int d0,
+                                         int d1, int q0, int q1) {
+  const int dk = (int)c.dk, n = d1 - d0, at = (r + d0) & (kW - 1);
+  const T* gk = static_cast<const T*>(a.k) + row * a.sk[0];
+  T* wk = static_cast<T*>(c.win_k) + ((int64_t)s * c.Hqk * kW + at) * dk;
+  const bool vec = ((dk | a.sk[0] | a.sk[1] | a.sk[2]) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.k) & 15u) == 0;
+  copy_tokens<T>(n * (q1 - q0), dk, vec, [&](int i) { return gk + (q0 + i / n) * a.sk[2] + path[d0 + i % n] * a.sk[1]; },
+                 [&](int i) { return wk + (int64_t)((q0 + i / n) * kW + i % n) * dk; });
+}
+
 // One CTA per (row, head): the path's tokens to their places and, where they end the block, its fold: the sum
 // of the pages below the level that it goes to, decayed, and of the 64 tokens' products.  kMma: bf16 tokens of whole
 // 16-byte pieces, whose products run on the tensor cores, exact keys against decayed values in three bf16
-// parts, as in the step; else fp32 multiply-adds.  The pages go from HBM to the fragments and the new
-// page from there.  Tokens of the next block replace those that the fold reads: a head's own
+// parts, as in the step; else fp32 multiply-adds.  Tokens of the next block replace those that the fold reads: a head's own
 // values behind its own reads, the keys that heads share by the row's last CTA to have read them.
 template <typename T, bool kMma>
 __global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll_cache c, AcceptArgs a) {
@@ -131,10 +168,7 @@ __global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll
   const int H = (int)c.H, Hqk = (int)c.Hqk, G = H / Hqk, dk = (int)c.dk, dv = (int)c.dv, M = (int)c.levels;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int row = blockIdx.x / H, h = blockIdx.x - row * H, hq = h / G;
-  wait_for_previous();
   const int s = a.slots[row], pos = a.pos[row];
-  const Scratch sc = scratch_of(c);
-  if (!owns(c, sc.owner, s, row)) return;
   const int j = pos >> kLogW, r = pos & (kW - 1), par = j & 1, to = __ffs(j + 1) - 1;
   if (w == 0) {
     const int x = lane < a.D ? a.path[(int64_t)row * a.D + lane] : -1, y = lane + 32 < a.D ? a.path[(int64_t)row * a.D + lane + 32] : -1;
@@ -142,155 +176,182 @@ __global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll
     path[lane + 32] = y;
     const unsigned x_end = __ballot_sync(0xffffffffu, x < 0), y_end = __ballot_sync(0xffffffffu, y < 0);
     if (lane == 0) count_s = x_end ? __ffs(x_end) - 1 : y_end ? 31 + __ffs(y_end) : 64;
-  } else if (w == 1) {  // the fold's pages, in case
-    const bool here = lane < M && (lane == to || (j >> lane & 1));
+  }
+  wait_for_previous();  // what the plan has settled
+  const Scratch sc = scratch_of(c);
+  const bool served = owns(c, sc.owner, s, row);
+  if (w == 1) {  // the fold's pages, in case (where there is one to go to, the plan has made it the slot's own)
+    const bool here = served && lane < M && (lane == to || (j >> lane & 1));
     const int e = here ? c.page_table[(int64_t)s * M + lane] : 0;
-    const bool gone = here && (e < 0 || e >= c.n_pages || (lane == to && c.refcount[e] != 1));
     if (lane < M) page_at[lane] = e;
-    const bool why = __any_sync(0xffffffffu, gone);
+    const bool why = __any_sync(0xffffffffu, e < 0 || e >= c.n_pages);
     if (lane == 0) why_s = why ? LL_CACHE_ERR_MISSING : 0;
   }
   __syncthreads();
+  if (!served) return;
   const int count = count_s;
   const bool fold = r + count >= kW;
   if (fold && why_s) {
     if (tid == 0 && h == 0) raise(c, why_s);
     return;
   }
+  if (!fold) {  // a few heads by one CTA
+    const int h1 = min(H, h + kTokenHeads);
+    if (h % kTokenHeads) return;
+    put_values<T>(c, a, row, s, r, path, 0, count, h, h1);
+    put_keys<T>(c, a, row, s, r, path, 0, count, (h + G - 1) / G, (h1 + G - 1) / G);  // whose first head is among them
+    if (h == 0 && tid == 0) a.new_pos[row] = pos + count;
+    return;
+  }
   const T* gk = static_cast<const T*>(a.k) + row * a.sk[0] + hq * a.sk[2];
   const T* gv = static_cast<const T*>(a.v) + row * a.sv[0] + h * a.sv[2];
   const float* ga = a.log_a ? a.log_a + (int64_t)row * a.N * H + h : nullptr;
-  T* wk = static_cast<T*>(c.win_k) + ((int64_t)s * Hqk + hq) * kW * dk;
-  T* wv = static_cast<T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
-  float* wa = c.win_log_a + ((int64_t)s * H + h) * kW;
-  const bool k_vec = ((dk | a.sk[0] | a.sk[1] | a.sk[2]) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.k) & 15u) == 0;
-  const bool v_vec = ((dv | a.sv[0] | a.sv[1] | a.sv[2]) * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.v) & 15u) == 0;
-  const int ends = min(count, kW - r);  // tokens in this block
-  if (fold) {
-    // the 64 tokens, of the block and of the path
-    auto key = [&](int i) { return i < r ? wk + i * dk : gk + path[i - r] * a.sk[1]; };
-    auto value = [&](int i) { return i < r ? wv + i * dv : gv + path[i - r] * a.sv[1]; };
-    const int kp = kMma ? dk + kPad : (dk + 3) & ~3, vp = kMma ? dv + kPad : dv;
-    __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(dyn);
-    __nv_bfloat16* vs = ks + kW * kp;
-    float* kf = reinterpret_cast<float*>(dyn);
-    float* vf = kf + kW * kp;
-    if constexpr (kMma) {
-      const int x = (tid & 15) * 8;
-      for (int i = tid >> 4; i < kW; i += kAcceptThreads / 16) {
-        if (x < dk) cp_async16(ks + i * kp + x, key(i) + x);
-        if (x < dv) cp_async16(vs + i * vp + x, value(i) + x);
-      }
-    } else {
-      const int x = tid & 127;
+  const T* wk = static_cast<const T*>(c.win_k) + ((int64_t)s * Hqk + hq) * kW * dk;
+  const T* wv = static_cast<const T*>(c.win_v) + ((int64_t)s * H + h) * kW * dv;
+  const float* wa = c.win_log_a + ((int64_t)s * H + h) * kW;
+  const int ends = kW - r;  // tokens of the path in this block
+  // the 64 tokens, of the block and of the path
+  auto key = [&](int i) { return i < r ? wk + i * dk : gk + path[i - r] * a.sk[1]; };
+  auto value = [&](int i) { return i < r ? wv + i * dv : gv + path[i - r] * a.sv[1]; };
+  const int kp = kMma ? dk + kPad : (dk + 3) & ~3, vp = kMma ? dv + kPad : dv;
+  __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(dyn);
+  __nv_bfloat16* vs = ks + kW * kp;
+  float* kf = reinterpret_cast<float*>(dyn);
+  float* vf = kf + kW * kp;
+  if constexpr (kMma) {
+    const int x = (tid & 15) * 8;
+    for (int i = tid >> 4; i < kW; i += kAcceptThreads / 16) {
+      if (x < dk) cp_async16(ks + i * kp + x, key(i) + x);
+      if (x < dv) cp_async16(vs + i * vp + x, value(i) + x);
+    }
+  } else {
+    const int x = tid & 127;
 #pragma unroll 4
-      for (int i = tid >> 7; i < kW; i += kAcceptThreads >> 7) {
-        if (x < kp) kf[i * kp + x] = x < dk ? to_f32(key(i)[x]) : 0.f;
-        if (x < dv) vf[i * vp + x] = to_f32(value(i)[x]);
-      }
-    }
-    if (w == 0) {
-      auto la = [&](int i) { return i < r ? wa[i] : ga ? ga[(int64_t)path[i - r] * H] : 0.f; };
-      float since;
-      block_decays(la(lane), la(lane + 32), kW, c.page_from[s * 2 + par], tok, &since);
-      tok[lane] = expf(tok[lane]);
-      tok[lane + 32] = expf(tok[lane + 32]);
-      const bool here = lane < M && (j >> lane & 1);
-      float* log = c.page_log + ((int64_t)s * 2 * M + lane) * H + h;
-      const float old = here ? log[(int64_t)par * M * H] + since : 0.f;
-      if (here && lane < to) page_e[lane] = expf(old);
-      // what the next block's calls read
-      if (lane < M && (lane == to || (here && lane > to))) log[(int64_t)(1 - par) * M * H] = lane == to ? 0.f : old;
-      if (h == 0 && lane == 0) c.page_from[s * 2 + 1 - par] = 0;
-    }
-    if constexpr (kMma) tc::cp_async_wait_all();
-    __syncthreads();
-    const int64_t size = (int64_t)dk * dv;
-    float* D = c.pages + ((int64_t)page_at[to] * H + h) * size;
-    auto page = [&](int m) { return c.pages + ((int64_t)page_at[m] * H + h) * size; };
-    if constexpr (kMma) {
-      const int g = lane >> 2, i = 2 * (lane & 3);
-      const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
-      for (int nt = w; nt < dv / 8; nt += kAcceptWarps) {
-        uint32_t b[kW / 16][3][2];
-        load_decayed(b, vs + 8 * nt, tok, vp);
-        // two row tiles at a time: their pages' values are on the way while the products run
-        for (int d = 0; d < dk; d += 32) {
-          const int64_t at = (int64_t)(d + g) * dv + 8 * nt + i;
-          float2 x[4];  // rows g, g + 8, g + 16, g + 24
-#pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = make_float2(0.f, 0.f);
-          for (int m = 0; m < to; ++m) {
-            const float e = page_e[m];
-            const float* P = page(m) + at;
-            float2 y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = d + 8 * u < dk ? __ldcs(reinterpret_cast<const float2*>(P + 8 * u * dv)) : make_float2(0.f, 0.f);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = make_float2(fmaf(e, y[u].x, x[u].x), fmaf(e, y[u].y, x[u].y));
-          }
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            if (d + 16 * z >= dk) continue;
-            float f[4] = {x[2 * z].x, x[2 * z].y, x[2 * z + 1].x, x[2 * z + 1].y};
-#pragma unroll
-            for (int q = 0; q < kW / 16; ++q) {
-              uint32_t ka[4];
-              ldmatrix_trans(ka, ks + (16 * q + mrow) * kp + d + 16 * z + mcol);
-#pragma unroll
-              for (int v = 2; v >= 0; --v) mma_bf16(f, ka, b[q][v][0], b[q][v][1]);
-            }
-            *reinterpret_cast<float2*>(D + at + 16 * z * dv) = make_float2(f[0], f[1]);
-            *reinterpret_cast<float2*>(D + at + (16 * z + 8) * dv) = make_float2(f[2], f[3]);
-          }
-        }
-      }
-    } else {  // four rows of four columns per thread and pass
-      const int groups = dv / 4, lanes = kAcceptThreads / groups, col = 4 * (tid % groups);
-      for (int d = 4 * (tid / groups); tid / groups < lanes && d < dk; d += 4 * lanes) {
-        float4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int m = 0; m < to; ++m)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (d + u < dk) x[u] = fma4(page_e[m], *reinterpret_cast<const float4*>(page(m) + (int64_t)(d + u) * dv + col), x[u]);
-        for (int i = 0; i < kW; ++i) {
-          const float4 v4 = *reinterpret_cast<const float4*>(vf + i * vp + col);
-          const float4 k4 = *reinterpret_cast<const float4*>(kf + i * kp + d);
-          const float e = tok[i];
-          x[0] = fma4(e * k4.x, v4, x[0]);
-          x[1] = fma4(e * k4.y, v4, x[1]);
-          x[2] = fma4(e * k4.z, v4, x[2]);
-          x[3] = fma4(e * k4.w, v4, x[3]);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (d + u < dk) *reinterpret_cast<float4*>(D + (int64_t)(d + u) * dv + col) = x[u];
-      }
+    for (int i = tid >> 7; i < kW; i += kAcceptThreads >> 7) {
+      if (x < kp) kf[i * kp + x] = x < dk ? to_f32(key(i)[x]) : 0.f;
+      if (x < dv) vf[i * vp + x] = to_f32(value(i)[x]);
     }
   }
-  // the tokens to their places: first those of this block, which no fold reads there
-  if (h % G == 0)
-    copy_tokens<T>(ends, dk, k_vec, [&](int d) { return gk + path[d] * a.sk[1]; }, [&](int d) { return wk + (r + d) * dk; });
-  copy_tokens<T>(count, dv, v_vec, [&](int d) { return gv + path[d] * a.sv[1]; },
-                 [&](int d) { return wv + ((r + d) & (kW - 1)) * dv; });
-  for (int d = tid; d < count; d += kAcceptThreads) wa[(r + d) & (kW - 1)] = ga ? ga[(int64_t)path[d] * H] : 0.f;
+  if (w == 0) {
+    auto la = [&](int i) { return i < r ? wa[i] : ga ? ga[(int64_t)path[i - r] * H] : 0.f; };
+    float since;
+    block_decays(la(lane), la(lane + 32), kW, c.page_from[s * 2 + par], tok, &since);
+    tok[lane] = expf(tok[lane]);
+    tok[lane + 32] = expf(tok[lane + 32]);
+    const bool here = lane < M && (j >> lane & 1);
+    float* log = c.page_log + ((int64_t)s * 2 * M + lane) * H + h;
+    const float old = here ? log[(int64_t)par * M * H] + since : 0.f;
+    if (here && lane < to) page_e[lane] = expf(old);
+    // what the next block's calls read
+    if (lane < M && (lane == to || (here && lane > to))) log[(int64_t)(1 - par) * M * H] = lane == to ? 0.f : old;
+    if (h == 0 && lane == 0) c.page_from[s * 2 + 1 - par] = 0;
+  }
+  __syncthreads();
+  const int64_t size = (int64_t)dk * dv;
+  float* D = c.pages + ((int64_t)page_at[to] * H + h) * size;
+  auto page = [&](int m) { return c.pages + ((int64_t)page_at[m] * H + h) * size; };
+  if constexpr (kMma) {
+    // first the pages' sum, to the new page, whose L2 lines the products then pick up: fragments of 32
+    // bytes per row would take HBM three times as long
+    for (int i0 = tid; to && i0 < size / 4; i0 += 4 * kAcceptThreads) {
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int m = 0; m < to; m += kTogether) {
+        float4 y[kTogether][4];
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (m + q < to && i0 + u * kAcceptThreads < size / 4)
+              y[q][u] = __ldcs(reinterpret_cast<const float4*>(page(m + q)) + i0 + u * kAcceptThreads);
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+          if (m + q < to)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = fma4(page_e[m + q], y[q][u], v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kAcceptThreads < size / 4) reinterpret_cast<float4*>(D)[i0 + u * kAcceptThreads] = v[u];
+    }
+    tc::cp_async_wait_all();
+    __syncthreads();
+  }
+  if constexpr (kMma) {
+    const int g = lane >> 2, i = 2 * (lane & 3);
+    const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
+    for (int nt = w; nt < dv / 8; nt += kAcceptWarps) {
+      uint32_t b[kW / 16][3][2];
+      load_decayed(b, vs + 8 * nt, tok, vp);
+      // two row tiles at a time
+      for (int d = 0; d < dk; d += 32) {
+        const int64_t at = (int64_t)(d + g) * dv + 8 * nt + i;
+        float2 x[4];  // rows g, g + 8, g + 16, g + 24
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (to && d + 8 * u < dk) x[u] = __ldcg(reinterpret_cast<const float2*>(D + at + 8 * u * dv));
+        float f[2][4] = {{x[0].x, x[0].y, x[1].x, x[1].y}, {x[2].x, x[2].y, x[3].x, x[3].y}};
+#pragma unroll
+        for (int v = 2; v >= 0; --v)
+#pragma unroll
+          for (int q = 0; q < kW / 16; ++q)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              uint32_t ka[4];  // (past the last row: of others, not stored)
+              ldmatrix_trans(ka, ks + (16 * q + mrow) * kp + min(d + 16 * z, dk - 16) + mcol);
+              mma_bf16(f[z], ka, b[q][v][0], b[q][v][1]);
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (d + 8 * u < dk)
+            *reinterpret_cast<float2*>(D + at + 8 * u * dv) = make_float2(f[u >> 1][2 * (u & 1)], f[u >> 1][2 * (u & 1) + 1]);
+      }
+    }
+  } else {  // four rows of four columns per thread and pass
+    const int groups = dv / 4, lanes = kAcceptThreads / groups, col = 4 * (tid % groups);
+    for (int d = 4 * (tid / groups); tid / groups < lanes && d < dk; d += 4 * lanes) {
+      float4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int m = 0; m < to; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (d + u < dk) x[u] = fma4(page_e[m], *reinterpret_cast<const float4*>(page(m) + (int64_t)(d + u) * dv + col), x[u]);
+      for (int i = 0; i < kW; ++i) {
+        const float4 v4 = *reinterpret_cast<const float4*>(vf + i * vp + col);
+        const float4 k4 = *reinterpret_cast<const float4*>(kf + i * kp + d);
+        const float e = tok[i];
+        x[0] = fma4(e * k4.x, v4, x[0]);
+        x[1] = fma4(e * k4.y, v4, x[1]);
+        x[2] = fma4(e * k4.z, v4, x[2]);
+        x[3] = fma4(e * k4.w, v4, x[3]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (d + u < dk) *reinterpret_cast<float4*>(D + (int64_t)(d + u) * dv + col) = x[u];
+    }
+  }
+  // the path's tokens to their places: those of this block, which no fold reads there, this head's values of the
+  // next one, and its keys where no other head reads them, else by the row's last CTA to have read this one's
+  put_values<T>(c, a, row, s, r, path, 0, ends, h, h + 1);
+  if (h % G == 0) put_keys<T>(c, a, row, s, r, path, 0, ends, hq, hq + 1);
   if (h == 0 && tid == 0) a.new_pos[row] = pos + count;
   if (count == ends) return;
-  // then the keys of the next block, by the row's last CTA to have read this one's
+  put_values<T>(c, a, row, s, r, path, ends, count, h, h + 1);
+  if (G == 1) {
+    put_keys<T>(c, a, row, s, r, path, ends, count, h, h + 1);
+    return;
+  }
   __syncthreads();
   if (tid == 0) {
     __threadfence();
     last_s = atomicAdd(sc.done + s, 1) == H - 1;
   }
   __syncthreads();
-  if (!last_s) return;
-  T* all_k = static_cast<T*>(c.win_k) + (int64_t)s * Hqk * kW * dk;
-  const T* all_g = static_cast<const T*>(a.k) + row * a.sk[0];
-  for (int q = 0; q < Hqk; ++q)
-    copy_tokens<T>(count - ends, dk, k_vec, [&](int d) { return all_g + q * a.sk[2] + path[ends + d] * a.sk[1]; },
-                   [&](int d) { return all_k + ((int64_t)q * kW + d) * dk; });
+  if (last_s) put_keys<T>(c, a, row, s, r, path, ends, count, 0, Hqk);
 }
 
 template <typename T, bool kMma>

@@ -365,6 +365,19 @@ __device__ __forceinline__ void load_decayed(uint32_t (&b)[kW / 16][3][2], const
   }
 }
 
+// x / d for x < 2^31, without a division.
+struct FastDiv {
+  uint32_t mul, log;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t log = 0;
+  while ((1ull << log) < d) ++log;
+  return {(uint32_t)((((1ull << log) - d) << 32) / d + 1), log};
+}
+__device__ __forceinline__ int operator/(int x, FastDiv d) {
+  return (int)((__umulhi((uint32_t)x, d.mul) + (uint32_t)x) >> d.log);
+}
+
 inline int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -17,19 +17,6 @@ namespace {
 
 constexpr int kNodes = LL_TREE_MAX;
 
-// x / d for x < 2^31, without a division.
-struct FastDiv {
-  uint32_t mul, log;
-};
-FastDiv fast_div(uint32_t d) {
-  uint32_t log = 0;
-  while ((1ull << log) < d) ++log;
-  return {(uint32_t)((((1ull << log) - d) << 32) / d + 1), log};
-}
-__device__ __forceinline__ int operator/(int x, FastDiv d) {
-  return (int)((__umulhi((uint32_t)x, d.mul) + (uint32_t)x) >> d.log);
-}
-
 struct TreeArgs {
   const int* slots;
   const int* pos;
