@@ -34,24 +34,25 @@ struct TreeArgs {
   FastDiv heads, per_qk;        // H, H / Hqk
 };
 
-// A CTA serves one (row, head) for up to 8 NT nodes: eight consumer warps, and a producer warp that
-// brings the pages in stages of up to 16 KB through a ring.  The products run on the tensor cores
+// A CTA serves one (row, head) for up to 8 NT nodes: eight warps that compute, and one that
+// keeps a ring of stages of up to 16 KB of the pages filled.  The products run on the tensor cores
 // as out^T = page^T q^T: a page's values go from the ring to the fragments as they are, and the nodes
 // are the narrow side.  mma.sync in tf32, not tcgen05: a page lies in memory with the output's
 // columns side by side, and every value of it is used for at most 64 nodes, so HBM and, with small
-// trees, the instructions around the products are the bounds, not the tensor pipe (17 % busy).
+// trees, the instructions around the products are the bounds, not the tensor pipe.
 //
-// Precision.  q of a bf16 cache is exact in tf32.  For bf16 outputs a page's value is rounded to
-// tf32 (2^-11 of each, an eighth of the output's own half step), for fp32 outputs it is two parts that
-// leave 2^-22; with fp32 tokens everything is two parts and their products but the least.  A token's
-// weight is two bf16 parts against exact bf16 values.  All sums are fp32, and a page is summed by
-// itself before it is weighted per node.
-constexpr int kTreeWarps = 8, kConsumerThreads = 32 * kTreeWarps, kTreeThreads = kConsumerThreads + 32;
+// Precision.  q of a bf16 cache is exact in tf32.  For bf16 outputs a page's value and a token's weight are rounded
+// to tf32 (2^-11 of each, an eighth of the output's own half step), for fp32 outputs they are two parts that
+// leave 2^-22; with fp32 tokens everything is two parts and their products but the least.  All sums are fp32, and a
+// page is summed by itself before it is weighted per node.
+constexpr int kTreeWarps = 8, kConsumers = 32 * kTreeWarps, kTreeThreads = kConsumers + 32;
+constexpr int kFiller = kTreeWarps;    // the warp that fills the ring
+constexpr int kWalkers = kTreeWarps - 2;  // the first of the two warps that have a node per thread
 constexpr int kStageBytes = 16384;
 constexpr int kMaxTreeStages = 8;
 constexpr int kTreeSplit = 8;          // CTAs of a cluster
 constexpr int kQPitch = 132;           // floats from query to query
-constexpr int kPPitch = kW + kNodes + 8;  // elements from node to node of the tokens' weights
+constexpr int kPPitch = kW + kNodes + 8;  // floats from node to node of the tokens' weights
 
 template <typename T>
 struct Parts {
@@ -65,14 +66,14 @@ struct TreeLayout {
   int vp, lp;                 // elements from row to row: v, lambda
   int p, v, q, lam, pw, end;  // where each begins
 };
-template <typename T, int NT>
+template <typename T, int NT, int kPage>
 __host__ __device__ __forceinline__ TreeLayout tree_layout(int dv, int N, int M) {
   const int dv16 = (dv + 15) & ~15, tokens = kW + ((N + 15) & ~15);
   TreeLayout l;
-  l.vp = dv16 + (sizeof(T) == 2 ? 8 : 4);  // an odd number of 16-byte pieces: ldmatrix without conflicts
+  l.vp = dv16 + (sizeof(T) == 2 ? 8 : 4);  // rows 2 i and 2 i + 1 of four threads fall into banks of their own
   l.lp = pad4(M + kLogW + 1);
   l.p = 0;
-  l.v = l.p + 2 * 8 * NT * kPPitch * (int)sizeof(T);  // two parts: bf16, or tf32 of an fp32 cache
+  l.v = l.p + kPage * 8 * NT * kPPitch * 4;
   l.q = l.v + tokens * l.vp * (int)sizeof(T);
   l.lam = l.q + Parts<T>::in * 8 * NT * kQPitch * 4;
   l.pw = l.lam + 8 * NT * l.lp * 4;
@@ -95,13 +96,12 @@ struct TreeSmem {
   unsigned long long above[kNodes];  // nodes on the path, itself included
   float since;
   unsigned bad[kTreeWarps + 1];      // what each warp found
-  unsigned bad_tree[2];
   int odd;                           // a node's v has infinities or NaN
 };
 
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kConsumerThreads) : "memory");
-}
+// Of the eight warps that compute, and of the two that have the nodes.
+__device__ __forceinline__ void consumer_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
+__device__ __forceinline__ void walkers_sync() { asm volatile("barrier.cta.sync 2, 64;" ::: "memory"); }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -115,9 +115,6 @@ __device__ __forceinline__ void ldmatrix4(uint32_t& r0, uint32_t& r1, uint32_t& 
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(at)
                : "memory");
-}
-__device__ __forceinline__ void ldmatrix2(uint32_t& r0, uint32_t& r1, uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
 }
 __device__ __forceinline__ void load2(float2& v, uint32_t at) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
@@ -145,14 +142,19 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   const float rest = fmaxf(fabsf(x) - fabsf(__uint_as_float(hi)), fminf(fabsf(x), 0x1p-126f));
   lo = __float_as_uint(rest) | (hi & 0x80000000u);
 }
-// x and y as two bf16 parts, packed; the same care.
-__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const uint32_t sign = (__float_as_uint(x) >> 16 & 0x8000u) | (__float_as_uint(y) & 0x80000000u);
-  float2 v = make_float2(fabsf(x), fabsf(y));
-  const float2 least = make_float2(fminf(v.x, 0x1p-133f), fminf(v.y, 0x1p-133f));
-  hi = take_bf16(v, least) | sign;
-  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(lo) : "f"(v.x), "f"(v.y));
-  lo |= sign;
+// A decay, of a sum of log decays; within 2^-20 where it is then rounded to tf32.
+template <int kPage>
+__device__ __forceinline__ float decay(float x) { return kPage == 1 ? __expf(x) : expf(x); }
+// Two neighbouring values as tf32 parts.
+__device__ __forceinline__ void parts2(const __nv_bfloat16* p, uint32_t (&part)[1][2]) {
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+  part[0][0] = x << 16;
+  part[0][1] = x & 0xffff0000u;
+}
+__device__ __forceinline__ void parts2(const float* p, uint32_t (&part)[2][2]) {
+  const float2 x = *reinterpret_cast<const float2*>(p);
+  split_tf32(x.x, part[0][0], part[1][0]);
+  split_tf32(x.y, part[0][1], part[1][1]);
 }
 
 // 8 values of a row from column k on, 0 past `width`, as they are.
@@ -211,7 +213,7 @@ __device__ __forceinline__ bool whole_pieces(const T* p, int64_t stride, int wid
 template <typename T>
 __device__ __forceinline__ void bring_rows(T* dst, int pitch, const T* src, int64_t stride, int rows, int width) {
   if (whole_pieces(src, stride, width)) {
-    constexpr int kPieces = 8 * (int)sizeof(T), kStep = kConsumerThreads / kPieces;  // 16-byte pieces of 128 columns
+    constexpr int kPieces = 8 * (int)sizeof(T), kStep = kConsumers / kPieces;  // 16-byte pieces of 128 columns
     const int y = threadIdx.x / kPieces, x = (threadIdx.x & (kPieces - 1)) * (16 / (int)sizeof(T));
     if (x >= width) return;
     uint32_t to = tc::smem_u32(dst + y * pitch + x);
@@ -220,7 +222,7 @@ __device__ __forceinline__ void bring_rows(T* dst, int pitch, const T* src, int6
   } else {
     const int x = threadIdx.x & 127;
     if (x < width)
-      for (int r = threadIdx.x >> 7; r < rows; r += kConsumerThreads >> 7) dst[r * pitch + x] = src[r * stride + x];
+      for (int r = threadIdx.x >> 7; r < rows; r += kConsumers >> 7) dst[r * pitch + x] = src[r * stride + x];
   }
 }
 
@@ -267,20 +269,20 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
   const int j = pos >> kLogW, r = pos & (kW - 1), par = j & 1, to = __ffs(j + 1) - 1, live = __popc(j);
   const int64_t first_node = (int64_t)row * a.N;
   uint8_t* body = dyn + a.own * kStageBytes;
-  const TreeLayout lay = tree_layout<T, NT>(dv, a.N, M);
-  T* ps = reinterpret_cast<T*>(body + lay.p);  // [2 parts][NQ][kPPitch]
+  const TreeLayout lay = tree_layout<T, NT, kPage>(dv, a.N, M);
+  float* ps = reinterpret_cast<float*>(body + lay.p);  // [kPage parts][NQ][kPPitch]
   T* vs = reinterpret_cast<T*>(body + lay.v);
   float* qs = reinterpret_cast<float*>(body + lay.q);  // [parts][NQ][kQPitch]; of every 8 columns the even ones, then the odd ones
   float* lam_s = reinterpret_cast<float*>(body + lay.lam);
   float* page_w = reinterpret_cast<float*>(body + lay.pw);
-  float* wt = reinterpret_cast<float*>(dyn + (a.own - 1) * kStageBytes);  // the last own stage, until the pages need it
+  float* wt = reinterpret_cast<float*>(dyn + (a.own - 1) * kStageBytes);  // log decays of the tree, in the last own stage until the pages need it
   float* red = reinterpret_cast<float*>(dyn);                               // the ring, behind the pages
 
   // geometry of the pages: col_boxes boxes of 32 columns, the rows in stages of box_rows
   const int col_boxes = (dv + 31) / 32, box_rows = a.box_rows, box_bytes = box_rows * 128;
   const int share = (((dk + 15) / 16 + Z - 1) >> a.split_log) * 16;
   const int k0 = min(dk, sp * share), k1 = min(dk, k0 + share);  // this CTA's rows
-  // the producer's place in the pages: page, row; stage and how often it was used
+  // the filler's place in the pages: page, row; stage and how often it was used
   int m = 0, d0 = k0, st = 0, use = 0;
   auto bring_stage = [&]() {
     tc::mbar_arrive_expect_tx(&sm.full[st], col_boxes * box_bytes);
@@ -300,8 +302,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
   const int lanes_g = lane >> 2, lanes_i = 2 * (lane & 3);
   const int tiles = kW / 16 + (N + 15) / 16;  // of 16 tokens: the block's, then the nodes; one per warp
   const bool mine = w < tiles && (w & (Z - 1)) == sp && (w >= kW / 16 || 16 * w < r);
-  // the last two consumer warps have a node per thread: their tiles are there for most nodes only
-  const int node = w < kTreeWarps ? tid - (kConsumerThreads - kNodes) : -1;
+  // the last two warps have a node per thread: their tiles are there for most nodes only
+  const int node = w >= kWalkers && w < kTreeWarps ? tid - 32 * kWalkers : -1;
   bool ok = true;
   float sc[NT][4];
 #pragma unroll
@@ -309,7 +311,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
 #pragma unroll
     for (int u = 0; u < 4; ++u) sc[t][u] = 0.f;
 
-  if (w == kTreeWarps) {
+  // everything that is read, first
+  if (w == kFiller) {
     const bool here = lane < M && (j >> lane) & 1;
     const int e = here ? c.page_table[(int64_t)s * M + lane] : 0;
     const float log = here ? c.page_log[(((int64_t)s * 2 + par) * M + lane) * H + h] : 0.f;
@@ -322,7 +325,6 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       tc::fence_mbar_init();
       sm.odd = 0;
     }
-    __syncwarp();
     if (here) {
       const int at = __popc(j & ((1 << lane) - 1));
       sm.page_at[at] = e;
@@ -330,14 +332,14 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       sm.page_log[at] = log;
     }
     const bool missing = __any_sync(0xffffffffu, e < 0 || e >= c.n_pages);
+    __syncwarp();
     if (lane == 0) {
       sm.bad[w] = (missing ? LL_CACHE_ERR_MISSING : 0) | (before ? LL_CACHE_ERR_POSITION : 0);
       if (!missing && k0 < k1)
         while (m < live && use == 0 && st < a.own - 1) bring_stage();
     }
-    __syncwarp();
+    __syncthreads();
   } else {
-    // everything that is read, first
     int up = -2;
     float la = 0.f;
     if (node >= 0 && node < a.N) {
@@ -366,12 +368,12 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
     for (int q = w; q < queries; q += kTreeWarps)
       if (lane < M + kLogW + 1)
         tc::cp_async4(lam_s + q * lay.lp + lane, a.lam + ((first_node + node0 + q) * H + h) * a.L + lane, 4);
-    {
+    if (node < 0) {
       const T* gq = static_cast<const T*>(a.q) + row * a.sq[0] + hq * a.sq[2] + node0 * a.sq[1];
       const bool vec = whole_pieces(gq, a.sq[1], dk);
       const int k = (tid & 15) * 8;
       if (k < ((dk + 31) & ~31))
-        for (int q = tid >> 4; q < queries; q += kConsumerThreads / 16) {
+        for (int q = tid >> 4; q < queries; q += 2 * kWalkers) {
           uint32_t part[kIn][8];
           parts_of(load8(gq + q * a.sq[1], k, dk, vec), part);
 #pragma unroll
@@ -386,48 +388,42 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
     bring_rows(vs, lay.vp, wv, dv, r, dv);
     bring_rows(vs + kW * lay.vp, lay.vp, gv, a.sv[1], N, dv);
     cp_async_commit();
-    unsigned bad = 0;
-    if (node >= 0) {
-      const bool fine = up < node && up >= -2;
-      if (!fine) bad = LL_CACHE_ERR_TREE;
-      sm.up[node] = fine ? up : -2;
-      sm.la[node] = up != -2 ? la : 0.f;
-    } else if (w == 0) {
-      float since;
-      block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], sm.after, &since);
-      if (lane == 0) sm.since = since;
-    }
-    bad = __reduce_or_sync(0xffffffffu, bad);
-    if (lane == 0) sm.bad[w] = bad;
-    cp_async_wait<1>();
-    consumer_sync();
-
-    if (node >= 0) {  // the nodes' paths; weights and log decays along those of the queries
-      unsigned long long above = 0;
-      int depth = -1;
-      const bool in = sm.up[node] != -2;
-      bad = 0;
-      for (int x = node; in && x >= 0; x = sm.up[x]) {
-        above |= 1ull << x;
-        ++depth;
-        if (sm.up[x] == -2) bad = LL_CACHE_ERR_TREE;  // a child of a node that is left out
-      }
-      const int q = node - node0, t = pos + depth;
-      if (in && !position_ok(c, t)) bad |= LL_CACHE_ERR_POSITION;
-      sm.above[node] = above;
-      sm.depth[node] = depth;
-      if (in && !bad && q >= 0 && q < queries) {
+    {
+      unsigned bad = 0;
+      if (node >= 0) {  // the nodes' paths, and the log decays along those of the queries
+        const bool fine = up < node && up >= -2;
+        sm.up[node] = up = fine ? up : -2;
+        sm.la[node] = up != -2 ? la : 0.f;
+        walkers_sync();
+        if (!fine) bad = LL_CACHE_ERR_TREE;
+        unsigned long long above = 0;
+        int depth = -1;
+        const int q = node - node0;
+        const bool asks = q >= 0 && q < queries;
         float acc = 0.f;  // log a behind x up to the node
-        for (int x = node, tx = t; x >= 0; x = sm.up[x], --tx) {
-          wt[q * kNodes + x] = lam_s[q * lay.lp + fenwick_level(t, tx)] * expf(acc);
+        for (int x = up == -2 ? -1 : node; x >= 0; x = sm.up[x]) {
+          above |= 1ull << x;
+          ++depth;
+          if (sm.up[x] == -2) bad = LL_CACHE_ERR_TREE;  // a child of a node that is left out
+          if (asks) wt[q * kNodes + x] = acc;
           acc += sm.la[x];
         }
         sm.first[node] = acc;
+        sm.above[node] = above;
+        sm.depth[node] = depth;
+        if (depth >= 0 && !position_ok(c, pos + depth)) bad |= LL_CACHE_ERR_POSITION;
+        tc::fence_proxy_async_smem();  // the stage's pages are written behind the decays
+      } else if (w == 0) {
+        float since;
+        block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], sm.after, &since);
+        if (lane == 0) sm.since = since;
       }
-      tc::fence_proxy_async_smem();  // the stage's pages are written behind the weights
       bad = __reduce_or_sync(0xffffffffu, bad);
-      if (lane == 0) sm.bad_tree[w - (kTreeWarps - 2)] = bad;
+      if (lane == 0) sm.bad[w] = bad;
     }
+    cp_async_wait<1>();
+    __syncthreads();
+
     // scores of 16 tokens per warp, K q^T, not yet weighted: step z of 32 columns takes the values 2 z and
     // 2 z + 1 of each thread's 8, of keys and of queries
     if (mine) {
@@ -457,20 +453,18 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       }
     }
   }
-  __syncthreads();
-  unsigned bad = sm.bad_tree[0] | sm.bad_tree[1];
+  unsigned bad = 0;
 #pragma unroll
   for (int i = 0; i <= kTreeWarps; ++i) bad |= sm.bad[i];
   if (bad) {
     if (tid == 0 && speaks) raise(c, bad);
-    if (w == kTreeWarps && lane == 0) {  // the copies on their way
+    if (w == kFiller && lane == 0)  // the copies on their way
       for (int i = 0; i < st; ++i) tc::mbar_wait_short(&sm.full[i], 0);
-    }
     tc::cp_async_wait_all();
     return;
   }
 
-  if (w == kTreeWarps) {
+  if (w == kFiller) {
     if (lane == 0 && k0 < k1) {
       while (m < live) {
         // the last own stage and those behind it have one more release, of what they hold first
@@ -487,61 +481,61 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       }
     }
     __syncwarp();
+    if (Z > 1) {
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+    }
   } else {
     // the weighted scores
     if (mine) {
       const bool nodes = w >= kW / 16;
       const int x0 = 16 * w + lanes_g - (nodes ? kW : 0);  // the thread's tokens: x0 and x0 + 8
-      const int s0 = (j << kLogW) + x0, s1 = s0 + 8;
+      // where they stand
+      const int s0 = nodes ? pos + sm.depth[x0] : (j << kLogW) + x0, s1 = nodes ? pos + sm.depth[x0 + 8] : s0 + 8;
       const float after0 = nodes ? 0.f : sm.after[x0], after1 = nodes ? 0.f : sm.after[x0 + 8];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int q = 8 * t + lanes_i;
+        float f[2][2];  // [node q, q + 1][token x0, x0 + 8]
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {  // node q + u
-          float f0, f1;
+        for (int u = 0; u < 2; ++u) {
+          const int depth = sm.depth[node0 + q + u], tq = pos + depth;
+          const float* lam = lam_s + (q + u) * lay.lp;
           if (nodes) {
             const unsigned long long up = sm.above[node0 + q + u] >> x0;
-            f0 = up & 1 ? wt[(q + u) * kNodes + x0] * sc[t][u] : 0.f;
-            f1 = up >> 8 & 1 ? wt[(q + u) * kNodes + x0 + 8] * sc[t][2 + u] : 0.f;
+            const float* log = wt + (q + u) * kNodes + x0;
+            f[u][0] = up & 1 ? lam[fenwick_level(tq, s0)] * decay<kPage>(log[0]) * sc[t][u] : 0.f;
+            f[u][1] = up >> 8 & 1 ? lam[fenwick_level(tq, s1)] * decay<kPage>(log[8]) * sc[t][2 + u] : 0.f;
           } else {
-            const int depth = sm.depth[node0 + q + u], tq = pos + depth;
             const float first = sm.first[node0 + q + u];
-            const float* lam = lam_s + (q + u) * lay.lp;
-            f0 = depth >= 0 && s0 < pos ? lam[fenwick_level(tq, s0)] * expf(after0 + first) * sc[t][u] : 0.f;
-            f1 = depth >= 0 && s1 < pos ? lam[fenwick_level(tq, s1)] * expf(after1 + first) * sc[t][2 + u] : 0.f;
+            f[u][0] = depth >= 0 && s0 < pos ? lam[fenwick_level(tq, s0)] * decay<kPage>(after0 + first) * sc[t][u] : 0.f;
+            f[u][1] = depth >= 0 && s1 < pos ? lam[fenwick_level(tq, s1)] * decay<kPage>(after1 + first) * sc[t][2 + u] : 0.f;
           }
-          sc[t][u] = f0;
-          sc[t][2 + u] = f1;
         }
-        T* at = ps + q * kPPitch + 16 * w + lanes_g;
+        float* at = ps + q * kPPitch + 16 * w + lanes_g;
 #pragma unroll
-        for (int u = 0; u < 4; u += 2) {  // token x0 + 4 u
-          if constexpr (sizeof(T) == 2) {
-            uint32_t hi, lo;
-            split_bf16(sc[t][u], sc[t][u + 1], hi, lo);
-            at[4 * u] = __ushort_as_bfloat16((unsigned short)hi);
-            at[4 * u + kPPitch] = __ushort_as_bfloat16((unsigned short)(hi >> 16));
-            at[4 * u + NQ * kPPitch] = __ushort_as_bfloat16((unsigned short)lo);
-            at[4 * u + (NQ + 1) * kPPitch] = __ushort_as_bfloat16((unsigned short)(lo >> 16));
+        for (int u = 0; u < 4; ++u) {
+          const float x = f[u & 1][u >> 1];
+          float* p = at + (u & 1) * kPPitch + (u >> 1) * 8;
+          if constexpr (kPage == 1) {
+            *p = __uint_as_float(tf32_of(x));
           } else {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t hi, lo;
-              split_tf32(sc[t][u + y], hi, lo);
-              at[4 * u + y * kPPitch] = __uint_as_float(hi);
-              at[4 * u + (NQ + y) * kPPitch] = __uint_as_float(lo);
-            }
+            uint32_t hi, lo;
+            split_tf32(x, hi, lo);
+            p[0] = __uint_as_float(hi);
+            p[NQ * kPPitch] = __uint_as_float(lo);
           }
         }
       }
     }
-    for (int x = tid; x < live * NQ; x += kConsumerThreads) {
+    for (int x = tid; x < live * NQ; x += kConsumers) {
       const int y = x / NQ, q = x - y * NQ, depth = sm.depth[node0 + q];
       float f = 0.f;
       if (depth >= 0) {
         const int lv = (pos + depth) >> kLogW > j ? max(sm.page_lv[y], to) : sm.page_lv[y];
-        f = lam_s[q * lay.lp + kLogW + 1 + lv] * expf(sm.page_log[y] + sm.since + sm.first[node0 + q]);
+        f = lam_s[q * lay.lp + kLogW + 1 + lv] * decay<kPage>(sm.page_log[y] + sm.since + sm.first[node0 + q]);
       }
       page_w[x] = f;
     }
@@ -552,9 +546,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       constexpr int kWords = 8 * (int)sizeof(T);  // 16-byte pieces that 128 columns have
       const int piece = tid & (kWords - 1), words = min(4, (dv * (int)sizeof(T) - 16 * piece) / 4);
       if (words > 0) {
-        for (int y = r + tid / kWords; y < ((r + 15) & ~15); y += kConsumerThreads / kWords)
+        for (int y = r + tid / kWords; y < ((r + 15) & ~15); y += kConsumers / kWords)
           reinterpret_cast<uint4*>(vs + y * lay.vp)[piece] = make_uint4(0u, 0u, 0u, 0u);
-        for (int y = tid / kWords; y < ((N + 15) & ~15); y += kConsumerThreads / kWords) {
+        for (int y = tid / kWords; y < ((N + 15) & ~15); y += kConsumers / kWords) {
           uint32_t* p = reinterpret_cast<uint32_t*>(vs + (kW + y) * lay.vp) + 4 * piece;
           if (y >= N || sm.up[y] == -2) {
             *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
@@ -571,7 +565,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
         }
       }
     }
-    consumer_sync();  // the tokens' weights and values are there, the tree's weights are done with
+    consumer_sync();  // the tokens' weights and values are there, the tree's decays are done with
     if (lane == 0) tc::mbar_arrive(&sm.empty[a.own - 1]);
 
     // a warp's 16 columns; where there are few, warps share them by tokens and by rows of the pages
@@ -589,58 +583,24 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       for (int tile = sp; tile < tiles; tile += Z) {
         if (tile < kW / 16 && 16 * tile >= r) continue;
         if ((turn++ & (kparts - 1)) != kp) continue;
-        if constexpr (sizeof(T) == 2) {
-          uint32_t va[4];  // columns g and g + 8: set right below
-          ldmatrix_trans(va, vs + (16 * tile + (lane & 7) + ((lane >> 4) << 3)) * lay.vp + 16 * ct + ((lane >> 3) & 1) * 8);
-          const uint32_t at = tc::smem_u32(ps) +
-                              (((lane & 7) + (NT > 1 ? (lane >> 4) << 3 : 0)) * kPPitch + 16 * tile + ((lane >> 3) & 1) * 8) * 2;
 #pragma unroll
-          for (int y = 1; y >= 0; --y) {
-            uint32_t pb[NT][2];
-            if constexpr (NT == 1) {
-              ldmatrix2(pb[0][0], pb[0][1], at + y * NQ * kPPitch * 2);
-            } else {
+        for (int y = 0; y < 2; ++y) {  // 8 tokens: 2 i and 2 i + 1 of each thread
+          const T* v0 = vs + (16 * tile + 8 * y + lanes_i) * lay.vp + col;
+          uint32_t va[kIn][2], vb[kIn][2];  // tokens 2 i and 2 i + 1
+          parts2(v0, va);
+          parts2(v0 + lay.vp, vb);
 #pragma unroll
-              for (int t = 0; t < NT; t += 2)
-                ldmatrix4(pb[t][0], pb[t][1], pb[t + 1][0], pb[t + 1][1], at + (y * NQ + 8 * t) * kPPitch * 2);
-            }
+          for (int t = 0; t < NT; ++t) {
+            const float* p = ps + (8 * t + lanes_g) * kPPitch + 16 * tile + 8 * y + lanes_i;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_bf16(acc[t], va, pb[t][0], pb[t][1]);
-          }
-        } else {
+            for (int x = kPage - 1; x >= 0; --x) {
+              const uint2 b = *reinterpret_cast<const uint2*>(p + x * NQ * kPPitch);
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {  // 8 tokens: 2 i and 2 i + 1 of each thread
-            const float* v0 = reinterpret_cast<const float*>(vs) + (16 * tile + 8 * z + lanes_i) * lay.vp + col;
-            const float2 x0 = *reinterpret_cast<const float2*>(v0), x1 = *reinterpret_cast<const float2*>(v0 + lay.vp);
-            uint32_t hi[4], lo[4];
-            split_tf32(x0.x, hi[0], lo[0]);
-            split_tf32(x0.y, hi[1], lo[1]);
-            split_tf32(x1.x, hi[2], lo[2]);
-            split_tf32(x1.y, hi[3], lo[3]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const float* p = reinterpret_cast<const float*>(ps) + (8 * t + lanes_g) * kPPitch + 16 * tile + 8 * z + lanes_i;
-              const uint2 ph = *reinterpret_cast<const uint2*>(p), pl = *reinterpret_cast<const uint2*>(p + NQ * kPPitch);
-              mma_tf32(acc[t], lo[0], lo[1], lo[2], lo[3], ph.x, ph.y);
-              mma_tf32(acc[t], hi[0], hi[1], hi[2], hi[3], pl.x, pl.y);
-              mma_tf32(acc[t], hi[0], hi[1], hi[2], hi[3], ph.x, ph.y);
+              for (int i = kIn - 1; i >= 0; --i)
+                if (x + i < 2) mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], b.x, b.y);
             }
           }
         }
-      }
-    }
-    if constexpr (sizeof(T) == 2) {  // from columns g and g + 8 of each thread to 2 g and 2 g + 1
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int src = (((2 * lanes_g + (u >> 1)) & 7) << 2) | (lane & 3);
-          const float lo = __shfl_sync(0xffffffffu, acc[t][u & 1], src), hi = __shfl_sync(0xffffffffu, acc[t][2 + (u & 1)], src);
-          y[u] = lanes_g < 4 ? lo : hi;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[t][u] = y[u];
       }
     }
     if (sm.odd && on && kp == 0 && col < dv) {
@@ -656,8 +616,10 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             const int q = 8 * t + lanes_i + (u & 1);
             const float v = u >> 1 ? v1 : v0;
             if (q >= queries || !(sm.above[node0 + q] >> y & 1) || !is_odd(v)) continue;
-            const T* p = ps + q * kPPitch + kW + y;
-            acc[t][u] = fmaf(to_f32(p[0]) + to_f32(p[NQ * kPPitch]), v, acc[t][u]);
+            float f = 0.f;
+#pragma unroll
+            for (int x = kPage - 1; x >= 0; --x) f += ps[(x * NQ + q) * kPPitch + kW + y];
+            acc[t][u] = fmaf(f, v, acc[t][u]);
           }
       }
     }
@@ -737,8 +699,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
     // sums over the warps that share columns, and over the cluster
     const bool pairs = (reinterpret_cast<uintptr_t>(a.out) & (a.out_f32 ? 7u : 3u)) == 0;
     const int64_t out_at = ((first_node + node0) * H + h) * dv;
-    auto put = [&](int t, int ct_, const float (&x)[4]) {
-      const int col_ = 16 * ct_ + 2 * lanes_g;
+    auto put = [&](int t, int tile, const float (&x)[4]) {  // of 16 columns
+      const int col_ = 16 * tile + 2 * lanes_g;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int q = 8 * t + lanes_i + u;
@@ -767,48 +729,38 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       if (on)
 #pragma unroll
         for (int t = 0; t < NT; ++t) put(t, ct, acc[t]);
-    } else {
-      consumer_sync();  // the ring is done with
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        *reinterpret_cast<float4*>(red + ((t * kTreeWarps + w) * 32 + lane) * 4) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-      if (Z == 1) {
-        consumer_sync();
-#pragma unroll 1
-        for (int x = w; x < NT * wide; x += kTreeWarps) {
-          const int t = x >> wide_log, ct_ = x & (wide - 1);
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = 0; p < kparts; ++p)
-            y = add4(y, *reinterpret_cast<const float4*>(red + ((t * kTreeWarps + p * wide + ct_) * 32 + lane) * 4));
-          const float z[4] = {y.x, y.y, y.z, y.w};
-          put(t, ct_, z);
-        }
-      }
+      return;
     }
-    if (Z > 1) {
-      __syncwarp();
+    consumer_sync();  // the ring is done with: [column tile][node tile][warp of the rows][thread]
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      *reinterpret_cast<float4*>(red + (((ct * NT + t) * kparts + kp) * 32 + lane) * 4) =
+          make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    const int sums = NT * wide;
+    if (Z == 1) {
+      consumer_sync();
+#pragma unroll 1
+      for (int x = w; x < sums; x += kTreeWarps) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < kparts; ++p) y = add4(y, *reinterpret_cast<const float4*>(red + ((x * kparts + p) * 32 + lane) * 4));
+        const float z[4] = {y.x, y.y, y.z, y.w};
+        put(x & (NT - 1), x / NT, z);
+      }
+    } else {
       cluster_arrive();
       cluster_wait();
 #pragma unroll 1
-      for (int x = w * Z + sp; x < NT * wide; x += kTreeWarps * Z) {
-        const int t = x >> wide_log, ct_ = x & (wide - 1);
+      for (int x = w * Z + sp; x < sums; x += kTreeWarps * Z) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int z = 0; z < Z; ++z)
-          for (int p = 0; p < kparts; ++p)
-            y = add4(y, load_remote4(red + ((t * kTreeWarps + p * wide + ct_) * 32 + lane) * 4, z));
+          for (int p = 0; p < kparts; ++p) y = add4(y, load_remote4(red + ((x * kparts + p) * 32 + lane) * 4, z));
         const float z[4] = {y.x, y.y, y.z, y.w};
-        put(t, ct_, z);
+        put(x & (NT - 1), x / NT, z);
       }
       __syncwarp();
       cluster_arrive();
       cluster_wait();
     }
-  }
-  if (w == kTreeWarps && Z > 1) {
-    cluster_arrive();
-    cluster_wait();
-    cluster_arrive();
-    cluster_wait();
   }
 }
 
@@ -832,7 +784,7 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   a.box_rows = std::min(col_boxes == 1 ? 128 : col_boxes == 2 ? 64 : 32, share);  // a stage, or a CTA's share
   a.heads = fast_div((uint32_t)c.H);
   a.per_qk = fast_div((uint32_t)(c.H / c.Hqk));
-  const TreeLayout lay = tree_layout<T, NT>(dv, a.N, (int)c.levels);
+  const TreeLayout lay = tree_layout<T, NT, kPage>(dv, a.N, (int)c.levels);
   const size_t own_smem = (sizeof(TreeSmem) + 1023) & ~(size_t)1023;  // the stages begin at a multiple of 1024
   const size_t fixed = own_smem + 1024;                              // (1024 of each CTA are the system's)
   // as many CTAs on an SM as leave the ring three stages, one of them from the start
