@@ -52,7 +52,6 @@ constexpr int kStageBytes = 16384;
 constexpr int kMaxTreeStages = 8;
 constexpr int kTreeSplit = 8;          // CTAs of a cluster
 constexpr int kQPitch = 132;           // floats from query to query
-constexpr int kPPitch = kW + kNodes + 8;  // floats from node to node of the tokens' weights
 
 template <typename T>
 struct Parts {
@@ -63,7 +62,7 @@ __host__ __device__ constexpr int pad4(int x) { return (x + 3) & ~3; }
 // Shared memory behind the ring's own stages, in bytes.  The tokens' weights and values are done with
 // before the pages: whole stages of their place then join the ring.
 struct TreeLayout {
-  int vp, lp;                 // elements from row to row: v, lambda
+  int vp, tp, lp;             // elements from row to row: v, the tokens' weights, lambda
   int p, v, q, lam, pw, end;  // where each begins
 };
 template <typename T, int NT, int kPage>
@@ -71,32 +70,32 @@ __host__ __device__ __forceinline__ TreeLayout tree_layout(int dv, int N, int M)
   const int dv16 = (dv + 15) & ~15, tokens = kW + ((N + 15) & ~15);
   TreeLayout l;
   l.vp = dv16 + (sizeof(T) == 2 ? 8 : 4);  // rows 2 i and 2 i + 1 of four threads fall into banks of their own
+  l.tp = tokens + 8;
   l.lp = pad4(M + kLogW + 1);
   l.p = 0;
-  l.v = l.p + kPage * 8 * NT * kPPitch * 4;
+  l.v = l.p + kPage * 8 * NT * l.tp * 4;
   l.q = l.v + tokens * l.vp * (int)sizeof(T);
   l.lam = l.q + Parts<T>::in * 8 * NT * kQPitch * 4;
-  l.pw = l.lam + 8 * NT * l.lp * 4;
+  l.pw = l.lam + (NT == 8 ? 8 * NT * l.lp * 4 : 0);  // (up to 32 nodes: with the tree's decays)
   l.end = l.pw + M * 8 * NT * 4;
   return l;
 }
 
 // CTAs that registers leave on an SM.
 template <typename T, int NT>
-constexpr int tree_ctas() { return sizeof(T) == 2 ? (NT <= 2 ? 3 : 2) : NT <= 2 ? 2 : 1; }
+constexpr int tree_ctas() { return sizeof(T) == 2 ? (NT <= 4 ? 3 : 2) : NT <= 2 ? 2 : 1; }
 
 struct TreeSmem {
   uint64_t full[kMaxTreeStages], empty[kMaxTreeStages];
   float after[kW];                   // log decay from each token of the block to the context's last
   float first[kNodes];               // log decay of the path to each node
-  float la[kNodes];
   float page_log[kMaxLevels];        // the live pages, lowest level first
   int page_at[kMaxLevels], page_lv[kMaxLevels];
-  int up[kNodes], depth[kNodes];
   unsigned long long above[kNodes];  // nodes on the path, itself included
   float since;
   unsigned bad[kTreeWarps + 1];      // what each warp found
   int odd;                           // a node's v has infinities or NaN
+  signed char up[kNodes], depth[kNodes];
 };
 
 // Of the eight warps that compute, and of the two that have the nodes.
@@ -270,12 +269,13 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
   const int64_t first_node = (int64_t)row * a.N;
   uint8_t* body = dyn + a.own * kStageBytes;
   const TreeLayout lay = tree_layout<T, NT, kPage>(dv, a.N, M);
-  float* ps = reinterpret_cast<float*>(body + lay.p);  // [kPage parts][NQ][kPPitch]
+  float* ps = reinterpret_cast<float*>(body + lay.p);  // [kPage parts][NQ][lay.tp]
   T* vs = reinterpret_cast<T*>(body + lay.v);
   float* qs = reinterpret_cast<float*>(body + lay.q);  // [parts][NQ][kQPitch]; of every 8 columns the even ones, then the odd ones
-  float* lam_s = reinterpret_cast<float*>(body + lay.lam);
   float* page_w = reinterpret_cast<float*>(body + lay.pw);
   float* wt = reinterpret_cast<float*>(dyn + (a.own - 1) * kStageBytes);  // log decays of the tree, in the last own stage until the pages need it
+  float* lam_s = NT == 8 ? reinterpret_cast<float*>(body + lay.lam) : wt + NQ * kNodes;
+  float* la_s = ps;                                                          // the nodes' log a, until their weights are there
   float* red = reinterpret_cast<float*>(dyn);                               // the ring, behind the pages
 
   // geometry of the pages: col_boxes boxes of 32 columns, the rows in stages of box_rows
@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       unsigned bad = 0;
       if (node >= 0) {  // the nodes' paths, and the log decays along those of the queries
         const bool fine = up < node && up >= -2;
-        sm.up[node] = up = fine ? up : -2;
-        sm.la[node] = up != -2 ? la : 0.f;
+        up = fine ? up : -2;
+        sm.up[node] = (signed char)up;
+        la_s[node] = up != -2 ? la : 0.f;
         walkers_sync();
         if (!fine) bad = LL_CACHE_ERR_TREE;
         unsigned long long above = 0;
@@ -406,13 +407,12 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
           ++depth;
           if (sm.up[x] == -2) bad = LL_CACHE_ERR_TREE;  // a child of a node that is left out
           if (asks) wt[q * kNodes + x] = acc;
-          acc += sm.la[x];
+          acc += la_s[x];
         }
         sm.first[node] = acc;
         sm.above[node] = above;
-        sm.depth[node] = depth;
+        sm.depth[node] = (signed char)depth;
         if (depth >= 0 && !position_ok(c, pos + depth)) bad |= LL_CACHE_ERR_POSITION;
-        tc::fence_proxy_async_smem();  // the stage's pages are written behind the decays
       } else if (w == 0) {
         float since;
         block_decays(c.win_log_a + ((int64_t)s * H + h) * kW, r, c.page_from[s * 2 + par], sm.after, &since);
@@ -514,18 +514,18 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             f[u][1] = depth >= 0 && s1 < pos ? lam[fenwick_level(tq, s1)] * decay<kPage>(after1 + first) * sc[t][2 + u] : 0.f;
           }
         }
-        float* at = ps + q * kPPitch + 16 * w + lanes_g;
+        float* at = ps + q * lay.tp + 16 * w + lanes_g;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float x = f[u & 1][u >> 1];
-          float* p = at + (u & 1) * kPPitch + (u >> 1) * 8;
+          float* p = at + (u & 1) * lay.tp + (u >> 1) * 8;
           if constexpr (kPage == 1) {
             *p = __uint_as_float(tf32_of(x));
           } else {
             uint32_t hi, lo;
             split_tf32(x, hi, lo);
             p[0] = __uint_as_float(hi);
-            p[NQ * kPPitch] = __uint_as_float(lo);
+            p[NQ * lay.tp] = __uint_as_float(lo);
           }
         }
       }
@@ -565,6 +565,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
         }
       }
     }
+    tc::fence_proxy_async_smem();  // the pages are written behind what the last own stage holds
     consumer_sync();  // the tokens' weights and values are there, the tree's decays are done with
     if (lane == 0) tc::mbar_arrive(&sm.empty[a.own - 1]);
 
@@ -591,10 +592,10 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
           parts2(v0 + lay.vp, vb);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float* p = ps + (8 * t + lanes_g) * kPPitch + 16 * tile + 8 * y + lanes_i;
+            const float* p = ps + (8 * t + lanes_g) * lay.tp + 16 * tile + 8 * y + lanes_i;
 #pragma unroll
             for (int x = kPage - 1; x >= 0; --x) {
-              const uint2 b = *reinterpret_cast<const uint2*>(p + x * NQ * kPPitch);
+              const uint2 b = *reinterpret_cast<const uint2*>(p + x * NQ * lay.tp);
 #pragma unroll
               for (int i = kIn - 1; i >= 0; --i)
                 if (x + i < 2) mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], b.x, b.y);
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             if (q >= queries || !(sm.above[node0 + q] >> y & 1) || !is_odd(v)) continue;
             float f = 0.f;
 #pragma unroll
-            for (int x = kPage - 1; x >= 0; --x) f += ps[(x * NQ + q) * kPPitch + kW + y];
+            for (int x = kPage - 1; x >= 0; --x) f += ps[(x * NQ + q) * lay.tp + kW + y];
             acc[t][u] = fmaf(f, v, acc[t][u]);
           }
       }
