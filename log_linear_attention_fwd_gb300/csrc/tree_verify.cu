@@ -38,13 +38,12 @@ constexpr Mass kOne = 1ull << kFraction;
 // x in [0, 1] (below and NaN: 0, above: 1) as fixed point, to the nearest, plus kBias.  A sum with 8
 // has x's first 20 fractional bits as its last ones, and what is left plus 2^-20 the next 23.
 constexpr Mass kBias = ((Mass)0x41000000u << 23) + 0x35800000u;
-__device__ __forceinline__ Mass biased_mass(float x) {
-  x = __saturatef(x);
+__device__ __forceinline__ Mass biased_mass(float x) {  // x in [0, 1]
   const float hi = __fadd_rz(x, 8.f);
   const float lo = __fadd_rn(__fsub_rn(x, __fsub_rn(hi, 8.f)), 0x1p-20f);
   return (Mass)__float_as_uint(hi) * (1u << 23) + __float_as_uint(lo);
 }
-__device__ __forceinline__ Mass to_mass(float x) { return biased_mass(x) - kBias; }
+__device__ __forceinline__ Mass to_mass(float x) { return biased_mass(__saturatef(x)) - kBias; }
 // floor(s x), x as above, for s < 2^62.
 __device__ __forceinline__ Mass mass_times(Mass s, float x) {
   const unsigned b = __float_as_uint(__saturatef(x)), m = (b & 0x7fffffu) | 0x800000u;
@@ -77,19 +76,31 @@ struct Vec {
   }
 };
 
-// What is drawn from: P alone (kPlain), max(P - Q, 0) (kFirst) or max(P - S Q, 0) (kMore).
+// What is drawn from: P alone (kPlain), max(P - Q, 0) (kFirst) or max(P - S Q, 0) (kMore), added to sum.
 enum Kind { kPlain, kFirst, kMore };
 template <int kKind>
+__device__ __forceinline__ void add_rest(Mass& sum, float p, float q, Mass S) {
+  if (kKind == kPlain) {
+    sum += to_mass(p);
+  } else if (kKind == kFirst) {  // (the biases cancel; rounding keeps the order)
+    p = __saturatef(p);
+    q = __saturatef(q);
+    if (p > q) sum += biased_mass(p) - biased_mass(q);
+  } else {
+    sum += less(to_mass(p), mass_times(S, q));
+  }
+}
+template <int kKind>
 __device__ __forceinline__ Mass rest_of(float p, float q, Mass S) {
-  if (kKind == kPlain) return to_mass(p);
-  if (kKind == kFirst) return less(biased_mass(p), biased_mass(q));
-  return less(to_mass(p), mass_times(S, q));
+  Mass sum = 0;
+  add_rest<kKind>(sum, p, q, S);
+  return sum;
 }
 
 // The calling warp's sum over [lo, hi) of a row.  vec: the two rows lie alike to 16 bytes, `off` elements behind one.
 template <typename T, int kKind>
 __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int64_t hi, bool vec, int off, Mass S) {
-  constexpr int n = Vec<T>::n, kFlight = 4;
+  constexpr int n = Vec<T>::n, kFlight = kKind == kPlain ? 8 : 4;  // 8 loads of a thread on their way
   const int lane = threadIdx.x & 31;
   int64_t a = hi, b = hi;  // whole vectors: [a, b)
   if (vec) {
@@ -97,7 +108,7 @@ __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int6
     b = max(a, ((hi + off) & ~(int64_t)(n - 1)) - off);
   }
   Mass sum = 0;
-  auto one = [&](int64_t x) { sum += rest_of<kKind>(to_f32(P[x]), kKind == kPlain ? 0.f : to_f32(Q[x]), S); };
+  auto one = [&](int64_t x) { add_rest<kKind>(sum, to_f32(P[x]), kKind == kPlain ? 0.f : to_f32(Q[x]), S); };
 #pragma unroll 1
   for (int64_t x = lo + lane; x < a; x += 32) one(x);
 #pragma unroll 1
@@ -117,7 +128,7 @@ __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int6
 #pragma unroll
     for (int u = 0; u < kFlight; ++u)
 #pragma unroll
-      for (int i = 0; i < n; ++i) sum += rest_of<kKind>(p[u].at(i), kKind == kPlain ? 0.f : q[u].at(i), S);
+      for (int i = 0; i < n; ++i) add_rest<kKind>(sum, p[u].at(i), kKind == kPlain ? 0.f : q[u].at(i), S);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -257,7 +268,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
           const float t = u * q, e = fmaf(u, q, -t), sp = __saturatef(p);
           ok = t < sp || (t == sp && e < 0.f);
         } else {
-          const Mass R = S == kOne ? less(biased_mass(p), biased_mass(q)) : less(to_mass(p), mass_times(S, q));
+          const Mass R = S == kOne ? rest_of<kFirst>(p, q, S) : rest_of<kMore>(p, q, S);
           ok = mass_times(mass_times(Z, q), u) < R;
         }
         if (!ok) {
