@@ -138,8 +138,8 @@ __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int6
 struct VerifySmem {
   int up[kNodes], tok[kNodes];
   float px[kNodes], qx[kNodes], us[kNodes];
-  Mass warp_sum[kVerifyWarps], scan[kVerifyWarps];
-  Mass cta_sum[2][kVerifySplit];  // of the cluster's CTAs, by turns
+  Mass warp_sum[2][kVerifyWarps], scan[kVerifyWarps];  // warp_sum, cta_sum: by turns, as a warp may be
+  Mass cta_sum[2][kVerifySplit];                       // at the next pass while another reads the last one's
 };
 
 __device__ __forceinline__ void store_remote(Mass* p, uint32_t rank, Mass v) {
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   auto run_at = [&](int64_t k, int off) { return k <= 0 ? 0 : k >= runs ? V : min(V, k * len - off); };
   int passes = 0;
   Mass total = 0, before = 0;  // of the last pass: of all, and of the CTAs before this one
+  Mass* warp_sum = nullptr;    // and of this one's warps
   unsigned long long gone = 0;  // rejected children (drafts that were given), one per token
   bool waited = C == 1;
   auto place = [&](const T* P, const T* Q, int* off) {  // how the rows lie
@@ -218,10 +219,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
         const int i = __ffsll(g) - 1;
         if (sm.tok[i] >= lo && sm.tok[i] < hi) sum -= to_mass(sm.px[i]);
       }
-    if (lane == 0) sm.warp_sum[w] = sum;
+    warp_sum = sm.warp_sum[passes & 1];
+    if (lane == 0) warp_sum[w] = sum;
     __syncthreads();
     Mass mine = 0;
-    for (int i = 0; i < kVerifyWarps; ++i) mine += sm.warp_sum[i];
+    for (int i = 0; i < kVerifyWarps; ++i) mine += warp_sum[i];
     total = mine;
     before = 0;
     if (C > 1) {
@@ -306,11 +308,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   if (total == 0) return;
   Mass target = min(mass_times(total, sm.us[0]), total - 1);
   Mass mine = 0;
-  for (int i = 0; i < kVerifyWarps; ++i) mine += sm.warp_sum[i];
+  for (int i = 0; i < kVerifyWarps; ++i) mine += warp_sum[i];
   if (target < before || target - before >= mine) return;  // another CTA's
   target -= before;
   int run = 0;
-  while (target >= sm.warp_sum[run]) target -= sm.warp_sum[run++];  // (ends: target is below their sum)
+  while (target >= warp_sum[run]) target -= warp_sum[run++];  // (ends: target is below their sum)
   const T* P = P0 + cur * V;
   const T* Q = plain || !Q0 || S == 0 ? nullptr : Q0 + cur * V;
   int off;
