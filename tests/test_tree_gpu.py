@@ -3,9 +3,9 @@ its drafts and the appending of the accepted path, against fp64.
 
 Tolerances as for the cache's step (tests/test_cache_gpu.py): fp32 outputs are sums of up to
 a few hundred products of fp32 values whose decays are off by a few 2^-24, rel-L2 below 1e-5.  With bf16
-caches the tokens are exact inputs, but a token's weight enters its product as two bf16 parts, off by
-2^-17 of it: with fp32 outputs another 2^-15 of the scale.  bf16 outputs add their half step, 2^-8 of each
-value, and the half step of tf32 at which the pages are read, 2^-11 of each product: the signs
+caches the tokens are exact inputs, but a token's weight and a page's value enter their products as two tf32
+parts, off by 2^-22: with fp32 outputs another 2^-20 of the scale.  bf16 outputs add their half step, 2^-8 of
+each value, and the half step of tf32 at which weights and pages are read, 2^-11 of each product: the signs
 are random, so the outputs' rms is the root of the products' sum of squares, and the sum of their
 magnitudes is at most sqrt(n) of that, n < 1024 products (4 pages of 128 rows and the tokens): 32 rms.
 Tokens, paths and tables are equal.
@@ -20,7 +20,7 @@ from tests.helpers import TOL_F32, rel_l2, to64
 from tests.test_cache_gpu import DT, i32, invariants, poison, same, snapshot
 
 pytestmark = pytest.mark.gpu
-TWO_PARTS, ONE_PART = 2.0 ** -15, 2.0 ** -11
+TWO_PARTS, ONE_PART = 2.0 ** -20, 2.0 ** -11
 
 
 @pytest.fixture(scope="module")
@@ -119,6 +119,112 @@ def test_more_items_than_sms(LL, n, H, Hqk, N, dtype):
         else:
             check(out[r], want[p], dtype == "bf16")
     assert cache.error() == 0
+
+
+@pytest.mark.parametrize("N", [5, 33, 64])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_deep_caches(LL, dtype, N):
+    """All 24 levels and positions near 2^29, from random states: chains over a block's end, then accepted."""
+    H, Hqk, dk, dv, M = 2, 1, 16, 12, 24
+    pos = [(1 << 29) + (1 << 20) + 37 - 64 * i for i in range(2)] + [(64 << M) - 1 - N, (1 << 29) - 2]
+    n, L, g = len(pos), M + 7, torch.Generator().manual_seed(N)
+    rand = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    cache = poison(LL.LogLinearCache.empty(n, 25 * n, H, dk, dv, M, Hqk=Hqk, dtype=DT[dtype]))
+    x = {"q": rand(n, N, Hqk, dk) / 4, "k": rand(n, N, Hqk, dk) / 4, "v": rand(n, N, H, dv)}
+    wk, wv = (rand(n, 64, Hqk, dk) / 4).to(DT[dtype]), rand(n, 64, H, dv).to(DT[dtype])
+    x = {k: t.to(DT[dtype]).cuda() for k, t in x.items()}
+    x["log_a"], x["lam"] = (-0.05 * torch.rand(n, N, H, generator=g)).cuda(), torch.rand(n, N, H, L, generator=g).cuda()
+    wa = -0.05 * torch.rand(n, 64, H, generator=g)
+    state = torch.zeros(n, H, L, dk, dv)
+    for r, t in enumerate(pos):
+        for m in range(M):
+            if t >> 6 >> m & 1:
+                state[r, :, 7 + m] = rand(H, dk, dv)
+        if t & 63:
+            LL.loglinear_cache_load(cache, i32([r]), t, state[r:r + 1].cuda(), wk[r:r + 1, 64 - t % 64:].cuda().contiguous(),
+                                    wv[r:r + 1, 64 - t % 64:].cuda().contiguous(), wa[r:r + 1, 64 - t % 64:].cuda().contiguous())
+    chain = [[i - 1 for i in range(N)]] * n
+    want = np.zeros((n, N, H, dv))
+    for r, t0 in enumerate(pos):
+        held, j = t0 % 64, t0 // 64
+        keys = torch.cat([wk[r, 64 - held:], x["k"][r].cpu()]).double().numpy()
+        vals = torch.cat([wv[r, 64 - held:], x["v"][r].cpu()]).double().numpy()
+        logs = torch.cat([wa[r, 64 - held:], x["log_a"][r].cpu()]).double().numpy()
+        S, lam, q = to64(state[r]), to64(x["lam"][r].cpu()), to64(x["q"][r].cpu())
+        for i in range(N):
+            t, last = t0 + i, held + i
+            for h in range(H):
+                # a prompt's states are as they are at its last position
+                acc = 0.0
+                back = logs[:, h].copy()
+                since = back[held:last + 1].sum()
+                to = ((t // 64) & -(t // 64)).bit_length() - 1 if t // 64 > j else 0
+                for m in range(M):
+                    if j >> m & 1:
+                        acc = acc + lam[i, h, 7 + max(m, to)] * np.exp(since) * (q[i, 0] @ S[h, 7 + m])
+                for s in range(last + 1):
+                    w = lam[i, h, oracle.level(t, 64 * j + s)] * np.exp(back[s + 1:last + 1].sum()) * (keys[s, 0] @ q[i, 0])
+                    acc = acc + w * vals[s, h]
+                want[r, i, h] = acc
+    for odt in (torch.float32, torch.bfloat16):
+        got = attend(LL, cache, list(range(n)), pos, chain, x, out_dtype=odt).cpu()
+        for r in range(n):
+            check(got[r], want[r], dtype == "bf16")
+    assert cache.error() == 0
+    # the first half accepted, the second half's nodes behind them: as before
+    half = (N + 1) // 2
+    new = LL.loglinear_cache_accept(cache, i32(list(range(n))), i32(pos), i32([list(range(half)) + [-1]] * n), x["k"], x["v"], x["log_a"])
+    assert new.tolist() == [p + half for p in pos] and cache.error() == 0
+    rest = {k: t[:, half:].contiguous() for k, t in x.items()}
+    got = attend(LL, cache, list(range(n)), new.tolist(), [[i - 1 for i in range(N - half)]] * n, rest, out_dtype=torch.float32).cpu()
+    for r in range(n):
+        check(got[r], want[r, half:], dtype == "bf16")
+    assert cache.error() == 0
+
+
+def test_pages_past_32_bits(LL):
+    """Pages, keys and values whose offsets in elements pass 2^32: low pages taken, high slots."""
+    H, Hqk, d, M, slots = 16, 16, 128, 3, 33000
+    n_pages = 16600                                            # of 2^18 elements
+    cache = LL.LogLinearCache.empty(slots, n_pages, H, d, d, M, Hqk=Hqk)
+    low = n_pages - 6
+    assert low * H * d * d > 2 ** 32 and (slots - 2) * H * 64 * d > 2 ** 32
+    cache.refcount[:low] = 1
+    N, pos, s = 9, [120, 186], [slots - 1, slots - 2]
+    ctx, tree = [], []
+    for i, T in enumerate(pos):
+        x = W.make_fwd_inputs(W.FwdConfig("c", 1, H, T + N, d, d, 16, M + 7, "bf16", True, "softplus", seed=i, Hqk=Hqk))
+        ctx.append({k: x[k][0, :T] for k in ("k", "v", "log_a")})
+        tree.append({k: x[k][0, T:] for k in ("q", "k", "v", "log_a", "lam")})
+        c = {k: v[:, :T].cuda().contiguous() for k, v in x.items()}
+        _, state = LL.loglinear_prefill(c["q"].float(), c["k"].float(), c["v"].float(), c["log_a"], c["lam"], 16, path="simt")
+        LL.loglinear_cache_load(cache, i32([s[i]]), T, state, c["k"][:, -64:], c["v"][:, -64:], c["log_a"][:, -64:])
+    x = {k: torch.stack([t[k] for t in tree]).cuda().contiguous() for k in tree[0]}
+    chain = [[i - 1 for i in range(N)]] * 2
+    want = [oracle.tree_attention(c, t, p) for c, t, p in zip(ctx, tree, chain)]
+    got = attend(LL, cache, s, pos, chain, x, out_dtype=torch.float32).cpu()
+    for r in range(2):
+        check(got[r], want[r], True)
+    new = LL.loglinear_cache_accept(cache, i32(s), i32(pos), i32([list(range(8))] * 2), x["k"], x["v"], x["log_a"])
+    assert new.tolist() == [128, 194] and cache.error() == 0
+    assert min(cache.page_table[s[0]].max().item(), cache.page_table[s[1]].max().item()) >= low
+    last = {k: t[:, 8:].contiguous() for k, t in x.items()}
+    got = attend(LL, cache, s, new.tolist(), [[-1]] * 2, last, out_dtype=torch.float32).cpu()
+    for r in range(2):
+        check(got[r], want[r][8:], True)
+
+
+def test_no_rows(LL):
+    cache = LL.LogLinearCache.empty(2, 2, 2, 16, 8, 2)
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt).cuda()  # noqa: E731
+    none = i32([])
+    k, v, la = z(0, 3, 2, 16), z(0, 3, 2, 8), z(0, 3, 2, dt=torch.float32)
+    empty = torch.zeros(0, 3, dtype=torch.int32).cuda()
+    assert LL.loglinear_cache_tree(cache, none, none, empty, k, k, v, la, z(0, 3, 2, 9, dt=torch.float32)).shape == (0, 3, 2, 8)
+    assert LL.loglinear_cache_accept(cache, none, none, empty, k, v, la).shape == (0,)
+    path, count, token = LL.loglinear_tree_verify(empty, empty, z(0, 3, 5), z(0, 3, dt=torch.float32))
+    assert path.shape == (0, 3) and count.shape == token.shape == (0,)
+    assert cache.error() == 0 and LL.device_error() == 0
 
 
 def test_a_tree_of_one_is_a_step(LL):
