@@ -138,6 +138,8 @@ __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int6
 struct VerifySmem {
   int up[kNodes], tok[kNodes];
   float px[kNodes], qx[kNodes], us[kNodes];
+  Mass rest[kNodes];         // drafts that were given: R of a child at its turn
+  unsigned first[2], ok[2];  // theirs, a bit per node: no earlier sibling has its token; accepted at its turn
   Mass warp_sum[2][kVerifyWarps], scan[kVerifyWarps];  // warp_sum, cta_sum: by turns, as a warp may be
   Mass cta_sum[2][kVerifySplit];                       // at the next pass while another reads the last one's
 };
@@ -148,16 +150,21 @@ __device__ __forceinline__ void store_remote(Mass* p, uint32_t rank, Mass v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
 
-// grid: row, CTA of its cluster (fastest).
-template <typename T>
+// As cluster_arrive, but orders no memory.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+// grid: row, CTA of its cluster (fastest).  kDrawn: with the draft's distributions.
+template <typename T, bool kDrawn>
 __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyArgs a) {
   __shared__ VerifySmem sm;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, N = a.N;
   const int C = a.split, rank = blockIdx.x % C;
   const int64_t V = a.V, row = blockIdx.x / C;
   const T* P0 = static_cast<const T*>(a.probs) + row * N * V;
-  const T* Q0 = a.draft ? static_cast<const T*>(a.draft) + row * N * V : nullptr;
-  if (C > 1) cluster_arrive();  // this CTA is there
+  const T* Q0 = kDrawn ? static_cast<const T*>(a.draft) + row * N * V : nullptr;
+  if (C > 1) cluster_arrive_relaxed();  // this CTA is there
   bool bad = false;
   if (tid < kNodes) {
     int up = -2, x = 0;
@@ -173,12 +180,32 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
     sm.tok[tid] = x;
     if (up >= 0) {
       sm.px[tid] = to_f32(P0[up * V + x]);
-      if (Q0) sm.qx[tid] = to_f32(Q0[up * V + x]);
+      if (kDrawn) sm.qx[tid] = to_f32(Q0[up * V + x]);
     }
   }
   __syncthreads();
-  if (tid < kNodes && sm.up[tid] >= 0) bad |= sm.up[sm.up[tid]] == -2;
+  // drafts that were given: a child's turn comes when all earlier siblings have been rejected, so R and Z there
+  // are known from the start: R is 0 where one of those has its token, Z what their R leave
+  int up = -2;
+  if (tid < kNodes) {
+    up = sm.up[tid];
+    if (up >= 0) bad |= sm.up[up] == -2;
+    if (!kDrawn) {
+      const int x = sm.tok[tid];
+      bool first = up >= 0;
+      for (int i = 0; i < tid; ++i) first &= sm.up[i] != up || sm.tok[i] != x;
+      sm.rest[tid] = first ? to_mass(sm.px[tid]) : 0;
+      const unsigned mask = __ballot_sync(0xffffffffu, first);
+      if (lane == 0) sm.first[w] = mask;
+    }
+  }
   bad = __syncthreads_or(bad);
+  if (!kDrawn && tid < kNodes) {
+    Mass before = 0;
+    for (int i = 0; i < tid; ++i) before += sm.up[i] == up ? sm.rest[i] : 0;
+    const unsigned mask = __ballot_sync(0xffffffffu, up >= 0 && mass_times(less(kOne, before), sm.us[tid]) < sm.rest[tid]);
+    if (lane == 0) sm.ok[w] = mask;
+  }
   int* path = a.path + row * N;
   if (rank == 0 && tid == 0) a.token[row] = -1;  // (the clusters' barriers order it before the token itself)
   if (bad || sm.up[0] != -1) {
@@ -207,14 +234,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   };
   auto pass = [&](Mass S, bool plain) {
     const T* P = P0 + cur * V;
-    const T* Q = plain || !Q0 || S == 0 ? nullptr : Q0 + cur * V;
+    const T* Q = plain || !kDrawn || S == 0 ? nullptr : Q0 + cur * V;
     int off;
     const bool vec = place(P, Q, &off);
     const int64_t k = (int64_t)rank * kVerifyWarps + w, lo = run_at(k, off), hi = run_at(k + 1, off);
-    Mass sum = !Q          ? sum_run<T, kPlain>(P, Q, lo, hi, vec, off, S)
-               : S == kOne ? sum_run<T, kFirst>(P, Q, lo, hi, vec, off, S)
-                           : sum_run<T, kMore>(P, Q, lo, hi, vec, off, S);
-    if (!plain)
+    Mass sum = !kDrawn || !Q ? sum_run<T, kPlain>(P, Q, lo, hi, vec, off, S)
+               : S == kOne   ? sum_run<T, kFirst>(P, Q, lo, hi, vec, off, S)
+                             : sum_run<T, kMore>(P, Q, lo, hi, vec, off, S);
+    if (!kDrawn && !plain)
       for (unsigned long long g = gone; g; g &= g - 1) {
         const int i = __ffsll(g) - 1;
         if (sm.tok[i] >= lo && sm.tok[i] < hi) sum -= to_mass(sm.px[i]);
@@ -247,51 +274,43 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   if (rank == 0 && tid == 0) path[0] = 0;
   Mass S = 0, Z = kOne;
   const int up0 = sm.up[lane], up1 = sm.up[lane + 32];
+  if (!kDrawn) __syncthreads();
+  const unsigned long long ok_of = kDrawn ? 0 : sm.ok[0] | (unsigned long long)sm.ok[1] << 32;
   for (;;) {
     unsigned long long kids = __ballot_sync(0xffffffffu, up0 == cur) |
                               (unsigned long long)__ballot_sync(0xffffffffu, up1 == cur) << 32;
-    bool moved = false;
-    for (; kids && !moved; kids &= kids - 1) {
+    int next = -1;
+    if (!kDrawn) {
+      if (kids & ok_of) next = __ffsll(kids & ok_of) - 1;
+      else gone = kids & (sm.first[0] | (unsigned long long)sm.first[1] << 32);
+    }
+    for (; kDrawn && kids && next < 0; kids &= kids - 1) {
       const int i = __ffsll(kids) - 1;
-      const float p = sm.px[i], u = sm.us[i];
+      const float p = sm.px[i], u = sm.us[i], q = __saturatef(sm.qx[i]);
       bool ok;
-      if (!Q0) {
-        bool left = true;
-        for (unsigned long long g = gone; g; g &= g - 1) left &= sm.tok[__ffsll(g) - 1] != sm.tok[i];
-        const Mass R = left ? to_mass(p) : 0;
-        ok = mass_times(Z, u) < R;
-        if (!ok && left) {
-          Z = less(Z, R);
-          gone |= 1ull << i;
-        }
+      if (S == 0) {  // exactly: the product's rounding error decides where it is p
+        const float t = u * q, e = fmaf(u, q, -t), sp = __saturatef(p);
+        ok = t < sp || (t == sp && e < 0.f);
       } else {
-        const float q = __saturatef(sm.qx[i]);
-        if (S == 0) {  // exactly: the product's rounding error decides where it is p
-          const float t = u * q, e = fmaf(u, q, -t), sp = __saturatef(p);
-          ok = t < sp || (t == sp && e < 0.f);
-        } else {
-          const Mass R = S == kOne ? rest_of<kFirst>(p, q, S) : rest_of<kMore>(p, q, S);
-          ok = mass_times(mass_times(Z, q), u) < R;
-        }
-        if (!ok) {
-          S += Z;
-          pass(S, false);
-          Z = total;
-          passed = cur;
-        }
+        const Mass R = S == kOne ? rest_of<kFirst>(p, q, S) : rest_of<kMore>(p, q, S);
+        ok = mass_times(mass_times(Z, q), u) < R;
       }
       if (ok) {
-        cur = i;
-        S = 0;
-        Z = kOne;
-        gone = 0;
-        passed = -1;
-        if (rank == 0 && tid == 0) path[count] = i;
-        ++count;
-        moved = true;
+        next = i;
+      } else {
+        S += Z;
+        pass(S, false);
+        Z = total;
+        passed = cur;
       }
     }
-    if (!moved) break;
+    if (next < 0) break;
+    cur = next;
+    S = 0;
+    Z = kOne;
+    passed = -1;
+    if (rank == 0 && tid == 0) path[count] = cur;
+    ++count;
   }
   if (rank == 0) {
     if (tid >= count && tid < N) path[tid] = -1;
@@ -314,7 +333,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   int run = 0;
   while (target >= warp_sum[run]) target -= warp_sum[run++];  // (ends: target is below their sum)
   const T* P = P0 + cur * V;
-  const T* Q = plain || !Q0 || S == 0 ? nullptr : Q0 + cur * V;
+  const T* Q = plain || !kDrawn || S == 0 ? nullptr : Q0 + cur * V;
   int off;
   place(P, Q, &off);
   const int64_t k = (int64_t)rank * kVerifyWarps + run, lo = run_at(k, off), hi = run_at(k + 1, off);
@@ -322,8 +341,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   const int64_t from = min(hi, lo + tid * each), to = min(hi, from + each);
   auto mass_at = [&](int64_t x) -> Mass {
     const float p = to_f32(P[x]);
-    if (Q) return S == kOne ? rest_of<kFirst>(p, to_f32(Q[x]), S) : rest_of<kMore>(p, to_f32(Q[x]), S);
-    if (!plain)
+    if (kDrawn && Q) return S == kOne ? rest_of<kFirst>(p, to_f32(Q[x]), S) : rest_of<kMore>(p, to_f32(Q[x]), S);
+    if (!kDrawn && !plain)
       for (unsigned long long g = gone; g; g &= g - 1)
         if (sm.tok[__ffsll(g) - 1] == x) return 0;
     return to_mass(p);
@@ -353,7 +372,7 @@ cudaError_t launch(VerifyArgs a, int n, cudaStream_t s) {
   // CTAs per row: doubled while all of them run at once (four to an SM) and each has 2048 values
   a.split = 1;
   while (a.split < kVerifySplit && (int64_t)n * a.split * 2 <= 4 * sm_count() && a.V >= (int64_t)4096 * a.split) a.split *= 2;
-  return launch_following(false, tree_verify_kernel<T>, dim3((unsigned)n * a.split), kVerifyThreads, 0, a.split, s, a);
+  return launch_following(false, a.draft ? tree_verify_kernel<T, true> : tree_verify_kernel<T, false>, dim3((unsigned)n * a.split), kVerifyThreads, 0, a.split, s, a);
 }
 
 }  // namespace
