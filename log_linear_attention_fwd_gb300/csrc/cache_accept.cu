@@ -158,7 +158,7 @@ __device__ __forceinline__ void put_keys(const ll_cache& c, const AcceptArgs& a,
 // parts, as in the step; else fp32 multiply-adds.  Tokens of the next block replace those that the fold reads: a head's own
 // values behind its own reads, the keys that heads share by the row's last CTA to have read them.
 template <typename T, bool kMma>
-__global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll_cache c, AcceptArgs a) {
+__global__ void __launch_bounds__(kAcceptThreads, kMma ? 4 : 2) accept_kernel(ll_cache c, AcceptArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ __align__(8) float tok[kW];
   __shared__ float page_e[kMaxLevels];
@@ -251,12 +251,41 @@ __global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll
   float* D = c.pages + ((int64_t)page_at[to] * H + h) * size;
   auto page = [&](int m) { return c.pages + ((int64_t)page_at[m] * H + h) * size; };
   if constexpr (kMma) {
-    // first the pages' sum, to the new page, whose L2 lines the products then pick up: fragments of 32
-    // bytes per row would take HBM three times as long
+    // first the tokens' products, to the new page, then the pages are added to what its L2 lines hold: fragments of
+    // the pages, 32 bytes per row, would take HBM three times as long
+    tc::cp_async_wait_all();
+    __syncthreads();
+    const int g = lane >> 2, i = 2 * (lane & 3);
+    const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
+    for (int nt = w; nt < dv / 8; nt += kAcceptWarps) {
+      uint32_t b[kW / 16][3][2];
+      load_decayed(b, vs + 8 * nt, tok, vp);
+      // two row tiles at a time
+      for (int d = 0; d < dk; d += 32) {
+        float f[2][4] = {};
+#pragma unroll
+        for (int v = 2; v >= 0; --v)
+#pragma unroll
+          for (int q = 0; q < kW / 16; ++q)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              uint32_t ka[4];  // (past the last row: of others, not stored)
+              ldmatrix_trans(ka, ks + (16 * q + mrow) * kp + min(d + 16 * z, dk - 16) + mcol);
+              mma_bf16(f[z], ka, b[q][v][0], b[q][v][1]);
+            }
+        const int64_t at = (int64_t)(d + g) * dv + 8 * nt + i;  // rows g, g + 8, g + 16, g + 24
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (d + 8 * u < dk)
+            *reinterpret_cast<float2*>(D + at + 8 * u * dv) = make_float2(f[u >> 1][2 * (u & 1)], f[u >> 1][2 * (u & 1) + 1]);
+      }
+    }
+    if (to) __syncthreads();
     for (int i0 = tid; to && i0 < size / 4; i0 += 4 * kAcceptThreads) {
       float4 v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kAcceptThreads < size / 4) v[u] = __ldcg(reinterpret_cast<const float4*>(D) + i0 + u * kAcceptThreads);
       for (int m = 0; m < to; m += kTogether) {
         float4 y[kTogether][4];
 #pragma unroll
@@ -274,41 +303,6 @@ __global__ void __launch_bounds__(kAcceptThreads, kMma ? 3 : 2) accept_kernel(ll
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (i0 + u * kAcceptThreads < size / 4) reinterpret_cast<float4*>(D)[i0 + u * kAcceptThreads] = v[u];
-    }
-    tc::cp_async_wait_all();
-    __syncthreads();
-  }
-  if constexpr (kMma) {
-    const int g = lane >> 2, i = 2 * (lane & 3);
-    const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = ((lane >> 3) & 1) << 3;
-    for (int nt = w; nt < dv / 8; nt += kAcceptWarps) {
-      uint32_t b[kW / 16][3][2];
-      load_decayed(b, vs + 8 * nt, tok, vp);
-      // two row tiles at a time
-      for (int d = 0; d < dk; d += 32) {
-        const int64_t at = (int64_t)(d + g) * dv + 8 * nt + i;
-        float2 x[4];  // rows g, g + 8, g + 16, g + 24
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (to && d + 8 * u < dk) x[u] = __ldcg(reinterpret_cast<const float2*>(D + at + 8 * u * dv));
-        float f[2][4] = {{x[0].x, x[0].y, x[1].x, x[1].y}, {x[2].x, x[2].y, x[3].x, x[3].y}};
-#pragma unroll
-        for (int v = 2; v >= 0; --v)
-#pragma unroll
-          for (int q = 0; q < kW / 16; ++q)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              uint32_t ka[4];  // (past the last row: of others, not stored)
-              ldmatrix_trans(ka, ks + (16 * q + mrow) * kp + min(d + 16 * z, dk - 16) + mcol);
-              mma_bf16(f[z], ka, b[q][v][0], b[q][v][1]);
-            }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (d + 8 * u < dk)
-            *reinterpret_cast<float2*>(D + at + 8 * u * dv) = make_float2(f[u >> 1][2 * (u & 1)], f[u >> 1][2 * (u & 1) + 1]);
-      }
     }
   } else {  // four rows of four columns per thread and pass
     const int groups = dv / 4, lanes = kAcceptThreads / groups, col = 4 * (tid % groups);
