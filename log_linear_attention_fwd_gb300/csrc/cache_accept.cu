@@ -1,5 +1,13 @@
 // Appending accepted drafts to the paged decode cache: the nodes of a path join their slot as
 // decode steps at pos, pos + 1, ... would have put them there, page reservation and fold included.
+//
+// Two kernels: a plan in one CTA, which claims the slots and settles the pages (3 us, 8 where blocks end), and a
+// CTA per (row, head), launched while the plan runs.  Measured (GB300, calls in a row; floor: bytes at the measured
+// copy rate): one sequence's path 5.6 us; 125 rows of 16 heads, d 128, ten of which end a block, 39 us (floor
+// 5.7): 13 without the ten, 24 with those that fold to no older page, and the rest is the one that folds seven pages, by
+// one CTA per head at 30 GB/s each; 32 rows of 48 heads, dv 64, all of which end a block: 46 us, 109 MB, floor 16.
+// CTAs of 128 (53, 46 us) or 512 threads (39, 62), persistent ones with a list of folds (36 to 48, 69 and more), and
+// pages through a ring in shared memory (47, 53) were no better.
 #include "cache_common.cuh"
 
 namespace ll {

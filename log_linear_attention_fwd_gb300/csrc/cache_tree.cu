@@ -43,8 +43,17 @@ struct TreeArgs {
 //
 // Precision.  q of a bf16 cache is exact in tf32.  For bf16 outputs a page's value and a token's weight are rounded
 // to tf32 (2^-11 of each, an eighth of the output's own half step), for fp32 outputs they are two parts that
-// leave 2^-22; with fp32 tokens everything is two parts and their products but the least.  All sums are fp32, and a
-// page is summed by itself before it is weighted per node.
+// leave 2^-22.  With fp32 tokens everything is two parts, and all four products of them are taken: the first parts are
+// cut off towards zero, so the fourth is of one sign and adds up (rel-L2 of the outputs 7e-7 with it, 1.2e-6
+// without).  All sums are fp32, and a page is summed by itself before it is weighted per node.
+//
+// Measured (GB300, calls in a row; floor: the bytes at the measured copy rate of 6.7 TB/s).  One sequence, 16 heads, d
+// 128, 8 nodes, position 12345: 9.0 us, a chain of latencies (inputs, scores, weights, values, pages, two cluster
+// barriers).  61 sequences of such heads at 0..16383, up to 32 nodes: 76 us, 4.0 TB/s, floor 45.  24 sequences of
+// 48 heads on one q/k head, dv 64, 64 nodes, 4096..131071: 118 us, 2.1 TB/s, floor 36; the tensor pipe is busy for 26 %,
+// 41 % of the issue slots are used, and no stall reason stands out.  There the part before the pages takes about as long
+// as the pages, and is only partly hidden by the SM's other CTA: registers and the weights' room allow two.  A
+// CTA per 32 nodes of 64 (126 us), 32 columns per warp (132), stages of 8 KB, and copying the pages to L2 first were slower.
 constexpr int kTreeWarps = 8, kConsumers = 32 * kTreeWarps, kTreeThreads = kConsumers + 32;
 constexpr int kFiller = kTreeWarps;    // the warp that fills the ring
 constexpr int kWalkers = kTreeWarps - 2;  // the first of the two warps that have a node per thread
@@ -139,7 +148,7 @@ __device__ __forceinline__ uint32_t tf32_of(float x) {
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
   const float rest = fmaxf(fabsf(x) - fabsf(__uint_as_float(hi)), fminf(fabsf(x), 0x1p-126f));
-  lo = __float_as_uint(rest) | (hi & 0x80000000u);
+  lo = tf32_of(rest) | (hi & 0x80000000u);
 }
 // A decay, of a sum of log decays; within 2^-20 where it is then rounded to tf32.
 template <int kPage>
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             const uint4* q = reinterpret_cast<const uint4*>(qs + (y * NQ + 8 * t + lanes_g) * kQPitch + 32 * d + 4 * lanes_i);
             const uint4 even = q[0], odd = q[1];
 #pragma unroll
-            for (int x = kIn - 1 - y; x >= 0; --x) {
+            for (int x = kIn - 1; x >= 0; --x) {
               mma_tf32(sc[t], ka[0][x][0], ka[1][x][0], ka[0][x][1], ka[1][x][1], even.x, odd.x);
               mma_tf32(sc[t], ka[0][x][2], ka[1][x][2], ka[0][x][3], ka[1][x][3], even.y, odd.y);
               mma_tf32(sc[t], ka[0][x][4], ka[1][x][4], ka[0][x][5], ka[1][x][5], even.z, odd.z);
@@ -598,7 +607,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
               const uint2 b = *reinterpret_cast<const uint2*>(p + x * NQ * lay.tp);
 #pragma unroll
               for (int i = kIn - 1; i >= 0; --i)
-                if (x + i < 2) mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], b.x, b.y);
+                mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], b.x, b.y);
             }
           }
         }
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
                 uint32_t b[4];
                 ldmatrix4(b[0], b[1], b[2], b[3], q + ((y * NQ + 8 * t) * kQPitch + 16 * z) * 4);
 #pragma unroll
-                for (int u = kPage - 1 - y; u >= 0; --u) {
+                for (int u = kPage - 1; u >= 0; --u) {
                   mma_tf32(part[t], pa[u][0], pa[u][1], pa[u][2], pa[u][3], b[0], b[1]);
                   mma_tf32(part[t], pa[u][4], pa[u][5], pa[u][6], pa[u][7], b[2], b[3]);
                 }
