@@ -527,7 +527,8 @@ LL_API int loglinear_cache_reserve(const ll_cache* cache, const int32_t* slots,
  * to earlier positions of the block (rejected drafts), its end included; but only until a call has
  * been made for it at a position of the next block, whose tokens replace the block's and whose
  * reservation gives up its pages, and not to before the end of a loaded prompt where the block
- * has pages.  Drafts that cross a block's end belong on a fork.
+ * has pages.  Drafts that cross a block's end belong on a fork, or go through loglinear_cache_tree and
+ * loglinear_cache_accept.
  *   q, k   [n, Hqk, dk] cache dtype;  v [n, H, dv] cache dtype
  *   log_a  [n, H] fp32 or NULL (no decay);  lambda [n, H, L] fp32, L >= M + 7
  *   out    [n, H, dv] out_dtype
