@@ -33,42 +33,32 @@ namespace {
 // chain of a few latencies: 2 us before a step of one row, 6 before one of 128.
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(ll_cache c, const int* slots,
                                                                      const int* pos, int64_t n) {
-  __shared__ int slot_s[kPlanThreads], pos_s[kPlanThreads];
+  __shared__ int slot_s[kPlanThreads];
   const Scratch sc = scratch_of(c);
   const int tid = threadIdx.x;
   let_next_start();
-  // the rows in shared memory, -1 for those that are left out; one at a time per thread where
-  // they fit, else their owners go through global memory
-  const bool few = n <= kPlanThreads;
-  if (few) {
+  if (n <= kPlanThreads) {  // a row per thread
     const int s = tid < n ? slots[tid] : -1, t = tid < n && pos ? pos[tid] : 0;
     slot_s[tid] = s;
+    bool bad = s < -1 || s >= c.slots, shared = false;
+    const bool ok = position_ok(c, t), fold = ok && (t & (kW - 1)) == kW - 1;
+    const int e = s >= 0 && !bad && fold ? fold_page(c, s, t >> kLogW, &shared) : -1;
     __syncthreads();
-    bool bad = s < -1 || s >= c.slots;
     if (s >= 0)
       for (int i = 0; i < tid; ++i) bad |= slot_s[i] == s;
     if (bad) raise(c, LL_CACHE_ERR_SLOT);
-    bool in = s >= 0 && !bad;
-    if (in && pos && !position_ok(c, t)) {
-      raise(c, LL_CACHE_ERR_POSITION);
-      in = false;
-    }
-    __syncthreads();
-    slot_s[tid] = in ? s : -1;
-    pos_s[tid] = t;
-  } else {
-    claim_slots(c, slots, n, sc.owner);
-    for (int64_t r = tid; pos && r < n; r += kPlanThreads)
-      if (owns(c, sc.owner, slots[r], r) && !position_ok(c, pos[r])) raise(c, LL_CACHE_ERR_POSITION);
+    const bool named = s >= 0 && !bad;
+    if (named && !ok) raise(c, LL_CACHE_ERR_POSITION);
+    settle_few(c, (int)n, named && ok ? s : -1, t >> kLogW, fold, e, shared);
+    return;
   }
-  auto slot_of = [&](int64_t r) {
-    if (few) return slot_s[r];
-    const int s = slots[r];
-    return owns(c, sc.owner, s, r) && (!pos || position_ok(c, pos[r])) ? s : -1;
-  };
-  auto pos_of = [&](int64_t r) { return !pos ? 0 : few ? pos_s[r] : pos[r]; };
+  claim_slots(c, slots, n, sc.owner);
+  for (int64_t r = tid; pos && r < n; r += kPlanThreads)
+    if (owns(c, sc.owner, slots[r], r) && !position_ok(c, pos[r])) raise(c, LL_CACHE_ERR_POSITION);
+  auto pos_of = [&](int64_t r) { return pos ? pos[r] : 0; };
   __syncthreads();
-  settle_pages(c, n, slot_of, [&](int64_t r) { return pos_of(r) >> kLogW; },
+  settle_pages(c, n, [&](int64_t r) { return owns(c, sc.owner, slots[r], r) && position_ok(c, pos_of(r)) ? slots[r] : -1; },
+               [&](int64_t r) { return pos_of(r) >> kLogW; },
                [&](int64_t r) { return (pos_of(r) & (kW - 1)) == kW - 1; });
 }
 

@@ -1,11 +1,11 @@
 // Appending accepted drafts to the paged decode cache: the nodes of a path join their slot as
 // decode steps at pos, pos + 1, ... would have put them there, page reservation and fold included.
 //
-// Two kernels: a plan in one CTA, which claims the slots and settles the pages (3 us, 8 where blocks end), and a
+// Two kernels: a plan in one CTA, which claims the slots and settles the pages (3 us, twice that where blocks end), and a
 // CTA per (row, head), launched while the plan runs.  Measured (GB300, calls in a row; floor: bytes at the measured
 // copy rate): one sequence's path 5.6 us; 125 rows of 16 heads, d 128, ten of which end a block, 39 us (floor
 // 5.7): 13 without the ten, 24 with those that fold to no older page, and the rest is the one that folds seven pages, by
-// one CTA per head at 30 GB/s each; 32 rows of 48 heads, dv 64, all of which end a block: 46 us, 109 MB, floor 16.
+// one CTA per head at 30 GB/s each; 32 rows of 48 heads, dv 64, all of which end a block: 45 us, 109 MB, floor 16.
 // CTAs of 128 (53, 46 us) or 512 threads (39, 62), persistent ones with a list of folds (36 to 48, 69 and more), and
 // pages through a ring in shared memory (47, 53) were no better.
 #include "cache_common.cuh"
@@ -36,23 +36,29 @@ __device__ __forceinline__ int path_length(const AcceptArgs& a, int64_t row) {
 }
 
 // Why a row whose slot is in range cannot be served, before its pages are looked at.
-__device__ __forceinline__ unsigned accept_bad(const ll_cache& c, int s, int pos, int count) {
+__device__ __forceinline__ unsigned accept_bad(const ll_cache& c, int pos, int count, bool before) {
   if (count < 0) return LL_CACHE_ERR_TREE;
   if (!position_ok(c, pos) || (count && !position_ok(c, (int64_t)pos + count - 1))) return LL_CACHE_ERR_POSITION;
-  return before_pages(c, s, pos) ? LL_CACHE_ERR_POSITION : 0;
+  return before ? LL_CACHE_ERR_POSITION : 0;
 }
 
 // As a reservation for each row's block: where the path ends the block, the page it is folded to.
 // owner: the rows that are served, ~row of those that are left out.
 __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, AcceptArgs a) {
-  __shared__ int slot_s[kPlanThreads], block_s[kPlanThreads], count_s[kPlanThreads];
+  __shared__ int slot_s[kPlanThreads], count_s[kPlanThreads];
   const Scratch sc = scratch_of(c);
   const int tid = threadIdx.x, lane = tid & 31;
   let_next_start();
-  const bool few = a.n <= kPlanThreads;
-  if (few) {
+  if (a.n <= kPlanThreads) {  // a row per thread
     const int s = tid < a.n ? a.slots[tid] : -1, pos = tid < a.n ? a.pos[tid] : 0;
     slot_s[tid] = s;
+    // what may be needed, ahead of knowing (the last block has no page to be folded to)
+    bool bad = s < -1 || s >= c.slots, shared = false, before = false;
+    int e = -1;
+    if (s >= 0 && !bad && position_ok(c, pos)) {
+      before = before_pages(c, s, pos);
+      if ((pos >> kLogW) + 1 < 1 << c.levels) e = fold_page(c, s, pos >> kLogW, &shared);
+    }
     for (int r = tid >> 5; r < a.n; r += kPlanThreads / 32) {  // a warp per path
       const int x = lane < a.D ? a.path[(int64_t)r * a.D + lane] : -1;
       const int y = lane + 32 < a.D ? a.path[(int64_t)r * a.D + lane + 32] : -1;
@@ -62,25 +68,18 @@ __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, A
       if (lane == 0) count_s[r] = len < 64 && z != -1 ? -1 : len;
     }
     __syncthreads();
-    bool bad = s < -1 || s >= c.slots;
     if (s >= 0)
       for (int i = 0; i < tid; ++i) bad |= slot_s[i] == s;
     if (bad) raise(c, LL_CACHE_ERR_SLOT);
     const bool named = s >= 0 && !bad;
     const int count = tid < a.n ? count_s[tid] : 0;
-    const unsigned why = named ? accept_bad(c, s, pos, count) : 0;
+    const unsigned why = named ? accept_bad(c, pos, count, before) : 0;
     if (why) raise(c, why);
     if (named) {
       sc.owner[s] = why ? ~tid : tid;
       sc.done[s] = 0;
     }
-    __syncthreads();
-    slot_s[tid] = named && !why ? s : -1;
-    block_s[tid] = pos >> kLogW;
-    count_s[tid] = (pos & (kW - 1)) + count >= kW;
-    __syncthreads();
-    settle_pages(c, a.n, [&](int64_t r) { return slot_s[r]; }, [&](int64_t r) { return block_s[r]; },
-                 [&](int64_t r) { return count_s[r] != 0; });
+    settle_few(c, a.n, named && !why ? s : -1, pos >> kLogW, (pos & (kW - 1)) + count >= kW, e, shared);
     return;
   }
   claim_slots(c, a.slots, a.n, sc.owner);
@@ -88,7 +87,8 @@ __global__ void __launch_bounds__(kPlanThreads) accept_plan_kernel(ll_cache c, A
   for (int64_t r = tid; r < a.n; r += kPlanThreads) {
     const int s = a.slots[r];
     if (!owns(c, sc.owner, s, r)) continue;
-    const unsigned why = accept_bad(c, s, a.pos[r], path_length(a, r));
+    const int pos = a.pos[r];
+    const unsigned why = accept_bad(c, pos, path_length(a, r), position_ok(c, pos) && before_pages(c, s, pos));
     if (why) raise(c, why);
     if (why) sc.owner[s] = ~(int)r;
     sc.done[s] = 0;

@@ -151,7 +151,7 @@ inline __device__ void take_pages(const ll_cache& c, const int* want, int count)
     for (int i = 0; i < 4; ++i)
       if (free_of[i]) {
         if (rank < count) {
-          c.page_table[__ldcg(want + rank)] = (int)(p0 + i);
+          c.page_table[want[rank]] = (int)(p0 + i);
           c.refcount[p0 + i] = 1;
         }
         ++rank;
@@ -215,6 +215,48 @@ __device__ __forceinline__ void settle_pages(const ll_cache& c, int64_t n, SlotO
   __syncthreads();
   if (count > c.n_pages && tid == 0) raise(c, LL_CACHE_ERR_PAGES);
   take_pages(c, sc.from, (int)min((int64_t)count, c.n_pages));
+}
+
+// The table's entry for the page that slot s folds block j to (-1: none), and whether that page is shared.
+__device__ __forceinline__ int fold_page(const ll_cache& c, int s, int j, bool* shared) {
+  const int e = c.page_table[(int64_t)s * c.levels + __ffs(j + 1) - 1];
+  const bool page = e >= 0 && e < c.n_pages;
+  *shared = page && __ldcg(c.refcount + e) != 1;
+  return page ? e : -1;
+}
+
+// settle_pages for up to kPlanThreads rows, thread r having row r: its slot (-1: left out), block j and, where the
+// block is folded, what fold_page gives before any of this.  Spares the general form's marks and lists in memory and
+// the reads behind them (reservation and step of 128 rows 101.9 -> 100.3 us).
+__device__ __forceinline__ void settle_few(const ll_cache& c, int n, int s, int j, bool fold, int e, bool shared) {
+  __shared__ int slot_s[kPlanThreads], block_s[kPlanThreads], want[kPlanThreads];
+  const int M = (int)c.levels, tid = threadIdx.x, at = s * M + __ffs(j + 1) - 1;
+  fold &= s >= 0;
+  const bool need = fold && (e < 0 || shared);
+  slot_s[tid] = s;
+  block_s[tid] = fold ? ~j : j;
+  const bool folds = __syncthreads_or(fold);
+  for (int k = tid; k < n * M; k += kPlanThreads) {
+    const int r = k / M, m = k - r * M, b = block_s[r], jr = b < 0 ? ~b : b;
+    if (slot_s[r] < 0 || (b < 0 && m == __ffs(jr + 1) - 1)) continue;
+    int* p = c.page_table + slot_s[r] * M + m;
+    const int x = *p;
+    if (x < -1 || (x >= 0 && !(jr >> m & 1))) {
+      drop_page(c, x);
+      *p = -1;
+    }
+  }
+  if (need) {
+    if (shared) drop_page(c, e);
+    c.page_table[at] = -1;
+  }
+  if (!folds) return;
+  int total;
+  const int rank = block_scan(need, &total);
+  if (need) want[rank] = at;
+  if (total == 0) return;
+  __syncthreads();
+  take_pages(c, want, total);
 }
 
 // ---------------------------------------------------------------- decays inside a block

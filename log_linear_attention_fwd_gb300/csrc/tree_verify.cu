@@ -23,7 +23,7 @@
 // chain of five latencies (tree, children's values, pass, cluster, run).  61 rows of 131072 with trees of 32: 20 us, 32 MB,
 // floor 4.8: the same chain, the slowest walks about 2 us of it, and the pass (4 us) is the only part that moves bytes.
 // 128 chains of 5 drawn drafts: 38 us, 134 MB, floor 20: 3.5 TB/s; rows that reject once have two passes.  32 trees
-// of 23 drawn drafts, 50021 bf16 values: 30 us, one pass per rejection, each about 2 us of latency.  Four CTAs of 256
+// of 23 drawn drafts, 50021 bf16 values: 29 us, one pass per rejection, each about 2 us of latency.  Four CTAs of 256
 // threads per SM: three leave the drawn chains at 54, two of 512 are slower on all of these but the second.
 #include <algorithm>
 
@@ -106,7 +106,7 @@ __device__ __forceinline__ Mass rest_of(float p, float q, Mass S) {
 // The calling warp's sum over [lo, hi) of a row.  vec: the two rows lie alike to 16 bytes, `off` elements behind one.
 template <typename T, int kKind>
 __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int64_t hi, bool vec, int off, Mass S) {
-  constexpr int n = Vec<T>::n, kFlight = kKind == kPlain ? 8 : 4;  // 8 loads of a thread on their way
+  constexpr int n = Vec<T>::n, kFlight = kKind == kPlain ? 8 : kKind == kFirst ? 4 : 2;  // loads on their way
   const int lane = threadIdx.x & 31;
   int64_t a = hi, b = hi;  // whole vectors: [a, b)
   if (vec) {
