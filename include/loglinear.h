@@ -630,7 +630,8 @@ LL_API int loglinear_cache_tree(const ll_cache* cache, const int32_t* slots, con
  *   new_pos device int32 [n], not pos itself: pos[row] + the path's length; rows that are left out
  *           keep theirs
  * A slot given to an earlier row, a path that is too long for the cache, names no node, or folds
- * without its pages: the row is left out (its pages reserved) and the error word raised.
+ * without its pages: the row is left out (in the last case with what it could reserve) and the error
+ * word raised.
  */
 LL_API int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, const int32_t* pos,
                                   const int32_t* path, const void* k, const ll_strides* k_strides,
@@ -660,7 +661,7 @@ LL_API int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, c
  * node 0 is no root or that has a token outside the vocabulary does too, and raises bit 5 of
  * loglinear_device_error.  Sums are exact, of values rounded to the nearest 2^-43, and the same in any
  * order: the results do not depend on the launch.  (Rows whose values sum to 2^18 or more overflow: the
- * token is then any in the vocabulary.)
+ * token is then any in the vocabulary, or -1.)
  * Errors: LL_ERR_INVALID (null pointer, negative size, N or V < 1), LL_ERR_DTYPE,
  * LL_ERR_UNSUPPORTED (N > LL_TREE_MAX, V > 2^30, n > 2^24), LL_ERR_ALIGN, LL_ERR_CUDA.  n = 0 is a no-op.
  */

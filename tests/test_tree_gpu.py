@@ -515,7 +515,7 @@ def test_accept_on_a_fork_leaves_its_source(LL):
     assert cache.error() == 0
 
 
-@pytest.mark.parametrize("n", [1100])
+@pytest.mark.parametrize("n", [1024, 1100])
 def test_accept_more_rows_than_a_plan_has_threads(LL, n):
     H, dk, dv, M = 1, 4, 4, 2
     cache = LL.LogLinearCache.empty(n + 5, n, H, dk, dv, M, dtype=torch.float32)
@@ -586,6 +586,69 @@ def test_verify_at_any_alignment(LL, dtype, offsets):
     for V in (999, 4096):
         x = drafts(4, 6, V, dtype, True, seed=V)
         check_verify(verify(LL, *x, offsets=offsets), *x)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,V", [(3, 9001), (700, 300)])
+def test_verify_many_siblings(LL, n, V, dtype, drawn):
+    """All 63 drafts behind one node, tokens among them twice, hard to accept: by clusters and by single CTAs."""
+    N = 64
+    _, _, probs, u, draft = drafts(n, N, V, dtype, drawn, seed=V)
+    g = torch.Generator().manual_seed(n)
+    tokens = [[0] + torch.multinomial(draft[r, 0].double() if drawn else torch.ones(V // 3, dtype=torch.float64), N - 1,
+                                      replacement=True, generator=g).tolist() for r in range(n)]
+    if not drawn:
+        assert max(len(t) - len(set(t)) for t in tokens) > 5
+    u = 1 - u ** 4 / 16
+    u[:, 0] = torch.rand(n, generator=g)
+    parents = [[-1] + [0] * (N - 1)] * n
+    got = LL.loglinear_tree_verify(i32(parents), i32(tokens), probs.cuda(), u.cuda(), draft=None if draft is None else draft.cuda())
+    check_verify(got, parents, tokens, probs, u, draft)
+    assert LL.device_error() == 0
+
+
+def test_two_streams_at_once(LL):
+    """Trees of one cache and verifications, at once on two streams, eager and as graphs: as by themselves."""
+    pos, N = [70, 126, 300], 12
+    cache, slots, ctx, tree, x = contexts(LL, pos, N, 4, 2, 64, 32, "bf16", True)
+    plans = [parents_of(3, N, "tree", 1), parents_of(3, N, "forest", 2)]
+    dr = [drafts(6, 9, 5003, "f32", True, seed=i) for i in range(2)]
+    dr = [(i32(p), i32(t), q.cuda(), u.cuda(), d.cuda()) for p, t, q, u, d in dr]
+    outs = [torch.zeros(3, N, 4, 32).cuda() for _ in range(2)]
+    res = [None, None]
+
+    dev = [(i32(slots), i32(pos), i32(p)) for p in plans]
+
+    def call(i):
+        LL.loglinear_cache_tree(cache, *dev[i], x["q"], x["k"], x["v"], x["log_a"], x["lam"], out=outs[i])
+        res[i] = LL.loglinear_tree_verify(*dr[i][:4], draft=dr[i][4])
+
+    want = []
+    for i in range(2):
+        call(i)
+        torch.cuda.synchronize()
+        want.append((outs[i].clone(), *[t.clone() for t in res[i]]))
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i)
+        graphs.append((g, res[i]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for graph in (False, True):
+        for i in range(2):
+            outs[i].zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i][0].replay() if graph else call(i)
+        torch.cuda.synchronize()
+        for i in range(2):
+            got = (outs[i], *(graphs[i][1] if graph else res[i]))
+            assert all(torch.equal(p, q) for p, q in zip(got, want[i]))
+    assert cache.error() == 0 and LL.device_error() == 0
 
 
 def test_verify_repeats_and_does_not_depend_on_the_batch(LL):
