@@ -20,11 +20,11 @@
 // holds the drawn token is read again.
 //
 // Measured (GB300, calls in a row; floor: bytes at the measured copy rate).  One row of 32768 fp32 values: 7.4 us, a
-// chain of five latencies (tree, children's values, pass, cluster, run).  61 rows of 131072 with trees of 32: 20 us, 32 MB,
-// floor 4.8: the same chain, the slowest walks about 2 us of it, and the pass (4 us) is the only part that moves bytes.
-// 128 chains of 5 drawn drafts: 38 us, 134 MB, floor 20: 3.5 TB/s; rows that reject once have two passes.  32 trees
-// of 23 drawn drafts, 50021 bf16 values: 29 us, one pass per rejection, each about 2 us of latency.  Four CTAs of 256
-// threads per SM: three leave the drawn chains at 54, two of 512 are slower on all of these but the second.
+// chain of five latencies (tree, children's values, pass, cluster, run).  61 rows of 131072 with trees of 32: 15 us, 32 MB,
+// floor 4.8: the same chain; the pass (4 us) is the only part that moves bytes.  128 chains of 5 drawn drafts: 33 us,
+// 134 MB, floor 20: 4.0 TB/s; rows that reject once have two passes.  32 trees of 23 drawn drafts, 50021 bf16
+// values: 30 us, one pass per rejection, each about 2 us of latency and of arithmetic.  Four CTAs of 256
+// threads per SM: three left the drawn chains at 54, two of 512 were slower on two of these.
 #include <algorithm>
 
 #include "cache_common.cuh"
@@ -141,12 +141,18 @@ __device__ __forceinline__ Mass sum_run(const T* P, const T* Q, int64_t lo, int6
   return sum;
 }
 
+// A function of its own: registers of the loop that has most to do (128 chains of drawn drafts 37 -> 33 us).
+template <typename T>
+__device__ __noinline__ Mass sum_first(const T* P, const T* Q, int64_t lo, int64_t hi, bool vec, int off) {
+  return sum_run<T, kFirst>(P, Q, lo, hi, vec, off, kOne);
+}
+
 struct VerifySmem {
   int up[kNodes], tok[kNodes];
   float px[kNodes], qx[kNodes], us[kNodes];
   Mass rest[kNodes];         // drafts that were given: R of a child at its turn
   unsigned first[2], ok[2];  // theirs, a bit per node: no earlier sibling has its token; accepted at its turn
-  Mass warp_sum[2][kVerifyWarps], scan[kVerifyWarps];  // warp_sum, cta_sum: by turns, as a warp may be
+  Mass warp_sum[2][kVerifyWarps], part[kVerifyWarps], scan[kVerifyWarps];  // warp_sum, cta_sum: by turns, as a warp may be
   Mass cta_sum[2][kVerifySplit];                       // at the next pass while another reads the last one's
 };
 
@@ -238,20 +244,27 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
     *off = (int)(p / sizeof(T)) & (n - 1);
     return ((p ^ q) & 15u) == 0;
   };
-  auto pass = [&](Mass S, bool plain) {
+  // the calling warp's sum over [lo, hi) of what is drawn from at the current node
+  auto sum_of = [&](int64_t lo, int64_t hi, Mass S, bool plain) {
     const T* P = P0 + cur * V;
     const T* Q = plain || !kDrawn || S == 0 ? nullptr : Q0 + cur * V;
     int off;
     const bool vec = place(P, Q, &off);
-    const int64_t k = (int64_t)rank * kVerifyWarps + w, lo = run_at(k, off), hi = run_at(k + 1, off);
     Mass sum = !kDrawn || !Q ? sum_run<T, kPlain>(P, Q, lo, hi, vec, off, S)
-               : S == kOne   ? sum_run<T, kFirst>(P, Q, lo, hi, vec, off, S)
+               : S == kOne   ? sum_first<T>(P, Q, lo, hi, vec, off)
                              : sum_run<T, kMore>(P, Q, lo, hi, vec, off, S);
     if (!kDrawn && !plain)
       for (unsigned long long g = gone; g; g &= g - 1) {
         const int i = __ffsll(g) - 1;
         if (sm.tok[i] >= lo && sm.tok[i] < hi) sum -= to_mass(sm.px[i]);
       }
+    return sum;
+  };
+  auto pass = [&](Mass S, bool plain) {
+    int off;
+    place(P0 + cur * V, nullptr, &off);
+    const int64_t k = (int64_t)rank * kVerifyWarps + w;
+    const Mass sum = sum_of(run_at(k, off), run_at(k + 1, off), S, plain);
     warp_sum = sm.warp_sum[passes & 1];
     if (lane == 0) warp_sum[w] = sum;
     __syncthreads();
@@ -341,8 +354,22 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
   const T* P = P0 + cur * V;
   const T* Q = plain || !kDrawn || S == 0 ? nullptr : Q0 + cur * V;
   int off;
-  place(P, Q, &off);
-  const int64_t k = (int64_t)rank * kVerifyWarps + run, lo = run_at(k, off), hi = run_at(k + 1, off);
+  place(P, nullptr, &off);
+  const int64_t k = (int64_t)rank * kVerifyWarps + run;
+  int64_t lo = run_at(k, off), hi = run_at(k + 1, off);
+  if (hi - lo > 4 * kVerifyThreads) {
+    // an eighth of a long run per warp first, 16 bytes at a time: only the one that holds the token then goes to all
+    // threads, whose few neighbouring values are read one by one (61 rows of 131072: 19.7 -> 15.1 us)
+    const int64_t begin = lo, end = hi, len = ((hi - lo + kVerifyWarps - 1) / kVerifyWarps + 7) & ~(int64_t)7;
+    auto part_at = [&](int i) { return i == 0 ? begin : i == kVerifyWarps ? end : min(end, begin + i * len - (begin ? 0 : off)); };
+    const Mass part = sum_of(part_at(w), part_at(w + 1), S, plain);
+    if (lane == 0) sm.part[w] = part;
+    __syncthreads();
+    int i = 0;
+    while (target >= sm.part[i]) target -= sm.part[i++];  // (ends: they are the run's sum)
+    lo = part_at(i);
+    hi = part_at(i + 1);
+  }
   const int64_t each = (hi - lo + kVerifyThreads - 1) / kVerifyThreads;
   const int64_t from = min(hi, lo + tid * each), to = min(hi, from + each);
   auto mass_at = [&](int64_t x) -> Mass {

@@ -588,6 +588,21 @@ def test_verify_at_any_alignment(LL, dtype, offsets):
         check_verify(verify(LL, *x, offsets=offsets), *x)
 
 
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_long_runs(LL, dtype, offset):
+    """Warps' runs of more than 1024 values, at their borders: every row's next token where u_0 puts it."""
+    n, V = 40, 70001
+    g = torch.Generator().manual_seed(offset)
+    for drawn in (False, True):
+        probs = torch.softmax(torch.randn(n, 2, V, generator=g), -1).to(DT[dtype])
+        draft = torch.softmax(torch.randn(n, 2, V, generator=g), -1).to(DT[dtype]) if drawn else None
+        tokens = [[0, int(torch.randint(V, (1,), generator=g))] for _ in range(n)]
+        u = torch.stack([torch.linspace(0, 1 - 2.0 ** -24, n), torch.full((n,), 1 - 2.0 ** -24)], 1)
+        x = ([[-1, 0]] * n, tokens, probs, u, draft)
+        check_verify(verify(LL, *x, offsets=(offset, offset)), *x)
+
+
 @pytest.mark.parametrize("drawn", [True, False])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,V", [(3, 9001), (700, 300)])
@@ -596,7 +611,7 @@ def test_verify_many_siblings(LL, n, V, dtype, drawn):
     N = 64
     _, _, probs, u, draft = drafts(n, N, V, dtype, drawn, seed=V)
     g = torch.Generator().manual_seed(n)
-    tokens = [[0] + torch.multinomial(draft[r, 0].double() if drawn else torch.ones(V // 3, dtype=torch.float64), N - 1,
+    tokens = [[0] + torch.multinomial(draft[r, 0].double() if drawn else torch.ones(100, dtype=torch.float64), N - 1,
                                       replacement=True, generator=g).tolist() for r in range(n)]
     if not drawn:
         assert max(len(t) - len(set(t)) for t in tokens) > 5
