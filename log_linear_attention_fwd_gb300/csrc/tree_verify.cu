@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
       if (bad) atomicOr(&g_verify_error, 1u << 5);
       a.count[row] = 0;
     }
+    if (C > 1) cluster_wait();
     return;
   }
 

@@ -701,8 +701,9 @@ def test_verify_borders(LL):
     assert LL.device_error() == 0
 
 
-def test_verify_rows_that_are_no_trees(LL):
-    n, N, V = 4, 4, 30
+@pytest.mark.parametrize("V", [30, 9001])
+def test_verify_rows_that_are_no_trees(LL, V):
+    n, N = 4, 4
     x = drafts(n, N, V, "f32", True, seed=2)
     good = x[0][0]
     for up, tok in (([-1, 1, 0, 0], None), ([-1, 0, -3, 0], None), ([0, 0, 0, 0], None), ([-1, -2, 1, 0], None),
