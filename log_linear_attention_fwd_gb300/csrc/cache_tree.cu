@@ -37,34 +37,36 @@ struct TreeArgs {
 // A CTA serves one (row, head) for up to 8 NT nodes: eight warps that compute, and one that
 // keeps a ring of stages of up to 16 KB of the pages filled.  The products run on the tensor cores
 // as out^T = page^T q^T: a page's values go from the ring to the fragments as they are, and the nodes
-// are the narrow side.  mma.sync in tf32, not tcgen05: a page lies in memory with the output's
+// are the narrow side.  mma.sync, not tcgen05: a page lies in memory with the output's
 // columns side by side, and every value of it is used for at most 64 nodes, so HBM and, with small
 // trees, the instructions around the products are the bounds, not the tensor pipe.
 //
-// Precision.  q of a bf16 cache is exact in tf32.  For bf16 outputs a page's value and a token's weight are rounded
-// to tf32 (2^-11 of each, an eighth of the output's own half step), for fp32 outputs they are two parts that
-// leave 2^-22.  With fp32 tokens everything is two parts, and all four products of them are taken: the first parts are
-// cut off towards zero, so the fourth is of one sign and adds up (rel-L2 of the outputs 7e-7 with it, 1.2e-6
-// without).  All sums are fp32, and a page is summed by itself before it is weighted per node.
+// Precision.  bf16 outputs are the fp32 ones, rounded once.  q, k and v of a bf16 cache enter their products as they are,
+// a page's value as three bf16 parts that together are the fp32 value, and a token's weight as two tf32 parts
+// that leave 2^-22.  (Pages and weights rounded to tf32 for bf16 outputs took 77 and 119 us where this takes 88 and 154, and
+// moved the outputs by up to 2^-11 of each product; pages as two tf32 parts, 108 and 176.)  With fp32 tokens everything
+// is two tf32 parts, and all four products of them are taken: the first parts are cut off towards zero, so the fourth
+// is of one sign and adds up (rel-L2 of the outputs 7e-7 with it, 1.2e-6 without).  All sums are fp32, and a page is
+// summed by itself before it is weighted per node.
 //
 // Measured (GB300, calls in a row; floor: the bytes at the measured copy rate of 6.7 TB/s).  One sequence, 16 heads, d
-// 128, 8 nodes, position 12345: 9.0 us, a chain of latencies (inputs, scores, weights, values, pages, two cluster
-// barriers).  61 sequences of such heads at 0..16383, up to 32 nodes: 76 us, 4.0 TB/s, floor 45.  24 sequences of
-// 48 heads on one q/k head, dv 64, 64 nodes, 4096..131071: 118 us, 2.1 TB/s, floor 36; the tensor pipe is busy for 26 %,
-// 41 % of the issue slots are used, and no stall reason stands out.  There the part before the pages takes about as long
-// as the pages, and is only partly hidden by the SM's other CTA: registers and the weights' room allow two.  A
-// CTA per 32 nodes of 64 (126 us), 32 columns per warp (132), stages of 8 KB, and copying the pages to L2 first were slower.
+// 128, 8 nodes, position 12345: 9.3 us, a chain of latencies (inputs, scores, weights, values, pages, two cluster
+// barriers).  61 sequences of such heads at 0..16383, up to 32 nodes: 88 us, 3.5 TB/s, floor 45.  24 sequences of
+// 48 heads on one q/k head, dv 64, 64 nodes, 4096..131071: 154 us, 1.6 TB/s, floor 36.  There a page's third part is 17 us
+// and a weight's second one 16; registers and the weights' room allow two CTAs per SM, which hide the part before the
+// pages only partly.
 constexpr int kTreeWarps = 8, kConsumers = 32 * kTreeWarps, kTreeThreads = kConsumers + 32;
 constexpr int kFiller = kTreeWarps;    // the warp that fills the ring
 constexpr int kWalkers = kTreeWarps - 2;  // the first of the two warps that have a node per thread
 constexpr int kStageBytes = 16384;
 constexpr int kMaxTreeStages = 8;
 constexpr int kTreeSplit = 8;          // CTAs of a cluster
-constexpr int kQPitch = 132;           // floats from query to query
+constexpr int kQPitch = 132;           // floats from query to query, of fp32 tokens
+constexpr int kPairPitch = 136;        // and bf16 ones, of bf16 tokens
 
 template <typename T>
 struct Parts {
-  static constexpr int in = sizeof(T) == 2 ? 1 : 2;  // of q and k, in tf32
+  static constexpr int in = sizeof(T) == 2 ? 1 : 2;  // of tokens, in tf32
 };
 __host__ __device__ constexpr int pad4(int x) { return (x + 3) & ~3; }
 
@@ -74,7 +76,7 @@ struct TreeLayout {
   int vp, tp, lp;             // elements from row to row: v, the tokens' weights, lambda
   int p, v, q, lam, pw, end;  // where each begins
 };
-template <typename T, int NT, int kPage>
+template <typename T, int NT>
 __host__ __device__ __forceinline__ TreeLayout tree_layout(int dv, int N, int M) {
   const int dv16 = (dv + 15) & ~15, tokens = kW + ((N + 15) & ~15);
   TreeLayout l;
@@ -82,9 +84,9 @@ __host__ __device__ __forceinline__ TreeLayout tree_layout(int dv, int N, int M)
   l.tp = tokens + 8;
   l.lp = pad4(M + kLogW + 1);
   l.p = 0;
-  l.v = l.p + kPage * 8 * NT * l.tp * 4;
+  l.v = l.p + 8 * NT * l.tp * 4;
   l.q = l.v + tokens * l.vp * (int)sizeof(T);
-  l.lam = l.q + Parts<T>::in * 8 * NT * kQPitch * 4;
+  l.lam = l.q + 8 * NT * (sizeof(T) == 2 ? kPairPitch * 2 : 2 * kQPitch * 4);
   l.pw = l.lam + (NT == 8 ? 8 * NT * l.lp * 4 : 0);  // (up to 32 nodes: with the tree's decays)
   l.end = l.pw + M * 8 * NT * 4;
   return l;
@@ -150,9 +152,14 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   const float rest = fmaxf(fabsf(x) - fabsf(__uint_as_float(hi)), fminf(fabsf(x), 0x1p-126f));
   lo = tf32_of(rest) | (hi & 0x80000000u);
 }
-// A decay, of a sum of log decays; within 2^-20 where it is then rounded to tf32.
-template <int kPage>
-__device__ __forceinline__ float decay(float x) { return kPage == 1 ? __expf(x) : expf(x); }
+// The leading 8 bits of x and y, as bf16; they keep the rest, so that three such parts are the fp32 value itself.
+// (Infinities leave NaN.)
+__device__ __forceinline__ uint32_t lead_bf16(float& x, float& y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  x -= __uint_as_float(a & 0xffff0000u);
+  y -= __uint_as_float(b & 0xffff0000u);
+  return __byte_perm(a, b, 0x7632);
+}
 // Two neighbouring values as tf32 parts.
 __device__ __forceinline__ void parts2(const __nv_bfloat16* p, uint32_t (&part)[1][2]) {
   const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
@@ -252,8 +259,8 @@ __device__ __forceinline__ float4 load_remote4(const float* p, uint32_t rank) {
   return v;
 }
 
-// grid: (row, head, group of nodes, share of the cluster), the last fastest.  kPage: parts of a page's values.
-template <typename T, int NT, int kPage>
+// grid: (row, head, group of nodes, share of the cluster), the last fastest.
+template <typename T, int NT>
 __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
     cache_tree_kernel(const __grid_constant__ CUtensorMap pages, const __grid_constant__ ll_cache c,
                       const __grid_constant__ TreeArgs a) {
@@ -277,10 +284,11 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
   const int j = pos >> kLogW, r = pos & (kW - 1), par = j & 1, to = __ffs(j + 1) - 1, live = __popc(j);
   const int64_t first_node = (int64_t)row * a.N;
   uint8_t* body = dyn + a.own * kStageBytes;
-  const TreeLayout lay = tree_layout<T, NT, kPage>(dv, a.N, M);
-  float* ps = reinterpret_cast<float*>(body + lay.p);  // [kPage parts][NQ][lay.tp]
+  const TreeLayout lay = tree_layout<T, NT>(dv, a.N, M);
+  float* ps = reinterpret_cast<float*>(body + lay.p);  // [NQ][lay.tp]
   T* vs = reinterpret_cast<T*>(body + lay.v);
-  float* qs = reinterpret_cast<float*>(body + lay.q);  // [parts][NQ][kQPitch]; of every 8 columns the even ones, then the odd ones
+  float* qs = reinterpret_cast<float*>(body + lay.q);  // fp32 tokens: [parts][NQ][kQPitch]; of every 8 columns the even ones, then the odd ones
+  __nv_bfloat16* qb = reinterpret_cast<__nv_bfloat16*>(body + lay.q);  // bf16 tokens: [NQ][kPairPitch]
   float* page_w = reinterpret_cast<float*>(body + lay.pw);
   float* wt = reinterpret_cast<float*>(dyn + (a.own - 1) * kStageBytes);  // log decays of the tree, in the last own stage until the pages need it
   float* lam_s = NT == 8 ? reinterpret_cast<float*>(body + lay.lam) : wt + NQ * kNodes;
@@ -382,14 +390,19 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       const bool vec = whole_pieces(gq, a.sq[1], dk);
       const int k = (tid & 15) * 8;
       if (k < ((dk + 31) & ~31))
-        for (int q = tid >> 4; q < queries; q += 2 * kWalkers) {
-          uint32_t part[kIn][8];
-          parts_of(load8(gq + q * a.sq[1], k, dk, vec), part);
+        for (int q = tid >> 4; q < (sizeof(T) == 2 ? NQ : queries); q += 2 * kWalkers) {
+          if constexpr (sizeof(T) == 2) {
+            // (0 behind the last: what stands there would make NaN, and those are summed once more)
+            *reinterpret_cast<uint4*>(qb + q * kPairPitch + k) = load8(gq + q * a.sq[1], k, q < queries ? dk : 0, vec);
+          } else {
+            uint32_t part[2][8];
+            parts_of(load8(gq + q * a.sq[1], k, dk, vec), part);
 #pragma unroll
-          for (int y = 0; y < kIn; ++y) {
-            uint4* to_ = reinterpret_cast<uint4*>(qs + (y * NQ + q) * kQPitch + k);
-            to_[0] = make_uint4(part[y][0], part[y][2], part[y][4], part[y][6]);
-            to_[1] = make_uint4(part[y][1], part[y][3], part[y][5], part[y][7]);
+            for (int y = 0; y < 2; ++y) {
+              uint4* to_ = reinterpret_cast<uint4*>(qs + (y * NQ + q) * kQPitch + k);
+              to_[0] = make_uint4(part[y][0], part[y][2], part[y][4], part[y][6]);
+              to_[1] = make_uint4(part[y][1], part[y][3], part[y][5], part[y][7]);
+            }
           }
         }
     }
@@ -433,32 +446,40 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
     cp_async_wait<1>();
     __syncthreads();
 
-    // scores of 16 tokens per warp, K q^T, not yet weighted: step z of 32 columns takes the values 2 z and
-    // 2 z + 1 of each thread's 8, of keys and of queries
+    // scores of 16 tokens per warp, K q^T, not yet weighted.  Of 32 columns each thread has 8 neighbouring ones of
+    // two keys, and takes those of its query: which column stands where in a product does not matter
     if (mine) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         if (32 * d >= dk) break;
-        uint32_t ka[2][kIn][8];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (sizeof(T) == 2) parts_of(key_e[d][u], ka[u]);
-          else parts_of(load8(key[u], 32 * d + 4 * lanes_i, key_width[u], key_vec), ka[u]);
-        }
-#pragma unroll
-        for (int y = kIn - 1; y >= 0; --y)
+        if constexpr (sizeof(T) == 2) {
+          const uint4 k0_ = key_e[d][0], k1_ = key_e[d][1];
+          const uint32_t ka[2][4] = {{k0_.x, k1_.x, k0_.y, k1_.y}, {k0_.z, k1_.z, k0_.w, k1_.w}};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint4* q = reinterpret_cast<const uint4*>(qs + (y * NQ + 8 * t + lanes_g) * kQPitch + 32 * d + 4 * lanes_i);
-            const uint4 even = q[0], odd = q[1];
-#pragma unroll
-            for (int x = kIn - 1; x >= 0; --x) {
-              mma_tf32(sc[t], ka[0][x][0], ka[1][x][0], ka[0][x][1], ka[1][x][1], even.x, odd.x);
-              mma_tf32(sc[t], ka[0][x][2], ka[1][x][2], ka[0][x][3], ka[1][x][3], even.y, odd.y);
-              mma_tf32(sc[t], ka[0][x][4], ka[1][x][4], ka[0][x][5], ka[1][x][5], even.z, odd.z);
-              mma_tf32(sc[t], ka[0][x][6], ka[1][x][6], ka[0][x][7], ka[1][x][7], even.w, odd.w);
-            }
+            const uint4 q = *reinterpret_cast<const uint4*>(qb + (8 * t + lanes_g) * kPairPitch + 32 * d + 4 * lanes_i);
+            mma_bf16(sc[t], ka[0], q.x, q.y);
+            mma_bf16(sc[t], ka[1], q.z, q.w);
           }
+        } else {
+          uint32_t ka[2][2][8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) parts_of(load8(key[u], 32 * d + 4 * lanes_i, key_width[u], key_vec), ka[u]);
+#pragma unroll
+          for (int y = 1; y >= 0; --y)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint4* q = reinterpret_cast<const uint4*>(qs + (y * NQ + 8 * t + lanes_g) * kQPitch + 32 * d + 4 * lanes_i);
+              const uint4 even = q[0], odd = q[1];
+#pragma unroll
+              for (int x = 1; x >= 0; --x) {
+                mma_tf32(sc[t], ka[0][x][0], ka[1][x][0], ka[0][x][1], ka[1][x][1], even.x, odd.x);
+                mma_tf32(sc[t], ka[0][x][2], ka[1][x][2], ka[0][x][3], ka[1][x][3], even.y, odd.y);
+                mma_tf32(sc[t], ka[0][x][4], ka[1][x][4], ka[0][x][5], ka[1][x][5], even.z, odd.z);
+                mma_tf32(sc[t], ka[0][x][6], ka[1][x][6], ka[0][x][7], ka[1][x][7], even.w, odd.w);
+              }
+            }
+        }
       }
     }
   }
@@ -515,28 +536,17 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
           if (nodes) {
             const unsigned long long up = sm.above[node0 + q + u] >> x0;
             const float* log = wt + (q + u) * kNodes + x0;
-            f[u][0] = up & 1 ? lam[fenwick_level(tq, s0)] * decay<kPage>(log[0]) * sc[t][u] : 0.f;
-            f[u][1] = up >> 8 & 1 ? lam[fenwick_level(tq, s1)] * decay<kPage>(log[8]) * sc[t][2 + u] : 0.f;
+            f[u][0] = up & 1 ? lam[fenwick_level(tq, s0)] * expf(log[0]) * sc[t][u] : 0.f;
+            f[u][1] = up >> 8 & 1 ? lam[fenwick_level(tq, s1)] * expf(log[8]) * sc[t][2 + u] : 0.f;
           } else {
             const float first = sm.first[node0 + q + u];
-            f[u][0] = depth >= 0 && s0 < pos ? lam[fenwick_level(tq, s0)] * decay<kPage>(after0 + first) * sc[t][u] : 0.f;
-            f[u][1] = depth >= 0 && s1 < pos ? lam[fenwick_level(tq, s1)] * decay<kPage>(after1 + first) * sc[t][2 + u] : 0.f;
+            f[u][0] = depth >= 0 && s0 < pos ? lam[fenwick_level(tq, s0)] * expf(after0 + first) * sc[t][u] : 0.f;
+            f[u][1] = depth >= 0 && s1 < pos ? lam[fenwick_level(tq, s1)] * expf(after1 + first) * sc[t][2 + u] : 0.f;
           }
         }
         float* at = ps + q * lay.tp + 16 * w + lanes_g;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float x = f[u & 1][u >> 1];
-          float* p = at + (u & 1) * lay.tp + (u >> 1) * 8;
-          if constexpr (kPage == 1) {
-            *p = __uint_as_float(tf32_of(x));
-          } else {
-            uint32_t hi, lo;
-            split_tf32(x, hi, lo);
-            p[0] = __uint_as_float(hi);
-            p[NQ * lay.tp] = __uint_as_float(lo);
-          }
-        }
+        for (int u = 0; u < 4; ++u) at[(u & 1) * lay.tp + (u >> 1) * 8] = f[u & 1][u >> 1];
       }
     }
     for (int x = tid; x < live * NQ; x += kConsumers) {
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       float f = 0.f;
       if (depth >= 0) {
         const int lv = (pos + depth) >> kLogW > j ? max(sm.page_lv[y], to) : sm.page_lv[y];
-        f = lam_s[q * lay.lp + kLogW + 1 + lv] * decay<kPage>(sm.page_log[y] + sm.since + sm.first[node0 + q]);
+        f = lam_s[q * lay.lp + kLogW + 1 + lv] * expf(sm.page_log[y] + sm.since + sm.first[node0 + q]);
       }
       page_w[x] = f;
     }
@@ -601,14 +611,13 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
           parts2(v0 + lay.vp, vb);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float* p = ps + (8 * t + lanes_g) * lay.tp + 16 * tile + 8 * y + lanes_i;
+            uint32_t p[2][2];
+            parts2(ps + (8 * t + lanes_g) * lay.tp + 16 * tile + 8 * y + lanes_i, p);
 #pragma unroll
-            for (int x = kPage - 1; x >= 0; --x) {
-              const uint2 b = *reinterpret_cast<const uint2*>(p + x * NQ * lay.tp);
+            for (int x = 1; x >= 0; --x)
 #pragma unroll
               for (int i = kIn - 1; i >= 0; --i)
-                mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], b.x, b.y);
-            }
+                mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], p[x][0], p[x][1]);
           }
         }
       }
@@ -626,10 +635,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             const int q = 8 * t + lanes_i + (u & 1);
             const float v = u >> 1 ? v1 : v0;
             if (q >= queries || !(sm.above[node0 + q] >> y & 1) || !is_odd(v)) continue;
-            float f = 0.f;
-#pragma unroll
-            for (int x = kPage - 1; x >= 0; --x) f += ps[(x * NQ + q) * lay.tp + kW + y];
-            acc[t][u] = fmaf(f, v, acc[t][u]);
+            acc[t][u] = fmaf(ps[q * lay.tp + kW + y], v, acc[t][u]);
           }
       }
     }
@@ -647,7 +653,10 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       const int chunk = 4 * (ct & 1) + (lanes_g >> 1), first_row = 16 * (wide > 1 ? 2 * kp : kp);
       const uint32_t rows_at = tc::smem_u32(dyn) + (ct >> 1) * box_bytes + (lanes_g & 1) * 8 + 128 * first_row;
       const uint32_t off0 = rows_at + tc::sw128_offset(lanes_i, chunk), off1 = rows_at + tc::sw128_offset(lanes_i + 1, chunk);
-      const uint32_t q_at = tc::smem_u32(qs) + (lane & 7) * kQPitch * 4 + (lane >> 3) * 16 + 4 * first_row;
+      // bf16: a step's 16 columns of two node tiles (of one, twice); fp32: 16 columns of a part of one
+      const uint32_t q_at = sizeof(T) == 2
+          ? tc::smem_u32(qb) + (((lane & 7) + (NT > 1 ? (lane >> 4) * 8 : 0)) * kPairPitch + (lane >> 3 & 1) * 8 + first_row) * 2
+          : tc::smem_u32(qs) + (lane & 7) * kQPitch * 4 + (lane >> 3) * 16 + 4 * first_row;
       int stage = 0, phase = 0;
       for (int x = 0; x < live; ++x) {
         float part[NT][4];
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
           for (int u = 0; u < 4; ++u) part[t][u] = 0.f;
         for (int d = k0; d < k1; d += box_rows) {
           if (ok) ok = tc::mbar_wait_short(&sm.full[stage], phase);
-          const uint32_t at0 = off0 + stage * kStageBytes, at1 = off1 + stage * kStageBytes, q = q_at + 4 * d;
+          const uint32_t at0 = off0 + stage * kStageBytes, at1 = off1 + stage * kStageBytes, q = q_at + (int)sizeof(T) * d;
           const int rows = min(box_rows, k1 - d) - first_row;  // from this warp's first on
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
@@ -667,25 +676,42 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             load2(v[1], at1 + 2048 * z);
             load2(v[2], at0 + 2048 * z + 1024);
             load2(v[3], at1 + 2048 * z + 1024);
-            uint32_t pa[kPage][8];
+            if constexpr (sizeof(T) == 2) {
+              uint32_t pa[3][4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const float f = u & 1 ? v[u >> 1].y : v[u >> 1].x;
-              if constexpr (kPage == 1) pa[0][u] = tf32_of(f);
-              else split_tf32(f, pa[0][u], pa[1][u]);
-            }
+              for (int u = 0; u < 3; ++u) {
+                pa[u][0] = lead_bf16(v[0].x, v[1].x);
+                pa[u][1] = lead_bf16(v[0].y, v[1].y);
+                pa[u][2] = lead_bf16(v[2].x, v[3].x);
+                pa[u][3] = lead_bf16(v[2].y, v[3].y);
+              }
 #pragma unroll
-            for (int y = kIn - 1; y >= 0; --y)
-#pragma unroll
-              for (int t = 0; t < NT; ++t) {
+              for (int t = 0; t < NT; t += 2) {
                 uint32_t b[4];
-                ldmatrix4(b[0], b[1], b[2], b[3], q + ((y * NQ + 8 * t) * kQPitch + 16 * z) * 4);
+                ldmatrix4(b[0], b[1], b[2], b[3], q + (8 * t * kPairPitch + 16 * z) * 2);
 #pragma unroll
-                for (int u = kPage - 1; u >= 0; --u) {
-                  mma_tf32(part[t], pa[u][0], pa[u][1], pa[u][2], pa[u][3], b[0], b[1]);
-                  mma_tf32(part[t], pa[u][4], pa[u][5], pa[u][6], pa[u][7], b[2], b[3]);
+                for (int u = 2; u >= 0; --u) {
+                  mma_bf16(part[t], pa[u], b[0], b[1]);
+                  if (NT > 1) mma_bf16(part[t + (NT > 1)], pa[u], b[2], b[3]);
                 }
               }
+            } else {
+              uint32_t pa[2][8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) split_tf32(u & 1 ? v[u >> 1].y : v[u >> 1].x, pa[0][u], pa[1][u]);
+#pragma unroll
+              for (int y = 1; y >= 0; --y)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  uint32_t b[4];
+                  ldmatrix4(b[0], b[1], b[2], b[3], q + ((y * NQ + 8 * t) * kQPitch + 16 * z) * 4);
+#pragma unroll
+                  for (int u = 1; u >= 0; --u) {
+                    mma_tf32(part[t], pa[u][0], pa[u][1], pa[u][2], pa[u][3], b[0], b[1]);
+                    mma_tf32(part[t], pa[u][4], pa[u][5], pa[u][6], pa[u][7], b[2], b[3]);
+                  }
+                }
+            }
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sm.empty[stage]);
@@ -693,6 +719,36 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             stage = 0;
             phase ^= 1;
           }
+        }
+        if constexpr (sizeof(T) == 2) {
+          // NaN: of the sum itself, or of an infinity's parts.  The sums that have it once more, value by value
+          bool nan = false;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) nan |= part[t][u] != part[t][u];
+          if (nan && on && col < dv) {
+            unsigned which = 0;
+#pragma unroll
+            for (int e = 0; e < 4 * NT; ++e)
+              if (part[e >> 2][e & 3] != part[e >> 2][e & 3] && sm.depth[node0 + 8 * (e >> 2) + lanes_i + (e & 1)] >= 0) which |= 1u << e;
+            const float* page = c.pages + ((int64_t)sm.page_at[x] * H + h) * dk * dv + col;
+#pragma unroll 1
+            for (; which; which &= which - 1) {
+              const int e = __ffs(which) - 1;
+              const __nv_bfloat16* qr = qb + (8 * (e >> 2) + lanes_i + (e & 1)) * kPairPitch;
+              float f = 0.f;
+#pragma unroll 1
+              for (int d = k0; d < k1; d += box_rows)
+#pragma unroll 1
+                for (int y = first_row; y < min(min(box_rows, k1 - d), first_row + (wide > 1 ? 32 : 16)); ++y)
+                  f = fmaf(page[(int64_t)(d + y) * dv + (e >> 1 & 1)], __bfloat162float(qr[d + y]), f);
+#pragma unroll
+              for (int i = 0; i < 4 * NT; ++i)
+                if (i == e) part[i >> 2][i & 3] = f;
+            }
+          }
+          __syncwarp();
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -783,7 +839,7 @@ int tree_split_log(int64_t items, int dk, int sms) {
 
 constexpr size_t kSm = 233472;  // shared memory of an SM
 
-template <typename T, int NT, int kPage>
+template <typename T, int NT>
 cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   const int dk = (int)c.dk, dv = (int)c.dv;
   a.groups_log = a.N > 8 * NT ? 1 : 0;
@@ -794,7 +850,7 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   a.box_rows = std::min(col_boxes == 1 ? 128 : col_boxes == 2 ? 64 : 32, share);  // a stage, or a CTA's share
   a.heads = fast_div((uint32_t)c.H);
   a.per_qk = fast_div((uint32_t)(c.H / c.Hqk));
-  const TreeLayout lay = tree_layout<T, NT, kPage>(dv, a.N, (int)c.levels);
+  const TreeLayout lay = tree_layout<T, NT>(dv, a.N, (int)c.levels);
   const size_t own_smem = (sizeof(TreeSmem) + 1023) & ~(size_t)1023;  // the stages begin at a multiple of 1024
   const size_t fixed = own_smem + 1024;                              // (1024 of each CTA are the system's)
   // as many CTAs on an SM as leave the ring three stages, one of them from the start
@@ -807,7 +863,7 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   const size_t smem = (size_t)a.own * kStageBytes + lay.end;
   CUtensorMap pages;
   if (!make_pages_map(&pages, c.pages, c.n_pages, c.H, c.dk, c.dv, a.box_rows)) return cudaErrorInvalidValue;
-  const auto kernel = cache_tree_kernel<T, NT, kPage>;
+  const auto kernel = cache_tree_kernel<T, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_following(false, kernel, dim3((unsigned)(items << a.split_log)), kTreeThreads, smem, split, s, pages, c, a);
@@ -815,12 +871,12 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
 
 // A tile for every 8 nodes, up to 64 of them; with fp32 tokens up to 32, whose two parts of everything are what
 // shared memory and registers hold, and two groups above that.
-template <typename T, int kPage>
+template <typename T>
 cudaError_t launch_nodes(const ll_cache& c, const TreeArgs& a, cudaStream_t s) {
-  if (a.N <= 8) return launch<T, 1, kPage>(c, a, s);
-  if (a.N <= 16) return launch<T, 2, kPage>(c, a, s);
-  if (a.N <= 32 || sizeof(T) == 4) return launch<T, 4, kPage>(c, a, s);
-  return launch<T, sizeof(T) == 4 ? 4 : 8, kPage>(c, a, s);
+  if (a.N <= 8) return launch<T, 1>(c, a, s);
+  if (a.N <= 16) return launch<T, 2>(c, a, s);
+  if (a.N <= 32 || sizeof(T) == 4) return launch<T, 4>(c, a, s);
+  return launch<T, sizeof(T) == 4 ? 4 : 8>(c, a, s);
 }
 
 }  // namespace
@@ -837,8 +893,7 @@ cudaError_t launch_cache_tree(const ll_cache& c, const int* slots, const int* po
     a.sk[i] = sk[i];
     a.sv[i] = sv[i];
   }
-  if (c.dtype == LL_F32) return launch_nodes<float, 2>(c, a, s);
-  return a.out_f32 ? launch_nodes<__nv_bfloat16, 2>(c, a, s) : launch_nodes<__nv_bfloat16, 1>(c, a, s);
+  return c.dtype == LL_F32 ? launch_nodes<float>(c, a, s) : launch_nodes<__nv_bfloat16>(c, a, s);
 }
 
 }  // namespace ll

@@ -1,0 +1,93 @@
+"""Speculative decoding on the GPU where it is easily wrong: bf16 outputs, deep decays, infinities.
+
+Tolerances as in tests/test_tree_gpu.py, by the same helpers; each test states what it adds.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests.helpers import TOL_F32, rel_l2
+from tests.test_tree_gpu import TWO_PARTS, attend, contexts, parents_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def LL():
+    import log_linear_attention_fwd_gb300 as m
+    return m
+
+
+def live_of(parents):
+    return torch.tensor(parents).cuda() != -2
+
+
+@pytest.mark.parametrize("N", [5, 13, 30, 64])
+@pytest.mark.parametrize("H,Hqk,dk,dv,dtype", [(4, 2, 128, 128, "bf16"), (6, 1, 128, 64, "bf16"), (2, 2, 72, 100, "bf16"),
+                                               (2, 1, 96, 36, "f32")])
+def test_bf16_outputs_are_the_fp32_outputs_rounded(LL, H, Hqk, dk, dv, dtype, N):
+    """The outputs' type decides about their last rounding only: equal to the bit."""
+    pos = [0, 63, 150, 448, 511, 1000]
+    parents = parents_of(len(pos), N, "tree")
+    cache, slots, ctx, tree, x = contexts(LL, pos, N, H, Hqk, dk, dv, dtype, True)
+    wide, narrow = (attend(LL, cache, slots, pos, parents, x, out_dtype=t) for t in (torch.float32, torch.bfloat16))
+    live = live_of(parents)
+    assert torch.equal(wide[live].bfloat16(), narrow[live])
+    assert cache.error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_deep_decays_that_decide(LL, dtype):
+    """Log decays down to -56 under level weights of up to e^56: the terms that have decayed most are the output.
+    A sum of log decays below 64 rounds by 2^-19 (half a step) at each of at most 6 additions, and so
+    moves its term by 6 2^-19 beside the tests' other bounds; bf16 outputs round that once."""
+    pos, N = [70, 200], 4
+    cache, slots, ctx, tree, x = contexts(LL, pos, N, 2, 1, 64, 32, dtype, True)
+    chain = [[-1, 0, 1, 2]] * 2
+    x["log_a"].fill_(-14.0)
+    for i in range(N):
+        x["lam"][:, i, :, 3:] *= float(np.exp(14.0 * (i + 1)))
+        x["lam"][:, i, :, :3] *= 0.125
+    for r, t in enumerate(tree):
+        t["log_a"], t["lam"] = x["log_a"][r].cpu(), x["lam"][r].cpu()
+    want = np.stack([oracle.tree_attention(c, t, p) for c, t, p in zip(ctx, tree, chain)])
+    got = attend(LL, cache, slots, pos, chain, x, out_dtype=torch.float32)
+    tol = TOL_F32 + TWO_PARTS + 6 * 2.0 ** -19
+    for r in range(2):
+        for i in range(N):
+            assert rel_l2(got[r, i], want[r, i]) <= tol, (r, i, rel_l2(got[r, i], want[r, i]))
+    assert torch.equal(attend(LL, cache, slots, pos, chain, x, out_dtype=torch.bfloat16), got.bfloat16())
+
+
+@pytest.mark.parametrize("n,H,Hqk,dk,dv,N", [(1, 1, 1, 32, 16, 5), (1, 2, 1, 128, 128, 30), (2, 2, 2, 96, 36, 64), (40, 4, 2, 33, 20, 9),
+                                             (40, 4, 1, 128, 64, 64), (24, 8, 2, 128, 128, 17)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinities_in_pages(LL, dtype, n, H, Hqk, dk, dv, N):
+    """A page's infinities and NaN: the outputs' column has q's sign of them for each node, NaN where q is 0 there or
+    two of them are of both signs; every other output is as without them, to the bit.  (Clusters; CTAs by themselves.)"""
+    pos = [70 + 64 * (i % 3) for i in range(n)]
+    cache, slots, ctx, tree, x = contexts(LL, pos[:3], N, H, Hqk, dk, dv, dtype, True)
+    slots = [slots[i % 3] for i in range(n)]
+    x = {k: v[[i % len(v) for i in range(n)]].contiguous() for k, v in x.items()}
+    x["q"][:, :, :, 3] = x["q"][:, :, :, 3].abs().clamp(min=0.125) * torch.tensor([1.0, -1.0]).repeat(N)[:N].cuda()[None, :, None]
+    x["q"][:, 0, :, 3] = 0.0
+    x["q"][:, :, :, dk - 1] = x["q"][:, :, :, dk - 1].abs().clamp(min=0.125)
+    parents = parents_of(n, N, "tree")
+    live = live_of(parents)
+    h, where = H - 1, {int(cache.page_table[s, next(m for m in range(5) if p >> 6 >> m & 1)]) for s, p in zip(slots, pos)}
+    for e in where:
+        cache.pages[e, h, [3, dk - 1], 1] = 0.0
+    zeros = lambda: torch.zeros(n, N, H, dv).cuda()  # noqa: E731
+    plain = attend(LL, cache, slots, pos, parents, x, out=zeros())
+    inf, nan = float("inf"), float("nan")
+    for at, last in ((inf, 0.0), (-inf, 0.0), (nan, 0.0), (inf, inf)):
+        for e in where:
+            cache.pages[e, h, 3, 1], cache.pages[e, h, dk - 1, 1] = at, last
+        got = attend(LL, cache, slots, pos, parents, x, out=zeros())
+        want = plain.clone()
+        want[:, :, h, 1] = x["q"][:, :, h // (H // Hqk), 3].float() * at + x["q"][:, :, h // (H // Hqk), dk - 1].float() * last
+        assert not torch.isfinite(want[:, :, h, 1]).any()
+        assert torch.equal(got[live].nan_to_num(5.0), want[live].nan_to_num(5.0)), (at, last)
+        assert torch.equal(torch.isnan(got[live]), torch.isnan(want[live]))
+    assert cache.error() == 0
