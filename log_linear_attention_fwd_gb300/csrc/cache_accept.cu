@@ -357,25 +357,24 @@ __global__ void __launch_bounds__(kAcceptThreads, kMma ? 4 : 2) accept_kernel(ll
 }
 
 template <typename T, bool kMma>
-cudaError_t launch_main(const ll_cache& c, const AcceptArgs& a, cudaStream_t s) {
+cudaError_t launch_both(const ll_cache& c, const AcceptArgs& a, cudaStream_t s) {
   const size_t row = kMma ? sizeof(T) * (size_t)(c.dk + c.dv + 2 * kPad) : sizeof(float) * (size_t)(((c.dk + 3) & ~3) + c.dv);
   const auto kernel = accept_kernel<T, kMma>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kW * row));
-  if (e != cudaSuccess) return e;
+  cudaError_t e = allow_shared(kernel);
+  if (e != cudaSuccess) return e;  // before the plan changes the tables
+  accept_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_following(true, kernel, dim3((unsigned)(a.n * c.H)), kAcceptThreads, kW * row, 1, s, c, a);
 }
 
 template <typename T>
 cudaError_t launch(const ll_cache& c, const AcceptArgs& a, cudaStream_t s) {
-  accept_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2) {
     const int64_t all = c.dk | c.dv | a.sk[0] | a.sk[1] | a.sk[2] | a.sv[0] | a.sv[1] | a.sv[2];
     const bool whole = all % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15u) == 0;
-    if (whole && c.dk % 16 == 0) return launch_main<T, true>(c, a, s);
+    if (whole && c.dk % 16 == 0) return launch_both<T, true>(c, a, s);
   }
-  return launch_main<T, false>(c, a, s);
+  return launch_both<T, false>(c, a, s);
 }
 
 }  // namespace

@@ -864,7 +864,7 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   CUtensorMap pages;
   if (!make_pages_map(&pages, c.pages, c.n_pages, c.H, c.dk, c.dv, a.box_rows)) return cudaErrorInvalidValue;
   const auto kernel = cache_tree_kernel<T, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared(kernel);
   if (e != cudaSuccess) return e;
   return launch_following(false, kernel, dim3((unsigned)(items << a.split_log)), kTreeThreads, smem, split, s, pages, c, a);
 }

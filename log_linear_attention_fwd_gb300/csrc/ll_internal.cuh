@@ -292,6 +292,18 @@ cudaError_t verify_take_error(cudaStream_t s, unsigned* flags);
 
 cudaError_t launch_level_map(int T, int tile, int lc, int8_t* levels, cudaStream_t s);
 
+// Lets the kernel's launches on the current device have all the shared memory that a block can have.  The
+// limit is the function's, for all host threads: set to what one call needs, it could be lowered by a call of another
+// thread before the first one's launch.
+template <typename... Params>
+cudaError_t allow_shared(void (*kernel)(Params...)) {
+  constexpr int kMost = 227 << 10;  // static and dynamic
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost - (int)at.sharedSizeBytes);
+}
+
 // Records a CUDA error for loglinear_last_cuda_error() and returns LL_ERR_CUDA.
 int report_cuda_error(cudaError_t e);
 
