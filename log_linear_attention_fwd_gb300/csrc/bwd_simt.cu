@@ -778,14 +778,9 @@ cudaError_t launch_typed(const BwdArgs& A, cudaStream_t s) {
   const size_t sm_dkv = sizeof(float) * (rows + 2 * kC * (kC + 1) + (size_t)kStage * 128);
   const size_t sm_r = sizeof(float) * (3 * 2 * kC * 128 + 2 * 2 * kC + 2);
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(bwd_dq_kernel<InT, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sm_dq)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(bwd_dkv_kernel<InT, GT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm_dkv)) !=
-          cudaSuccess ||
-      (e = cudaFuncSetAttribute(bwd_rstate_kernel<InT, GT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm_r)) !=
-          cudaSuccess)
+  if ((e = allow_shared(bwd_dq_kernel<InT, GT>)) != cudaSuccess ||
+      (e = allow_shared(bwd_dkv_kernel<InT, GT>)) != cudaSuccess ||
+      (e = allow_shared(bwd_rstate_kernel<InT, GT>)) != cudaSuccess)
     return e;
   bwd_dq_kernel<InT, GT><<<grid, kThreads, sm_dq, s>>>(A);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

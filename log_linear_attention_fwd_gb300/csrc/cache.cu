@@ -1142,8 +1142,7 @@ cudaError_t launch_step(const ll_cache& c, StepArgs a, cudaStream_t s) {
   a.stages = (int)std::max<size_t>(2, std::min<size_t>(kMaxStages, (115000 - sizeof(StepSmem) - window) / (kStageFloats * 4)));
   const size_t smem = window + (size_t)a.stages * kStageFloats * 4;
   const auto kernel = cache_step_kernel<T, OutT, kQueue>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared(kernel);
   if (e != cudaSuccess) return e;
   // early only in the split form (8.3 -> 7.5 us with the reservation): in the queue's, CTAs that
   // find the reservation's still on their SM cost more than the launch (101 -> 104 us)

@@ -220,13 +220,8 @@ cudaError_t launch_typed(const FwdArgs& a, cudaStream_t s, StageEvents* ev) {
   const size_t sm3 = sizeof(float) * ((size_t)a.C * (2 * a.dk + a.dv) + (size_t)a.C * a.C +
                                       (size_t)kRowsPerStage * a.dv + a.C + (size_t)a.C * a.L);
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(simt_chunk_state<InT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sm1)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(simt_intra_readout<InT, OutT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm3)) !=
-      cudaSuccess)
-    return e;
+  if ((e = allow_shared(simt_chunk_state<InT>)) != cudaSuccess) return e;
+  if ((e = allow_shared(simt_intra_readout<InT, OutT>)) != cudaSuccess) return e;
   if (ev && (e = ev->record(s)) != cudaSuccess) return e;
   simt_chunk_state<InT><<<grid_c, kThreads, sm1, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -244,8 +239,7 @@ cudaError_t launch_typed(const FwdArgs& a, cudaStream_t s, StageEvents* ev) {
 template <typename InT>
 cudaError_t launch_states_typed(const FwdArgs& a, cudaStream_t s) {
   const size_t sm1 = sizeof(float) * ((size_t)a.C * 2 * kPad + 2 * a.C);
-  cudaError_t e = cudaFuncSetAttribute(simt_chunk_state<InT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm1);
+  cudaError_t e = allow_shared(simt_chunk_state<InT>);
   if (e != cudaSuccess) return e;
   simt_chunk_state<InT><<<dim3(a.N, a.H, a.B), kThreads, sm1, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -247,8 +247,7 @@ cudaError_t launch_lv(const GdnFwdArgs& a, cudaStream_t s) {
   const size_t smem = (size_t)2 * 2 * kStage * row_words * 4 +
                       sizeof(float) * ((size_t)2 * kStage * kDk + kStage + kStage * kCols +
                                        kStage * kLv + 2 * kStage + kStage * kCols);
-  cudaError_t e = cudaFuncSetAttribute(gdn_fwd_kernel<InT, OutT, kLv>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(gdn_fwd_kernel<InT, OutT, kLv>);
   if (e != cudaSuccess) return e;
   const int slices = (a.dv + kCols - 1) / kCols;
   const int64_t grid = (int64_t)a.B * a.H * slices;

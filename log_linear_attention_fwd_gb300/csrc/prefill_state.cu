@@ -264,18 +264,12 @@ cudaError_t launch_prefill_state(const FwdArgs& a, bool tc_layout, int in_dtype,
   cudaError_t e = cudaSuccess;
   if (in_dtype == LL_BF16) {
     if (tc_layout) {
-      if ((e = cudaFuncSetAttribute(prefill_state_kernel<__nv_bfloat16, true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) ==
-          cudaSuccess)
+      if ((e = allow_shared(prefill_state_kernel<__nv_bfloat16, true>)) == cudaSuccess)
         prefill_state_kernel<__nv_bfloat16, true><<<grid, kThreads, smem, s>>>(a, state, vec_in);
-    } else if ((e = cudaFuncSetAttribute(prefill_state_kernel<__nv_bfloat16, false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem)) == cudaSuccess) {
+    } else if ((e = allow_shared(prefill_state_kernel<__nv_bfloat16, false>)) == cudaSuccess) {
       prefill_state_kernel<__nv_bfloat16, false><<<grid, kThreads, smem, s>>>(a, state, vec_in);
     }
-  } else if ((e = cudaFuncSetAttribute(prefill_state_kernel<float, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) ==
-             cudaSuccess) {
+  } else if ((e = allow_shared(prefill_state_kernel<float, false>)) == cudaSuccess) {
     prefill_state_kernel<float, false><<<grid, kThreads, smem, s>>>(a, state, vec_in);
   }
   if (e != cudaSuccess) return e;

@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+import workloads as W
 from log_linear_attention_fwd_gb300 import _binding
 from tests.test_cache_gpu import i32, same, snapshot
 from tests.test_tree_gpu import contexts, parents_of
@@ -89,3 +90,38 @@ def test_accepts(LL, monkeypatch):
         want.append(snapshot(cache))
     at_once(works, 20000)
     assert all(same(snapshot(c), w) and c.error() == 0 for (c, _, _), w in zip(caches, want))
+
+
+@pytest.mark.parametrize("call", ["forward", "prefill", "backward", "delta forward", "step"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_other_calls(LL, monkeypatch, dtype, call):
+    works, outs, want = [], [], []
+    for T, chunk, dk, dv, L in ((70, 64, 128, 128, 12), (40, 16, 16, 4, 9), (65, 32, 64, 96, 10)):
+        x = W.make_fwd_inputs(W.FwdConfig("c", 1, 2, T, dk, dv, chunk, L, dtype, True, "softplus", seed=T))
+        x = {k: v.cuda() for k, v in x.items()}
+        args = (x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+        ws = torch.zeros(1 << 24, dtype=torch.uint8).cuda()
+        out, keep = torch.zeros_like(x["v"]), []
+        if call == "forward":
+            work = lambda: keep.append(LL.loglinear_fwd(*args, chunk, out=out, workspace=ws, path="simt"))  # noqa: E731
+        elif call == "prefill":
+            state = torch.zeros(1, 2, L, dk, dv).cuda()
+            work = lambda: keep.extend(LL.loglinear_prefill(*args, chunk, out=out, state=state, workspace=ws, path="simt"))  # noqa: E731
+        elif call == "backward":
+            work = lambda: keep.extend(LL.loglinear_bwd(*args, x["v"], workspace=ws, path="simt"))  # noqa: E731
+        elif call == "delta forward":
+            k = torch.nn.functional.normalize(x["k"].float(), dim=-1).to(x["k"].dtype)
+            args = (x["q"], k, x["v"], x["log_a"], torch.rand(1, T, 2).cuda(), x["lam"])
+            work = lambda: keep.append(LL.loglinear_gdn_fwd(*args, out=out))  # noqa: E731
+        else:
+            cache, slots, ctx, tree, y = contexts(LL, [70, 130], 1, 2, 1, dk, dv, dtype, True)
+            one = [None if y[n] is None else y[n][:, 0].contiguous() for n in ("q", "k", "v", "log_a", "lam")]
+            at = (cache, i32(slots), i32([70, 130]))
+            out = torch.zeros_like(one[2])
+            work = lambda: keep.extend((LL.loglinear_cache_step(*at, *one, out=out), one, at))  # noqa: E731
+        works.append(recorded(monkeypatch, work))
+        outs.append((keep, args, ws, out))
+        want.append([t.clone() for t in keep if torch.is_tensor(t)])
+    at_once(works, 5000)
+    for (keep, *_), w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip([t for t in keep if torch.is_tensor(t)], w))
