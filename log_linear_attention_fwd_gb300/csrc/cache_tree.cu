@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       page_w[x] = f;
     }
     // the values.  Behind the block's tokens and the nodes, and where a node is left out: 0.  Infinities
-    // and NaN of a node go by themselves, to the nodes below it alone
+    // and NaN of a node go by themselves, to the nodes below it alone; in the products an infinity is the least normal value
+    // of its sign (an infinite weight makes the sum's infinity of that, where 0 would make NaN), NaN is 0
     tc::cp_async_wait_all();
     {
       constexpr int kWords = 8 * (int)sizeof(T);  // 16-byte pieces that 128 columns have
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
               T* e = reinterpret_cast<T*>(p);
 #pragma unroll 1
               for (int u = 0; u < words * 4 / (int)sizeof(T); ++u)
-                if (is_odd(to_f32(e[u]))) e[u] = from_f32<T>(0.f);
+                if (const float f = to_f32(e[u]); is_odd(f)) e[u] = from_f32<T>(f != f ? 0.f : copysignf(0x1p-126f, f));
             }
           }
         }

@@ -91,3 +91,27 @@ def test_infinities_in_pages(LL, dtype, n, H, Hqk, dk, dv, N):
         assert torch.equal(got[live].nan_to_num(5.0), want[live].nan_to_num(5.0)), (at, last)
         assert torch.equal(torch.isnan(got[live]), torch.isnan(want[live]))
     assert cache.error() == 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype,odt", [("f32", torch.float32), ("bf16", torch.float32), ("bf16", torch.bfloat16)])
+def test_an_infinite_weight_on_an_infinite_value(LL, dtype, odt, value):
+    """inf * inf is an infinity of the sum, with the signs' product; what the node's other values and the other
+    branches get is as without it."""
+    pos, N, H, dk, dv = [70], 6, 1, 32, 16
+    cache, slots, ctx, tree, x = contexts(LL, pos, N, H, H, dk, dv, dtype, True)
+    for name in ("q", "k"):
+        x[name].abs_()
+        x[name].clamp_(min=0.125)
+    parents = [[-1, 0, 1, 1, 2, 0]]
+    plain = attend(LL, cache, slots, pos, parents, x, out_dtype=odt)
+    x["v"][0, 2, 0, 9] = value
+    x["lam"][0, 4, 0, oracle.level(73, 72)] = float("inf")      # node 4 (t 73) from node 2 (t 72)
+    got = attend(LL, cache, slots, pos, parents, x, out_dtype=odt)
+    same_value = (lambda a: bool(torch.isnan(a))) if value != value else (lambda a: float(a) == value)
+    assert same_value(got[0, 4, 0, 9]) and same_value(got[0, 2, 0, 9])
+    rest = [c for c in range(dv) if c != 9]
+    assert torch.equal(got[0, 4, 0, rest].float(), torch.sign(x["v"][0, 2, 0, rest].float()) * float("inf"))
+    assert torch.equal(got[0, 2, 0, rest], plain[0, 2, 0, rest])
+    for i in (0, 1, 3, 5):
+        assert torch.equal(got[0, i], plain[0, i])
