@@ -661,7 +661,9 @@ LL_API int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, c
  * node 0 is no root or that has a token outside the vocabulary does too, and raises bit 5 of
  * loglinear_device_error.  Sums are exact, of values rounded to the nearest 2^-43, and the same in any
  * order: the results do not depend on the launch.  (Rows whose values sum to 2^18 or more overflow: the
- * token is then any in the vocabulary, or -1.)
+ * token is then any in the vocabulary, or -1.  With draft, the sum of the Z of the rejections at one node counts as at
+ * most 2^19, which matters where rows sum to more than 2^13: a value that is left there can be
+ * too large, of tokens whose Q is below 2^-19.)
  * Errors: LL_ERR_INVALID (null pointer, negative size, N or V < 1), LL_ERR_DTYPE,
  * LL_ERR_UNSUPPORTED (N > LL_TREE_MAX, V > 2^30, n > 2^24), LL_ERR_ALIGN, LL_ERR_CUDA.  n = 0 is a no-op.
  */

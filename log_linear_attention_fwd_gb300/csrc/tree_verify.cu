@@ -40,6 +40,7 @@ constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifySplit = 8;  // CTAs of a cluster
 typedef unsigned long long Mass;
 constexpr Mass kOne = 1ull << kFraction;
+constexpr Mass kMost = (1ull << 62) - 1;  // what S counts as at most, nearly 2^19: its products need 62 bits
 
 // x in [0, 1] (below and NaN: 0, above: 1) as fixed point, to the nearest, plus kBias.  A sum with 8
 // has x's first 20 fractional bits as its last ones, and what is left plus 2^-20 the next 23.
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(VerifyAr
       if (ok) {
         next = i;
       } else {
-        S += Z;
+        S += min(Z, kMost - S);
         pass(S, false);
         Z = total;
         passed = cur;

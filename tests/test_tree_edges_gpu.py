@@ -1,4 +1,5 @@
-"""Speculative decoding on the GPU where it is easily wrong: bf16 outputs, deep decays, infinities.
+"""Speculative decoding on the GPU where it is easily wrong: bf16 outputs, deep decays, infinities, and rows
+that do not sum to 1.
 
 Tolerances as in tests/test_tree_gpu.py, by the same helpers; each test states what it adds.
 """
@@ -8,6 +9,7 @@ import torch
 
 import oracle
 from tests.helpers import TOL_F32, rel_l2
+from tests.test_cache_gpu import i32
 from tests.test_tree_gpu import TWO_PARTS, attend, contexts, parents_of
 
 pytestmark = pytest.mark.gpu
@@ -115,3 +117,25 @@ def test_an_infinite_weight_on_an_infinite_value(LL, dtype, odt, value):
     assert torch.equal(got[0, 2, 0, rest], plain[0, 2, 0, rest])
     for i in (0, 1, 3, 5):
         assert torch.equal(got[0, i], plain[0, i])
+
+
+@pytest.mark.parametrize("rows", [1, 310])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_verify_rows_that_sum_to_more(LL, dtype, rows):
+    """Rows of 2^17 ones, with drafts that they have at 0: S grows by 2^17 with each rejection, past 2^19 after four
+    of them and past 2^21 after seventeen.  What Q has reached is at 0 from the second one on and stays there: a
+    token of it is neither accepted nor drawn.  (One row by a cluster; many by a CTA each.)"""
+    some, ones = 1000, 2 ** 17
+    V, N = some + ones + 8, 30
+    probs, draft = (torch.zeros(rows, N, V, dtype=dtype, device="cuda") for _ in range(2))
+    probs[-1, 0, :some + ones] = 1.0
+    draft[-1, 0, :some], draft[-1, 0, some + ones:] = 2.0 ** -12, 2.0 ** -10
+    parents = torch.full((rows, N), -2, dtype=torch.int32).cuda()          # the other rows are padding
+    parents[-1] = i32([-1] + [0] * (N - 1))
+    for at in (3, 5, 10, 17, 18, 21, 29):                                   # the child that has a token of Q's
+        tokens, u = [V - 1] * N, torch.full((N,), 0.25)
+        tokens[at], u[0], u[at] = 5, 0.0, 0.0
+        assert oracle.tree_verify(parents[-1].tolist(), tokens, probs[-1].cpu(), u, draft[-1].cpu()) == ([0], some)
+        path, count, token = LL.loglinear_tree_verify(parents, i32([tokens] * rows), probs, u.repeat(rows, 1).cuda(), draft=draft)
+        assert (path[-1].tolist(), int(count[-1]), int(token[-1])) == ([0] + [-1] * (N - 1), 1, some), at
+        assert LL.device_error() == 0
