@@ -1,5 +1,5 @@
-"""Speculative decoding on the GPU where it is easily wrong: bf16 outputs, deep decays, infinities, and rows
-that do not sum to 1.
+"""Speculative decoding on the GPU where it is easily wrong: bf16 outputs, deep decays, infinities, rows that do
+not sum to 1, and pages that are shared or overwritten, in both forms of the plan.
 
 Tolerances as in tests/test_tree_gpu.py, by the same helpers; each test states what it adds.
 """
@@ -9,7 +9,7 @@ import torch
 
 import oracle
 from tests.helpers import TOL_F32, rel_l2
-from tests.test_cache_gpu import i32
+from tests.test_cache_gpu import decode, filled, i32, invariants, snapshot
 from tests.test_tree_gpu import TWO_PARTS, attend, contexts, parents_of
 
 pytestmark = pytest.mark.gpu
@@ -139,3 +139,95 @@ def test_verify_rows_that_sum_to_more(LL, dtype, rows):
         path, count, token = LL.loglinear_tree_verify(parents, i32([tokens] * rows), probs, u.repeat(rows, 1).cuda(), draft=draft)
         assert (path[-1].tolist(), int(count[-1]), int(token[-1])) == ([0] + [-1] * (N - 1), 1, some), at
         assert LL.device_error() == 0
+
+
+def leftover(LL):
+    """Slots 0 and 4 at 188, in block 2, with block 1's page of level 0 left over, which is slot 3's live one
+    (at 74) too; block 2 folds to that level."""
+    cache, x, _ = filled(LL, n=1, T=(64 + 10,), more=160)
+    LL.loglinear_cache_fork(cache, i32([0, 0]), i32([3, 4]), i32([74, 74]))
+    one = {k: v[:1] for k, v in x.items()}
+    two = {k: torch.cat([v, v]) for k, v in one.items()}
+    pos = 74
+    while pos < 188:
+        _, (pos, _) = decode(LL, cache, two, [0, 4], [pos, pos], 1, reserve=pos in (127,))
+    page = int(cache.page_table[0, 0])
+    assert page >= 0 and (cache.page_table[[0, 3, 4], 0] == page).all() and cache.refcount[page] == 3 and cache.error() == 0
+    return cache, one, two, page, oracle.forward_direct(x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+
+
+def padded(values, rows, fill=-1):
+    """values, then `fill` up to `rows` rows (more than 1024: the plan's other form)."""
+    return values + [fill] * (rows - len(values))
+
+
+@pytest.mark.parametrize("rows", [2, 1100])
+def test_an_accepted_fold_never_writes_a_shared_page(LL, rows):
+    """A page left over where the fold goes, and shared, is replaced: its other holders keep it."""
+    cache, one, two, page, want = leftover(LL)
+    held, N = cache.pages[page].clone(), 6
+    k, v, la = (torch.zeros(rows, N, *one[n].shape[2:], dtype=one[n].dtype).cuda() for n in ("k", "v", "log_a"))
+    for t, n in ((k, "k"), (v, "v"), (la, "log_a")):
+        t[:2] = two[n][:, 188:194].cuda()
+    new = LL.loglinear_cache_accept(cache, i32(padded([0, 4], rows)), i32(padded([188, 188], rows, 0)),
+                                    i32([list(range(N))] * rows), k, v, la, new_pos=i32([-9] * rows))
+    assert new.tolist() == padded([194, 194], rows, -9) and cache.error() == 0
+    assert torch.equal(cache.pages[page], held) and int(cache.page_table[3, 0]) == page and cache.refcount[page] == 1
+    mine = cache.page_table[[0, 4], 0].tolist()
+    assert len({page, *mine}) == 3 and cache.refcount[mine].tolist() == [1, 1]
+    invariants(cache, {0: 194, 4: 194, 3: 74})
+    got, _ = decode(LL, cache, two, [0, 4], [194, 194], 40)
+    for r in range(2):
+        assert rel_l2(got[r].cpu(), want[0, 194:234]) <= TOL_F32
+    got, _ = decode(LL, cache, one, [3], [74], 40)
+    assert rel_l2(got[0].cpu(), want[0, 74:114]) <= TOL_F32
+    assert cache.error() == 0
+
+
+def test_reservations_of_both_forms_settle_shared_pages_alike(LL):
+    """The same rows in a call of 2 and in one of more than 1024: the same tables and counts, and whole outputs."""
+    cache, one, two, page, want = leftover(LL)
+    _, (pos, _) = decode(LL, cache, two, [0, 4], [188, 188], 3, reserve=False)
+    assert pos == 191
+    held, twin = cache.pages[page].clone(), LL.LogLinearCache(*snapshot(cache))
+    for c, rows in ((cache, 2), (twin, 1100)):
+        LL.loglinear_cache_reserve(c, i32(padded([0, 4], rows)), i32(padded([191, 191], rows, 0)))
+        assert c.error() == 0 and torch.equal(c.pages[page], held) and c.refcount[page] == 1
+    assert torch.equal(cache.page_table, twin.page_table) and torch.equal(cache.refcount, twin.refcount)
+    for c in (cache, twin):
+        got, _ = decode(LL, c, two, [0, 4], [191, 191], 1, reserve=False)
+        tail, _ = decode(LL, c, two, [0, 4], [192, 192], 40)
+        for r in range(2):
+            assert rel_l2(torch.cat([got, tail], 1)[r].cpu(), want[0, 191:232]) <= TOL_F32
+        invariants(c, {0: 232, 4: 232, 3: 74})
+        got, _ = decode(LL, c, one, [3], [74], 40)
+        assert rel_l2(got[0].cpu(), want[0, 74:114]) <= TOL_F32
+        assert c.error() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 1100])
+@pytest.mark.parametrize("call", ["free", "reserve", "accept"])
+def test_overwritten_tables_in_both_forms(LL, call, rows):
+    """Entries below -1 and past the pool count for no page: whoever holds the others keeps them."""
+    cache, x, T = filled(LL)
+    cache.page_table[2] = i32([-2, 10 ** 6, -3, -4])
+    count = cache.refcount.clone()
+    slots = i32(padded([2], rows))
+    if call == "free":
+        LL.loglinear_cache_free(cache, slots)
+    elif call == "reserve":
+        LL.loglinear_cache_reserve(cache, slots, i32(padded([383], rows, 0)))   # block 5 is live and folds into level 1
+    else:                                                                        # its path ends block 5, whose page of level 0 is not there
+        z = lambda *s: torch.zeros(rows, 2, *s).cuda()  # noqa: E731
+        new = LL.loglinear_cache_accept(cache, slots, i32(padded([382], rows, 0)), i32([[0, 1]] * rows), z(2, 16), z(2, 8), None,
+                                        new_pos=i32([-9] * rows))
+        assert (new == -9).all()
+    taken = [e for e in cache.page_table[2].tolist() if 0 <= e < len(count)]
+    assert len(taken) == (call != "free") and all(count[e] == 0 for e in taken)
+    count[taken] = 1
+    assert torch.equal(cache.refcount, count)
+    assert cache.error() == (LL.CACHE_ERR_MISSING if call == "accept" else 0)
+    want = oracle.forward_direct(x["q"], x["k"], x["v"], x["log_a"], x["lam"])
+    got, _ = decode(LL, cache, {k: v[:2] for k, v in x.items()}, [0, 1], T[:2], 70)
+    for r in range(2):
+        assert rel_l2(got[r].cpu(), want[r, T[r]:T[r] + 70]) <= TOL_F32
