@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
 #pragma unroll 1
               for (int d = k0; d < k1; d += box_rows)
 #pragma unroll 1
-                for (int y = first_row; y < min(min(box_rows, k1 - d), first_row + (wide > 1 ? 32 : 16)); ++y)
+                for (int y = first_row; f == f && y < min(min(box_rows, k1 - d), first_row + (wide > 1 ? 32 : 16)); ++y)
                   f = fmaf(page[(int64_t)(d + y) * dv + (e >> 1 & 1)], __bfloat162float(qr[d + y]), f);
 #pragma unroll
               for (int i = 0; i < 4 * NT; ++i)
