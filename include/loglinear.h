@@ -640,9 +640,11 @@ LL_API int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, c
                                   ll_stream_t stream);
 
 /*
- * Verification of drafts by speculative sampling: the accepted tokens and the next one are
- * distributed as the target's.  The walk starts at node 0 and tries the current node's children in the
- * order of their index, with R the target's row P of that node and Z = 1 at first.  Node i, token x:
+ * Verification of drafts by speculative sampling: where the rows of probs (and of draft) sum to 1, the
+ * accepted tokens and the next one are distributed as the target's.  (Z starts at 1, not at the row's
+ * own sum: a sum that is off by e moves a draft's chance by about e; rounded to bf16, up to 2^-8.)
+ * The walk starts at node 0 and tries the current node's children in the order of their index, with
+ * R the target's row P of that node and Z = 1 at first.  Node i, token x:
  *     draft NULL (drafts that were given, such as the likeliest tokens): accepted where u_i Z < R(x);
  *         else R(x) is taken off Z and set to 0.
  *     draft (each child drawn from its parent's row Q of it, independently): accepted where
@@ -661,9 +663,9 @@ LL_API int loglinear_cache_accept(const ll_cache* cache, const int32_t* slots, c
  * node 0 is no root or that has a token outside the vocabulary does too, and raises bit 5 of
  * loglinear_device_error.  Sums are exact, of values rounded to the nearest 2^-43, and the same in any
  * order: the results do not depend on the launch.  (Rows whose values sum to 2^18 or more overflow: the
- * token is then any in the vocabulary, or -1.  With draft, the sum of the Z of the rejections at one node counts as at
- * most 2^19, which matters where rows sum to more than 2^13: a value that is left there can be
- * too large, of tokens whose Q is below 2^-19.)
+ * token is then any in the vocabulary, or -1.  With draft, the sum of the rejections' Z at one node
+ * counts as at most 2^19, which matters where rows sum to more than 2^13: R can then be too large at
+ * tokens whose Q is below 2^-19.)
  * Errors: LL_ERR_INVALID (null pointer, negative size, N or V < 1), LL_ERR_DTYPE,
  * LL_ERR_UNSUPPORTED (N > LL_TREE_MAX, V > 2^30, n > 2^24), LL_ERR_ALIGN, LL_ERR_CUDA.  n = 0 is a no-op.
  */

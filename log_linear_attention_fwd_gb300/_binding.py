@@ -885,12 +885,13 @@ def loglinear_cache_tree(cache, slots, pos, parents, q, k, v, log_a, lam, out=No
 
 def loglinear_tree_verify(parents, tokens, probs, u, draft=None, path=None, count=None, token=None,
                           stream=None):
-    """Which drafts of a tree stand, by speculative sampling from given random numbers.  parents,
-    tokens [n,N] int32 (node 0: the pending token; a row whose node 0 is -2 is padding); probs
-    [n,N,V] fp32 or bf16: the target's distribution after each node; u [n,N] fp32 in [0,1), u[:,0] for
-    the next token; draft [n,N,V] in probs' dtype: the distribution that each node's children were drawn
-    from, or None for drafts that were given.  Returns (path [n,N] int32: node 0, the accepted
-    nodes, -1 behind them; count [n] int32; token [n] int32: the next pending token)."""
+    """Which drafts of a tree stand, by speculative sampling from given random numbers: distributed as
+    the target's tokens where the rows of probs (and draft) sum to 1.  parents, tokens [n,N] int32
+    (node 0: the pending token; a row whose node 0 is -2 is padding); probs [n,N,V] fp32 or bf16: the
+    target's distribution after each node; u [n,N] fp32 in [0,1), u[:,0] for the next token; draft
+    [n,N,V] in probs' dtype: the distribution that each node's children were drawn from, or None for
+    drafts that were given.  Returns (path [n,N] int32: node 0, the accepted nodes, -1 behind them;
+    count [n] int32; token [n] int32: the next pending token), allocated where they are not given."""
     dev = _current_device_of("probs", probs)
     if probs.dim() != 3:
         raise ValueError(f"probs has shape {tuple(probs.shape)}, expected (n, N, V)")

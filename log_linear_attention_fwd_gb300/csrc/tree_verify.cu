@@ -7,7 +7,7 @@
 //     u Z_k < R_k(x)              (drafts that were given: x is removed from R when it is rejected)
 //     u Z_k q(x) < R_k(x)         (drafts drawn from q: then R_{k+1} = max(R_k - Z_k q, 0), Z_{k+1} = sum of it)
 // and else the next one is tried; where none is left the next token is drawn from R_k.  So the
-// tokens are distributed as the target's own.  R_k is max(P - S_k q, 0) with S_k = Z_0 + .. + Z_{k-1}, as
+// tokens are distributed as the target's own, where its rows sum to 1.  R_k is max(P - S_k q, 0) with S_k = Z_0 + .. + Z_{k-1}, as
 // what has once reached 0 stays there: one product per value, whatever was rejected before.
 //
 // Sums over a vocabulary are 64-bit fixed point with 43 fractional bits: the same in every order, so
@@ -22,7 +22,8 @@
 // Measured (GB300, calls in a row; floor: bytes at the measured copy rate).  One row of 32768 fp32 values: 7.4 us, a
 // chain of five latencies (tree, children's values, pass, cluster, run).  61 rows of 131072 with trees of 32: 15 us, 32 MB,
 // floor 4.8: the same chain; the pass (4 us) is the only part that moves bytes.  128 chains of 5 drawn drafts: 33 us,
-// 134 MB, floor 20: 4.0 TB/s; rows that reject once have two passes.  32 trees of 23 drawn drafts, 50021 bf16
+// 134 MB, floor 20: one pass per row (a chain's node has no sibling to try behind a rejection), all rows at once and in step, so
+// that nothing moves before the pass and during the search behind it.  32 trees of 23 drawn drafts, 50021 bf16
 // values: 30 us, one pass per rejection, each about 2 us of latency and of arithmetic.  Four CTAs of 256
 // threads per SM: three left the drawn chains at 54, two of 512 were slower on two of these.
 #include <algorithm>
