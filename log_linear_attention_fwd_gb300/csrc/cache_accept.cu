@@ -6,6 +6,8 @@
 // copy rate): one sequence's path 5.6 us; 125 rows of 16 heads, d 128, ten of which end a block, 39 us (floor
 // 5.7): 13 without the ten, 24 with those that fold to no older page, and the rest is the one that folds seven pages, by
 // one CTA per head at 30 GB/s each; 32 rows of 48 heads, dv 64, all of which end a block: 45 us, 109 MB, floor 16.
+// Folds on the CUDA cores: those of fp32 tokens 214 us (batch: 83), 123 MB, floor 18, bound by the latency of their reads
+// with two CTAs per SM (25 % of the issue slots); bf16 of d_k 72 and d_v 36 130 us, 38 MB, floor 6.
 // CTAs of 128 (53, 46 us) or 512 threads (39, 62), persistent ones with a list of folds (36 to 48, 69 and more), and
 // pages through a ring in shared memory (47, 53) were no better.
 #include "cache_common.cuh"

@@ -53,8 +53,10 @@ struct TreeArgs {
 // 128, 8 nodes, position 12345: 9.3 us, a chain of latencies (inputs, scores, weights, values, pages, two cluster
 // barriers).  61 sequences of such heads at 0..16383, up to 32 nodes: 88 us, 3.5 TB/s, floor 45.  24 sequences of
 // 48 heads on one q/k head, dv 64, 64 nodes, 4096..131071: 154 us, 1.6 TB/s, floor 36.  There a page's third part is 17 us
-// and a weight's second one 16; registers and the weights' room allow two CTAs per SM, which hide the part before the
-// pages only partly.
+// and a weight's second one 16; registers and the weights' room allow two CTAs per SM (18 warps; 40 % of the issue slots,
+// tensor pipe 27 %), which hide the part before the pages only partly: one stage of pages is on its way in it, and none in
+// the batch's.  fp32 tokens, of which a CTA per SM fits above 16 nodes: the batch 208 us, its trees of 48 nodes, which pass the
+// pages twice, 390 us, the shared heads 365 us (floors 52, 56, 39).
 constexpr int kTreeWarps = 8, kConsumers = 32 * kTreeWarps, kTreeThreads = kConsumers + 32;
 constexpr int kFiller = kTreeWarps;    // the warp that fills the ring
 constexpr int kWalkers = kTreeWarps - 2;  // the first of the two warps that have a node per thread
@@ -854,7 +856,9 @@ cudaError_t launch(const ll_cache& c, TreeArgs a, cudaStream_t s) {
   const TreeLayout lay = tree_layout<T, NT>(dv, a.N, (int)c.levels);
   const size_t own_smem = (sizeof(TreeSmem) + 1023) & ~(size_t)1023;  // the stages begin at a multiple of 1024
   const size_t fixed = own_smem + 1024;                              // (1024 of each CTA are the system's)
-  // as many CTAs on an SM as leave the ring three stages, one of them from the start
+  // as many CTAs on an SM as leave the ring three stages, one of them its own.  The last of its own holds the tree's decays
+  // until the tokens are done with: where it is the only one (bf16: d_v from 96 on and 17 nodes or more), no page is on its
+  // way before that
   const int later = lay.q / kStageBytes;
   int ctas = tree_ctas<T, NT>();
   while (ctas > 1 && fixed + lay.end + std::max(1, 3 - later) * kStageBytes > kSm / ctas) --ctas;
