@@ -6,7 +6,6 @@ import pytest
 import torch
 
 import workloads as W
-from log_linear_attention_fwd_gb300 import _binding
 from tests.test_cache_gpu import i32, same, snapshot
 from tests.test_tree_gpu import contexts, parents_of
 
@@ -21,6 +20,7 @@ def LL():
 
 def recorded(monkeypatch, call):
     """The library calls that `call` makes, which it makes once: (function, arguments), the last one the stream."""
+    from log_linear_attention_fwd_gb300 import _binding
     made, real = [], _binding._lib
 
     class Recorder:
