@@ -211,12 +211,6 @@ __device__ __forceinline__ Float8 load8(const float* row, int k, int width, bool
   return x;
 }
 // As tf32 parts: part[p][u] of value u.
-__device__ __forceinline__ void parts_of(const uint4& x, uint32_t (&part)[1][8]) {
-  part[0][0] = x.x << 16; part[0][1] = x.x & 0xffff0000u;
-  part[0][2] = x.y << 16; part[0][3] = x.y & 0xffff0000u;
-  part[0][4] = x.z << 16; part[0][5] = x.z & 0xffff0000u;
-  part[0][6] = x.w << 16; part[0][7] = x.w & 0xffff0000u;
-}
 __device__ __forceinline__ void parts_of(const Float8& x, uint32_t (&part)[2][8]) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) split_tf32(x.e[u], part[0][u], part[1][u]);
