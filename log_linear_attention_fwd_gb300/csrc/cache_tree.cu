@@ -46,7 +46,8 @@ struct TreeArgs {
 // that leave 2^-22.  (Pages and weights rounded to tf32 for bf16 outputs took 77 and 119 us where this takes 88 and 154, and
 // moved the outputs by up to 2^-11 of each product; pages as two tf32 parts, 108 and 176.)  With fp32 tokens everything
 // is two tf32 parts, and all four products of them are taken: the first parts are cut off towards zero, so the fourth
-// is of one sign and adds up (rel-L2 of the outputs 7e-7 with it, 1.2e-6 without).  All sums are fp32, and a page is
+// is of one sign and adds up.  The three with a second part are summed apart from the first (rel-L2 of the outputs
+// 3.3e-7 for the batch below in fp32, 1.1e-6 in one sum; 2.3e-7 in fp32 multiply-adds).  All sums are fp32, and a page is
 // summed by itself before it is weighted per node.
 //
 // Measured (GB300, calls in a row; floor: the bytes at the measured copy rate of 6.7 TB/s).  One sequence, 16 heads, d
@@ -55,8 +56,8 @@ struct TreeArgs {
 // 48 heads on one q/k head, dv 64, 64 nodes, 4096..131071: 154 us, 1.6 TB/s, floor 36.  There a page's third part is 17 us
 // and a weight's second one 16; registers and the weights' room allow two CTAs per SM (18 warps; 40 % of the issue slots,
 // tensor pipe 27 %), which hide the part before the pages only partly: one stage of pages is on its way in it, and none in
-// the batch's.  fp32 tokens, of which a CTA per SM fits above 16 nodes: the batch 208 us, its trees of 48 nodes, which pass the
-// pages twice, 390 us, the shared heads 365 us (floors 52, 56, 39).
+// the batch's.  fp32 tokens, of which a CTA per SM fits above 16 nodes: the batch 209 us, its trees of 48 nodes, which pass the
+// pages twice, 393 us, the shared heads 367 us (floors 52, 56, 39).
 constexpr int kTreeWarps = 8, kConsumers = 32 * kTreeWarps, kTreeThreads = kConsumers + 32;
 constexpr int kFiller = kTreeWarps;    // the warp that fills the ring
 constexpr int kWalkers = kTreeWarps - 2;  // the first of the two warps that have a node per thread
@@ -161,6 +162,15 @@ __device__ __forceinline__ uint32_t lead_bf16(float& x, float& y) {
   x -= __uint_as_float(a & 0xffff0000u);
   y -= __uint_as_float(b & 0xffff0000u);
   return __byte_perm(a, b, 0x7632);
+}
+// The products with a second part are summed apart: the tensor cores cut a sum off at its own size, towards zero, and
+// would lose most of them, all of one sign, behind the products of the first parts.
+template <int NT>
+__device__ __forceinline__ void add_parts(float (&sum)[NT][4], const float (&low)[NT][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum[t][u] += low[t][u];
 }
 // Two neighbouring values as tf32 parts.
 __device__ __forceinline__ void parts2(const __nv_bfloat16* p, uint32_t (&part)[1][2]) {
@@ -458,6 +468,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             mma_bf16(sc[t], ka[1], q.z, q.w);
           }
         } else {
+          float low[NT][4] = {};
           uint32_t ka[2][2][8];
 #pragma unroll
           for (int u = 0; u < 2; ++u) parts_of(load8(key[u], 32 * d + 4 * lanes_i, key_width[u], key_vec), ka[u]);
@@ -469,12 +480,14 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
               const uint4 even = q[0], odd = q[1];
 #pragma unroll
               for (int x = 1; x >= 0; --x) {
-                mma_tf32(sc[t], ka[0][x][0], ka[1][x][0], ka[0][x][1], ka[1][x][1], even.x, odd.x);
-                mma_tf32(sc[t], ka[0][x][2], ka[1][x][2], ka[0][x][3], ka[1][x][3], even.y, odd.y);
-                mma_tf32(sc[t], ka[0][x][4], ka[1][x][4], ka[0][x][5], ka[1][x][5], even.z, odd.z);
-                mma_tf32(sc[t], ka[0][x][6], ka[1][x][6], ka[0][x][7], ka[1][x][7], even.w, odd.w);
+                float(&f)[4] = x + y ? low[t] : sc[t];
+                mma_tf32(f, ka[0][x][0], ka[1][x][0], ka[0][x][1], ka[1][x][1], even.x, odd.x);
+                mma_tf32(f, ka[0][x][2], ka[1][x][2], ka[0][x][3], ka[1][x][3], even.y, odd.y);
+                mma_tf32(f, ka[0][x][4], ka[1][x][4], ka[0][x][5], ka[1][x][5], even.z, odd.z);
+                mma_tf32(f, ka[0][x][6], ka[1][x][6], ka[0][x][7], ka[1][x][7], even.w, odd.w);
               }
             }
+          add_parts(sc, low);
         }
       }
     }
@@ -597,6 +610,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
       for (int u = 0; u < 4; ++u) acc[t][u] = 0.f;
     if (on) {
       int turn = 0;
+      float low[kIn == 2 ? NT : 1][4] = {};
       for (int tile = sp; tile < tiles; tile += Z) {
         if (tile < kW / 16 && 16 * tile >= r) continue;
         if ((turn++ & (kparts - 1)) != kp) continue;
@@ -614,10 +628,11 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             for (int x = 1; x >= 0; --x)
 #pragma unroll
               for (int i = kIn - 1; i >= 0; --i)
-                mma_tf32(acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], p[x][0], p[x][1]);
+                mma_tf32(kIn == 2 && x + i ? low[kIn == 2 ? t : 0] : acc[t], va[i][0], va[i][1], vb[i][0], vb[i][1], p[x][0], p[x][1]);
           }
         }
       }
+      if constexpr (kIn == 2) add_parts(acc, low);
     }
     if (sm.odd && on && kp == 0 && col < dv) {
 #pragma unroll 1
@@ -656,11 +671,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
           : tc::smem_u32(qs) + (lane & 7) * kQPitch * 4 + (lane >> 3) * 16 + 4 * first_row;
       int stage = 0, phase = 0;
       for (int x = 0; x < live; ++x) {
-        float part[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) part[t][u] = 0.f;
+        float part[NT][4] = {}, low[kIn == 2 ? NT : 1][4] = {};
         for (int d = k0; d < k1; d += box_rows) {
           if (ok) ok = tc::mbar_wait_short(&sm.full[stage], phase);
           const uint32_t at0 = off0 + stage * kStageBytes, at1 = off1 + stage * kStageBytes, q = q_at + (int)sizeof(T) * d;
@@ -704,8 +715,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
                   ldmatrix4(b[0], b[1], b[2], b[3], q + ((y * NQ + 8 * t) * kQPitch + 16 * z) * 4);
 #pragma unroll
                   for (int u = 1; u >= 0; --u) {
-                    mma_tf32(part[t], pa[u][0], pa[u][1], pa[u][2], pa[u][3], b[0], b[1]);
-                    mma_tf32(part[t], pa[u][4], pa[u][5], pa[u][6], pa[u][7], b[2], b[3]);
+                    float(&f)[4] = u + y ? low[t] : part[t];
+                    mma_tf32(f, pa[u][0], pa[u][1], pa[u][2], pa[u][3], b[0], b[1]);
+                    mma_tf32(f, pa[u][4], pa[u][5], pa[u][6], pa[u][7], b[2], b[3]);
                   }
                 }
             }
@@ -746,6 +758,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<T, NT>())
             }
           }
           __syncwarp();
+        } else {
+          add_parts(part, low);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import oracle
-from tests.helpers import TOL_F32, rel_l2
+from tests.helpers import TOL_F32, rel_l2, to64
 from tests.test_cache_gpu import decode, filled, i32, invariants, snapshot
 from tests.test_tree_gpu import TWO_PARTS, attend, contexts, parents_of
 
@@ -60,6 +60,44 @@ def test_deep_decays_that_decide(LL, dtype):
         for i in range(N):
             assert rel_l2(got[r, i], want[r, i]) <= tol, (r, i, rel_l2(got[r, i], want[r, i]))
     assert torch.equal(attend(LL, cache, slots, pos, chain, x, out_dtype=torch.bfloat16), got.bfloat16())
+
+
+@pytest.mark.parametrize("rows", [1, 80])
+@pytest.mark.parametrize("N", [5, 16, 20, 40])
+def test_fp32_trees_lose_no_more_than_their_parts_leave(LL, N, rows):
+    """fp32 tokens and outputs, seven pages of random states and no decay.  A term has at most three factors that are
+    taken as parts, which leave 2^-22 of each, and three roundings of 2^-24; signs and amounts are random, so
+    that together with the sums' own roundings (2^-24 of what stands there, 2^-24 sqrt(128) over a page's rows if all went
+    one way by half) the whole is below 2^-21 of the outputs' norm."""
+    H, Hqk, d, M = 2, 1, 128, 9
+    pos, L = 64 * 0b101111110 + 37, M + 7
+    g = torch.Generator().manual_seed(N)
+    rand = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = {"q": rand(1, N, Hqk, d) / 8, "k": rand(1, N, Hqk, d) / 8, "v": rand(1, N, H, d), "lam": torch.rand(1, N, H, L, generator=g)}
+    wk, wv, state = rand(1, 37, Hqk, d) / 8, rand(1, 37, H, d), torch.zeros(1, H, L, d, d)
+    live = [m for m in range(M) if pos >> 6 >> m & 1]
+    for m in live:
+        state[0, :, 7 + m] = rand(H, d, d)
+    cache = LL.LogLinearCache.empty(1, 10, H, d, d, M, Hqk=Hqk, dtype=torch.float32)
+    LL.loglinear_cache_load(cache, i32([0]), pos, state.cuda(), wk.cuda(), wv.cuda(), None)
+    assert len(live) == 7 and cache.error() == 0
+    chain = [list(range(-1, N - 1))] * rows
+    y = {k: v.cuda().repeat(rows, 1, 1, 1) for k, v in x.items()}
+    got = attend(LL, cache, [0] * rows, [pos] * rows, chain, dict(y, log_a=None)).cpu()
+    q, lam, S = to64(x["q"][0, :, 0]), to64(x["lam"][0]), to64(state[0])
+    keys, vals = to64(torch.cat([wk, x["k"]], 1)[0, :, 0]), to64(torch.cat([wv, x["v"]], 1)[0])
+    want = np.zeros((N, H, d))
+    for i in range(N):
+        t = pos + i
+        over = t >> 6 != pos >> 6
+        to = ((t >> 6) & -(t >> 6)).bit_length() - 1 if over else 0
+        w = np.stack([lam[i, :, oracle.level(t, pos - 37 + s)] * (keys[s] @ q[i]) for s in range(38 + i)])
+        want[i] = np.einsum("sh,shd->hd", w, vals[:38 + i])
+        for m in live:
+            want[i] += lam[i, :, 7 + max(m, to), None] * (q[i] @ S[:, 7 + m])
+    for r in range(rows):
+        assert rel_l2(got[r], want) <= 2.0 ** -21, rel_l2(got[r], want)
+    assert cache.error() == 0
 
 
 @pytest.mark.parametrize("n,H,Hqk,dk,dv,N", [(1, 1, 1, 32, 16, 5), (1, 2, 1, 128, 128, 30), (2, 2, 2, 96, 36, 64), (40, 4, 2, 33, 20, 9),
